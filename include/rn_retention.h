@@ -367,6 +367,197 @@ rn_status rn_groupnorm_gate(int32_t B, int32_t H, int32_t N, int32_t d_v,
 rn_status rn_chunkwise_check(const rn_desc* desc, int32_t chunk, const void* workspace,
                              size_t workspace_bytes, void* stream);
 
+/*
+ * ---- operators around retention -----------------------------------------------------------
+ * Layer norm, rotary positions and linear attention with a decay per head and token. Same
+ * conventions as above, except that tensors are described by strides (in elements; the last
+ * axis is always contiguous), so that the rows of a projection's output need no copy.
+ * Strides are >= 0 and at most 2^40; a stride of 0 repeats an input along that axis (outputs
+ * must not overlap themselves).
+ */
+
+/*
+ * Layer norm of rows of d values, with the residual sum before it (the norm in front of a
+ * retention layer, whose input is the residual stream):
+ *     h = x + residual        (h = x where residual is NULL)
+ *     out = (h - mean(h)) / sqrt(var(h) + eps) * weight + bias,   biased variance.
+ * Statistics and the normalised values are formed in float32 from the float32 sum h; sum_out
+ * receives h rounded to in_dtype (the next residual stream).
+ */
+typedef struct rn_norm_desc {
+    int64_t rows;          /* 1 .. 2^40 */
+    int32_t d;             /* 1 .. 16384 */
+    rn_dtype in_dtype;     /* x, residual, sum_out; backward: x, dsum, dx */
+    rn_dtype out_dtype;    /* out; backward: dout */
+    float eps;             /* finite, >= 0 */
+    int64_t x_stride;      /* elements between rows: x */
+    int64_t res_stride;    /* residual; backward: dsum */
+    int64_t sum_stride;    /* sum_out; backward: dx */
+    int64_t out_stride;    /* out; backward: dout */
+} rn_norm_desc;
+
+/*
+ * weight, bias: DEVICE float32 [d] or NULL (1 and 0). residual and sum_out: NULL, or rows of
+ * in_dtype (sum_out needs no residual; it then receives a copy of x). sum_out may equal x or
+ * residual with the same stride, out may equal x where in_dtype == out_dtype and the strides
+ * agree (out and sum_out must differ).
+ */
+rn_status rn_layernorm_forward(const rn_norm_desc* desc, const void* x, const void* residual,
+                               const float* weight, const float* bias, void* sum_out, void* out,
+                               void* stream);
+
+/* Bytes of device workspace rn_layernorm_backward needs (0 for an invalid descriptor). */
+size_t rn_layernorm_backward_workspace_bytes(const rn_norm_desc* desc);
+
+/*
+ * Gradients of out = LN(x) with x the rows the forward call normalised (its sum_out where it
+ * had a residual); statistics are recomputed, nothing else from the forward call is needed:
+ *     g = dout * weight,  xh = (x - mean) / sqrt(var + eps)
+ *     dx = (g - mean(g) - xh mean(g xh)) / sqrt(var + eps) + dsum
+ *     dweight = sum over rows of dout xh,   dbias = sum over rows of dout.
+ * dsum: the gradient reaching the residual sum by its other path, or NULL (0); dx is then the
+ * gradient of both x and residual. dx: in_dtype, may equal dout or dsum where types and
+ * strides agree. dweight, dbias: DEVICE float32 [d] or NULL, written (not added to); their
+ * sums run in a fixed order (the same bits on every call). workspace: 256-byte aligned, at
+ * least rn_layernorm_backward_workspace_bytes(desc); unused (may be NULL) when both dweight
+ * and dbias are NULL.
+ */
+rn_status rn_layernorm_backward(const rn_norm_desc* desc, const void* dout, const void* x,
+                                const float* weight, const void* dsum, void* dx, float* dweight,
+                                float* dbias, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/*
+ * Rotary positions: coordinate pairs of the first `rot` of d coordinates of every head are
+ * turned by the angle p * theta_j of their token's position p and scaled by `magnitude`:
+ *     (a, b) -> magnitude * (a cos - b sin, a sin + b cos),
+ * where pair j is coordinates (2j, 2j+1), or (j, j + rot/2) with RN_ROTARY_HALF. The other
+ * coordinates are copied. RN_ROTARY_INVERSE turns by -p theta_j: the transpose, hence also
+ * the gradient's way back (with the same magnitude). Angles are formed and reduced in float64.
+ * Retention called with theta = 0 on tensors turned here equals retention with its own
+ * rotation (interleaved pairs, rot = d_k, magnitude 1).
+ */
+#define RN_ROTARY_HALF      (1u << 0)
+#define RN_ROTARY_INVERSE   (1u << 1)
+#define RN_ROTARY_POS_TOKEN (1u << 2) /* pos is [B, N] (row-major): a position per token */
+
+typedef struct rn_rotary_desc {
+    int32_t B, N;          /* >= 1; B * N <= 2^31 - 1 */
+    int32_t H_q, H_k;      /* heads of q (>= 1) and k (>= 0; 0 = no k); at most 65535 in all */
+    int32_t d;             /* 2 .. 512 */
+    int32_t rot;           /* even, 2 .. min(d, 256) */
+    rn_dtype dtype;        /* of all four tensors */
+    uint32_t flags;        /* RN_ROTARY_* */
+    int64_t pos0;          /* position of token 0 where pos is NULL, in [0, 2^40] */
+    float magnitude;       /* finite */
+    const double* theta;   /* HOST [rot/2]: finite */
+    int64_t q_stride[3];   /* elements between batch rows, heads, tokens */
+    int64_t k_stride[3];
+    int64_t q_out_stride[3];
+    int64_t k_out_stride[3];
+} rn_rotary_desc;
+
+/*
+ * q [B, H_q, N, d], k [B, H_k, N, d] (any strides) -> q_out, k_out. An output may be its own
+ * input (same pointer and strides): then the coordinates past `rot` are not touched.
+ * pos: DEVICE int64, 8-byte aligned: NULL (token t of every row sits at pos0 + t), [B] (at
+ * pos[b] + t), or [B, N] with RN_ROTARY_POS_TOKEN. Values are not checked (they move no
+ * memory access); |p| <= 2^40 keeps the angles accurate.
+ */
+rn_status rn_rotary(const rn_rotary_desc* desc, const int64_t* pos, const void* q, const void* k,
+                    void* q_out, void* k_out, void* stream);
+
+/*
+ * The rot/2 angles theta_j = base^(-2j/rot), and their forms for contexts `factor` times as
+ * long as the `length` positions a model was trained on. Host only.
+ *   RN_ROPE_PLAIN     theta_j
+ *   RN_ROPE_LINEAR    theta_j / factor
+ *   RN_ROPE_BASE      base replaced by base * factor^(rot/(rot-2)): the slowest pair is
+ *                     stretched by factor, the fastest keeps its angle (rot >= 4)
+ *   RN_ROPE_BY_PARTS  with n_j = length theta_j / (2 pi) turns over the trained length: pairs
+ *                     with n_j >= fast keep theta_j, pairs with n_j <= slow take theta_j /
+ *                     factor, those between are mixed in proportion to n_j; *magnitude
+ *                     becomes 0.1 ln(factor) + 1 (1 for the other kinds).
+ * factor >= 1; base > 1; for BY_PARTS length >= 1 and 0 <= slow < fast.
+ */
+#define RN_ROPE_PLAIN    0
+#define RN_ROPE_LINEAR   1
+#define RN_ROPE_BASE     2
+#define RN_ROPE_BY_PARTS 3
+rn_status rn_rotary_frequencies(int32_t rot, double base, int32_t kind, double factor,
+                                double length, double slow, double fast, double* theta,
+                                float* magnitude);
+
+/*
+ * Linear attention with a decay per head and token (retention whose decay the tokens set):
+ *     S_t = exp(g_t) S_{t-1} + k_t^T v_t,     o_t = qk_scale q_t S_t
+ * with log decays g <= 0 (DEVICE float32; -inf clears the state before the token; NaN
+ * propagates). No rotation is applied (see rn_rotary). Heads: H states and outputs; q, k and v
+ * may have fewer, each dividing H: head h reads q head h / (H / H_q), and so on.
+ *
+ * Precision: float32 inputs, and bf16 inputs with a float32 output, run float32 arithmetic
+ * throughout. bf16 inputs with a bf16 output run matrix products where d_k is at most 256 and
+ * rows are 16-byte aligned: scores and the state's copy read by the queries are rounded to
+ * bf16, the state itself is carried in float32 from products of three bf16 parts (float32
+ * accuracy). All other calls run float32 arithmetic.
+ * A NaN or infinity in a token's q, k, v or decay reaches only outputs of that token and later
+ * ones of its sequence, and the final state.
+ */
+#define RN_LINEAR_ZERO_REST (1u << 0)  /* chunked: rows of `out` behind each sequence (padded), or
+                                          behind the last one (packed), are set to zero */
+#define RN_LINEAR_GENERIC   (1u << 8)  /* take the float32 kernels (for testing) */
+
+typedef struct rn_linear_desc {
+    int32_t S;             /* sequences, 1 .. 65535 */
+    int32_t N;             /* most tokens of a sequence, 1 .. 2^30; the step form needs 1 */
+    int32_t H;             /* heads of the state, decays and output: 1 .. 65535 */
+    int32_t H_q, H_k, H_v; /* heads of q, k, v: divisors of H */
+    int32_t d_k;           /* 1 .. 256 */
+    int32_t d_v;           /* 1 .. 512 */
+    rn_dtype in_dtype;     /* q, k, v */
+    rn_dtype out_dtype;    /* out */
+    uint32_t flags;        /* RN_LINEAR_* */
+    float qk_scale;        /* finite */
+    int64_t T;             /* packed batches: token rows of the tensors, 1 .. 2^31 - 1; else 0 */
+    int32_t n_slots;       /* states in state_in / state_out where slots are given */
+    int64_t q_stride[3];   /* elements between sequences (ignored if packed), heads, tokens */
+    int64_t k_stride[3];
+    int64_t v_stride[3];
+    int64_t g_stride[3];
+    int64_t out_stride[3];
+} rn_linear_desc;
+
+/* Bytes of device workspace rn_linear_attention_chunked needs (0 when it needs none, or for an
+ * invalid descriptor). */
+size_t rn_linear_attention_workspace_bytes(const rn_linear_desc* desc);
+
+/*
+ * Prompts: every sequence's tokens at once.
+ * Padded (T = 0): sequence s holds lengths[s] tokens (DEVICE int32 [S], clamped to [0, N]; NULL
+ * = N) at rows s of the tensors. Packed (T > 0): cu_seqlens, DEVICE int32 [S+1], holds each
+ * sequence's first token row, 0 first; rows cu_seqlens[s] .. cu_seqlens[s+1]-1 are sequence s
+ * (clamped to [0, T] and to N tokens). Rows of no sequence are not written (but see
+ * RN_LINEAR_ZERO_REST).
+ * state_in, state_out: float32 [S, H, d_k, d_v], or [n_slots, H, d_k, d_v] with slots (DEVICE
+ * int32 [S]: the state of sequence s is slot slots[s]; one outside [0, n_slots) starts from
+ * zeros and keeps no state; two sequences must not share a slot). 16-byte aligned; NULL = start
+ * from zeros / discard; they may be the same buffer. A sequence without tokens passes its
+ * state on. workspace: 256-byte aligned, rn_linear_attention_workspace_bytes(desc) bytes.
+ */
+rn_status rn_linear_attention_chunked(const rn_linear_desc* desc, const int32_t* cu_seqlens,
+                                      const int32_t* lengths, const int32_t* slots, const void* q,
+                                      const void* k, const void* v, const float* log_decay,
+                                      const float* state_in, float* state_out, void* out,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One token for each of S sequences; `state` is updated in place (layout and slots as above; a
+ * sequence whose slot is outside [0, n_slots) is skipped and its output row set to zero).
+ */
+rn_status rn_linear_attention_step(const rn_linear_desc* desc, const int32_t* slots, const void* q,
+                                   const void* k, const void* v, const float* log_decay,
+                                   float* state, void* out, void* stream);
+
 /* Static name of a status code. */
 const char* rn_status_str(rn_status s);
 /* Message describing the last failure on the calling thread ("" if none). */

@@ -1,6 +1,7 @@
 """Multi-scale retention (RetNet) forward pass on MI355X — Python binding.
 
 A thin ctypes layer over ``librn_retention.so`` (C ABI in include/rn_retention.h).
+(The operators around retention live in block_ops.py and are exported here.)
 Functions carry the C names; they only marshal arguments: check tensors, allocate
 outputs with torch, pass device pointers and the current HIP stream. Every step of
 the computation runs in the library's HIP kernels. There is no CPU fallback: if the
@@ -30,6 +31,11 @@ __all__ = [
     "rn_retention_chunkwise_backward", "rn_chunkwise_backward_workspace_bytes", "rn_chunkwise_workspace_bytes", "rn_parallel_workspace_bytes",
     "rn_version", "make_desc", "rn_msr_layer_forward", "rn_msr_layer_workspace_bytes",
     "rn_retention_chunkwise_noalloc",
+    "RN_ROTARY_HALF", "RN_ROTARY_INVERSE", "RN_ROTARY_POS_TOKEN", "RN_ROPE_PLAIN", "RN_ROPE_LINEAR",
+    "RN_ROPE_BASE", "RN_ROPE_BY_PARTS", "RN_LINEAR_ZERO_REST", "RN_LINEAR_GENERIC",
+    "RnNormDesc", "RnRotaryDesc", "RnLinearDesc", "rn_layernorm", "rn_layernorm_backward",
+    "rn_layernorm_backward_workspace_bytes", "rn_rotary", "rn_rotary_frequencies",
+    "rn_linear_attention_chunked", "rn_linear_attention_step", "rn_linear_attention_workspace_bytes",
 ]
 
 # The in-tree build; RN_LIB_PATH names another build of the same sources (the host-side
@@ -52,6 +58,9 @@ EXPORTED_SYMBOLS = (
     "rn_version", "rn_retention_chunkwise_backward", "rn_chunkwise_backward_workspace_bytes",
     "rn_msr_layer_workspace_bytes", "rn_msr_layer_forward", "rn_chunkwise_check",
     "rn_retention_chunkwise_noalloc",
+    "rn_layernorm_forward", "rn_layernorm_backward", "rn_layernorm_backward_workspace_bytes",
+    "rn_rotary", "rn_rotary_frequencies", "rn_linear_attention_workspace_bytes",
+    "rn_linear_attention_chunked", "rn_linear_attention_step",
 )
 
 
@@ -575,3 +584,10 @@ def rn_chunkwise_check(q, v, gamma, theta, chunk, workspace, *, gn=False, gate=N
     if st not in (RN_OK, RN_ERR_EXCHANGE, RN_ERR_NONFINITE):
         _check(st)
     return st
+
+
+from .block_ops import (  # noqa: E402  (needs the library and the names above)
+    RN_LINEAR_GENERIC, RN_LINEAR_ZERO_REST, RN_ROPE_BASE, RN_ROPE_BY_PARTS, RN_ROPE_LINEAR, RN_ROPE_PLAIN,
+    RN_ROTARY_HALF, RN_ROTARY_INVERSE, RN_ROTARY_POS_TOKEN, RnLinearDesc, RnNormDesc, RnRotaryDesc,
+    rn_layernorm, rn_layernorm_backward, rn_layernorm_backward_workspace_bytes, rn_linear_attention_chunked,
+    rn_linear_attention_step, rn_linear_attention_workspace_bytes, rn_rotary, rn_rotary_frequencies)

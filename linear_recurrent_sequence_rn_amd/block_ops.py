@@ -1,0 +1,459 @@
+"""The operators around retention: layer norm (forward with the residual sum, backward),
+rotary positions, and linear attention with a decay per head and token.
+
+As the retention calls: the functions carry the C names and only marshal arguments. Tensors
+may have any strides as long as their last axis is contiguous (a projection's output split
+into heads needs no copy). Calls run on the current stream of their tensors' device; that
+device need not be the current one. New outputs are allocated with torch.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import numpy as np
+import torch
+
+from . import RN_BF16, RN_F32, _check, lib
+
+RN_ROTARY_HALF, RN_ROTARY_INVERSE, RN_ROTARY_POS_TOKEN = 1, 2, 4
+RN_ROPE_PLAIN, RN_ROPE_LINEAR, RN_ROPE_BASE, RN_ROPE_BY_PARTS = 0, 1, 2, 3
+RN_LINEAR_ZERO_REST, RN_LINEAR_GENERIC = 1, 1 << 8
+
+_i32, _i64, _f32, _f64, _vp, _sz = (ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_double,
+                                    ctypes.c_void_p, ctypes.c_size_t)
+
+
+class RnNormDesc(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("d", _i32), ("in_dtype", _i32), ("out_dtype", _i32), ("eps", _f32),
+                ("x_stride", _i64), ("res_stride", _i64), ("sum_stride", _i64), ("out_stride", _i64)]
+
+
+class RnRotaryDesc(ctypes.Structure):
+    _fields_ = [("B", _i32), ("N", _i32), ("H_q", _i32), ("H_k", _i32), ("d", _i32), ("rot", _i32),
+                ("dtype", _i32), ("flags", ctypes.c_uint32), ("pos0", _i64), ("magnitude", _f32),
+                ("theta", ctypes.c_void_p), ("q_stride", _i64 * 3), ("k_stride", _i64 * 3),
+                ("q_out_stride", _i64 * 3), ("k_out_stride", _i64 * 3)]
+
+
+class RnLinearDesc(ctypes.Structure):
+    _fields_ = [("S", _i32), ("N", _i32), ("H", _i32), ("H_q", _i32), ("H_k", _i32), ("H_v", _i32),
+                ("d_k", _i32), ("d_v", _i32), ("in_dtype", _i32), ("out_dtype", _i32),
+                ("flags", ctypes.c_uint32), ("qk_scale", _f32), ("T", _i64), ("n_slots", _i32),
+                ("q_stride", _i64 * 3), ("k_stride", _i64 * 3), ("v_stride", _i64 * 3),
+                ("g_stride", _i64 * 3), ("out_stride", _i64 * 3)]
+
+
+def _bind(L):
+    ND, RD, LD = (ctypes.POINTER(t) for t in (RnNormDesc, RnRotaryDesc, RnLinearDesc))
+    for name, args, res in (
+            ("rn_layernorm_forward", [ND] + [_vp] * 7, _i32),
+            ("rn_layernorm_backward_workspace_bytes", [ND], _sz),
+            ("rn_layernorm_backward", [ND] + [_vp] * 8 + [_sz, _vp], _i32),
+            ("rn_rotary", [RD] + [_vp] * 6, _i32),
+            ("rn_rotary_frequencies", [_i32, _f64, _i32, _f64, _f64, _f64, _f64, _vp, _vp], _i32),
+            ("rn_linear_attention_workspace_bytes", [LD], _sz),
+            ("rn_linear_attention_chunked", [LD] + [_vp] * 11 + [_sz, _vp], _i32),
+            ("rn_linear_attention_step", [LD] + [_vp] * 8, _i32)):
+        f = getattr(L, name)
+        f.argtypes, f.restype = args, res
+
+
+_bind(lib)
+_byref = ctypes.byref
+_CODES = {torch.float32: RN_F32, torch.bfloat16: RN_BF16}
+
+
+def _code(t: torch.dtype) -> int:
+    c = _CODES.get(t)
+    if c is None:
+        raise TypeError(f"unsupported dtype {t}; use float32 or bfloat16")
+    return c
+
+
+class _on:
+    """Makes ``device`` current for a call, where it is not already, and gives its current
+    stream. (A kernel launched on another device's stream would fail.)"""
+    __slots__ = ("device", "last")
+
+    def __init__(self, device):
+        self.device = device
+
+    def __enter__(self):
+        i = self.device.index
+        self.last = torch.cuda.current_device()
+        if i != self.last:
+            torch.cuda.set_device(i)
+        return torch.cuda.current_stream(i).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.device.index != self.last:
+            torch.cuda.set_device(self.last)
+
+
+def _device(first, *others):
+    """The GPU all given tensors live on."""
+    if not first.is_cuda:
+        raise ValueError("tensors must live on the GPU")
+    dev = first.device
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors must be on one device ({dev}); got {t.device}")
+    return dev
+
+
+def _p(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _whole(t, dtype, shape, name):
+    """A contiguous tensor of that type and shape, or None."""
+    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
+        raise ValueError(f"{name} must be contiguous {dtype} {tuple(shape)}; got {t.dtype} {tuple(t.shape)}")
+
+
+def _get_workspace(workspace, need, device):
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+    return workspace
+
+
+# ---- layer norm ---------------------------------------------------------------------------
+
+def _row_stride(t, name) -> int:
+    """Elements between the rows of [..., d]: leading axes must step like one axis."""
+    d = t.dim()
+    if t.is_contiguous():
+        return t.shape[-1]
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    stride, span = None, 1
+    for i in range(d - 2, -1, -1):
+        n, s = t.shape[i], t.stride(i)
+        if n == 1:
+            continue
+        if stride is None:
+            stride = s
+        elif s != stride * span:
+            raise ValueError(f"{name}: the leading axes must have one common row stride")
+        span *= n
+    return t.shape[-1] if stride is None else stride
+
+
+def _like(t, x, name):
+    if t is not None and (t.shape != x.shape or t.dtype != x.dtype):
+        raise ValueError(f"{name} must be {x.dtype} {tuple(x.shape)}; got {t.dtype} {tuple(t.shape)}")
+
+
+def rn_layernorm(x, weight=None, bias=None, eps=1e-5, *, residual=None, sum_out=None, out=None,
+                 out_dtype=None):
+    """Layer norm over the last axis of x [..., d], after adding ``residual`` (same shape and
+    type) where given. weight, bias: float32 [d] or None. Returns out, or (out, sum) where a
+    residual or ``sum_out`` is given; sum = x + residual in x's type (the next residual
+    stream). ``sum_out`` may be x or residual, ``out`` may be x."""
+    dev = _device(x, residual, weight, bias, sum_out, out)
+    d = x.shape[-1] if x.dim() else 0
+    if x.numel() == 0:
+        raise ValueError(f"x must be [..., d] with at least one row; got {tuple(x.shape)}")
+    _like(residual, x, "residual")
+    _whole(weight, torch.float32, (d,), "weight")
+    _whole(bias, torch.float32, (d,), "bias")
+    od = x.dtype if out_dtype is None else out_dtype
+    if out is None:
+        out = torch.empty(x.shape, dtype=od, device=dev)
+    elif out.shape != x.shape or (out_dtype is not None and out.dtype != od):
+        raise ValueError(f"out must be {od} {tuple(x.shape)}; got {out.dtype} {tuple(out.shape)}")
+    if sum_out is None:
+        if residual is not None:
+            sum_out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    else:
+        _like(sum_out, x, "sum_out")
+    desc = RnNormDesc(x.numel() // d, d, _code(x.dtype), _code(out.dtype), eps, _row_stride(x, "x"),
+                      0 if residual is None else _row_stride(residual, "residual"),
+                      0 if sum_out is None else _row_stride(sum_out, "sum_out"), _row_stride(out, "out"))
+    with _on(dev) as stream:
+        _check(lib.rn_layernorm_forward(_byref(desc), x.data_ptr(), _p(residual), _p(weight), _p(bias),
+                                        _p(sum_out), out.data_ptr(), stream))
+    return out if sum_out is None else (out, sum_out)
+
+
+def _norm_backward_desc(dout, x, eps, dsum, dx):
+    return RnNormDesc(x.numel() // x.shape[-1], x.shape[-1], _code(x.dtype), _code(dout.dtype), eps,
+                      _row_stride(x, "x"), 0 if dsum is None else _row_stride(dsum, "dsum"),
+                      _row_stride(dx, "dx"), _row_stride(dout, "dout"))
+
+
+def rn_layernorm_backward_workspace_bytes(dout, x) -> int:
+    return int(lib.rn_layernorm_backward_workspace_bytes(_byref(_norm_backward_desc(dout, x, 0.0, None, x))))
+
+
+def rn_layernorm_backward(dout, x, weight=None, eps=1e-5, *, dsum=None, dx=None, want_dweight=True,
+                          want_dbias=True, workspace=None):
+    """Gradients of ``rn_layernorm``: x are the rows it normalised (its sum where it had a
+    residual), ``dsum`` the gradient that reaches this sum by its other path, in x's type.
+    Returns a dict with dx (the gradient of x and of the residual; in x's type) and, unless not
+    wanted, dweight and dbias (float32 [d])."""
+    dev = _device(x, dout, weight, dsum, dx)
+    if x.numel() == 0:
+        raise ValueError(f"x must be [..., d] with at least one row; got {tuple(x.shape)}")
+    d = x.shape[-1]
+    if dout.shape != x.shape:
+        raise ValueError(f"dout must have x's shape {tuple(x.shape)}; got {tuple(dout.shape)}")
+    _whole(weight, torch.float32, (d,), "weight")
+    _like(dsum, x, "dsum")
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    else:
+        _like(dx, x, "dx")
+    desc = _norm_backward_desc(dout, x, eps, dsum, dx)
+    got = {"dx": dx}
+    if want_dweight:
+        got["dweight"] = torch.empty(d, dtype=torch.float32, device=dev)
+    if want_dbias:
+        got["dbias"] = torch.empty(d, dtype=torch.float32, device=dev)
+    with _on(dev) as stream:
+        if want_dweight or want_dbias:
+            workspace = _get_workspace(workspace, int(lib.rn_layernorm_backward_workspace_bytes(_byref(desc))), dev)
+            if workspace is not None:
+                _device(x, workspace)
+        else:
+            workspace = None
+        _check(lib.rn_layernorm_backward(
+            _byref(desc), dout.data_ptr(), x.data_ptr(), _p(weight), _p(dsum), dx.data_ptr(),
+            _p(got.get("dweight")), _p(got.get("dbias")), _p(workspace),
+            0 if workspace is None else workspace.numel(), stream))
+    return got
+
+
+# ---- rotary positions -----------------------------------------------------------------------
+
+def _bhn(t, name):
+    """Strides of [B, H, N, ...] with a contiguous last axis (if there is a fourth)."""
+    if t.dim() == 4 and t.shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    return (_i64 * 3)(*t.stride()[:3])
+
+
+def _new_like(t, shape=None, dtype=None):
+    """A new tensor of t's (or the given) shape [B, H, N, d], token-major in memory where t is."""
+    B, H, N, d = t.shape if shape is None else shape
+    dtype = t.dtype if dtype is None else dtype
+    if t.stride(1) < t.stride(2):
+        return torch.empty((B, N, H, d), dtype=dtype, device=t.device).transpose(1, 2)
+    return torch.empty((B, H, N, d), dtype=dtype, device=t.device)
+
+
+_NO_STRIDE = (_i64 * 3)()
+
+
+def rn_rotary(q, k=None, theta=None, *, pos0=0, pos=None, half=False, inverse=False, magnitude=1.0,
+              q_out=None, k_out=None):
+    """Rotary positions on q [B, H_q, N, d] and k [B, H_k, N, d] (k may be None): pair j of the
+    first 2 len(theta) coordinates of every head is turned by position * theta[j] and scaled by
+    ``magnitude``; the others are copied. Pairs are (2j, 2j+1), or (j, j + len(theta)) with
+    ``half``. ``inverse`` turns back: the transpose, so it takes output gradients to input
+    gradients. theta: host angles (float64 is kept). pos: device int64 [B] (positions of the
+    first tokens) or [B, N]; None = ``pos0`` + token. Returns q_out, or (q_out, k_out); an output
+    given may be its input (in place)."""
+    if theta is None:
+        raise ValueError("theta is required")
+    dev = _device(q, k, pos, q_out, k_out)
+    if q.dim() != 4 or (k is not None and (k.dim() != 4 or k.dtype != q.dtype or k.shape[0] != q.shape[0] or
+                                           k.shape[2:] != q.shape[2:])):
+        raise ValueError(f"expected q [B,H_q,N,d] and k [B,H_k,N,d] of one type; got {q.dtype} {tuple(q.shape)}"
+                         + ("" if k is None else f", {k.dtype} {tuple(k.shape)}"))
+    if q.numel() == 0 or (k is not None and k.numel() == 0):
+        raise ValueError("q and k must not be empty")
+    B, Hq, N, d = q.shape
+    th = np.ascontiguousarray(theta, dtype=np.float64)
+    if th.ndim != 1:
+        raise ValueError("theta must be one-dimensional")
+    flags = (RN_ROTARY_HALF if half else 0) | (RN_ROTARY_INVERSE if inverse else 0)
+    if pos is not None:
+        if pos.dtype != torch.int64 or not pos.is_contiguous() or tuple(pos.shape) not in ((B,), (B, N)):
+            raise ValueError(f"pos must be contiguous int64 [{B}] or [{B}, {N}]; got {pos.dtype} {tuple(pos.shape)}")
+        if pos.dim() == 2:
+            flags |= RN_ROTARY_POS_TOKEN
+    for t, like, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
+        if t is not None:
+            if like is None:
+                raise ValueError("k_out without k")
+            _like(t, like, name)
+    if q_out is None:
+        q_out = _new_like(q)
+    if k is not None and k_out is None:
+        k_out = _new_like(k)
+    desc = RnRotaryDesc(B, N, Hq, 0 if k is None else k.shape[1], d, 2 * th.size, _code(q.dtype), flags, pos0,
+                        magnitude, th.ctypes.data, _bhn(q, "q"), _NO_STRIDE if k is None else _bhn(k, "k"),
+                        _bhn(q_out, "q_out"), _NO_STRIDE if k is None else _bhn(k_out, "k_out"))
+    with _on(dev) as stream:
+        _check(lib.rn_rotary(_byref(desc), _p(pos), q.data_ptr(), _p(k), q_out.data_ptr(), _p(k_out), stream))
+    return q_out if k is None else (q_out, k_out)
+
+
+_ROPE_KINDS = {"plain": RN_ROPE_PLAIN, "linear": RN_ROPE_LINEAR, "base": RN_ROPE_BASE, "by_parts": RN_ROPE_BY_PARTS}
+
+
+def rn_rotary_frequencies(rot, base=10000.0, kind="plain", *, factor=1.0, length=4096.0, slow=1.0, fast=32.0):
+    """Angles of rot/2 coordinate pairs (float64 host array) and the magnitude to pass with
+    them. kind: "plain", or stretched for contexts ``factor`` times the trained ``length``:
+    "linear" (every angle / factor), "base" (a larger base), "by_parts" (pairs turning at most
+    ``slow`` times over the trained length / factor, those turning ``fast`` times unchanged,
+    mixed between)."""
+    if kind not in _ROPE_KINDS:
+        raise ValueError(f"kind must be one of {', '.join(_ROPE_KINDS)}; got {kind!r}")
+    theta = np.empty(max(int(rot) // 2, 1), dtype=np.float64)
+    m = _f32()
+    _check(lib.rn_rotary_frequencies(rot, base, _ROPE_KINDS[kind], factor, length, slow, fast, theta.ctypes.data,
+                                     ctypes.addressof(m)))
+    return theta, m.value
+
+
+# ---- linear attention -----------------------------------------------------------------------
+
+def _linear_shapes(q, k, v, g):
+    if not (q.dim() == k.dim() == v.dim() == 4):
+        raise ValueError(f"expected q [B,H_q,N,d_k], k [B,H_k,N,d_k], v [B,H_v,N,d_v]; got {tuple(q.shape)}, "
+                         f"{tuple(k.shape)}, {tuple(v.shape)}")
+    B, _, rows, dk = q.shape
+    if k.shape[0] != B or k.shape[2] != rows or k.shape[3] != dk or v.shape[0] != B or v.shape[2] != rows:
+        raise ValueError(f"q, k and v must agree in batch and tokens, q and k in d_k; got {tuple(q.shape)}, "
+                         f"{tuple(k.shape)}, {tuple(v.shape)}")
+    if not (q.dtype == k.dtype == v.dtype):
+        raise TypeError("q, k, v must share one dtype")
+    if g.dim() != 3 or g.dtype != torch.float32 or g.shape[0] != B or g.shape[2] != rows:
+        raise ValueError(f"log_decay must be float32 [{B}, H, {rows}]; got {g.dtype} {tuple(g.shape)}")
+
+
+def _linear_desc(q, k, v, g, S, N, T, n_slots, out_dtype, flags, qk_scale, out):
+    return RnLinearDesc(S, N, g.shape[1], q.shape[1], k.shape[1], v.shape[1], q.shape[3], v.shape[3], _code(q.dtype),
+                        _code(out_dtype), flags, qk_scale, T, n_slots, _bhn(q, "q"), _bhn(k, "k"), _bhn(v, "v"),
+                        (_i64 * 3)(*g.stride()), out)
+
+
+def _linear_out(out, q, v, H, out_dtype):
+    """The output and whether it is new."""
+    shape = (v.shape[0], H, v.shape[2], v.shape[3])
+    od = (q.dtype if out is None else out.dtype) if out_dtype is None else out_dtype
+    if out is None:
+        return _new_like(v, shape, od), True
+    if tuple(out.shape) != shape or out.dtype != od:
+        raise ValueError(f"out must be {od} {shape}; got {out.dtype} {tuple(out.shape)}")
+    return out, False
+
+
+def _int32(t, n, name):
+    if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != (n,) or not t.is_contiguous()):
+        raise ValueError(f"{name} must be contiguous int32 [{n}]; got {t.dtype} {tuple(t.shape)}")
+
+
+def _linear_state(s, shape, slots, name):
+    if s is None:
+        return
+    if s.dtype != torch.float32 or not s.is_contiguous() or s.dim() != 4 or tuple(s.shape[1:]) != shape[1:] or \
+            (slots is None and s.shape[0] != shape[0]) or s.shape[0] < 1:
+        raise ValueError(f"{name} must be contiguous float32 [{'slots' if slots is not None else shape[0]}, "
+                         f"{shape[1]}, {shape[2]}, {shape[3]}]; got {s.dtype} {tuple(s.shape)}")
+
+
+def _linear_call(q, k, v, g, qk_scale, lengths, cu, max_len, state_in, state_out, slots, out, out_dtype, generic):
+    B, rows = q.shape[0], q.shape[2]
+    if cu is not None:
+        if B != 1 or lengths is not None or cu.dim() != 1 or cu.numel() < 2:
+            raise ValueError("a packed batch is [1, H, T, d] with cu_seqlens [S + 1] and without lengths")
+        S, T, N = cu.numel() - 1, rows, rows
+    else:
+        S, T, N = B, 0, rows
+    if max_len is not None:
+        if not 1 <= max_len <= N:
+            raise ValueError(f"max_len={max_len} outside [1, {N}]")
+        N = max_len
+    flags = RN_LINEAR_GENERIC if generic else 0
+    H = g.shape[1]
+    out, new = _linear_out(out, q, v, H, out_dtype)
+    if new and (cu is not None or lengths is not None):
+        flags |= RN_LINEAR_ZERO_REST
+    if new and cu is None and N < rows:
+        out[:, :, N:].zero_()
+    shape = (S, H, q.shape[-1], v.shape[-1])
+    if slots is not None and state_out is True:
+        raise ValueError("with slots, state_out must be a tensor")
+    _linear_state(state_in, shape, slots, "state_in")
+    if state_out is True:
+        state_out = torch.empty(shape, dtype=torch.float32, device=q.device)
+    elif state_out is False:
+        state_out = None
+    else:
+        _linear_state(state_out, shape, slots, "state_out")
+    n_slots = 0
+    if slots is not None:
+        sizes = {s.shape[0] for s in (state_in, state_out) if s is not None}
+        if len(sizes) > 1:
+            raise ValueError("state_in and state_out must have the same number of slots")
+        n_slots = sizes.pop() if sizes else 1
+    return _linear_desc(q, k, v, g, S, N, T, n_slots, out.dtype, flags, qk_scale, _bhn(out, "out")), out, state_out
+
+
+def rn_linear_attention_workspace_bytes(q, k, v, log_decay, *, cu_seqlens=None, max_len=None, out_dtype=None,
+                                        force_generic=False) -> int:
+    """Bytes of workspace ``rn_linear_attention_chunked`` needs for these tensors."""
+    _linear_shapes(q, k, v, log_decay)
+    B, rows = q.shape[0], q.shape[2]
+    S, T = (B, 0) if cu_seqlens is None else (cu_seqlens.numel() - 1, rows)
+    o = (_i64 * 3)(log_decay.shape[1] * rows * v.shape[-1], rows * v.shape[-1], v.shape[-1])
+    desc = _linear_desc(q, k, v, log_decay, S, max_len or rows, T, 0, out_dtype or q.dtype,
+                        RN_LINEAR_GENERIC if force_generic else 0, 1.0, o)
+    return int(lib.rn_linear_attention_workspace_bytes(_byref(desc)))
+
+
+def rn_linear_attention_chunked(q, k, v, log_decay, *, qk_scale=1.0, lengths=None, cu_seqlens=None, max_len=None,
+                                state_in=None, state_out=None, slots=None, out=None, out_dtype=None,
+                                workspace=None, force_generic=False):
+    """Linear attention with a decay per head and token over prompts:
+    S_t = exp(g_t) S_{t-1} + k_t^T v_t, o_t = qk_scale q_t S_t; returns (out, state_out).
+
+    q [B, H_q, N, d_k], k [B, H_k, N, d_k], v [B, H_v, N, d_v]; log_decay float32 [B, H, N]
+    (<= 0; -inf clears the state; a stride of 0 along N gives one decay per head). H_q, H_k and
+    H_v divide H. Padded batch: ``lengths`` device int32 [B] or None. Packed batch: B = 1 and
+    ``cu_seqlens`` device int32 [S + 1], first entry 0. ``max_len``: no sequence is longer (host
+    number; longer ones are cut). Rows of no sequence are not written (zero in a new out).
+    state_in, state_out: float32 [S, H, d_k, d_v], or pools [slots, H, d_k, d_v] with ``slots``
+    device int32 [S] (distinct; -1: start from zeros, keep nothing); state_out may be True (new;
+    not with slots), None/False (discarded) or state_in itself."""
+    dev = _device(q, k, v, log_decay, lengths, cu_seqlens, slots, out, workspace, state_in,
+                  state_out if isinstance(state_out, torch.Tensor) else None)
+    _linear_shapes(q, k, v, log_decay)
+    desc, out, state_out = _linear_call(q, k, v, log_decay, qk_scale, lengths, cu_seqlens, max_len, state_in,
+                                        state_out, slots, out, out_dtype, force_generic)
+    _int32(lengths, desc.S, "lengths")
+    _int32(cu_seqlens, desc.S + 1, "cu_seqlens")
+    _int32(slots, desc.S, "slots")
+    with _on(dev) as stream:
+        workspace = _get_workspace(workspace, int(lib.rn_linear_attention_workspace_bytes(_byref(desc))), dev)
+        _check(lib.rn_linear_attention_chunked(
+            _byref(desc), _p(cu_seqlens), _p(lengths), _p(slots), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            log_decay.data_ptr(), _p(state_in), _p(state_out), out.data_ptr(), _p(workspace),
+            0 if workspace is None else workspace.numel(), stream))
+    return out, state_out
+
+
+def rn_linear_attention_step(q, k, v, log_decay, state, *, qk_scale=1.0, slots=None, out=None, out_dtype=None):
+    """One token for each of S sequences: q [S, H_q, 1, d_k], k, v, log_decay [S, H, 1] as in
+    ``rn_linear_attention_chunked``; ``state`` (float32 [S, H, d_k, d_v], or a pool with ``slots``)
+    is updated in place. Returns out [S, H, 1, d_v]; a sequence with slot -1 is skipped, its row
+    of out set to zero."""
+    dev = _device(q, k, v, log_decay, state, slots, out)
+    _linear_shapes(q, k, v, log_decay)
+    if q.shape[2] != 1:
+        raise ValueError(f"the step takes one token a sequence: q [S,H_q,1,d_k]; got {tuple(q.shape)}")
+    S, H = q.shape[0], log_decay.shape[1]
+    out, _ = _linear_out(out, q, v, H, out_dtype)
+    _linear_state(state, (S, H, q.shape[-1], v.shape[-1]), slots, "state")
+    _int32(slots, S, "slots")
+    desc = _linear_desc(q, k, v, log_decay, S, 1, 0, state.shape[0], out.dtype, 0, qk_scale, _bhn(out, "out"))
+    with _on(dev) as stream:
+        _check(lib.rn_linear_attention_step(_byref(desc), _p(slots), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                            log_decay.data_ptr(), state.data_ptr(), out.data_ptr(), stream))
+    return out

@@ -1,0 +1,84 @@
+// Linear attention with a decay per head and token: what its kernels share.
+#pragma once
+#include "rn_kernels.h"
+
+namespace rn {
+
+// Where a kernel starts and ends: a whole sequence; the state a segment adds on its own
+// (first pass over a sequence cut into segments); the outputs of a segment whose starting
+// state the scan left in the workspace (third pass).
+enum LinMode : int { kLinWhole = 0, kLinState = 1, kLinOut = 2 };
+
+struct LinArgs {
+  int32_t S, N, H, Hq, Hk, Hv, dk, dv;
+  int32_t n_slots;
+  int32_t seg_len, n_seg;     // tokens a segment (a multiple of 64), most segments a sequence
+  int64_t T;                  // packed rows, 0 for a padded batch
+  float scale;
+  bool zero_rest;
+  int64_t qs[3], ks[3], vs[3], gs[3], os[3];
+  const int32_t* cu;
+  const int32_t* lens;
+  const int32_t* slots;
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* g;
+  const float* state_in;
+  float* state_out;
+  void* out;
+  float* seg_state;           // [segments][H][dk][dv]
+  float* seg_decay;           // [segments][H]
+};
+
+// First token row (packed), number of tokens, and number of rows of sequence s, whatever the
+// device arrays hold: never outside the tensors. Sequence S of a packed batch is the rows
+// behind the last one.
+__device__ __forceinline__ void lin_span(const LinArgs& a, int s, int64_t* row0, int* len, int64_t* own) {
+  if (a.T > 0) {
+    const int64_t b = min(max(static_cast<int64_t>(a.cu[s]), int64_t(0)), a.T);
+    const int64_t e = s == a.S ? a.T : min(max(static_cast<int64_t>(a.cu[s + 1]), b), a.T);
+    *row0 = b;
+    *own = e - b;
+    *len = s == a.S ? 0 : static_cast<int>(min(e - b, static_cast<int64_t>(a.N)));
+  } else {
+    *row0 = 0;
+    *own = a.N;
+    *len = a.lens ? min(max(a.lens[s], 0), a.N) : a.N;
+  }
+}
+// Offset of the sequence's first token in a tensor with strides st (head and token aside).
+__device__ __forceinline__ int64_t lin_base(const LinArgs& a, const int64_t* st, int s, int64_t row0) {
+  return a.T > 0 ? row0 * st[2] : s * st[0];
+}
+// Index of the state of sequence s in the caller's buffers, or -1.
+__device__ __forceinline__ int lin_slot(const LinArgs& a, int s) {
+  if (!a.slots) return s;
+  const int x = a.slots[s];
+  return x >= 0 && x < a.n_slots ? x : -1;
+}
+// Row of segment g of sequence s in the workspace: distinct for all segments of a packed
+// batch (a sequence starting at row r owns r/L + s on), below lin_segments() always.
+__device__ __forceinline__ int64_t lin_segment(const LinArgs& a, int s, int64_t row0, int g) {
+  return a.T > 0 ? row0 / a.seg_len + s + g : static_cast<int64_t>(s) * a.n_seg + g;
+}
+// Zeros into the columns [c0, c0 + nc) of head h in the rows of sequence s behind its tokens
+// (flag RN_LINEAR_ZERO_REST); the blocks of its segments share them.
+template <int OUT>
+__device__ __forceinline__ void lin_zero_rest(const LinArgs& a, int s, int g, int h, int c0, int nc,
+                                              int64_t row0, int len, int64_t own) {
+  const int64_t base = (a.T > 0 ? row0 * a.os[2] : s * a.os[0]) + h * a.os[1] + c0;
+  const int64_t step = static_cast<int64_t>(a.n_seg) * a.seg_len;
+  for (int64_t t0 = len + static_cast<int64_t>(g) * a.seg_len; t0 < own; t0 += step) {
+    const int64_t n = min(own - t0, static_cast<int64_t>(a.seg_len)) * nc;
+    for (int64_t i = threadIdx.x; i < n; i += blockDim.x)
+      Elem<OUT>::store(a.out, base + (t0 + i / nc) * a.os[2] + i % nc, 0.f);
+  }
+}
+
+// Matrix-core kernel (bf16 in and out, whole 16-byte rows).
+bool lin_mfma_supported(const LinCall& c);
+int lin_mfma_blocks(const LinCall& c);     // blocks a sequence and segment takes
+hipError_t launch_lin_mfma(const LinArgs& a, LinMode mode, hipStream_t st);
+
+}  // namespace rn

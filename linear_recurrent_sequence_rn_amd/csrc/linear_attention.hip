@@ -1,0 +1,393 @@
+// Linear attention with a decay per head and token, in float32:
+//     S_t = exp(g_t) S_{t-1} + k_t^T v_t,     o_t = scale q_t S_t.
+//
+// lin_step: one token a sequence. Bound by HBM: the float32 state is read and written once.
+// lin_recurrent: prompts of any type and head size by the recurrence itself, token by token,
+// the state in registers. Bound by the vector units: three multiply-adds a state element
+// and token. Long sequences are cut into segments: one pass gives the state each
+// segment adds on its own, lin_scan carries the states over the segments, a second pass
+// gives the outputs; the same three passes carry the matrix-core kernel's segments.
+#include <algorithm>
+
+#include "linear_attention.h"
+
+namespace rn {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+// ---- one token a sequence ---------------------------------------------------------------
+// A block owns NQ * VEC columns of one (sequence, head) state; thread (group, column vector)
+// takes rows group, group + G, ... in batches of 8, the next batch's loads issued before
+// the present one is updated. Non-temporal: a batch's states are larger than the caches and
+// are read once a step.
+constexpr int kStepThreads = 256;
+constexpr int kBatch = 8;
+
+template <int IN, int OUT, int VEC, int NQ>
+__global__ void __launch_bounds__(kStepThreads) lin_step(LinArgs a, int slices) {
+  constexpr int G = kStepThreads / NQ;
+  constexpr int W = NQ * VEC;
+  __shared__ float qh[kMaxDk];
+  __shared__ float kh[kMaxDk];
+  __shared__ float part[G * W];
+  const int h = blockIdx.x / slices, c0 = (blockIdx.x - h * slices) * W;
+  const int s = blockIdx.y, tid = threadIdx.x;
+  const int cq = tid % NQ, grp = tid / NQ;
+  const int slot = lin_slot(a, s);
+  const int64_t oo = s * a.os[0] + h * a.os[1] + c0;
+  const int nc = min(W, a.dv - c0);
+  if (slot < 0) {
+    for (int c = tid; c < nc; c += kStepThreads) Elem<OUT>::store(a.out, oo + c, 0.f);
+    return;
+  }
+  const int64_t qo = s * a.qs[0] + h / (a.H / a.Hq) * a.qs[1];
+  const int64_t ko = s * a.ks[0] + h / (a.H / a.Hk) * a.ks[1];
+  const int64_t vo = s * a.vs[0] + h / (a.H / a.Hv) * a.vs[1] + c0;
+  for (int d = tid; d < a.dk; d += kStepThreads) {
+    qh[d] = Elem<IN>::load(a.q, qo + d);
+    kh[d] = Elem<IN>::load(a.k, ko + d);
+  }
+  const bool col = cq * VEC < nc;
+  const float dec = expf(a.g[s * a.gs[0] + h * a.gs[1]]);
+  float vr[VEC], acc[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    vr[i] = col ? Elem<IN>::load(a.v, vo + cq * VEC + i) : 0.f;
+    acc[i] = 0.f;
+  }
+  float* S = a.state_out + (static_cast<int64_t>(slot) * a.H + h) * a.dk * a.dv + c0 + cq * VEC;
+  const int dv = a.dv;
+  auto load = [&](int d0, float (*x)[VEC]) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int d = d0 + u * G;
+      if (col && d < a.dk) {
+        if constexpr (VEC == 4) {
+          const f32x4 y = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(S + static_cast<int64_t>(d) * dv));
+          x[u][0] = y.x; x[u][1] = y.y; x[u][2] = y.z; x[u][3] = y.w;
+        } else {
+          x[u][0] = __builtin_nontemporal_load(S + static_cast<int64_t>(d) * dv);
+        }
+      }
+    }
+  };
+  auto update = [&](int d0, float (*x)[VEC]) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int d = d0 + u * G;
+      if (col && d < a.dk) {
+        const float kd = kh[d], qd = qh[d];
+        float y[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          y[i] = fmaf(dec, x[u][i], kd * vr[i]);
+          acc[i] = fmaf(qd, y[i], acc[i]);
+        }
+        if constexpr (VEC == 4) {
+          const f32x4 z = {y[0], y[1], y[2], y[3]};
+          __builtin_nontemporal_store(z, reinterpret_cast<f32x4*>(S + static_cast<int64_t>(d) * dv));
+        } else {
+          __builtin_nontemporal_store(y[0], S + static_cast<int64_t>(d) * dv);
+        }
+      }
+    }
+  };
+  float xa[kBatch][VEC], xb[kBatch][VEC];
+  load(grp, xa);
+  __syncthreads();
+  for (int d0 = grp; d0 < a.dk; d0 += 2 * G * kBatch) {
+    load(d0 + G * kBatch, xb);
+    update(d0, xa);
+    load(d0 + 2 * G * kBatch, xa);
+    update(d0 + G * kBatch, xb);
+  }
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) part[grp * W + cq * VEC + i] = acc[i];
+  __syncthreads();
+  for (int c = tid; c < nc; c += kStepThreads) {
+    float o = 0.f;
+    for (int i = 0; i < G; ++i) o += part[i * W + c];
+    Elem<OUT>::store(a.out, oo + c, a.scale * o);
+  }
+}
+
+// ---- prompts by the recurrence ------------------------------------------------------------
+// A block owns 64 columns of one head's state over one segment of one sequence: lane = column,
+// wave w holds the rows [w RW, (w+1) RW) in registers (rows past d_k stay zero). Tokens come
+// in blocks of 16 through LDS, the next block's loads in flight meanwhile; the four waves'
+// shares of each output meet in LDS.
+constexpr int kTok = 16;
+constexpr int kCols = 64;
+
+template <int IN, int OUT, int RW, LinMode MODE>
+__global__ void __launch_bounds__(256) lin_recurrent(LinArgs a, int slices) {
+  constexpr int D = 4 * RW;
+  constexpr int E = kTok * D / 256;       // q (or k) elements a thread stages
+  __shared__ float qt[kTok][D];
+  __shared__ float kt[kTok][D];
+  __shared__ float vt[kTok][kCols];
+  __shared__ float gt[kTok];
+  __shared__ float part[4][kTok][kCols];
+  const int h = blockIdx.x / slices, c0 = (blockIdx.x - h * slices) * kCols;
+  const int seg = blockIdx.y, s = blockIdx.z;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int nc = min(kCols, a.dv - c0);
+  int64_t row0, own;
+  int len;
+  lin_span(a, s, &row0, &len, &own);
+  if (MODE != kLinState && a.zero_rest) lin_zero_rest<OUT>(a, s, seg, h, c0, nc, row0, len, own);
+  if (s == a.S) return;
+  const int t0 = seg * a.seg_len;
+  const int t1 = min(len, t0 + a.seg_len);
+  const int slot = lin_slot(a, s);
+  const int64_t sh = static_cast<int64_t>(a.dk) * a.dv;
+  const bool keep = a.state_out && slot >= 0;
+  if (MODE == kLinWhole ? (len == 0 && !keep) : t0 >= t1) return;
+  if (MODE == kLinState && t1 == len && !keep) return;   // nobody reads the last segment's state
+
+  float S[RW];
+  {
+    const float* from = MODE == kLinWhole ? (a.state_in && slot >= 0 ? a.state_in + (static_cast<int64_t>(slot) * a.H + h) * sh : nullptr)
+                        : MODE == kLinOut ? a.seg_state + (lin_segment(a, s, row0, seg) * a.H + h) * sh
+                                          : nullptr;
+#pragma unroll
+    for (int r = 0; r < RW; ++r) {
+      const int d = wave * RW + r;
+      S[r] = from && d < a.dk && lane < nc ? from[static_cast<int64_t>(d) * a.dv + c0 + lane] : 0.f;
+    }
+  }
+  const int64_t qo = lin_base(a, a.qs, s, row0) + h / (a.H / a.Hq) * a.qs[1];
+  const int64_t ko = lin_base(a, a.ks, s, row0) + h / (a.H / a.Hk) * a.ks[1];
+  const int64_t vo = lin_base(a, a.vs, s, row0) + h / (a.H / a.Hv) * a.vs[1] + c0;
+  const int64_t go = lin_base(a, a.gs, s, row0) + h * a.gs[1];
+  const int64_t oo = lin_base(a, a.os, s, row0) + h * a.os[1] + c0;
+
+  float rq[E], rk[E], rv[kTok * kCols / 256], rg = 0.f;
+  auto fetch = [&](int t) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int i = tid + 256 * e, tt = t + i / D, d = i % D;
+      const bool ok = tt < t1 && d < a.dk;
+      if constexpr (MODE != kLinState) rq[e] = ok ? Elem<IN>::load(a.q, qo + tt * a.qs[2] + d) : 0.f;
+      rk[e] = ok ? Elem<IN>::load(a.k, ko + tt * a.ks[2] + d) : 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < kTok * kCols / 256; ++e) {
+      const int i = tid + 256 * e, tt = t + i / kCols, c = i % kCols;
+      rv[e] = tt < t1 && c < nc ? Elem<IN>::load(a.v, vo + tt * a.vs[2] + c) : 0.f;
+    }
+    if (tid < kTok) rg = t + tid < t1 ? a.g[go + (t + tid) * a.gs[2]] : 0.f;
+  };
+  double gsum = 0.0;
+  fetch(t0);
+  for (int t = t0; t < t1; t += kTok) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int i = tid + 256 * e;
+      if constexpr (MODE != kLinState) qt[i / D][i % D] = rq[e];
+      kt[i / D][i % D] = rk[e];
+    }
+#pragma unroll
+    for (int e = 0; e < kTok * kCols / 256; ++e) {
+      const int i = tid + 256 * e;
+      vt[i / kCols][i % kCols] = rv[e];
+    }
+    if (tid < kTok) gt[tid] = rg;
+    __syncthreads();
+    const int n = min(kTok, t1 - t);
+    fetch(t + kTok);
+    for (int i = 0; i < n; ++i) {
+      const float gi = gt[i];
+      if (MODE == kLinState) gsum += gi;
+      const float dec = expf(gi);
+      const float vv = vt[i][lane];
+      float acc = 0.f;
+#pragma unroll
+      for (int r = 0; r < RW; r += 4) {
+        const float4 k4 = *reinterpret_cast<const float4*>(&kt[i][wave * RW + r]);
+        S[r] = fmaf(dec, S[r], k4.x * vv);
+        S[r + 1] = fmaf(dec, S[r + 1], k4.y * vv);
+        S[r + 2] = fmaf(dec, S[r + 2], k4.z * vv);
+        S[r + 3] = fmaf(dec, S[r + 3], k4.w * vv);
+        if constexpr (MODE != kLinState) {
+          const float4 q4 = *reinterpret_cast<const float4*>(&qt[i][wave * RW + r]);
+          acc = fmaf(q4.x, S[r], acc);
+          acc = fmaf(q4.y, S[r + 1], acc);
+          acc = fmaf(q4.z, S[r + 2], acc);
+          acc = fmaf(q4.w, S[r + 3], acc);
+        }
+      }
+      if constexpr (MODE != kLinState) part[wave][i][lane] = acc;
+    }
+    __syncthreads();
+    if constexpr (MODE != kLinState) {
+#pragma unroll
+      for (int e = 0; e < kTok / 4; ++e) {
+        const int i = wave + 4 * e;
+        if (i < n && lane < nc)
+          Elem<OUT>::store(a.out, oo + (t + i) * a.os[2] + lane,
+                           a.scale * ((part[0][i][lane] + part[1][i][lane]) + (part[2][i][lane] + part[3][i][lane])));
+      }
+    }
+  }
+  float* to = nullptr;
+  if (MODE == kLinWhole && keep) to = a.state_out + (static_cast<int64_t>(slot) * a.H + h) * sh;
+  if (MODE == kLinState) {
+    const int64_t i = lin_segment(a, s, row0, seg) * a.H + h;
+    to = a.seg_state + i * sh;
+    if (c0 == 0 && tid == 0) a.seg_decay[i] = expf(static_cast<float>(gsum));
+  }
+  if (to && lane < nc) {
+#pragma unroll
+    for (int r = 0; r < RW; ++r) {
+      const int d = wave * RW + r;
+      if (d < a.dk) to[static_cast<int64_t>(d) * a.dv + c0 + lane] = S[r];
+    }
+  }
+}
+
+// ---- states over the segments ---------------------------------------------------------------
+// One thread a state element: the segments' own states become the states they start from,
+// and the last one the final state.
+__global__ void __launch_bounds__(256) lin_scan(LinArgs a) {
+  const int h = blockIdx.y, s = blockIdx.z;
+  const int64_t sh = static_cast<int64_t>(a.dk) * a.dv;
+  const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (e >= sh) return;
+  int64_t row0, own;
+  int len;
+  lin_span(a, s, &row0, &len, &own);
+  const int slot = lin_slot(a, s);
+  const int n = (len + a.seg_len - 1) / a.seg_len;
+  const int64_t at = (static_cast<int64_t>(slot) * a.H + h) * sh + e;
+  float x = a.state_in && slot >= 0 ? a.state_in[at] : 0.f;
+  const int64_t first = lin_segment(a, s, row0, 0) * a.H + h;
+  const bool last = a.state_out && slot >= 0;
+  float* p = a.seg_state + first * sh + e;
+  const float* d = a.seg_decay + first;
+  const int64_t ps = sh * a.H;
+  // eight segments' states in flight
+  for (int g = 0; g < n; g += 8) {
+    float u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = g + i < n && (last || g + i + 1 < n) ? p[(g + i) * ps] : 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (g + i < n) {
+        p[(g + i) * ps] = x;
+        if (last || g + i + 1 < n) x = fmaf(d[static_cast<int64_t>(g + i) * a.H], x, u[i]);
+      }
+  }
+  if (last) a.state_out[at] = x;
+}
+
+template <int IN, int OUT, LinMode MODE>
+hipError_t launch_recurrent_t(const LinArgs& a, hipStream_t st) {
+  const int slices = (a.dv + kCols - 1) / kCols;
+  const bool rest = a.T > 0 && a.zero_rest && MODE != kLinState;
+  const dim3 grid(a.H * slices, a.n_seg, a.S + (rest ? 1 : 0));
+  const int rw = (a.dk + 3) / 4;
+  if (rw <= 16) hipLaunchKernelGGL((lin_recurrent<IN, OUT, 16, MODE>), grid, dim3(256), 0, st, a, slices);
+  else if (rw <= 32) hipLaunchKernelGGL((lin_recurrent<IN, OUT, 32, MODE>), grid, dim3(256), 0, st, a, slices);
+  else hipLaunchKernelGGL((lin_recurrent<IN, OUT, 64, MODE>), grid, dim3(256), 0, st, a, slices);
+  return hipGetLastError();
+}
+
+template <LinMode MODE>
+hipError_t launch_recurrent(const LinArgs& a, int in_dt, int out_dt, hipStream_t st) {
+  if (in_dt == RN_F32)
+    return out_dt == RN_F32 ? launch_recurrent_t<RN_F32, RN_F32, MODE>(a, st) : launch_recurrent_t<RN_F32, RN_BF16, MODE>(a, st);
+  return out_dt == RN_F32 ? launch_recurrent_t<RN_BF16, RN_F32, MODE>(a, st) : launch_recurrent_t<RN_BF16, RN_BF16, MODE>(a, st);
+}
+
+template <int IN, int OUT>
+hipError_t launch_step_t(const LinArgs& a, hipStream_t st) {
+  // Columns a block: as many as the row has (long runs of one state row), but fewer where
+  // that leaves the chip's 256 CUs without two blocks each (states are independent by column).
+  const int64_t states = static_cast<int64_t>(a.S) * a.H;
+#define RN_STEP(VEC, NQ)                                                                            \
+  do {                                                                                              \
+    const int slices = (a.dv + VEC * NQ - 1) / (VEC * NQ);                                          \
+    hipLaunchKernelGGL((lin_step<IN, OUT, VEC, NQ>), dim3(a.H * slices, a.S), dim3(kStepThreads), 0, st, a, slices); \
+    return hipGetLastError();                                                                       \
+  } while (0)
+  if (a.dv % 4 == 0) {
+    if (a.dv >= 256 && states * ((a.dv + 255) / 256) >= 512) RN_STEP(4, 64);
+    if (a.dv >= 128 && states * ((a.dv + 127) / 128) >= 512) RN_STEP(4, 32);
+    if (a.dv >= 64 && states * ((a.dv + 63) / 64) >= 512) RN_STEP(4, 16);
+    RN_STEP(4, 4);
+  }
+  RN_STEP(1, 64);
+#undef RN_STEP
+}
+
+// Tokens a segment, and how many segments the longest sequence has: one segment where the
+// sequences and heads fill the chip by themselves, else enough segments for `want` blocks.
+void segments(const LinCall& c, int* len, int* n) {
+  const int64_t per = lin_use_mfma(c) ? lin_mfma_blocks(c) : static_cast<int64_t>(c.H) * ((c.dv + kCols - 1) / kCols);
+  const int64_t tokens = c.T > 0 ? std::min<int64_t>(c.T, static_cast<int64_t>(c.S) * c.N) : static_cast<int64_t>(c.S) * c.N;
+  const int64_t want = 512;
+  int64_t L = tokens * per / want;
+  L = std::max<int64_t>((L + 63) / 64 * 64, 256);
+  if (2 * L > c.N) L = c.N;
+  L = std::max<int64_t>(L, (c.N + 65534) / 65535);
+  L = (L + 63) / 64 * 64;
+  *len = static_cast<int>(L);
+  *n = static_cast<int>((c.N + L - 1) / L);
+}
+
+int64_t total_segments(const LinCall& c, int len, int n) {
+  return c.T > 0 ? c.T / len + c.S : static_cast<int64_t>(c.S) * n;
+}
+
+}  // namespace
+
+bool lin_use_mfma(const LinCall&) { return false; }
+int lin_mfma_blocks(const LinCall&) { return 1; }
+hipError_t launch_lin_mfma(const LinArgs&, LinMode, hipStream_t) { return hipErrorInvalidValue; }
+
+size_t lin_ws_bytes(const LinCall& c) {
+  int len, n;
+  segments(c, &len, &n);
+  if (n == 1) return 0;
+  const size_t rows = static_cast<size_t>(total_segments(c, len, n)) * c.H;
+  return rows * sizeof(float) * c.dk * c.dv + ((rows * sizeof(float) + 255) & ~size_t(255));
+}
+
+static LinArgs lin_args(const LinCall& c) {
+  LinArgs a;
+  a.S = c.S; a.N = c.N; a.H = c.H; a.Hq = c.Hq; a.Hk = c.Hk; a.Hv = c.Hv; a.dk = c.dk; a.dv = c.dv;
+  a.n_slots = c.n_slots; a.T = c.T; a.scale = c.scale; a.zero_rest = c.zero_rest;
+  for (int i = 0; i < 3; ++i) {
+    a.qs[i] = c.qs[i]; a.ks[i] = c.ks[i]; a.vs[i] = c.vs[i]; a.gs[i] = c.gs[i]; a.os[i] = c.os[i];
+  }
+  a.cu = c.cu; a.lens = c.lens; a.slots = c.slots;
+  a.q = c.q; a.k = c.k; a.v = c.v; a.g = c.g; a.state_in = c.state_in; a.state_out = c.state_out; a.out = c.out;
+  a.seg_len = c.N; a.n_seg = 1; a.seg_state = nullptr; a.seg_decay = nullptr;
+  return a;
+}
+
+hipError_t launch_linear_step(const LinCall& c, hipStream_t st) {
+  const LinArgs a = lin_args(c);
+  if (c.in_dt == RN_F32)
+    return c.out_dt == RN_F32 ? launch_step_t<RN_F32, RN_F32>(a, st) : launch_step_t<RN_F32, RN_BF16>(a, st);
+  return c.out_dt == RN_F32 ? launch_step_t<RN_BF16, RN_F32>(a, st) : launch_step_t<RN_BF16, RN_BF16>(a, st);
+}
+
+hipError_t launch_linear_chunked(const LinCall& c, hipStream_t st) {
+  LinArgs a = lin_args(c);
+  segments(c, &a.seg_len, &a.n_seg);
+  const bool mfma = lin_use_mfma(c);
+  if (a.n_seg == 1) return mfma ? launch_lin_mfma(a, kLinWhole, st) : launch_recurrent<kLinWhole>(a, c.in_dt, c.out_dt, st);
+  const size_t rows = static_cast<size_t>(total_segments(c, a.seg_len, a.n_seg)) * c.H;
+  a.seg_decay = static_cast<float*>(c.ws);
+  a.seg_state = a.seg_decay + ((rows + 63) & ~size_t(63));
+  hipError_t e = mfma ? launch_lin_mfma(a, kLinState, st) : launch_recurrent<kLinState>(a, c.in_dt, c.out_dt, st);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(lin_scan, dim3((c.dk * c.dv + 255) / 256, c.H, c.S), dim3(256), 0, st, a);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  return mfma ? launch_lin_mfma(a, kLinOut, st) : launch_recurrent<kLinOut>(a, c.in_dt, c.out_dt, st);
+}
+
+}  // namespace rn

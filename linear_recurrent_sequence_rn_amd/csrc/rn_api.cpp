@@ -14,8 +14,10 @@
 #include "rn_retention.h"
 
 namespace {
-
 thread_local char g_err[512] = "";
+}
+
+namespace rn {
 
 rn_status fail(rn_status s, const char* fmt, ...) {
   va_list ap;
@@ -29,6 +31,15 @@ rn_status hip_status(hipError_t e, const char* what) {
   if (e == hipSuccess) return RN_OK;
   return fail(RN_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
+
+void clear_error() { g_err[0] = 0; }
+
+}  // namespace rn
+
+namespace {
+
+using rn::fail;
+using rn::hip_status;
 
 enum class Form { kParallel, kChunkwise, kStep };
 

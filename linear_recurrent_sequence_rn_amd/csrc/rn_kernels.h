@@ -82,4 +82,74 @@ int layer_output(const LayerArgs& L, const void* o, void* ot, const void* w_o, v
                  int out_dtype, hipStream_t stream);
 const char* blas_status_string(int status);
 
+// ---- operators around retention (layernorm.hip, rotary.hip, linear_attention.hip) ----------
+struct NormCall {
+  int64_t rows;
+  int32_t d;
+  int in_dt, out_dt;
+  float eps;
+  bool backward;
+  bool vec;                       // every row and pointer allows 16-byte accesses
+  int64_t xs, rs, ss, os;         // row strides: x, residual / dsum, sum_out / dx, out / dout
+  const void* x;
+  const void* r;
+  const float* w;
+  const float* b;
+  void* sum;
+  void* out;
+  const void* dout;
+  float* dw;
+  float* db;
+  void* ws;
+};
+size_t norm_backward_ws_bytes(const NormCall& n);
+hipError_t launch_layernorm(const NormCall& n, hipStream_t st);
+
+constexpr int kMaxRot = 256;
+struct RotaryCall {
+  int32_t B, N, Hq, Hk, d, rot;
+  int dt;
+  bool half, inverse, pos_token;
+  float magnitude;
+  int64_t pos0;
+  const int64_t* pos;
+  const double* theta;            // host
+  const int64_t *qs, *ks, *qos, *kos;   // host [3]: batch, head, token
+  const void* q;
+  const void* k;
+  void* q_out;
+  void* k_out;
+};
+hipError_t launch_rotary(const RotaryCall& c, hipStream_t st);
+
+struct LinCall {
+  int32_t S, N, H, Hq, Hk, Hv, dk, dv;
+  int in_dt, out_dt;
+  bool generic, zero_rest;
+  float scale;
+  int64_t T;
+  int32_t n_slots;
+  const int64_t *qs, *ks, *vs, *gs, *os;   // host [3]: sequence, head, token
+  const int32_t* cu;
+  const int32_t* lens;
+  const int32_t* slots;
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* g;
+  const float* state_in;
+  float* state_out;
+  void* out;
+  void* ws;
+};
+bool lin_use_mfma(const LinCall& c);
+size_t lin_ws_bytes(const LinCall& c);
+hipError_t launch_linear_step(const LinCall& c, hipStream_t st);
+hipError_t launch_linear_chunked(const LinCall& c, hipStream_t st);
+
+// Records the message of a failed call (rn_last_error) and returns its status.
+rn_status fail(rn_status s, const char* fmt, ...);
+rn_status hip_status(hipError_t e, const char* what);
+void clear_error();
+
 }  // namespace rn

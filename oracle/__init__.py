@@ -7,7 +7,9 @@ tests/test_oracle_backward.py (gradients against central finite differences of t
 forward oracle), tests/test_oracle_vector.py (pair decays: reduction to the scalar
 oracle, decomposition by coordinate pair, agreement of the forms) and
 tests/test_oracle_layer.py (the gated multi-scale layer: explicit loops, identity
-projections, head permutation); no function here is left unpinned.
+projections, head permutation) and tests/test_oracle_block.py (layer norm, rotary
+positions, linear attention: finite differences, closed forms, agreement with the
+retention oracle); no function here is left unpinned.
 """
 from .retention import *  # noqa: F401,F403
 from .retention import __all__ as _fwd_all
@@ -17,4 +19,6 @@ from .vector_decay import __all__ as _vec_all
 from .layer import *  # noqa: F401,F403
 from .layer import __all__ as _layer_all
 
-__all__ = list(_fwd_all) + ["backward"] + list(_vec_all) + list(_layer_all)
+from . import block  # noqa: F401
+
+__all__ = list(_fwd_all) + ["backward", "block"] + list(_vec_all) + list(_layer_all)

@@ -1,0 +1,205 @@
+"""Host-side checks of the operators around retention (no GPU needed): invalid arguments are
+rejected before any HIP call. Pointers passed here are never dereferenced."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import linear_recurrent_sequence_rn_amd as rn
+
+FAKE = 0x10000
+L = rn.lib
+INV, UNS, WS = rn.RN_ERR_INVALID_ARG, rn.RN_ERR_UNSUPPORTED, rn.RN_ERR_WORKSPACE
+
+
+def fill(cls, base, kw):
+    d = cls()
+    for name, v in {**base, **kw}.items():
+        if isinstance(v, tuple):
+            v = (ctypes.c_int64 * 3)(*v)
+        setattr(d, name, v)
+    return d
+
+
+def norm(**kw):
+    return fill(rn.RnNormDesc, dict(rows=4, d=64, in_dtype=1, out_dtype=1, eps=1e-5, x_stride=64, res_stride=64,
+                                    sum_stride=64, out_stride=64), kw)
+
+
+def norm_forward(d, x=FAKE, r=None, s=None, out=2 * FAKE):
+    return L.rn_layernorm_forward(ctypes.byref(d), x, r, None, None, s, out, None)
+
+
+def norm_backward(d, dout=FAKE, x=FAKE, dx=2 * FAKE, dw=FAKE, ws=FAKE, n=1 << 40):
+    return L.rn_layernorm_backward(ctypes.byref(d), dout, x, None, None, dx, dw, None, ws, n, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(rows=0), INV), (dict(d=0), INV), (dict(d=16385), UNS), (dict(rows=(1 << 40) + 1), UNS),
+    (dict(in_dtype=2), INV), (dict(out_dtype=-1), INV), (dict(eps=-1.0), INV), (dict(eps=math.nan), INV),
+    (dict(eps=math.inf), INV), (dict(x_stride=-64), INV), (dict(res_stride=(1 << 40) + 1), INV),
+    (dict(out_stride=63), INV), (dict(sum_stride=10), INV)])
+def test_norm_descriptors(kw, code):
+    d = norm(**kw)
+    out_only = "out_stride" in kw and kw["out_stride"] > 0
+    assert norm_forward(d, s=3 * FAKE) == code and L.rn_last_error() != b""
+    assert out_only or norm_backward(d) == code
+    if not ({"out_stride", "sum_stride"} & set(kw)):
+        assert L.rn_layernorm_backward_workspace_bytes(ctypes.byref(d)) == 0
+
+
+def test_norm_pointers_and_workspace():
+    d = norm()
+    assert L.rn_layernorm_forward(None, FAKE, None, None, None, None, FAKE, None) == INV
+    assert norm_forward(d, x=None) == INV and norm_forward(d, out=None) == INV
+    assert norm_forward(d, x=FAKE + 1) == INV                       # bf16 on an odd address
+    assert norm_forward(d, s=2 * FAKE) == INV                       # out and sum_out the same
+    assert norm_forward(norm(out_dtype=0), x=FAKE, out=FAKE) == INV  # in place with other types
+    assert norm_forward(norm(out_stride=128), x=FAKE, out=FAKE) == INV
+    assert norm_backward(d, dx=None) == INV and norm_backward(d, dout=None) == INV
+    assert norm_backward(d, dx=FAKE, dout=FAKE, x=5 * FAKE, ws=None) == WS
+    need = L.rn_layernorm_backward_workspace_bytes(ctypes.byref(d))
+    assert need > 0 and norm_backward(d, n=need - 1) == WS
+    assert norm_backward(d, ws=FAKE + 16) == INV
+    assert norm_backward(norm(out_dtype=0), dout=FAKE, dx=FAKE) == INV
+
+
+TH = np.ones(128)
+
+
+def rot(**kw):
+    s = (4096, 512, 128)
+    return fill(rn.RnRotaryDesc, dict(B=1, N=4, H_q=8, H_k=8, d=128, rot=128, dtype=1, flags=0, pos0=0, magnitude=1.0,
+                                      theta=TH.ctypes.data, q_stride=s, k_stride=s, q_out_stride=s, k_out_stride=s), kw)
+
+
+def rotary(d, pos=None, q=FAKE, k=2 * FAKE, qo=3 * FAKE, ko=4 * FAKE):
+    return L.rn_rotary(ctypes.byref(d), pos, q, k, qo, ko, None)
+
+
+BAD_TH = np.full(128, np.nan)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(B=0), INV), (dict(N=0), INV), (dict(H_q=0), INV), (dict(H_k=-1), INV), (dict(d=1), INV),
+    (dict(rot=0), INV), (dict(rot=127), INV), (dict(rot=130), INV), (dict(d=513), UNS),
+    (dict(d=512, rot=258), UNS), (dict(H_q=65530, H_k=6), UNS), (dict(B=1 << 16, N=1 << 15), UNS),
+    (dict(dtype=2), INV), (dict(flags=8), INV), (dict(pos0=-1), INV), (dict(pos0=(1 << 40) + 1), INV),
+    (dict(magnitude=math.inf), INV), (dict(theta=None), INV), (dict(theta=BAD_TH.ctypes.data), INV),
+    (dict(flags=4), INV), (dict(q_stride=(-1, 512, 128)), INV), (dict(q_out_stride=(4096, 0, 128)), INV),
+    (dict(k_out_stride=(4096, 512, 127)), INV), (dict(q_out_stride=(0, 128, 512)), INV)])
+def test_rotary_descriptors(kw, code):
+    if kw.get("q_out_stride", (1,))[0] == 0:
+        kw = dict(kw, B=2)
+    assert rotary(rot(**kw)) == code and L.rn_last_error() != b""
+
+
+def test_rotary_pointers():
+    assert L.rn_rotary(None, None, FAKE, FAKE, FAKE, FAKE, None) == INV
+    for kw in (dict(q=None), dict(qo=None), dict(k=None), dict(ko=None), dict(q=FAKE + 1), dict(ko=4 * FAKE + 1),
+               dict(pos=FAKE + 4), dict(qo=4 * FAKE)):
+        assert rotary(rot(), **kw) == INV, kw
+    assert rotary(rot(q_out_stride=(8192, 1024, 256)), qo=FAKE) == INV   # in place, other strides
+
+
+def test_rotary_frequencies():
+    t, m = rn.rn_rotary_frequencies(64)
+    j = np.arange(32)
+    assert m == 1.0 and np.abs(t / 10000.0 ** (-j / 32) - 1).max() < 1e-14
+    t2, _ = rn.rn_rotary_frequencies(64, kind="linear", factor=4)
+    assert np.abs(t2 * 4 / t - 1).max() < 1e-14
+    t3, m3 = rn.rn_rotary_frequencies(64, kind="base", factor=4)
+    assert m3 == 1.0 and t3[0] == 1.0 and abs(t3[-1] * 4 / t[-1] - 1) < 1e-12
+    t4, m4 = rn.rn_rotary_frequencies(64, kind="by_parts", factor=8, length=4096, slow=1, fast=32)
+    turns = 4096 * t / (2 * np.pi)
+    assert abs(m4 - (0.1 * math.log(8) + 1)) < 1e-6
+    assert np.array_equal(t4[turns >= 32], t[turns >= 32]) and (turns >= 32).any()
+    assert np.abs(t4[turns <= 1] * 8 / t[turns <= 1] - 1).max() < 1e-14 and (turns <= 1).any()
+    mid = (turns > 1) & (turns < 32)
+    keep = (turns[mid] - 1) / 31
+    assert np.abs(t4[mid] / (t[mid] * (keep + (1 - keep) / 8)) - 1).max() < 1e-13 and mid.any()
+    for bad in (dict(rot=3), dict(rot=0), dict(rot=258), dict(rot=64, base=1.0), dict(rot=64, base=math.inf),
+                dict(rot=64, kind="linear", factor=0.5), dict(rot=2, kind="base", factor=2),
+                dict(rot=64, kind="by_parts", factor=2, slow=3, fast=3),
+                dict(rot=64, kind="by_parts", factor=2, length=0), dict(rot=64, kind="linear", factor=math.nan)):
+        with pytest.raises(rn.RnError):
+            rn.rn_rotary_frequencies(**bad)
+    with pytest.raises(ValueError):
+        rn.rn_rotary_frequencies(64, kind="stretched")
+    assert L.rn_rotary_frequencies(64, 1e4, 7, 1.0, 1.0, 0.0, 1.0, t.ctypes.data, t.ctypes.data) == INV
+    assert L.rn_rotary_frequencies(64, 1e4, 0, 1.0, 1.0, 0.0, 1.0, None, None) == INV
+
+
+def lin(**kw):
+    s = (1 << 20, 1 << 14, 64)
+    return fill(rn.RnLinearDesc, dict(S=2, N=100, H=8, H_q=8, H_k=8, H_v=8, d_k=64, d_v=64, in_dtype=1, out_dtype=1,
+                                      flags=0, qk_scale=1.0, T=0, n_slots=0, q_stride=s, k_stride=s, v_stride=s,
+                                      g_stride=(800, 100, 1), out_stride=s), kw)
+
+
+def chunked(d, cu=None, lens=None, slots=None, q=FAKE, g=FAKE, s0=None, s1=None, out=FAKE, ws=FAKE, n=1 << 40):
+    return L.rn_linear_attention_chunked(ctypes.byref(d), cu, lens, slots, q, FAKE, FAKE, g, s0, s1, out, ws, n, None)
+
+
+def step(d, slots=None, state=FAKE, q=FAKE, out=FAKE):
+    return L.rn_linear_attention_step(ctypes.byref(d), slots, q, FAKE, FAKE, FAKE, state, out, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(S=0), INV), (dict(H=0), INV), (dict(H_q=0), INV), (dict(H_k=3), INV), (dict(H_v=16), INV), (dict(d_k=0), INV),
+    (dict(d_k=257), UNS), (dict(d_v=513), UNS), (dict(S=65535), UNS), (dict(H=65536, H_q=1, H_k=1, H_v=1), UNS),
+    (dict(in_dtype=2), INV), (dict(out_dtype=9), INV), (dict(flags=2), INV), (dict(qk_scale=math.nan), INV),
+    (dict(T=-1), INV), (dict(T=1 << 31), INV), (dict(q_stride=(0, -1, 1)), INV),
+    (dict(out_stride=(1 << 20, 1 << 14, 63)), INV), (dict(out_stride=(1 << 20, 64, 64)), INV)])
+def test_linear_descriptors(kw, code):
+    assert chunked(lin(**kw)) == code and L.rn_last_error() != b""
+    assert L.rn_linear_attention_workspace_bytes(ctypes.byref(lin(**kw))) == 0
+    if "out_stride" not in kw:                          # the step has one token: any token stride
+        assert step(lin(**{"N": 1, **kw})) == code
+
+
+def test_linear_calls():
+    assert L.rn_linear_attention_workspace_bytes(None) == 0
+    assert chunked(lin(N=0)) == INV and chunked(lin(N=(1 << 30) + 1, out_stride=(1 << 40, 64, 512))) == UNS
+    assert step(lin()) == INV                                        # N != 1
+    assert step(lin(N=1, T=5)) == INV and step(lin(N=1), state=None) == INV
+    assert step(lin(N=1), state=FAKE + 4) == INV and step(lin(N=1), slots=FAKE) == INV     # n_slots = 0
+    assert step(lin(N=1, n_slots=4), slots=FAKE + 2) == INV
+    assert step(lin(N=1), q=None) == INV and step(lin(N=1), out=FAKE + 1) == INV
+    d = lin()
+    for kw in (dict(cu=FAKE), dict(lens=FAKE + 1), dict(slots=FAKE), dict(q=None), dict(g=None), dict(g=FAKE + 2),
+               dict(s0=FAKE + 8), dict(s1=FAKE + 8), dict(out=None)):
+        assert chunked(d, **kw) == INV, kw
+    packed = lin(T=200, S=3)
+    assert chunked(packed) == INV                                    # no cu_seqlens
+    assert chunked(packed, cu=FAKE, lens=FAKE) == INV
+    assert chunked(lin(T=99), cu=FAKE) == INV                        # N > T
+    long = lin(N=1 << 16, q_stride=(1 << 30, 64, 512), out_stride=(1 << 30, 64, 512))
+    need = L.rn_linear_attention_workspace_bytes(ctypes.byref(long))
+    assert need > 0
+    assert chunked(long, n=need - 1) == WS and chunked(long, ws=None) == WS and chunked(long, ws=FAKE + 16) == INV
+
+
+def test_workspace_size_passes_32_bits():
+    """A million tokens of 128 heads: sizes are formed in 64 bits."""
+    d = lin(S=64, N=1 << 20, H=128, H_q=128, H_k=128, H_v=128, d_k=256, d_v=512, flags=rn.RN_LINEAR_GENERIC,
+            out_stride=(1 << 40, 512, 512 * 128))
+    a = L.rn_linear_attention_workspace_bytes(ctypes.byref(d))
+    assert a % 256 == 0
+
+
+def test_binding_refuses_cpu_tensors_and_wrong_shapes():
+    x = torch.zeros(4, 64)
+    with pytest.raises(ValueError):
+        rn.rn_layernorm(x)
+    with pytest.raises(ValueError):
+        rn.rn_layernorm_backward(x, x)
+    with pytest.raises(ValueError):
+        rn.rn_rotary(torch.zeros(1, 2, 3, 8), None, np.ones(4))
+    z = torch.zeros(1, 2, 3, 8)
+    with pytest.raises(ValueError):
+        rn.rn_linear_attention_chunked(z, z, z, torch.zeros(1, 2, 3))
+    with pytest.raises(ValueError):
+        rn.rn_linear_attention_step(z, z, z, torch.zeros(1, 2, 3), torch.zeros(1, 2, 8, 8))

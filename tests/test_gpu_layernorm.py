@@ -1,0 +1,206 @@
+"""Layer norm and its gradients on the GPU against the float64 oracle.
+
+Tolerances. u = 2^-24. Sums over a row run over at most 64 values a lane and 10 joins, so the
+mean is off by at most 74 u mean|h| and the variance, relatively, by at most 80 u (plus the
+square of the mean's error): the normalised value xh by at most 80 u (rms(h) rstd + |xh|),
+counting the roundings around. A result in bf16 adds half a step, 2^-8 of its value."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import block as K
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+U = 2.0 ** -24
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def rn():
+    import linear_recurrent_sequence_rn_amd as m
+    return m
+
+
+def half_step(t):
+    return torch.finfo(t).eps / 2
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def rows(gen, n, d, dt, mean=0.25, std=1.5):
+    return (torch.randn(n, d, generator=gen) * std + mean).to(dt)
+
+
+def spread(gen, n, d, dt, extra):
+    """A [n, d] view of a wider buffer: rows `extra` elements apart from each other."""
+    wide = torch.zeros(n, d + extra, dtype=dt, device=DEV)
+    wide[:, :d] = rows(gen, n, d, dt).to(DEV)
+    return wide[:, :d]
+
+
+def check(got, want, tol):
+    off = np.abs(np64(got) - want)
+    assert (off <= tol).all(), f"{(off / tol).max()} of the tolerance"
+
+
+SIZES = [(1, 1), (3, 2), (5, 7), (1, 64), (4, 512), (9, 513), (2, 1024), (130, 1000), (33, 1537), (7, 2048),
+         (5, 2056), (3, 4096), (6, 4100), (2, 8192), (3, 8200), (2, 16384), (2, 16383), (2049 * 4 + 1, 64), (2100, 2560)]
+
+
+@pytest.mark.parametrize("n,d", SIZES)
+@pytest.mark.parametrize("kind", ["f32", "bf16", "bf16->f32", "f32->bf16"])
+def test_forward(n, d, kind):
+    dt, od = DT[kind.split("->")[0]], DT[kind.split("->")[-1]]
+    g = torch.Generator().manual_seed(n * 31 + d)
+    x, r = rows(g, n, d, dt), rows(g, n, d, dt, 0.0, 1.0)
+    w, b = torch.randn(d, generator=g) * 0.2 + 1, torch.randn(d, generator=g) * 0.2
+    for res, aff in ((None, True), (r, False), (r, True)):
+        y, h = K.layernorm(x, w if aff else None, b if aff else None, 1e-5, res)
+        xh, _ = K.layernorm(x, None, None, 1e-5, res)
+        got = rn().rn_layernorm(x.to(DEV), w.to(DEV) if aff else None, b.to(DEV) if aff else None,
+                                residual=None if res is None else res.to(DEV), out_dtype=od)
+        out, total = got if res is not None else (got, None)
+        assert out.dtype == od and out.shape == (n, d)
+        rms = np.sqrt((h * h).mean(-1, keepdims=True) / (h.var(-1, keepdims=True) + 1e-5))
+        ww, bb = (np64(w), np64(b)) if aff else (1.0, 0.0)
+        check(out, y, 80 * U * (rms + np.abs(xh)) * np.abs(ww) + 2 * U * np.abs(bb) + half_step(od) * 1.01 * np.abs(y) + 1e-30)
+        if res is not None:
+            assert total.dtype == dt
+            check(total, h, (U + half_step(dt)) * 1.01 * np.abs(h))
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("d,extra", [(256, 8), (256, 1), (100, 28), (4096, 4096)])
+def test_strided_rows_and_in_place(kind, d, extra):
+    dt = DT[kind]
+    g = torch.Generator().manual_seed(d + extra)
+    x, r = spread(g, 37, d, dt, extra), spread(g, 37, d, dt, 2 * extra)
+    base = x._base
+    y, h = K.layernorm(x.cpu(), None, None, 1e-5, r.cpu())
+    want, total = rn().rn_layernorm(x, residual=r)
+    keep_r = r.clone()
+    out, s = rn().rn_layernorm(x, residual=r, out=x, sum_out=r)        # both in place
+    assert out is x and s is r
+    assert torch.equal(out, want) and torch.equal(s, total) and not torch.equal(keep_r, r)
+    assert int(torch.count_nonzero(base[:, d:])) == 0                  # nothing between the rows
+    check(out, y, 80 * U * (np.sqrt((h * h).mean(-1, keepdims=True)) / h.std(-1, keepdims=True) + np.abs(y))
+          + half_step(dt) * 1.01 * np.abs(y))
+    # an input whose rows are all the same row
+    one = rows(g, 1, d, dt).to(DEV)
+    same = rn().rn_layernorm(one.expand(5, d))
+    assert torch.equal(same, rn().rn_layernorm(one).expand(5, d))
+    # leading axes that step like one, and ones that do not
+    z = torch.zeros(4, 6, d + extra, dtype=dt, device=DEV)[..., :d]
+    assert rn().rn_layernorm(z).shape == z.shape
+    with pytest.raises(ValueError):
+        rn().rn_layernorm(z.transpose(0, 1))
+
+
+def test_eps_zero_constant_and_nonfinite_rows():
+    x = torch.full((6, 96), 3.0, device=DEV)
+    x[1, 5] = float("nan")
+    x[2, 7] = float("inf")
+    x[4] = torch.arange(96.0)
+    w, b = torch.full((96,), 2.0, device=DEV), torch.full((96,), -1.0, device=DEV)
+    out = rn().rn_layernorm(x, w, b)
+    assert torch.equal(out[0], b) and torch.equal(out[3], b) and torch.equal(out[5], b)
+    assert out[1].isnan().all() and out[2].isnan().all()
+    assert out[4].isfinite().all()
+    assert rn().rn_layernorm(x[:1], w, b, 0.0).isnan().all()           # 0 / 0
+    assert torch.equal(rn().rn_layernorm(x[4:5], w, b), out[4:5])      # rows do not meet
+
+
+@pytest.mark.parametrize("n,d", SIZES)
+@pytest.mark.parametrize("kind", ["f32", "bf16", "bf16->f32"])
+def test_backward(n, d, kind):
+    """dx: two further means of products of sizes |g| and |g xh|, and xh's own error; sums over
+    rows: at most n/1024 + 5 rows one after another, 32 + 16 joins of partial sums, each term
+    with xh's error."""
+    dt, od = DT[kind.split("->")[0]], DT[kind.split("->")[-1]]
+    g = torch.Generator().manual_seed(n * 17 + d)
+    x, dy, dh = rows(g, n, d, dt), rows(g, n, d, od, 0.1, 1.0), rows(g, n, d, dt, 0.0, 1.0)
+    w = torch.randn(d, generator=g) * 0.2 + 1
+    for res, aff in ((None, True), (dh, False), (dh, True)):
+        ww = w if aff else None
+        dx, dw, db = K.layernorm_backward(dy, x, ww, 1e-5, res)
+        got = rn().rn_layernorm_backward(dy.to(DEV), x.to(DEV), None if ww is None else ww.to(DEV),
+                                         dsum=None if res is None else res.to(DEV))
+        xx, gg = np64(x), np64(dy) * (np64(w) if aff else 1.0)
+        sd = np.sqrt(xx.var(-1, keepdims=True) + 1e-5)
+        xh = (xx - xx.mean(-1, keepdims=True)) / sd
+        exh = 80 * U * (np.sqrt((xx * xx).mean(-1, keepdims=True)) / sd + np.abs(xh))
+        m1, m2 = np.abs(gg).mean(-1, keepdims=True), np.abs(gg * xh).mean(-1, keepdims=True)
+        e2 = (np.abs(gg) * exh).mean(-1, keepdims=True) + 80 * U * m2
+        tol = (90 * U * (np.abs(gg) + m1 + np.abs(xh) * m2) + exh * m2 + np.abs(xh) * e2) / sd
+        tol = tol + half_step(dt) * 1.01 * np.abs(dx) + (0 if res is None else U * np.abs(np64(res)))
+        check(got["dx"], dx, tol + 1e-30)
+        chain = n / 1024 + 5 + 48
+        check(got["dweight"], dw, (np.abs(np64(dy)) * (exh + chain * U * np.abs(xh))).sum(0) + 1e-30)
+        check(got["dbias"], db, chain * U * np.abs(np64(dy)).sum(0) + 1e-30)
+        assert got["dx"].dtype == dt and got["dweight"].dtype == got["dbias"].dtype == torch.float32
+
+
+def test_backward_against_differences():
+    """The float32 forward call's own differences: (f(x + e) - f(x - e)) / 2e of loss =
+    sum(dy y) + sum(dh h) at e = 2^-6: the truncation error is of order e^2, the rounding error
+    of y, 1e-6 a value, over e."""
+    g = torch.Generator().manual_seed(5)
+    x, dy, dh = (torch.randn(3, 40, generator=g).to(DEV) for _ in range(3))
+    w, b = (torch.randn(40, generator=g) * 0.3 + 1).to(DEV), torch.randn(40, generator=g).to(DEV)
+    got = rn().rn_layernorm_backward(dy, x, w, dsum=dh)
+
+    def loss(x_, w_, b_):
+        y, s = rn().rn_layernorm(x_, w_, b_, sum_out=torch.empty_like(x_))
+        return ((y.double() * dy).sum() + (s.double() * dh).sum()).item()
+
+    e = 2.0 ** -6
+    for a, grad, f in ((x, got["dx"], lambda t: loss(t, w, b)), (w, got["dweight"], lambda t: loss(x, t, b)),
+                       (b, got["dbias"], lambda t: loss(x, w, t))):
+        flat = grad.flatten()
+        for i in range(0, a.numel(), 7):
+            up, dn = a.clone(), a.clone()
+            up.view(-1)[i] += e
+            dn.view(-1)[i] -= e
+            num = (f(up) - f(dn)) / (2 * e)
+            assert abs(num - flat[i].item()) < 4e-3 * max(1.0, abs(num)), (i, num, flat[i].item())
+
+
+def test_backward_options():
+    g = torch.Generator().manual_seed(6)
+    x, dy, dh = (torch.randn(300, 130, generator=g).to(DEV) for _ in range(3))
+    w = torch.randn(130, generator=g).to(DEV)
+    full = rn().rn_layernorm_backward(dy, x, w, dsum=dh)
+    again = rn().rn_layernorm_backward(dy, x, w, dsum=dh)
+    assert all(torch.equal(full[k], again[k]) for k in full)           # the same bits
+    only = rn().rn_layernorm_backward(dy, x, w, dsum=dh, want_dweight=False, want_dbias=False)
+    assert set(only) == {"dx"} and torch.equal(only["dx"], full["dx"])
+    one = rn().rn_layernorm_backward(dy, x, w, dsum=dh, want_dbias=False)
+    assert torch.equal(one["dweight"], full["dweight"]) and "dbias" not in one
+    ws = torch.empty(rn().rn_layernorm_backward_workspace_bytes(dy, x), dtype=torch.uint8, device=DEV)
+    ws.fill_(255)
+    assert torch.equal(rn().rn_layernorm_backward(dy, x, w, dsum=dh, workspace=ws)["dbias"], full["dbias"])
+    with pytest.raises(rn().RnError, match="RN_ERR_WORKSPACE"):
+        rn().rn_layernorm_backward(dy, x, w, workspace=ws[:16])
+    d2 = dy.clone()
+    assert torch.equal(rn().rn_layernorm_backward(d2, x, w, dsum=dh, dx=d2)["dx"], full["dx"])   # over dout
+    d3 = dh.clone()
+    assert torch.equal(rn().rn_layernorm_backward(dy, x, w, dsum=d3, dx=d3)["dx"], full["dx"])   # over dsum
+
+
+def test_refusals():
+    x = torch.zeros(4, 64, device=DEV)
+    for kw in (dict(residual=torch.zeros(4, 65, device=DEV)), dict(residual=x.bfloat16()), dict(weight=x[0].bfloat16()),
+               dict(weight=torch.zeros(63, device=DEV)), dict(bias=torch.zeros(64)), dict(out=torch.zeros(3, 64, device=DEV)),
+               dict(sum_out=x.bfloat16())):
+        with pytest.raises(ValueError):
+            rn().rn_layernorm(x, **kw)
+    with pytest.raises(ValueError):
+        rn().rn_layernorm(torch.zeros(0, 64, device=DEV))
+    with pytest.raises(TypeError):
+        rn().rn_layernorm(x.half())
+    with pytest.raises(ValueError):
+        rn().rn_layernorm(torch.zeros(64, 4, device=DEV).t())
+    with pytest.raises(rn().RnError, match="RN_ERR_UNSUPPORTED"):
+        rn().rn_layernorm(torch.zeros(1, 16392, device=DEV))
