@@ -77,8 +77,7 @@ __device__ __forceinline__ void lin_zero_rest(const LinArgs& a, int s, int g, in
 }
 
 // Matrix-core kernel (bf16 in and out, whole 16-byte rows).
-bool lin_mfma_supported(const LinCall& c);
-int lin_mfma_blocks(const LinCall& c);     // blocks a sequence and segment takes
+int lin_mfma_blocks(const LinArgs& a);     // blocks a sequence and segment takes
 hipError_t launch_lin_mfma(const LinArgs& a, LinMode mode, hipStream_t st);
 
 }  // namespace rn

@@ -322,10 +322,38 @@ hipError_t launch_step_t(const LinArgs& a, hipStream_t st) {
 #undef RN_STEP
 }
 
+LinArgs lin_args(const LinCall& c) {
+  LinArgs a;
+  a.S = c.S; a.N = c.N; a.H = c.H; a.Hq = c.Hq; a.Hk = c.Hk; a.Hv = c.Hv; a.dk = c.dk; a.dv = c.dv;
+  a.n_slots = c.n_slots; a.T = c.T; a.scale = c.scale; a.zero_rest = c.zero_rest;
+  for (int i = 0; i < 3; ++i) {
+    a.qs[i] = c.qs[i]; a.ks[i] = c.ks[i]; a.vs[i] = c.vs[i]; a.gs[i] = c.gs[i]; a.os[i] = c.os[i];
+  }
+  a.cu = c.cu; a.lens = c.lens; a.slots = c.slots;
+  a.q = c.q; a.k = c.k; a.v = c.v; a.g = c.g; a.state_in = c.state_in; a.state_out = c.state_out; a.out = c.out;
+  a.seg_len = c.N; a.n_seg = 1; a.seg_state = nullptr; a.seg_decay = nullptr;
+  return a;
+}
+
+// Matrix cores: bf16 in and out, head sizes and rows in whole 16-byte pieces. (The pointers are
+// not known when the workspace is sized: a call with an unaligned one runs the recurrence on
+// the same segments.)
+bool mfma_shape(const LinCall& c) {
+  bool ok = !c.generic && c.in_dt == RN_BF16 && c.out_dt == RN_BF16 && c.dk % 8 == 0 && c.dv % 8 == 0;
+  for (const int64_t* s : {c.qs, c.ks, c.vs, c.os})
+    for (int i = 0; i < 3; ++i) ok = ok && s[i] % 8 == 0;
+  return ok;
+}
+bool mfma_call(const LinCall& c) {
+  bool ok = mfma_shape(c);
+  for (const void* p : {c.q, c.k, c.v, static_cast<const void*>(c.out)}) ok = ok && reinterpret_cast<uintptr_t>(p) % 16 == 0;
+  return ok;
+}
+
 // Tokens a segment, and how many segments the longest sequence has: one segment where the
 // sequences and heads fill the chip by themselves, else enough segments for `want` blocks.
 void segments(const LinCall& c, int* len, int* n) {
-  const int64_t per = lin_use_mfma(c) ? lin_mfma_blocks(c) : static_cast<int64_t>(c.H) * ((c.dv + kCols - 1) / kCols);
+  const int64_t per = mfma_shape(c) ? lin_mfma_blocks(lin_args(c)) : static_cast<int64_t>(c.H) * ((c.dv + kCols - 1) / kCols);
   const int64_t tokens = c.T > 0 ? std::min<int64_t>(c.T, static_cast<int64_t>(c.S) * c.N) : static_cast<int64_t>(c.S) * c.N;
   const int64_t want = 512;
   int64_t L = tokens * per / want;
@@ -343,29 +371,12 @@ int64_t total_segments(const LinCall& c, int len, int n) {
 
 }  // namespace
 
-bool lin_use_mfma(const LinCall&) { return false; }
-int lin_mfma_blocks(const LinCall&) { return 1; }
-hipError_t launch_lin_mfma(const LinArgs&, LinMode, hipStream_t) { return hipErrorInvalidValue; }
-
 size_t lin_ws_bytes(const LinCall& c) {
   int len, n;
   segments(c, &len, &n);
   if (n == 1) return 0;
   const size_t rows = static_cast<size_t>(total_segments(c, len, n)) * c.H;
   return rows * sizeof(float) * c.dk * c.dv + ((rows * sizeof(float) + 255) & ~size_t(255));
-}
-
-static LinArgs lin_args(const LinCall& c) {
-  LinArgs a;
-  a.S = c.S; a.N = c.N; a.H = c.H; a.Hq = c.Hq; a.Hk = c.Hk; a.Hv = c.Hv; a.dk = c.dk; a.dv = c.dv;
-  a.n_slots = c.n_slots; a.T = c.T; a.scale = c.scale; a.zero_rest = c.zero_rest;
-  for (int i = 0; i < 3; ++i) {
-    a.qs[i] = c.qs[i]; a.ks[i] = c.ks[i]; a.vs[i] = c.vs[i]; a.gs[i] = c.gs[i]; a.os[i] = c.os[i];
-  }
-  a.cu = c.cu; a.lens = c.lens; a.slots = c.slots;
-  a.q = c.q; a.k = c.k; a.v = c.v; a.g = c.g; a.state_in = c.state_in; a.state_out = c.state_out; a.out = c.out;
-  a.seg_len = c.N; a.n_seg = 1; a.seg_state = nullptr; a.seg_decay = nullptr;
-  return a;
 }
 
 hipError_t launch_linear_step(const LinCall& c, hipStream_t st) {
@@ -378,7 +389,7 @@ hipError_t launch_linear_step(const LinCall& c, hipStream_t st) {
 hipError_t launch_linear_chunked(const LinCall& c, hipStream_t st) {
   LinArgs a = lin_args(c);
   segments(c, &a.seg_len, &a.n_seg);
-  const bool mfma = lin_use_mfma(c);
+  const bool mfma = mfma_call(c);
   if (a.n_seg == 1) return mfma ? launch_lin_mfma(a, kLinWhole, st) : launch_recurrent<kLinWhole>(a, c.in_dt, c.out_dt, st);
   const size_t rows = static_cast<size_t>(total_segments(c, a.seg_len, a.n_seg)) * c.H;
   a.seg_decay = static_cast<float*>(c.ws);

@@ -142,7 +142,6 @@ struct LinCall {
   void* out;
   void* ws;
 };
-bool lin_use_mfma(const LinCall& c);
 size_t lin_ws_bytes(const LinCall& c);
 hipError_t launch_linear_step(const LinCall& c, hipStream_t st);
 hipError_t launch_linear_chunked(const LinCall& c, hipStream_t st);
