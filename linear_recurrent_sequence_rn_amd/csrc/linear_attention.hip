@@ -355,7 +355,7 @@ bool mfma_call(const LinCall& c) {
 void segments(const LinCall& c, int* len, int* n) {
   const int64_t per = mfma_shape(c) ? lin_mfma_blocks(lin_args(c)) : static_cast<int64_t>(c.H) * ((c.dv + kCols - 1) / kCols);
   const int64_t tokens = c.T > 0 ? std::min<int64_t>(c.T, static_cast<int64_t>(c.S) * c.N) : static_cast<int64_t>(c.S) * c.N;
-  const int64_t want = 512;
+  const int64_t want = 256;
   int64_t L = tokens * per / want;
   L = std::max<int64_t>((L + 63) / 64 * 64, 256);
   if (2 * L > c.N) L = c.N;

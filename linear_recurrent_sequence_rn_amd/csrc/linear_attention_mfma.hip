@@ -4,20 +4,23 @@
 //     O = (Q K^T o D) V + diag(2^c) Q S,     D_ts = 2^(c_t - c_s) for s <= t, else 0
 //     S <- 2^(c_63) S + K^T (w o V),         w_s = 2^(c_63 - c_s).
 //
-// A block of four waves owns one segment of one sequence and 4 CW columns of one head's state
-// and output; it walks over the segment's chunks with the state in its registers. A wave owns
-// CW columns for all rows, so the state never leaves the wave: as accumulator of K^T (w V) it
-// has the column in the lane and four rows in the registers, which is just the operand
-// layout that Q S needs for its transposed result O^T (rows and columns of the reduction may
-// be numbered alike in any order, and all operands here use the order 4g..4g+3,
+// A block owns one segment of one sequence and VW CW columns of one head's state and output;
+// it walks over the segment's chunks with the state in its registers. A wave owns CW columns
+// and d_k / DW rows, so the state never leaves the wave: as accumulator of K^T (w V) it has
+// the column in the lane and four rows in the registers, which is just the operand layout
+// that Q S needs for its transposed result O^T (rows and columns of the reduction may be
+// numbered alike in any order, and all operands here use the order 4g..4g+3,
 // 16+4g..16+4g+3 of each 32). K^T and V^T come out of row-major LDS tiles by transposing reads.
-// The scores are the one product the waves share: each forms the scores of 16 queries, and
-// the tile goes through LDS.
+// The scores are shared by all waves: their ten 16 x 16 tiles are dealt out to the waves and
+// meet in LDS. With DW = 2 the two waves of a column pair each have a share of Q S of every
+// query; each hands the other its share of two of the four query tiles, through LDS.
 //
 // Rounding: the scores times their decay, and the copy of the state that Q S reads, are rounded
 // to bf16 once (the outputs are bf16 themselves). The state is float32: w o V is split in
 // three bf16 parts, which hold all 24 bits of it, and K is bf16 already, so that the products
 // carry float32 accuracy (two parts where only outputs, not the final state, depend on it).
+#include <type_traits>
+
 #include "linear_attention.h"
 
 namespace rn {
@@ -29,7 +32,6 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr int kChunk = 64;
-constexpr int kThreads = 256;
 constexpr double kLog2e = 1.4426950408889634;
 constexpr double kFloor = -173.0;      // 2^-173 is 0 in float32: log decays below stand for 0
 
@@ -47,20 +49,25 @@ __device__ __forceinline__ int at(int row, int col) {
   return row * (2 * W) + (((col >> 3) ^ f) << 4) + (col & 7) * 2;
 }
 
-// Operand whose lane holds row `row`, columns c..c+3 and c+16..c+19 (c = 32 ks + 4 g).
-template <int W>
-__device__ __forceinline__ bf16x8 row_operand(const char* tile, int row, int c) {
-  const uint2 lo = *reinterpret_cast<const uint2*>(tile + at<W>(row, c));
-  const uint2 hi = *reinterpret_cast<const uint2*>(tile + at<W>(row, c + 16));
+// The permutation only XORs bits of the offset, and so do steps of whole 16 columns: all offsets
+// a lane needs come from one base per way of reading, XORed with constants, and from
+// constants added for steps of 16 rows.
+//
+// Operand whose lane holds its row, columns c..c+3 and c+16..c+19 with c = 32 ks + g4;
+// base = at<W>(l16, g4), rows = byte offset of the tile of 16 rows.
+__device__ __forceinline__ bf16x8 row_operand(const char* tile, int base, int ks, int rows) {
+  const uint2 lo = *reinterpret_cast<const uint2*>(tile + (base ^ (ks << 6)) + rows);
+  const uint2 hi = *reinterpret_cast<const uint2*>(tile + (base ^ (ks << 6 | 32)) + rows);
   return __builtin_bit_cast(bf16x8, make_uint4(lo.x, lo.y, hi.x, hi.y));
 }
-// Operand whose lane holds column col0 + l16, rows r..r+3 and r+16..r+19 (r = 32 ks + 4 g).
+// Operand whose lane holds column 16 i + l16, rows r..r+3 and r+16..r+19 with r = 32 ks + g4;
+// base = at<W>(g4 + l16 / 4, 4 (l16 % 4)).
 template <int W>
-__device__ __forceinline__ bf16x8 col_operand(const char* tile, int r, int col0, int l16) {
-  const int row = r + (l16 >> 2), col = col0 + (l16 & 3) * 4;
+__device__ __forceinline__ bf16x8 col_operand(const char* tile, int base, int ks, int i) {
+  const char* p = tile + (base ^ (i << 5)) + ks * (32 * 2 * W);
   struct { s16x4 lo, hi; } v;
-  v.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(tile + at<W>(row, col)));
-  v.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(tile + at<W>(row + 16, col)));
+  v.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p));
+  v.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 16 * 2 * W));
   return __builtin_bit_cast(bf16x8, v);
 }
 
@@ -72,18 +79,51 @@ struct alignas(16) Decays {   // of one chunk
   int bad;               // v holds a NaN or an infinity
 };
 
-// Wave 0: the decays of a chunk from each lane's log decay. Sums in float64, so that
+// x and y in PARTS bf16 parts each, packed in pairs at out[0], out[stride], ...; with SAFE an
+// infinity or NaN has no lower parts.
+template <int PARTS, bool SAFE>
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t* out, int stride) {
+#pragma unroll
+  for (int p = 0; p < PARTS; ++p) {
+    const uint32_t u = pack_bf16x2(x, y);
+    out[p * stride] = u;
+    if (p + 1 < PARTS) {
+      const float hx = __uint_as_float(u << 16), hy = __uint_as_float(u & 0xffff0000u);
+      x -= hx;
+      y -= hy;
+      if (SAFE) {
+        if (!(fabsf(hx) < INFINITY)) x = 0.f;
+        if (!(fabsf(hy) < INFINITY)) y = 0.f;
+      }
+    }
+  }
+}
+
+// x moved across lanes by a DPP control; lanes without a source (or outside the row mask) get 0.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_or_zero(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(u), CTRL, ROWS, 0xf, true);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(u >> 32), CTRL, ROWS, 0xf, true);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+// One wave: the decays of a chunk from each lane's log decay. Sums in float64, so that
 // differences of far sums keep float32 accuracy. Returns the chunk's sum of log2 decays.
 __device__ __forceinline__ double scan_decays(float g, Decays* d) {
   const int lane = threadIdx.x & 63;
   double x = static_cast<double>(g) * kLog2e;
   if (x < kFloor) x = kFloor;           // (a NaN stays)
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const double y = __shfl_up(x, o, 64);
-    if (lane >= o) x += y;
-  }
-  const double last = __shfl(x, 63, 64);
+  x += dpp_or_zero<0x111, 0xf>(x);      // inclusive sums over the 16 lanes of a row ...
+  x += dpp_or_zero<0x112, 0xf>(x);
+  x += dpp_or_zero<0x114, 0xf>(x);
+  x += dpp_or_zero<0x118, 0xf>(x);
+  x += dpp_or_zero<0x142, 0xa>(x);      // ... lane 15 into rows 1 and 3, lane 31 into rows 2 and 3
+  x += dpp_or_zero<0x143, 0xc>(x);
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(u), 63);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(u >> 32), 63);
+  const double last = __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
   d->c[lane] = static_cast<float>(x);
   d->e[lane] = exp2f(static_cast<float>(x));
   d->w[lane] = exp2f(static_cast<float>(last - x));
@@ -92,64 +132,101 @@ __device__ __forceinline__ double scan_decays(float g, Decays* d) {
 }
 
 // One 64-row tile of W columns on its way from memory to LDS: 16 bytes a thread and step.
-template <int W>
+// The chunk's start is a scalar; offsets inside a chunk are 32 bits where the stride allows it.
+template <int W, int NT>
 struct Tile {
   static constexpr int kPer = W / 8;                       // 16-byte pieces a row
-  static constexpr int kStep = kThreads / kPer;            // rows a step
+  static constexpr int kStep = NT / kPer;                  // rows a step
   static constexpr int kN = kChunk / kStep;
   uint4 r[kN];
-  // Rows t0.. of `p` (row stride st, `cols` columns in use); rows past `last` read row `last`.
-  __device__ __forceinline__ void load(const uint16_t* p, int64_t st, int t0, int last, int cols) {
+  // This thread's offset in a chunk whose 64 rows all exist.
+  static __device__ __forceinline__ uint32_t lane_offset(int64_t st, int cols) {
     const int row = threadIdx.x / kPer, c = threadIdx.x % kPer * 8;
-    const uint16_t* q = p + (c < cols ? c : 0);
+    return row * static_cast<uint32_t>(st) + (c < cols ? c : 0);
+  }
+  // The 64 rows from `p` on (row stride st, `cols` columns in use), of which `rows` exist: the
+  // others repeat the last one.
+  __device__ __forceinline__ void load(const uint16_t* p, int64_t st, uint32_t off, int rows, int cols) {
+    if (rows >= kChunk && st < (1 << 24)) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) r[i] = *reinterpret_cast<const uint4*>(p + i * kStep * st + off);
+    } else {
+      const int row = threadIdx.x / kPer, c = threadIdx.x % kPer * 8;
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+        r[i] = *reinterpret_cast<const uint4*>(p + min(row + i * kStep, rows - 1) * st + (c < cols ? c : 0));
+    }
+  }
+  // Rows from `rows` on and columns from `cols` on become zeros.
+  __device__ __forceinline__ void trim(int rows, int cols) {
+    if (rows >= kChunk && cols >= W) return;
+    const int row = threadIdx.x / kPer, c = threadIdx.x % kPer * 8;
 #pragma unroll
     for (int i = 0; i < kN; ++i)
-      r[i] = *reinterpret_cast<const uint4*>(q + min(t0 + row + i * kStep, last) * st);
+      if (c >= cols || row + i * kStep >= rows) r[i] = make_uint4(0, 0, 0, 0);
   }
-  // Into LDS; rows from `rows` on and columns from `cols` on become zeros.
-  __device__ __forceinline__ void store(char* tile, int rows, int cols) {
+  __device__ __forceinline__ void store(char* tile) const {
     const int row = threadIdx.x / kPer, c = threadIdx.x % kPer * 8;
-    const bool whole = rows >= kChunk && cols >= W;
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      if (!whole && (c >= cols || row + i * kStep >= rows)) r[i] = make_uint4(0, 0, 0, 0);
-      *reinterpret_cast<uint4*>(tile + at<W>(row + i * kStep, c)) = r[i];
-    }
+    for (int i = 0; i < kN; ++i) *reinterpret_cast<uint4*>(tile + at<W>(row + i * kStep, c)) = r[i];
   }
   // Whether a value is a NaN or an infinity (largest exponent).
   __device__ __forceinline__ bool nonfinite() const {
-    uint32_t m = 0;
+    typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 m = {0, 0};
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       const uint32_t u[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t hi = (u[j] & 0x7fff0000u), lo = (u[j] & 0x7fffu) << 16;
-        m = max(m, max(hi, lo));
-      }
+      for (int j = 0; j < 4; ++j) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, u[j] & 0x7fff7fffu));
     }
-    return m >= 0x7f800000u;
+    return max(m.x, m.y) >= 0x7f80;
+  }
+  // The values of step i times w, in PARTS bf16 parts that add up to it, largest first.
+  template <int PARTS, bool SAFE>
+  __device__ __forceinline__ void split(int i, float w, uint4* part) const {
+    const uint32_t u[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+    uint32_t o[PARTS][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      split_pair<PARTS, SAFE>(__uint_as_float(u[j] << 16) * w, __uint_as_float(u[j] & 0xffff0000u) * w, &o[0][j], 4);
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) part[p] = make_uint4(o[p][0], o[p][1], o[p][2], o[p][3]);
   }
 };
 
-template <int DK, int CW, LinMode MODE>
-__global__ void __launch_bounds__(kThreads, DK == 256 ? 1 : 2) lin_chunks(LinArgs a, int slices) {
-  constexpr int DV = 4 * CW;             // columns a block
+template <int DK, int CW, int VW, int DW, LinMode MODE>
+__global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(LinArgs a, int slices) {
+  constexpr int NT = 64 * VW * DW;
+  constexpr int DV = VW * CW;            // columns a block
   constexpr int VT = CW / 16;            // 16-column tiles a wave
-  constexpr int AT = DK / 16;            // 16-row tiles of the state
+  constexpr int AT = DK / 16 / DW;       // 16-row tiles of the state a wave
   constexpr int KS = DK / 32;            // reduction steps along d_k
+  constexpr int OT = 4 / DW;             // 16-query tiles of the output a wave finishes
   constexpr int PARTS = MODE == kLinOut ? 2 : 3;
   constexpr bool kOut = MODE != kLinState;
-  __shared__ __align__(16) char smem[(kOut ? 2 : 1) * kChunk * DK * 2 + kChunk * DV * 2 + (kOut ? kChunk * kChunk * 2 : 0)];
-  __shared__ __align__(16) Decays dec[2];
+  constexpr int kTileQ = kChunk * DK * 2, kTileV = kChunk * DV * 2, kTileP = kChunk * kChunk * 2;
+  constexpr int kSwap = DW == 2 ? VW * DW * 2 * VT * 1024 : 0;
+  // Two waves need each part of w V where DW is 2: they are formed once, on the way to LDS, as
+  // long as the tiles fit in it; else each wave forms its own in registers.
+  constexpr int kBase = kTileQ + (kOut ? kTileV + kTileQ + kTileP + kSwap : 0);
+  constexpr bool kParts = DW == 2 && kBase + PARTS * kTileV <= 156 * 1024;
+  constexpr bool kHasV = kOut || !kParts;    // V itself is needed in LDS
+  __shared__ __align__(16) char smem[kBase + (kParts ? PARTS * kTileV : 0) + (kOut || kParts ? 0 : kTileV)];
+  __shared__ Decays dec[2];
   char* kt = smem;
-  char* vt = kt + kChunk * DK * 2;
-  char* qt = vt + kChunk * DV * 2;
-  char* pt = qt + kChunk * DK * 2;
+  char* vt = kt + kTileQ;
+  char* wt = vt + (kHasV ? kTileV : 0);
+  char* qt = wt + (kParts ? PARTS * kTileV : 0);
+  char* pt = qt + kTileQ;
+  f32x4* swap = reinterpret_cast<f32x4*>(pt + kTileP);
 
   const int h = blockIdx.x / slices, c0 = (blockIdx.x - h * slices) * DV;
   const int seg = blockIdx.y, s = blockIdx.z;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, g4 = (lane >> 4) * 4;
+  const int tid = threadIdx.x;
+  const int lane = tid & 63, l16 = lane & 15, g4 = (lane >> 4) * 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wv = wave % VW, wd = wave / VW;              // column tile and row half of this wave
   const int nc = min(DV, a.dv - c0);
   int64_t row0, own;
   int len;
@@ -163,7 +240,8 @@ __global__ void __launch_bounds__(kThreads, DK == 256 ? 1 : 2) lin_chunks(LinArg
   if (MODE == kLinState && t1 == len && !keep) return;   // nobody reads the last segment's state
 
   const int64_t sh = static_cast<int64_t>(a.dk) * a.dv;
-  const int vcol = c0 + wave * CW + l16;                 // this lane's state columns: vcol + 16 j
+  const int vcol = c0 + wv * CW + l16;                   // this lane's state columns: vcol + 16 j
+  const int drow = wd * (DK / DW);                       // and rows: drow + 16 i + g4 + r
   f32x4 S[AT][VT];
   {
     const float* from = MODE == kLinWhole ? (a.state_in && slot >= 0 ? a.state_in + (static_cast<int64_t>(slot) * a.H + h) * sh : nullptr)
@@ -175,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, DK == 256 ? 1 : 2) lin_chunks(LinArg
       for (int j = 0; j < VT; ++j)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int d = 16 * i + g4 + r, v = vcol + 16 * j;
+          const int d = drow + 16 * i + g4 + r, v = vcol + 16 * j;
           S[i][j][r] = from && d < a.dk && v < a.dv ? from[static_cast<int64_t>(d) * a.dv + v] : 0.f;
         }
   }
@@ -183,14 +261,16 @@ __global__ void __launch_bounds__(kThreads, DK == 256 ? 1 : 2) lin_chunks(LinArg
   const uint16_t* kp = static_cast<const uint16_t*>(a.k) + lin_base(a, a.ks, s, row0) + h / (a.H / a.Hk) * a.ks[1];
   const uint16_t* vp = static_cast<const uint16_t*>(a.v) + lin_base(a, a.vs, s, row0) + h / (a.H / a.Hv) * a.vs[1] + c0;
   const float* gp = a.g + lin_base(a, a.gs, s, row0) + h * a.gs[1];
-  uint16_t* op = static_cast<uint16_t*>(a.out) + lin_base(a, a.os, s, row0) + h * a.os[1] + c0 + wave * CW;
+  uint16_t* op = static_cast<uint16_t*>(a.out) + lin_base(a, a.os, s, row0) + h * a.os[1] + c0 + wv * CW;
 
-  Tile<DK> tq, tk;
-  Tile<DV> tv;
+  Tile<DK, NT> tq, tk;
+  Tile<DV, NT> tv;
+  const uint32_t qoff = tq.lane_offset(a.qs[2], a.dk), koff = tk.lane_offset(a.ks[2], a.dk), voff = tv.lane_offset(a.vs[2], nc);
   auto fetch = [&](int t) {
-    if constexpr (kOut) tq.load(qp, a.qs[2], t, len - 1, a.dk);
-    tk.load(kp, a.ks[2], t, len - 1, a.dk);
-    tv.load(vp, a.vs[2], t, len - 1, nc);
+    const int n = len - t;
+    if constexpr (kOut) tq.load(qp + t * a.qs[2], a.qs[2], qoff, n, a.dk);
+    tk.load(kp + t * a.ks[2], a.ks[2], koff, n, a.dk);
+    tv.load(vp + t * a.vs[2], a.vs[2], voff, n, nc);
   };
   auto log_decay = [&](int t) { return t + lane < t1 ? gp[(t + lane) * a.gs[2]] : 0.f; };
 
@@ -198,31 +278,69 @@ __global__ void __launch_bounds__(kThreads, DK == 256 ? 1 : 2) lin_chunks(LinArg
   float gnext = 0.f;
   if (t0 < t1) {
     fetch(t0);
-    if (wave == 0) {
+    if (wave == NT / 64 - 1) {              // (the last wave has the fewest score tiles)
       gsum += scan_decays(log_decay(t0), &dec[0]);
       gnext = log_decay(t0 + kChunk);
     }
     if (tid == 0) dec[0].bad = 0;
-    if constexpr (kOut) {   // score tiles above the diagonal that the products read
-      for (int i = tid; i < 2 * 16 * 4; i += kThreads) {
-        const int t = (i >> 6) * 32 + (i & 15), col = (i >> 6) * 32 + 16 + ((i >> 4) & 3) * 4;
-        *reinterpret_cast<uint2*>(pt + at<kChunk>(t, col)) = make_uint2(0, 0);
-      }
-    }
     __syncthreads();
   }
+  // The outputs of a chunk are stored when the next one's tiles have arrived: loads and stores
+  // are waited for in one count, and stores issued between a chunk's loads and their use would
+  // have to reach memory first.
+  uint2 done[OT][VT];
+  op += l16 * a.os[2] + g4;
+  auto store_out = [&](int t) {
+    const int n = min(kChunk, t1 - t);
+#pragma unroll
+    for (int x = 0; x < OT; ++x) {
+      const int j = DW == 1 ? x : wd == 0 ? 3 * x : 1 + x;
+#pragma unroll
+      for (int v = 0; v < VT; ++v)
+        if (16 * j + l16 < n && wv * CW + 16 * v + g4 < nc)
+          *reinterpret_cast<uint2*>(op + (t + 16 * j) * a.os[2] + 16 * v) = done[x][v];
+    }
+  };
+  int rq = at<DK>(l16, g4), rp = at<kChunk>(l16, g4);
+  int ck = at<DK>(g4 + (l16 >> 2), drow + (l16 & 3) * 4), cv = at<DV>(g4 + (l16 >> 2), wv * CW + (l16 & 3) * 4);
   int buf = 0;
   for (int t = t0; t < t1; t += kChunk, buf ^= 1) {
     const int n = min(kChunk, t1 - t);
-    if (tv.nonfinite()) dec[buf].bad = 1;   // (columns past d_v repeat others of the row)
-    if constexpr (kOut) tq.store(qt, n, a.dk);
-    tk.store(kt, n, a.dk);
-    tv.store(vt, n, nc);
+    // opaque, so that what is XORed from them is formed where it is used and not kept in registers
+    // over the whole loop
+    asm volatile("" : "+v"(rq), "+v"(rp), "+v"(ck), "+v"(cv));
+    asm volatile("" : "+v"(gnext));         // arrived with the tiles, not after the next ones
+    const bool mine = tv.nonfinite();       // (columns past d_v repeat others of the row)
+    if (mine) dec[buf].bad = 1;
+    if constexpr (kOut) {
+      tq.trim(n, a.dk);
+      tq.store(qt);
+    }
+    tk.trim(n, a.dk);
+    tk.store(kt);
+    tv.trim(n, nc);
+    if constexpr (kHasV) tv.store(vt);
+    if constexpr (kParts) {
+      using TV = Tile<DV, NT>;
+      const int row = tid / TV::kPer, c = tid % TV::kPer * 8;
+#pragma unroll
+      for (int i = 0; i < TV::kN; ++i) {
+        uint4 part[PARTS];
+        const float w = dec[buf].w[row + i * TV::kStep];
+        if (mine) tv.template split<PARTS, true>(i, w, part);
+        else tv.template split<PARTS, false>(i, w, part);
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p)
+          *reinterpret_cast<uint4*>(wt + p * kTileV + at<DV>(row + i * TV::kStep, c)) = part[p];
+      }
+    }
+    if constexpr (kOut)
+      if (t > t0) store_out(t - kChunk);
     __syncthreads();
     const Decays& D = dec[buf];
     if (t + kChunk < t1) {
       fetch(t + kChunk);
-      if (wave == 0) {
+      if (wave == NT / 64 - 1) {
         gsum += scan_decays(gnext, &dec[buf ^ 1]);
         gnext = log_decay(t + 2 * kChunk);
       }
@@ -230,23 +348,33 @@ __global__ void __launch_bounds__(kThreads, DK == 256 ? 1 : 2) lin_chunks(LinArg
     }
     f32x4 O[4][VT];
     if constexpr (kOut) {
-      // scores of the 16 queries of this wave: P^T = K Q^T, keys in the rows
-      const int tw = 16 * wave + l16;
-      const float ct = D.c[tw];
-      bf16x8 qf[KS];
+      // scores P^T = K Q^T, keys in the rows: a wave has one tile of 16 keys and meets all query
+      // tiles (four waves), or half of them (eight), with it; above the diagonal it writes zeros
+      constexpr int JT = 16 / (NT / 64);    // query tiles a wave
+      const int i = wave & 3, j0 = JT == 4 ? 0 : (wave >> 2) * 2;
+      if (JT == 4 || i <= j0 + 1) {         // (of the first 32 queries, nobody reads keys from 32 on)
+        bf16x8 kf[KS];
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) qf[ks] = row_operand<DK>(qt, tw, 32 * ks + g4);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (i > wave) break;
-        f32x4 p = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) p = mfma(row_operand<DK>(kt, 16 * i + l16, 32 * ks + g4), qf[ks], p);
+        for (int ks = 0; ks < KS; ++ks) kf[ks] = row_operand(kt, rq + i * 32 * DK, ks, 0);
         const f32x4 cs = *reinterpret_cast<const f32x4*>(&D.c[16 * i + g4]);
-        float x[4];
+        const int rj = rq + j0 * 32 * DK, pj = (rp ^ (i << 5)) + j0 * 32 * kChunk;
+        f32x4 p[JT];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) x[r] = 16 * i + g4 + r <= tw ? p[r] * exp2f(ct - cs[r]) : 0.f;
-        *reinterpret_cast<uint2*>(pt + at<kChunk>(tw, 16 * i + g4)) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+        for (int j = 0; j < JT; ++j) p[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int j = 0; j < JT; ++j) p[j] = mfma(kf[ks], row_operand(qt, rj, ks, j * 32 * DK), p[j]);
+        const int ahead = l16 - g4 + 16 * (j0 - i);   // queries' lead over the lane's first key
+#pragma unroll
+        for (int j = 0; j < JT; ++j) {
+          const float ct = D.c[16 * (j0 + j) + l16];
+          float x[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            x[r] = ahead + 16 * j >= r ? p[j][r] * __builtin_amdgcn_exp2f(ct - cs[r]) : 0.f;
+          *reinterpret_cast<uint2*>(pt + pj + j * 32 * kChunk) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+        }
       }
       // what the state in front of the chunk gives: O^T = S^T Q^T, scaled by 2^c of the query
 #pragma unroll
@@ -254,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, DK == 256 ? 1 : 2) lin_chunks(LinArg
 #pragma unroll
         for (int v = 0; v < VT; ++v) O[j][v] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
+      for (int ks = 0; ks < KS / DW; ++ks) {
         bf16x8 sf[VT];
 #pragma unroll
         for (int v = 0; v < VT; ++v) {
@@ -264,115 +392,141 @@ __global__ void __launch_bounds__(kThreads, DK == 256 ? 1 : 2) lin_chunks(LinArg
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const bf16x8 q = row_operand<DK>(qt, 16 * j + l16, 32 * ks + g4);
+          const bf16x8 q = row_operand(qt, rq ^ (drow * 2), ks, j * 32 * DK);
 #pragma unroll
           for (int v = 0; v < VT; ++v) O[j][v] = mfma(sf[v], q, O[j][v]);
         }
       }
+      if constexpr (DW == 2) {              // tiles 0 and 3 are finished by wd 0, 1 and 2 by wd 1
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float e = D.e[16 * j + l16];
+        for (int x = 0; x < 2; ++x)
 #pragma unroll
-        for (int v = 0; v < VT; ++v) O[j][v] *= e;
+          for (int v = 0; v < VT; ++v)
+            swap[((wave * 2 + x) * VT + v) * 64 + lane] = wd == 0 ? O[1 + x][v] : O[3 * x][v];
       }
-      __syncthreads();                      // the score tile is whole
     }
     const bool bad = D.bad;
     bf16x8 vf[2][VT];
+    if constexpr (kHasV)
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
+      for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-      for (int v = 0; v < VT; ++v) vf[ks][v] = col_operand<DV>(vt, 32 * ks + g4, wave * CW + 16 * v, l16);
-    if constexpr (kOut) {
-      if (!bad) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int ks = 0; ks <= j / 2; ++ks) {
-            const bf16x8 p = row_operand<kChunk>(pt, 16 * j + l16, 32 * ks + g4);
-#pragma unroll
-            for (int v = 0; v < VT; ++v) O[j][v] = mfma(vf[ks][v], p, O[j][v]);
-          }
-      } else {
-        // 0 times a NaN or an infinity of a later token must not reach this one: the same sums,
-        // over the tokens up to the query's only
-        for (int j = 0; j < 4; ++j)
-          for (int k = 0; k < 16 * j + 16; ++k) {
-            const int q = 16 * j + l16;
-            const float p = bf16_to_f32(*reinterpret_cast<const uint16_t*>(pt + at<kChunk>(q, k)));
-#pragma unroll
-            for (int v = 0; v < VT; ++v) {
-              const uint2 x = *reinterpret_cast<const uint2*>(vt + at<DV>(k, wave * CW + 16 * v + g4));
-              const float y[4] = {__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u),
-                                  __uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u)};
-#pragma unroll
-              for (int jj = 0; jj < 4; ++jj)
-                if (jj == j)
-#pragma unroll
-                  for (int r = 0; r < 4; ++r) O[jj][v][r] = k <= q ? fmaf(p, y[r], O[jj][v][r]) : O[jj][v][r];
-            }
-          }
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int tt = 16 * j + l16;
-#pragma unroll
-        for (int v = 0; v < VT; ++v) {
-          const f32x4 o = O[j][v] * a.scale;
-          if (tt < n && wave * CW + 16 * v + g4 < nc)
-            *reinterpret_cast<uint2*>(op + (t + tt) * a.os[2] + 16 * v + g4) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
-        }
-      }
-    }
+        for (int v = 0; v < VT; ++v) vf[ks][v] = col_operand<DV>(vt, cv, ks, v);
     if (MODE != kLinOut || t + kChunk < t1) {
       // S <- a S + K^T (w V): the parts of w V in the same order of tokens as K^T
-      bf16x8 wf[2][VT][PARTS];
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        const f32x4 w0 = *reinterpret_cast<const f32x4*>(&D.w[32 * ks + g4]);
-        const f32x4 w1 = *reinterpret_cast<const f32x4*>(&D.w[32 * ks + 16 + g4]);
-#pragma unroll
-        for (int v = 0; v < VT; ++v) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            float x = static_cast<float>(vf[ks][v][j]) * (j < 4 ? w0[j & 3] : w1[j & 3]);
-#pragma unroll
-            for (int p = 0; p < PARTS; ++p) {
-              wf[ks][v][p][j] = static_cast<__bf16>(x);
-              x -= static_cast<float>(wf[ks][v][p][j]);
-            }
-          }
-          if (bad)                          // an infinity has no lower parts
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (!(fabsf(static_cast<float>(wf[ks][v][0][j])) < INFINITY))
-#pragma unroll
-                for (int p = 1; p < PARTS; ++p) wf[ks][v][p][j] = static_cast<__bf16>(0.f);
-        }
-      }
       const float dec64 = D.a;
 #pragma unroll
-      for (int i = 0; i < AT; ++i) {
+      for (int i = 0; i < AT; ++i)
 #pragma unroll
         for (int v = 0; v < VT; ++v) S[i][v] *= dec64;
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          const bf16x8 kf = col_operand<DK>(kt, 32 * ks + g4, 16 * i, l16);
+      for (int ks = 0; ks < 2; ++ks) {
+        bf16x8 wf[VT][PARTS];
+        if constexpr (kParts) {
 #pragma unroll
           for (int v = 0; v < VT; ++v)
 #pragma unroll
-            for (int p = PARTS - 1; p >= 0; --p) S[i][v] = mfma(kf, wf[ks][v][p], S[i][v]);
+            for (int p = 0; p < PARTS; ++p) wf[v][p] = col_operand<DV>(wt + p * kTileV, cv, ks, v);
+        } else {
+          const f32x4 w0 = *reinterpret_cast<const f32x4*>(&D.w[32 * ks + g4]);
+          const f32x4 w1 = *reinterpret_cast<const f32x4*>(&D.w[32 * ks + 16 + g4]);
+          auto parts = [&](auto safe) {
+#pragma unroll
+            for (int v = 0; v < VT; ++v) {
+              const uint4 u = __builtin_bit_cast(uint4, vf[ks][v]);
+              const uint32_t uu[4] = {u.x, u.y, u.z, u.w};
+              uint32_t o[PARTS][4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float x = j < 2 ? w0[2 * j] : w1[2 * j - 4], y = j < 2 ? w0[2 * j + 1] : w1[2 * j - 3];
+                split_pair<PARTS, decltype(safe)::value>(__uint_as_float(uu[j] << 16) * x, __uint_as_float(uu[j] & 0xffff0000u) * y, &o[0][j], 4);
+              }
+#pragma unroll
+              for (int p = 0; p < PARTS; ++p) wf[v][p] = __builtin_bit_cast(bf16x8, make_uint4(o[p][0], o[p][1], o[p][2], o[p][3]));
+            }
+          };
+          if (bad) parts(std::true_type{});
+          else parts(std::false_type{});
+        }
+        // four state tiles at a time, part by part: products that follow each other have
+        // different accumulators
+        constexpr int B = AT < 4 ? AT : 4;
+#pragma unroll
+        for (int i0 = 0; i0 < AT; i0 += B) {
+          bf16x8 kf[B];
+#pragma unroll
+          for (int i = 0; i < B; ++i) kf[i] = col_operand<DK>(kt, ck, ks, i0 + i);
+#pragma unroll
+          for (int p = PARTS - 1; p >= 0; --p)
+#pragma unroll
+            for (int i = 0; i < B; ++i)
+#pragma unroll
+              for (int v = 0; v < VT; ++v) S[i0 + i][v] = mfma(kf[i], wf[v][p], S[i0 + i][v]);
         }
       }
     }
-    __syncthreads();                        // the tiles are free
+    // The score tile and the shares are whole, and the tiles of Q, K and V are free: what follows
+    // reads neither, and the next chunk's tiles may be written meanwhile.
+    __syncthreads();
+    if constexpr (kOut) {
+#pragma unroll
+      for (int x = 0; x < OT; ++x) {
+        const int j = DW == 1 ? x : wd == 0 ? 3 * x : 1 + x;
+        const float e = D.e[16 * j + l16];
+        f32x4 o[VT];
+#pragma unroll
+        for (int v = 0; v < VT; ++v) {
+          if constexpr (DW == 2) {
+            o[v] = wd == 0 ? O[3 * x][v] : O[1 + x][v];
+            o[v] += swap[(((wave ^ VW) * 2 + x) * VT + v) * 64 + lane];
+          } else {
+            o[v] = O[x][v];
+          }
+          o[v] *= e;
+        }
+        const int tt = 16 * j + l16;
+        if (!bad) {
+          // keys up to the query's tile: 32 or 64
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks)
+            if (ks <= j / 2) {
+              const bf16x8 p = row_operand(pt, rp, ks, j * 32 * kChunk);
+#pragma unroll
+              for (int v = 0; v < VT; ++v) o[v] = mfma(vf[ks][v], p, o[v]);
+            }
+        } else {
+          // 0 times a NaN or an infinity of a later token must not reach this one: the same
+          // sums, over the tokens up to the query's only
+#pragma unroll 1
+          for (int k = 0; k < 16 * j + 16; ++k) {
+            const float p = bf16_to_f32(*reinterpret_cast<const uint16_t*>(pt + at<kChunk>(tt, k)));
+#pragma unroll
+            for (int v = 0; v < VT; ++v) {
+              const uint2 u = *reinterpret_cast<const uint2*>(vt + at<DV>(k, wv * CW + 16 * v + g4));
+              const float y[4] = {__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                                  __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u)};
+#pragma unroll
+              for (int r = 0; r < 4; ++r) o[v][r] = k <= tt ? fmaf(p, y[r], o[v][r]) : o[v][r];
+            }
+          }
+        }
+#pragma unroll
+        for (int v = 0; v < VT; ++v) {
+          o[v] *= a.scale;
+          done[x][v] = make_uint2(pack_bf16x2(o[v][0], o[v][1]), pack_bf16x2(o[v][2], o[v][3]));
+        }
+      }
+      if (bad) __syncthreads();             // (the V tile was read here)
+    }
   }
+  if constexpr (kOut)
+    if (t0 < t1) store_out(t0 + (t1 - t0 - 1) / kChunk * kChunk);
   float* to = nullptr;
   if (MODE == kLinWhole && keep) to = a.state_out + (static_cast<int64_t>(slot) * a.H + h) * sh;
   if (MODE == kLinState) {
     const int64_t i = lin_segment(a, s, row0, seg) * a.H + h;
     to = a.seg_state + i * sh;
-    if (c0 == 0 && tid == 0) a.seg_decay[i] = exp2f(static_cast<float>(gsum));
+    if (c0 == 0 && wave == NT / 64 - 1 && lane == 0) a.seg_decay[i] = exp2f(static_cast<float>(gsum));
   }
   if (to) {
 #pragma unroll
@@ -381,39 +535,36 @@ __global__ void __launch_bounds__(kThreads, DK == 256 ? 1 : 2) lin_chunks(LinArg
       for (int j = 0; j < VT; ++j)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int d = 16 * i + g4 + r, v = vcol + 16 * j;
+          const int d = drow + 16 * i + g4 + r, v = vcol + 16 * j;
           if (d < a.dk && v < a.dv) to[static_cast<int64_t>(d) * a.dv + v] = S[i][j][r];
         }
   }
 }
 
-// Columns a wave: 32 where d_v has a second half for them (each chunk's Q and K are then read
-// from LDS for twice the columns), else 16.
-int columns(const LinArgs& a) { return a.dv > 64 ? 32 : 16; }
+// Columns a block: 128 where d_v has them (each chunk's Q and K are then read from LDS for
+// twice the columns), else 64.
+int columns(const LinArgs& a) { return a.dk > 128 && a.dv > 64 ? 128 : 64; }
 
-template <int DK, int CW>
+template <int DK, int CW, int VW, int DW>
 hipError_t launch_t(const LinArgs& a, LinMode mode, hipStream_t st) {
-  const int slices = (a.dv + 4 * CW - 1) / (4 * CW);
+  const int slices = (a.dv + VW * CW - 1) / (VW * CW);
   const bool rest = a.T > 0 && a.zero_rest && mode != kLinState;
-  const dim3 grid(a.H * slices, a.n_seg, a.S + (rest ? 1 : 0));
-  if (mode == kLinWhole) hipLaunchKernelGGL((lin_chunks<DK, CW, kLinWhole>), grid, dim3(kThreads), 0, st, a, slices);
-  else if (mode == kLinState) hipLaunchKernelGGL((lin_chunks<DK, CW, kLinState>), grid, dim3(kThreads), 0, st, a, slices);
-  else hipLaunchKernelGGL((lin_chunks<DK, CW, kLinOut>), grid, dim3(kThreads), 0, st, a, slices);
+  const dim3 grid(a.H * slices, a.n_seg, a.S + (rest ? 1 : 0)), block(64 * VW * DW);
+  if (mode == kLinWhole) hipLaunchKernelGGL((lin_chunks<DK, CW, VW, DW, kLinWhole>), grid, block, 0, st, a, slices);
+  else if (mode == kLinState) hipLaunchKernelGGL((lin_chunks<DK, CW, VW, DW, kLinState>), grid, block, 0, st, a, slices);
+  else hipLaunchKernelGGL((lin_chunks<DK, CW, VW, DW, kLinOut>), grid, block, 0, st, a, slices);
   return hipGetLastError();
 }
 
 }  // namespace
 
-int lin_mfma_blocks(const LinArgs& a) {
-  const int w = 4 * columns(a);
-  return a.H * ((a.dv + w - 1) / w);
-}
+int lin_mfma_blocks(const LinArgs& a) { return a.H * ((a.dv + columns(a) - 1) / columns(a)); }
 
 hipError_t launch_lin_mfma(const LinArgs& a, LinMode mode, hipStream_t st) {
-  const bool wide = columns(a) == 32;
-  if (a.dk <= 64) return wide ? launch_t<64, 32>(a, mode, st) : launch_t<64, 16>(a, mode, st);
-  if (a.dk <= 128) return wide ? launch_t<128, 32>(a, mode, st) : launch_t<128, 16>(a, mode, st);
-  return wide ? launch_t<256, 32>(a, mode, st) : launch_t<256, 16>(a, mode, st);
+  const bool wide = columns(a) == 128;
+  if (a.dk <= 64) return launch_t<64, 16, 4, 1>(a, mode, st);
+  if (a.dk <= 128) return launch_t<128, 16, 4, 1>(a, mode, st);
+  return wide ? launch_t<256, 32, 4, 2>(a, mode, st) : launch_t<256, 16, 4, 2>(a, mode, st);
 }
 
 }  // namespace rn
