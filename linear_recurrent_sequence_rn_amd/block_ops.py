@@ -9,6 +9,7 @@ device need not be the current one. New outputs are allocated with torch.
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Optional
 
 import numpy as np
@@ -44,23 +45,33 @@ class RnLinearDesc(ctypes.Structure):
                 ("g_stride", _i64 * 3), ("out_stride", _i64 * 3)]
 
 
+# The calls below fill their descriptors with struct, several times as fast as setting the
+# fields one by one: a call costs the host a few microseconds in all, which is what the
+# smallest ones take.
+_pack_norm = struct.Struct("@qiiifqqqq").pack
+_pack_rotary = struct.Struct("@iiiiiiiIqfP12q").pack
+_pack_linear = struct.Struct("@10iIfqi15q").pack
+assert struct.calcsize("@qiiifqqqq") == ctypes.sizeof(RnNormDesc)
+assert struct.calcsize("@iiiiiiiIqfP12q") == ctypes.sizeof(RnRotaryDesc)
+assert struct.calcsize("@10iIfqi15q") == ctypes.sizeof(RnLinearDesc)
+
+
 def _bind(L):
-    ND, RD, LD = (ctypes.POINTER(t) for t in (RnNormDesc, RnRotaryDesc, RnLinearDesc))
+    # descriptors as plain pointers: byref(...) of the structures above, or packed bytes
     for name, args, res in (
-            ("rn_layernorm_forward", [ND] + [_vp] * 7, _i32),
-            ("rn_layernorm_backward_workspace_bytes", [ND], _sz),
-            ("rn_layernorm_backward", [ND] + [_vp] * 8 + [_sz, _vp], _i32),
-            ("rn_rotary", [RD] + [_vp] * 6, _i32),
+            ("rn_layernorm_forward", [_vp] * 8, _i32),
+            ("rn_layernorm_backward_workspace_bytes", [_vp], _sz),
+            ("rn_layernorm_backward", [_vp] * 9 + [_sz, _vp], _i32),
+            ("rn_rotary", [_vp] * 7, _i32),
             ("rn_rotary_frequencies", [_i32, _f64, _i32, _f64, _f64, _f64, _f64, _vp, _vp], _i32),
-            ("rn_linear_attention_workspace_bytes", [LD], _sz),
-            ("rn_linear_attention_chunked", [LD] + [_vp] * 11 + [_sz, _vp], _i32),
-            ("rn_linear_attention_step", [LD] + [_vp] * 8, _i32)):
+            ("rn_linear_attention_workspace_bytes", [_vp], _sz),
+            ("rn_linear_attention_chunked", [_vp] * 12 + [_sz, _vp], _i32),
+            ("rn_linear_attention_step", [_vp] * 9, _i32)):
         f = getattr(L, name)
         f.argtypes, f.restype = args, res
 
 
 _bind(lib)
-_byref = ctypes.byref
 _CODES = {torch.float32: RN_F32, torch.bfloat16: RN_BF16}
 
 
@@ -71,35 +82,33 @@ def _code(t: torch.dtype) -> int:
     return c
 
 
-class _on:
-    """Makes ``device`` current for a call, where it is not already, and gives its current
-    stream. (A kernel launched on another device's stream would fail.)"""
-    __slots__ = ("device", "last")
-
-    def __init__(self, device):
-        self.device = device
-
-    def __enter__(self):
-        i = self.device.index
-        self.last = torch.cuda.current_device()
-        if i != self.last:
-            torch.cuda.set_device(i)
-        return torch.cuda.current_stream(i).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.device.index != self.last:
-            torch.cuda.set_device(self.last)
+# torch's own short ways to the current device and stream, where this torch has them
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
-def _device(first, *others):
-    """The GPU all given tensors live on."""
-    if not first.is_cuda:
+def _call(i, f, *args):
+    """f(*args, stream) on the current stream of GPU i, which need not be the current GPU (a
+    kernel launched on another device's stream would fail)."""
+    if _current_device() == i:
+        st = f(*args, _raw_stream(i))
+    else:
+        with torch.cuda.device(i):
+            st = f(*args, _raw_stream(i))
+    if st:
+        _check(st)
+
+
+def _device(first, *others) -> int:
+    """The number of the GPU that all given tensors live on."""
+    i = first.get_device()
+    if i < 0:
         raise ValueError("tensors must live on the GPU")
-    dev = first.device
     for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors must be on one device ({dev}); got {t.device}")
-    return dev
+        if t is not None and t.get_device() != i:
+            raise ValueError(f"tensors must be on one device ({first.device}); got {t.device}")
+    return i
 
 
 def _p(t: Optional[torch.Tensor]):
@@ -108,13 +117,13 @@ def _p(t: Optional[torch.Tensor]):
 
 def _whole(t, dtype, shape, name):
     """A contiguous tensor of that type and shape, or None."""
-    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
+    if t is not None and (t.dtype != dtype or t.shape != shape or not t.is_contiguous()):
         raise ValueError(f"{name} must be contiguous {dtype} {tuple(shape)}; got {t.dtype} {tuple(t.shape)}")
 
 
-def _get_workspace(workspace, need, device):
+def _get_workspace(workspace, need, like):
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+        return torch.empty(need, dtype=torch.uint8, device=like.device) if need else None
     if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
     return workspace
@@ -124,14 +133,14 @@ def _get_workspace(workspace, need, device):
 
 def _row_stride(t, name) -> int:
     """Elements between the rows of [..., d]: leading axes must step like one axis."""
-    d = t.dim()
+    if t is None:
+        return 0
     if t.is_contiguous():
         return t.shape[-1]
     if t.shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name}: the last axis must be contiguous")
     stride, span = None, 1
-    for i in range(d - 2, -1, -1):
-        n, s = t.shape[i], t.stride(i)
+    for n, s in zip(t.shape[-2::-1], t.stride()[-2::-1]):
         if n == 1:
             continue
         if stride is None:
@@ -140,6 +149,13 @@ def _row_stride(t, name) -> int:
             raise ValueError(f"{name}: the leading axes must have one common row stride")
         span *= n
     return t.shape[-1] if stride is None else stride
+
+
+def _new(x, dtype):
+    """A new contiguous tensor of x's shape."""
+    if x.dtype == dtype and x.is_contiguous():
+        return torch.empty_like(x)
+    return torch.empty(x.shape, dtype=dtype, device=x.device)
 
 
 def _like(t, x, name):
@@ -154,39 +170,38 @@ def rn_layernorm(x, weight=None, bias=None, eps=1e-5, *, residual=None, sum_out=
     residual or ``sum_out`` is given; sum = x + residual in x's type (the next residual
     stream). ``sum_out`` may be x or residual, ``out`` may be x."""
     dev = _device(x, residual, weight, bias, sum_out, out)
-    d = x.shape[-1] if x.dim() else 0
-    if x.numel() == 0:
-        raise ValueError(f"x must be [..., d] with at least one row; got {tuple(x.shape)}")
+    shape = x.shape
+    d = shape[-1] if shape else 0
+    n = x.numel()
+    if n == 0:
+        raise ValueError(f"x must be [..., d] with at least one row; got {tuple(shape)}")
     _like(residual, x, "residual")
     _whole(weight, torch.float32, (d,), "weight")
     _whole(bias, torch.float32, (d,), "bias")
-    od = x.dtype if out_dtype is None else out_dtype
     if out is None:
-        out = torch.empty(x.shape, dtype=od, device=dev)
-    elif out.shape != x.shape or (out_dtype is not None and out.dtype != od):
-        raise ValueError(f"out must be {od} {tuple(x.shape)}; got {out.dtype} {tuple(out.shape)}")
+        out = _new(x, x.dtype if out_dtype is None else out_dtype)
+    elif out.shape != shape or (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError(f"out must be {out_dtype or out.dtype} {tuple(shape)}; got {out.dtype} {tuple(out.shape)}")
     if sum_out is None:
         if residual is not None:
-            sum_out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+            sum_out = _new(x, x.dtype)
     else:
         _like(sum_out, x, "sum_out")
-    desc = RnNormDesc(x.numel() // d, d, _code(x.dtype), _code(out.dtype), eps, _row_stride(x, "x"),
-                      0 if residual is None else _row_stride(residual, "residual"),
-                      0 if sum_out is None else _row_stride(sum_out, "sum_out"), _row_stride(out, "out"))
-    with _on(dev) as stream:
-        _check(lib.rn_layernorm_forward(_byref(desc), x.data_ptr(), _p(residual), _p(weight), _p(bias),
-                                        _p(sum_out), out.data_ptr(), stream))
+    desc = _pack_norm(n // d, d, _code(x.dtype), _code(out.dtype), eps, _row_stride(x, "x"),
+                      _row_stride(residual, "residual"), _row_stride(sum_out, "sum_out"), _row_stride(out, "out"))
+    _call(dev, lib.rn_layernorm_forward, desc, x.data_ptr(), _p(residual), _p(weight), _p(bias), _p(sum_out),
+          out.data_ptr())
     return out if sum_out is None else (out, sum_out)
 
 
 def _norm_backward_desc(dout, x, eps, dsum, dx):
-    return RnNormDesc(x.numel() // x.shape[-1], x.shape[-1], _code(x.dtype), _code(dout.dtype), eps,
-                      _row_stride(x, "x"), 0 if dsum is None else _row_stride(dsum, "dsum"),
-                      _row_stride(dx, "dx"), _row_stride(dout, "dout"))
+    d = x.shape[-1]
+    return _pack_norm(x.numel() // d, d, _code(x.dtype), _code(dout.dtype), eps, _row_stride(x, "x"),
+                      _row_stride(dsum, "dsum"), _row_stride(dx, "dx"), _row_stride(dout, "dout"))
 
 
 def rn_layernorm_backward_workspace_bytes(dout, x) -> int:
-    return int(lib.rn_layernorm_backward_workspace_bytes(_byref(_norm_backward_desc(dout, x, 0.0, None, x))))
+    return int(lib.rn_layernorm_backward_workspace_bytes(_norm_backward_desc(dout, x, 0.0, None, x)))
 
 
 def rn_layernorm_backward(dout, x, weight=None, eps=1e-5, *, dsum=None, dx=None, want_dweight=True,
@@ -195,7 +210,7 @@ def rn_layernorm_backward(dout, x, weight=None, eps=1e-5, *, dsum=None, dx=None,
     residual), ``dsum`` the gradient that reaches this sum by its other path, in x's type.
     Returns a dict with dx (the gradient of x and of the residual; in x's type) and, unless not
     wanted, dweight and dbias (float32 [d])."""
-    dev = _device(x, dout, weight, dsum, dx)
+    dev = _device(x, dout, weight, dsum, dx, workspace)
     if x.numel() == 0:
         raise ValueError(f"x must be [..., d] with at least one row; got {tuple(x.shape)}")
     d = x.shape[-1]
@@ -204,26 +219,21 @@ def rn_layernorm_backward(dout, x, weight=None, eps=1e-5, *, dsum=None, dx=None,
     _whole(weight, torch.float32, (d,), "weight")
     _like(dsum, x, "dsum")
     if dx is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        dx = _new(x, x.dtype)
     else:
         _like(dx, x, "dx")
     desc = _norm_backward_desc(dout, x, eps, dsum, dx)
     got = {"dx": dx}
     if want_dweight:
-        got["dweight"] = torch.empty(d, dtype=torch.float32, device=dev)
+        got["dweight"] = torch.empty(d, dtype=torch.float32, device=x.device)
     if want_dbias:
-        got["dbias"] = torch.empty(d, dtype=torch.float32, device=dev)
-    with _on(dev) as stream:
-        if want_dweight or want_dbias:
-            workspace = _get_workspace(workspace, int(lib.rn_layernorm_backward_workspace_bytes(_byref(desc))), dev)
-            if workspace is not None:
-                _device(x, workspace)
-        else:
-            workspace = None
-        _check(lib.rn_layernorm_backward(
-            _byref(desc), dout.data_ptr(), x.data_ptr(), _p(weight), _p(dsum), dx.data_ptr(),
-            _p(got.get("dweight")), _p(got.get("dbias")), _p(workspace),
-            0 if workspace is None else workspace.numel(), stream))
+        got["dbias"] = torch.empty(d, dtype=torch.float32, device=x.device)
+    if want_dweight or want_dbias:
+        workspace = _get_workspace(workspace, lib.rn_layernorm_backward_workspace_bytes(desc), x)
+    else:
+        workspace = None
+    _call(dev, lib.rn_layernorm_backward, desc, dout.data_ptr(), x.data_ptr(), _p(weight), _p(dsum), dx.data_ptr(),
+          _p(got.get("dweight")), _p(got.get("dbias")), _p(workspace), 0 if workspace is None else workspace.numel())
     return got
 
 
@@ -233,19 +243,20 @@ def _bhn(t, name):
     """Strides of [B, H, N, ...] with a contiguous last axis (if there is a fourth)."""
     if t.dim() == 4 and t.shape[3] > 1 and t.stride(3) != 1:
         raise ValueError(f"{name}: the last axis must be contiguous")
-    return (_i64 * 3)(*t.stride()[:3])
+    return t.stride()[:3]
 
 
 def _new_like(t, shape=None, dtype=None):
     """A new tensor of t's (or the given) shape [B, H, N, d], token-major in memory where t is."""
     B, H, N, d = t.shape if shape is None else shape
     dtype = t.dtype if dtype is None else dtype
-    if t.stride(1) < t.stride(2):
-        return torch.empty((B, N, H, d), dtype=dtype, device=t.device).transpose(1, 2)
+    _, h, n, _ = t.stride()
+    if h < n:                             # [B, N, H, d] in memory
+        return torch.empty_strided((B, H, N, d), (N * H * d, d, H * d, 1), dtype=dtype, device=t.device)
     return torch.empty((B, H, N, d), dtype=dtype, device=t.device)
 
 
-_NO_STRIDE = (_i64 * 3)()
+_NO_STRIDE = (0, 0, 0)
 
 
 def rn_rotary(q, k=None, theta=None, *, pos0=0, pos=None, half=False, inverse=False, magnitude=1.0,
@@ -272,7 +283,7 @@ def rn_rotary(q, k=None, theta=None, *, pos0=0, pos=None, half=False, inverse=Fa
         raise ValueError("theta must be one-dimensional")
     flags = (RN_ROTARY_HALF if half else 0) | (RN_ROTARY_INVERSE if inverse else 0)
     if pos is not None:
-        if pos.dtype != torch.int64 or not pos.is_contiguous() or tuple(pos.shape) not in ((B,), (B, N)):
+        if pos.dtype != torch.int64 or not pos.is_contiguous() or pos.shape not in ((B,), (B, N)):
             raise ValueError(f"pos must be contiguous int64 [{B}] or [{B}, {N}]; got {pos.dtype} {tuple(pos.shape)}")
         if pos.dim() == 2:
             flags |= RN_ROTARY_POS_TOKEN
@@ -285,11 +296,11 @@ def rn_rotary(q, k=None, theta=None, *, pos0=0, pos=None, half=False, inverse=Fa
         q_out = _new_like(q)
     if k is not None and k_out is None:
         k_out = _new_like(k)
-    desc = RnRotaryDesc(B, N, Hq, 0 if k is None else k.shape[1], d, 2 * th.size, _code(q.dtype), flags, pos0,
-                        magnitude, th.ctypes.data, _bhn(q, "q"), _NO_STRIDE if k is None else _bhn(k, "k"),
-                        _bhn(q_out, "q_out"), _NO_STRIDE if k is None else _bhn(k_out, "k_out"))
-    with _on(dev) as stream:
-        _check(lib.rn_rotary(_byref(desc), _p(pos), q.data_ptr(), _p(k), q_out.data_ptr(), _p(k_out), stream))
+    qs, qos = _bhn(q, "q"), _bhn(q_out, "q_out")
+    ks, kos = (_NO_STRIDE, _NO_STRIDE) if k is None else (_bhn(k, "k"), _bhn(k_out, "k_out"))
+    desc = _pack_rotary(B, N, Hq, 0 if k is None else k.shape[1], d, 2 * th.size, _code(q.dtype), flags, pos0,
+                        magnitude, th.ctypes.data, *qs, *ks, *qos, *kos)
+    _call(dev, lib.rn_rotary, desc, _p(pos), q.data_ptr(), _p(k), q_out.data_ptr(), _p(k_out))
     return q_out if k is None else (q_out, k_out)
 
 
@@ -328,9 +339,9 @@ def _linear_shapes(q, k, v, g):
 
 
 def _linear_desc(q, k, v, g, S, N, T, n_slots, out_dtype, flags, qk_scale, out):
-    return RnLinearDesc(S, N, g.shape[1], q.shape[1], k.shape[1], v.shape[1], q.shape[3], v.shape[3], _code(q.dtype),
-                        _code(out_dtype), flags, qk_scale, T, n_slots, _bhn(q, "q"), _bhn(k, "k"), _bhn(v, "v"),
-                        (_i64 * 3)(*g.stride()), out)
+    return _pack_linear(S, N, g.shape[1], q.shape[1], k.shape[1], v.shape[1], q.shape[3], v.shape[3], _code(q.dtype),
+                        _code(out_dtype), flags, qk_scale, T, n_slots, *_bhn(q, "q"), *_bhn(k, "k"), *_bhn(v, "v"),
+                        *g.stride(), *out)
 
 
 def _linear_out(out, q, v, H, out_dtype):
@@ -339,20 +350,20 @@ def _linear_out(out, q, v, H, out_dtype):
     od = (q.dtype if out is None else out.dtype) if out_dtype is None else out_dtype
     if out is None:
         return _new_like(v, shape, od), True
-    if tuple(out.shape) != shape or out.dtype != od:
+    if out.shape != shape or out.dtype != od:
         raise ValueError(f"out must be {od} {shape}; got {out.dtype} {tuple(out.shape)}")
     return out, False
 
 
 def _int32(t, n, name):
-    if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != (n,) or not t.is_contiguous()):
+    if t is not None and (t.dtype != torch.int32 or t.shape != (n,) or not t.is_contiguous()):
         raise ValueError(f"{name} must be contiguous int32 [{n}]; got {t.dtype} {tuple(t.shape)}")
 
 
 def _linear_state(s, shape, slots, name):
     if s is None:
         return
-    if s.dtype != torch.float32 or not s.is_contiguous() or s.dim() != 4 or tuple(s.shape[1:]) != shape[1:] or \
+    if s.dtype != torch.float32 or not s.is_contiguous() or s.dim() != 4 or s.shape[1:] != shape[1:] or \
             (slots is None and s.shape[0] != shape[0]) or s.shape[0] < 1:
         raise ValueError(f"{name} must be contiguous float32 [{'slots' if slots is not None else shape[0]}, "
                          f"{shape[1]}, {shape[2]}, {shape[3]}]; got {s.dtype} {tuple(s.shape)}")
@@ -393,7 +404,8 @@ def _linear_call(q, k, v, g, qk_scale, lengths, cu, max_len, state_in, state_out
         if len(sizes) > 1:
             raise ValueError("state_in and state_out must have the same number of slots")
         n_slots = sizes.pop() if sizes else 1
-    return _linear_desc(q, k, v, g, S, N, T, n_slots, out.dtype, flags, qk_scale, _bhn(out, "out")), out, state_out
+    desc = _linear_desc(q, k, v, g, S, N, T, n_slots, out.dtype, flags, qk_scale, _bhn(out, "out"))
+    return desc, S, out, state_out
 
 
 def rn_linear_attention_workspace_bytes(q, k, v, log_decay, *, cu_seqlens=None, max_len=None, out_dtype=None,
@@ -402,10 +414,10 @@ def rn_linear_attention_workspace_bytes(q, k, v, log_decay, *, cu_seqlens=None, 
     _linear_shapes(q, k, v, log_decay)
     B, rows = q.shape[0], q.shape[2]
     S, T = (B, 0) if cu_seqlens is None else (cu_seqlens.numel() - 1, rows)
-    o = (_i64 * 3)(log_decay.shape[1] * rows * v.shape[-1], rows * v.shape[-1], v.shape[-1])
+    o = (log_decay.shape[1] * rows * v.shape[-1], rows * v.shape[-1], v.shape[-1])
     desc = _linear_desc(q, k, v, log_decay, S, max_len or rows, T, 0, out_dtype or q.dtype,
                         RN_LINEAR_GENERIC if force_generic else 0, 1.0, o)
-    return int(lib.rn_linear_attention_workspace_bytes(_byref(desc)))
+    return int(lib.rn_linear_attention_workspace_bytes(desc))
 
 
 def rn_linear_attention_chunked(q, k, v, log_decay, *, qk_scale=1.0, lengths=None, cu_seqlens=None, max_len=None,
@@ -425,17 +437,15 @@ def rn_linear_attention_chunked(q, k, v, log_decay, *, qk_scale=1.0, lengths=Non
     dev = _device(q, k, v, log_decay, lengths, cu_seqlens, slots, out, workspace, state_in,
                   state_out if isinstance(state_out, torch.Tensor) else None)
     _linear_shapes(q, k, v, log_decay)
-    desc, out, state_out = _linear_call(q, k, v, log_decay, qk_scale, lengths, cu_seqlens, max_len, state_in,
-                                        state_out, slots, out, out_dtype, force_generic)
-    _int32(lengths, desc.S, "lengths")
-    _int32(cu_seqlens, desc.S + 1, "cu_seqlens")
-    _int32(slots, desc.S, "slots")
-    with _on(dev) as stream:
-        workspace = _get_workspace(workspace, int(lib.rn_linear_attention_workspace_bytes(_byref(desc))), dev)
-        _check(lib.rn_linear_attention_chunked(
-            _byref(desc), _p(cu_seqlens), _p(lengths), _p(slots), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-            log_decay.data_ptr(), _p(state_in), _p(state_out), out.data_ptr(), _p(workspace),
-            0 if workspace is None else workspace.numel(), stream))
+    desc, S, out, state_out = _linear_call(q, k, v, log_decay, qk_scale, lengths, cu_seqlens, max_len, state_in,
+                                           state_out, slots, out, out_dtype, force_generic)
+    _int32(lengths, S, "lengths")
+    _int32(cu_seqlens, S + 1, "cu_seqlens")
+    _int32(slots, S, "slots")
+    workspace = _get_workspace(workspace, lib.rn_linear_attention_workspace_bytes(desc), q)
+    _call(dev, lib.rn_linear_attention_chunked, desc, _p(cu_seqlens), _p(lengths), _p(slots), q.data_ptr(),
+          k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _p(state_in), _p(state_out), out.data_ptr(), _p(workspace),
+          0 if workspace is None else workspace.numel())
     return out, state_out
 
 
@@ -453,7 +463,6 @@ def rn_linear_attention_step(q, k, v, log_decay, state, *, qk_scale=1.0, slots=N
     _linear_state(state, (S, H, q.shape[-1], v.shape[-1]), slots, "state")
     _int32(slots, S, "slots")
     desc = _linear_desc(q, k, v, log_decay, S, 1, 0, state.shape[0], out.dtype, 0, qk_scale, _bhn(out, "out"))
-    with _on(dev) as stream:
-        _check(lib.rn_linear_attention_step(_byref(desc), _p(slots), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                            log_decay.data_ptr(), state.data_ptr(), out.data_ptr(), stream))
+    _call(dev, lib.rn_linear_attention_step, desc, _p(slots), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          log_decay.data_ptr(), state.data_ptr(), out.data_ptr())
     return out
