@@ -6,7 +6,7 @@
 // xh mean(g xh)) + dh, dw = sum_rows dy xh, db = sum_rows dy.
 //
 // Bound by HBM: every tensor is read or written once. A row lives in the registers of one
-// wave (W = 1, four rows per 256-thread block) or of a whole block (W = 4), so the passes
+// wave (W = 1, four rows per 256-thread block) or of a whole block (W = 4 or 16), so the passes
 // over it (mean, centred squares, result) cost no memory access. Blocks walk over rows:
 // the weights, and in the backward the column sums of dw and db, then stay in registers
 // too, and the backward writes one partial row of sums per block, which a second kernel
@@ -19,7 +19,8 @@
 namespace rn {
 namespace {
 
-constexpr int kThreads = 256;
+// Threads of a block whose rows take W waves each.
+constexpr int threads(int W) { return W > 4 ? 64 * W : 256; }
 
 // V consecutive elements of type DT from a 16-byte (V > 1) or element-aligned address.
 template <int DT, int V> struct Vec;
@@ -73,37 +74,75 @@ template <int V> struct Vec<RN_BF16, V> {   // V = 4 or 8
   }
 };
 
-// Sum of two values over the W waves that share a row; every thread receives both. `red`
-// holds 2 W floats per use; callers alternate between two areas, so that one barrier per
-// sum is enough.
-template <int W>
-__device__ __forceinline__ void row_sum2(float& a, float& b, float* red) {
+// The same elements as they are in memory, for rows on their way: V elements of type DT.
+template <int DT, int V>
+struct Raw {
+  static constexpr int kBytes = V * (DT == RN_F32 ? 4 : 2);
+  uint32_t u[(kBytes + 3) / 4];
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    if constexpr (kBytes == 2) {
+      u[0] = static_cast<const uint16_t*>(p)[i];
+    } else {
+      const char* s = static_cast<const char*>(p) + i * (kBytes / V);
 #pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) {
-    a += __shfl_xor(a, o, 64);
-    b += __shfl_xor(b, o, 64);
+      for (int j = 0; j < kBytes / 4; j += 4) {
+        if constexpr (kBytes >= 16) {
+          const uint4 x = reinterpret_cast<const uint4*>(s)[j / 4];
+          u[j] = x.x; u[j + 1] = x.y; u[j + 2] = x.z; u[j + 3] = x.w;
+        } else if constexpr (kBytes == 8) {
+          const uint2 x = *reinterpret_cast<const uint2*>(s);
+          u[0] = x.x; u[1] = x.y;
+        } else {
+          u[0] = *reinterpret_cast<const uint32_t*>(s);
+        }
+      }
+    }
   }
-  if constexpr (W > 1) {
-    const int w = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0) { red[2 * w] = a; red[2 * w + 1] = b; }
-    __syncthreads();
-    a = 0.f; b = 0.f;
+  __device__ __forceinline__ float get(int j) const {
+    if constexpr (DT == RN_F32) return __uint_as_float(u[j]);
+    else return j % 2 ? __uint_as_float(u[j / 2] & 0xffff0000u) : __uint_as_float(u[j / 2] << 16);
+  }
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int i = 0; i < W; ++i) { a += red[2 * i]; b += red[2 * i + 1]; }
+    for (int j = 0; j < (kBytes + 3) / 4; ++j) u[j] = 0;
   }
+};
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_or_zero(float x) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, ROWS, 0xf, true));
 }
-template <int W>
-__device__ __forceinline__ float row_sum(float a, float* red) {
-  a = wave_sum(a);
+// Sum over a wave, in every lane: over the 16 lanes of each row, over the rows, from lane 63.
+__device__ __forceinline__ float wave_total(float x) {
+  x += dpp_or_zero<0x111, 0xf>(x);
+  x += dpp_or_zero<0x112, 0xf>(x);
+  x += dpp_or_zero<0x114, 0xf>(x);
+  x += dpp_or_zero<0x118, 0xf>(x);
+  x += dpp_or_zero<0x142, 0xa>(x);
+  x += dpp_or_zero<0x143, 0xc>(x);
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 63));
+}
+
+// Sums of N values over the W waves that share a row; every thread receives them. `red` holds
+// W N floats. The caller does not write the same area again before a barrier has passed since.
+template <int W, int N>
+__device__ __forceinline__ void row_sums(float (&x)[N], float* red) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) x[n] = wave_total(x[n]);
   if constexpr (W > 1) {
     const int w = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0) red[w] = a;
-    __syncthreads();
-    a = 0.f;
+    if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) a += red[i];
+      for (int n = 0; n < N; ++n) red[w * N + n] = x[n];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      x[n] = 0.f;
+#pragma unroll
+      for (int i = 0; i < W; ++i) x[n] += red[i * N + n];
+    }
   }
-  return a;
 }
 
 struct NormArgs {
@@ -123,23 +162,20 @@ struct NormArgs {
 
 // Thread `lane` of a row's 64 W lanes holds elements [V (lane + 64 W i), +V) for i < NV.
 template <int IN, int OUT, int V, int W, int NV>
-__global__ void __launch_bounds__(kThreads) norm_rows(NormArgs a) {
+__global__ void __launch_bounds__(threads(W)) norm_rows(NormArgs a) {
   constexpr int L = 64 * W;
-  constexpr int R = kThreads / L;         // rows per block
-  constexpr bool kHold = NV * V <= 16;    // weights kept in registers
+  constexpr int R = threads(W) / L;       // rows per block
   __shared__ float red[2][W];
   const int lane = threadIdx.x % L;
-  float w[kHold ? NV * V : 1], b[kHold ? NV * V : 1];
-  if constexpr (kHold) {
+  float w[NV * V], b[NV * V];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = V * (lane + L * i);
+  for (int i = 0; i < NV; ++i) {
+    const int c = V * (lane + L * i);
 #pragma unroll
-      for (int j = 0; j < V; ++j) { w[i * V + j] = 1.f; b[i * V + j] = 0.f; }
-      if (c < a.d) {
-        if (a.w) Vec<RN_F32, V>::load(a.w, c, w + i * V);
-        if (a.b) Vec<RN_F32, V>::load(a.b, c, b + i * V);
-      }
+    for (int j = 0; j < V; ++j) { w[i * V + j] = 1.f; b[i * V + j] = 0.f; }
+    if (c < a.d) {
+      if (a.w) Vec<RN_F32, V>::load(a.w, c, w + i * V);
+      if (a.b) Vec<RN_F32, V>::load(a.b, c, b + i * V);
     }
   }
   const int64_t step = static_cast<int64_t>(gridDim.x) * R;
@@ -171,114 +207,124 @@ __global__ void __launch_bounds__(kThreads) norm_rows(NormArgs a) {
         if (c < a.d) Vec<IN, V>::store(a.sum, row * a.ss + c, h + i * V);
       }
     }
-    float s = 0.f;
+    float s[1] = {0.f};
 #pragma unroll
-    for (int i = 0; i < NV * V; ++i) s += h[i];
-    const float mean = row_sum<W>(s, red[0]) / a.fd;
-    float s2 = 0.f;
+    for (int i = 0; i < NV * V; ++i) s[0] += h[i];
+    row_sums<W>(s, red[0]);
+    const float mean = s[0] / a.fd;
+    float s2[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         h[i * V + j] -= mean;
-        if (V * (lane + L * i) < a.d) s2 = fmaf(h[i * V + j], h[i * V + j], s2);
+        if (V * (lane + L * i) < a.d) s2[0] = fmaf(h[i * V + j], h[i * V + j], s2[0]);
       }
-    const float rstd = 1.0f / sqrtf(row_sum<W>(s2, red[1]) / a.fd + a.eps);
+    row_sums<W>(s2, red[1]);
+    const float rstd = 1.0f / sqrtf(s2[0] / a.fd + a.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = V * (lane + L * i);
       if (c < a.d) {
-        float y[V], wt[V], bt[V];
-        if constexpr (!kHold) {
+        float y[V];
 #pragma unroll
-          for (int j = 0; j < V; ++j) { wt[j] = 1.f; bt[j] = 0.f; }
-          if (a.w) Vec<RN_F32, V>::load(a.w, c, wt);
-          if (a.b) Vec<RN_F32, V>::load(a.b, c, bt);
-        }
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-          y[j] = fmaf(h[i * V + j] * rstd, kHold ? w[i * V + j] : wt[j], kHold ? b[i * V + j] : bt[j]);
+        for (int j = 0; j < V; ++j) y[j] = fmaf(h[i * V + j] * rstd, w[i * V + j], b[i * V + j]);
         Vec<OUT, V>::store(a.out, row * a.os + c, y);
       }
     }
   }
 }
 
+// With c = x - mean: the sums of c c, g and g c after the mean are all a row needs (mean(g xh)
+// is rstd mean(g c)), so a row takes two joins of the block. The next row's values are on
+// their way while a row is worked on.
 template <int IN, int OUT, int V, int W, int NV>
-__global__ void __launch_bounds__(kThreads) norm_rows_backward(NormArgs a) {
+__global__ void __launch_bounds__(threads(W)) norm_rows_backward(NormArgs a) {
   constexpr int L = 64 * W;
-  constexpr int R = kThreads / L;
-  __shared__ float red[2][2 * W];
+  constexpr int R = threads(W) / L;
+  constexpr bool kAhead = W < 16 || NV * V <= 4;   // blocks of 16 waves have 128 registers a lane
+  __shared__ float red[2][4 * W];         // rows take the areas in turn
   __shared__ float merge[W == 1 ? 64 * NV * V : 1];
   const int lane = threadIdx.x % L;
   float dw[NV * V], db[NV * V];
 #pragma unroll
   for (int i = 0; i < NV * V; ++i) { dw[i] = 0.f; db[i] = 0.f; }
-  const int64_t step = static_cast<int64_t>(gridDim.x) * R;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * R + threadIdx.x / L; row < a.rows; row += step) {
-    float x[NV * V], g[NV * V];
-    float s = 0.f;
+  Raw<IN, V> rx[NV], rr[NV];
+  Raw<OUT, V> rg[NV];
+  auto fetch = [&](int64_t row) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = V * (lane + L * i);
-#pragma unroll
-      for (int j = 0; j < V; ++j) { x[i * V + j] = 0.f; g[i * V + j] = 0.f; }
       if (c < a.d) {
-        Vec<IN, V>::load(a.x, row * a.xs + c, x + i * V);
-        Vec<OUT, V>::load(a.dout, row * a.os + c, g + i * V);
+        rx[i].load(a.x, row * a.xs + c);
+        rg[i].load(a.dout, row * a.os + c);
+        if (a.r) rr[i].load(a.r, row * a.rs + c);
       }
     }
+  };
 #pragma unroll
-    for (int i = 0; i < NV * V; ++i) s += x[i];
-    const float mean = row_sum<W>(s, red[0]) / a.fd;
-    float s2 = 0.f;
+  for (int i = 0; i < NV; ++i) { rx[i].clear(); rg[i].clear(); rr[i].clear(); }
+  const int64_t step = static_cast<int64_t>(gridDim.x) * R;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * R + threadIdx.x / L;
+  if (kAhead && row < a.rows) fetch(row);
+  for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
+    if (!kAhead) fetch(row);
+    float x[NV * V], g[NV * V], t[NV * V];
+    float s[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        x[i * V + j] -= mean;
-        if (V * (lane + L * i) < a.d) s2 = fmaf(x[i * V + j], x[i * V + j], s2);
+        x[i * V + j] = rx[i].get(j);
+        g[i * V + j] = rg[i].get(j);
+        t[i * V + j] = rr[i].get(j);
+        s[0] += x[i * V + j];
       }
-    const float rstd = 1.0f / sqrtf(row_sum<W>(s2, red[1]) / a.fd + a.eps);
-    float sg = 0.f, sgx = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = V * (lane + L * i);
-      float wt[V];
-#pragma unroll
-      for (int j = 0; j < V; ++j) wt[j] = 1.f;
-      if (a.w && c < a.d) Vec<RN_F32, V>::load(a.w, c, wt);
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int e = i * V + j;
-        x[e] *= rstd;
-        if (c < a.d) {
-          dw[e] = fmaf(g[e], x[e], dw[e]);
-          db[e] += g[e];
-          g[e] *= wt[j];
-          sg += g[e];
-          sgx = fmaf(g[e], x[e], sgx);
-        }
-      }
-    }
-    // the first area was last read before the second barrier of this row
-    row_sum2<W>(sg, sgx, red[0]);
-    sg /= a.fd;
-    sgx /= a.fd;
+    if (kAhead && row + step < a.rows) fetch(row + step);
+    row_sums<W>(s, red[turn]);
+    const float mean = s[0] / a.fd;
+    float m[3] = {0.f, 0.f, 0.f};         // sums of c c, g w, g w c
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = V * (lane + L * i);
       if (c < a.d) {
-        float t[V];
+        float wt[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) t[j] = 0.f;
-        if (a.r) Vec<IN, V>::load(a.r, row * a.rs + c, t);
+        for (int j = 0; j < V; ++j) wt[j] = 1.f;
+        if (a.w) Vec<RN_F32, V>::load(a.w, c, wt);
 #pragma unroll
-        for (int j = 0; j < V; ++j) t[j] = fmaf(rstd, g[i * V + j] - sg - x[i * V + j] * sgx, t[j]);
-        Vec<IN, V>::store(a.sum, row * a.ss + c, t);
+        for (int j = 0; j < V; ++j) {
+          const int e = i * V + j;
+          x[e] -= mean;
+          db[e] += g[e];
+          const float gw = g[e] * wt[j];
+          m[0] = fmaf(x[e], x[e], m[0]);
+          m[1] += gw;
+          m[2] = fmaf(gw, x[e], m[2]);
+        }
       }
     }
-    if constexpr (W > 1) __syncthreads();   // the areas are free for the next row
+    row_sums<W>(m, red[turn] + W);
+    const float rstd = 1.0f / sqrtf(m[0] / a.fd + a.eps);
+    const float sg = m[1] / a.fd, sgx = m[2] / a.fd * rstd;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = V * (lane + L * i);
+      if (c < a.d) {
+        float wt[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) wt[j] = 1.f;
+        if (a.w) Vec<RN_F32, V>::load(a.w, c, wt);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const int e = i * V + j;
+          const float xh = x[e] * rstd;
+          dw[e] = fmaf(g[e], xh, dw[e]);
+          t[e] = fmaf(rstd, g[e] * wt[j] - sg - xh * sgx, t[e]);
+        }
+        Vec<IN, V>::store(a.sum, row * a.ss + c, t + i * V);
+      }
+    }
   }
   if (!a.part) return;
   float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.d;
@@ -321,46 +367,49 @@ __global__ void __launch_bounds__(kThreads) norm_rows_backward(NormArgs a) {
   }
 }
 
-// dweight and dbias: the partial rows added in the order of their blocks, 16 interleaved
-// sums a column which are then added in turn. One block takes 64 columns of the 2 d.
+// dweight and dbias: the partial rows added in the order of their blocks, 32 interleaved sums
+// a column which are then added in turn. One block takes 32 columns of the 2 d.
 __global__ void __launch_bounds__(1024) norm_reduce(const float* part, int blocks, int d, float* dw, float* db) {
-  __shared__ float red[16][64];
-  const int col = blockIdx.x * 64 + (threadIdx.x & 63);
-  const int grp = threadIdx.x >> 6;
+  __shared__ float red[32][33];
+  const int col = blockIdx.x * 32 + (threadIdx.x & 31);
+  const int grp = threadIdx.x >> 5;
   float s = 0.f;
-  if (col < 2 * d)
-    for (int i = grp; i < blocks; i += 16) s += part[static_cast<int64_t>(i) * 2 * d + col];
-  red[grp][threadIdx.x & 63] = s;
+  if (col < 2 * d) {
+#pragma unroll 8
+    for (int i = grp; i < blocks; i += 32) s += part[static_cast<int64_t>(i) * 2 * d + col];
+  }
+  red[grp][threadIdx.x & 31] = s;
   __syncthreads();
   if (grp == 0 && col < 2 * d) {
     s = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s += red[i][threadIdx.x];
+    for (int i = 0; i < 32; ++i) s += red[i][threadIdx.x];
     float* out = col < d ? dw : db;
     if (out) out[col < d ? col : col - d] = s;
   }
 }
 
 int backward_blocks(const NormCall& n) {
-  // four blocks a CU at most, and at least four rows a block, so that the partial rows
-  // (2 d floats a block, written and read once) stay small beside the tensors
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((n.rows + 3) / 4, 512)));
+  // Three blocks a CU, which is what their registers allow, and at least four rows a block, so
+  // that the partial rows (2 d floats a block, written and read once) stay small beside the
+  // tensors.
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((n.rows + 3) / 4, 768)));
 }
 
 template <int IN, int OUT, int V, int W, int NV>
 hipError_t launch_one(const NormCall& n, NormArgs a, hipStream_t st) {
   if (!n.backward) {
-    constexpr int R = kThreads / (64 * W);
+    constexpr int R = threads(W) / (64 * W);
     const int64_t need = (n.rows + R - 1) / R;
     hipLaunchKernelGGL((norm_rows<IN, OUT, V, W, NV>), dim3(static_cast<unsigned>(std::min<int64_t>(need, 2048))),
-                       dim3(kThreads), 0, st, a);
+                       dim3(threads(W)), 0, st, a);
     return hipGetLastError();
   }
   const int blocks = backward_blocks(n);
-  hipLaunchKernelGGL((norm_rows_backward<IN, OUT, V, W, NV>), dim3(blocks), dim3(kThreads), 0, st, a);
+  hipLaunchKernelGGL((norm_rows_backward<IN, OUT, V, W, NV>), dim3(blocks), dim3(threads(W)), 0, st, a);
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && a.part) {
-    hipLaunchKernelGGL(norm_reduce, dim3((2 * n.d + 63) / 64), dim3(1024), 0, st, a.part, blocks, n.d, n.dw, n.db);
+    hipLaunchKernelGGL(norm_reduce, dim3((2 * n.d + 31) / 32), dim3(1024), 0, st, a.part, blocks, n.d, n.dw, n.db);
     e = hipGetLastError();
   }
   return e;
@@ -368,6 +417,8 @@ hipError_t launch_one(const NormCall& n, NormArgs a, hipStream_t st) {
 
 template <int IN, int OUT>
 hipError_t launch_t(const NormCall& n, const NormArgs& a, hipStream_t st) {
+  // Waves a row and vectors a lane: at most 16 values of each tensor a lane, so that two rows
+  // (one worked on, one on its way) and the sums over rows fit in its registers.
   constexpr int V = IN == RN_BF16 ? 8 : 4;   // 16 bytes of the input type
   if (n.vec) {
     const int nv = (n.d / V + 63) / 64;      // vectors a lane of one wave
@@ -375,17 +426,22 @@ hipError_t launch_t(const NormCall& n, const NormArgs& a, hipStream_t st) {
     if (nv <= 2) return launch_one<IN, OUT, V, 1, 2>(n, a, st);
     if (nv <= 4) return launch_one<IN, OUT, V, 4, 1>(n, a, st);
     if (nv <= 8) return launch_one<IN, OUT, V, 4, 2>(n, a, st);
-    if (nv <= 16) return launch_one<IN, OUT, V, 4, 4>(n, a, st);
-    if (nv <= 32) return launch_one<IN, OUT, V, 4, 8>(n, a, st);
-    if constexpr (V == 4) return launch_one<IN, OUT, V, 4, 16>(n, a, st);
-    return hipErrorInvalidValue;
+    if constexpr (V == 8) {
+      if (nv <= 16) return launch_one<IN, OUT, V, 16, 1>(n, a, st);
+      return launch_one<IN, OUT, V, 16, 2>(n, a, st);
+    } else {
+      if (nv <= 16) return launch_one<IN, OUT, V, 4, 4>(n, a, st);
+      if (nv <= 32) return launch_one<IN, OUT, V, 16, 2>(n, a, st);
+      return launch_one<IN, OUT, V, 16, 4>(n, a, st);
+    }
   }
   const int nv = (n.d + 63) / 64;
   if (nv <= 4) return launch_one<IN, OUT, 1, 1, 4>(n, a, st);
   if (nv <= 16) return launch_one<IN, OUT, 1, 4, 4>(n, a, st);
   if (nv <= 32) return launch_one<IN, OUT, 1, 4, 8>(n, a, st);
-  if (nv <= 64) return launch_one<IN, OUT, 1, 4, 16>(n, a, st);
-  return launch_one<IN, OUT, 1, 4, 64>(n, a, st);
+  if (nv <= 64) return launch_one<IN, OUT, 1, 16, 4>(n, a, st);
+  if (nv <= 128) return launch_one<IN, OUT, 1, 16, 8>(n, a, st);
+  return launch_one<IN, OUT, 1, 16, 16>(n, a, st);
 }
 
 }  // namespace
