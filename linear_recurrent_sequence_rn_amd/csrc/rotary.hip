@@ -34,35 +34,41 @@ struct RotArgs {
   double theta[kMaxRot / 2];
 };
 
-// Reads and writes V elements (16 bytes for V > 1).
+// V elements as they are in memory: 16 bytes for V > 1.
 template <int DT, int V>
-__device__ __forceinline__ void load_v(const void* p, int64_t i, float* f) {
-  if constexpr (V == 1) {
-    f[0] = Elem<DT>::load(p, i);
-  } else if constexpr (DT == RN_F32) {
-    const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-    f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
-  } else {
-    const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+struct Piece {
+  uint4 r;
+  __device__ __forceinline__ void load(const char* p) {
+    if constexpr (V > 1) r = *reinterpret_cast<const uint4*>(p);
+    else if constexpr (DT == RN_F32) r.x = *reinterpret_cast<const uint32_t*>(p);
+    else r.x = *reinterpret_cast<const uint16_t*>(p);
+  }
+  __device__ __forceinline__ void store(char* p) const {
+    if constexpr (V > 1) *reinterpret_cast<uint4*>(p) = r;
+    else if constexpr (DT == RN_F32) *reinterpret_cast<uint32_t*>(p) = r.x;
+    else *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(r.x);
+  }
+  __device__ __forceinline__ void get(float* f) const {
+    const uint32_t u[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      f[2 * j] = __uint_as_float(u[j] << 16);
-      f[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+    for (int j = 0; j < V; ++j) {
+      if constexpr (DT == RN_F32) f[j] = __uint_as_float(u[j]);
+      else f[j] = j % 2 ? __uint_as_float(u[j / 2] & 0xffff0000u) : __uint_as_float(u[j / 2] << 16);
     }
   }
-}
-template <int DT, int V>
-__device__ __forceinline__ void store_v(void* p, int64_t i, const float* f) {
-  if constexpr (V == 1) {
-    Elem<DT>::store(p, i, f[0]);
-  } else if constexpr (DT == RN_F32) {
-    *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(f[0], f[1], f[2], f[3]);
-  } else {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) =
-        make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+  __device__ __forceinline__ void set(const float* f) {
+    if constexpr (DT == RN_F32) {
+      uint32_t u[4] = {};
+#pragma unroll
+      for (int j = 0; j < V; ++j) u[j] = __float_as_uint(f[j]);
+      r = make_uint4(u[0], u[1], u[2], u[3]);
+    } else if constexpr (V == 1) {
+      r.x = f32_to_bf16(f[0]);
+    } else {
+      r = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+    }
   }
-}
+};
 
 // cos and sin of p theta, both in float64 up to the reduction to [-pi, pi] (as angle_cs,
 // with theta in float64: a float32 theta would already be 0.06 rad off at p = 1e6).
@@ -79,85 +85,108 @@ __device__ __forceinline__ float2 angle(int64_t p, double theta) {
   return cs;
 }
 
-// LANES consecutive threads take one head of one token; V elements an access (pairs of
-// scalar accesses where V is 1).
+// `lanes` consecutive threads take one head of one token. A unit of work is two pieces of V
+// elements: with HALF one of each half; else neighbours, or, where V is 1, the elements of a
+// pair. Units from `turn` on are copied. The pieces of U heads are in flight.
 template <int DT, int V, bool HALF>
 __global__ void __launch_bounds__(kThreads) rotary(RotArgs a, int lanes) {
+  constexpr int U = 4;
+  constexpr int E = DT == RN_F32 ? 4 : 2;      // bytes an element
   __shared__ float2 cs[kTable];
+  __shared__ int64_t base[kMaxTile][4];   // token offsets: q, k, q_out, k_out
   const int half = a.rot / 2;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.tile;
   const int tile = static_cast<int>(min(static_cast<int64_t>(a.tile), a.rows - row0));
   for (int i = threadIdx.x; i < tile * half; i += kThreads) {
     const int t = i / half, j = i - t * half;
-    const int64_t row = row0 + t;
-    const int64_t b = row / a.N, n = row - b * a.N;
+    const uint32_t row = static_cast<uint32_t>(row0) + t;      // (B * N is below 2^31)
+    const uint32_t b = row / static_cast<uint32_t>(a.N), n = row - b * a.N;
     const int64_t p = !a.pos ? a.pos0 + n : a.pos_token ? a.pos[row] : a.pos[b] + n;
     float2 v = angle(p, a.theta[j]);
     v.x *= a.magnitude;
     v.y *= a.inverse ? -a.magnitude : a.magnitude;
     cs[i] = v;
   }
+  for (int i = threadIdx.x; i < tile * 4; i += kThreads) {
+    const uint32_t row = static_cast<uint32_t>(row0) + i / 4;
+    const uint32_t b = row / static_cast<uint32_t>(a.N), n = row - b * a.N;
+    base[i / 4][i % 4] = b * a.s[i % 4][0] + n * a.s[i % 4][2];
+  }
   __syncthreads();
   const int lane = threadIdx.x & (lanes - 1);
   const int per = kThreads / lanes;
   const int h0 = blockIdx.y * a.heads;
   const int nh = min(a.heads, a.H - h0);
-  // units of work of one (token, head): pairs of vectors (or vectors of pairs), then copies
-  const int turn = HALF ? half / V : (V == 1 ? half : a.rot / V);
-  for (int i = threadIdx.x / lanes; i < tile * nh; i += per) {
-    const int t = i / nh, h = h0 + i - t * nh;
-    const int64_t row = row0 + t;
-    const int64_t b = row / a.N, n = row - b * a.N;
-    const int isk = h >= a.Hq;
-    const int hh = isk ? h - a.Hq : h;
-    const int64_t* si = a.s[isk];
-    const int64_t* so = a.s[2 + isk];
-    const int64_t x = b * si[0] + hh * si[1] + n * si[2];
-    const int64_t y = b * so[0] + hh * so[1] + n * so[2];
-    const void* in = a.in[isk];
-    void* out = a.out[isk];
-    const bool copy = in != out;
-    const float2* c = cs + t * half;
-    for (int u = lane; u < turn; u += lanes) {
-      if constexpr (HALF) {
-        float p[V], q[V], f[V], g[V];
-        load_v<DT, V>(in, x + u * V, p);
-        load_v<DT, V>(in, x + half + u * V, q);
+  const int turn = half / V + (!HALF && half % V ? 1 : 0);     // units of turned elements
+  const int units = turn + (a.d - a.rot + 2 * V - 1) / (2 * V);
+  // byte offsets of a unit's pieces in its head, and how many it has
+  auto pieces = [&](int u, int* x, int* y) {
+    if (u < turn) {
+      *x = (HALF ? u * V : 2 * u * V) * E;
+      *y = *x + (HALF ? half : V) * E;
+      return HALF || 2 * u * V + V < a.rot ? 2 : 1;
+    }
+    *x = (a.rot + 2 * (u - turn) * V) * E;
+    *y = *x + V * E;
+    return a.rot + 2 * (u - turn) * V + V < a.d ? 2 : 1;
+  };
+  const int qt = per / nh, qh = per - qt * nh;   // a step of `per` heads in (token, head)
+  for (int u = lane; u < units; u += lanes) {
+    int ox, oy;
+    const int np = pieces(u, &ox, &oy);
+    const bool turned = u < turn;
+    int i = threadIdx.x / lanes;
+    int t = i / nh, h = i - t * nh;
+    while (t < tile) {
+      Piece<DT, V> x[U], y[U];
+      char* out[U];
+      int tt[U];
+      int n = 0;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float2 v = c[u * V + j];
-          f[j] = p[j] * v.x - q[j] * v.y;
-          g[j] = p[j] * v.y + q[j] * v.x;
+      for (int k = 0; k < U; ++k) {
+        if (t < tile) {
+          const int hd = h0 + h;
+          const int isk = hd >= a.Hq;
+          const int hh = isk ? hd - a.Hq : hd;
+          const char* in = static_cast<const char*>(a.in[isk]) + (base[t][isk] + hh * a.s[isk][1]) * E;
+          out[k] = static_cast<char*>(a.out[isk]) + (base[t][2 + isk] + hh * a.s[2 + isk][1]) * E;
+          if (!turned && a.in[isk] == a.out[isk]) out[k] = nullptr;   // in place: nothing to copy
+          tt[k] = t;
+          n = k + 1;
+          if (out[k]) x[k].load(in + ox);
+          if (out[k] && np == 2) y[k].load(in + oy);
+          h += qh;
+          t += qt;
+          if (h >= nh) { h -= nh; ++t; }
         }
-        store_v<DT, V>(out, y + u * V, f);
-        store_v<DT, V>(out, y + half + u * V, g);
-      } else if constexpr (V == 1) {
-        float p[2], f[2];
-        load_v<DT, 1>(in, x + 2 * u, p);
-        load_v<DT, 1>(in, x + 2 * u + 1, p + 1);
-        const float2 v = c[u];
-        f[0] = p[0] * v.x - p[1] * v.y;
-        f[1] = p[0] * v.y + p[1] * v.x;
-        store_v<DT, 1>(out, y + 2 * u, f);
-        store_v<DT, 1>(out, y + 2 * u + 1, f + 1);
-      } else {
-        float p[V], f[V];
-        load_v<DT, V>(in, x + u * V, p);
+      }
 #pragma unroll
-        for (int j = 0; j < V / 2; ++j) {
-          const float2 v = c[u * (V / 2) + j];
-          f[2 * j] = p[2 * j] * v.x - p[2 * j + 1] * v.y;
-          f[2 * j + 1] = p[2 * j] * v.y + p[2 * j + 1] * v.x;
+      for (int k = 0; k < U; ++k) {
+        if (k < n) {
+          if (turned) {
+            float p[2 * V];
+            x[k].get(p);
+            if (np == 2) y[k].get(p + V);
+            const float2* c = cs + tt[k] * half + u * V;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+              // (the pairs of a last single piece end with it)
+              if (HALF || j < V / 2 || V == 1 || np == 2) {
+                const int e = HALF ? j : 2 * j, f = HALF ? j + V : 2 * j + 1;
+                const float2 v = c[j];
+                const float re = p[e], im = p[f];
+                p[e] = re * v.x - im * v.y;
+                p[f] = re * v.y + im * v.x;
+              }
+            }
+            x[k].set(p);
+            if (np == 2) y[k].set(p + V);
+          }
+          if (out[k]) x[k].store(out[k] + ox);
+          if (out[k] && np == 2) y[k].store(out[k] + oy);
         }
-        store_v<DT, V>(out, y + u * V, f);
       }
     }
-    if (copy)
-      for (int e = a.rot + lane * V; e < a.d; e += lanes * V) {
-        float p[V];
-        load_v<DT, V>(in, x + e, p);
-        store_v<DT, V>(out, y + e, p);
-      }
   }
 }
 
@@ -173,7 +202,7 @@ hipError_t launch_t(const RotaryCall& c, RotArgs& a, hipStream_t st) {
     for (int j = 0; j < 3; ++j) vec = vec && a.s[i][j] % V == 0 && a.s[2 + i][j] % V == 0;
   }
   const int w = vec ? V : 1;
-  const int units = std::max(c.half ? half / w : std::max(1, a.rot / std::max(w, 2)), (a.d - a.rot + w - 1) / w);
+  const int units = (half + w - 1) / w + (a.d - a.rot + 2 * w - 1) / (2 * w);
   int lanes = 1;
   while (lanes < units && lanes < 64) lanes *= 2;
   // tokens a block: the angles' cost is shared by all heads whatever the tile, so the tile
