@@ -193,16 +193,19 @@ __global__ void __launch_bounds__(256) lin_recurrent(LinArgs a, int slices) {
       const int i = tid + 256 * e;
       vt[i / kCols][i % kCols] = rv[e];
     }
-    if (tid < kTok) gt[tid] = rg;
+    if (tid < kTok) {
+      gt[tid] = expf(rg);
+      gsum += rg;
+    }
     __syncthreads();
     const int n = min(kTok, t1 - t);
     fetch(t + kTok);
-    for (int i = 0; i < n; ++i) {
-      const float gi = gt[i];
-      if (MODE == kLinState) gsum += gi;
-      const float dec = expf(gi);
+    // tokens behind the last have decay 1 and k = q = v = 0, and change nothing
+#pragma unroll 4
+    for (int i = 0; i < kTok; ++i) {
+      const float dec = gt[i];
       const float vv = vt[i][lane];
-      float acc = 0.f;
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int r = 0; r < RW; r += 4) {
         const float4 k4 = *reinterpret_cast<const float4*>(&kt[i][wave * RW + r]);
@@ -212,13 +215,13 @@ __global__ void __launch_bounds__(256) lin_recurrent(LinArgs a, int slices) {
         S[r + 3] = fmaf(dec, S[r + 3], k4.w * vv);
         if constexpr (MODE != kLinState) {
           const float4 q4 = *reinterpret_cast<const float4*>(&qt[i][wave * RW + r]);
-          acc = fmaf(q4.x, S[r], acc);
-          acc = fmaf(q4.y, S[r + 1], acc);
-          acc = fmaf(q4.z, S[r + 2], acc);
-          acc = fmaf(q4.w, S[r + 3], acc);
+          acc[0] = fmaf(q4.x, S[r], acc[0]);
+          acc[1] = fmaf(q4.y, S[r + 1], acc[1]);
+          acc[2] = fmaf(q4.z, S[r + 2], acc[2]);
+          acc[3] = fmaf(q4.w, S[r + 3], acc[3]);
         }
       }
-      if constexpr (MODE != kLinState) part[wave][i][lane] = acc;
+      if constexpr (MODE != kLinState) part[wave][i][lane] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
     }
     __syncthreads();
     if constexpr (MODE != kLinState) {
@@ -236,6 +239,9 @@ __global__ void __launch_bounds__(256) lin_recurrent(LinArgs a, int slices) {
   if (MODE == kLinState) {
     const int64_t i = lin_segment(a, s, row0, seg) * a.H + h;
     to = a.seg_state + i * sh;
+    // (thread t holds the sum of tokens t, t + 16, ... of the segment)
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1) gsum += __shfl_xor(gsum, o, 16);
     if (c0 == 0 && tid == 0) a.seg_decay[i] = expf(static_cast<float>(gsum));
   }
   if (to && lane < nc) {
@@ -248,12 +254,14 @@ __global__ void __launch_bounds__(256) lin_recurrent(LinArgs a, int slices) {
 }
 
 // ---- states over the segments ---------------------------------------------------------------
-// One thread a state element: the segments' own states become the states they start from,
-// and the last one the final state.
+// V neighbouring state elements a thread: the segments' own states become the states they start
+// from, and the last one the final state.
+template <int V>
 __global__ void __launch_bounds__(256) lin_scan(LinArgs a) {
+  typedef float fv __attribute__((ext_vector_type(V)));
   const int h = blockIdx.y, s = blockIdx.z;
   const int64_t sh = static_cast<int64_t>(a.dk) * a.dv;
-  const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t e = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * V;
   if (e >= sh) return;
   int64_t row0, own;
   int len;
@@ -261,7 +269,8 @@ __global__ void __launch_bounds__(256) lin_scan(LinArgs a) {
   const int slot = lin_slot(a, s);
   const int n = (len + a.seg_len - 1) / a.seg_len;
   const int64_t at = (static_cast<int64_t>(slot) * a.H + h) * sh + e;
-  float x = a.state_in && slot >= 0 ? a.state_in[at] : 0.f;
+  fv x = {};
+  if (a.state_in && slot >= 0) x = *reinterpret_cast<const fv*>(a.state_in + at);
   const int64_t first = lin_segment(a, s, row0, 0) * a.H + h;
   const bool last = a.state_out && slot >= 0;
   float* p = a.seg_state + first * sh + e;
@@ -269,17 +278,22 @@ __global__ void __launch_bounds__(256) lin_scan(LinArgs a) {
   const int64_t ps = sh * a.H;
   // eight segments' states in flight
   for (int g = 0; g < n; g += 8) {
-    float u[8];
+    fv u[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) u[i] = g + i < n && (last || g + i + 1 < n) ? p[(g + i) * ps] : 0.f;
+    for (int i = 0; i < 8; ++i)
+      if (g + i < n && (last || g + i + 1 < n)) u[i] = *reinterpret_cast<const fv*>(p + (g + i) * ps);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (g + i < n) {
-        p[(g + i) * ps] = x;
-        if (last || g + i + 1 < n) x = fmaf(d[static_cast<int64_t>(g + i) * a.H], x, u[i]);
+        *reinterpret_cast<fv*>(p + (g + i) * ps) = x;
+        if (last || g + i + 1 < n) {
+          const float dec = d[static_cast<int64_t>(g + i) * a.H];
+#pragma unroll
+          for (int v = 0; v < V; ++v) x[v] = fmaf(dec, x[v], u[i][v]);
+        }
       }
   }
-  if (last) a.state_out[at] = x;
+  if (last) *reinterpret_cast<fv*>(a.state_out + at) = x;
 }
 
 template <int IN, int OUT, LinMode MODE>
@@ -350,15 +364,18 @@ bool mfma_call(const LinCall& c) {
   return ok;
 }
 
-// Tokens a segment, and how many segments the longest sequence has: one segment where the
-// sequences and heads fill the chip by themselves, else enough segments for `want` blocks.
+// Tokens a segment, and how many segments the longest sequence has: one where the sequences and
+// heads fill the chip by themselves; else enough that the blocks of all segments do. Cutting
+// costs a second pass over the tokens for the states and the scan over them, so a longest
+// sequence of less than three segments stays whole.
 void segments(const LinCall& c, int* len, int* n) {
-  const int64_t per = mfma_shape(c) ? lin_mfma_blocks(lin_args(c)) : static_cast<int64_t>(c.H) * ((c.dv + kCols - 1) / kCols);
+  const bool mfma = mfma_shape(c);
+  const int64_t per = mfma ? lin_mfma_blocks(lin_args(c)) : static_cast<int64_t>(c.H) * ((c.dv + kCols - 1) / kCols);
   const int64_t tokens = c.T > 0 ? std::min<int64_t>(c.T, static_cast<int64_t>(c.S) * c.N) : static_cast<int64_t>(c.S) * c.N;
-  const int64_t want = 256;
-  int64_t L = tokens * per / want;
-  L = std::max<int64_t>((L + 63) / 64 * 64, 256);
-  if (2 * L > c.N) L = c.N;
+  // blocks the 256 CUs hold at once, by their LDS and registers
+  const int64_t want = 256 * (!mfma || c.dk <= 64 ? 3 : c.dk <= 128 ? 2 : 1);
+  int64_t L = std::max<int64_t>((tokens * per / want + 63) / 64 * 64, mfma ? 256 : 64);
+  if (3 * L > c.N) L = c.N;
   L = std::max<int64_t>(L, (c.N + 65534) / 65535);
   L = (L + 63) / 64 * 64;
   *len = static_cast<int>(L);
@@ -396,7 +413,10 @@ hipError_t launch_linear_chunked(const LinCall& c, hipStream_t st) {
   a.seg_state = a.seg_decay + ((rows + 63) & ~size_t(63));
   hipError_t e = mfma ? launch_lin_mfma(a, kLinState, st) : launch_recurrent<kLinState>(a, c.in_dt, c.out_dt, st);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(lin_scan, dim3((c.dk * c.dv + 255) / 256, c.H, c.S), dim3(256), 0, st, a);
+  if (c.dk * c.dv % 4 == 0)   // (states are 16-byte aligned, here and in the caller's buffers)
+    hipLaunchKernelGGL(lin_scan<4>, dim3((c.dk * c.dv + 1023) / 1024, c.H, c.S), dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL(lin_scan<1>, dim3((c.dk * c.dv + 255) / 256, c.H, c.S), dim3(256), 0, st, a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   return mfma ? launch_lin_mfma(a, kLinOut, st) : launch_recurrent<kLinOut>(a, c.in_dt, c.out_dt, st);
 }
