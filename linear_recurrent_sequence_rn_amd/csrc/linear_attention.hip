@@ -105,10 +105,28 @@ __global__ void __launch_bounds__(kStepThreads) lin_step(LinArgs a, int slices) 
 #pragma unroll
   for (int i = 0; i < VEC; ++i) part[grp * W + cq * VEC + i] = acc[i];
   __syncthreads();
-  for (int c = tid; c < nc; c += kStepThreads) {
+  if constexpr (G > 8) {                   // many groups: all threads add a few, then the columns' own
+    constexpr int T = kStepThreads / W, P = G / T;
+    const int c = tid % W, i0 = tid / W * P;
     float o = 0.f;
-    for (int i = 0; i < G; ++i) o += part[i * W + c];
-    Elem<OUT>::store(a.out, oo + c, a.scale * o);
+#pragma unroll
+    for (int i = 0; i < P; ++i) o += part[(i0 + i) * W + c];
+    __syncthreads();
+    part[tid / W * W + c] = o;
+    __syncthreads();
+    if (tid < nc) {
+      o = 0.f;
+#pragma unroll
+      for (int i = 0; i < T; ++i) o += part[i * W + tid];
+      Elem<OUT>::store(a.out, oo + tid, a.scale * o);
+    }
+  } else {
+    for (int c = tid; c < nc; c += kStepThreads) {
+      float o = 0.f;
+#pragma unroll
+      for (int i = 0; i < G; ++i) o += part[i * W + c];
+      Elem<OUT>::store(a.out, oo + c, a.scale * o);
+    }
   }
 }
 
@@ -327,9 +345,9 @@ hipError_t launch_step_t(const LinArgs& a, hipStream_t st) {
     return hipGetLastError();                                                                       \
   } while (0)
   if (a.dv % 4 == 0) {
-    if (a.dv >= 256 && states * ((a.dv + 255) / 256) >= 512) RN_STEP(4, 64);
-    if (a.dv >= 128 && states * ((a.dv + 127) / 128) >= 512) RN_STEP(4, 32);
-    if (a.dv >= 64 && states * ((a.dv + 63) / 64) >= 512) RN_STEP(4, 16);
+    if (a.dv > 128 && states * ((a.dv + 255) / 256) >= 512) RN_STEP(4, 64);
+    if (a.dv > 64 && states * ((a.dv + 127) / 128) >= 512) RN_STEP(4, 32);
+    if (a.dv > 16 && states * ((a.dv + 63) / 64) >= 512) RN_STEP(4, 16);
     RN_STEP(4, 4);
   }
   RN_STEP(1, 64);

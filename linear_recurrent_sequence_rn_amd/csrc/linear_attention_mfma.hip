@@ -266,18 +266,19 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
   Tile<DK, NT> tq, tk;
   Tile<DV, NT> tv;
   const uint32_t qoff = tq.lane_offset(a.qs[2], a.dk), koff = tk.lane_offset(a.ks[2], a.dk), voff = tv.lane_offset(a.vs[2], nc);
-  auto fetch = [&](int t) {
-    const int n = len - t;
-    if constexpr (kOut) tq.load(qp + t * a.qs[2], a.qs[2], qoff, n, a.dk);
-    tk.load(kp + t * a.ks[2], a.ks[2], koff, n, a.dk);
-    tv.load(vp + t * a.vs[2], a.vs[2], voff, n, nc);
+  auto fetch_q = [&](int t) {
+    if constexpr (kOut) tq.load(qp + t * a.qs[2], a.qs[2], qoff, len - t, a.dk);
   };
+  auto fetch_k = [&](int t) { tk.load(kp + t * a.ks[2], a.ks[2], koff, len - t, a.dk); };
+  auto fetch_v = [&](int t) { tv.load(vp + t * a.vs[2], a.vs[2], voff, len - t, nc); };
   auto log_decay = [&](int t) { return t + lane < t1 ? gp[(t + lane) * a.gs[2]] : 0.f; };
 
   double gsum = 0.0;
   float gnext = 0.f;
   if (t0 < t1) {
-    fetch(t0);
+    fetch_v(t0);
+    fetch_k(t0);
+    fetch_q(t0);
     if (wave == NT / 64 - 1) {              // (the last wave has the fewest score tiles)
       gsum += scan_decays(log_decay(t0), &dec[0]);
       gnext = log_decay(t0 + kChunk);
@@ -338,8 +339,11 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
       if (t > t0) store_out(t - kChunk);
     __syncthreads();
     const Decays& D = dec[buf];
-    if (t + kChunk < t1) {
-      fetch(t + kChunk);
+    // (the next tiles' loads are issued in three parts: all at once they would fill the memory
+    // pipe and hold the waves up)
+    const bool more = t + kChunk < t1;
+    if (more) {
+      fetch_v(t + kChunk);
       if (wave == NT / 64 - 1) {
         gsum += scan_decays(gnext, &dec[buf ^ 1]);
         gnext = log_decay(t + 2 * kChunk);
@@ -376,6 +380,7 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
           *reinterpret_cast<uint2*>(pt + pj + j * 32 * kChunk) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
         }
       }
+      if (more) fetch_k(t + kChunk);
       // what the state in front of the chunk gives: O^T = S^T Q^T, scaled by 2^c of the query
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -405,6 +410,10 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
             swap[((wave * 2 + x) * VT + v) * 64 + lane] = wd == 0 ? O[1 + x][v] : O[3 * x][v];
       }
     }
+    if (more) {
+      if constexpr (kOut) fetch_q(t + kChunk);
+      else fetch_k(t + kChunk);
+    }
     const bool bad = D.bad;
     bf16x8 vf[2][VT];
     if constexpr (kHasV)
@@ -412,7 +421,7 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
       for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
         for (int v = 0; v < VT; ++v) vf[ks][v] = col_operand<DV>(vt, cv, ks, v);
-    if (MODE != kLinOut || t + kChunk < t1) {
+    if (MODE != kLinOut || more) {
       // S <- a S + K^T (w V): the parts of w V in the same order of tokens as K^T
       const float dec64 = D.a;
 #pragma unroll
