@@ -173,7 +173,7 @@ def rn_layernorm(x, weight=None, bias=None, eps=1e-5, *, residual=None, sum_out=
     shape = x.shape
     d = shape[-1] if shape else 0
     n = x.numel()
-    if n == 0:
+    if n == 0 or d == 0:
         raise ValueError(f"x must be [..., d] with at least one row; got {tuple(shape)}")
     _like(residual, x, "residual")
     _whole(weight, torch.float32, (d,), "weight")
@@ -211,7 +211,7 @@ def rn_layernorm_backward(dout, x, weight=None, eps=1e-5, *, dsum=None, dx=None,
     Returns a dict with dx (the gradient of x and of the residual; in x's type) and, unless not
     wanted, dweight and dbias (float32 [d])."""
     dev = _device(x, dout, weight, dsum, dx, workspace)
-    if x.numel() == 0:
+    if x.numel() == 0 or x.dim() == 0:
         raise ValueError(f"x must be [..., d] with at least one row; got {tuple(x.shape)}")
     d = x.shape[-1]
     if dout.shape != x.shape:
@@ -408,14 +408,19 @@ def _linear_call(q, k, v, g, qk_scale, lengths, cu, max_len, state_in, state_out
     return desc, S, out, state_out
 
 
-def rn_linear_attention_workspace_bytes(q, k, v, log_decay, *, cu_seqlens=None, max_len=None, out_dtype=None,
-                                        force_generic=False) -> int:
-    """Bytes of workspace ``rn_linear_attention_chunked`` needs for these tensors."""
+def rn_linear_attention_workspace_bytes(q, k, v, log_decay, *, cu_seqlens=None, max_len=None, out=None,
+                                        out_dtype=None, force_generic=False) -> int:
+    """Bytes of workspace ``rn_linear_attention_chunked`` needs for these tensors (and the ``out``
+    it is given, where it is)."""
     _linear_shapes(q, k, v, log_decay)
     B, rows = q.shape[0], q.shape[2]
     S, T = (B, 0) if cu_seqlens is None else (cu_seqlens.numel() - 1, rows)
-    o = (log_decay.shape[1] * rows * v.shape[-1], rows * v.shape[-1], v.shape[-1])
-    desc = _linear_desc(q, k, v, log_decay, S, max_len or rows, T, 0, out_dtype or q.dtype,
+    if out is None:
+        o = (log_decay.shape[1] * rows * v.shape[-1], rows * v.shape[-1], v.shape[-1])
+        dtype = out_dtype or q.dtype
+    else:
+        o, dtype = _bhn(out, "out"), out.dtype
+    desc = _linear_desc(q, k, v, log_decay, S, max_len or rows, T, 0, dtype,
                         RN_LINEAR_GENERIC if force_generic else 0, 1.0, o)
     return int(lib.rn_linear_attention_workspace_bytes(desc))
 

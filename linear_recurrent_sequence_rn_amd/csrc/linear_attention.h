@@ -51,6 +51,16 @@ __device__ __forceinline__ void lin_span(const LinArgs& a, int s, int64_t* row0,
 __device__ __forceinline__ int64_t lin_base(const LinArgs& a, const int64_t* st, int s, int64_t row0) {
   return a.T > 0 ? row0 * st[2] : s * st[0];
 }
+// Head and column slice of a block. Blocks are dealt to the 8 XCDs, each with an L2 of its own,
+// by their number modulo 8: the slices of a head, and heads that share q and k, come at
+// distances of the number of such groups, so that (with 8 groups or a multiple) they meet in
+// one L2 and q and k reach it once.
+__device__ __forceinline__ void lin_block(const LinArgs& a, int x, int* h, int* slice) {
+  const int groups = min(a.Hq, a.Hk), each = a.H / groups;
+  const int g = x % groups, rest = x / groups;
+  *slice = rest / each;
+  *h = g * each + (rest - *slice * each);
+}
 // Index of the state of sequence s in the caller's buffers, or -1.
 __device__ __forceinline__ int lin_slot(const LinArgs& a, int s) {
   if (!a.slots) return s;

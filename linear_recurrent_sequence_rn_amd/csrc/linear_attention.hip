@@ -139,7 +139,7 @@ constexpr int kTok = 16;
 constexpr int kCols = 64;
 
 template <int IN, int OUT, int RW, LinMode MODE>
-__global__ void __launch_bounds__(256) lin_recurrent(LinArgs a, int slices) {
+__global__ void __launch_bounds__(256) lin_recurrent(LinArgs a) {
   constexpr int D = 4 * RW;
   constexpr int E = kTok * D / 256;       // q (or k) elements a thread stages
   __shared__ float qt[kTok][D];
@@ -147,7 +147,9 @@ __global__ void __launch_bounds__(256) lin_recurrent(LinArgs a, int slices) {
   __shared__ float vt[kTok][kCols];
   __shared__ float gt[kTok];
   __shared__ float part[4][kTok][kCols];
-  const int h = blockIdx.x / slices, c0 = (blockIdx.x - h * slices) * kCols;
+  int h, c0;
+  lin_block(a, blockIdx.x, &h, &c0);
+  c0 *= kCols;
   const int seg = blockIdx.y, s = blockIdx.z;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int nc = min(kCols, a.dv - c0);
@@ -320,9 +322,9 @@ hipError_t launch_recurrent_t(const LinArgs& a, hipStream_t st) {
   const bool rest = a.T > 0 && a.zero_rest && MODE != kLinState;
   const dim3 grid(a.H * slices, a.n_seg, a.S + (rest ? 1 : 0));
   const int rw = (a.dk + 3) / 4;
-  if (rw <= 16) hipLaunchKernelGGL((lin_recurrent<IN, OUT, 16, MODE>), grid, dim3(256), 0, st, a, slices);
-  else if (rw <= 32) hipLaunchKernelGGL((lin_recurrent<IN, OUT, 32, MODE>), grid, dim3(256), 0, st, a, slices);
-  else hipLaunchKernelGGL((lin_recurrent<IN, OUT, 64, MODE>), grid, dim3(256), 0, st, a, slices);
+  if (rw <= 16) hipLaunchKernelGGL((lin_recurrent<IN, OUT, 16, MODE>), grid, dim3(256), 0, st, a);
+  else if (rw <= 32) hipLaunchKernelGGL((lin_recurrent<IN, OUT, 32, MODE>), grid, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL((lin_recurrent<IN, OUT, 64, MODE>), grid, dim3(256), 0, st, a);
   return hipGetLastError();
 }
 

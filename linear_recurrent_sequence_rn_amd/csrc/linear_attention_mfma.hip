@@ -196,7 +196,7 @@ struct Tile {
 };
 
 template <int DK, int CW, int VW, int DW, LinMode MODE>
-__global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(LinArgs a, int slices) {
+__global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(LinArgs a) {
   constexpr int NT = 64 * VW * DW;
   constexpr int DV = VW * CW;            // columns a block
   constexpr int VT = CW / 16;            // 16-column tiles a wave
@@ -221,7 +221,9 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
   char* pt = qt + kTileQ;
   f32x4* swap = reinterpret_cast<f32x4*>(pt + kTileP);
 
-  const int h = blockIdx.x / slices, c0 = (blockIdx.x - h * slices) * DV;
+  int h, c0;
+  lin_block(a, blockIdx.x, &h, &c0);
+  c0 *= DV;
   const int seg = blockIdx.y, s = blockIdx.z;
   const int tid = threadIdx.x;
   const int lane = tid & 63, l16 = lane & 15, g4 = (lane >> 4) * 4;
@@ -559,9 +561,9 @@ hipError_t launch_t(const LinArgs& a, LinMode mode, hipStream_t st) {
   const int slices = (a.dv + VW * CW - 1) / (VW * CW);
   const bool rest = a.T > 0 && a.zero_rest && mode != kLinState;
   const dim3 grid(a.H * slices, a.n_seg, a.S + (rest ? 1 : 0)), block(64 * VW * DW);
-  if (mode == kLinWhole) hipLaunchKernelGGL((lin_chunks<DK, CW, VW, DW, kLinWhole>), grid, block, 0, st, a, slices);
-  else if (mode == kLinState) hipLaunchKernelGGL((lin_chunks<DK, CW, VW, DW, kLinState>), grid, block, 0, st, a, slices);
-  else hipLaunchKernelGGL((lin_chunks<DK, CW, VW, DW, kLinOut>), grid, block, 0, st, a, slices);
+  if (mode == kLinWhole) hipLaunchKernelGGL((lin_chunks<DK, CW, VW, DW, kLinWhole>), grid, block, 0, st, a);
+  else if (mode == kLinState) hipLaunchKernelGGL((lin_chunks<DK, CW, VW, DW, kLinState>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((lin_chunks<DK, CW, VW, DW, kLinOut>), grid, block, 0, st, a);
   return hipGetLastError();
 }
 
