@@ -73,7 +73,8 @@ __device__ __forceinline__ bf16x8 col_operand(const char* tile, int base, int ks
 
 struct alignas(16) Decays {   // of one chunk
   float c[kChunk];       // running sum of log2 decays
-  float e[kChunk];       // 2^c
+  float q[kChunk];       // the same + log2 |scale|: the queries' side of a score's decay
+  float e[kChunk];       // 2^c |scale|
   float w[kChunk];       // 2^(c_63 - c)
   float a;               // 2^c_63
   int bad;               // v holds a NaN or an infinity
@@ -110,7 +111,7 @@ __device__ __forceinline__ double dpp_or_zero(double x) {
 
 // One wave: the decays of a chunk from each lane's log decay. Sums in float64, so that
 // differences of far sums keep float32 accuracy. Returns the chunk's sum of log2 decays.
-__device__ __forceinline__ double scan_decays(float g, Decays* d) {
+__device__ __forceinline__ double scan_decays(float g, float log2_scale, Decays* d) {
   const int lane = threadIdx.x & 63;
   double x = static_cast<double>(g) * kLog2e;
   if (x < kFloor) x = kFloor;           // (a NaN stays)
@@ -125,7 +126,8 @@ __device__ __forceinline__ double scan_decays(float g, Decays* d) {
   const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(u >> 32), 63);
   const double last = __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
   d->c[lane] = static_cast<float>(x);
-  d->e[lane] = exp2f(static_cast<float>(x));
+  d->q[lane] = static_cast<float>(x + log2_scale);
+  d->e[lane] = exp2f(static_cast<float>(x + log2_scale));
   d->w[lane] = exp2f(static_cast<float>(last - x));
   if (lane == 63) d->a = exp2f(static_cast<float>(x));
   return last;
@@ -229,6 +231,9 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
   const int lane = tid & 63, l16 = lane & 15, g4 = (lane >> 4) * 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wv = wave % VW, wd = wave / VW;              // column tile and row half of this wave
+  // Key tile of this wave's scores: the first meets four query tiles, the last one, so the tiles
+  // go round the waves (and SIMDs) from block to block.
+  const int keys = (wave + blockIdx.x) & 3;
   const int nc = min(DV, a.dv - c0);
   int64_t row0, own;
   int len;
@@ -275,6 +280,7 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
   auto fetch_v = [&](int t) { tv.load(vp + t * a.vs[2], a.vs[2], voff, len - t, nc); };
   auto log_decay = [&](int t) { return t + lane < t1 ? gp[(t + lane) * a.gs[2]] : 0.f; };
 
+  const float log2_scale = log2f(fabsf(a.scale));   // (-inf for 0: the outputs become 0)
   double gsum = 0.0;
   float gnext = 0.f;
   if (t0 < t1) {
@@ -282,10 +288,16 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
     fetch_k(t0);
     fetch_q(t0);
     if (wave == NT / 64 - 1) {              // (the last wave has the fewest score tiles)
-      gsum += scan_decays(log_decay(t0), &dec[0]);
+      gsum += scan_decays(log_decay(t0), log2_scale, &dec[0]);
       gnext = log_decay(t0 + kChunk);
     }
     if (tid == 0) dec[0].bad = 0;
+    if constexpr (kOut) {                   // score tiles above the diagonal that are read
+      if (tid < 2 * 16 * 4) {
+        const int tt = (tid >> 6) * 32 + (tid & 15), col = (tid >> 6) * 32 + 16 + ((tid >> 4) & 3) * 4;
+        *reinterpret_cast<uint2*>(pt + at<kChunk>(tt, col)) = make_uint2(0, 0);
+      }
+    }
     __syncthreads();
   }
   // The outputs of a chunk are stored when the next one's tiles have arrived: loads and stores
@@ -347,39 +359,53 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
     if (more) {
       fetch_v(t + kChunk);
       if (wave == NT / 64 - 1) {
-        gsum += scan_decays(gnext, &dec[buf ^ 1]);
+        gsum += scan_decays(gnext, log2_scale, &dec[buf ^ 1]);
         gnext = log_decay(t + 2 * kChunk);
       }
       if (tid == 0) dec[buf ^ 1].bad = 0;
     }
     f32x4 O[4][VT];
     if constexpr (kOut) {
-      // scores P^T = K Q^T, keys in the rows: a wave has one tile of 16 keys and meets all query
-      // tiles (four waves), or half of them (eight), with it; above the diagonal it writes zeros
+      // scores P^T = K Q^T, keys in the rows: a wave has one tile of 16 keys and meets the query
+      // tiles from its own on (four waves), or half of them (eight), with it
       constexpr int JT = 16 / (NT / 64);    // query tiles a wave
-      const int i = wave & 3, j0 = JT == 4 ? 0 : (wave >> 2) * 2;
-      if (JT == 4 || i <= j0 + 1) {         // (of the first 32 queries, nobody reads keys from 32 on)
-        bf16x8 kf[KS];
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) kf[ks] = row_operand(kt, rq + i * 32 * DK, ks, 0);
-        const f32x4 cs = *reinterpret_cast<const f32x4*>(&D.c[16 * i + g4]);
-        const int rj = rq + j0 * 32 * DK, pj = (rp ^ (i << 5)) + j0 * 32 * kChunk;
-        f32x4 p[JT];
-#pragma unroll
-        for (int j = 0; j < JT; ++j) p[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-          for (int j = 0; j < JT; ++j) p[j] = mfma(kf[ks], row_operand(qt, rj, ks, j * 32 * DK), p[j]);
-        const int ahead = l16 - g4 + 16 * (j0 - i);   // queries' lead over the lane's first key
-#pragma unroll
-        for (int j = 0; j < JT; ++j) {
-          const float ct = D.c[16 * (j0 + j) + l16];
+      const int j0 = JT == 4 ? 0 : (wave >> 2) * 2;
+      if (keys <= j0 + JT - 1) {
+        const int rk = rq + keys * 32 * DK, rj = rq + j0 * 32 * DK, pj = (rp ^ (keys << 5)) + j0 * 32 * kChunk;
+        const f32x4 cs = *reinterpret_cast<const f32x4*>(&D.c[16 * keys + g4]);
+        const int ahead = l16 - g4 + 16 * (j0 - keys);   // queries' lead over the lane's first key
+        auto finish = [&](int j, const f32x4& p) {
+          const float ct = D.q[16 * (j0 + j) + l16];
           float x[4];
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            x[r] = ahead + 16 * j >= r ? p[j][r] * __builtin_amdgcn_exp2f(ct - cs[r]) : 0.f;
+            x[r] = ahead + 16 * j >= r ? p[r] * __builtin_amdgcn_exp2f(ct - cs[r]) : 0.f;
           *reinterpret_cast<uint2*>(pt + pj + j * 32 * kChunk) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+        };
+        if constexpr (JT == 4) {
+          bf16x8 kf[KS];
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) kf[ks] = row_operand(kt, rk, ks, 0);
+#pragma unroll
+          for (int j = 0; j < JT; ++j) {
+            if (j0 + j < keys) continue;
+            f32x4 p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) p = mfma(kf[ks], row_operand(qt, rj, ks, j * 32 * DK), p);
+            finish(j, p);
+          }
+        } else {                            // both tiles at once: no room for all of the keys' operands
+          f32x4 p[JT];
+#pragma unroll
+          for (int j = 0; j < JT; ++j) p[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            const bf16x8 kf = row_operand(kt, rk, ks, 0);
+#pragma unroll
+            for (int j = 0; j < JT; ++j) p[j] = mfma(kf, row_operand(qt, rj, ks, j * 32 * DK), p[j]);
+          }
+#pragma unroll
+          for (int j = 0; j < JT; ++j) finish(j, p[j]);
         }
       }
       if (more) fetch_k(t + kChunk);
@@ -416,6 +442,8 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
       if constexpr (kOut) fetch_q(t + kChunk);
       else fetch_k(t + kChunk);
     }
+    // (the largest head has no register left for products started early)
+    if constexpr (DK == 256) __builtin_amdgcn_sched_barrier(0);
     const bool bad = D.bad;
     bf16x8 vf[2][VT];
     if constexpr (kHasV)
@@ -432,6 +460,7 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
         for (int v = 0; v < VT; ++v) S[i][v] *= dec64;
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
+        if constexpr (DK == 256) __builtin_amdgcn_sched_barrier(0);
         bf16x8 wf[VT][PARTS];
         if constexpr (kParts) {
 #pragma unroll
@@ -523,7 +552,7 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
         }
 #pragma unroll
         for (int v = 0; v < VT; ++v) {
-          o[v] *= a.scale;
+          if (a.scale < 0.f) o[v] = -o[v];
           done[x][v] = make_uint2(pack_bf16x2(o[v][0], o[v][1]), pack_bf16x2(o[v][2], o[v][3]));
         }
       }
@@ -552,30 +581,41 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
   }
 }
 
-// Columns a block: 128 where d_v has them (each chunk's Q and K are then read from LDS for
-// twice the columns), else 64.
+// Columns a block. With d_k above 128, 128 where d_v has them: each chunk's Q and K are then read
+// from memory and LDS for twice the columns (8 sequences of 2048 tokens, 16 heads of 256 x 512:
+// 598 us, against 684 us with 64 columns). Below, 64: more blocks a CU hide more of the waits
+// between a chunk's phases (13 packed sequences of 32 heads of 64 x 128: 140 us, against 168 us
+// with 128 columns).
 int columns(const LinArgs& a) { return a.dk > 128 && a.dv > 64 ? 128 : 64; }
 
-template <int DK, int CW, int VW, int DW>
-hipError_t launch_t(const LinArgs& a, LinMode mode, hipStream_t st) {
+template <int DK, int CW, int VW, int DW, LinMode MODE>
+hipError_t launch_t(const LinArgs& a, hipStream_t st) {
   const int slices = (a.dv + VW * CW - 1) / (VW * CW);
-  const bool rest = a.T > 0 && a.zero_rest && mode != kLinState;
+  const bool rest = a.T > 0 && a.zero_rest && MODE != kLinState;
   const dim3 grid(a.H * slices, a.n_seg, a.S + (rest ? 1 : 0)), block(64 * VW * DW);
-  if (mode == kLinWhole) hipLaunchKernelGGL((lin_chunks<DK, CW, VW, DW, kLinWhole>), grid, block, 0, st, a);
-  else if (mode == kLinState) hipLaunchKernelGGL((lin_chunks<DK, CW, VW, DW, kLinState>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((lin_chunks<DK, CW, VW, DW, kLinOut>), grid, block, 0, st, a);
+  hipLaunchKernelGGL((lin_chunks<DK, CW, VW, DW, MODE>), grid, block, 0, st, a);
   return hipGetLastError();
+}
+
+template <LinMode MODE>
+hipError_t launch_mode(const LinArgs& a, hipStream_t st) {
+  if (a.dk <= 64) return launch_t<64, 16, 4, 1, MODE>(a, st);
+  if (a.dk <= 128) return launch_t<128, 16, 4, 1, MODE>(a, st);
+  if (columns(a) == 128) return launch_t<256, 32, 4, 2, MODE>(a, st);
+  return launch_t<256, 16, 4, 2, MODE>(a, st);
 }
 
 }  // namespace
 
-int lin_mfma_blocks(const LinArgs& a) { return a.H * ((a.dv + columns(a) - 1) / columns(a)); }
+int lin_mfma_blocks(const LinArgs& a) {
+  const int w = columns(a);
+  return a.H * ((a.dv + w - 1) / w);
+}
 
 hipError_t launch_lin_mfma(const LinArgs& a, LinMode mode, hipStream_t st) {
-  const bool wide = columns(a) == 128;
-  if (a.dk <= 64) return launch_t<64, 16, 4, 1>(a, mode, st);
-  if (a.dk <= 128) return launch_t<128, 16, 4, 1>(a, mode, st);
-  return wide ? launch_t<256, 32, 4, 2>(a, mode, st) : launch_t<256, 16, 4, 2>(a, mode, st);
+  if (mode == kLinWhole) return launch_mode<kLinWhole>(a, st);
+  if (mode == kLinState) return launch_mode<kLinState>(a, st);
+  return launch_mode<kLinOut>(a, st);
 }
 
 }  // namespace rn
