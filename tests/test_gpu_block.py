@@ -185,3 +185,15 @@ def test_captured_and_replayed_with_changing_inputs():
         want = calls(*n, theta)                       # eager work between the replays
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(first, want)) and torch.equal(after, n[4])
+
+
+def test_tensors_of_another_device_than_the_current_one(monkeypatch):
+    """The binding makes the tensors' GPU current for the call (here it is told that another is)."""
+    from linear_recurrent_sequence_rn_amd import block_ops
+    s = setup(11)
+    theta = 10000.0 ** (-np.arange(32) / 32)
+    copy = [t.clone() if torch.is_tensor(t) else t for t in s]
+    want = calls(*copy, theta)
+    monkeypatch.setattr(block_ops, "_current_device", lambda: 7)
+    got = calls(*s, theta)
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.cuda.current_device() == 0

@@ -189,6 +189,27 @@ def test_backward_options():
     assert torch.equal(rn().rn_layernorm_backward(dy, x, w, dsum=d3, dx=d3)["dx"], full["dx"])   # over dsum
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("d,extra", [(256, 8), (256, 1), (100, 28), (2000, 3)])
+def test_backward_of_strided_rows(kind, d, extra):
+    """Rows with gaps, and rows that are all the same one: the bits of the contiguous call where
+    the same kernel runs, and its numbers where the rows' alignment takes another."""
+    dt = DT[kind]
+    g = torch.Generator().manual_seed(d * 3 + extra)
+    x, dy, dh, dx = (spread(g, 37, d, dt, n * extra) for n in (1, 2, 3, 4))
+    w = torch.randn(d, generator=g).to(DEV)
+    got = rn().rn_layernorm_backward(dy, x, w, dsum=dh, dx=dx)
+    assert got["dx"] is dx and int(torch.count_nonzero(dx._base[:, d:])) == 0
+    want = rn().rn_layernorm_backward(*(t.contiguous() for t in (dy, x)), w, dsum=dh.contiguous())
+    for name in ("dx", "dweight", "dbias"):
+        a, b = got[name].double(), want[name].double()
+        assert (a - b).abs().max() <= (2 * half_step(dt) if name == "dx" else 1e-5) * b.abs().max() + 1e-6
+    one = dy[:1].contiguous()
+    same = rn().rn_layernorm_backward(one.expand(37, d), x, w)
+    full = rn().rn_layernorm_backward(one.expand(37, d).contiguous(), x, w)
+    assert all(torch.equal(same[n], full[n]) or extra % 8 for n in full)
+
+
 def test_refusals():
     x = torch.zeros(4, 64, device=DEV)
     for kw in (dict(residual=torch.zeros(4, 65, device=DEV)), dict(residual=x.bfloat16()), dict(weight=x[0].bfloat16()),
@@ -196,8 +217,11 @@ def test_refusals():
                dict(sum_out=x.bfloat16())):
         with pytest.raises(ValueError):
             rn().rn_layernorm(x, **kw)
-    with pytest.raises(ValueError):
-        rn().rn_layernorm(torch.zeros(0, 64, device=DEV))
+    for empty in (torch.zeros(0, 64, device=DEV), torch.zeros(4, 0, device=DEV), torch.tensor(1.0, device=DEV)):
+        with pytest.raises(ValueError):
+            rn().rn_layernorm(empty)
+        with pytest.raises(ValueError):
+            rn().rn_layernorm_backward(empty, empty)
     with pytest.raises(TypeError):
         rn().rn_layernorm(x.half())
     with pytest.raises(ValueError):

@@ -321,6 +321,79 @@ def test_offsets_past_32_bits():
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("kind,generic", [("bf16", False), ("bf16", True), ("f32", False)])
+def test_many_segments(kind, generic):
+    """More segments than the scan holds in flight, of a padded batch with a short and an empty
+    sequence beside the long one; the final state, and one without."""
+    B, H, N, d = 3, 1, 9000, 16
+    q, k, v, g = inputs(B, H, H, H, H, N, d, d, kind, 21, True, fade=16.0)
+    s0 = torch.randn(B, H, d, d, device=DEV, generator=torch.Generator(DEV).manual_seed(9))
+    lens = [9000, 5, 0]
+    ln = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    out, S = rn().rn_linear_attention_chunked(q, k, v, g, lengths=ln, state_in=s0, state_out=True, force_generic=generic)
+    drop, _ = rn().rn_linear_attention_chunked(q, k, v, g, lengths=ln, state_in=s0, force_generic=generic)
+    assert torch.equal(out, drop) and torch.equal(S[2], s0[2])
+    for b in range(2):
+        n = lens[b]
+        check_sequence(out[b, :, :n], S[b], q[b, :, :n], k[b, :, :n], v[b, :, :n], g[b, :, :n], 1.0, s0[b], kind == "bf16" and not generic)
+
+
+@pytest.mark.parametrize("N", [100, 2000])
+@pytest.mark.parametrize("off,pad", [(0, 0), (0, 8), (0, 3), (1, 7), (3, 0), (8, 24)])
+def test_views_of_a_projection(N, off, pad):
+    """q, k, v as slices of one bf16 buffer at odd places and strides, out into a buffer of its
+    own with gaps, which keep their bits; 16-byte rows or not, the numbers hold."""
+    H, dk, dv = 2, 32, 40
+    cols = H * (2 * dk + dv) + pad
+    g_ = torch.Generator().manual_seed(22 + off + pad)
+    buf = torch.randn(1, N, off + cols, generator=g_).bfloat16().to(DEV)
+    dec = torch.nn.functional.logsigmoid(torch.randn(1, H, N, generator=g_) + 2).to(DEV) / 4
+    cut = lambda c0, d: buf[..., off + c0:off + c0 + H * d].unflatten(-1, (H, d)).transpose(1, 2)  # noqa: E731
+    q, k, v = cut(0, dk), cut(H * dk, dk), cut(2 * H * dk, dv)
+    wide = torch.full((1, N, off + H * dv + pad), 7.0, dtype=torch.bfloat16, device=DEV)
+    out = wide[..., off:off + H * dv].unflatten(-1, (H, dv)).transpose(1, 2)
+    ws = torch.empty(rn().rn_linear_attention_workspace_bytes(q, k, v, dec, out=out) or 16, dtype=torch.uint8, device=DEV)
+    _, S = rn().rn_linear_attention_chunked(q, k, v, dec, out=out, state_out=True, workspace=ws)
+    check_sequence(out[0], S[0], q[0], k[0], v[0], dec[0], 1.0, None, True)
+    assert (wide[..., :off] == 7.0).all() and (wide[..., off + H * dv:] == 7.0).all()
+
+
+@pytest.mark.parametrize("scale", [-0.7, 0.0, 1e-30, 1e4])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_scales(kind, scale):
+    q, k, v, g = inputs(1, 2, 2, 2, 2, 150, 64, 64, kind, 23)
+    out, S = rn().rn_linear_attention_chunked(q, k, v, g, qk_scale=scale, state_out=True)
+    o, _ = K.linear_attention(q[0], k[0], v[0], g[0], scale)
+    if scale == 0.0:
+        assert int(torch.count_nonzero(out)) == 0
+    else:
+        check_sequence(out[0], S[0], q[0], k[0], v[0], g[0], scale, None, kind == "bf16")
+    ref, R = rn().rn_linear_attention_chunked(q, k, v, g, state_out=True)
+    assert torch.equal(S, R)                               # the scale never enters the state
+
+
+def test_two_graphs_on_one_workspace():
+    """Two captured calls that share a workspace, replayed in turn, against eager calls."""
+    sets = [inputs(1, 2, 2, 2, 2, 2000, 64, 64, "bf16", s) for s in (24, 25)]
+    n = rn().rn_linear_attention_workspace_bytes(*sets[0])
+    assert n > 0
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    run = lambda t: rn().rn_linear_attention_chunked(*t, state_out=True, workspace=ws)  # noqa: E731
+    want = [tuple(x.clone() for x in run(t)) for t in sets]
+    torch.cuda.synchronize()
+    graphs, got = [], []
+    for t in sets:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got.append(run(t))
+        graphs.append(graph)
+    for turn in (0, 1, 1, 0, 1):
+        ws.fill_(255)
+        graphs[turn].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got[turn], want[turn]))
+
+
 def test_refusals():
     q, k, v, g = inputs(2, 4, 4, 2, 4, 8, 16, 16, "f32", 20)
     f, st = rn().rn_linear_attention_chunked, rn().rn_linear_attention_step

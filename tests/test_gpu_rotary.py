@@ -132,6 +132,19 @@ def test_rotated_tensors_feed_retention(kind):
     assert ((got - own).abs() <= 2 * 2.1 * h * mass * 2).all()      # a turned pair: up to sqrt 2 of |a| + |b| each
 
 
+@pytest.mark.parametrize("half", [False, True])
+def test_far_positions_and_many_tokens(half):
+    """Positions beyond 2^32 (the product with theta is the same float64 number on both sides),
+    and more tokens than one round of blocks."""
+    g = torch.Generator().manual_seed(6)
+    theta = np.array([1.0, 0.37, 1e-3, 1e-9])
+    x = torch.randn(2, 1, 5, 8, generator=g).to(DEV)
+    far = torch.tensor([(1 << 33) + 1, (1 << 36) - 7], device=DEV)
+    check(rn().rn_rotary(x, None, theta, pos=far, half=half), x, theta, far.cpu().numpy()[:, None] + np.arange(5), half, False, 1.0)
+    x = torch.randn(3, 1, 30001, 8, generator=g).to(DEV)
+    check(rn().rn_rotary(x, None, theta, pos0=5, half=half), x, theta, np.arange(30001)[None].repeat(3, 0) + 5, half, False, 1.0)
+
+
 def test_refusals():
     q = torch.zeros(2, 4, 8, 64, device=DEV)
     th = np.ones(32)
