@@ -378,8 +378,11 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
           const float ct = D.q[16 * (j0 + j) + l16];
           float x[4];
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            x[r] = ahead + 16 * j >= r ? p[r] * __builtin_amdgcn_exp2f(ct - cs[r]) : 0.f;
+          for (int r = 0; r < 4; ++r) x[r] = p[r] * __builtin_amdgcn_exp2f(ct - cs[r]);
+          if (j0 + j <= keys) {             // on the diagonal (or above it)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[r] = ahead + 16 * j >= r ? x[r] : 0.f;
+          }
           *reinterpret_cast<uint2*>(pt + pj + j * 32 * kChunk) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
         };
         if constexpr (JT == 4) {
