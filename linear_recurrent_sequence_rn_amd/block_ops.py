@@ -240,16 +240,18 @@ def rn_layernorm_backward(dout, x, weight=None, eps=1e-5, *, dsum=None, dx=None,
 # ---- rotary positions -----------------------------------------------------------------------
 
 def _bhn(t, name):
-    """Strides of [B, H, N, ...] with a contiguous last axis (if there is a fourth)."""
-    if t.dim() == 4 and t.shape[3] > 1 and t.stride(3) != 1:
+    """Strides of [B, H, N, d] with a contiguous last axis."""
+    st = t.stride()
+    if st[3] != 1 and t.shape[3] > 1:
         raise ValueError(f"{name}: the last axis must be contiguous")
-    return t.stride()[:3]
+    return st[:3]
 
 
-def _new_like(t, shape=None, dtype=None):
-    """A new tensor of t's (or the given) shape [B, H, N, d], token-major in memory where t is."""
-    B, H, N, d = t.shape if shape is None else shape
-    dtype = t.dtype if dtype is None else dtype
+def _new_like(t, shape, dtype):
+    """A new tensor of the given shape [B, H, N, d], token-major in memory where t is."""
+    if t.dtype == dtype and t.shape == shape:
+        return torch.empty_like(t)
+    B, H, N, d = shape
     _, h, n, _ = t.stride()
     if h < n:                             # [B, N, H, d] in memory
         return torch.empty_strided((B, H, N, d), (N * H * d, d, H * d, 1), dtype=dtype, device=t.device)
@@ -271,13 +273,14 @@ def rn_rotary(q, k=None, theta=None, *, pos0=0, pos=None, half=False, inverse=Fa
     if theta is None:
         raise ValueError("theta is required")
     dev = _device(q, k, pos, q_out, k_out)
-    if q.dim() != 4 or (k is not None and (k.dim() != 4 or k.dtype != q.dtype or k.shape[0] != q.shape[0] or
-                                           k.shape[2:] != q.shape[2:])):
+    sq, sk = q.shape, None if k is None else k.shape
+    if len(sq) != 4 or (k is not None and (len(sk) != 4 or k.dtype != q.dtype or sk[0] != sq[0] or sk[2] != sq[2] or
+                                           sk[3] != sq[3])):
         raise ValueError(f"expected q [B,H_q,N,d] and k [B,H_k,N,d] of one type; got {q.dtype} {tuple(q.shape)}"
                          + ("" if k is None else f", {k.dtype} {tuple(k.shape)}"))
-    if q.numel() == 0 or (k is not None and k.numel() == 0):
+    if 0 in sq or (k is not None and 0 in sk):
         raise ValueError("q and k must not be empty")
-    B, Hq, N, d = q.shape
+    B, Hq, N, d = sq
     th = np.ascontiguousarray(theta, dtype=np.float64)
     if th.ndim != 1:
         raise ValueError("theta must be one-dimensional")
@@ -293,12 +296,12 @@ def rn_rotary(q, k=None, theta=None, *, pos0=0, pos=None, half=False, inverse=Fa
                 raise ValueError("k_out without k")
             _like(t, like, name)
     if q_out is None:
-        q_out = _new_like(q)
+        q_out = torch.empty_like(q)         # dense, its axes in memory as q's
     if k is not None and k_out is None:
-        k_out = _new_like(k)
+        k_out = torch.empty_like(k)
     qs, qos = _bhn(q, "q"), _bhn(q_out, "q_out")
     ks, kos = (_NO_STRIDE, _NO_STRIDE) if k is None else (_bhn(k, "k"), _bhn(k_out, "k_out"))
-    desc = _pack_rotary(B, N, Hq, 0 if k is None else k.shape[1], d, 2 * th.size, _code(q.dtype), flags, pos0,
+    desc = _pack_rotary(B, N, Hq, 0 if k is None else sk[1], d, 2 * len(th), _code(q.dtype), flags, pos0,
                         magnitude, th.ctypes.data, *qs, *ks, *qos, *kos)
     _call(dev, lib.rn_rotary, desc, _p(pos), q.data_ptr(), _p(k), q_out.data_ptr(), _p(k_out))
     return q_out if k is None else (q_out, k_out)
@@ -325,17 +328,18 @@ def rn_rotary_frequencies(rot, base=10000.0, kind="plain", *, factor=1.0, length
 # ---- linear attention -----------------------------------------------------------------------
 
 def _linear_shapes(q, k, v, g):
-    if not (q.dim() == k.dim() == v.dim() == 4):
-        raise ValueError(f"expected q [B,H_q,N,d_k], k [B,H_k,N,d_k], v [B,H_v,N,d_v]; got {tuple(q.shape)}, "
-                         f"{tuple(k.shape)}, {tuple(v.shape)}")
-    B, _, rows, dk = q.shape
-    if k.shape[0] != B or k.shape[2] != rows or k.shape[3] != dk or v.shape[0] != B or v.shape[2] != rows:
-        raise ValueError(f"q, k and v must agree in batch and tokens, q and k in d_k; got {tuple(q.shape)}, "
-                         f"{tuple(k.shape)}, {tuple(v.shape)}")
+    sq, sk, sv, sg = q.shape, k.shape, v.shape, g.shape
+    if not (len(sq) == len(sk) == len(sv) == 4):
+        raise ValueError(f"expected q [B,H_q,N,d_k], k [B,H_k,N,d_k], v [B,H_v,N,d_v]; got {tuple(sq)}, {tuple(sk)}, "
+                         f"{tuple(sv)}")
+    B, _, rows, dk = sq
+    if sk[0] != B or sk[2] != rows or sk[3] != dk or sv[0] != B or sv[2] != rows:
+        raise ValueError(f"q, k and v must agree in batch and tokens, q and k in d_k; got {tuple(sq)}, {tuple(sk)}, "
+                         f"{tuple(sv)}")
     if not (q.dtype == k.dtype == v.dtype):
         raise TypeError("q, k, v must share one dtype")
-    if g.dim() != 3 or g.dtype != torch.float32 or g.shape[0] != B or g.shape[2] != rows:
-        raise ValueError(f"log_decay must be float32 [{B}, H, {rows}]; got {g.dtype} {tuple(g.shape)}")
+    if len(sg) != 3 or g.dtype != torch.float32 or sg[0] != B or sg[2] != rows:
+        raise ValueError(f"log_decay must be float32 [{B}, H, {rows}]; got {g.dtype} {tuple(sg)}")
 
 
 def _linear_desc(q, k, v, g, S, N, T, n_slots, out_dtype, flags, qk_scale, out):
