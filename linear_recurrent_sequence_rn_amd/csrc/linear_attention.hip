@@ -17,16 +17,17 @@ namespace {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 // ---- one token a sequence ---------------------------------------------------------------
-// A block owns NQ * VEC columns of one (sequence, head) state; thread (group, column vector)
-// takes rows group, group + G, ... in batches of 8, the next batch's loads issued before
-// the present one is updated. Non-temporal: a batch's states are larger than the caches and
-// are read once a step.
-constexpr int kStepThreads = 256;
+// A block of NT threads owns NQ * VEC columns of one (sequence, head) state; thread (group,
+// column vector) takes rows group, group + G, ... in batches of 8, the next batch's loads issued
+// before the present one is updated. Non-temporal: a batch's states are larger than the caches
+// and are read once a step. FULL: every thread has a column and every batch its rows, so that
+// no load hangs on a condition (128 states of 16 heads of 256 x 512: 375 us, 5.7 TB/s; with
+// conditions and half the columns a block 460 us).
 constexpr int kBatch = 8;
 
-template <int IN, int OUT, int VEC, int NQ>
-__global__ void __launch_bounds__(kStepThreads) lin_step(LinArgs a, int slices) {
-  constexpr int G = kStepThreads / NQ;
+template <int IN, int OUT, int VEC, int NQ, int NT, bool FULL>
+__global__ void __launch_bounds__(NT) lin_step(LinArgs a, int slices) {
+  constexpr int G = NT / NQ;
   constexpr int W = NQ * VEC;
   __shared__ float qh[kMaxDk];
   __shared__ float kh[kMaxDk];
@@ -38,31 +39,20 @@ __global__ void __launch_bounds__(kStepThreads) lin_step(LinArgs a, int slices) 
   const int64_t oo = s * a.os[0] + h * a.os[1] + c0;
   const int nc = min(W, a.dv - c0);
   if (slot < 0) {
-    for (int c = tid; c < nc; c += kStepThreads) Elem<OUT>::store(a.out, oo + c, 0.f);
+    for (int c = tid; c < nc; c += NT) Elem<OUT>::store(a.out, oo + c, 0.f);
     return;
   }
   const int64_t qo = s * a.qs[0] + h / (a.H / a.Hq) * a.qs[1];
   const int64_t ko = s * a.ks[0] + h / (a.H / a.Hk) * a.ks[1];
   const int64_t vo = s * a.vs[0] + h / (a.H / a.Hv) * a.vs[1] + c0;
-  for (int d = tid; d < a.dk; d += kStepThreads) {
-    qh[d] = Elem<IN>::load(a.q, qo + d);
-    kh[d] = Elem<IN>::load(a.k, ko + d);
-  }
-  const bool col = cq * VEC < nc;
-  const float dec = expf(a.g[s * a.gs[0] + h * a.gs[1]]);
-  float vr[VEC], acc[VEC];
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    vr[i] = col ? Elem<IN>::load(a.v, vo + cq * VEC + i) : 0.f;
-    acc[i] = 0.f;
-  }
-  float* S = a.state_out + (static_cast<int64_t>(slot) * a.H + h) * a.dk * a.dv + c0 + cq * VEC;
-  const int dv = a.dv;
+  const int dk = a.dk, dv = a.dv;
+  const bool col = FULL || cq * VEC < nc;
+  float* S = a.state_out + (static_cast<int64_t>(slot) * a.H + h) * dk * dv + c0 + cq * VEC;
   auto load = [&](int d0, float (*x)[VEC]) {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       const int d = d0 + u * G;
-      if (col && d < a.dk) {
+      if (FULL || (col && d < dk)) {
         if constexpr (VEC == 4) {
           const f32x4 y = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(S + static_cast<int64_t>(d) * dv));
           x[u][0] = y.x; x[u][1] = y.y; x[u][2] = y.z; x[u][3] = y.w;
@@ -72,11 +62,24 @@ __global__ void __launch_bounds__(kStepThreads) lin_step(LinArgs a, int slices) 
       }
     }
   };
+  float xa[kBatch][VEC], xb[kBatch][VEC];
+  load(grp, xa);
+  for (int d = tid; d < dk; d += NT) {
+    qh[d] = Elem<IN>::load(a.q, qo + d);
+    kh[d] = Elem<IN>::load(a.k, ko + d);
+  }
+  const float dec = expf(a.g[s * a.gs[0] + h * a.gs[1]]);
+  float vr[VEC], acc[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    vr[i] = col ? Elem<IN>::load(a.v, vo + cq * VEC + i) : 0.f;
+    acc[i] = 0.f;
+  }
   auto update = [&](int d0, float (*x)[VEC]) {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       const int d = d0 + u * G;
-      if (col && d < a.dk) {
+      if (FULL || (col && d < dk)) {
         const float kd = kh[d], qd = qh[d];
         float y[VEC];
 #pragma unroll
@@ -93,20 +96,20 @@ __global__ void __launch_bounds__(kStepThreads) lin_step(LinArgs a, int slices) 
       }
     }
   };
-  float xa[kBatch][VEC], xb[kBatch][VEC];
-  load(grp, xa);
   __syncthreads();
-  for (int d0 = grp; d0 < a.dk; d0 += 2 * G * kBatch) {
-    load(d0 + G * kBatch, xb);
+  for (int d0 = grp; d0 < dk; d0 += 2 * G * kBatch) {
+    // (with FULL, d_k - d0 is a multiple of a batch plus the group: these tests are uniform)
+    const bool second = d0 - grp + G * kBatch < dk, third = d0 - grp + 2 * G * kBatch < dk;
+    if (second) load(d0 + G * kBatch, xb);
     update(d0, xa);
-    load(d0 + 2 * G * kBatch, xa);
-    update(d0 + G * kBatch, xb);
+    if (third) load(d0 + 2 * G * kBatch, xa);
+    if (second) update(d0 + G * kBatch, xb);
   }
 #pragma unroll
   for (int i = 0; i < VEC; ++i) part[grp * W + cq * VEC + i] = acc[i];
   __syncthreads();
-  if constexpr (G > 8) {                   // many groups: all threads add a few, then the columns' own
-    constexpr int T = kStepThreads / W, P = G / T;
+  if constexpr (G > 8 && W < NT) {          // many groups: all threads add a few, then the columns' own
+    constexpr int T = NT / W, P = G / T;
     const int c = tid % W, i0 = tid / W * P;
     float o = 0.f;
 #pragma unroll
@@ -121,7 +124,7 @@ __global__ void __launch_bounds__(kStepThreads) lin_step(LinArgs a, int slices) 
       Elem<OUT>::store(a.out, oo + tid, a.scale * o);
     }
   } else {
-    for (int c = tid; c < nc; c += kStepThreads) {
+    for (int c = tid; c < nc; c += NT) {
       float o = 0.f;
 #pragma unroll
       for (int i = 0; i < G; ++i) o += part[i * W + c];
@@ -340,19 +343,25 @@ hipError_t launch_step_t(const LinArgs& a, hipStream_t st) {
   // Columns a block: as many as the row has (long runs of one state row), but fewer where
   // that leaves the chip's 256 CUs without two blocks each (states are independent by column).
   const int64_t states = static_cast<int64_t>(a.S) * a.H;
-#define RN_STEP(VEC, NQ)                                                                            \
+#define RN_STEP(VEC, NQ, NT, FULL)                                                                  \
   do {                                                                                              \
     const int slices = (a.dv + VEC * NQ - 1) / (VEC * NQ);                                          \
-    hipLaunchKernelGGL((lin_step<IN, OUT, VEC, NQ>), dim3(a.H * slices, a.S), dim3(kStepThreads), 0, st, a, slices); \
+    hipLaunchKernelGGL((lin_step<IN, OUT, VEC, NQ, NT, FULL>), dim3(a.H * slices, a.S), dim3(NT), 0, st, a, slices); \
     return hipGetLastError();                                                                       \
   } while (0)
   if (a.dv % 4 == 0) {
-    if (a.dv > 128 && states * ((a.dv + 255) / 256) >= 512) RN_STEP(4, 64);
-    if (a.dv > 64 && states * ((a.dv + 127) / 128) >= 512) RN_STEP(4, 32);
-    if (a.dv > 16 && states * ((a.dv + 63) / 64) >= 512) RN_STEP(4, 16);
-    RN_STEP(4, 4);
+    if (states >= 512) {
+      if (a.dv == 512 && a.dk % 32 == 0) RN_STEP(4, 128, 512, true);
+      if (a.dv == 256 && a.dk % 64 == 0) RN_STEP(4, 64, 512, true);
+      if (a.dv == 128 && a.dk % 64 == 0) RN_STEP(4, 32, 256, true);
+      if (a.dv == 64 && a.dk % 128 == 0) RN_STEP(4, 16, 256, true);
+    }
+    if (a.dv > 128 && states * ((a.dv + 255) / 256) >= 512) RN_STEP(4, 64, 256, false);
+    if (a.dv > 64 && states * ((a.dv + 127) / 128) >= 512) RN_STEP(4, 32, 256, false);
+    if (a.dv > 16 && states * ((a.dv + 63) / 64) >= 512) RN_STEP(4, 16, 256, false);
+    RN_STEP(4, 4, 256, false);
   }
-  RN_STEP(1, 64);
+  RN_STEP(1, 64, 256, false);
 #undef RN_STEP
 }
 
