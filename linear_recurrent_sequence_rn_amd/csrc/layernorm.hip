@@ -22,91 +22,92 @@ namespace {
 // Threads of a block whose rows take W waves each.
 constexpr int threads(int W) { return W > 4 ? 64 * W : 256; }
 
-// V consecutive elements of type DT from a 16-byte (V > 1) or element-aligned address.
-template <int DT, int V> struct Vec;
-template <> struct Vec<RN_F32, 1> {
-  __device__ static __forceinline__ void load(const void* p, int64_t i, float* f) { f[0] = static_cast<const float*>(p)[i]; }
-  __device__ static __forceinline__ void store(void* p, int64_t i, const float* f) { static_cast<float*>(p)[i] = f[0]; }
-};
-template <> struct Vec<RN_BF16, 1> {
-  __device__ static __forceinline__ void load(const void* p, int64_t i, float* f) { f[0] = Elem<RN_BF16>::load(p, i); }
-  __device__ static __forceinline__ void store(void* p, int64_t i, const float* f) { Elem<RN_BF16>::store(p, i, f[0]); }
-};
-template <int V> struct Vec<RN_F32, V> {
-  __device__ static __forceinline__ void load(const void* p, int64_t i, float* f) {
-    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-#pragma unroll
-    for (int j = 0; j < V / 4; ++j) {
-      const float4 x = s[j];
-      f[4 * j] = x.x; f[4 * j + 1] = x.y; f[4 * j + 2] = x.z; f[4 * j + 3] = x.w;
-    }
-  }
-  __device__ static __forceinline__ void store(void* p, int64_t i, const float* f) {
-    float4* s = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-#pragma unroll
-    for (int j = 0; j < V / 4; ++j) s[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
-  }
-};
-template <int V> struct Vec<RN_BF16, V> {   // V = 4 or 8
-  __device__ static __forceinline__ void load(const void* p, int64_t i, float* f) {
-    const uint32_t* s = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p) + i);
-    uint32_t u[V / 2];
-    if constexpr (V == 8) {
-      const uint4 x = *reinterpret_cast<const uint4*>(s);
-      u[0] = x.x; u[1] = x.y; u[2] = x.z; u[3] = x.w;
-    } else {
-      const uint2 x = *reinterpret_cast<const uint2*>(s);
-      u[0] = x.x; u[1] = x.y;
-    }
-#pragma unroll
-    for (int j = 0; j < V / 2; ++j) {
-      f[2 * j] = __uint_as_float(u[j] << 16);
-      f[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
-    }
-  }
-  __device__ static __forceinline__ void store(void* p, int64_t i, const float* f) {
-    uint32_t u[V / 2];
-#pragma unroll
-    for (int j = 0; j < V / 2; ++j) u[j] = pack_bf16x2(f[2 * j], f[2 * j + 1]);
-    uint16_t* s = static_cast<uint16_t*>(p) + i;
-    if constexpr (V == 8) *reinterpret_cast<uint4*>(s) = make_uint4(u[0], u[1], u[2], u[3]);
-    else *reinterpret_cast<uint2*>(s) = make_uint2(u[0], u[1]);
-  }
-};
+// 16 or 8 bytes, past the caches with STREAM (which pays for calls larger than the last-level
+// cache; what a smaller call leaves behind is soon read again).
+template <bool STREAM, class T>
+__device__ __forceinline__ T get(const void* p) {
+  if constexpr (STREAM) return __builtin_nontemporal_load(static_cast<const T*>(p));
+  else return *static_cast<const T*>(p);
+}
+template <bool STREAM, class T>
+__device__ __forceinline__ void put(void* p, const T& x) {
+  if constexpr (STREAM) __builtin_nontemporal_store(x, static_cast<T*>(p));
+  else *static_cast<T*>(p) = x;
+}
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-// The same elements as they are in memory, for rows on their way: V elements of type DT.
-template <int DT, int V>
+// V consecutive elements of type DT as they are in memory; an address of 16 bytes (or the whole,
+// where that is less).
+template <int DT, int V, bool STREAM = false>
 struct Raw {
-  static constexpr int kBytes = V * (DT == RN_F32 ? 4 : 2);
+  static constexpr int kElem = DT == RN_F32 ? 4 : 2;
+  static constexpr int kBytes = V * kElem;
   uint32_t u[(kBytes + 3) / 4];
   __device__ __forceinline__ void load(const void* p, int64_t i) {
-    if constexpr (kBytes == 2) {
-      u[0] = static_cast<const uint16_t*>(p)[i];
-    } else {
-      const char* s = static_cast<const char*>(p) + i * (kBytes / V);
+    const char* s = static_cast<const char*>(p) + i * kElem;
+    if constexpr (kBytes >= 16) {
 #pragma unroll
-      for (int j = 0; j < kBytes / 4; j += 4) {
-        if constexpr (kBytes >= 16) {
-          const uint4 x = reinterpret_cast<const uint4*>(s)[j / 4];
-          u[j] = x.x; u[j + 1] = x.y; u[j + 2] = x.z; u[j + 3] = x.w;
-        } else if constexpr (kBytes == 8) {
-          const uint2 x = *reinterpret_cast<const uint2*>(s);
-          u[0] = x.x; u[1] = x.y;
-        } else {
-          u[0] = *reinterpret_cast<const uint32_t*>(s);
-        }
+      for (int j = 0; j < kBytes / 16; ++j) {
+        const u32x4 x = get<STREAM, u32x4>(s + 16 * j);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) u[4 * j + k] = x[k];
       }
+    } else if constexpr (kBytes == 8) {
+      const u32x2 x = get<STREAM, u32x2>(s);
+      u[0] = x[0]; u[1] = x[1];
+    } else if constexpr (kBytes == 4) {
+      u[0] = *reinterpret_cast<const uint32_t*>(s);
+    } else {
+      u[0] = *reinterpret_cast<const uint16_t*>(s);
     }
   }
-  __device__ __forceinline__ float get(int j) const {
+  __device__ __forceinline__ void store(void* p, int64_t i) const {
+    char* s = static_cast<char*>(p) + i * kElem;
+    if constexpr (kBytes >= 16) {
+#pragma unroll
+      for (int j = 0; j < kBytes / 16; ++j) put<STREAM>(s + 16 * j, u32x4{u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]});
+    } else if constexpr (kBytes == 8) {
+      put<STREAM>(s, u32x2{u[0], u[1]});
+    } else if constexpr (kBytes == 4) {
+      *reinterpret_cast<uint32_t*>(s) = u[0];
+    } else {
+      *reinterpret_cast<uint16_t*>(s) = static_cast<uint16_t>(u[0]);
+    }
+  }
+  __device__ __forceinline__ float value(int j) const {
     if constexpr (DT == RN_F32) return __uint_as_float(u[j]);
     else return j % 2 ? __uint_as_float(u[j / 2] & 0xffff0000u) : __uint_as_float(u[j / 2] << 16);
+  }
+  __device__ __forceinline__ void set(const float* f) {
+    if constexpr (DT == RN_F32) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) u[j] = __float_as_uint(f[j]);
+    } else if constexpr (V == 1) {
+      u[0] = f32_to_bf16(f[0]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) u[j] = pack_bf16x2(f[2 * j], f[2 * j + 1]);
+    }
   }
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int j = 0; j < (kBytes + 3) / 4; ++j) u[j] = 0;
   }
 };
+template <int DT, int V, bool STREAM = false>
+__device__ __forceinline__ void load(const void* p, int64_t i, float* f) {
+  Raw<DT, V, STREAM> r;
+  r.load(p, i);
+#pragma unroll
+  for (int j = 0; j < V; ++j) f[j] = r.value(j);
+}
+template <int DT, int V, bool STREAM = false>
+__device__ __forceinline__ void store(void* p, int64_t i, const float* f) {
+  Raw<DT, V, STREAM> r;
+  r.set(f);
+  r.store(p, i);
+}
 
 template <int CTRL, int ROWS>
 __device__ __forceinline__ float dpp_or_zero(float x) {
@@ -161,7 +162,7 @@ struct NormArgs {
 };
 
 // Thread `lane` of a row's 64 W lanes holds elements [V (lane + 64 W i), +V) for i < NV.
-template <int IN, int OUT, int V, int W, int NV>
+template <int IN, int OUT, int V, int W, int NV, bool FULL, bool STREAM>
 __global__ void __launch_bounds__(threads(W)) norm_rows(NormArgs a) {
   constexpr int L = 64 * W;
   constexpr int R = threads(W) / L;       // rows per block
@@ -173,9 +174,9 @@ __global__ void __launch_bounds__(threads(W)) norm_rows(NormArgs a) {
     const int c = V * (lane + L * i);
 #pragma unroll
     for (int j = 0; j < V; ++j) { w[i * V + j] = 1.f; b[i * V + j] = 0.f; }
-    if (c < a.d) {
-      if (a.w) Vec<RN_F32, V>::load(a.w, c, w + i * V);
-      if (a.b) Vec<RN_F32, V>::load(a.b, c, b + i * V);
+    if (FULL || c < a.d) {
+      if (a.w) load<RN_F32, V>(a.w, c, w + i * V);
+      if (a.b) load<RN_F32, V>(a.b, c, b + i * V);
     }
   }
   const int64_t step = static_cast<int64_t>(gridDim.x) * R;
@@ -186,15 +187,15 @@ __global__ void __launch_bounds__(threads(W)) norm_rows(NormArgs a) {
       const int c = V * (lane + L * i);
 #pragma unroll
       for (int j = 0; j < V; ++j) h[i * V + j] = 0.f;
-      if (c < a.d) Vec<IN, V>::load(a.x, row * a.xs + c, h + i * V);
+      if (FULL || c < a.d) load<IN, V, STREAM>(a.x, row * a.xs + c, h + i * V);
     }
     if (a.r) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = V * (lane + L * i);
-        if (c < a.d) {
+        if (FULL || c < a.d) {
           float t[V];
-          Vec<IN, V>::load(a.r, row * a.rs + c, t);
+          load<IN, V, STREAM>(a.r, row * a.rs + c, t);
 #pragma unroll
           for (int j = 0; j < V; ++j) h[i * V + j] += t[j];
         }
@@ -204,7 +205,7 @@ __global__ void __launch_bounds__(threads(W)) norm_rows(NormArgs a) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = V * (lane + L * i);
-        if (c < a.d) Vec<IN, V>::store(a.sum, row * a.ss + c, h + i * V);
+        if (FULL || c < a.d) store<IN, V, STREAM>(a.sum, row * a.ss + c, h + i * V);
       }
     }
     float s[1] = {0.f};
@@ -218,18 +219,18 @@ __global__ void __launch_bounds__(threads(W)) norm_rows(NormArgs a) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         h[i * V + j] -= mean;
-        if (V * (lane + L * i) < a.d) s2[0] = fmaf(h[i * V + j], h[i * V + j], s2[0]);
+        if (FULL || V * (lane + L * i) < a.d) s2[0] = fmaf(h[i * V + j], h[i * V + j], s2[0]);
       }
     row_sums<W>(s2, red[1]);
     const float rstd = 1.0f / sqrtf(s2[0] / a.fd + a.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = V * (lane + L * i);
-      if (c < a.d) {
+      if (FULL || c < a.d) {
         float y[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) y[j] = fmaf(h[i * V + j] * rstd, w[i * V + j], b[i * V + j]);
-        Vec<OUT, V>::store(a.out, row * a.os + c, y);
+        store<OUT, V, STREAM>(a.out, row * a.os + c, y);
       }
     }
   }
@@ -238,7 +239,7 @@ __global__ void __launch_bounds__(threads(W)) norm_rows(NormArgs a) {
 // With c = x - mean: the sums of c c, g and g c after the mean are all a row needs (mean(g xh)
 // is rstd mean(g c)), so a row takes two joins of the block. The next row's values are on
 // their way while a row is worked on.
-template <int IN, int OUT, int V, int W, int NV>
+template <int IN, int OUT, int V, int W, int NV, bool FULL, bool STREAM>
 __global__ void __launch_bounds__(threads(W)) norm_rows_backward(NormArgs a) {
   constexpr int L = 64 * W;
   constexpr int R = threads(W) / L;
@@ -249,13 +250,13 @@ __global__ void __launch_bounds__(threads(W)) norm_rows_backward(NormArgs a) {
   float dw[NV * V], db[NV * V];
 #pragma unroll
   for (int i = 0; i < NV * V; ++i) { dw[i] = 0.f; db[i] = 0.f; }
-  Raw<IN, V> rx[NV], rr[NV];
-  Raw<OUT, V> rg[NV];
+  Raw<IN, V, STREAM> rx[NV], rr[NV];
+  Raw<OUT, V, STREAM> rg[NV];
   auto fetch = [&](int64_t row) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = V * (lane + L * i);
-      if (c < a.d) {
+      if (FULL || c < a.d) {
         rx[i].load(a.x, row * a.xs + c);
         rg[i].load(a.dout, row * a.os + c);
         if (a.r) rr[i].load(a.r, row * a.rs + c);
@@ -275,9 +276,9 @@ __global__ void __launch_bounds__(threads(W)) norm_rows_backward(NormArgs a) {
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        x[i * V + j] = rx[i].get(j);
-        g[i * V + j] = rg[i].get(j);
-        t[i * V + j] = rr[i].get(j);
+        x[i * V + j] = rx[i].value(j);
+        g[i * V + j] = rg[i].value(j);
+        t[i * V + j] = rr[i].value(j);
         s[0] += x[i * V + j];
       }
     if (kAhead && row + step < a.rows) fetch(row + step);
@@ -287,11 +288,11 @@ __global__ void __launch_bounds__(threads(W)) norm_rows_backward(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = V * (lane + L * i);
-      if (c < a.d) {
+      if (FULL || c < a.d) {
         float wt[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) wt[j] = 1.f;
-        if (a.w) Vec<RN_F32, V>::load(a.w, c, wt);
+        if (a.w) load<RN_F32, V>(a.w, c, wt);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           const int e = i * V + j;
@@ -310,11 +311,11 @@ __global__ void __launch_bounds__(threads(W)) norm_rows_backward(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = V * (lane + L * i);
-      if (c < a.d) {
+      if (FULL || c < a.d) {
         float wt[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) wt[j] = 1.f;
-        if (a.w) Vec<RN_F32, V>::load(a.w, c, wt);
+        if (a.w) load<RN_F32, V>(a.w, c, wt);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           const int e = i * V + j;
@@ -322,7 +323,7 @@ __global__ void __launch_bounds__(threads(W)) norm_rows_backward(NormArgs a) {
           dw[e] = fmaf(g[e], xh, dw[e]);
           t[e] = fmaf(rstd, g[e] * wt[j] - sg - xh * sgx, t[e]);
         }
-        Vec<IN, V>::store(a.sum, row * a.ss + c, t + i * V);
+        store<IN, V, STREAM>(a.sum, row * a.ss + c, t + i * V);
       }
     }
   }
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(threads(W)) norm_rows_backward(NormArgs a) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           const int c = V * (lane + L * i);
-          if (c < a.d) {
+          if (FULL || c < a.d) {
 #pragma unroll
             for (int j = 0; j < V; ++j) part[static_cast<int64_t>(which) * a.d + c + j] = merge[(i * V + j) * 64 + lane];
           }
@@ -359,9 +360,9 @@ __global__ void __launch_bounds__(threads(W)) norm_rows_backward(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = V * (lane + L * i);
-      if (c < a.d) {
-        Vec<RN_F32, V>::store(part, c, dw + i * V);
-        Vec<RN_F32, V>::store(part + a.d, c, db + i * V);
+      if (FULL || c < a.d) {
+        store<RN_F32, V>(part, c, dw + i * V);
+        store<RN_F32, V>(part + a.d, c, db + i * V);
       }
     }
   }
@@ -396,23 +397,38 @@ int backward_blocks(const NormCall& n) {
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((n.rows + 3) / 4, 768)));
 }
 
-template <int IN, int OUT, int V, int W, int NV>
-hipError_t launch_one(const NormCall& n, NormArgs a, hipStream_t st) {
+template <int IN, int OUT, int V, int W, int NV, bool FULL, bool STREAM>
+hipError_t launch_full(const NormCall& n, NormArgs a, hipStream_t st) {
   if (!n.backward) {
     constexpr int R = threads(W) / (64 * W);
     const int64_t need = (n.rows + R - 1) / R;
-    hipLaunchKernelGGL((norm_rows<IN, OUT, V, W, NV>), dim3(static_cast<unsigned>(std::min<int64_t>(need, 2048))),
+    hipLaunchKernelGGL((norm_rows<IN, OUT, V, W, NV, FULL, STREAM>), dim3(static_cast<unsigned>(std::min<int64_t>(need, 2048))),
                        dim3(threads(W)), 0, st, a);
     return hipGetLastError();
   }
   const int blocks = backward_blocks(n);
-  hipLaunchKernelGGL((norm_rows_backward<IN, OUT, V, W, NV>), dim3(blocks), dim3(threads(W)), 0, st, a);
+  hipLaunchKernelGGL((norm_rows_backward<IN, OUT, V, W, NV, FULL, STREAM>), dim3(blocks), dim3(threads(W)), 0, st, a);
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && a.part) {
     hipLaunchKernelGGL(norm_reduce, dim3((2 * n.d + 31) / 32), dim3(1024), 0, st, a.part, blocks, n.d, n.dw, n.db);
     e = hipGetLastError();
   }
   return e;
+}
+
+// FULL: every lane has all its vectors, so that no access hangs on a condition.
+template <int IN, int OUT, int V, int W, int NV>
+hipError_t launch_one(const NormCall& n, const NormArgs& a, hipStream_t st) {
+  if constexpr (V > 1)
+    if (n.d == V * 64 * W * NV) {
+      // the call's bytes against the 256 MB last-level cache
+      // (16384 x 4096 bf16 with residual: 96 us past the caches, 103 us through them; backward
+      // 108 and 114 us)
+      const int64_t bytes = n.rows * n.d * ((IN == RN_F32 ? 4 : 2) * (n.r ? 2 : 1) + (OUT == RN_F32 ? 4 : 2) + (n.sum ? (IN == RN_F32 ? 4 : 2) : 0));
+      return bytes > (int64_t(256) << 20) ? launch_full<IN, OUT, V, W, NV, true, true>(n, a, st)
+                                          : launch_full<IN, OUT, V, W, NV, true, false>(n, a, st);
+    }
+  return launch_full<IN, OUT, V, W, NV, false, false>(n, a, st);
 }
 
 template <int IN, int OUT>

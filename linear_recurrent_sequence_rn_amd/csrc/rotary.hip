@@ -86,8 +86,10 @@ __device__ __forceinline__ float2 angle(int64_t p, double theta) {
 }
 
 // `lanes` consecutive threads take one head of one token. A unit of work is two pieces of V
-// elements: with HALF one of each half; else neighbours, or, where V is 1, the elements of a
-// pair. Units from `turn` on are copied. The pieces of U heads are in flight.
+// elements, so placed that neighbouring lanes have neighbouring pieces: with HALF one of each
+// half; else, and for the copied rest, one of the first half of the pieces and one of the
+// second (where V is 1: the two elements of a pair). Units from `turn` on are copied. The pieces
+// of U heads are in flight.
 template <int DT, int V, bool HALF>
 __global__ void __launch_bounds__(kThreads) rotary(RotArgs a, int lanes) {
   constexpr int U = 4;
@@ -117,18 +119,22 @@ __global__ void __launch_bounds__(kThreads) rotary(RotArgs a, int lanes) {
   const int per = kThreads / lanes;
   const int h0 = blockIdx.y * a.heads;
   const int nh = min(a.heads, a.H - h0);
-  const int turn = half / V + (!HALF && half % V ? 1 : 0);     // units of turned elements
-  const int units = turn + (a.d - a.rot + 2 * V - 1) / (2 * V);
+  const int turn = (half + V - 1) / V;           // units of turned elements
+  const int copies = (a.d - a.rot + 2 * V - 1) / (2 * V);
+  const int units = turn + copies;
+  const int second = HALF ? half : V == 1 ? 1 : turn * V;      // from a unit's first piece to its other
   // byte offsets of a unit's pieces in its head, and how many it has
   auto pieces = [&](int u, int* x, int* y) {
     if (u < turn) {
-      *x = (HALF ? u * V : 2 * u * V) * E;
-      *y = *x + (HALF ? half : V) * E;
-      return HALF || 2 * u * V + V < a.rot ? 2 : 1;
+      const int e = V == 1 && !HALF ? 2 * u : u * V;
+      *x = e * E;
+      *y = (e + second) * E;
+      return HALF || e + second < a.rot ? 2 : 1;
     }
-    *x = (a.rot + 2 * (u - turn) * V) * E;
-    *y = *x + V * E;
-    return a.rot + 2 * (u - turn) * V + V < a.d ? 2 : 1;
+    const int e = a.rot + (u - turn) * V;
+    *x = e * E;
+    *y = (e + copies * V) * E;
+    return e + copies * V < a.d ? 2 : 1;
   };
   const int qt = per / nh, qh = per - qt * nh;   // a step of `per` heads in (token, head)
   for (int u = lane; u < units; u += lanes) {
@@ -167,13 +173,14 @@ __global__ void __launch_bounds__(kThreads) rotary(RotArgs a, int lanes) {
             float p[2 * V];
             x[k].get(p);
             if (np == 2) y[k].get(p + V);
-            const float2* c = cs + tt[k] * half + u * V;
+            const float2* c = cs + tt[k] * half;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-              // (the pairs of a last single piece end with it)
-              if (HALF || j < V / 2 || V == 1 || np == 2) {
-                const int e = HALF ? j : 2 * j, f = HALF ? j + V : 2 * j + 1;
-                const float2 v = c[j];
+              // pair j of the unit: one element of each piece, or two of one
+              const bool other = !HALF && V > 1 && j >= V / 2;
+              if (!other || np == 2) {
+                const int e = HALF || V == 1 ? j : 2 * j, f = HALF || V == 1 ? j + V : 2 * j + 1;
+                const float2 v = c[HALF || V == 1 ? u * V + j : other ? (u + turn) * (V / 2) + j - V / 2 : u * (V / 2) + j];
                 const float re = p[e], im = p[f];
                 p[e] = re * v.x - im * v.y;
                 p[f] = re * v.y + im * v.x;
@@ -206,9 +213,9 @@ hipError_t launch_t(const RotaryCall& c, RotArgs& a, hipStream_t st) {
   int lanes = 1;
   while (lanes < units && lanes < 64) lanes *= 2;
   // tokens a block: the angles' cost is shared by all heads whatever the tile, so the tile
-  // only has to give every thread work, and 1024 blocks where the call is large enough
+  // only has to give every thread work, and 2048 blocks where the call is large enough
   int tile = std::min(kMaxTile, kTable / half);
-  while (tile > 1 && (a.rows + tile - 1) / tile < 1024) tile /= 2;
+  while (tile > 1 && (a.rows + tile - 1) / tile < 2048) tile /= 2;
   const int64_t tiles = (a.rows + tile - 1) / tile;
   int groups = 1;
   while (tiles * groups < 512 && groups * 2 * (kThreads / lanes) <= tile * a.H) groups *= 2;
