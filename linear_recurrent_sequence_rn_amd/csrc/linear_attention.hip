@@ -3,10 +3,12 @@
 //
 // lin_step: one token a sequence. Bound by HBM: the float32 state is read and written once.
 // lin_recurrent: prompts of any type and head size by the recurrence itself, token by token,
-// the state in registers. Bound by the vector units: three multiply-adds a state element
-// and token. Long sequences are cut into segments: one pass gives the state each
-// segment adds on its own, lin_scan carries the states over the segments, a second pass
-// gives the outputs; the same three passes carry the matrix-core kernel's segments.
+// the state in registers. Bound by the vector units and by LDS, whose broadcast reads of q and k
+// take as long as the three operations a state element and token (padded float32 batch of 3
+// sequences of up to 2001 tokens, 5 heads of 48 x 81: 41 us, of which the scan is 8). Long
+// sequences are cut into segments: one pass gives the state each segment adds on its own, lin_scan
+// carries the states over the segments, a second pass gives the outputs; the same three passes
+// carry the matrix-core kernel's segments.
 #include <algorithm>
 
 #include "linear_attention.h"
@@ -21,7 +23,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 // column vector) takes rows group, group + G, ... in batches of 8, the next batch's loads issued
 // before the present one is updated. Non-temporal: a batch's states are larger than the caches
 // and are read once a step. FULL: every thread has a column and every batch its rows, so that
-// no load hangs on a condition (128 states of 16 heads of 256 x 512: 375 us, 5.7 TB/s; with
+// no load hangs on a condition (128 states of 16 heads of 256 x 512: 357 us, 6.0 TB/s; with
 // conditions and half the columns a block 460 us).
 constexpr int kBatch = 8;
 
@@ -224,27 +226,53 @@ __global__ void __launch_bounds__(256) lin_recurrent(LinArgs a) {
     const int n = min(kTok, t1 - t);
     fetch(t + kTok);
     // tokens behind the last have decay 1 and k = q = v = 0, and change nothing
-#pragma unroll 4
-    for (int i = 0; i < kTok; ++i) {
-      const float dec = gt[i];
-      const float vv = vt[i][lane];
+    auto token = [&](int i, const float4* k4, const float4* q4, float dec, float vv) {
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int r = 0; r < RW; r += 4) {
-        const float4 k4 = *reinterpret_cast<const float4*>(&kt[i][wave * RW + r]);
-        S[r] = fmaf(dec, S[r], k4.x * vv);
-        S[r + 1] = fmaf(dec, S[r + 1], k4.y * vv);
-        S[r + 2] = fmaf(dec, S[r + 2], k4.z * vv);
-        S[r + 3] = fmaf(dec, S[r + 3], k4.w * vv);
+      for (int r = 0; r < RW / 4; ++r) {
+        const float kk[4] = {k4[r].x, k4[r].y, k4[r].z, k4[r].w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) S[4 * r + x] = fmaf(dec, S[4 * r + x], kk[x] * vv);
         if constexpr (MODE != kLinState) {
-          const float4 q4 = *reinterpret_cast<const float4*>(&qt[i][wave * RW + r]);
-          acc[0] = fmaf(q4.x, S[r], acc[0]);
-          acc[1] = fmaf(q4.y, S[r + 1], acc[1]);
-          acc[2] = fmaf(q4.z, S[r + 2], acc[2]);
-          acc[3] = fmaf(q4.w, S[r + 3], acc[3]);
+          const float qq[4] = {q4[r].x, q4[r].y, q4[r].z, q4[r].w};
+#pragma unroll
+          for (int x = 0; x < 4; ++x) acc[x] = fmaf(qq[x], S[4 * r + x], acc[x]);
         }
       }
       if constexpr (MODE != kLinState) part[wave][i][lane] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+    };
+    const float4* kp = reinterpret_cast<const float4*>(&kt[0][wave * RW]);
+    const float4* qp = reinterpret_cast<const float4*>(&qt[0][wave * RW]);
+    if constexpr (RW <= 32) {
+      // A token's values are read from LDS while the one before it is worked on; waited for one by
+      // one they made a 4-token block 27 waits long (that batch: 45.5 us,
+      // now 41.4). At 128 rows the registers that hold them cost waves: 4 heads of 333 tokens,
+      // 128 x 256: 68 -> 50 us, 2 x 8 of 777, 128 x 128: 77 -> 66, but 32 of 2048: 212 -> 241.
+      // 256 rows have no registers for it.
+      float4 ka[RW / 4], qa[RW / 4], kb[RW / 4], qb[RW / 4];
+      float da, va, db, vb;
+      auto read = [&](int i, float4* k4, float4* q4, float& dec, float& vv) {
+        dec = gt[i];
+        vv = vt[i][lane];
+#pragma unroll
+        for (int r = 0; r < RW / 4; ++r) {
+          k4[r] = kp[i * (D / 4) + r];
+          if constexpr (MODE != kLinState) q4[r] = qp[i * (D / 4) + r];
+        }
+      };
+      read(0, ka, qa, da, va);
+#pragma unroll 2
+      for (int i = 0; i < kTok; i += 2) {
+        read(i + 1, kb, qb, db, vb);
+        __builtin_amdgcn_sched_barrier(0);
+        token(i, ka, qa, da, va);
+        read(i + 2 < kTok ? i + 2 : 0, ka, qa, da, va);
+        __builtin_amdgcn_sched_barrier(0);
+        token(i + 1, kb, qb, db, vb);
+      }
+    } else {
+#pragma unroll 4
+      for (int i = 0; i < kTok; ++i) token(i, kp + i * (D / 4), qp + i * (D / 4), gt[i], vt[i][lane]);
     }
     __syncthreads();
     if constexpr (MODE != kLinState) {
