@@ -5,7 +5,10 @@
 // rstd w + b. Backward, with g = dy w and xh = (x - mean) rstd: dx = rstd (g - mean(g) -
 // xh mean(g xh)) + dh, dw = sum_rows dy xh, db = sum_rows dy.
 //
-// Bound by HBM: every tensor is read or written once. A row lives in the registers of one
+// Bound by HBM: every tensor is read or written once (16384 x 4096 bf16: forward with residual
+// 96 us, 5.6 TB/s; backward with the residual's gradient 109 us, 5.0 TB/s; a large copy reaches
+// 4.9 to 5.4 TB/s on the card). Odd widths read element by element and are bound by latency
+// (backward of 3001 x 1537 float32: 27 us). A row lives in the registers of one
 // wave (W = 1, four rows per 256-thread block) or of a whole block (W = 4 or 16), so the passes
 // over it (mean, centred squares, result) cost no memory access. Blocks walk over rows:
 // the weights, and in the backward the column sums of dw and db, then stay in registers
