@@ -3,12 +3,12 @@
 //
 // lin_step: one token a sequence. Bound by HBM: the float32 state is read and written once.
 // lin_recurrent: prompts of any type and head size by the recurrence itself, token by token,
-// the state in registers. Bound by the vector units and by LDS, whose broadcast reads of q and k
-// take as long as the three operations a state element and token (padded float32 batch of 3
-// sequences of up to 2001 tokens, 5 heads of 48 x 81: 41 us, of which the scan is 8). Long
-// sequences are cut into segments: one pass gives the state each segment adds on its own, lin_scan
-// carries the states over the segments, a second pass gives the outputs; the same three passes
-// carry the matrix-core kernel's segments.
+// the state in registers. Bound by the vector units (three operations a state element and token)
+// and by the chain of tokens where few states leave a compute unit one block (padded float32
+// batch of 3 sequences of up to 2001 tokens, 5 heads of 48 x 81: 39 us, of which the scan is 8).
+// Long sequences are cut into segments: one pass gives the state each segment adds on its own,
+// lin_scan carries the states over the segments, a second pass gives the outputs; the same three
+// passes carry the matrix-core kernel's segments.
 #include <algorithm>
 
 #include "linear_attention.h"
@@ -136,12 +136,21 @@ __global__ void __launch_bounds__(NT) lin_step(LinArgs a, int slices) {
 }
 
 // ---- prompts by the recurrence ------------------------------------------------------------
-// A block owns 64 columns of one head's state over one segment of one sequence: lane = column,
-// wave w holds the rows [w RW, (w+1) RW) in registers (rows past d_k stay zero). Tokens come
-// in blocks of 16 through LDS, the next block's loads in flight meanwhile; the four waves'
-// shares of each output meet in LDS.
+// A block owns 64 columns of one head's state over one segment of one sequence, in registers: wave
+// w holds the rows [w RW, (w+1) RW), and each of its lanes RW / 4 rows of 4 neighbouring columns
+// (lane = 4 column quad + row group), so that 16 bytes from LDS feed 16 state elements (rows past
+// d_k stay zero). Tokens come in blocks of 16 through LDS, the next block's loads in flight
+// meanwhile; the four row groups' shares of an output meet by DPP, the waves' in LDS. (One column
+// and RW rows a lane read 16 bytes of LDS for 4 elements and were bound by that: 12 x 16 heads of
+// 212 bf16 tokens, 128 x 81: 218 -> 94 us; 3 heads of 1169 float32 tokens, 192 x 81: 135 -> 65.)
 constexpr int kTok = 16;
 constexpr int kCols = 64;
+
+// the value of the lane whose number differs in bit B of a quad
+template <int B>
+__device__ __forceinline__ float quad_swap(float x) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), B == 1 ? 0xB1 : 0x4E, 0xf, 0xf, true));
+}
 
 template <int IN, int OUT, int RW, LinMode MODE>
 __global__ void __launch_bounds__(256) lin_recurrent(LinArgs a) {
@@ -171,15 +180,31 @@ __global__ void __launch_bounds__(256) lin_recurrent(LinArgs a) {
   if (MODE == kLinWhole ? (len == 0 && !keep) : t0 >= t1) return;
   if (MODE == kLinState && t1 == len && !keep) return;   // nobody reads the last segment's state
 
-  float S[RW];
+  constexpr int RL = RW / 4;
+  const int sub = lane & 3, cq = lane & ~3;
+  auto row = [&](int r) { return wave * RW + (r >> 2) * 16 + sub * 4 + (r & 3); };
+  const bool quads = a.dv % 4 == 0;   // (states are 16-byte aligned)
+  float S[RL][4];
   {
     const float* from = MODE == kLinWhole ? (a.state_in && slot >= 0 ? a.state_in + (static_cast<int64_t>(slot) * a.H + h) * sh : nullptr)
                         : MODE == kLinOut ? a.seg_state + (lin_segment(a, s, row0, seg) * a.H + h) * sh
                                           : nullptr;
 #pragma unroll
-    for (int r = 0; r < RW; ++r) {
-      const int d = wave * RW + r;
-      S[r] = from && d < a.dk && lane < nc ? from[static_cast<int64_t>(d) * a.dv + c0 + lane] : 0.f;
+    for (int r = 0; r < RL; ++r) {
+      const int d = row(r);
+      f32x4 x = {};
+      if (from && d < a.dk) {
+        const float* p = from + (static_cast<int64_t>(d) * a.dv + c0 + cq);
+        if (quads) {
+          if (cq < nc) x = *reinterpret_cast<const f32x4*>(p);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (cq + c < nc) x[c] = p[c];
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) S[r][c] = x[c];
     }
   }
   const int64_t qo = lin_base(a, a.qs, s, row0) + h / (a.H / a.Hq) * a.qs[1];
@@ -189,90 +214,88 @@ __global__ void __launch_bounds__(256) lin_recurrent(LinArgs a) {
   const int64_t oo = lin_base(a, a.os, s, row0) + h * a.os[1] + c0;
 
   float rq[E], rk[E], rv[kTok * kCols / 256], rg = 0.f;
+  // every load is of a token and an element that exist; what should be zero is made so after it
   auto fetch = [&](int t) {
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const int i = tid + 256 * e, tt = t + i / D, d = i % D;
-      const bool ok = tt < t1 && d < a.dk;
-      if constexpr (MODE != kLinState) rq[e] = ok ? Elem<IN>::load(a.q, qo + tt * a.qs[2] + d) : 0.f;
-      rk[e] = ok ? Elem<IN>::load(a.k, ko + tt * a.ks[2] + d) : 0.f;
+      const int i = tid + 256 * e, tt = min(t + i / D, t1 - 1), d = min(i % D, a.dk - 1);
+      if constexpr (MODE != kLinState) rq[e] = Elem<IN>::load(a.q, qo + tt * a.qs[2] + d);
+      rk[e] = Elem<IN>::load(a.k, ko + tt * a.ks[2] + d);
     }
 #pragma unroll
     for (int e = 0; e < kTok * kCols / 256; ++e) {
-      const int i = tid + 256 * e, tt = t + i / kCols, c = i % kCols;
-      rv[e] = tt < t1 && c < nc ? Elem<IN>::load(a.v, vo + tt * a.vs[2] + c) : 0.f;
+      const int i = tid + 256 * e, tt = min(t + i / kCols, t1 - 1), c = min(i % kCols, nc - 1);
+      rv[e] = Elem<IN>::load(a.v, vo + tt * a.vs[2] + c);
     }
-    if (tid < kTok) rg = t + tid < t1 ? a.g[go + (t + tid) * a.gs[2]] : 0.f;
+    rg = a.g[go + min(t + (tid & (kTok - 1)), t1 - 1) * a.gs[2]];
   };
   double gsum = 0.0;
-  fetch(t0);
+  if (t0 < t1) fetch(t0);
   for (int t = t0; t < t1; t += kTok) {
+    const int n = min(kTok, t1 - t);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const int i = tid + 256 * e;
-      if constexpr (MODE != kLinState) qt[i / D][i % D] = rq[e];
-      kt[i / D][i % D] = rk[e];
+      const bool ok = i / D < n && i % D < a.dk;
+      if constexpr (MODE != kLinState) qt[i / D][i % D] = ok ? rq[e] : 0.f;
+      kt[i / D][i % D] = ok ? rk[e] : 0.f;
     }
 #pragma unroll
     for (int e = 0; e < kTok * kCols / 256; ++e) {
       const int i = tid + 256 * e;
-      vt[i / kCols][i % kCols] = rv[e];
+      vt[i / kCols][i % kCols] = i / kCols < n && i % kCols < nc ? rv[e] : 0.f;
     }
     if (tid < kTok) {
-      gt[tid] = expf(rg);
-      gsum += rg;
+      gt[tid] = tid < n ? expf(rg) : 1.f;
+      gsum += tid < n ? rg : 0.f;
     }
     __syncthreads();
-    const int n = min(kTok, t1 - t);
-    fetch(t + kTok);
-    // tokens behind the last have decay 1 and k = q = v = 0, and change nothing
-    auto token = [&](int i, const float4* k4, const float4* q4, float dec, float vv) {
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    if (t + kTok < t1) fetch(t + kTok);
+    // A token's values are read from LDS while the one before it is worked on. (Tokens behind the
+    // last have decay 1 and k = q = v = 0, and change nothing.)
+    struct Token { float4 k[RL / 4], q[RL / 4], v; float dec; } ta, tb;
+    auto read = [&](int i, Token& x) {
+      x.dec = gt[i];
+      x.v = *reinterpret_cast<const float4*>(&vt[i][cq]);
 #pragma unroll
-      for (int r = 0; r < RW / 4; ++r) {
-        const float kk[4] = {k4[r].x, k4[r].y, k4[r].z, k4[r].w};
-#pragma unroll
-        for (int x = 0; x < 4; ++x) S[4 * r + x] = fmaf(dec, S[4 * r + x], kk[x] * vv);
-        if constexpr (MODE != kLinState) {
-          const float qq[4] = {q4[r].x, q4[r].y, q4[r].z, q4[r].w};
-#pragma unroll
-          for (int x = 0; x < 4; ++x) acc[x] = fmaf(qq[x], S[4 * r + x], acc[x]);
-        }
+      for (int j = 0; j < RL / 4; ++j) {
+        x.k[j] = *reinterpret_cast<const float4*>(&kt[i][wave * RW + 16 * j + 4 * sub]);
+        if constexpr (MODE != kLinState) x.q[j] = *reinterpret_cast<const float4*>(&qt[i][wave * RW + 16 * j + 4 * sub]);
       }
-      if constexpr (MODE != kLinState) part[wave][i][lane] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
     };
-    const float4* kp = reinterpret_cast<const float4*>(&kt[0][wave * RW]);
-    const float4* qp = reinterpret_cast<const float4*>(&qt[0][wave * RW]);
-    if constexpr (RW <= 32) {
-      // A token's values are read from LDS while the one before it is worked on; waited for one by
-      // one they made a 4-token block 27 waits long (that batch: 45.5 us,
-      // now 41.4). At 128 rows the registers that hold them cost waves: 4 heads of 333 tokens,
-      // 128 x 256: 68 -> 50 us, 2 x 8 of 777, 128 x 128: 77 -> 66, but 32 of 2048: 212 -> 241.
-      // 256 rows have no registers for it.
-      float4 ka[RW / 4], qa[RW / 4], kb[RW / 4], qb[RW / 4];
-      float da, va, db, vb;
-      auto read = [&](int i, float4* k4, float4* q4, float& dec, float& vv) {
-        dec = gt[i];
-        vv = vt[i][lane];
+    auto work = [&](int i, const Token& x) {
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      const float v[4] = {x.v.x, x.v.y, x.v.z, x.v.w};
 #pragma unroll
-        for (int r = 0; r < RW / 4; ++r) {
-          k4[r] = kp[i * (D / 4) + r];
-          if constexpr (MODE != kLinState) q4[r] = qp[i * (D / 4) + r];
-        }
-      };
-      read(0, ka, qa, da, va);
-#pragma unroll 2
-      for (int i = 0; i < kTok; i += 2) {
-        read(i + 1, kb, qb, db, vb);
-        __builtin_amdgcn_sched_barrier(0);
-        token(i, ka, qa, da, va);
-        read(i + 2 < kTok ? i + 2 : 0, ka, qa, da, va);
-        __builtin_amdgcn_sched_barrier(0);
-        token(i + 1, kb, qb, db, vb);
+      for (int j = 0; j < RL / 4; ++j) {
+        const float k[4] = {x.k[j].x, x.k[j].y, x.k[j].z, x.k[j].w};
+        const float q[4] = {x.q[j].x, x.q[j].y, x.q[j].z, x.q[j].w};
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float& st = S[4 * j + r][c];
+            st = fmaf(x.dec, st, k[r] * v[c]);
+            if constexpr (MODE != kLinState) acc[c] = fmaf(q[r], st, acc[c]);
+          }
       }
-    } else {
-#pragma unroll 4
-      for (int i = 0; i < kTok; ++i) token(i, kp + i * (D / 4), qp + i * (D / 4), gt[i], vt[i][lane]);
+      if constexpr (MODE != kLinState) {
+        // the sum over the quad's lanes; lane i of a quad keeps column i
+        const bool b1 = lane & 2, b0 = lane & 1;
+        const float u0 = (b1 ? acc[2] : acc[0]) + quad_swap<2>(b1 ? acc[0] : acc[2]);
+        const float u1 = (b1 ? acc[3] : acc[1]) + quad_swap<2>(b1 ? acc[1] : acc[3]);
+        part[wave][i][lane] = (b0 ? u1 : u0) + quad_swap<1>(b0 ? u0 : u1);
+      }
+    };
+    read(0, ta);
+#pragma unroll 2
+    for (int i = 0; i < kTok; i += 2) {
+      read(i + 1, tb);
+      __builtin_amdgcn_sched_barrier(0);
+      work(i, ta);
+      read(i + 2 < kTok ? i + 2 : 0, ta);
+      __builtin_amdgcn_sched_barrier(0);
+      work(i + 1, tb);
     }
     __syncthreads();
     if constexpr (MODE != kLinState) {
@@ -295,11 +318,21 @@ __global__ void __launch_bounds__(256) lin_recurrent(LinArgs a) {
     for (int o = 8; o >= 1; o >>= 1) gsum += __shfl_xor(gsum, o, 16);
     if (c0 == 0 && tid == 0) a.seg_decay[i] = expf(static_cast<float>(gsum));
   }
-  if (to && lane < nc) {
+  if (to) {
 #pragma unroll
-    for (int r = 0; r < RW; ++r) {
-      const int d = wave * RW + r;
-      if (d < a.dk) to[static_cast<int64_t>(d) * a.dv + c0 + lane] = S[r];
+    for (int r = 0; r < RL; ++r) {
+      const int d = row(r);
+      if (d < a.dk) {
+        float* p = to + (static_cast<int64_t>(d) * a.dv + c0 + cq);
+        if (quads) {
+          const f32x4 x = {S[r][0], S[r][1], S[r][2], S[r][3]};
+          if (cq < nc) *reinterpret_cast<f32x4*>(p) = x;
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (cq + c < nc) p[c] = S[r][c];
+        }
+      }
     }
   }
 }
@@ -355,6 +388,7 @@ hipError_t launch_recurrent_t(const LinArgs& a, hipStream_t st) {
   const int rw = (a.dk + 3) / 4;
   if (rw <= 16) hipLaunchKernelGGL((lin_recurrent<IN, OUT, 16, MODE>), grid, dim3(256), 0, st, a);
   else if (rw <= 32) hipLaunchKernelGGL((lin_recurrent<IN, OUT, 32, MODE>), grid, dim3(256), 0, st, a);
+  else if (rw <= 48) hipLaunchKernelGGL((lin_recurrent<IN, OUT, 48, MODE>), grid, dim3(256), 0, st, a);
   else hipLaunchKernelGGL((lin_recurrent<IN, OUT, 64, MODE>), grid, dim3(256), 0, st, a);
   return hipGetLastError();
 }
