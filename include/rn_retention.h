@@ -459,7 +459,8 @@ typedef struct rn_rotary_desc {
 
 /*
  * q [B, H_q, N, d], k [B, H_k, N, d] (any strides) -> q_out, k_out. An output may be its own
- * input (same pointer and strides): then the coordinates past `rot` are not touched.
+ * input (same pointer and strides; the coordinates past `rot` are then not touched), and overlaps
+ * nothing else.
  * pos: DEVICE int64, 8-byte aligned: NULL (token t of every row sits at pos0 + t), [B] (at
  * pos[b] + t), or [B, N] with RN_ROTARY_POS_TOKEN. Values are not checked (they move no
  * memory access); |p| <= 2^40 keeps the angles accurate.

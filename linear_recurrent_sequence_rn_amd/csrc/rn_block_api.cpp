@@ -150,6 +150,12 @@ rn_status check_linear_ptrs(const rn_linear_desc* d, const int32_t* slots, const
   return RN_OK;
 }
 
+// Blocks read q, k and v while others write out.
+rn_status check_apart(const rn::LinCall& c) {
+  if (c.out == c.q || c.out == c.k || c.out == c.v) return fail(RN_ERR_INVALID_ARG, "out must not be q, k or v");
+  return RN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -248,6 +254,7 @@ rn_status rn_rotary(const rn_rotary_desc* desc, const int64_t* pos, const void* 
     if (k == k_out && std::memcmp(d->k_stride, d->k_out_stride, sizeof(d->k_stride)))
       return fail(RN_ERR_INVALID_ARG, "k in place needs equal strides");
     if (q_out == k_out) return fail(RN_ERR_INVALID_ARG, "q_out and k_out must differ");
+    if (q_out == k || k_out == q) return fail(RN_ERR_INVALID_ARG, "an output may only be its own input");
   }
   rn::RotaryCall c;
   c.B = d->B; c.N = d->N; c.Hq = d->H_q; c.Hk = d->H_k; c.d = d->d; c.rot = d->rot; c.dt = d->dtype;
@@ -313,6 +320,7 @@ rn_status rn_linear_attention_chunked(const rn_linear_desc* desc, const int32_t*
   if (!aligned(state_in, 16) || !aligned(state_out, 16))
     return fail(RN_ERR_INVALID_ARG, "states must be 16-byte aligned");
   if ((s = check_workspace(workspace, workspace_bytes, rn_linear_attention_workspace_bytes(desc))) != RN_OK) return s;
+  if ((s = check_apart(c)) != RN_OK) return s;
   c.cu = cu_seqlens; c.lens = lengths; c.state_in = state_in; c.state_out = state_out; c.ws = workspace;
   rn::clear_error();
   return hip_status(rn::launch_linear_chunked(c, static_cast<hipStream_t>(stream)), "linear attention launch");
@@ -326,6 +334,7 @@ rn_status rn_linear_attention_step(const rn_linear_desc* desc, const int32_t* sl
   if ((s = check_linear_ptrs(desc, slots, q, k, v, log_decay, out, &c)) != RN_OK) return s;
   if (!state) return fail(RN_ERR_INVALID_ARG, "state pointer is NULL");
   if (!aligned(state, 16)) return fail(RN_ERR_INVALID_ARG, "state must be 16-byte aligned");
+  if ((s = check_apart(c)) != RN_OK) return s;
   c.state_out = state;
   rn::clear_error();
   return hip_status(rn::launch_linear_step(c, static_cast<hipStream_t>(stream)), "linear attention step launch");

@@ -203,3 +203,14 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes():
         rn.rn_linear_attention_chunked(z, z, z, torch.zeros(1, 2, 3))
     with pytest.raises(ValueError):
         rn.rn_linear_attention_step(z, z, z, torch.zeros(1, 2, 3), torch.zeros(1, 2, 8, 8))
+
+
+def test_outputs_that_are_other_inputs_are_refused():
+    """Blocks read what others would overwrite: an output that is another operand's input."""
+    d = rot()
+    assert rotary(d, q=FAKE, k=2 * FAKE, qo=2 * FAKE) == INV and b"own input" in L.rn_last_error()
+    assert rotary(d, q=FAKE, k=2 * FAKE, ko=FAKE) == INV and b"own input" in L.rn_last_error()
+    d = lin()
+    for kw in (dict(out=FAKE), dict(q=5 * FAKE, out=FAKE)):         # (k and v are FAKE)
+        assert chunked(d, **kw) == INV and b"must not be q, k or v" in L.rn_last_error()
+    assert step(lin(N=1), q=5 * FAKE, out=5 * FAKE) == INV and b"must not be q, k or v" in L.rn_last_error()
