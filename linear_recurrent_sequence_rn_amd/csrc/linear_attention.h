@@ -6,7 +6,9 @@ namespace rn {
 
 // Where a kernel starts and ends: a whole sequence; the state a segment adds on its own
 // (first pass over a sequence cut into segments); the outputs of a segment whose starting
-// state the scan left in the workspace (third pass).
+// state the scan left in the workspace (third pass). Where the sequences' lengths are not known
+// and most may be of one segment (`flat`), the third pass is of the first kind: it takes such
+// sequences whole, and the other two leave them out.
 enum LinMode : int { kLinWhole = 0, kLinState = 1, kLinOut = 2 };
 
 struct LinArgs {
@@ -16,6 +18,7 @@ struct LinArgs {
   int64_t T;                  // packed rows, 0 for a padded batch
   float scale;
   bool zero_rest;
+  bool flat;                  // blocks along a packed batch's segments, not sequences x n_seg
   int64_t qs[3], ks[3], vs[3], gs[3], os[3];
   const int32_t* cu;
   const int32_t* lens;
@@ -72,13 +75,42 @@ __device__ __forceinline__ int lin_slot(const LinArgs& a, int s) {
 __device__ __forceinline__ int64_t lin_segment(const LinArgs& a, int s, int64_t row0, int g) {
   return a.T > 0 ? row0 / a.seg_len + s + g : static_cast<int64_t>(s) * a.n_seg + g;
 }
+// The segment and sequence of a block. In a flat grid, block w has the workspace row w: sequence
+// s has those from lin_segment(s, 0) on up to the next one's, found by bisection. False: none.
+__device__ __forceinline__ bool lin_place(const LinArgs& a, int* s, int* seg) {
+  if (!a.flat) {
+    *s = blockIdx.z;
+    *seg = blockIdx.y;
+    return true;
+  }
+  const int64_t w = blockIdx.y + static_cast<int64_t>(blockIdx.z) * gridDim.y;
+  auto first = [&](int i) { return min(max(static_cast<int64_t>(a.cu[i]), int64_t(0)), a.T) / a.seg_len + i; };
+  int lo = 0, hi = a.S;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (first(mid) <= w) lo = mid;
+    else hi = mid - 1;
+  }
+  const int64_t g = w - first(lo);
+  *s = lo;
+  *seg = static_cast<int>(g);
+  return g >= 0;                // (past the sequence's tokens: rows to be zeroed, or nothing)
+}
+// The grid of a pass, with x blocks along heads and columns; `rest`: for the rows behind a packed
+// batch's last sequence too.
+inline dim3 lin_grid(const LinArgs& a, int x, bool rest) {
+  if (!a.flat) return dim3(x, a.n_seg, a.S + (rest ? 1 : 0));
+  const int64_t all = a.T / a.seg_len + a.S + 1, y = all < 65535 ? all : 65535;
+  return dim3(x, static_cast<unsigned>(y), static_cast<unsigned>((all + y - 1) / y));
+}
 // Zeros into the columns [c0, c0 + nc) of head h in the rows of sequence s behind its tokens
 // (flag RN_LINEAR_ZERO_REST); the blocks of its segments share them.
 template <int OUT>
 __device__ __forceinline__ void lin_zero_rest(const LinArgs& a, int s, int g, int h, int c0, int nc,
                                               int64_t row0, int len, int64_t own) {
   const int64_t base = (a.T > 0 ? row0 * a.os[2] : s * a.os[0]) + h * a.os[1] + c0;
-  const int64_t step = static_cast<int64_t>(a.n_seg) * a.seg_len;
+  const int64_t blocks = a.flat ? (row0 + own) / a.seg_len - row0 / a.seg_len + 1 : a.n_seg;
+  const int64_t step = blocks * a.seg_len;
   for (int64_t t0 = len + static_cast<int64_t>(g) * a.seg_len; t0 < own; t0 += step) {
     const int64_t n = min(own - t0, static_cast<int64_t>(a.seg_len)) * nc;
     for (int64_t i = threadIdx.x; i < n; i += blockDim.x)

@@ -164,7 +164,8 @@ __global__ void __launch_bounds__(256) lin_recurrent(LinArgs a) {
   int h, c0;
   lin_block(a, blockIdx.x, &h, &c0);
   c0 *= kCols;
-  const int seg = blockIdx.y, s = blockIdx.z;
+  int seg, s;
+  if (!lin_place(a, &s, &seg)) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int nc = min(kCols, a.dv - c0);
   int64_t row0, own;
@@ -172,13 +173,14 @@ __global__ void __launch_bounds__(256) lin_recurrent(LinArgs a) {
   lin_span(a, s, &row0, &len, &own);
   if (MODE != kLinState && a.zero_rest) lin_zero_rest<OUT>(a, s, seg, h, c0, nc, row0, len, own);
   if (s == a.S) return;
-  const int t0 = seg * a.seg_len;
+  const int t0 = min(seg, a.n_seg) * a.seg_len;
   const int t1 = min(len, t0 + a.seg_len);
   const int slot = lin_slot(a, s);
   const int64_t sh = static_cast<int64_t>(a.dk) * a.dv;
   const bool keep = a.state_out && slot >= 0;
-  if (MODE == kLinWhole ? (len == 0 && !keep) : t0 >= t1) return;
-  if (MODE == kLinState && t1 == len && !keep) return;   // nobody reads the last segment's state
+  const bool one = len <= a.seg_len;      // (always, where kLinWhole is the only pass)
+  if (t0 >= t1 && !(MODE == kLinWhole && seg == 0 && keep)) return;
+  if (MODE == kLinState && t1 == len && (!keep || (a.flat && one))) return;   // nobody reads the last segment's state
 
   constexpr int RL = RW / 4;
   const int sub = lane & 3, cq = lane & ~3;
@@ -186,9 +188,9 @@ __global__ void __launch_bounds__(256) lin_recurrent(LinArgs a) {
   const bool quads = a.dv % 4 == 0;   // (states are 16-byte aligned)
   float S[RL][4];
   {
-    const float* from = MODE == kLinWhole ? (a.state_in && slot >= 0 ? a.state_in + (static_cast<int64_t>(slot) * a.H + h) * sh : nullptr)
-                        : MODE == kLinOut ? a.seg_state + (lin_segment(a, s, row0, seg) * a.H + h) * sh
-                                          : nullptr;
+    const float* from = MODE == kLinState ? nullptr
+                        : MODE == kLinOut || !one ? a.seg_state + (lin_segment(a, s, row0, seg) * a.H + h) * sh
+                        : a.state_in && slot >= 0 ? a.state_in + (static_cast<int64_t>(slot) * a.H + h) * sh : nullptr;
 #pragma unroll
     for (int r = 0; r < RL; ++r) {
       const int d = row(r);
@@ -309,7 +311,7 @@ __global__ void __launch_bounds__(256) lin_recurrent(LinArgs a) {
     }
   }
   float* to = nullptr;
-  if (MODE == kLinWhole && keep) to = a.state_out + (static_cast<int64_t>(slot) * a.H + h) * sh;
+  if (MODE == kLinWhole && keep && one) to = a.state_out + (static_cast<int64_t>(slot) * a.H + h) * sh;
   if (MODE == kLinState) {
     const int64_t i = lin_segment(a, s, row0, seg) * a.H + h;
     to = a.seg_state + i * sh;
@@ -352,6 +354,7 @@ __global__ void __launch_bounds__(256) lin_scan(LinArgs a) {
   lin_span(a, s, &row0, &len, &own);
   const int slot = lin_slot(a, s);
   const int n = (len + a.seg_len - 1) / a.seg_len;
+  if (a.flat && n <= 1) return;
   const int64_t at = (static_cast<int64_t>(slot) * a.H + h) * sh + e;
   fv x = {};
   if (a.state_in && slot >= 0) x = *reinterpret_cast<const fv*>(a.state_in + at);
@@ -384,7 +387,7 @@ template <int IN, int OUT, LinMode MODE>
 hipError_t launch_recurrent_t(const LinArgs& a, hipStream_t st) {
   const int slices = (a.dv + kCols - 1) / kCols;
   const bool rest = a.T > 0 && a.zero_rest && MODE != kLinState;
-  const dim3 grid(a.H * slices, a.n_seg, a.S + (rest ? 1 : 0));
+  const dim3 grid = lin_grid(a, a.H * slices, rest);
   const int rw = (a.dk + 3) / 4;
   if (rw <= 16) hipLaunchKernelGGL((lin_recurrent<IN, OUT, 16, MODE>), grid, dim3(256), 0, st, a);
   else if (rw <= 32) hipLaunchKernelGGL((lin_recurrent<IN, OUT, 32, MODE>), grid, dim3(256), 0, st, a);
@@ -436,7 +439,7 @@ LinArgs lin_args(const LinCall& c) {
   }
   a.cu = c.cu; a.lens = c.lens; a.slots = c.slots;
   a.q = c.q; a.k = c.k; a.v = c.v; a.g = c.g; a.state_in = c.state_in; a.state_out = c.state_out; a.out = c.out;
-  a.seg_len = c.N; a.n_seg = 1; a.seg_state = nullptr; a.seg_decay = nullptr;
+  a.seg_len = c.N; a.n_seg = 1; a.flat = false; a.seg_state = nullptr; a.seg_decay = nullptr;
   return a;
 }
 
@@ -499,6 +502,9 @@ hipError_t launch_linear_chunked(const LinCall& c, hipStream_t st) {
   segments(c, &a.seg_len, &a.n_seg);
   const bool mfma = mfma_call(c);
   if (a.n_seg == 1) return mfma ? launch_lin_mfma(a, kLinWhole, st) : launch_recurrent<kLinWhole>(a, c.in_dt, c.out_dt, st);
+  // Where N says little about the lengths (256 packed sequences of 224 tokens and no nearer bound
+  // than the 57344 tokens of all, 16 heads of 64 x 64: FIG us).
+  a.flat = c.T > 0 && static_cast<int64_t>(c.S) * a.n_seg > 2 * (c.T / a.seg_len + c.S + 1);
   const size_t rows = static_cast<size_t>(total_segments(c, a.seg_len, a.n_seg)) * c.H;
   a.seg_decay = static_cast<float*>(c.ws);
   a.seg_state = a.seg_decay + ((rows + 63) & ~size_t(63));
@@ -509,6 +515,7 @@ hipError_t launch_linear_chunked(const LinCall& c, hipStream_t st) {
   else
     hipLaunchKernelGGL(lin_scan<1>, dim3((c.dk * c.dv + 255) / 256, c.H, c.S), dim3(256), 0, st, a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (a.flat) return mfma ? launch_lin_mfma(a, kLinWhole, st) : launch_recurrent<kLinWhole>(a, c.in_dt, c.out_dt, st);
   return mfma ? launch_lin_mfma(a, kLinOut, st) : launch_recurrent<kLinOut>(a, c.in_dt, c.out_dt, st);
 }
 

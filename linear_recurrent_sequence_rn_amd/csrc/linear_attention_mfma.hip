@@ -237,7 +237,8 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
   int h, c0;
   lin_block(a, blockIdx.x, &h, &c0);
   c0 *= DV;
-  const int seg = blockIdx.y, s = blockIdx.z;
+  int seg, s;
+  if (!lin_place(a, &s, &seg)) return;
   const int tid = threadIdx.x;
   const int lane = tid & 63, l16 = lane & 15, g4 = (lane >> 4) * 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -251,20 +252,21 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
   lin_span(a, s, &row0, &len, &own);
   if (kOut && a.zero_rest) lin_zero_rest<RN_BF16>(a, s, seg, h, c0, nc, row0, len, own);
   if (s == a.S) return;
-  const int t0 = seg * a.seg_len, t1 = min(len, t0 + a.seg_len);
+  const int t0 = min(seg, a.n_seg) * a.seg_len, t1 = min(len, t0 + a.seg_len);
   const int slot = lin_slot(a, s);
   const bool keep = a.state_out && slot >= 0;
-  if (MODE == kLinWhole ? (len == 0 && !keep) : t0 >= t1) return;
-  if (MODE == kLinState && t1 == len && !keep) return;   // nobody reads the last segment's state
+  const bool one = len <= a.seg_len;      // (always, where kLinWhole is the only pass)
+  if (t0 >= t1 && !(MODE == kLinWhole && seg == 0 && keep)) return;
+  if (MODE == kLinState && t1 == len && (!keep || (a.flat && one))) return;   // nobody reads the last segment's state
 
   const int64_t sh = static_cast<int64_t>(a.dk) * a.dv;
   const int vcol = c0 + wv * CW + l16;                   // this lane's state columns: vcol + 16 j
   const int drow = wd * (DK / DW);                       // and rows: drow + 16 i + g4 + r
   f32x4 S[AT][VT];
   {
-    const float* from = MODE == kLinWhole ? (a.state_in && slot >= 0 ? a.state_in + (static_cast<int64_t>(slot) * a.H + h) * sh : nullptr)
-                        : MODE == kLinOut ? a.seg_state + (lin_segment(a, s, row0, seg) * a.H + h) * sh
-                                          : nullptr;
+    const float* from = MODE == kLinState ? nullptr
+                        : MODE == kLinOut || !one ? a.seg_state + (lin_segment(a, s, row0, seg) * a.H + h) * sh
+                        : a.state_in && slot >= 0 ? a.state_in + (static_cast<int64_t>(slot) * a.H + h) * sh : nullptr;
 #pragma unroll
     for (int i = 0; i < AT; ++i)
 #pragma unroll
@@ -576,7 +578,7 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
   if constexpr (kOut)
     if (t0 < t1) store_out(t0 + (t1 - t0 - 1) / kChunk * kChunk);
   float* to = nullptr;
-  if (MODE == kLinWhole && keep) to = a.state_out + (static_cast<int64_t>(slot) * a.H + h) * sh;
+  if (MODE == kLinWhole && keep && one) to = a.state_out + (static_cast<int64_t>(slot) * a.H + h) * sh;
   if (MODE == kLinState) {
     const int64_t i = lin_segment(a, s, row0, seg) * a.H + h;
     to = a.seg_state + i * sh;
@@ -606,7 +608,7 @@ template <int DK, int CW, int VW, int DW, LinMode MODE>
 hipError_t launch_t(const LinArgs& a, hipStream_t st) {
   const int slices = (a.dv + VW * CW - 1) / (VW * CW);
   const bool rest = a.T > 0 && a.zero_rest && MODE != kLinState;
-  const dim3 grid(a.H * slices, a.n_seg, a.S + (rest ? 1 : 0)), block(64 * VW * DW);
+  const dim3 grid = lin_grid(a, a.H * slices, rest), block(64 * VW * DW);
   hipLaunchKernelGGL((lin_chunks<DK, CW, VW, DW, MODE>), grid, block, 0, st, a);
   return hipGetLastError();
 }

@@ -423,3 +423,67 @@ def test_refusals():
         st(*one, S[:1])
     with pytest.raises(ValueError):
         st(*one, S, slots=i32(0))
+
+
+@pytest.mark.parametrize("kind,dk,dv", [("f32", 33, 24), ("bf16", 64, 64), ("bf16", 256, 96)])
+@pytest.mark.parametrize("longest", [300, 2100])
+def test_many_packed_sequences_without_a_bound(kind, dk, dv, longest):
+    """Forty sequences, most of one segment or none, one longer, with no nearer bound on their
+    lengths than the rows of all: outputs, states (in place, in a pool, some without a slot), the
+    sequences without tokens and the rows behind the last; then an out that is given, and a bound
+    that cuts the longest sequence."""
+    gen = np.random.default_rng(21)
+    S, H = 40, 2
+    lens = gen.integers(0, 60, S)
+    lens[[0, 7, 39]] = 0
+    lens[11] = longest
+    T = int(lens.sum()) + 70
+    q, k, v, g = inputs(1, H, 1, H, 2, T, dk, dv, kind, 22, True)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device=DEV)
+    e = int(lens.sum())
+    for t in (q, k, v, g):
+        t[:, :, e:] = float("nan")
+    pool = torch.randn(S + 2, H, dk, dv, device=DEV, generator=torch.Generator(DEV).manual_seed(8))
+    before = pool.clone()
+    order = gen.permutation(S + 2)[:S].astype(np.int32)
+    order[[3, 11 if longest < 1000 else 12]] = -1
+    slots = torch.tensor(order, device=DEV)
+    out, _ = rn().rn_linear_attention_chunked(q, k, v, g, cu_seqlens=cu, state_in=pool, state_out=pool, slots=slots)
+    assert (out[:, :, e:] == 0.0).all()
+    for s in range(S):
+        a, b, slot = int(cu[s]), int(cu[s + 1]), int(order[s])
+        if b > a:
+            check_sequence(out[0, :, a:b], pool[slot] if slot >= 0 else None, q[0, :, a:b], k[0, :, a:b], v[0, :, a:b],
+                           g[0, :, a:b], 1.0, before[slot] if slot >= 0 else None, uses_mfma(kind, DT[kind], dk, dv, False))
+        elif slot >= 0:
+            assert torch.equal(pool[slot], before[slot])
+    for i in set(range(S + 2)) - set(order.tolist()):
+        assert torch.equal(pool[i], before[i])
+    mine = torch.full_like(out, 7.0)
+    _, new = rn().rn_linear_attention_chunked(q, k, v, g, cu_seqlens=cu, state_out=True, out=mine)
+    assert (mine[:, :, e:] == 7.0).all() and int(torch.count_nonzero(new[7])) == 0
+    a = int(cu[11])
+    stop = longest - 100
+    cut, _ = rn().rn_linear_attention_chunked(q, k, v, g, cu_seqlens=cu, max_len=stop, state_out=True)
+    assert (cut[:, :, a + stop:a + longest] == 0.0).all() and (cut[:, :, e:] == 0.0).all()
+    check_sequence(cut[0, :, a:a + stop], None, q[0, :, a:a + stop], k[0, :, a:a + stop], v[0, :, a:a + stop],
+                   g[0, :, a:a + stop], 1.0, None, uses_mfma(kind, DT[kind], dk, dv, False))
+
+
+def test_flat_grid_without_tokens_and_with_disordered_bounds():
+    """Every sequence without tokens; entries outside the tensors and out of order: nothing is
+    written outside."""
+    H, dk, dv, T, S = 2, 64, 64, 2000, 50
+    q, k, v, g = inputs(1, H, H, H, H, T, dk, dv, "bf16", 23, True)
+    none = torch.zeros(S + 1, dtype=torch.int32, device=DEV)
+    s0 = torch.randn(S, H, dk, dv, device=DEV, generator=torch.Generator(DEV).manual_seed(9))
+    out, new = rn().rn_linear_attention_chunked(q, k, v, g, cu_seqlens=none, state_in=s0, state_out=True)
+    assert int(torch.count_nonzero(out)) == 0 and torch.equal(new, s0)
+    guard = torch.full((T + 200, H, dv), 7.0, dtype=torch.bfloat16, device=DEV)
+    o = guard[100:100 + T].transpose(0, 1)[None]
+    bad = np.random.default_rng(24).integers(-3000, 5000, S + 1).astype(np.int32)
+    for generic in (True, False):
+        rn().rn_linear_attention_chunked(q, k, v, g, cu_seqlens=torch.tensor(bad, device=DEV), out=o, state_out=True,
+                                         force_generic=generic)
+    torch.cuda.synchronize()
+    assert (guard[:100] == 7.0).all() and (guard[100 + T:] == 7.0).all()
