@@ -439,7 +439,7 @@ def rn_linear_attention_chunked(q, k, v, log_decay, *, qk_scale=1.0, lengths=Non
     (<= 0; -inf clears the state; a stride of 0 along N gives one decay per head). H_q, H_k and
     H_v divide H. Padded batch: ``lengths`` device int32 [B] or None. Packed batch: B = 1 and
     ``cu_seqlens`` device int32 [S + 1], first entry 0. ``max_len``: no sequence is longer (host
-    number; longer ones are cut). Rows of no sequence are not written (zero in a new out).
+    number; longer ones are cut); many short packed sequences run best with it. Rows of no sequence are not written (zero in a new out).
     state_in, state_out: float32 [S, H, d_k, d_v], or pools [slots, H, d_k, d_v] with ``slots``
     device int32 [S] (distinct; -1: start from zeros, keep nothing); state_out may be True (new;
     not with slots), None/False (discarded) or state_in itself."""

@@ -75,8 +75,24 @@ __device__ __forceinline__ int lin_slot(const LinArgs& a, int s) {
 __device__ __forceinline__ int64_t lin_segment(const LinArgs& a, int s, int64_t row0, int g) {
   return a.T > 0 ? row0 / a.seg_len + s + g : static_cast<int64_t>(s) * a.n_seg + g;
 }
+// The last of the sequences 0 .. S of a packed batch that a predicate holds for, which holds up to
+// one of them (whatever it says, one of them): a lane a candidate.
+template <class F>
+__device__ __forceinline__ int lin_last(const LinArgs& a, F holds) {
+  int lo = 0;
+  for (int n = a.S + 1; n > 1;) {
+    const int each = (n + 63) / 64, at = static_cast<int>(threadIdx.x & 63) * each;
+    const int k = 63 - __clzll(__ballot(at < n && holds(lo + at)) | 1);
+    lo += k * each;
+    n = min(each, n - k * each);
+  }
+  return lo;
+}
+__device__ __forceinline__ int64_t lin_first(const LinArgs& a, int s) {
+  return min(max(static_cast<int64_t>(a.cu[s]), int64_t(0)), a.T);
+}
 // The segment and sequence of a block. In a flat grid, block w has the workspace row w: sequence
-// s has those from lin_segment(s, 0) on up to the next one's, found by bisection. False: none.
+// s has those from lin_segment(s, 0) on up to the next one's. False: none.
 __device__ __forceinline__ bool lin_place(const LinArgs& a, int* s, int* seg) {
   if (!a.flat) {
     *s = blockIdx.z;
@@ -84,13 +100,8 @@ __device__ __forceinline__ bool lin_place(const LinArgs& a, int* s, int* seg) {
     return true;
   }
   const int64_t w = blockIdx.y + static_cast<int64_t>(blockIdx.z) * gridDim.y;
-  auto first = [&](int i) { return min(max(static_cast<int64_t>(a.cu[i]), int64_t(0)), a.T) / a.seg_len + i; };
-  int lo = 0, hi = a.S;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    if (first(mid) <= w) lo = mid;
-    else hi = mid - 1;
-  }
+  auto first = [&](int i) { return lin_first(a, i) / a.seg_len + i; };
+  const int lo = lin_last(a, [&](int i) { return first(i) <= w; });
   const int64_t g = w - first(lo);
   *s = lo;
   *seg = static_cast<int>(g);

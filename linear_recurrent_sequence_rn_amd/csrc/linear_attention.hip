@@ -345,16 +345,21 @@ __global__ void __launch_bounds__(256) lin_recurrent(LinArgs a) {
 template <int V>
 __global__ void __launch_bounds__(256) lin_scan(LinArgs a) {
   typedef float fv __attribute__((ext_vector_type(V)));
-  const int h = blockIdx.y, s = blockIdx.z;
+  const int h = blockIdx.y;
+  // In a flat grid block m - 1 has the sequence of more than one segment that starts in front of
+  // token row m L, the first such row behind its start, and ends behind it.
+  const int64_t m = blockIdx.z + int64_t(1);
+  const int s = a.flat ? lin_last(a, [&](int i) { return lin_first(a, i) <= m * a.seg_len; }) : static_cast<int>(blockIdx.z);
+  if (s == a.S) return;
   const int64_t sh = static_cast<int64_t>(a.dk) * a.dv;
   const int64_t e = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * V;
   if (e >= sh) return;
   int64_t row0, own;
   int len;
   lin_span(a, s, &row0, &len, &own);
+  if (a.flat && (len <= a.seg_len || row0 / a.seg_len + 1 != m)) return;
   const int slot = lin_slot(a, s);
   const int n = (len + a.seg_len - 1) / a.seg_len;
-  if (a.flat && n <= 1) return;
   const int64_t at = (static_cast<int64_t>(slot) * a.H + h) * sh + e;
   fv x = {};
   if (a.state_in && slot >= 0) x = *reinterpret_cast<const fv*>(a.state_in + at);
@@ -502,18 +507,20 @@ hipError_t launch_linear_chunked(const LinCall& c, hipStream_t st) {
   segments(c, &a.seg_len, &a.n_seg);
   const bool mfma = mfma_call(c);
   if (a.n_seg == 1) return mfma ? launch_lin_mfma(a, kLinWhole, st) : launch_recurrent<kLinWhole>(a, c.in_dt, c.out_dt, st);
-  // Where N says little about the lengths (256 packed sequences of 224 tokens and no nearer bound
-  // than the 57344 tokens of all, 16 heads of 64 x 64: FIG us).
+  // Where N says little about the lengths: 1024 packed sequences of 28 tokens, 8 heads of 64 x 128,
+  // and no nearer bound than the tokens of all: 216 us, 1382 us with S n_seg blocks (160 where the
+  // bound is given, in one pass). (S N is then more than T, and T / L at most 768 by the choice of L.)
   a.flat = c.T > 0 && static_cast<int64_t>(c.S) * a.n_seg > 2 * (c.T / a.seg_len + c.S + 1);
   const size_t rows = static_cast<size_t>(total_segments(c, a.seg_len, a.n_seg)) * c.H;
   a.seg_decay = static_cast<float*>(c.ws);
   a.seg_state = a.seg_decay + ((rows + 63) & ~size_t(63));
   hipError_t e = mfma ? launch_lin_mfma(a, kLinState, st) : launch_recurrent<kLinState>(a, c.in_dt, c.out_dt, st);
   if (e != hipSuccess) return e;
+  const unsigned z = a.flat ? static_cast<unsigned>(std::max<int64_t>(1, c.T / a.seg_len)) : c.S;
   if (c.dk * c.dv % 4 == 0)   // (states are 16-byte aligned, here and in the caller's buffers)
-    hipLaunchKernelGGL(lin_scan<4>, dim3((c.dk * c.dv + 1023) / 1024, c.H, c.S), dim3(256), 0, st, a);
+    hipLaunchKernelGGL(lin_scan<4>, dim3((c.dk * c.dv + 1023) / 1024, c.H, z), dim3(256), 0, st, a);
   else
-    hipLaunchKernelGGL(lin_scan<1>, dim3((c.dk * c.dv + 255) / 256, c.H, c.S), dim3(256), 0, st, a);
+    hipLaunchKernelGGL(lin_scan<1>, dim3((c.dk * c.dv + 255) / 256, c.H, z), dim3(256), 0, st, a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   if (a.flat) return mfma ? launch_lin_mfma(a, kLinWhole, st) : launch_recurrent<kLinWhole>(a, c.in_dt, c.out_dt, st);
   return mfma ? launch_lin_mfma(a, kLinOut, st) : launch_recurrent<kLinOut>(a, c.in_dt, c.out_dt, st);
