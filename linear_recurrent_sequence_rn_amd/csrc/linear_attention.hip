@@ -2,10 +2,11 @@
 //     S_t = exp(g_t) S_{t-1} + k_t^T v_t,     o_t = scale q_t S_t.
 //
 // lin_step: one token a sequence. Bound by HBM: the float32 state is read and written once.
-// lin_recurrent: prompts of any type and head size by the recurrence itself, token by token,
-// the state in registers. Bound by the vector units (three operations a state element and token)
-// and by the chain of tokens where few states leave a compute unit one block (padded float32
-// batch of 3 sequences of up to 2001 tokens, 5 heads of 48 x 81: 39 us, of which the scan is 8).
+// lin_float: prompts of any type and head size in chunks of 16 tokens on the float32 matrix cores.
+// Bound by the wait for each chunk's phases and the padding of small heads (padded float32 batch of
+// 3 sequences of up to 2001 tokens, 5 heads of 48 x 81: 33 us, of which the scan is 8; 32 heads of
+// 2048 tokens, 128 x 128: 129 us). The recurrence itself, token by token on the vector units,
+// took 39 and 172 us.
 // Long sequences are cut into segments: one pass gives the state each segment adds on its own,
 // lin_scan carries the states over the segments, a second pass gives the outputs; the same three
 // passes carry the matrix-core kernel's segments.
@@ -135,38 +136,81 @@ __global__ void __launch_bounds__(NT) lin_step(LinArgs a, int slices) {
   }
 }
 
-// ---- prompts by the recurrence ------------------------------------------------------------
-// A block owns 64 columns of one head's state over one segment of one sequence, in registers: wave
-// w holds the rows [w RW, (w+1) RW), and each of its lanes RW / 4 rows of 4 neighbouring columns
-// (lane = 4 column quad + row group), so that 16 bytes from LDS feed 16 state elements (rows past
-// d_k stay zero). Tokens come in blocks of 16 through LDS, the next block's loads in flight
-// meanwhile; the four row groups' shares of an output meet by DPP, the waves' in LDS. (One column
-// and RW rows a lane read 16 bytes of LDS for 4 elements and were bound by that: 12 x 16 heads of
-// 212 bf16 tokens, 128 x 81: 218 -> 94 us; 3 heads of 1169 float32 tokens, 192 x 81: 135 -> 65.)
+// ---- prompts in float32 -------------------------------------------------------------------
+// Chunks of 16 tokens, with c_t the running sum of the log2 decays inside one:
+//     O = (Q K^T o D) V + diag(2^c) Q S,  D_ts = 2^(c_t - c_s) for s <= t;
+//     S <- 2^(c_15) S + K^T (w o V),  w_s = 2^(c_15 - c_s),
+// all products on the float32 matrix cores. A block owns 64 columns of one head's state over one
+// segment of one sequence; wave w has its rows [w RW, (w+1) RW) as accumulators (rows past d_k stay
+// zero), which hold four rows of a column a lane: with the reduction's rows numbered 4 (l / 16) + r
+// they are the operand of Q S as they are. Each wave forms its rows' shares of the scores and of
+// Q S; the shares meet in LDS, and wave w finishes the columns [16 w, 16 w + 16).
 constexpr int kTok = 16;
 constexpr int kCols = 64;
+constexpr int kPad = 4;      // floats behind each LDS row, so that 16 rows at a column, and 4 rows of
+                             // 16 columns at a distance of 4 rows, lie in different banks
 
-// the value of the lane whose number differs in bit B of a quad
-template <int B>
-__device__ __forceinline__ float quad_swap(float x) {
-  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), B == 1 ? 0xB1 : 0x4E, 0xf, 0xf, true));
+struct alignas(16) Decays16 {   // of one chunk
+  double c[kTok];        // running sum of log2 decays
+  float e[kTok];         // 2^c
+  float w[kTok];         // 2^(c_15 - c)
+  float a;               // 2^c_15
+  int bad;               // v holds a NaN or an infinity
+};
+
+__device__ __forceinline__ f32x4 mfma32(float a, float b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+}
+template <int CTRL>
+__device__ __forceinline__ double row_shifted(double x) {   // 0 where a row of 16 lanes has no such lane
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(u), CTRL, 0xf, 0xf, true);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(u >> 32), CTRL, 0xf, 0xf, true);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+// One wave whose lanes l hold the log decay of token l % 16. Returns the sum of log2 decays. (A
+// decay of 0 counts as 2^-173, which is 0 as a float32 factor.)
+__device__ __forceinline__ double scan_decays16(float g, Decays16* d) {
+  const int lane = threadIdx.x & 63;
+  double x = static_cast<double>(g) * 1.4426950408889634;
+  if (x < -173.0) x = -173.0;           // (a NaN stays)
+  x += row_shifted<0x111>(x);
+  x += row_shifted<0x112>(x);
+  x += row_shifted<0x114>(x);
+  x += row_shifted<0x118>(x);
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(u), 15);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(u >> 32), 15);
+  const double last = __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+  if (lane < kTok) {
+    d->c[lane] = x;
+    d->e[lane] = exp2f(static_cast<float>(x));
+    d->w[lane] = exp2f(static_cast<float>(last - x));
+    if (lane == 15) d->a = exp2f(static_cast<float>(x));
+  }
+  return last;
 }
 
 template <int IN, int OUT, int RW, LinMode MODE>
-__global__ void __launch_bounds__(256) lin_recurrent(LinArgs a) {
+__global__ void __launch_bounds__(256) lin_float(LinArgs a) {
   constexpr int D = 4 * RW;
+  constexpr int RT = RW / 16;             // 16-row tiles of the state a wave
+  constexpr int CT = kCols / 16;          // 16-column tiles
   constexpr int E = kTok * D / 256;       // q (or k) elements a thread stages
-  __shared__ float qt[kTok][D];
-  __shared__ float kt[kTok][D];
-  __shared__ float vt[kTok][kCols];
-  __shared__ float gt[kTok];
-  __shared__ float part[4][kTok][kCols];
+  constexpr bool kOut = MODE != kLinState;
+  __shared__ __align__(16) float qt[kOut ? kTok : 1][D + kPad];
+  __shared__ __align__(16) float kt[kTok][D + kPad];
+  __shared__ __align__(16) float vt[kTok][kCols + kPad];
+  __shared__ __align__(16) float pt[kOut ? 4 : 1][kTok][kTok + kPad];       // the waves' shares of the scores
+  __shared__ __align__(16) float part[kOut ? 4 : 1][kTok][kCols + kPad];    // and of Q S
+  __shared__ Decays16 dec[2];
   int h, c0;
   lin_block(a, blockIdx.x, &h, &c0);
   c0 *= kCols;
   int seg, s;
   if (!lin_place(a, &s, &seg)) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nc = min(kCols, a.dv - c0);
   int64_t row0, own;
   int len;
@@ -182,32 +226,21 @@ __global__ void __launch_bounds__(256) lin_recurrent(LinArgs a) {
   if (t0 >= t1 && !(MODE == kLinWhole && seg == 0 && keep)) return;
   if (MODE == kLinState && t1 == len && (!keep || (a.flat && one))) return;   // nobody reads the last segment's state
 
-  constexpr int RL = RW / 4;
-  const int sub = lane & 3, cq = lane & ~3;
-  auto row = [&](int r) { return wave * RW + (r >> 2) * 16 + sub * 4 + (r & 3); };
-  const bool quads = a.dv % 4 == 0;   // (states are 16-byte aligned)
-  float S[RL][4];
+  const int l16 = lane & 15, g4 = (lane >> 4) * 4;
+  f32x4 S[RT][CT];                        // rows wave RW + 16 i + g4 + r, column 16 c + l16
   {
     const float* from = MODE == kLinState ? nullptr
                         : MODE == kLinOut || !one ? a.seg_state + (lin_segment(a, s, row0, seg) * a.H + h) * sh
                         : a.state_in && slot >= 0 ? a.state_in + (static_cast<int64_t>(slot) * a.H + h) * sh : nullptr;
 #pragma unroll
-    for (int r = 0; r < RL; ++r) {
-      const int d = row(r);
-      f32x4 x = {};
-      if (from && d < a.dk) {
-        const float* p = from + (static_cast<int64_t>(d) * a.dv + c0 + cq);
-        if (quads) {
-          if (cq < nc) x = *reinterpret_cast<const f32x4*>(p);
-        } else {
+    for (int i = 0; i < RT; ++i)
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (cq + c < nc) x[c] = p[c];
+      for (int c = 0; c < CT; ++c)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int d = wave * RW + 16 * i + g4 + r, v = 16 * c + l16;
+          S[i][c][r] = from && d < a.dk && v < nc ? from[static_cast<int64_t>(d) * a.dv + c0 + v] : 0.f;
         }
-      }
-#pragma unroll
-      for (int c = 0; c < 4; ++c) S[r][c] = x[c];
-    }
   }
   const int64_t qo = lin_base(a, a.qs, s, row0) + h / (a.H / a.Hq) * a.qs[1];
   const int64_t ko = lin_base(a, a.ks, s, row0) + h / (a.H / a.Hk) * a.ks[1];
@@ -232,82 +265,126 @@ __global__ void __launch_bounds__(256) lin_recurrent(LinArgs a) {
     rg = a.g[go + min(t + (tid & (kTok - 1)), t1 - 1) * a.gs[2]];
   };
   double gsum = 0.0;
-  if (t0 < t1) fetch(t0);
-  for (int t = t0; t < t1; t += kTok) {
+  if (t0 < t1) {
+    fetch(t0);
+    if (tid < 2) dec[tid].bad = 0;
+    __syncthreads();
+  }
+  int buf = 0;
+  for (int t = t0; t < t1; t += kTok, buf ^= 1) {
     const int n = min(kTok, t1 - t);
+    // (tokens behind the last have decay 1 and k = q = v = 0, and change nothing)
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const int i = tid + 256 * e;
       const bool ok = i / D < n && i % D < a.dk;
-      if constexpr (MODE != kLinState) qt[i / D][i % D] = ok ? rq[e] : 0.f;
+      if constexpr (kOut) qt[i / D][i % D] = ok ? rq[e] : 0.f;
       kt[i / D][i % D] = ok ? rk[e] : 0.f;
     }
+    bool mine = false;
 #pragma unroll
     for (int e = 0; e < kTok * kCols / 256; ++e) {
       const int i = tid + 256 * e;
-      vt[i / kCols][i % kCols] = i / kCols < n && i % kCols < nc ? rv[e] : 0.f;
+      const float x = i / kCols < n && i % kCols < nc ? rv[e] : 0.f;
+      mine |= !(fabsf(x) < INFINITY);
+      vt[i / kCols][i % kCols] = x;
     }
-    if (tid < kTok) {
-      gt[tid] = tid < n ? expf(rg) : 1.f;
-      gsum += tid < n ? rg : 0.f;
-    }
+    if (kOut && mine) dec[buf].bad = 1;
+    if (wave == 3) gsum += scan_decays16((lane & 15) < n ? rg : 0.f, &dec[buf]);
     __syncthreads();
     if (t + kTok < t1) fetch(t + kTok);
-    // A token's values are read from LDS while the one before it is worked on. (Tokens behind the
-    // last have decay 1 and k = q = v = 0, and change nothing.)
-    struct Token { float4 k[RL / 4], q[RL / 4], v; float dec; } ta, tb;
-    auto read = [&](int i, Token& x) {
-      x.dec = gt[i];
-      x.v = *reinterpret_cast<const float4*>(&vt[i][cq]);
+    const Decays16& Y = dec[buf];
+    float vf[4];                          // tokens g4 + n of this wave's output columns
+    if constexpr (kOut) {
 #pragma unroll
-      for (int j = 0; j < RL / 4; ++j) {
-        x.k[j] = *reinterpret_cast<const float4*>(&kt[i][wave * RW + 16 * j + 4 * sub]);
-        if constexpr (MODE != kLinState) x.q[j] = *reinterpret_cast<const float4*>(&qt[i][wave * RW + 16 * j + 4 * sub]);
+      for (int n = 0; n < 4; ++n) vf[n] = vt[g4 + n][16 * wave + l16];
+      f32x4 P = {}, O[CT];
+#pragma unroll
+      for (int c = 0; c < CT; ++c) O[c] = f32x4{};
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        const f32x4 q = *reinterpret_cast<const f32x4*>(&qt[l16][wave * RW + 16 * i + g4]);
+        const f32x4 k = *reinterpret_cast<const f32x4*>(&kt[l16][wave * RW + 16 * i + g4]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          P = mfma32(q[r], k[r], P);
+#pragma unroll
+          for (int c = 0; c < CT; ++c) O[c] = mfma32(q[r], S[i][c][r], O[c]);
+        }
       }
-    };
-    auto work = [&](int i, const Token& x) {
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
-      const float v[4] = {x.v.x, x.v.y, x.v.z, x.v.w};
 #pragma unroll
-      for (int j = 0; j < RL / 4; ++j) {
-        const float k[4] = {x.k[j].x, x.k[j].y, x.k[j].z, x.k[j].w};
-        const float q[4] = {x.q[j].x, x.q[j].y, x.q[j].z, x.q[j].w};
+      for (int r = 0; r < 4; ++r) {
+        pt[wave][g4 + r][l16] = P[r];
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float& st = S[4 * j + r][c];
-            st = fmaf(x.dec, st, k[r] * v[c]);
-            if constexpr (MODE != kLinState) acc[c] = fmaf(q[r], st, acc[c]);
-          }
+        for (int c = 0; c < CT; ++c) part[wave][g4 + r][16 * c + l16] = O[c][r];
       }
-      if constexpr (MODE != kLinState) {
-        // the sum over the quad's lanes; lane i of a quad keeps column i
-        const bool b1 = lane & 2, b0 = lane & 1;
-        const float u0 = (b1 ? acc[2] : acc[0]) + quad_swap<2>(b1 ? acc[0] : acc[2]);
-        const float u1 = (b1 ? acc[3] : acc[1]) + quad_swap<2>(b1 ? acc[1] : acc[3]);
-        part[wave][i][lane] = (b0 ? u1 : u0) + quad_swap<1>(b0 ? u0 : u1);
-      }
-    };
-    read(0, ta);
-#pragma unroll 2
-    for (int i = 0; i < kTok; i += 2) {
-      read(i + 1, tb);
-      __builtin_amdgcn_sched_barrier(0);
-      work(i, ta);
-      read(i + 2 < kTok ? i + 2 : 0, ta);
-      __builtin_amdgcn_sched_barrier(0);
-      work(i + 1, tb);
     }
-    __syncthreads();
-    if constexpr (MODE != kLinState) {
+    if (MODE != kLinOut || t + kTok < t1) {
+      const float a16 = Y.a;
 #pragma unroll
-      for (int e = 0; e < kTok / 4; ++e) {
-        const int i = wave + 4 * e;
-        if (i < n && lane < nc)
-          Elem<OUT>::store(a.out, oo + (t + i) * a.os[2] + lane,
-                           a.scale * ((part[0][i][lane] + part[1][i][lane]) + (part[2][i][lane] + part[3][i][lane])));
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int c = 0; c < CT; ++c) S[i][c] *= a16;
+      const f32x4 w = *reinterpret_cast<const f32x4*>(&Y.w[g4]);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        float wv[CT];
+#pragma unroll
+        for (int c = 0; c < CT; ++c) wv[c] = w[n] * vt[g4 + n][16 * c + l16];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          const float k = kt[g4 + n][wave * RW + 16 * i + l16];
+#pragma unroll
+          for (int c = 0; c < CT; ++c) S[i][c] = mfma32(k, wv[c], S[i][c]);
+        }
       }
+    }
+    if (tid == 0) dec[buf ^ 1].bad = 0;
+    // The shares are whole, and the tiles of Q, K and V are free (but see `bad`).
+    __syncthreads();
+    if constexpr (kOut) {
+      const f32x4 e = *reinterpret_cast<const f32x4*>(&Y.e[g4]);
+      f32x4 o;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float* x = &part[0][g4 + r][16 * wave + l16];
+        constexpr int W = kTok * (kCols + kPad);
+        o[r] = e[r] * ((x[0] + x[W]) + (x[2 * W] + x[3 * W]));
+      }
+      const bool bad = __builtin_amdgcn_readfirstlane(Y.bad);   // (one for the block)
+      if (bad)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) vf[n] = fabsf(vf[n]) < INFINITY ? vf[n] : 0.f;
+      f32x4 p = *reinterpret_cast<const f32x4*>(&pt[0][l16][g4]);
+#pragma unroll
+      for (int w = 1; w < 4; ++w) p += *reinterpret_cast<const f32x4*>(&pt[w][l16][g4]);
+      const double cq = Y.c[l16];
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const float x = p[n] * exp2f(static_cast<float>(cq - Y.c[g4 + n]));
+        o = mfma32(g4 + n <= l16 ? x : 0.f, vf[n], o);
+      }
+      if (bad) {
+        // 0 times a NaN or an infinity of a later token must not reach this one: what was left out
+        // of the product, for the queries that see it
+#pragma unroll 1
+        for (int k = 0; k < g4 + 4; ++k) {
+          const float v = vt[k][16 * wave + l16];
+          if (!(fabsf(v) < INFINITY)) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int q = g4 + r;
+              const float x = (pt[0][q][k] + pt[1][q][k] + pt[2][q][k] + pt[3][q][k]) * exp2f(static_cast<float>(Y.c[q] - Y.c[k]));
+              o[r] = k <= q ? fmaf(x, v, o[r]) : o[r];
+            }
+          }
+        }
+        __syncthreads();
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (g4 + r < n && 16 * wave + l16 < nc)
+          Elem<OUT>::store(a.out, oo + (t + g4 + r) * a.os[2] + 16 * wave + l16, a.scale * o[r]);
     }
   }
   float* to = nullptr;
@@ -315,27 +392,18 @@ __global__ void __launch_bounds__(256) lin_recurrent(LinArgs a) {
   if (MODE == kLinState) {
     const int64_t i = lin_segment(a, s, row0, seg) * a.H + h;
     to = a.seg_state + i * sh;
-    // (thread t holds the sum of tokens t, t + 16, ... of the segment)
-#pragma unroll
-    for (int o = 8; o >= 1; o >>= 1) gsum += __shfl_xor(gsum, o, 16);
-    if (c0 == 0 && tid == 0) a.seg_decay[i] = expf(static_cast<float>(gsum));
+    if (c0 == 0 && tid == 192) a.seg_decay[i] = exp2f(static_cast<float>(gsum));
   }
   if (to) {
 #pragma unroll
-    for (int r = 0; r < RL; ++r) {
-      const int d = row(r);
-      if (d < a.dk) {
-        float* p = to + (static_cast<int64_t>(d) * a.dv + c0 + cq);
-        if (quads) {
-          const f32x4 x = {S[r][0], S[r][1], S[r][2], S[r][3]};
-          if (cq < nc) *reinterpret_cast<f32x4*>(p) = x;
-        } else {
+    for (int i = 0; i < RT; ++i)
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (cq + c < nc) p[c] = S[r][c];
+      for (int c = 0; c < CT; ++c)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int d = wave * RW + 16 * i + g4 + r, v = 16 * c + l16;
+          if (d < a.dk && v < nc) to[static_cast<int64_t>(d) * a.dv + c0 + v] = S[i][c][r];
         }
-      }
-    }
   }
 }
 
@@ -389,23 +457,23 @@ __global__ void __launch_bounds__(256) lin_scan(LinArgs a) {
 }
 
 template <int IN, int OUT, LinMode MODE>
-hipError_t launch_recurrent_t(const LinArgs& a, hipStream_t st) {
+hipError_t launch_float_t(const LinArgs& a, hipStream_t st) {
   const int slices = (a.dv + kCols - 1) / kCols;
   const bool rest = a.T > 0 && a.zero_rest && MODE != kLinState;
   const dim3 grid = lin_grid(a, a.H * slices, rest);
   const int rw = (a.dk + 3) / 4;
-  if (rw <= 16) hipLaunchKernelGGL((lin_recurrent<IN, OUT, 16, MODE>), grid, dim3(256), 0, st, a);
-  else if (rw <= 32) hipLaunchKernelGGL((lin_recurrent<IN, OUT, 32, MODE>), grid, dim3(256), 0, st, a);
-  else if (rw <= 48) hipLaunchKernelGGL((lin_recurrent<IN, OUT, 48, MODE>), grid, dim3(256), 0, st, a);
-  else hipLaunchKernelGGL((lin_recurrent<IN, OUT, 64, MODE>), grid, dim3(256), 0, st, a);
+  if (rw <= 16) hipLaunchKernelGGL((lin_float<IN, OUT, 16, MODE>), grid, dim3(256), 0, st, a);
+  else if (rw <= 32) hipLaunchKernelGGL((lin_float<IN, OUT, 32, MODE>), grid, dim3(256), 0, st, a);
+  else if (rw <= 48) hipLaunchKernelGGL((lin_float<IN, OUT, 48, MODE>), grid, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL((lin_float<IN, OUT, 64, MODE>), grid, dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
 template <LinMode MODE>
-hipError_t launch_recurrent(const LinArgs& a, int in_dt, int out_dt, hipStream_t st) {
+hipError_t launch_float(const LinArgs& a, int in_dt, int out_dt, hipStream_t st) {
   if (in_dt == RN_F32)
-    return out_dt == RN_F32 ? launch_recurrent_t<RN_F32, RN_F32, MODE>(a, st) : launch_recurrent_t<RN_F32, RN_BF16, MODE>(a, st);
-  return out_dt == RN_F32 ? launch_recurrent_t<RN_BF16, RN_F32, MODE>(a, st) : launch_recurrent_t<RN_BF16, RN_BF16, MODE>(a, st);
+    return out_dt == RN_F32 ? launch_float_t<RN_F32, RN_F32, MODE>(a, st) : launch_float_t<RN_F32, RN_BF16, MODE>(a, st);
+  return out_dt == RN_F32 ? launch_float_t<RN_BF16, RN_F32, MODE>(a, st) : launch_float_t<RN_BF16, RN_BF16, MODE>(a, st);
 }
 
 template <int IN, int OUT>
@@ -449,8 +517,8 @@ LinArgs lin_args(const LinCall& c) {
 }
 
 // Matrix cores: bf16 in and out, head sizes and rows in whole 16-byte pieces. (The pointers are
-// not known when the workspace is sized: a call with an unaligned one runs the recurrence on
-// the same segments.)
+// not known when the workspace is sized: a call with an unaligned one takes the float32
+// kernel on the same segments.)
 bool mfma_shape(const LinCall& c) {
   bool ok = !c.generic && c.in_dt == RN_BF16 && c.out_dt == RN_BF16 && c.dk % 8 == 0 && c.dv % 8 == 0;
   for (const int64_t* s : {c.qs, c.ks, c.vs, c.os})
@@ -506,7 +574,7 @@ hipError_t launch_linear_chunked(const LinCall& c, hipStream_t st) {
   LinArgs a = lin_args(c);
   segments(c, &a.seg_len, &a.n_seg);
   const bool mfma = mfma_call(c);
-  if (a.n_seg == 1) return mfma ? launch_lin_mfma(a, kLinWhole, st) : launch_recurrent<kLinWhole>(a, c.in_dt, c.out_dt, st);
+  if (a.n_seg == 1) return mfma ? launch_lin_mfma(a, kLinWhole, st) : launch_float<kLinWhole>(a, c.in_dt, c.out_dt, st);
   // Where N says little about the lengths: 1024 packed sequences of 28 tokens, 8 heads of 64 x 128,
   // and no nearer bound than the tokens of all: 216 us, 1382 us with S n_seg blocks (160 where the
   // bound is given, in one pass). (S N is then more than T, and T / L at most 768 by the choice of L.)
@@ -514,7 +582,7 @@ hipError_t launch_linear_chunked(const LinCall& c, hipStream_t st) {
   const size_t rows = static_cast<size_t>(total_segments(c, a.seg_len, a.n_seg)) * c.H;
   a.seg_decay = static_cast<float*>(c.ws);
   a.seg_state = a.seg_decay + ((rows + 63) & ~size_t(63));
-  hipError_t e = mfma ? launch_lin_mfma(a, kLinState, st) : launch_recurrent<kLinState>(a, c.in_dt, c.out_dt, st);
+  hipError_t e = mfma ? launch_lin_mfma(a, kLinState, st) : launch_float<kLinState>(a, c.in_dt, c.out_dt, st);
   if (e != hipSuccess) return e;
   const unsigned z = a.flat ? static_cast<unsigned>(std::max<int64_t>(1, c.T / a.seg_len)) : c.S;
   if (c.dk * c.dv % 4 == 0)   // (states are 16-byte aligned, here and in the caller's buffers)
@@ -522,8 +590,8 @@ hipError_t launch_linear_chunked(const LinCall& c, hipStream_t st) {
   else
     hipLaunchKernelGGL(lin_scan<1>, dim3((c.dk * c.dv + 255) / 256, c.H, z), dim3(256), 0, st, a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  if (a.flat) return mfma ? launch_lin_mfma(a, kLinWhole, st) : launch_recurrent<kLinWhole>(a, c.in_dt, c.out_dt, st);
-  return mfma ? launch_lin_mfma(a, kLinOut, st) : launch_recurrent<kLinOut>(a, c.in_dt, c.out_dt, st);
+  if (a.flat) return mfma ? launch_lin_mfma(a, kLinWhole, st) : launch_float<kLinWhole>(a, c.in_dt, c.out_dt, st);
+  return mfma ? launch_lin_mfma(a, kLinOut, st) : launch_float<kLinOut>(a, c.in_dt, c.out_dt, st);
 }
 
 }  // namespace rn

@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
     }
     // (the largest head has no register left for products started early)
     if constexpr (DK == 256) __builtin_amdgcn_sched_barrier(0);
-    const bool bad = D.bad;
+    const bool bad = __builtin_amdgcn_readfirstlane(D.bad);   // (one for the block)
     bf16x8 vf[2][VT];
     if constexpr (kHasV)
 #pragma unroll
