@@ -184,9 +184,9 @@ __device__ __forceinline__ double scan_decays16(float g, Decays16* d) {
   const double last = __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
   if (lane < kTok) {
     d->c[lane] = x;
-    d->e[lane] = exp2f(static_cast<float>(x));
-    d->w[lane] = exp2f(static_cast<float>(last - x));
-    if (lane == 15) d->a = exp2f(static_cast<float>(x));
+    d->e[lane] = __builtin_amdgcn_exp2f(static_cast<float>(x));
+    d->w[lane] = __builtin_amdgcn_exp2f(static_cast<float>(last - x));
+    if (lane == 15) d->a = __builtin_amdgcn_exp2f(static_cast<float>(x));
   }
   return last;
 }
@@ -262,11 +262,15 @@ __global__ void __launch_bounds__(256) lin_float(LinArgs a) {
       const int i = tid + 256 * e, tt = min(t + i / kCols, t1 - 1), c = min(i % kCols, nc - 1);
       rv[e] = Elem<IN>::load(a.v, vo + tt * a.vs[2] + c);
     }
-    rg = a.g[go + min(t + (tid & (kTok - 1)), t1 - 1) * a.gs[2]];
   };
+  // (log decays are fetched two chunks ahead: one wave forms a chunk's decays during the one before)
+  auto fetch_g = [&](int t) { rg = t + l16 < t1 ? a.g[go + (t + l16) * a.gs[2]] : 0.f; };
   double gsum = 0.0;
   if (t0 < t1) {
     fetch(t0);
+    fetch_g(t0);
+    if (wave == 3) gsum += scan_decays16(rg, &dec[0]);
+    fetch_g(t0 + kTok);
     if (tid < 2) dec[tid].bad = 0;
     __syncthreads();
   }
@@ -290,9 +294,12 @@ __global__ void __launch_bounds__(256) lin_float(LinArgs a) {
       vt[i / kCols][i % kCols] = x;
     }
     if (kOut && mine) dec[buf].bad = 1;
-    if (wave == 3) gsum += scan_decays16((lane & 15) < n ? rg : 0.f, &dec[buf]);
     __syncthreads();
-    if (t + kTok < t1) fetch(t + kTok);
+    if (t + kTok < t1) {
+      fetch(t + kTok);
+      if (wave == 3) gsum += scan_decays16(rg, &dec[buf ^ 1]);
+      fetch_g(t + 2 * kTok);
+    }
     const Decays16& Y = dec[buf];
     float vf[4];                          // tokens g4 + n of this wave's output columns
     if constexpr (kOut) {
@@ -361,7 +368,7 @@ __global__ void __launch_bounds__(256) lin_float(LinArgs a) {
       const double cq = Y.c[l16];
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
-        const float x = p[n] * exp2f(static_cast<float>(cq - Y.c[g4 + n]));
+        const float x = p[n] * __builtin_amdgcn_exp2f(static_cast<float>(cq - Y.c[g4 + n]));
         o = mfma32(g4 + n <= l16 ? x : 0.f, vf[n], o);
       }
       if (bad) {
@@ -374,7 +381,7 @@ __global__ void __launch_bounds__(256) lin_float(LinArgs a) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               const int q = g4 + r;
-              const float x = (pt[0][q][k] + pt[1][q][k] + pt[2][q][k] + pt[3][q][k]) * exp2f(static_cast<float>(Y.c[q] - Y.c[k]));
+              const float x = (pt[0][q][k] + pt[1][q][k] + pt[2][q][k] + pt[3][q][k]) * __builtin_amdgcn_exp2f(static_cast<float>(Y.c[q] - Y.c[k]));
               o[r] = k <= q ? fmaf(x, v, o[r]) : o[r];
             }
           }
@@ -392,7 +399,7 @@ __global__ void __launch_bounds__(256) lin_float(LinArgs a) {
   if (MODE == kLinState) {
     const int64_t i = lin_segment(a, s, row0, seg) * a.H + h;
     to = a.seg_state + i * sh;
-    if (c0 == 0 && tid == 192) a.seg_decay[i] = exp2f(static_cast<float>(gsum));
+    if (c0 == 0 && tid == 192) a.seg_decay[i] = __builtin_amdgcn_exp2f(static_cast<float>(gsum));
   }
   if (to) {
 #pragma unroll
@@ -436,14 +443,14 @@ __global__ void __launch_bounds__(256) lin_scan(LinArgs a) {
   float* p = a.seg_state + first * sh + e;
   const float* d = a.seg_decay + first;
   const int64_t ps = sh * a.H;
-  // eight segments' states in flight
-  for (int g = 0; g < n; g += 8) {
-    fv u[8];
+  // sixteen segments' states in flight
+  for (int g = 0; g < n; g += 16) {
+    fv u[16];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 16; ++i)
       if (g + i < n && (last || g + i + 1 < n)) u[i] = *reinterpret_cast<const fv*>(p + (g + i) * ps);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 16; ++i)
       if (g + i < n) {
         *reinterpret_cast<fv*>(p + (g + i) * ps) = x;
         if (last || g + i + 1 < n) {
