@@ -60,6 +60,15 @@ __device__ __forceinline__ int at(int row, int col) {
   return row * (2 * W) + (((col >> 3) ^ f) << 4) + (col & 7) * 2;
 }
 
+// Tiles whose rows are read as row operands have 64 bytes behind each 16 rows: two such reads a
+// whole number of 512 bytes apart would become one instruction whose halves meet in the same banks
+// (18 cycles in place of 2 x 4; 8 x 2048 tokens, 32 heads of 128 x 128: 169 us, without them 175).
+constexpr int kGap = 64;
+template <int W>
+constexpr int kRows = 32 * W + kGap;    // bytes of 16 rows
+template <int W>
+__device__ __forceinline__ int at_gap(int row, int col) { return at<W>(row, col) + (row >> 4) * kGap; }
+
 // The permutation only XORs bits of the offset, and so do steps of whole 16 columns: all offsets
 // a lane needs come from one base per way of reading, XORed with constants, and from
 // constants added for steps of 16 rows.
@@ -73,12 +82,12 @@ __device__ __forceinline__ bf16x8 row_operand(const char* tile, int base, int ks
 }
 // Operand whose lane holds column 16 i + l16, rows r..r+3 and r+16..r+19 with r = 32 ks + g4;
 // base = at<W>(g4 + l16 / 4, 4 (l16 % 4)).
-template <int W>
+template <int ROWS>   // bytes of 16 rows
 __device__ __forceinline__ bf16x8 col_operand(const char* tile, int base, int ks, int i) {
-  const char* p = tile + (base ^ (i << 5)) + ks * (32 * 2 * W);
+  const char* p = tile + (base ^ (i << 5)) + ks * (2 * ROWS);
   struct { s16x4 lo, hi; } v;
   v.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p));
-  v.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 16 * 2 * W));
+  v.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + ROWS));
   return __builtin_bit_cast(bf16x8, v);
 }
 
@@ -178,10 +187,12 @@ struct Tile {
     for (int i = 0; i < kN; ++i)
       if (c >= cols || row + i * kStep >= rows) r[i] = make_uint4(0, 0, 0, 0);
   }
+  template <bool GAP>
   __device__ __forceinline__ void store(char* tile) const {
     const int row = threadIdx.x / kPer, c = threadIdx.x % kPer * 8;
 #pragma unroll
-    for (int i = 0; i < kN; ++i) *reinterpret_cast<uint4*>(tile + at<W>(row + i * kStep, c)) = r[i];
+    for (int i = 0; i < kN; ++i)
+      *reinterpret_cast<uint4*>(tile + (GAP ? at_gap<W>(row + i * kStep, c) : at<W>(row + i * kStep, c))) = r[i];
   }
   // Whether a value is a NaN or an infinity (largest exponent).
   __device__ __forceinline__ bool nonfinite() const {
@@ -218,7 +229,7 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
   constexpr int OT = 4 / DW;             // 16-query tiles of the output a wave finishes
   constexpr int PARTS = MODE == kLinOut ? 2 : 3;
   constexpr bool kOut = MODE != kLinState;
-  constexpr int kTileQ = kChunk * DK * 2, kTileV = kChunk * DV * 2, kTileP = kChunk * kChunk * 2;
+  constexpr int kTileQ = 4 * kRows<DK>, kTileV = kChunk * DV * 2, kTileP = 4 * kRows<kChunk>;
   constexpr int kSwap = DW == 2 ? VW * DW * 2 * VT * 1024 : 0;
   // Two waves need each part of w V where DW is 2: they are formed once, on the way to LDS, as
   // long as the tiles fit in it; else each wave forms its own in registers.
@@ -308,7 +319,7 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
     if constexpr (kOut) {                   // score tiles above the diagonal that are read
       if (tid < 2 * 16 * 4) {
         const int tt = (tid >> 6) * 32 + (tid & 15), col = (tid >> 6) * 32 + 16 + ((tid >> 4) & 3) * 4;
-        *reinterpret_cast<uint2*>(pt + at<kChunk>(tt, col)) = make_uint2(0, 0);
+        *reinterpret_cast<uint2*>(pt + at_gap<kChunk>(tt, col)) = make_uint2(0, 0);
       }
     }
     __syncthreads();
@@ -342,12 +353,12 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
     if (mine) dec[buf].bad = 1;
     if constexpr (kOut) {
       tq.trim(n, a.dk);
-      tq.store(qt);
+      tq.template store<true>(qt);
     }
     tk.trim(n, a.dk);
-    tk.store(kt);
+    tk.template store<true>(kt);
     tv.trim(n, nc);
-    if constexpr (kHasV) tv.store(vt);
+    if constexpr (kHasV) tv.template store<false>(vt);
     if constexpr (kParts) {
       using TV = Tile<DV, NT>;
       const int row = tid / TV::kPer, c = tid % TV::kPer * 8;
@@ -384,7 +395,9 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
       constexpr int JT = 16 / (NT / 64);    // query tiles a wave
       const int j0 = JT == 4 ? 0 : (wave >> 2) * 2;
       if (keys <= j0 + JT - 1) {
-        const int rk = rq + keys * 32 * DK, rj = rq + j0 * 32 * DK, pj = (rp ^ (keys << 5)) + j0 * 32 * kChunk;
+        const char* kk = kt + keys * kRows<DK>;
+        const char* qq = qt + j0 * kRows<DK>;
+        const int pj = (rp ^ (keys << 5)) + j0 * kRows<kChunk>;
         const f32x4 cs = *reinterpret_cast<const f32x4*>(&D.c[16 * keys + g4]);
         const int ahead = l16 - g4 + 16 * (j0 - keys);   // queries' lead over the lane's first key
         auto finish = [&](int j, const f32x4& p) {
@@ -396,18 +409,18 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
 #pragma unroll
             for (int r = 0; r < 4; ++r) x[r] = ahead + 16 * j >= r ? x[r] : 0.f;
           }
-          *reinterpret_cast<uint2*>(pt + pj + j * 32 * kChunk) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+          *reinterpret_cast<uint2*>(pt + pj + j * kRows<kChunk>) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
         };
         if constexpr (JT == 4) {
           bf16x8 kf[KS];
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks) kf[ks] = row_operand(kt, rk, ks, 0);
+          for (int ks = 0; ks < KS; ++ks) kf[ks] = row_operand(kk, rq, ks, 0);
 #pragma unroll
           for (int j = 0; j < JT; ++j) {
             if (j0 + j < keys) continue;
             f32x4 p = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) p = mfma(kf[ks], row_operand(qt, rj, ks, j * 32 * DK), p);
+            for (int ks = 0; ks < KS; ++ks) p = mfma(kf[ks], row_operand(qq, rq, ks, j * kRows<DK>), p);
             finish(j, p);
           }
         } else {                            // both tiles at once: no room for all of the keys' operands
@@ -416,9 +429,9 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
           for (int j = 0; j < JT; ++j) p[j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks) {
-            const bf16x8 kf = row_operand(kt, rk, ks, 0);
+            const bf16x8 kf = row_operand(kk, rq, ks, 0);
 #pragma unroll
-            for (int j = 0; j < JT; ++j) p[j] = mfma(kf, row_operand(qt, rj, ks, j * 32 * DK), p[j]);
+            for (int j = 0; j < JT; ++j) p[j] = mfma(kf, row_operand(qq, rq, ks, j * kRows<DK>), p[j]);
           }
 #pragma unroll
           for (int j = 0; j < JT; ++j) finish(j, p[j]);
@@ -441,7 +454,7 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const bf16x8 q = row_operand(qt, rq ^ (drow * 2), ks, j * 32 * DK);
+          const bf16x8 q = row_operand(qt, rq ^ (drow * 2), ks, j * kRows<DK>);
 #pragma unroll
           for (int v = 0; v < VT; ++v) O[j][v] = mfma(sf[v], q, O[j][v]);
         }
@@ -466,7 +479,7 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-        for (int v = 0; v < VT; ++v) vf[ks][v] = col_operand<DV>(vt, cv, ks, v);
+        for (int v = 0; v < VT; ++v) vf[ks][v] = col_operand<32 * DV>(vt, cv, ks, v);
     if (MODE != kLinOut || more) {
       // S <- a S + K^T (w V): the parts of w V in the same order of tokens as K^T
       const float dec64 = D.a;
@@ -482,7 +495,7 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
 #pragma unroll
           for (int v = 0; v < VT; ++v)
 #pragma unroll
-            for (int p = 0; p < PARTS; ++p) wf[v][p] = col_operand<DV>(wt + p * kTileV, cv, ks, v);
+            for (int p = 0; p < PARTS; ++p) wf[v][p] = col_operand<32 * DV>(wt + p * kTileV, cv, ks, v);
         } else {
           const f32x4 w0 = *reinterpret_cast<const f32x4*>(&D.w[32 * ks + g4]);
           const f32x4 w1 = *reinterpret_cast<const f32x4*>(&D.w[32 * ks + 16 + g4]);
@@ -511,7 +524,7 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
         for (int i0 = 0; i0 < AT; i0 += B) {
           bf16x8 kf[B];
 #pragma unroll
-          for (int i = 0; i < B; ++i) kf[i] = col_operand<DK>(kt, ck, ks, i0 + i);
+          for (int i = 0; i < B; ++i) kf[i] = col_operand<kRows<DK>>(kt, ck, ks, i0 + i);
 #pragma unroll
           for (int p = PARTS - 1; p >= 0; --p)
 #pragma unroll
@@ -546,7 +559,7 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
 #pragma unroll
           for (int ks = 0; ks < 2; ++ks)
             if (ks <= j / 2) {
-              const bf16x8 p = row_operand(pt, rp, ks, j * 32 * kChunk);
+              const bf16x8 p = row_operand(pt, rp, ks, j * kRows<kChunk>);
 #pragma unroll
               for (int v = 0; v < VT; ++v) o[v] = mfma(vf[ks][v], p, o[v]);
             }
@@ -555,7 +568,7 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
           // sums, over the tokens up to the query's only
 #pragma unroll 1
           for (int k = 0; k < 16 * j + 16; ++k) {
-            const float p = bf16_to_f32(*reinterpret_cast<const uint16_t*>(pt + at<kChunk>(tt, k)));
+            const float p = bf16_to_f32(*reinterpret_cast<const uint16_t*>(pt + at_gap<kChunk>(tt, k)));
 #pragma unroll
             for (int v = 0; v < VT; ++v) {
               const uint2 u = *reinterpret_cast<const uint2*>(vt + at<DV>(k, wv * CW + 16 * v + g4));
