@@ -7,14 +7,15 @@
 //
 // Bound by HBM: every tensor is read or written once (16384 x 4096 bf16: forward with residual
 // 96 us, 5.6 TB/s; backward with the residual's gradient 109 us, 5.0 TB/s; a large copy reaches
-// 4.9 to 5.4 TB/s on the card). Odd widths read element by element and are bound by latency
-// (backward of 3001 x 1537 float32: 27 us). A row lives in the registers of one
+// 4.9 to 5.4 TB/s on the card). Smaller calls are bound by latency (backward of 3001 x 1537
+// float32: 22 us, of which the reduction of the weights' sums 5). A row lives in the registers of one
 // wave (W = 1, four rows per 256-thread block) or of a whole block (W = 4 or 16), so the passes
 // over it (mean, centred squares, result) cost no memory access. Blocks walk over rows:
 // the weights, and in the backward the column sums of dw and db, then stay in registers
 // too, and the backward writes one partial row of sums per block, which a second kernel
 // adds in a fixed order.
 #include <algorithm>
+#include <type_traits>
 
 #include "rn_device.h"
 #include "rn_kernels.h"
@@ -24,6 +25,13 @@ namespace {
 
 // Threads of a block whose rows take W waves each.
 constexpr int threads(int W) { return W > 4 ? 64 * W : 256; }
+
+// How a row falls into pieces of V elements: every lane has all its pieces; some have none; or rows
+// start anywhere and the last piece may be short. Memory takes 16-byte accesses at any element's
+// address, so the last kind differs only in that piece (backward of 3001 x 1537 float32: 22 us, element
+// by element 27; of 2000 x 10001 bf16: 75 and 216 us; forward 44 and 77. Only rows much shorter than
+// a wave's lanes lose: 20000 x 101 bf16, backward 26 and 18 us).
+enum Fit : int { kFull, kSome, kOdd };
 
 // 16 or 8 bytes, past the caches with STREAM (which pays for calls larger than the last-level
 // cache; what a smaller call leaves behind is soon read again).
@@ -39,43 +47,55 @@ __device__ __forceinline__ void put(void* p, const T& x) {
 }
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+// the same at any address of a 16-bit element
+typedef uint32_t u32x4a __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2a __attribute__((ext_vector_type(2), aligned(2)));
 
 // V consecutive elements of type DT as they are in memory; an address of 16 bytes (or the whole,
-// where that is less).
-template <int DT, int V, bool STREAM = false>
+// where that is less) but for kOdd. `left`: elements of the row from here on (kOdd).
+template <int DT, int V, Fit FIT, bool STREAM = false>
 struct Raw {
   static constexpr int kElem = DT == RN_F32 ? 4 : 2;
   static constexpr int kBytes = V * kElem;
-  uint32_t u[(kBytes + 3) / 4];
-  __device__ __forceinline__ void load(const void* p, int64_t i) {
+  using T4 = typename std::conditional<FIT == kOdd, u32x4a, u32x4>::type;
+  using T2 = typename std::conditional<FIT == kOdd, u32x2a, u32x2>::type;
+  uint32_t u[kBytes / 4];
+  __device__ __forceinline__ void load(const void* p, int64_t i, int left) {
     const char* s = static_cast<const char*>(p) + i * kElem;
-    if constexpr (kBytes >= 16) {
+    if (FIT == kOdd && left < V) {
+      clear();
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (j < left) {
+          if constexpr (DT == RN_F32) u[j] = *reinterpret_cast<const uint32_t*>(s + 4 * j);
+          else u[j / 2] |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(s + 2 * j)) << (j % 2 * 16);
+        }
+    } else if constexpr (kBytes >= 16) {
 #pragma unroll
       for (int j = 0; j < kBytes / 16; ++j) {
-        const u32x4 x = get<STREAM, u32x4>(s + 16 * j);
+        const T4 x = get<STREAM, T4>(s + 16 * j);
 #pragma unroll
         for (int k = 0; k < 4; ++k) u[4 * j + k] = x[k];
       }
-    } else if constexpr (kBytes == 8) {
-      const u32x2 x = get<STREAM, u32x2>(s);
-      u[0] = x[0]; u[1] = x[1];
-    } else if constexpr (kBytes == 4) {
-      u[0] = *reinterpret_cast<const uint32_t*>(s);
     } else {
-      u[0] = *reinterpret_cast<const uint16_t*>(s);
+      const T2 x = get<STREAM, T2>(s);
+      u[0] = x[0]; u[1] = x[1];
     }
   }
-  __device__ __forceinline__ void store(void* p, int64_t i) const {
+  __device__ __forceinline__ void store(void* p, int64_t i, int left) const {
     char* s = static_cast<char*>(p) + i * kElem;
-    if constexpr (kBytes >= 16) {
+    if (FIT == kOdd && left < V) {
 #pragma unroll
-      for (int j = 0; j < kBytes / 16; ++j) put<STREAM>(s + 16 * j, u32x4{u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]});
-    } else if constexpr (kBytes == 8) {
-      put<STREAM>(s, u32x2{u[0], u[1]});
-    } else if constexpr (kBytes == 4) {
-      *reinterpret_cast<uint32_t*>(s) = u[0];
+      for (int j = 0; j < V; ++j)
+        if (j < left) {
+          if constexpr (DT == RN_F32) *reinterpret_cast<uint32_t*>(s + 4 * j) = u[j];
+          else *reinterpret_cast<uint16_t*>(s + 2 * j) = static_cast<uint16_t>(u[j / 2] >> (j % 2 * 16));
+        }
+    } else if constexpr (kBytes >= 16) {
+#pragma unroll
+      for (int j = 0; j < kBytes / 16; ++j) put<STREAM>(s + 16 * j, T4{u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]});
     } else {
-      *reinterpret_cast<uint16_t*>(s) = static_cast<uint16_t>(u[0]);
+      put<STREAM>(s, T2{u[0], u[1]});
     }
   }
   __device__ __forceinline__ float value(int j) const {
@@ -86,8 +106,6 @@ struct Raw {
     if constexpr (DT == RN_F32) {
 #pragma unroll
       for (int j = 0; j < V; ++j) u[j] = __float_as_uint(f[j]);
-    } else if constexpr (V == 1) {
-      u[0] = f32_to_bf16(f[0]);
     } else {
 #pragma unroll
       for (int j = 0; j < V / 2; ++j) u[j] = pack_bf16x2(f[2 * j], f[2 * j + 1]);
@@ -95,21 +113,21 @@ struct Raw {
   }
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int j = 0; j < (kBytes + 3) / 4; ++j) u[j] = 0;
+    for (int j = 0; j < kBytes / 4; ++j) u[j] = 0;
   }
 };
-template <int DT, int V, bool STREAM = false>
-__device__ __forceinline__ void load(const void* p, int64_t i, float* f) {
-  Raw<DT, V, STREAM> r;
-  r.load(p, i);
+template <int DT, int V, Fit FIT, bool STREAM = false>
+__device__ __forceinline__ void load(const void* p, int64_t i, int left, float* f) {
+  Raw<DT, V, FIT, STREAM> r;
+  r.load(p, i, left);
 #pragma unroll
   for (int j = 0; j < V; ++j) f[j] = r.value(j);
 }
-template <int DT, int V, bool STREAM = false>
-__device__ __forceinline__ void store(void* p, int64_t i, const float* f) {
-  Raw<DT, V, STREAM> r;
+template <int DT, int V, Fit FIT, bool STREAM = false>
+__device__ __forceinline__ void store(void* p, int64_t i, int left, const float* f) {
+  Raw<DT, V, FIT, STREAM> r;
   r.set(f);
-  r.store(p, i);
+  r.store(p, i, left);
 }
 
 template <int CTRL, int ROWS>
@@ -165,7 +183,7 @@ struct NormArgs {
 };
 
 // Thread `lane` of a row's 64 W lanes holds elements [V (lane + 64 W i), +V) for i < NV.
-template <int IN, int OUT, int V, int W, int NV, bool FULL, bool STREAM>
+template <int IN, int OUT, int V, int W, int NV, Fit FIT, bool STREAM>
 __global__ void __launch_bounds__(threads(W)) norm_rows(NormArgs a) {
   constexpr int L = 64 * W;
   constexpr int R = threads(W) / L;       // rows per block
@@ -177,9 +195,9 @@ __global__ void __launch_bounds__(threads(W)) norm_rows(NormArgs a) {
     const int c = V * (lane + L * i);
 #pragma unroll
     for (int j = 0; j < V; ++j) { w[i * V + j] = 1.f; b[i * V + j] = 0.f; }
-    if (FULL || c < a.d) {
-      if (a.w) load<RN_F32, V>(a.w, c, w + i * V);
-      if (a.b) load<RN_F32, V>(a.b, c, b + i * V);
+    if (FIT == kFull || c < a.d) {
+      if (a.w) load<RN_F32, V, FIT>(a.w, c, a.d - c, w + i * V);
+      if (a.b) load<RN_F32, V, FIT>(a.b, c, a.d - c, b + i * V);
     }
   }
   const int64_t step = static_cast<int64_t>(gridDim.x) * R;
@@ -190,15 +208,15 @@ __global__ void __launch_bounds__(threads(W)) norm_rows(NormArgs a) {
       const int c = V * (lane + L * i);
 #pragma unroll
       for (int j = 0; j < V; ++j) h[i * V + j] = 0.f;
-      if (FULL || c < a.d) load<IN, V, STREAM>(a.x, row * a.xs + c, h + i * V);
+      if (FIT == kFull || c < a.d) load<IN, V, FIT, STREAM>(a.x, row * a.xs + c, a.d - c, h + i * V);
     }
     if (a.r) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = V * (lane + L * i);
-        if (FULL || c < a.d) {
+        if (FIT == kFull || c < a.d) {
           float t[V];
-          load<IN, V, STREAM>(a.r, row * a.rs + c, t);
+          load<IN, V, FIT, STREAM>(a.r, row * a.rs + c, a.d - c, t);
 #pragma unroll
           for (int j = 0; j < V; ++j) h[i * V + j] += t[j];
         }
@@ -208,7 +226,7 @@ __global__ void __launch_bounds__(threads(W)) norm_rows(NormArgs a) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = V * (lane + L * i);
-        if (FULL || c < a.d) store<IN, V, STREAM>(a.sum, row * a.ss + c, h + i * V);
+        if (FIT == kFull || c < a.d) store<IN, V, FIT, STREAM>(a.sum, row * a.ss + c, a.d - c, h + i * V);
       }
     }
     float s[1] = {0.f};
@@ -222,18 +240,18 @@ __global__ void __launch_bounds__(threads(W)) norm_rows(NormArgs a) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         h[i * V + j] -= mean;
-        if (FULL || V * (lane + L * i) < a.d) s2[0] = fmaf(h[i * V + j], h[i * V + j], s2[0]);
+        if (FIT == kFull || V * (lane + L * i) + (FIT == kOdd ? j : 0) < a.d) s2[0] = fmaf(h[i * V + j], h[i * V + j], s2[0]);
       }
     row_sums<W>(s2, red[1]);
     const float rstd = 1.0f / sqrtf(s2[0] / a.fd + a.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = V * (lane + L * i);
-      if (FULL || c < a.d) {
+      if (FIT == kFull || c < a.d) {
         float y[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) y[j] = fmaf(h[i * V + j] * rstd, w[i * V + j], b[i * V + j]);
-        store<OUT, V, STREAM>(a.out, row * a.os + c, y);
+        store<OUT, V, FIT, STREAM>(a.out, row * a.os + c, a.d - c, y);
       }
     }
   }
@@ -242,7 +260,7 @@ __global__ void __launch_bounds__(threads(W)) norm_rows(NormArgs a) {
 // With c = x - mean: the sums of c c, g and g c after the mean are all a row needs (mean(g xh)
 // is rstd mean(g c)), so a row takes two joins of the block. The next row's values are on
 // their way while a row is worked on.
-template <int IN, int OUT, int V, int W, int NV, bool FULL, bool STREAM>
+template <int IN, int OUT, int V, int W, int NV, Fit FIT, bool STREAM>
 __global__ void __launch_bounds__(threads(W)) norm_rows_backward(NormArgs a) {
   constexpr int L = 64 * W;
   constexpr int R = threads(W) / L;
@@ -253,16 +271,16 @@ __global__ void __launch_bounds__(threads(W)) norm_rows_backward(NormArgs a) {
   float dw[NV * V], db[NV * V];
 #pragma unroll
   for (int i = 0; i < NV * V; ++i) { dw[i] = 0.f; db[i] = 0.f; }
-  Raw<IN, V, STREAM> rx[NV], rr[NV];
-  Raw<OUT, V, STREAM> rg[NV];
+  Raw<IN, V, FIT, STREAM> rx[NV], rr[NV];
+  Raw<OUT, V, FIT, STREAM> rg[NV];
   auto fetch = [&](int64_t row) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = V * (lane + L * i);
-      if (FULL || c < a.d) {
-        rx[i].load(a.x, row * a.xs + c);
-        rg[i].load(a.dout, row * a.os + c);
-        if (a.r) rr[i].load(a.r, row * a.rs + c);
+      if (FIT == kFull || c < a.d) {
+        rx[i].load(a.x, row * a.xs + c, a.d - c);
+        rg[i].load(a.dout, row * a.os + c, a.d - c);
+        if (a.r) rr[i].load(a.r, row * a.rs + c, a.d - c);
       }
     }
   };
@@ -291,15 +309,15 @@ __global__ void __launch_bounds__(threads(W)) norm_rows_backward(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = V * (lane + L * i);
-      if (FULL || c < a.d) {
+      if (FIT == kFull || c < a.d) {
         float wt[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) wt[j] = 1.f;
-        if (a.w) load<RN_F32, V>(a.w, c, wt);
+        if (a.w) load<RN_F32, V, FIT>(a.w, c, a.d - c, wt);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           const int e = i * V + j;
-          x[e] -= mean;
+          x[e] = FIT != kOdd || c + j < a.d ? x[e] - mean : 0.f;
           db[e] += g[e];
           const float gw = g[e] * wt[j];
           m[0] = fmaf(x[e], x[e], m[0]);
@@ -314,11 +332,11 @@ __global__ void __launch_bounds__(threads(W)) norm_rows_backward(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = V * (lane + L * i);
-      if (FULL || c < a.d) {
+      if (FIT == kFull || c < a.d) {
         float wt[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) wt[j] = 1.f;
-        if (a.w) load<RN_F32, V>(a.w, c, wt);
+        if (a.w) load<RN_F32, V, FIT>(a.w, c, a.d - c, wt);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           const int e = i * V + j;
@@ -326,7 +344,7 @@ __global__ void __launch_bounds__(threads(W)) norm_rows_backward(NormArgs a) {
           dw[e] = fmaf(g[e], xh, dw[e]);
           t[e] = fmaf(rstd, g[e] * wt[j] - sg - xh * sgx, t[e]);
         }
-        store<IN, V, STREAM>(a.sum, row * a.ss + c, t + i * V);
+        store<IN, V, FIT, STREAM>(a.sum, row * a.ss + c, a.d - c, t + i * V);
       }
     }
   }
@@ -351,9 +369,10 @@ __global__ void __launch_bounds__(threads(W)) norm_rows_backward(NormArgs a) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           const int c = V * (lane + L * i);
-          if (FULL || c < a.d) {
+          if (FIT == kFull || c < a.d) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) part[static_cast<int64_t>(which) * a.d + c + j] = merge[(i * V + j) * 64 + lane];
+            for (int j = 0; j < V; ++j)
+              if (FIT != kOdd || c + j < a.d) part[static_cast<int64_t>(which) * a.d + c + j] = merge[(i * V + j) * 64 + lane];
           }
         }
       }
@@ -363,9 +382,9 @@ __global__ void __launch_bounds__(threads(W)) norm_rows_backward(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = V * (lane + L * i);
-      if (FULL || c < a.d) {
-        store<RN_F32, V>(part, c, dw + i * V);
-        store<RN_F32, V>(part + a.d, c, db + i * V);
+      if (FIT == kFull || c < a.d) {
+        store<RN_F32, V, FIT>(part, c, a.d - c, dw + i * V);
+        store<RN_F32, V, FIT>(part + a.d, c, a.d - c, db + i * V);
       }
     }
   }
@@ -400,17 +419,17 @@ int backward_blocks(const NormCall& n) {
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((n.rows + 3) / 4, 768)));
 }
 
-template <int IN, int OUT, int V, int W, int NV, bool FULL, bool STREAM>
+template <int IN, int OUT, int V, int W, int NV, Fit FIT, bool STREAM>
 hipError_t launch_full(const NormCall& n, NormArgs a, hipStream_t st) {
   if (!n.backward) {
     constexpr int R = threads(W) / (64 * W);
     const int64_t need = (n.rows + R - 1) / R;
-    hipLaunchKernelGGL((norm_rows<IN, OUT, V, W, NV, FULL, STREAM>), dim3(static_cast<unsigned>(std::min<int64_t>(need, 2048))),
+    hipLaunchKernelGGL((norm_rows<IN, OUT, V, W, NV, FIT, STREAM>), dim3(static_cast<unsigned>(std::min<int64_t>(need, 2048))),
                        dim3(threads(W)), 0, st, a);
     return hipGetLastError();
   }
   const int blocks = backward_blocks(n);
-  hipLaunchKernelGGL((norm_rows_backward<IN, OUT, V, W, NV, FULL, STREAM>), dim3(blocks), dim3(threads(W)), 0, st, a);
+  hipLaunchKernelGGL((norm_rows_backward<IN, OUT, V, W, NV, FIT, STREAM>), dim3(blocks), dim3(threads(W)), 0, st, a);
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && a.part) {
     hipLaunchKernelGGL(norm_reduce, dim3((2 * n.d + 31) / 32), dim3(1024), 0, st, a.part, blocks, n.d, n.dw, n.db);
@@ -419,19 +438,16 @@ hipError_t launch_full(const NormCall& n, NormArgs a, hipStream_t st) {
   return e;
 }
 
-// FULL: every lane has all its vectors, so that no access hangs on a condition.
 template <int IN, int OUT, int V, int W, int NV>
 hipError_t launch_one(const NormCall& n, const NormArgs& a, hipStream_t st) {
-  if constexpr (V > 1)
-    if (n.d == V * 64 * W * NV) {
-      // the call's bytes against the 256 MB last-level cache
-      // (16384 x 4096 bf16 with residual: 96 us past the caches, 103 us through them; backward
-      // 108 and 114 us)
-      const int64_t bytes = n.rows * n.d * ((IN == RN_F32 ? 4 : 2) * (n.r ? 2 : 1) + (OUT == RN_F32 ? 4 : 2) + (n.sum ? (IN == RN_F32 ? 4 : 2) : 0));
-      return bytes > (int64_t(256) << 20) ? launch_full<IN, OUT, V, W, NV, true, true>(n, a, st)
-                                          : launch_full<IN, OUT, V, W, NV, true, false>(n, a, st);
-    }
-  return launch_full<IN, OUT, V, W, NV, false, false>(n, a, st);
+  if (!n.vec) return launch_full<IN, OUT, V, W, NV, kOdd, false>(n, a, st);
+  if (n.d != V * 64 * W * NV) return launch_full<IN, OUT, V, W, NV, kSome, false>(n, a, st);
+  // the call's bytes against the 256 MB last-level cache
+  // (16384 x 4096 bf16 with residual: 96 us past the caches, 103 us through them; backward
+  // 108 and 114 us)
+  const int64_t bytes = n.rows * n.d * ((IN == RN_F32 ? 4 : 2) * (n.r ? 2 : 1) + (OUT == RN_F32 ? 4 : 2) + (n.sum ? (IN == RN_F32 ? 4 : 2) : 0));
+  return bytes > (int64_t(256) << 20) ? launch_full<IN, OUT, V, W, NV, kFull, true>(n, a, st)
+                                      : launch_full<IN, OUT, V, W, NV, kFull, false>(n, a, st);
 }
 
 template <int IN, int OUT>
@@ -439,28 +455,19 @@ hipError_t launch_t(const NormCall& n, const NormArgs& a, hipStream_t st) {
   // Waves a row and vectors a lane: at most 16 values of each tensor a lane, so that two rows
   // (one worked on, one on its way) and the sums over rows fit in its registers.
   constexpr int V = IN == RN_BF16 ? 8 : 4;   // 16 bytes of the input type
-  if (n.vec) {
-    const int nv = (n.d / V + 63) / 64;      // vectors a lane of one wave
-    if (nv <= 1) return launch_one<IN, OUT, V, 1, 1>(n, a, st);
-    if (nv <= 2) return launch_one<IN, OUT, V, 1, 2>(n, a, st);
-    if (nv <= 4) return launch_one<IN, OUT, V, 4, 1>(n, a, st);
-    if (nv <= 8) return launch_one<IN, OUT, V, 4, 2>(n, a, st);
-    if constexpr (V == 8) {
-      if (nv <= 16) return launch_one<IN, OUT, V, 16, 1>(n, a, st);
-      return launch_one<IN, OUT, V, 16, 2>(n, a, st);
-    } else {
-      if (nv <= 16) return launch_one<IN, OUT, V, 4, 4>(n, a, st);
-      if (nv <= 32) return launch_one<IN, OUT, V, 16, 2>(n, a, st);
-      return launch_one<IN, OUT, V, 16, 4>(n, a, st);
-    }
+  const int nv = ((n.d + V - 1) / V + 63) / 64;      // vectors a lane of one wave
+  if (nv <= 1) return launch_one<IN, OUT, V, 1, 1>(n, a, st);
+  if (nv <= 2) return launch_one<IN, OUT, V, 1, 2>(n, a, st);
+  if (nv <= 4) return launch_one<IN, OUT, V, 4, 1>(n, a, st);
+  if (nv <= 8) return launch_one<IN, OUT, V, 4, 2>(n, a, st);
+  if constexpr (V == 8) {
+    if (nv <= 16) return launch_one<IN, OUT, V, 16, 1>(n, a, st);
+    return launch_one<IN, OUT, V, 16, 2>(n, a, st);
+  } else {
+    if (nv <= 16) return launch_one<IN, OUT, V, 4, 4>(n, a, st);
+    if (nv <= 32) return launch_one<IN, OUT, V, 16, 2>(n, a, st);
+    return launch_one<IN, OUT, V, 16, 4>(n, a, st);
   }
-  const int nv = (n.d + 63) / 64;
-  if (nv <= 4) return launch_one<IN, OUT, 1, 1, 4>(n, a, st);
-  if (nv <= 16) return launch_one<IN, OUT, 1, 4, 4>(n, a, st);
-  if (nv <= 32) return launch_one<IN, OUT, 1, 4, 8>(n, a, st);
-  if (nv <= 64) return launch_one<IN, OUT, 1, 16, 4>(n, a, st);
-  if (nv <= 128) return launch_one<IN, OUT, 1, 16, 8>(n, a, st);
-  return launch_one<IN, OUT, 1, 16, 16>(n, a, st);
 }
 
 }  // namespace
