@@ -2,7 +2,7 @@
 // coordinates is turned by p theta_j and scaled; the coordinates behind are copied.
 //
 // Bound by HBM (each value read and written once: 16384 tokens of 40 heads of 128, half of each
-// turned, bf16: 76 us, 4.4 TB/s; 2 x 2047 tokens of 32 heads of 256 float32: 61 us, 4.4 TB/s) as
+// turned, bf16: 73 us, 4.6 TB/s; 2 x 2047 tokens of 32 heads of 256 float32: 59 us, 4.6 TB/s) as
 // long as the sines stay cheap: an angle
 // takes a float64 product and reduction and a float32 sine and cosine, about as long as
 // moving forty values. So a block takes a few tokens, forms their cosines and sines once,
@@ -36,22 +36,34 @@ struct RotArgs {
   double theta[kMaxRot / 2];
 };
 
-// V elements as they are in memory: 16 bytes for V > 1.
+// V elements as they are in memory, at any element's address (memory takes them so).
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u32x1 __attribute__((aligned(2)));
 template <int DT, int V>
 struct Piece {
-  uint4 r;
+  static constexpr int kBytes = V * (DT == RN_F32 ? 4 : 2);
+  uint32_t u[kBytes < 4 ? 1 : kBytes / 4];
   __device__ __forceinline__ void load(const char* p) {
-    if constexpr (V > 1) r = *reinterpret_cast<const uint4*>(p);
-    else if constexpr (DT == RN_F32) r.x = *reinterpret_cast<const uint32_t*>(p);
-    else r.x = *reinterpret_cast<const uint16_t*>(p);
+    if constexpr (kBytes == 16) {
+      const u32x4 x = *reinterpret_cast<const u32x4*>(p);
+      u[0] = x[0]; u[1] = x[1]; u[2] = x[2]; u[3] = x[3];
+    } else if constexpr (kBytes == 8) {
+      const u32x2 x = *reinterpret_cast<const u32x2*>(p);
+      u[0] = x[0]; u[1] = x[1];
+    } else if constexpr (kBytes == 4) {
+      u[0] = *reinterpret_cast<const u32x1*>(p);
+    } else {
+      u[0] = *reinterpret_cast<const uint16_t*>(p);
+    }
   }
   __device__ __forceinline__ void store(char* p) const {
-    if constexpr (V > 1) *reinterpret_cast<uint4*>(p) = r;
-    else if constexpr (DT == RN_F32) *reinterpret_cast<uint32_t*>(p) = r.x;
-    else *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(r.x);
+    if constexpr (kBytes == 16) *reinterpret_cast<u32x4*>(p) = u32x4{u[0], u[1], u[2], u[3]};
+    else if constexpr (kBytes == 8) *reinterpret_cast<u32x2*>(p) = u32x2{u[0], u[1]};
+    else if constexpr (kBytes == 4) *reinterpret_cast<u32x1*>(p) = u[0];
+    else *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(u[0]);
   }
   __device__ __forceinline__ void get(float* f) const {
-    const uint32_t u[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       if constexpr (DT == RN_F32) f[j] = __uint_as_float(u[j]);
@@ -60,14 +72,13 @@ struct Piece {
   }
   __device__ __forceinline__ void set(const float* f) {
     if constexpr (DT == RN_F32) {
-      uint32_t u[4] = {};
 #pragma unroll
       for (int j = 0; j < V; ++j) u[j] = __float_as_uint(f[j]);
-      r = make_uint4(u[0], u[1], u[2], u[3]);
     } else if constexpr (V == 1) {
-      r.x = f32_to_bf16(f[0]);
+      u[0] = f32_to_bf16(f[0]);
     } else {
-      r = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) u[j] = pack_bf16x2(f[2 * j], f[2 * j + 1]);
     }
   }
 };
@@ -201,16 +212,11 @@ __global__ void __launch_bounds__(kThreads) rotary(RotArgs a, int lanes) {
 
 template <int DT>
 hipError_t launch_t(const RotaryCall& c, RotArgs& a, hipStream_t st) {
-  constexpr int V = DT == RN_BF16 ? 8 : 4;
   const int half = a.rot / 2;
-  // 16-byte accesses need every run of coordinates, stride and pointer in whole vectors
-  bool vec = a.d % V == 0 && (c.half ? half % V == 0 : a.rot % V == 0);
-  for (int i = 0; i < 2; ++i) {
-    if (i == 1 && c.Hk == 0) break;
-    vec = vec && reinterpret_cast<uintptr_t>(a.in[i]) % 16 == 0 && reinterpret_cast<uintptr_t>(a.out[i]) % 16 == 0;
-    for (int j = 0; j < 3; ++j) vec = vec && a.s[i][j] % V == 0 && a.s[2 + i][j] % V == 0;
-  }
-  const int w = vec ? V : 1;
+  // Elements a piece: the most of 16 bytes that divide every run of coordinates (37 x 222 tokens of
+  // 80 heads of 102 bf16, a position per token: 135 us in twos, 244 us one by one).
+  int w = DT == RN_BF16 ? 8 : 4;
+  while (w > 1 && (a.d % w || (c.half ? half : a.rot) % w)) w /= 2;
   const int units = (half + w - 1) / w + (a.d - a.rot + 2 * w - 1) / (2 * w);
   int lanes = 1;
   while (lanes < units && lanes < 64) lanes *= 2;
@@ -224,13 +230,16 @@ hipError_t launch_t(const RotaryCall& c, RotArgs& a, hipStream_t st) {
   a.tile = tile;
   a.heads = (a.H + groups - 1) / groups;
   const dim3 grid(static_cast<unsigned>(tiles), (a.H + a.heads - 1) / a.heads);
-  if (c.half) {
-    if (vec) hipLaunchKernelGGL((rotary<DT, V, true>), grid, dim3(kThreads), 0, st, a, lanes);
-    else hipLaunchKernelGGL((rotary<DT, 1, true>), grid, dim3(kThreads), 0, st, a, lanes);
-  } else {
-    if (vec) hipLaunchKernelGGL((rotary<DT, V, false>), grid, dim3(kThreads), 0, st, a, lanes);
-    else hipLaunchKernelGGL((rotary<DT, 1, false>), grid, dim3(kThreads), 0, st, a, lanes);
+#define RN_ROTARY(W)                                                                                             \
+  if (w == W) {                                                                                                  \
+    if (c.half) hipLaunchKernelGGL((rotary<DT, W, true>), grid, dim3(kThreads), 0, st, a, lanes);                \
+    else hipLaunchKernelGGL((rotary<DT, W, false>), grid, dim3(kThreads), 0, st, a, lanes);                      \
   }
+  if constexpr (DT == RN_BF16) RN_ROTARY(8)
+  RN_ROTARY(4)
+  RN_ROTARY(2)
+  RN_ROTARY(1)
+#undef RN_ROTARY
   return hipGetLastError();
 }
 

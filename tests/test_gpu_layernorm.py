@@ -228,3 +228,30 @@ def test_refusals():
         rn().rn_layernorm(torch.zeros(64, 4, device=DEV).t())
     with pytest.raises(rn().RnError, match="RN_ERR_UNSUPPORTED"):
         rn().rn_layernorm(torch.zeros(1, 16392, device=DEV))
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("n,d", [(40, 64), (9, 1001), (5, 4096), (3, 9003)])
+def test_tensors_that_start_at_any_element(kind, n, d):
+    """x, residual, weight, bias and the outputs one element into their buffers: the same bits as
+    from aligned copies where the pieces are the same, and nothing in front of or behind them."""
+    dt = DT[kind]
+    g = torch.Generator().manual_seed(d)
+    flat = lambda t: torch.cat([t.new_full((1,), 7.0), t.reshape(-1), t.new_full((1,), 7.0)]).to(DEV)  # noqa: E731
+    bufs = [flat(rows(g, n, d, dt)) for _ in range(5)]
+    x, r, out, total, dy = (b[1:-1].view(n, d) for b in bufs)
+    wb = [flat(torch.randn(d, generator=g)) for _ in range(2)]
+    w, b = (t[1:-1] for t in wb)
+    y, h = K.layernorm(x.cpu(), w.cpu(), b.cpu(), 1e-5, r.cpu())
+    xh, _ = K.layernorm(x.cpu(), None, None, 1e-5, r.cpu())
+    rn().rn_layernorm(x, w, b, residual=r, out=out, sum_out=total)
+    rms = np.sqrt((h * h).mean(-1, keepdims=True) / (h.var(-1, keepdims=True) + 1e-5))
+    check(out, y, 80 * U * (rms + np.abs(xh)) * np.abs(np64(w)) + 2 * U * np.abs(np64(b)) + half_step(dt) * 1.01 * np.abs(y) + 1e-30)
+    check(total, h, (U + half_step(dt)) * 1.01 * np.abs(h))
+    want = rn().rn_layernorm_backward(dy.clone(), total.clone(), w.clone())
+    got = rn().rn_layernorm_backward(dy, total, w, dx=x)
+    scale = {k: float(v.abs().max()) for k, v in want.items()}
+    for k in ("dx", "dweight", "dbias"):     # the two differ in the order of float32 sums and in dx's rounding
+        assert float((got[k].float() - want[k].float()).abs().max()) <= (1e-5 + 2 * half_step(got[k].dtype)) * scale[k]
+    for t in bufs + wb:
+        assert float(t[0]) == 7.0 and float(t[-1]) == 7.0

@@ -163,3 +163,24 @@ def test_refusals():
         rn().rn_rotary(q.half(), None, th)
     with pytest.raises(ValueError):
         rn().rn_rotary(q[:, :, :0], None, th)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("d,rot", [(102, 102), (102, 4), (66, 50), (36, 12), (44, 24), (40, 40)])
+def test_pieces_of_every_size_at_any_address(kind, half, d, rot):
+    """Head sizes that pieces of 2, 4 and 8 elements divide, in views that start one element in
+    and whose rows are an odd number of elements apart: nothing around them is written."""
+    B, N, H = 2, 21, 3
+    g = torch.Generator().manual_seed(d + rot)
+    theta = 50.0 ** (-2.0 * np.arange(rot // 2) / rot)
+    wide = torch.randn(B, N, H, d + 3, generator=g).to(DT[kind]).to(DEV)
+    x = wide[..., 1:1 + d].transpose(1, 2)
+    into = torch.full((B, H, N, d + 1), 7.0, dtype=DT[kind], device=DEV)
+    got = rn().rn_rotary(x, None, theta, pos0=3, half=half, q_out=into[..., 1:])
+    check(got, x, theta, np.arange(N)[None].repeat(B, 0) + 3, half, False, 1.0)
+    assert torch.equal(got[..., rot:], x[..., rot:]) and (into[..., 0] == 7.0).all()
+    before = wide.clone()
+    rn().rn_rotary(x, None, theta, pos0=3, half=half, q_out=x)
+    assert torch.equal(x, got)
+    assert torch.equal(wide[..., 0], before[..., 0]) and torch.equal(wide[..., 1 + d:], before[..., 1 + d:])
