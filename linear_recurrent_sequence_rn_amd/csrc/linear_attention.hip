@@ -4,7 +4,7 @@
 // lin_step: one token a sequence. Bound by HBM: the float32 state is read and written once.
 // lin_float: prompts of any type and head size in chunks of 16 tokens on the float32 matrix cores.
 // Bound by the wait for each chunk's phases and the padding of small heads (padded float32 batch of
-// 3 sequences of up to 2001 tokens, 5 heads of 48 x 81: 33 us, of which the scan is 8; 32 heads of
+// 3 sequences of up to 2001 tokens, 5 heads of 48 x 81: 32 us, of which the scan is 8; 32 heads of
 // 2048 tokens, 128 x 128: 129 us). The recurrence itself, token by token on the vector units,
 // took 39 and 172 us.
 // Long sequences are cut into segments: one pass gives the state each segment adds on its own,
@@ -443,14 +443,14 @@ __global__ void __launch_bounds__(256) lin_scan(LinArgs a) {
   float* p = a.seg_state + first * sh + e;
   const float* d = a.seg_decay + first;
   const int64_t ps = sh * a.H;
-  // sixteen segments' states in flight
-  for (int g = 0; g < n; g += 16) {
-    fv u[16];
+  // eight segments' states in flight
+  for (int g = 0; g < n; g += 8) {
+    fv u[8];
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < 8; ++i)
       if (g + i < n && (last || g + i + 1 < n)) u[i] = *reinterpret_cast<const fv*>(p + (g + i) * ps);
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < 8; ++i)
       if (g + i < n) {
         *reinterpret_cast<fv*>(p + (g + i) * ps) = x;
         if (last || g + i + 1 < n) {
@@ -541,7 +541,8 @@ bool mfma_call(const LinCall& c) {
 // Tokens a segment, and how many segments the longest sequence has: one where the sequences and
 // heads fill the chip by themselves; else enough that the blocks of all segments do. Cutting
 // costs a second pass over the tokens for the states and the scan over them, so a longest
-// sequence of less than three segments stays whole.
+// sequence of less than three segments stays whole. (In float32, segments of
+// 32 tokens: 8 heads of 300, 64 x 64, 24 -> 21 us, but of 2000 32 -> 40.)
 void segments(const LinCall& c, int* len, int* n) {
   const bool mfma = mfma_shape(c);
   const int64_t per = mfma ? lin_mfma_blocks(lin_args(c)) : static_cast<int64_t>(c.H) * ((c.dv + kCols - 1) / kCols);
