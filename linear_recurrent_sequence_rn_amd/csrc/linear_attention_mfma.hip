@@ -20,11 +20,11 @@
 // The next tiles are on their way in registers meanwhile.
 //
 // What bounds it: heads of 256 x 512, the matrix cores at the clock they reach under load (8192
-// tokens, 16 heads: states 130 us, scan 13 us, outputs 235 us for 225 GFLOP, of which the three
+// tokens, 16 heads: states 130 us, scan 13 us, outputs 229 us for 225 GFLOP, of which the three
 // parts of w V are 103; one large bf16 product reaches 1230 TFLOP/s on the card). Heads of 64 and
 // 128: instruction issue, about 390 vector and 43 matrix instructions a wave and chunk at d_k 64,
-// with two or three blocks a CU (13 packed sequences, 14001 tokens, 32 heads of 64 x 128: 138 us,
-// 2.1 TB/s; 8 sequences of 2048 tokens, 32 heads of 128 x 128: 180 us, 3.0 TB/s).
+// with two or three blocks a CU (13 packed sequences, 14001 tokens, 32 heads of 64 x 128: 135 us,
+// 2.1 TB/s; 8 sequences of 2048 tokens, 32 heads of 128 x 128: 169 us, 3.2 TB/s).
 //
 // Rounding: the scores times their decay, and the copy of the state that Q S reads, are rounded
 // to bf16 once (the outputs are bf16 themselves). The state is float32: w o V is split in
