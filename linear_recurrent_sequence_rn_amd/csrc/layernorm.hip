@@ -8,8 +8,9 @@
 // Bound by HBM: every tensor is read or written once (16384 x 4096 bf16: forward with residual
 // 96 us, 5.6 TB/s; backward with the residual's gradient 109 us, 5.0 TB/s; a large copy reaches
 // 4.9 to 5.4 TB/s on the card). Smaller calls are bound by latency (backward of 3001 x 1537
-// float32: 22 us, of which the reduction of the weights' sums 5). A row lives in the registers of one
-// wave (W = 1, four rows per 256-thread block) or of a whole block (W = 4 or 16), so the passes
+// float32: 22 us, of which the reduction of the weights' sums 5). A row lives in the registers of 16
+// lanes (W = 0, 16 rows per 256-thread block), of one wave (W = 1) or of a whole block (W = 4 or
+// 16), so the passes
 // over it (mean, centred squares, result) cost no memory access. Blocks walk over rows:
 // the weights, and in the backward the column sums of dw and db, then stay in registers
 // too, and the backward writes one partial row of sums per block, which a second kernel
@@ -23,14 +24,14 @@
 namespace rn {
 namespace {
 
-// Threads of a block whose rows take W waves each.
+// Threads of a block whose rows take W waves each (0: 16 lanes), and lanes of a row.
 constexpr int threads(int W) { return W > 4 ? 64 * W : 256; }
+constexpr int lanes(int W) { return W ? 64 * W : 16; }
 
 // How a row falls into pieces of V elements: every lane has all its pieces; some have none; or rows
 // start anywhere and the last piece may be short. Memory takes 16-byte accesses at any element's
 // address, so the last kind differs only in that piece (backward of 3001 x 1537 float32: 22 us, element
-// by element 27; of 2000 x 10001 bf16: 75 and 216 us; forward 44 and 77. Only rows much shorter than
-// a wave's lanes lose: 20000 x 101 bf16, backward 26 and 18 us).
+// by element 27; of 2000 x 10001 bf16: 75 and 216 us; forward 44 and 77).
 enum Fit : int { kFull, kSome, kOdd };
 
 // 16 or 8 bytes, past the caches with STREAM (which pays for calls larger than the last-level
@@ -145,12 +146,24 @@ __device__ __forceinline__ float wave_total(float x) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 63));
 }
 
+// Sum over the 16 lanes of each row of a wave, in all of them.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float row_total(float x) {
+  x += dpp<0xB1>(x);                      // lane ^ 1
+  x += dpp<0x4E>(x);                      // lane ^ 2
+  x += dpp<0x141>(x);                     // lane i <-> 7 - i within 8
+  return x + dpp<0x140>(x);               // lane i <-> 15 - i
+}
+
 // Sums of N values over the W waves that share a row; every thread receives them. `red` holds
 // W N floats. The caller does not write the same area again before a barrier has passed since.
 template <int W, int N>
 __device__ __forceinline__ void row_sums(float (&x)[N], float* red) {
 #pragma unroll
-  for (int n = 0; n < N; ++n) x[n] = wave_total(x[n]);
+  for (int n = 0; n < N; ++n) x[n] = W ? wave_total(x[n]) : row_total(x[n]);
   if constexpr (W > 1) {
     const int w = threadIdx.x >> 6;
     if ((threadIdx.x & 63) == 0) {
@@ -182,12 +195,12 @@ struct NormArgs {
   float* part;              // partial sums of the backward: [blocks][2][d] or null
 };
 
-// Thread `lane` of a row's 64 W lanes holds elements [V (lane + 64 W i), +V) for i < NV.
+// Thread `lane` of a row's L lanes holds elements [V (lane + L i), +V) for i < NV.
 template <int IN, int OUT, int V, int W, int NV, Fit FIT, bool STREAM>
 __global__ void __launch_bounds__(threads(W)) norm_rows(NormArgs a) {
-  constexpr int L = 64 * W;
+  constexpr int L = lanes(W);
   constexpr int R = threads(W) / L;       // rows per block
-  __shared__ float red[2][W];
+  __shared__ float red[2][W ? W : 1];
   const int lane = threadIdx.x % L;
   float w[NV * V], b[NV * V];
 #pragma unroll
@@ -262,11 +275,11 @@ __global__ void __launch_bounds__(threads(W)) norm_rows(NormArgs a) {
 // their way while a row is worked on.
 template <int IN, int OUT, int V, int W, int NV, Fit FIT, bool STREAM>
 __global__ void __launch_bounds__(threads(W)) norm_rows_backward(NormArgs a) {
-  constexpr int L = 64 * W;
+  constexpr int L = lanes(W);
   constexpr int R = threads(W) / L;
   constexpr bool kAhead = W < 16 || NV * V <= 4;   // blocks of 16 waves have 128 registers a lane
-  __shared__ float red[2][4 * W];         // rows take the areas in turn
-  __shared__ float merge[W == 1 ? 64 * NV * V : 1];
+  __shared__ float red[2][W ? 4 * W : 1];         // rows take the areas in turn
+  __shared__ float merge[W <= 1 ? L * NV * V : 1];
   const int lane = threadIdx.x % L;
   float dw[NV * V], db[NV * V];
 #pragma unroll
@@ -350,29 +363,36 @@ __global__ void __launch_bounds__(threads(W)) norm_rows_backward(NormArgs a) {
   }
   if (!a.part) return;
   float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.d;
-  if constexpr (W == 1) {
-    // the four waves' sums, added in their order
+  if constexpr (W <= 1) {
+    // the sums of a wave's rows, then of the four waves, added in their order
+    if constexpr (W == 0) {
+#pragma unroll
+      for (int i = 0; i < NV * V; ++i) {
+        dw[i] += __shfl_xor(dw[i], 16); dw[i] += __shfl_xor(dw[i], 32);
+        db[i] += __shfl_xor(db[i], 16); db[i] += __shfl_xor(db[i], 32);
+      }
+    }
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
       float* v = which ? db : dw;
       for (int wv = 0; wv < 4; ++wv) {
-        if (static_cast<int>(threadIdx.x >> 6) == wv) {
+        if (static_cast<int>(threadIdx.x >> 6) == wv && (threadIdx.x & 63) < L) {
 #pragma unroll
           for (int i = 0; i < NV * V; ++i) {
-            float* m = &merge[i * 64 + lane];
+            float* m = &merge[i * L + lane];
             *m = wv == 0 ? v[i] : *m + v[i];
           }
         }
         __syncthreads();
       }
-      if (threadIdx.x < 64) {
+      if (threadIdx.x < L) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           const int c = V * (lane + L * i);
           if (FIT == kFull || c < a.d) {
 #pragma unroll
             for (int j = 0; j < V; ++j)
-              if (FIT != kOdd || c + j < a.d) part[static_cast<int64_t>(which) * a.d + c + j] = merge[(i * V + j) * 64 + lane];
+              if (FIT != kOdd || c + j < a.d) part[static_cast<int64_t>(which) * a.d + c + j] = merge[(i * V + j) * L + lane];
           }
         }
       }
@@ -412,17 +432,23 @@ __global__ void __launch_bounds__(1024) norm_reduce(const float* part, int block
   }
 }
 
+// Rows that 16 lanes hold in two pieces each: four rows a wave (262144 x 128 bf16: forward 42 us,
+// backward 44; with a wave a row 80 and 135).
+bool narrow(const NormCall& n) { return n.d <= 32 * (n.in_dt == RN_BF16 ? 8 : 4); }
+
 int backward_blocks(const NormCall& n) {
-  // Three blocks a CU, which is what their registers allow, and at least four rows a block, so
+  // Three blocks a CU, which is what their registers allow, and at least four rows a block (16
+  // narrow ones, which it takes at a time), so
   // that the partial rows (2 d floats a block, written and read once) stay small beside the
   // tensors.
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((n.rows + 3) / 4, 768)));
+  const int rows = narrow(n) ? 16 : 4;
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((n.rows + rows - 1) / rows, 768)));
 }
 
 template <int IN, int OUT, int V, int W, int NV, Fit FIT, bool STREAM>
 hipError_t launch_full(const NormCall& n, NormArgs a, hipStream_t st) {
   if (!n.backward) {
-    constexpr int R = threads(W) / (64 * W);
+    constexpr int R = threads(W) / lanes(W);
     const int64_t need = (n.rows + R - 1) / R;
     hipLaunchKernelGGL((norm_rows<IN, OUT, V, W, NV, FIT, STREAM>), dim3(static_cast<unsigned>(std::min<int64_t>(need, 2048))),
                        dim3(threads(W)), 0, st, a);
@@ -441,7 +467,7 @@ hipError_t launch_full(const NormCall& n, NormArgs a, hipStream_t st) {
 template <int IN, int OUT, int V, int W, int NV>
 hipError_t launch_one(const NormCall& n, const NormArgs& a, hipStream_t st) {
   if (!n.vec) return launch_full<IN, OUT, V, W, NV, kOdd, false>(n, a, st);
-  if (n.d != V * 64 * W * NV) return launch_full<IN, OUT, V, W, NV, kSome, false>(n, a, st);
+  if (n.d != V * lanes(W) * NV) return launch_full<IN, OUT, V, W, NV, kSome, false>(n, a, st);
   // the call's bytes against the 256 MB last-level cache
   // (16384 x 4096 bf16 with residual: 96 us past the caches, 103 us through them; backward
   // 108 and 114 us)
@@ -456,6 +482,7 @@ hipError_t launch_t(const NormCall& n, const NormArgs& a, hipStream_t st) {
   // (one worked on, one on its way) and the sums over rows fit in its registers.
   constexpr int V = IN == RN_BF16 ? 8 : 4;   // 16 bytes of the input type
   const int nv = ((n.d + V - 1) / V + 63) / 64;      // vectors a lane of one wave
+  if (narrow(n)) return n.d <= 16 * V ? launch_one<IN, OUT, V, 0, 1>(n, a, st) : launch_one<IN, OUT, V, 0, 2>(n, a, st);
   if (nv <= 1) return launch_one<IN, OUT, V, 1, 1>(n, a, st);
   if (nv <= 2) return launch_one<IN, OUT, V, 1, 2>(n, a, st);
   if (nv <= 4) return launch_one<IN, OUT, V, 4, 1>(n, a, st);

@@ -255,3 +255,11 @@ def test_tensors_that_start_at_any_element(kind, n, d):
         assert float((got[k].float() - want[k].float()).abs().max()) <= (1e-5 + 2 * half_step(got[k].dtype)) * scale[k]
     for t in bufs + wb:
         assert float(t[0]) == 7.0 and float(t[-1]) == 7.0
+
+
+@pytest.mark.parametrize("n,d", [(1, 17), (15, 64), (1000, 65), (777, 129), (300, 200), (50, 255), (13000, 128), (33, 257)])
+@pytest.mark.parametrize("kind", ["f32", "bf16", "bf16->f32"])
+def test_narrow_rows(n, d, kind):
+    """Rows of a head's width, several to a wave, in numbers that leave waves and blocks part empty."""
+    test_forward(n, d, kind)
+    test_backward(n, d, kind)
