@@ -498,9 +498,9 @@ rn_status rn_rotary_frequencies(int32_t rot, double base, int32_t kind, double f
  *
  * Precision: prompts with bf16 inputs and a bf16 output run matrix products where d_k and d_v are
  * multiples of 8 and rows start on 16 bytes (strides multiples of 8, pointers 16-byte aligned):
- * scores and the state's copy read by the queries are rounded to bf16, the state itself is
- * carried in float32 from products of three bf16 parts (float32 accuracy). All other calls run
- * float32 arithmetic throughout.
+ * scores and the state's copy read by the queries enter them in two bf16 parts (2^-16 relative, so
+ * that an output is the float32 result rounded once), the state itself is carried in float32 from
+ * products of three bf16 parts (float32 accuracy). All other calls run float32 arithmetic throughout.
  * Outputs must not overlap the inputs (states: see below).
  * A NaN or infinity in a token's q, k, v or decay reaches only outputs of that token and later
  * ones of its sequence, and the final state.

@@ -26,10 +26,12 @@
 // with two or three blocks a CU (13 packed sequences, 14001 tokens, 32 heads of 64 x 128: 135 us,
 // 2.1 TB/s; 8 sequences of 2048 tokens, 32 heads of 128 x 128: 169 us, 3.2 TB/s).
 //
-// Rounding: the scores times their decay, and the copy of the state that Q S reads, are rounded
-// to bf16 once (the outputs are bf16 themselves). The state is float32: w o V is split in
-// three bf16 parts, which hold all 24 bits of it, and K is bf16 already, so that the products
-// carry float32 accuracy (two parts where only outputs, not the final state, depend on it).
+// Rounding: Q, K and V are bf16 already, and what is formed from them in float32 enters a product
+// in several bf16 parts. Outputs depend on two parts of each score times its decay, of the state's
+// copy that Q S reads and, in the pass that only gives outputs, of w o V: what two parts leave out is
+// at most 2^-16 of the value, 1/256 of the one rounding that a bf16 output takes (one part, which is
+// 45 of 343 us less for 8192 tokens of 16 heads of 256 x 512, doubles that rounding). The state that
+// is kept is float32: w o V in three parts, which hold all 24 bits of it.
 #include <type_traits>
 
 #include "linear_attention.h"
@@ -90,6 +92,18 @@ __device__ __forceinline__ bf16x8 col_operand(const char* tile, int base, int ks
   v.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + ROWS));
   return __builtin_bit_cast(bf16x8, v);
 }
+
+// Byte offset of a score's lower part, from that of its upper part: queries 0 .. 31 (row tiles 0 and
+// 1) see keys 0 .. 31 only, whose lower parts take the columns 32 .. 63 of the same rows; the
+// others' are in two more row tiles.
+__device__ __forceinline__ int low_part(int p, int tile) {
+  const int t0 = tile * kRows<kChunk>;
+  return tile < 2 ? ((p - t0) ^ 64) + t0 : p + 2 * kRows<kChunk>;
+}
+
+// For the lower parts of values of which the largest is `top`: none where an upper part is an
+// infinity (what is left of it would be a NaN; the output that such values reach has no others).
+__device__ __forceinline__ uint32_t low_mask(float top) { return top <= 0x1.fep127f ? ~0u : 0u; }
 
 struct alignas(16) Decays {   // of one chunk
   float c[kChunk];       // running sum of log2 decays
@@ -229,12 +243,13 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
   constexpr int OT = 4 / DW;             // 16-query tiles of the output a wave finishes
   constexpr int PARTS = MODE == kLinOut ? 2 : 3;
   constexpr bool kOut = MODE != kLinState;
-  constexpr int kTileQ = 4 * kRows<DK>, kTileV = kChunk * DV * 2, kTileP = 4 * kRows<kChunk>;
+  // (the scores' upper parts in four row tiles; see low_part() for the lower ones)
+  constexpr int kTileQ = 4 * kRows<DK>, kTileV = kChunk * DV * 2, kTileP = 6 * kRows<kChunk>;
   constexpr int kSwap = DW == 2 ? VW * DW * 2 * VT * 1024 : 0;
   // Two waves need each part of w V where DW is 2: they are formed once, on the way to LDS, as
   // long as the tiles fit in it; else each wave forms its own in registers.
   constexpr int kBase = kTileQ + (kOut ? kTileV + kTileQ + kTileP + kSwap : 0);
-  constexpr bool kParts = DW == 2 && kBase + PARTS * kTileV <= 156 * 1024;
+  constexpr bool kParts = DW == 2 && kBase + PARTS * kTileV + 2 * sizeof(Decays) <= 160 * 1024;
   constexpr bool kHasV = kOut || !kParts;    // V itself is needed in LDS
   __shared__ __align__(16) char smem[kBase + (kParts ? PARTS * kTileV : 0) + (kOut || kParts ? 0 : kTileV)];
   __shared__ Decays dec[2];
@@ -319,7 +334,9 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
     if constexpr (kOut) {                   // score tiles above the diagonal that are read
       if (tid < 2 * 16 * 4) {
         const int tt = (tid >> 6) * 32 + (tid & 15), col = (tid >> 6) * 32 + 16 + ((tid >> 4) & 3) * 4;
-        *reinterpret_cast<uint2*>(pt + at_gap<kChunk>(tt, col)) = make_uint2(0, 0);
+        const int p = at_gap<kChunk>(tt, col);
+        *reinterpret_cast<uint2*>(pt + p) = make_uint2(0, 0);
+        *reinterpret_cast<uint2*>(pt + low_part(p, tt >> 4)) = make_uint2(0, 0);
       }
     }
     __syncthreads();
@@ -409,7 +426,13 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
 #pragma unroll
             for (int r = 0; r < 4; ++r) x[r] = ahead + 16 * j >= r ? x[r] : 0.f;
           }
-          *reinterpret_cast<uint2*>(pt + pj + j * kRows<kChunk>) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+          uint32_t u[2][2];
+          split_pair<2, false>(x[0], x[1], &u[0][0], 2);
+          split_pair<2, false>(x[2], x[3], &u[0][1], 2);
+          const uint32_t m = low_mask(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
+          const int p0 = pj + j * kRows<kChunk>;
+          *reinterpret_cast<uint2*>(pt + p0) = make_uint2(u[0][0], u[0][1]);
+          *reinterpret_cast<uint2*>(pt + low_part(p0, j0 + j)) = make_uint2(u[1][0] & m, u[1][1] & m);
         };
         if constexpr (JT == 4) {
           bf16x8 kf[KS];
@@ -443,20 +466,41 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int v = 0; v < VT; ++v) O[j][v] = f32x4{0.f, 0.f, 0.f, 0.f};
+      uint32_t mask[VT];
+#pragma unroll
+      for (int v = 0; v < VT; ++v) {
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < AT; ++i) top = fmaxf(fmaxf(fmaxf(top, fabsf(S[i][v][0])), fmaxf(fabsf(S[i][v][1]), fabsf(S[i][v][2]))), fabsf(S[i][v][3]));
+        mask[v] = low_mask(top);
+      }
 #pragma unroll
       for (int ks = 0; ks < KS / DW; ++ks) {
-        bf16x8 sf[VT];
+        bf16x8 sf[2][VT];
 #pragma unroll
         for (int v = 0; v < VT; ++v) {
           const f32x4 x = S[2 * ks][v], y = S[2 * ks + 1][v];
-          sf[v] = __builtin_bit_cast(bf16x8, make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                                        pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])));
+          uint32_t u[2][4];
+          split_pair<2, false>(x[0], x[1], &u[0][0], 4);
+          split_pair<2, false>(x[2], x[3], &u[0][1], 4);
+          split_pair<2, false>(y[0], y[1], &u[0][2], 4);
+          split_pair<2, false>(y[2], y[3], &u[0][3], 4);
+          sf[0][v] = __builtin_bit_cast(bf16x8, make_uint4(u[0][0], u[0][1], u[0][2], u[0][3]));
+          sf[1][v] = __builtin_bit_cast(bf16x8, make_uint4(u[1][0] & mask[v], u[1][1] & mask[v], u[1][2] & mask[v], u[1][3] & mask[v]));
         }
+        // products that follow each other have different accumulators
+        constexpr int JB = 4 / VT;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const bf16x8 q = row_operand(qt, rq ^ (drow * 2), ks, j * kRows<DK>);
+        for (int j0 = 0; j0 < 4; j0 += JB) {
+          bf16x8 q[JB];
 #pragma unroll
-          for (int v = 0; v < VT; ++v) O[j][v] = mfma(sf[v], q, O[j][v]);
+          for (int j = 0; j < JB; ++j) q[j] = row_operand(qt, rq ^ (drow * 2), ks, (j0 + j) * kRows<DK>);
+#pragma unroll
+          for (int p = 1; p >= 0; --p)
+#pragma unroll
+            for (int j = 0; j < JB; ++j)
+#pragma unroll
+              for (int v = 0; v < VT; ++v) O[j0 + j][v] = mfma(sf[p][v], q[j], O[j0 + j][v]);
         }
       }
       if constexpr (DW == 2) {              // tiles 0 and 3 are finished by wd 0, 1 and 2 by wd 1
@@ -559,16 +603,21 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
 #pragma unroll
           for (int ks = 0; ks < 2; ++ks)
             if (ks <= j / 2) {
-              const bf16x8 p = row_operand(pt, rp, ks, j * kRows<kChunk>);
+              const bf16x8 lo = row_operand(pt, rp, j < 2 ? 1 : ks, (j < 2 ? j : j + 2) * kRows<kChunk>);
+              const bf16x8 hi = row_operand(pt, rp, ks, j * kRows<kChunk>);
 #pragma unroll
-              for (int v = 0; v < VT; ++v) o[v] = mfma(vf[ks][v], p, o[v]);
+              for (int v = 0; v < VT; ++v) o[v] = mfma(vf[ks][v], lo, o[v]);
+#pragma unroll
+              for (int v = 0; v < VT; ++v) o[v] = mfma(vf[ks][v], hi, o[v]);
             }
         } else {
           // 0 times a NaN or an infinity of a later token must not reach this one: the same
           // sums, over the tokens up to the query's only
 #pragma unroll 1
           for (int k = 0; k < 16 * j + 16; ++k) {
-            const float p = bf16_to_f32(*reinterpret_cast<const uint16_t*>(pt + at_gap<kChunk>(tt, k)));
+            const int at_p = at_gap<kChunk>(tt, k);
+            const float p = bf16_to_f32(*reinterpret_cast<const uint16_t*>(pt + at_p)) +
+                            bf16_to_f32(*reinterpret_cast<const uint16_t*>(pt + low_part(at_p, j)));
 #pragma unroll
             for (int v = 0; v < VT; ++v) {
               const uint2 u = *reinterpret_cast<const uint2*>(vt + at<DV>(k, wv * CW + 16 * v + g4));

@@ -487,3 +487,40 @@ def test_flat_grid_without_tokens_and_with_disordered_bounds():
                                          force_generic=generic)
     torch.cuda.synchronize()
     assert (guard[:100] == 7.0).all() and (guard[100 + T:] == 7.0).all()
+
+
+@pytest.mark.parametrize("dk,dv,N,scale", [(64, 64, 200, 0.125), (16, 40, 700, -1.5), (128, 128, 900, 1.0), (256, 96, 130, 0.0625),
+                                           (256, 512, 150, 0.0625), (256, 512, 900, 1.0), (192, 256, 850, 0.3)])
+def test_bf16_prompts_are_rounded_once(dk, dv, N, scale):
+    """A bf16 output is the float32 result rounded once (H16 of it). Scores, the state's copy that
+    queries read, and the tokens' shares of the state in a pass that only gives outputs are held in
+    two bf16 parts: what is left of a value after two roundings is at most H16^2 = 2^-16 of it. A
+    score or a state value meets one such loss on its own side and one in the tokens behind it: 2
+    H16^2 M beside the float32 bound c M. (1 and 3 segments at each width of the state.)"""
+    H = 2
+    q, k, v, g = inputs(1, H, H, H, H, N, dk, dv, "bf16", 26 + dk, True, fade=16.0, resets=0.002)
+    s0 = torch.randn(1, H, dk, dv, device=DEV, generator=torch.Generator(DEV).manual_seed(10))
+    for want in (True, False):
+        out, _ = rn().rn_linear_attention_chunked(q, k, v, g, qk_scale=scale, state_in=s0, state_out=want)
+        o, _ = K.linear_attention(q[0], k[0], v[0], g[0], scale, s0[0])
+        mo, _ = K.linear_attention(q[0].abs(), k[0].abs(), v[0].abs(), g[0], abs(scale), s0[0].abs())
+        c = (3 * reach(g[0]) + dk + 64) * U
+        tol = (c + 2 * H16 * H16) * mo * (1 + 2 * H16) + H16 * np.abs(o) + 1e-30
+        off = np.abs(np64(out[0]) - o)
+        assert (off <= tol).all(), f"{(off / tol).max()} of the tolerance at {np.unravel_index((off / tol).argmax(), off.shape)}"
+
+
+@pytest.mark.parametrize("dk,dv,N", [(64, 64, 70), (128, 128, 900), (256, 512, 130), (256, 64, 70)])
+def test_infinite_states_stay_infinite(dk, dv, N):
+    """An infinity in the starting state reaches its column of every output, as an infinity of the
+    sign that the query gives it, and no other column."""
+    q, k, v, g = inputs(1, 2, 2, 2, 2, N, dk, dv, "bf16", 27, True, fade=16.0)
+    s0 = torch.randn(1, 2, dk, dv, device=DEV, generator=torch.Generator(DEV).manual_seed(11))
+    q[..., 5] = torch.where(q[..., 5] == 0, 1.0, q[..., 5])
+    clean, _ = rn().rn_linear_attention_chunked(q, k, v, g, state_in=s0)
+    s0[0, 1, 5, 7] = float("inf")
+    base, _ = rn().rn_linear_attention_chunked(q, k, v, g, state_in=s0)
+    sign = torch.sign(q[0, 1, :, 5].float())
+    assert torch.equal(base[0, 1, :, 7].float(), sign * float("inf"))
+    rest = [c for c in range(dv) if c != 7]
+    assert torch.equal(base[0, 0], clean[0, 0]) and torch.equal(base[0, 1][:, rest], clean[0, 1][:, rest])
