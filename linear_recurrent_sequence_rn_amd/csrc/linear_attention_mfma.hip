@@ -106,8 +106,11 @@ __device__ __forceinline__ int low_part(int p, int tile) {
 __device__ __forceinline__ uint32_t low_mask(float top) { return top <= 0x1.fep127f ? ~0u : 0u; }
 
 struct alignas(16) Decays {   // of one chunk
-  float c[kChunk];       // running sum of log2 decays
-  float q[kChunk];       // the same + log2 |scale|: the queries' side of a score's decay
+  // Running sum of log2 decays, as the sum of two floats: with zeros among the decays it passes 1e4,
+  // and differences of such sums keep float32 accuracy only if both parts are subtracted.
+  float c[kChunk];
+  float l[kChunk];
+  float q[kChunk];       // l + log2 |scale|: the queries' side of a score's decay
   float e[kChunk];       // 2^c |scale|
   float w[kChunk];       // 2^(c_63 - c)
   float a;               // 2^c_63
@@ -143,8 +146,8 @@ __device__ __forceinline__ double dpp_or_zero(double x) {
   return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
 }
 
-// One wave: the decays of a chunk from each lane's log decay. Sums in float64, so that
-// differences of far sums keep float32 accuracy. Returns the chunk's sum of log2 decays.
+// One wave: the decays of a chunk from each lane's log decay, their sums in float64. Returns the
+// chunk's sum of log2 decays.
 __device__ __forceinline__ double scan_decays(float g, float log2_scale, Decays* d) {
   const int lane = threadIdx.x & 63;
   double x = static_cast<double>(g) * kLog2e;
@@ -159,8 +162,11 @@ __device__ __forceinline__ double scan_decays(float g, float log2_scale, Decays*
   const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(u), 63);
   const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(u >> 32), 63);
   const double last = __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
-  d->c[lane] = static_cast<float>(x);
-  d->q[lane] = static_cast<float>(x + log2_scale);
+  const float c = static_cast<float>(x);
+  const float l = static_cast<float>(x - c);
+  d->c[lane] = c;
+  d->l[lane] = l;
+  d->q[lane] = l + log2_scale;
   d->e[lane] = exp2f(static_cast<float>(x + log2_scale));
   d->w[lane] = exp2f(static_cast<float>(last - x));
   if (lane == 63) d->a = exp2f(static_cast<float>(x));
@@ -416,12 +422,13 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
         const char* qq = qt + j0 * kRows<DK>;
         const int pj = (rp ^ (keys << 5)) + j0 * kRows<kChunk>;
         const f32x4 cs = *reinterpret_cast<const f32x4*>(&D.c[16 * keys + g4]);
+        const f32x4 ls = *reinterpret_cast<const f32x4*>(&D.l[16 * keys + g4]);
         const int ahead = l16 - g4 + 16 * (j0 - keys);   // queries' lead over the lane's first key
         auto finish = [&](int j, const f32x4& p) {
-          const float ct = D.q[16 * (j0 + j) + l16];
+          const float ct = D.c[16 * (j0 + j) + l16], lt = D.q[16 * (j0 + j) + l16];
           float x[4];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) x[r] = p[r] * __builtin_amdgcn_exp2f(ct - cs[r]);
+          for (int r = 0; r < 4; ++r) x[r] = p[r] * __builtin_amdgcn_exp2f((ct - cs[r]) + (lt - ls[r]));
           if (j0 + j <= keys) {             // on the diagonal (or above it)
 #pragma unroll
             for (int r = 0; r < 4; ++r) x[r] = ahead + 16 * j >= r ? x[r] : 0.f;

@@ -524,3 +524,20 @@ def test_infinite_states_stay_infinite(dk, dv, N):
     assert torch.equal(base[0, 1, :, 7].float(), sign * float("inf"))
     rest = [c for c in range(dv) if c != 7]
     assert torch.equal(base[0, 0], clean[0, 0]) and torch.equal(base[0, 1][:, rest], clean[0, 1][:, rest])
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 64), (256, 512)])
+def test_decays_behind_many_resets(dk, dv):
+    """Fifty zero decays, then mild ones, in one chunk: the sums of log decays are far from zero where
+    the differences that count are small. Tolerance as for outputs that are rounded once."""
+    H, N, scale = 2, 128, 0.37
+    q, k, v, g = inputs(1, H, H, H, H, N, dk, dv, "bf16", 28 + dk, True, fade=16.0)
+    g[:, :, 3:53] = -float("inf")
+    out, S = rn().rn_linear_attention_chunked(q, k, v, g, qk_scale=scale, state_out=True)
+    o, So = K.linear_attention(q[0], k[0], v[0], g[0], scale)
+    mo, mS = K.linear_attention(q[0].abs(), k[0].abs(), v[0].abs(), g[0], scale)
+    c = (3 * reach(g[0]) + dk + 64) * U
+    off, tol = np.abs(np64(out[0]) - o), (c + 2 * H16 * H16) * mo * (1 + 2 * H16) + H16 * np.abs(o) + 1e-30
+    assert (off <= tol).all(), f"{(off / tol).max()} of the tolerance at {np.unravel_index((off / tol).argmax(), off.shape)}"
+    off, tol = np.abs(np64(S[0]) - So), c * mS + 1e-30
+    assert (off <= tol).all(), f"state: {(off / tol).max()} of the tolerance"
