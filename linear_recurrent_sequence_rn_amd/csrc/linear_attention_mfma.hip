@@ -46,7 +46,8 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr int kChunk = 64;
 constexpr double kLog2e = 1.4426950408889634;
-constexpr double kFloor = -173.0;      // 2^-173 is 0 in float32: log decays below stand for 0
+// Log decays below stand for 0: 2^-300 is 0 in float32, also times the largest scale.
+constexpr double kFloor = -300.0;
 
 __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);

@@ -541,3 +541,14 @@ def test_decays_behind_many_resets(dk, dv):
     assert (off <= tol).all(), f"{(off / tol).max()} of the tolerance at {np.unravel_index((off / tol).argmax(), off.shape)}"
     off, tol = np.abs(np64(S[0]) - So), c * mS + 1e-30
     assert (off <= tol).all(), f"state: {(off / tol).max()} of the tolerance"
+
+
+@pytest.mark.parametrize("kind,dk,dv", [("bf16", 64, 64), ("bf16", 256, 512), ("f32", 64, 64)])
+def test_a_reset_clears_the_state_at_any_scale(kind, dk, dv):
+    """Nothing of a large state is left behind a zero decay, whatever the scale."""
+    q, k, v, g = inputs(1, 2, 2, 2, 2, 70, dk, dv, kind, 29)
+    k.zero_()
+    g[:, :, 1] = -float("inf")
+    s0 = torch.full((1, 2, dk, dv), 1e30, device=DEV)
+    out, S = rn().rn_linear_attention_chunked(q, k, v, g, qk_scale=1e25, state_in=s0, state_out=True)
+    assert int(torch.count_nonzero(out[:, :, 1:])) == 0 and int(torch.count_nonzero(S)) == 0
