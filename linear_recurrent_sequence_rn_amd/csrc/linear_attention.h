@@ -70,10 +70,12 @@ __device__ __forceinline__ int lin_slot(const LinArgs& a, int s) {
   const int x = a.slots[s];
   return x >= 0 && x < a.n_slots ? x : -1;
 }
-// Row of segment g of sequence s in the workspace: distinct for all segments of a packed
-// batch (a sequence starting at row r owns r/L + s on), below lin_segments() always.
+// Row of segment g of sequence s in the workspace: distinct for all segments, and below
+// total_segments() whatever the device arrays hold. In a flat grid only sequences of more than one
+// segment use it, and one that starts at token row r owns 2r/L on: with n tokens, n > L, that is
+// 2n/L rows (rounded down) at least, and ceil(n/L) of them are needed.
 __device__ __forceinline__ int64_t lin_segment(const LinArgs& a, int s, int64_t row0, int g) {
-  return a.T > 0 ? row0 / a.seg_len + s + g : static_cast<int64_t>(s) * a.n_seg + g;
+  return a.flat ? 2 * row0 / a.seg_len + g : static_cast<int64_t>(s) * a.n_seg + g;
 }
 // The last of the sequences 0 .. S of a packed batch that a predicate holds for, which holds up to
 // one of them (whatever it says, one of them): a lane a candidate.
@@ -91,8 +93,8 @@ __device__ __forceinline__ int lin_last(const LinArgs& a, F holds) {
 __device__ __forceinline__ int64_t lin_first(const LinArgs& a, int s) {
   return min(max(static_cast<int64_t>(a.cu[s]), int64_t(0)), a.T);
 }
-// The segment and sequence of a block. In a flat grid, block w has the workspace row w: sequence
-// s has those from lin_segment(s, 0) on up to the next one's. False: none.
+// The segment and sequence of a block. In a flat grid, sequence s, starting at row r, has the blocks
+// from r/L + s on up to the next one's first. False: none.
 __device__ __forceinline__ bool lin_place(const LinArgs& a, int* s, int* seg) {
   if (!a.flat) {
     *s = blockIdx.z;

@@ -557,8 +557,19 @@ void segments(const LinCall& c, int* len, int* n) {
   *n = static_cast<int>((c.N + L - 1) / L);
 }
 
+// Blocks along the segments of all sequences, where N says little about the lengths: 1024 packed
+// sequences of 28 tokens, 8 heads of 64 x 128, and no nearer bound than the tokens of all: 216 us,
+// 1382 us with S n_seg blocks (160 where the bound is given, in one pass). (S N is then more than T,
+// and T / L at most 768 by the choice of L.)
+bool flat_grid(const LinCall& c, int len, int n) {
+  return n > 1 && c.T > 0 && static_cast<int64_t>(c.S) * n > 2 * (c.T / len + c.S + 1);
+}
+
+// Segment states in the workspace (lin_segment()). In a packed batch they grow with the tokens, not
+// with S or with T alone: S n is at most 2 (T / L + S + 1) where the grid is not flat, and n is at
+// least three.
 int64_t total_segments(const LinCall& c, int len, int n) {
-  return c.T > 0 ? c.T / len + c.S : static_cast<int64_t>(c.S) * n;
+  return flat_grid(c, len, n) ? 2 * c.T / len : static_cast<int64_t>(c.S) * n;
 }
 
 }  // namespace
@@ -583,10 +594,7 @@ hipError_t launch_linear_chunked(const LinCall& c, hipStream_t st) {
   segments(c, &a.seg_len, &a.n_seg);
   const bool mfma = mfma_call(c);
   if (a.n_seg == 1) return mfma ? launch_lin_mfma(a, kLinWhole, st) : launch_float<kLinWhole>(a, c.in_dt, c.out_dt, st);
-  // Where N says little about the lengths: 1024 packed sequences of 28 tokens, 8 heads of 64 x 128,
-  // and no nearer bound than the tokens of all: 216 us, 1382 us with S n_seg blocks (160 where the
-  // bound is given, in one pass). (S N is then more than T, and T / L at most 768 by the choice of L.)
-  a.flat = c.T > 0 && static_cast<int64_t>(c.S) * a.n_seg > 2 * (c.T / a.seg_len + c.S + 1);
+  a.flat = flat_grid(c, a.seg_len, a.n_seg);
   const size_t rows = static_cast<size_t>(total_segments(c, a.seg_len, a.n_seg)) * c.H;
   a.seg_decay = static_cast<float*>(c.ws);
   a.seg_state = a.seg_decay + ((rows + 63) & ~size_t(63));

@@ -214,3 +214,22 @@ def test_outputs_that_are_other_inputs_are_refused():
     for kw in (dict(out=FAKE), dict(q=5 * FAKE, out=FAKE)):         # (k and v are FAKE)
         assert chunked(d, **kw) == INV and b"must not be q, k or v" in L.rn_last_error()
     assert step(lin(N=1), q=5 * FAKE, out=5 * FAKE) == INV and b"must not be q, k or v" in L.rn_last_error()
+
+
+@pytest.mark.parametrize("generic", [0, rn.RN_LINEAR_GENERIC])
+def test_packed_workspace_does_not_grow_with_the_sequences(generic):
+    """The states kept between passes are those of segments, of which a fixed number of tokens has a
+    bounded number, however many sequences share them."""
+    T = 1 << 20
+
+    def need(S, N=T):
+        return L.rn_linear_attention_workspace_bytes(ctypes.byref(lin(S=S, N=N, T=T, d_k=256, d_v=512, flags=generic,
+                                                                           out_stride=(0, 512, 4096))))
+
+    few = need(1)                     # one sequence: a state for each segment
+    assert few > 0
+    for S in (2, 30, 1000, 20000, 65534):
+        assert 0 < need(S) <= 2 * few + 4096, S
+    for N in (T // 50, T // 500, 1000):   # a bound on the lengths, in a buffer with room for many more
+        for S in (1, 3, 100, 1000, 20000):
+            assert need(S, N) <= 2 * few + 4096, (S, N)

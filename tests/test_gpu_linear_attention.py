@@ -552,3 +552,28 @@ def test_a_reset_clears_the_state_at_any_scale(kind, dk, dv):
     s0 = torch.full((1, 2, dk, dv), 1e30, device=DEV)
     out, S = rn().rn_linear_attention_chunked(q, k, v, g, qk_scale=1e25, state_in=s0, state_out=True)
     assert int(torch.count_nonzero(out[:, :, 1:])) == 0 and int(torch.count_nonzero(S)) == 0
+
+
+@pytest.mark.parametrize("kind,dk,dv,L", [("f32", 33, 24, 64), ("bf16", 64, 64, 256), ("bf16", 256, 96, 256)])
+def test_flat_grid_with_many_sequences_of_several_segments(kind, dk, dv, L):
+    """Sequences just above, at and below whole numbers of segments (of L tokens here), short ones
+    between: every state and output, into a workspace of just the bytes asked for, and nothing
+    behind it."""
+    H = 2
+    lens = [L + 1, 1, L + 1, 2 * L + 1, 0, L, L + 1, 3, 2 * L, L + 2, L - 1, 3 * L + 1, 0, L + 1, L + 1, 5]
+    S, T = len(lens), sum(lens)
+    q, k, v, g = inputs(1, H, H, 1, H, T, dk, dv, kind, 30, True, fade=16.0)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device=DEV)
+    s0 = torch.randn(S, H, dk, dv, device=DEV, generator=torch.Generator(DEV).manual_seed(12))
+    need = rn().rn_linear_attention_workspace_bytes(q, k, v, g, cu_seqlens=cu)
+    assert need > 0
+    guard = torch.full((need + 4096,), 77, dtype=torch.uint8, device=DEV)
+    out, new = rn().rn_linear_attention_chunked(q, k, v, g, cu_seqlens=cu, state_in=s0, state_out=True, workspace=guard[:need])
+    assert (guard[need:] == 77).all()
+    for s in range(S):
+        a, b = int(cu[s]), int(cu[s + 1])
+        if b > a:
+            check_sequence(out[0, :, a:b], new[s], q[0, :, a:b], k[0, :, a:b], v[0, :, a:b], g[0, :, a:b], 1.0, s0[s],
+                           uses_mfma(kind, DT[kind], dk, dv, False))
+        else:
+            assert torch.equal(new[s], s0[s])
