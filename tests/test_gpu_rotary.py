@@ -184,3 +184,19 @@ def test_pieces_of_every_size_at_any_address(kind, half, d, rot):
     rn().rn_rotary(x, None, theta, pos0=3, half=half, q_out=x)
     assert torch.equal(x, got)
     assert torch.equal(wide[..., 0], before[..., 0]) and torch.equal(wide[..., 1 + d:], before[..., 1 + d:])
+
+
+@pytest.mark.parametrize("half", [False, True])
+def test_float32_keeps_what_the_angles_have(half):
+    """The error in the mean square. One rounding is off by at most U / sqrt(3) of its value there. A
+    turned value a c - b s takes one of the sum, one of one of its two products (half of the square),
+    and those of c and s (each half of it): sqrt(2.5) U / sqrt(3) together. An angle rounded to
+    float32 would add about 0.77 U (angles spread over a turn), 1.2 U with these."""
+    B, H, N, d = 2, 4, 3000, 64
+    g = torch.Generator().manual_seed(31)
+    x = torch.randn(B, H, N, d, generator=g).to(DEV)
+    theta = 10000.0 ** (-2.0 * np.arange(d // 2) / d)
+    got = rn().rn_rotary(x, None, theta, pos0=12345, half=half)
+    want = K.rotary(x.cpu(), theta, np.arange(N)[None].repeat(B, 0) + 12345, half)
+    off = np.linalg.norm(got.double().cpu().numpy() - want) / np.linalg.norm(want)
+    assert off <= (2.5 / 3) ** 0.5 * U, off / U
