@@ -19,6 +19,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxTile = 32;       // tokens a block
 constexpr int kTable = 2048;       // cosine/sine pairs in LDS: tile * rot/2 at most
+constexpr int64_t kGridX = 1 << 23;  // tiles along a grid's x: a launch has fewer than 2^32 threads there
 
 struct RotArgs {
   int32_t N, Hq, H, d, rot;        // H: heads of q and k together
@@ -113,7 +114,8 @@ __global__ void __launch_bounds__(kThreads) rotary(RotArgs a, int lanes) {
   __shared__ float2 cs[kTable];
   __shared__ int64_t base[kMaxTile][4];   // token offsets: q, k, q_out, k_out
   const int half = a.rot / 2;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.tile;
+  const int64_t row0 = (static_cast<int64_t>(blockIdx.z) * gridDim.x + blockIdx.x) * a.tile;
+  if (row0 >= a.rows) return;
   const int tile = static_cast<int>(min(static_cast<int64_t>(a.tile), a.rows - row0));
   for (int i = threadIdx.x; i < tile * half; i += kThreads) {
     const int t = i / half, j = i - t * half;
@@ -232,7 +234,8 @@ hipError_t launch_t(const RotaryCall& c, RotArgs& a, hipStream_t st) {
   while (tiles * groups < 512 && groups * 2 * (kThreads / lanes) <= tile * a.H) groups *= 2;
   a.tile = tile;
   a.heads = (a.H + groups - 1) / groups;
-  const dim3 grid(static_cast<unsigned>(tiles), (a.H + a.heads - 1) / a.heads);
+  const int64_t x = std::min(tiles, kGridX);
+  const dim3 grid(static_cast<unsigned>(x), (a.H + a.heads - 1) / a.heads, static_cast<unsigned>((tiles + x - 1) / x));
 #define RN_ROTARY(W)                                                                                             \
   if (w == W) {                                                                                                  \
     if (c.half) hipLaunchKernelGGL((rotary<DT, W, true>), grid, dim3(kThreads), 0, st, a, lanes);                \

@@ -200,3 +200,17 @@ def test_float32_keeps_what_the_angles_have(half):
     want = K.rotary(x.cpu(), theta, np.arange(N)[None].repeat(B, 0) + 12345, half)
     off = np.linalg.norm(got.double().cpu().numpy() - want) / np.linalg.norm(want)
     assert off <= (2.5 / 3) ** 0.5 * U, off / U
+
+
+def test_more_tiles_than_one_grid_axis_takes():
+    """2^29 + 37 tokens (2 GiB): tokens from all over the call equal those of short calls at their
+    positions, bit by bit."""
+    N = (1 << 29) + 37
+    one = torch.randn(1, 1, 1, 2, generator=torch.Generator().manual_seed(32)).bfloat16().to(DEV)
+    theta = np.array([0.37])
+    out = torch.empty(1, 1, N, 2, dtype=torch.bfloat16, device=DEV)
+    rn().rn_rotary(one.expand(1, 1, N, 2), None, theta, q_out=out)
+    for at in (0, (1 << 28) - 50, (1 << 29) - 50, N - 100, 123456789):
+        n = min(100, N - at)
+        want = rn().rn_rotary(one.expand(1, 1, n, 2), None, theta, pos0=at)
+        assert torch.equal(out[:, :, at:at + n], want), at
