@@ -16,7 +16,7 @@ __global__ void __launch_bounds__(256) gn_gate_rows(int64_t rows, int H, int N, 
                                                     const float* w, const float* b, float eps,
                                                     void* out) {
   const int lane = threadIdx.x & 63;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int64_t row = (static_cast<int64_t>(blockIdx.z) * gridDim.x + blockIdx.x) * 4 + (threadIdx.x >> 6);
   if (row >= rows) return;
   const int head = static_cast<int>((row / N) % H);
   const int64_t off = row * dv;
@@ -54,7 +54,9 @@ template <int IN, int OUT>
 hipError_t launch_t(int B, int H, int N, int dv, const void* x, const void* gate, const float* w,
                     const float* b, float eps, void* out, hipStream_t st) {
   const int64_t rows = static_cast<int64_t>(B) * H * N;
-  dim3 grid(static_cast<unsigned>((rows + 3) / 4));
+  // (a launch has fewer than 2^32 threads along x)
+  const int64_t blocks = (rows + 3) / 4, x_blocks = blocks < (1 << 23) ? blocks : 1 << 23;
+  dim3 grid(static_cast<unsigned>(x_blocks), 1, static_cast<unsigned>((blocks + x_blocks - 1) / x_blocks));
   hipLaunchKernelGGL((gn_gate_rows<IN, OUT>), grid, dim3(256), 0, st, rows, H, N, dv, x, gate, w,
                      b, eps, out);
   return hipGetLastError();

@@ -197,3 +197,13 @@ def test_tensors_of_another_device_than_the_current_one(monkeypatch):
     monkeypatch.setattr(block_ops, "_current_device", lambda: 7)
     got = calls(*s, theta)
     assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.cuda.current_device() == 0
+
+
+def test_group_norm_of_more_rows_than_one_grid_axis_takes():
+    """2^26 + 9 rows of 4 values: rows from all over the call equal those of short calls, bit by bit."""
+    N = (1 << 26) + 9
+    x = torch.randn(1, 1, N, 4, generator=torch.Generator(DEV).manual_seed(33), device=DEV).bfloat16()
+    out = rn().rn_groupnorm_gate(x, out=torch.zeros_like(x))
+    for at in (0, (1 << 25) - 50, (1 << 26) - 50, N - 100, 12345678):
+        n = min(100, N - at)
+        assert torch.equal(out[:, :, at:at + n], rn().rn_groupnorm_gate(x[:, :, at:at + n].contiguous())), at
