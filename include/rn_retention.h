@@ -510,7 +510,7 @@ rn_status rn_rotary_frequencies(int32_t rot, double base, int32_t kind, double f
 #define RN_LINEAR_GENERIC   (1u << 8)  /* take the float32 kernels (for testing) */
 
 typedef struct rn_linear_desc {
-    int32_t S;             /* sequences, 1 .. 65535 */
+    int32_t S;             /* sequences, 1 .. 65534 */
     int32_t N;             /* most tokens of a sequence, 1 .. 2^30; the step form needs 1 */
     int32_t H;             /* heads of the state, decays and output: 1 .. 65535 */
     int32_t H_q, H_k, H_v; /* heads of q, k, v: divisors of H */

@@ -233,3 +233,17 @@ def test_packed_workspace_does_not_grow_with_the_sequences(generic):
     for N in (T // 50, T // 500, 1000):   # a bound on the lengths, in a buffer with room for many more
         for S in (1, 3, 100, 1000, 20000):
             assert need(S, N) <= 2 * few + 4096, (S, N)
+
+
+def test_header_limits_are_the_calls_limits():
+    """The largest sizes that the header gives for linear attention are taken, the next ones are not."""
+    import pathlib
+    import re
+    text = (pathlib.Path(__file__).parent.parent / "include" / "rn_retention.h").read_text()
+    text = text[text.index("typedef struct rn_linear_desc"):text.index("} rn_linear_desc;")]
+    wide = dict(out_stride=(1 << 40, 1 << 24, 512), q_stride=(0, 0, 0), k_stride=(0, 0, 0), v_stride=(0, 0, 0), N=1, H=1,
+                H_q=1, H_k=1, H_v=1)
+    for field in ("S", "H", "d_k", "d_v"):
+        most = int(re.search(r"\b%s;[^\n]*?1 \.\. (\d+)" % field, text).group(1))
+        for n, code in ((most, INV), (most + 1, UNS)):       # (a NULL pointer, once the sizes are taken)
+            assert chunked(lin(**{**wide, field: n}), q=None) == code, (field, n)
