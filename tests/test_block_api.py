@@ -247,3 +247,29 @@ def test_header_limits_are_the_calls_limits():
         most = int(re.search(r"\b%s;[^\n]*?1 \.\. (\d+)" % field, text).group(1))
         for n, code in ((most, INV), (most + 1, UNS)):       # (a NULL pointer, once the sizes are taken)
             assert chunked(lin(**{**wide, field: n}), q=None) == code, (field, n)
+
+
+def test_workspace_bytes():
+    """The exact need of a known shape, and a bound that holds for all: a pass cuts the tokens so that
+    about 256 to 768 blocks of at most 64 KiB of state (128 KiB for 128 columns) run at once; rests of
+    segments and the room that ragged lengths need multiply that by at most 8."""
+    d = lin(S=1, N=8192, H=16, H_q=16, H_k=16, H_v=16, d_k=256, d_v=512, q_stride=(0, 256, 4096), k_stride=(0, 256, 4096),
+            v_stride=(0, 512, 8192), out_stride=(0, 512, 8192))
+    # 64 blocks a segment on 256 compute units: four segments of 2048 tokens
+    assert L.rn_linear_attention_workspace_bytes(ctypes.byref(d)) == 4 * 16 * 256 * 512 * 4 + 256
+    rng = np.random.default_rng(41)
+    seen = 0
+    for _ in range(4000):
+        S, N = (int(2 ** rng.uniform(0, b)) for b in (15.9, 30))
+        H = int(2 ** rng.uniform(0, 10))
+        dk, dv = int(rng.integers(1, 257)), int(rng.integers(1, 513))
+        packed = rng.random() < 0.6
+        T = min(N * int(2 ** rng.uniform(0, 12)), (1 << 31) - 1) if packed else 0
+        st = (0, 1 << 10, 1 << 20) if packed else (1 << 40, 0 if H == 1 else dv, H * dv)
+        if not packed and N * H * dv > 1 << 40:
+            continue
+        need = L.rn_linear_attention_workspace_bytes(ctypes.byref(lin(
+            S=S, N=N, T=T, H=H, H_q=1, H_k=1, H_v=1, d_k=dk, d_v=dv, out_stride=st, flags=int(rng.choice([0, rn.RN_LINEAR_GENERIC])))))
+        assert need <= 8 * 768 * (64 << 10) + (1 << 20), (S, N, H, dk, dv, T)
+        seen += need > 0
+    assert seen > 100

@@ -263,3 +263,18 @@ def test_narrow_rows(n, d, kind):
     """Rows of a head's width, several to a wave, in numbers that leave waves and blocks part empty."""
     test_forward(n, d, kind)
     test_backward(n, d, kind)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("d,extra", [(256, 8), (256, 1), (100, 28), (2000, 3), (1537, 0)])
+def test_backward_of_one_repeated_gradient_row(kind, d, extra):
+    """An output gradient that is one row repeated by a stride of 0, beside rows of x with and without
+    gaps: alignment takes the same kernel as for the copied rows, and so the same bits come out."""
+    g = torch.Generator().manual_seed(d + extra)
+    x = spread(g, 37, d, DT[kind], extra)
+    one = torch.randn(1, d, generator=g).to(DT[kind]).to(DEV)
+    w = torch.randn(d, generator=g).to(DEV)
+    same = rn().rn_layernorm_backward(one.expand(37, d), x, w)
+    full = rn().rn_layernorm_backward(one.expand(37, d).contiguous(), x, w)
+    assert all(torch.equal(same[n], full[n]) for n in full)
+    assert all(int(torch.count_nonzero(full[n])) > 0 for n in full)
