@@ -399,8 +399,8 @@ typedef struct rn_norm_desc {
 /*
  * weight, bias: DEVICE float32 [d] or NULL (1 and 0). residual and sum_out: NULL, or rows of
  * in_dtype (sum_out needs no residual; it then receives a copy of x). sum_out may equal x or
- * residual with the same stride, out may equal x where in_dtype == out_dtype and the strides
- * agree (out and sum_out must differ).
+ * residual with the same stride, out may equal x or residual where in_dtype == out_dtype and the
+ * strides agree (out and sum_out must differ); outputs overlap nothing else.
  */
 rn_status rn_layernorm_forward(const rn_norm_desc* desc, const void* x, const void* residual,
                                const float* weight, const float* bias, void* sum_out, void* out,
@@ -416,8 +416,8 @@ size_t rn_layernorm_backward_workspace_bytes(const rn_norm_desc* desc);
  *     dx = (g - mean(g) - xh mean(g xh)) / sqrt(var + eps) + dsum
  *     dweight = sum over rows of dout xh,   dbias = sum over rows of dout.
  * dsum: the gradient reaching the residual sum by its other path, or NULL (0); dx is then the
- * gradient of both x and residual. dx: in_dtype, may equal dout or dsum where types and
- * strides agree. dweight, dbias: DEVICE float32 [d] or NULL, written (not added to); their
+ * gradient of both x and residual. dx: in_dtype, may equal x, dout or dsum where types and
+ * strides agree, and overlaps nothing else. dweight, dbias: DEVICE float32 [d] or NULL, written (not added to); their
  * sums run in a fixed order (the same bits on every call). workspace: 256-byte aligned, at
  * least rn_layernorm_backward_workspace_bytes(desc); unused (may be NULL) when both dweight
  * and dbias are NULL.

@@ -168,7 +168,7 @@ def rn_layernorm(x, weight=None, bias=None, eps=1e-5, *, residual=None, sum_out=
     """Layer norm over the last axis of x [..., d], after adding ``residual`` (same shape and
     type) where given. weight, bias: float32 [d] or None. Returns out, or (out, sum) where a
     residual or ``sum_out`` is given; sum = x + residual in x's type (the next residual
-    stream). ``sum_out`` may be x or residual, ``out`` may be x."""
+    stream). ``sum_out`` and ``out`` (of x's type) may be x or residual, not both the same one."""
     dev = _device(x, residual, weight, bias, sum_out, out)
     shape = x.shape
     d = shape[-1] if shape else 0
@@ -209,7 +209,7 @@ def rn_layernorm_backward(dout, x, weight=None, eps=1e-5, *, dsum=None, dx=None,
     """Gradients of ``rn_layernorm``: x are the rows it normalised (its sum where it had a
     residual), ``dsum`` the gradient that reaches this sum by its other path, in x's type.
     Returns a dict with dx (the gradient of x and of the residual; in x's type) and, unless not
-    wanted, dweight and dbias (float32 [d])."""
+    wanted, dweight and dbias (float32 [d]). ``dx`` may be x, dsum, or dout of x's type."""
     dev = _device(x, dout, weight, dsum, dx, workspace)
     if x.numel() == 0 or x.dim() == 0:
         raise ValueError(f"x must be [..., d] with at least one row; got {tuple(x.shape)}")

@@ -278,3 +278,29 @@ def test_backward_of_one_repeated_gradient_row(kind, d, extra):
     full = rn().rn_layernorm_backward(one.expand(37, d).contiguous(), x, w)
     assert all(torch.equal(same[n], full[n]) for n in full)
     assert all(int(torch.count_nonzero(full[n])) > 0 for n in full)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("n,d", [(37, 64), (13001, 64), (300, 512), (3500, 600), (9, 4096), (3, 16384), (5, 1000), (3500, 333)])
+def test_every_operand_that_an_output_may_replace(kind, n, d):
+    """out in place of x or the residual, sum_out in place of either, dx in place of x, dout or dsum: the
+    bits of the call with outputs of its own."""
+    dt = DT[kind]
+    g = torch.Generator().manual_seed(n + d)
+    x, r, dy, dh = (rows(g, n, d, dt).to(DEV) for _ in range(4))
+    w, b = (torch.randn(d, generator=g).to(DEV) for _ in range(2))
+    f = rn().rn_layernorm
+    out, total = f(x, w, b, residual=r)
+    for o, s in (("x", None), ("r", None), ("x", "r"), ("r", "x"), (None, "x"), (None, "r")):
+        t = {"x": x.clone(), "r": r.clone()}
+        a, c = f(t["x"], w, b, residual=t["r"], out=t.get(o), sum_out=t.get(s))
+        assert torch.equal(a, out) and torch.equal(c, total), (o, s)
+        assert (o is None or a is t[o]) and (s is None or c is t[s])
+        for name, kept in (("x", x), ("r", r)):
+            assert name in (o, s) or torch.equal(t[name], kept)
+    want = rn().rn_layernorm_backward(dy, x, w, dsum=dh)
+    for name in ("x", "dy", "dh"):
+        t = {"x": x.clone(), "dy": dy.clone(), "dh": dh.clone()}
+        got = rn().rn_layernorm_backward(t["dy"], t["x"], w, dsum=t["dh"], dx=t[name])
+        assert all(torch.equal(got[i], want[i]) for i in want), name
+        assert all(i == name or torch.equal(t[i], kept) for i, kept in (("x", x), ("dy", dy), ("dh", dh)))
