@@ -373,7 +373,9 @@ rn_status rn_chunkwise_check(const rn_desc* desc, int32_t chunk, const void* wor
  * conventions as above, except that tensors are described by strides (in elements; the last
  * axis is always contiguous), so that the rows of a projection's output need no copy.
  * Strides are >= 0 and at most 2^40; a stride of 0 repeats an input along that axis (outputs
- * must not overlap themselves).
+ * must not overlap themselves). An output overlaps other operands only where that is allowed below;
+ * the calls refuse what two tensors of one type and the same strides show of it, and of the rest the
+ * caller has to take care.
  */
 
 /*

@@ -95,6 +95,53 @@ rn_status check_distinct(const int64_t* s, int64_t n0, int64_t n1, int64_t n2, i
   return RN_OK;
 }
 
+// A tensor: three strided axes of elements of `es` bytes, and d contiguous ones.
+struct Box {
+  const void* p;
+  int64_t es, s[3], n[3], d;
+};
+
+// Whether elements at i . s + [0, a.d) and diff + j . s + [0, b.d) meet, i and j inside the boxes: the
+// steps k = i - j along the axes from `axis` on, ordered by falling stride, that bring diff near 0.
+bool meets(int64_t diff, const Box& a, const Box& b, const int64_t* s, const int* order, int axis) {
+  if (axis == 3) return diff < a.d * a.es && -diff < b.d * b.es;
+  const int x = order[axis];
+  const int64_t st = s[x] * a.es, up = a.n[x] - 1, down = b.n[x] - 1;
+  if (st == 0) return meets(diff, a, b, s, order, axis + 1);
+  const int64_t k0 = diff / st;           // (k st is at most st from diff, an address, away)
+  for (int64_t k = k0 - 1; k <= k0 + 1; ++k)
+    if (k <= up && -k <= down && meets(diff - k * st, a, b, s, order, axis + 1)) return true;
+  return false;
+}
+
+// Whether an output overlaps another operand, as far as two tensors of one type and the same strides
+// show it (of others nothing is said). The same tensor in both places is no overlap here.
+bool overlaps(const Box& out, const Box& in) {
+  if (!in.p || in.p == out.p || out.es != in.es) return false;
+  int64_t s[3];
+  int order[3] = {0, 1, 2};
+  for (int i = 0; i < 3; ++i) {
+    if (out.n[i] > 1 && in.n[i] > 1 && out.s[i] != in.s[i]) return false;
+    s[i] = out.n[i] > 1 ? out.s[i] : in.n[i] > 1 ? in.s[i] : 0;
+  }
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 3; ++j)
+      if (s[order[j]] > s[order[i]]) std::swap(order[i], order[j]);
+  const int64_t diff = static_cast<int64_t>(reinterpret_cast<uintptr_t>(in.p) - reinterpret_cast<uintptr_t>(out.p));
+  return meets(diff, out, in, s, order, 0);
+}
+
+rn_status check_no_overlap(const Box& out, const Box& in, const char* what, const char* other) {
+  if (overlaps(out, in)) return fail(RN_ERR_INVALID_ARG, "%s overlaps %s", what, other);
+  return RN_OK;
+}
+Box box(const void* p, rn_dtype dt, const int64_t* s, int64_t n0, int64_t n1, int64_t n2, int64_t d) {
+  return Box{p, size_of(dt), {s[0], s[1], s[2]}, {n0, n1, n2}, d};
+}
+Box row_box(const void* p, rn_dtype dt, int64_t stride, const rn::NormCall& n) {
+  return Box{p, size_of(dt), {0, 0, stride}, {1, 1, n.rows}, n.d};
+}
+
 // ---- linear attention -----------------------------------------------------------------------
 
 rn_status check_linear(const rn_linear_desc* d, bool step, rn::LinCall* c) {
@@ -151,8 +198,15 @@ rn_status check_linear_ptrs(const rn_linear_desc* d, const int32_t* slots, const
 }
 
 // Blocks read q, k and v while others write out.
-rn_status check_apart(const rn::LinCall& c) {
+rn_status check_apart(const rn_linear_desc* d, const rn::LinCall& c) {
   if (c.out == c.q || c.out == c.k || c.out == c.v) return fail(RN_ERR_INVALID_ARG, "out must not be q, k or v");
+  const int64_t S = d->T ? 1 : d->S, N = d->T ? d->T : d->N;
+  const Box out = box(c.out, d->out_dtype, d->out_stride, S, d->H, N, d->d_v);
+  rn_status s;
+  if ((s = check_no_overlap(out, box(c.q, d->in_dtype, d->q_stride, S, d->H_q, N, d->d_k), "out", "q")) ||
+      (s = check_no_overlap(out, box(c.k, d->in_dtype, d->k_stride, S, d->H_k, N, d->d_k), "out", "k")) ||
+      (s = check_no_overlap(out, box(c.v, d->in_dtype, d->v_stride, S, d->H_v, N, d->d_v), "out", "v")))
+    return s;
   return RN_OK;
 }
 
@@ -176,6 +230,12 @@ rn_status rn_layernorm_forward(const rn_norm_desc* desc, const void* x, const vo
       (out == residual && (desc->in_dtype != desc->out_dtype || n.os != n.rs)) ||
       (sum_out && ((sum_out == x && n.ss != n.xs) || (sum_out == residual && n.ss != n.rs))))
     return fail(RN_ERR_INVALID_ARG, "in place needs equal types and strides");
+  const Box bx = row_box(x, desc->in_dtype, n.xs, n), br = row_box(residual, desc->in_dtype, n.rs, n),
+            bs = row_box(sum_out, desc->in_dtype, n.ss, n), bo = row_box(out, desc->out_dtype, n.os, n);
+  if ((s = check_no_overlap(bo, bx, "out", "x")) || (s = check_no_overlap(bo, br, "out", "residual")) ||
+      (s = check_no_overlap(bo, bs, "out", "sum_out")) ||
+      (sum_out && ((s = check_no_overlap(bs, bx, "sum_out", "x")) || (s = check_no_overlap(bs, br, "sum_out", "residual")))))
+    return s;
   n.x = x; n.r = residual; n.w = weight; n.b = bias; n.sum = sum_out; n.out = out;
   n.vec = norm_vectors(n);
   rn::clear_error();
@@ -203,6 +263,11 @@ rn_status rn_layernorm_backward(const rn_norm_desc* desc, const void* dout, cons
   if ((dx == dout && (desc->in_dtype != desc->out_dtype || n.ss != n.os)) || (dx == x && n.ss != n.xs) ||
       (dx == dsum && n.ss != n.rs))
     return fail(RN_ERR_INVALID_ARG, "in place needs equal types and strides");
+  const Box bd = row_box(dx, desc->in_dtype, n.ss, n);
+  if ((s = check_no_overlap(bd, row_box(x, desc->in_dtype, n.xs, n), "dx", "x")) ||
+      (s = check_no_overlap(bd, row_box(dout, desc->out_dtype, n.os, n), "dx", "dout")) ||
+      (s = check_no_overlap(bd, row_box(dsum, desc->in_dtype, n.rs, n), "dx", "dsum")))
+    return s;
   if (dweight || dbias) {
     const size_t need = (rn::norm_backward_ws_bytes(n) + 255) & ~size_t(255);
     if ((s = check_workspace(workspace, workspace_bytes, need)) != RN_OK) return s;
@@ -255,6 +320,14 @@ rn_status rn_rotary(const rn_rotary_desc* desc, const int64_t* pos, const void* 
       return fail(RN_ERR_INVALID_ARG, "k in place needs equal strides");
     if (q_out == k_out) return fail(RN_ERR_INVALID_ARG, "q_out and k_out must differ");
     if (q_out == k || k_out == q) return fail(RN_ERR_INVALID_ARG, "an output may only be its own input");
+  }
+  const Box bq = box(q, d->dtype, d->q_stride, d->B, d->H_q, d->N, d->d), bqo = box(q_out, d->dtype, d->q_out_stride, d->B, d->H_q, d->N, d->d);
+  if ((s = check_no_overlap(bqo, bq, "q_out", "q"))) return s;
+  if (d->H_k) {
+    const Box bk = box(k, d->dtype, d->k_stride, d->B, d->H_k, d->N, d->d), bko = box(k_out, d->dtype, d->k_out_stride, d->B, d->H_k, d->N, d->d);
+    if ((s = check_no_overlap(bqo, bk, "q_out", "k")) || (s = check_no_overlap(bqo, bko, "q_out", "k_out")) ||
+        (s = check_no_overlap(bko, bk, "k_out", "k")) || (s = check_no_overlap(bko, bq, "k_out", "q")))
+      return s;
   }
   rn::RotaryCall c;
   c.B = d->B; c.N = d->N; c.Hq = d->H_q; c.Hk = d->H_k; c.d = d->d; c.rot = d->rot; c.dt = d->dtype;
@@ -320,7 +393,7 @@ rn_status rn_linear_attention_chunked(const rn_linear_desc* desc, const int32_t*
   if (!aligned(state_in, 16) || !aligned(state_out, 16))
     return fail(RN_ERR_INVALID_ARG, "states must be 16-byte aligned");
   if ((s = check_workspace(workspace, workspace_bytes, rn_linear_attention_workspace_bytes(desc))) != RN_OK) return s;
-  if ((s = check_apart(c)) != RN_OK) return s;
+  if ((s = check_apart(desc, c)) != RN_OK) return s;
   c.cu = cu_seqlens; c.lens = lengths; c.state_in = state_in; c.state_out = state_out; c.ws = workspace;
   rn::clear_error();
   return hip_status(rn::launch_linear_chunked(c, static_cast<hipStream_t>(stream)), "linear attention launch");
@@ -334,7 +407,7 @@ rn_status rn_linear_attention_step(const rn_linear_desc* desc, const int32_t* sl
   if ((s = check_linear_ptrs(desc, slots, q, k, v, log_decay, out, &c)) != RN_OK) return s;
   if (!state) return fail(RN_ERR_INVALID_ARG, "state pointer is NULL");
   if (!aligned(state, 16)) return fail(RN_ERR_INVALID_ARG, "state must be 16-byte aligned");
-  if ((s = check_apart(c)) != RN_OK) return s;
+  if ((s = check_apart(desc, c)) != RN_OK) return s;
   c.state_out = state;
   rn::clear_error();
   return hip_status(rn::launch_linear_step(c, static_cast<hipStream_t>(stream)), "linear attention step launch");

@@ -273,3 +273,72 @@ def test_workspace_bytes():
         assert need <= 8 * 768 * (64 << 10) + (1 << 20), (S, N, H, dk, dv, T)
         seen += need > 0
     assert seen > 100
+
+
+def test_outputs_that_partly_overlap_are_refused():
+    """Rows or heads shifted by less than apart; views that interleave without meeting stay allowed
+    (such calls fail for the reason put into them: an unknown flag or a missing pointer)."""
+    B = 1 << 20
+    d = norm(rows=1000)                                                # 1000 rows of 64 bf16, 128 bytes apart
+    for shift in (2, 126, 128, -128, 999 * 128, -999 * 128 + 126):
+        assert norm_forward(d, x=B, out=B + shift) == INV and b"out overlaps x" in L.rn_last_error(), shift
+        assert norm_forward(d, x=B, r=4 * B, s=4 * B + shift, out=8 * B) == INV and b"sum_out overlaps residual" in L.rn_last_error()
+        assert norm_backward(d, dout=B, x=4 * B, dx=B + shift) == INV and b"dx overlaps dout" in L.rn_last_error()
+        assert norm_backward(d, dout=B, x=4 * B, dx=4 * B + shift) == INV and b"dx overlaps x" in L.rn_last_error()
+    assert norm_forward(d, x=B, out=8 * B, s=8 * B + 2) == INV and b"out overlaps sum_out" in L.rn_last_error()
+    wide = norm(rows=1000, x_stride=160, out_stride=160, sum_stride=160)
+    for shift in (128, 192, -128, 320 * 1000, 320 * 999 + 128, -320 * 1000):      # columns beside x's own, or rows behind
+        assert norm_backward(wide, dout=4 * B, x=B, dx=B + shift, ws=None) == WS, shift
+    for shift in (126, 194, -126, 320 + 126, 320 * 999 - 126):
+        assert norm_backward(wide, dout=4 * B, x=B, dx=B + shift, ws=None) == INV and b"dx overlaps x" in L.rn_last_error(), shift
+    # heads of one projection [2, 100, 12 heads of 128]: q has eight of them, k four
+    s = (12 * 128 * 100, 128, 12 * 128)
+    d = rot(B=2, N=100, H_k=4, q_stride=s, k_stride=s, q_out_stride=s, k_out_stride=s)
+    args = dict(q=B, k=B + 8 * 256, qo=16 * B, ko=32 * B)
+    for kw, text in ((dict(qo=B + 256), b"q_out overlaps q"), (dict(qo=B + 24 * 128 * 7 + 6), b"q_out overlaps q"),
+                     (dict(qo=B + 9 * 256), b"q_out overlaps q"), (dict(ko=B + 7 * 256), b"k_out overlaps"),
+                     (dict(qo=16 * B, ko=16 * B + 256), b"q_out overlaps k_out")):
+        assert rotary(d, **{**args, **kw}) == INV and text in L.rn_last_error(), kw
+    # linear attention: out among the heads of v's buffer
+    s = (0, 64, 1024)
+    one = dict(S=1, N=1 << 12, H=4, H_q=4, H_k=4, H_v=4, q_stride=s, k_stride=s, v_stride=s, out_stride=s, flags=rn.RN_LINEAR_GENERIC)
+    d = lin(**one)
+    assert L.rn_linear_attention_workspace_bytes(ctypes.byref(d)) > 0
+    f = lambda q, k, v, out: L.rn_linear_attention_chunked(  # noqa: E731
+        ctypes.byref(d), None, None, None, q, k, v, FAKE, None, None, out, 1 << 30, 1 << 40, None)
+    q, k, v = B, B + 4 * 128, B + 8 * 128
+    for out, text in ((B + 128, b"out overlaps q"), (B + 5 * 128, b"out overlaps k"), (B + 9 * 128, b"out overlaps v"),
+                      (B - 128, b"out overlaps q"), (B + 2048 * 50 + 130, b"out overlaps q")):
+        assert f(q, k, v, out) == INV and text in L.rn_last_error(), out
+
+
+def test_overlap_of_strided_boxes_against_sets_of_addresses():
+    """The layer norm's and rotary's refusals against the sets of elements that the views have."""
+    rng = np.random.default_rng(42)
+    cells = lambda n, s, d: (np.add.outer(np.add.outer(np.add.outer(np.arange(n[0]) * s[0], np.arange(n[1]) * s[1]),  # noqa: E731
+                                                       np.arange(n[2]) * s[2]), np.arange(d))).ravel()
+    base, hit, clear = 1 << 20, 0, 0
+    for _ in range(3000):
+        n, d = [int(x) for x in rng.integers(1, 5, 3)], 2 * int(rng.integers(1, 4))
+        order, s, span = rng.permutation(3), [0, 0, 0], d
+        for a in order:
+            s[a] = span + int(rng.integers(0, 4)) * int(rng.integers(0, 6))
+            span = s[a] * n[a]
+        diff = int(rng.integers(-span - d, span + d + 1))
+        if diff == 0:
+            continue
+        own = cells(n, s, d)
+        meet = bool(np.intersect1d(own, own + diff).size)
+        desc = rot(B=n[0], H_q=n[1], H_k=0, N=n[2], d=d, rot=2, q_stride=tuple(s), q_out_stride=tuple(s), dtype=1)
+        # (a call that is not refused for its overlap would launch: an unaligned pos is found before it)
+        code = L.rn_rotary(ctypes.byref(desc), None, base, None, base + 2 * diff, None, None) if meet else None
+        if meet:
+            assert code == INV and b"q_out overlaps q" in L.rn_last_error(), (n, s, d, diff)
+            hit += 1
+        else:
+            nd = norm(rows=n[2], d=d, x_stride=s[2], sum_stride=s[2], out_stride=s[2])
+            m1 = bool(np.intersect1d(cells((1, 1, n[2]), s, d), cells((1, 1, n[2]), s, d) + diff).size)
+            got = norm_backward(nd, dout=1 << 24, x=base, dx=base + 2 * diff, ws=None)
+            assert got == (INV if m1 or (n[2] > 1 and s[2] < d) else WS), (n, s, d, diff)
+            clear += got == WS
+    assert hit > 300 and clear > 300
