@@ -24,8 +24,10 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 // column vector) takes rows group, group + G, ... in batches of 8, the next batch's loads issued
 // before the present one is updated. Non-temporal: a batch's states are larger than the caches
 // and are read once a step. FULL: every thread has a column and every batch its rows, so that
-// no load hangs on a condition (128 states of 16 heads of 256 x 512: 357 us, 6.0 TB/s; with
-// conditions and half the columns a block 460 us).
+// no load hangs on a condition (128 states of 16 heads of 256 x 512: 355 us, 6.1 TB/s, where a
+// program steps the same states, 380 to 390 on states in a pool's order; with conditions and half the
+// columns a block 460 us. Of 256 x 384 in three slices of 128 columns: 289 us, with conditions 432; of
+// 128 x 192 in three of 64: 67 and 98 us).
 constexpr int kBatch = 8;
 
 template <int IN, int OUT, int VEC, int NQ, int NT, bool FULL>
@@ -495,11 +497,11 @@ hipError_t launch_step_t(const LinArgs& a, hipStream_t st) {
     return hipGetLastError();                                                                       \
   } while (0)
   if (a.dv % 4 == 0) {
-    if (states >= 512) {
-      if (a.dv == 512 && a.dk % 32 == 0) RN_STEP(4, 128, 512, true);
-      if (a.dv == 256 && a.dk % 64 == 0) RN_STEP(4, 64, 512, true);
-      if (a.dv == 128 && a.dk % 64 == 0) RN_STEP(4, 32, 256, true);
-      if (a.dv == 64 && a.dk % 128 == 0) RN_STEP(4, 16, 256, true);
+    if (states >= 512) {      // the widest slices of whole columns that whole batches of rows go with
+      if (a.dv % 512 == 0 && a.dk % 32 == 0) RN_STEP(4, 128, 512, true);
+      if (a.dv % 256 == 0 && a.dk % 64 == 0) RN_STEP(4, 64, 512, true);
+      if (a.dv % 128 == 0 && a.dk % 64 == 0) RN_STEP(4, 32, 256, true);
+      if (a.dv % 64 == 0 && a.dk % 128 == 0) RN_STEP(4, 16, 256, true);
     }
     if (a.dv > 128 && states * ((a.dv + 255) / 256) >= 512) RN_STEP(4, 64, 256, false);
     if (a.dv > 64 && states * ((a.dv + 127) / 128) >= 512) RN_STEP(4, 32, 256, false);

@@ -577,3 +577,16 @@ def test_flat_grid_with_many_sequences_of_several_segments(kind, dk, dv, L):
                            uses_mfma(kind, DT[kind], dk, dv, False))
         else:
             assert torch.equal(new[s], s0[s])
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("S,H,dk,dv", [(130, 4, 128, 192), (33, 16, 128, 320), (64, 8, 64, 384), (520, 1, 256, 448), (520, 1, 192, 384)])
+def test_step_in_several_whole_slices(kind, S, H, dk, dv):
+    """Enough states for the kernel whose threads all have columns and rows, and values of two to seven
+    of its widths of columns."""
+    q, k, v, g = inputs(S, H, H, 1, H, 1, dk, dv, kind, S + dv, resets=0.1)
+    state = torch.randn(S, H, dk, dv, device=DEV, generator=torch.Generator(DEV).manual_seed(13))
+    before = state.clone()
+    out = rn().rn_linear_attention_step(q, k, v, g, state, qk_scale=0.3)
+    for s in (0, 1, S // 2, S - 1):
+        check_sequence(out[s], state[s], q[s], k[s], v[s], g[s], 0.3, before[s])
