@@ -466,14 +466,17 @@ hipError_t launch_full(const NormCall& n, NormArgs a, hipStream_t st) {
 
 template <int IN, int OUT, int V, int W, int NV>
 hipError_t launch_one(const NormCall& n, const NormArgs& a, hipStream_t st) {
-  if (!n.vec) return launch_full<IN, OUT, V, W, NV, kOdd, false>(n, a, st);
-  if (n.d != V * lanes(W) * NV) return launch_full<IN, OUT, V, W, NV, kSome, false>(n, a, st);
-  // the call's bytes against the 256 MB last-level cache
-  // (16384 x 4096 bf16 with residual: 96 us past the caches, 103 us through them; backward
-  // 108 and 114 us)
+  // Past the caches: the call's bytes against the 256 MB last-level cache (16384 x 4096 bf16 with
+  // residual: 96 us past the caches, 103 us through them, backward 108 and 114; 16384 x 6144 138 and 148,
+  // 185 and 193; 16384 x 4001 114 and 119, 171 and 175). Not where short rows share their 64-byte lines,
+  // which would then be fetched for each (300000 x 200 bf16: 125 and 112, 124 and 116).
   const int64_t bytes = n.rows * n.d * ((IN == RN_F32 ? 4 : 2) * (n.r ? 2 : 1) + (OUT == RN_F32 ? 4 : 2) + (n.sum ? (IN == RN_F32 ? 4 : 2) : 0));
-  return bytes > (int64_t(256) << 20) ? launch_full<IN, OUT, V, W, NV, kFull, true>(n, a, st)
-                                      : launch_full<IN, OUT, V, W, NV, kFull, false>(n, a, st);
+  const int64_t row = static_cast<int64_t>(n.d) * (IN == RN_F32 ? 4 : 2);
+  const bool stream = bytes > (int64_t(256) << 20) && (row % 64 == 0 || row >= 2048);
+  if (!n.vec) return stream ? launch_full<IN, OUT, V, W, NV, kOdd, true>(n, a, st) : launch_full<IN, OUT, V, W, NV, kOdd, false>(n, a, st);
+  if (n.d != V * lanes(W) * NV)
+    return stream ? launch_full<IN, OUT, V, W, NV, kSome, true>(n, a, st) : launch_full<IN, OUT, V, W, NV, kSome, false>(n, a, st);
+  return stream ? launch_full<IN, OUT, V, W, NV, kFull, true>(n, a, st) : launch_full<IN, OUT, V, W, NV, kFull, false>(n, a, st);
 }
 
 template <int IN, int OUT>

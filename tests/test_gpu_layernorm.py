@@ -304,3 +304,32 @@ def test_every_operand_that_an_output_may_replace(kind, n, d):
         got = rn().rn_layernorm_backward(t["dy"], t["x"], w, dsum=t["dh"], dx=t[name])
         assert all(torch.equal(got[i], want[i]) for i in want), name
         assert all(i == name or torch.equal(t[i], kept) for i, kept in (("x", x), ("dy", dy), ("dh", dh)))
+
+
+@pytest.mark.parametrize("kind,n,d", [("bf16", 16411, 2568), ("f32", 30001, 96 * 9), ("bf16", 700001, 96), ("bf16", 25001, 2001),
+                                      ("f32", 9001, 4999), ("bf16", 300001, 200)])
+def test_calls_larger_than_the_caches(kind, n, d):
+    """Rows of whole and of broken pieces and lines in calls of more than 256 MB: each row comes out as
+    in a call of a few rows. The weights' gradients against float64: sums of at most n / 768 + 1 rows one
+    after another, then 24 + 32 of blocks, of products that hold 48 roundings of the normalised value (of
+    its own size and of the mean's, at most that of one)."""
+    dt = DT[kind]
+    g = torch.Generator(DEV).manual_seed(n)
+    x, r, dy = (torch.randn(n, d, generator=g, device=DEV).to(dt) for _ in range(3))
+    w, b = (torch.randn(d, generator=g, device=DEV) for _ in range(2))
+    out, total = rn().rn_layernorm(x, w, b, residual=r)
+    got = rn().rn_layernorm_backward(dy, x, w, dsum=r)
+    for at in (0, n // 3, n - 40):
+        cut = slice(at, at + 40)
+        a, c = rn().rn_layernorm(x[cut].clone(), w, b, residual=r[cut].clone())
+        assert torch.equal(out[cut], a) and torch.equal(total[cut], c)
+        dx = rn().rn_layernorm_backward(dy[cut].clone(), x[cut].clone(), w, dsum=r[cut].clone(), want_dweight=False, want_dbias=False)["dx"]
+        assert torch.equal(got["dx"][cut], dx)
+    del out, total, r
+    xd = x.double()
+    xd -= xd.mean(-1, keepdim=True)
+    xd /= (xd.square().mean(-1, keepdim=True) + 1e-5).sqrt()
+    c = (n / 768 + 1 + 24 + 32 + 48) * U
+    dyd = dy.double()
+    assert ((got["dbias"] - dyd.sum(0)).abs() <= c * dyd.abs().sum(0)).all()
+    assert ((got["dweight"] - (dyd * xd).sum(0)).abs() <= c * (dyd.abs() * (xd.abs() + 1)).sum(0)).all()
