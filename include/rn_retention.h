@@ -481,7 +481,7 @@ rn_status rn_rotary(const rn_rotary_desc* desc, const int64_t* pos, const void* 
  *                     with n_j >= fast keep theta_j, pairs with n_j <= slow take theta_j /
  *                     factor, those between are mixed in proportion to n_j; *magnitude
  *                     becomes 0.1 ln(factor) + 1 (1 for the other kinds).
- * factor >= 1; base > 1; for BY_PARTS length >= 1 and 0 <= slow < fast.
+ * factor >= 1; base > 1 and finite, the replaced one too; for BY_PARTS length >= 1 and 0 <= slow < fast.
  */
 #define RN_ROPE_PLAIN    0
 #define RN_ROPE_LINEAR   1

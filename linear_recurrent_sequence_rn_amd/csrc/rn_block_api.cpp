@@ -355,6 +355,7 @@ rn_status rn_rotary_frequencies(int32_t rot, double base, int32_t kind, double f
     return fail(RN_ERR_INVALID_ARG, "RN_ROPE_BY_PARTS needs length >= 1 and 0 <= slow < fast");
   if (!theta || !magnitude) return fail(RN_ERR_INVALID_ARG, "theta/magnitude pointer is NULL");
   const double b = kind == RN_ROPE_BASE ? base * std::pow(factor, double(rot) / (rot - 2)) : base;
+  if (!std::isfinite(b)) return fail(RN_ERR_INVALID_ARG, "base * factor^(rot/(rot-2)) is not finite");
   *magnitude = kind == RN_ROPE_BY_PARTS ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.f;
   for (int j = 0; j < rot / 2; ++j) {
     const double th = std::pow(b, -2.0 * j / rot);

@@ -342,3 +342,13 @@ def test_overlap_of_strided_boxes_against_sets_of_addresses():
             assert got == (INV if m1 or (n[2] > 1 and s[2] < d) else WS), (n, s, d, diff)
             clear += got == WS
     assert hit > 300 and clear > 300
+
+
+def test_a_replaced_base_has_to_be_finite():
+    """Past the largest number it would turn every pair but the first by nothing."""
+    with pytest.raises(rn.RnError):
+        rn.rn_rotary_frequencies(4, kind="base", factor=1e200)
+    with pytest.raises(rn.RnError):
+        rn.rn_rotary_frequencies(128, kind="base", factor=1e306)
+    theta, _ = rn.rn_rotary_frequencies(128, kind="base", factor=1e290)
+    assert np.abs(theta / (1e4 * 1e290 ** (128 / 126)) ** (-np.arange(64) / 64) - 1).max() < 1e-12
