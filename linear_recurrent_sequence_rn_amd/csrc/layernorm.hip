@@ -6,9 +6,9 @@
 // xh mean(g xh)) + dh, dw = sum_rows dy xh, db = sum_rows dy.
 //
 // Bound by HBM: every tensor is read or written once (16384 x 4096 bf16: forward with residual
-// 96 us, 5.6 TB/s; backward with the residual's gradient 109 us, 5.0 TB/s; a large copy reaches
+// 96 us, 5.6 TB/s; backward with the residual's gradient 108 us, 5.0 TB/s; a large copy reaches
 // 4.9 to 5.4 TB/s on the card). Smaller calls are bound by latency (backward of 3001 x 1537
-// float32: 22 us, of which the reduction of the weights' sums 5). A row lives in the registers of 16
+// float32: 22 us, of which the reduction of the weights' sums is 5). A row lives in the registers of 16
 // lanes (W = 0, 16 rows per 256-thread block), of one wave (W = 1) or of a whole block (W = 4 or
 // 16), so the passes
 // over it (mean, centred squares, result) cost no memory access. Blocks walk over rows:
@@ -437,10 +437,12 @@ __global__ void __launch_bounds__(1024) norm_reduce(const float* part, int block
 bool narrow(const NormCall& n) { return n.d <= 32 * (n.in_dt == RN_BF16 ? 8 : 4); }
 
 int backward_blocks(const NormCall& n) {
-  // Three blocks a CU, which is what their registers allow, and at least four rows a block (16
-  // narrow ones, which it takes at a time), so
-  // that the partial rows (2 d floats a block, written and read once) stay small beside the
-  // tensors.
+  // Three blocks a CU, which is what registers allow (rows of 16 waves: one), and at least four rows a
+  // block (16 narrow ones, which it takes at a time). A block leaves 2 d floats of partial sums, written
+  // and read once: with four rows that is half as much again as bf16 tensors with a residual, but
+  // fewer blocks leave the chip empty (bf16 rows of 4096 with residual, at least 2, 4 or 8 rows a block:
+  // 1024 rows 19, 17 and 21 us, 2048 rows 24, 23 and 23; 2048 rows of 12288 72, 59 and 50; 3001 x 1537
+  // float32 24, 25 and 28).
   const int rows = narrow(n) ? 16 : 4;
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((n.rows + rows - 1) / rows, 768)));
 }

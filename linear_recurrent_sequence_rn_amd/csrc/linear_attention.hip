@@ -2,10 +2,11 @@
 //     S_t = exp(g_t) S_{t-1} + k_t^T v_t,     o_t = scale q_t S_t.
 //
 // lin_step: one token a sequence. Bound by HBM: the float32 state is read and written once.
-// lin_float: prompts of any type and head size in chunks of 16 tokens on the float32 matrix cores.
+// lin_float: prompts of any type and head size in chunks of 16 tokens on the float32 matrix cores
+// (bf16 in and float32 out, 32 heads of 2048 tokens, 128 x 128: 129 us; bf16 of 100 x 100: 126 us).
 // Bound by the wait for each chunk's phases and the padding of small heads (padded float32 batch of
 // 3 sequences of up to 2001 tokens, 5 heads of 48 x 81: 32 us, of which the scan is 8; 32 heads of
-// 2048 tokens, 128 x 128: 129 us). The recurrence itself, token by token on the vector units,
+// 2048 tokens, 128 x 128: 131 us). The recurrence itself, token by token on the vector units,
 // took 39 and 172 us.
 // Long sequences are cut into segments: one pass gives the state each segment adds on its own,
 // lin_scan carries the states over the segments, a second pass gives the outputs; the same three
@@ -560,8 +561,8 @@ void segments(const LinCall& c, int* len, int* n) {
 }
 
 // Blocks along the segments of all sequences, where N says little about the lengths: 1024 packed
-// sequences of 28 tokens, 8 heads of 64 x 128, and no nearer bound than the tokens of all: 216 us,
-// 1382 us with S n_seg blocks (160 where the bound is given, in one pass). (S N is then more than T,
+// sequences of 28 tokens, 8 heads of 64 x 128, and no nearer bound than the tokens of all: 233 us,
+// 1622 us with S n_seg blocks (175 where the bound is given, in one pass). (S N is then more than T,
 // and T / L at most 768 by the choice of L.)
 bool flat_grid(const LinCall& c, int len, int n) {
   return n > 1 && c.T > 0 && static_cast<int64_t>(c.S) * n > 2 * (c.T / len + c.S + 1);

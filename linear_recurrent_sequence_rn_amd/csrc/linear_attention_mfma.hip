@@ -20,18 +20,19 @@
 // The next tiles are on their way in registers meanwhile.
 //
 // What bounds it: heads of 256 x 512, the matrix cores at the clock they reach under load (8192
-// tokens, 16 heads: states 130 us, scan 13 us, outputs 229 us for 225 GFLOP, of which the three
-// parts of w V are 103; one large bf16 product reaches 1230 TFLOP/s on the card). Heads of 64 and
-// 128: instruction issue, about 390 vector and 43 matrix instructions a wave and chunk at d_k 64,
-// with two or three blocks a CU (13 packed sequences, 14001 tokens, 32 heads of 64 x 128: 135 us,
-// 2.1 TB/s; 8 sequences of 2048 tokens, 32 heads of 128 x 128: 169 us, 3.2 TB/s).
+// tokens, 16 heads: 350 us for 266 GFLOP, of which the three parts of w V are 103; under the profiler
+// states 124 us, scan 13 us, outputs 293 us; one large bf16 product reaches 1230 TFLOP/s on the
+// card). Heads of 64 and 128: instruction issue, about 540 vector and 57 matrix instructions a wave
+// and chunk at d_k 64, with two or three blocks a CU (13 packed sequences, 14001 tokens, 32 heads of
+// 64 x 128: 137 to 185 us, by how long the longest is, 1.6 to 2.1 TB/s; 8 sequences of 2048 tokens, 32
+// heads of 128 x 128: 193 us, 2.8 TB/s).
 //
 // Rounding: Q, K and V are bf16 already, and what is formed from them in float32 enters a product
 // in several bf16 parts. Outputs depend on two parts of each score times its decay, of the state's
 // copy that Q S reads and, in the pass that only gives outputs, of w o V: what two parts leave out is
 // at most 2^-16 of the value, 1/256 of the one rounding that a bf16 output takes (one part, which is
-// 45 of 343 us less for 8192 tokens of 16 heads of 256 x 512, doubles that rounding). The state that
-// is kept is float32: w o V in three parts, which hold all 24 bits of it.
+// 45 us less for 8192 tokens of 16 heads of 256 x 512, doubles that rounding). The state that is kept
+// is float32: w o V in three parts, which hold all 24 bits of it.
 #include <type_traits>
 
 #include "linear_attention.h"
@@ -65,7 +66,7 @@ __device__ __forceinline__ int at(int row, int col) {
 
 // Tiles whose rows are read as row operands have 64 bytes behind each 16 rows: two such reads a
 // whole number of 512 bytes apart would become one instruction whose halves meet in the same banks
-// (18 cycles in place of 2 x 4; 8 x 2048 tokens, 32 heads of 128 x 128: 169 us, without them 175).
+// (18 cycles in place of 2 x 4; 8 x 2048 tokens, 32 heads of 128 x 128: 193 us, without them 199).
 constexpr int kGap = 64;
 template <int W>
 constexpr int kRows = 32 * W + kGap;    // bytes of 16 rows
@@ -668,10 +669,10 @@ __global__ void __launch_bounds__(64 * VW * DW, DK == 64 ? 3 : 2) lin_chunks(Lin
 }
 
 // Columns a block. With d_k above 128, 128 where d_v has them: each chunk's Q and K are then read
-// from memory and LDS for twice the columns (8 sequences of 2048 tokens, 16 heads of 256 x 512:
-// 598 us, against 684 us with 64 columns). Below, 64: more blocks a CU hide more of the waits
-// between a chunk's phases (13 packed sequences of 32 heads of 64 x 128: 140 us, against 168 us
-// with 128 columns).
+// from memory and LDS for twice the columns (8192 tokens, 16 heads of 256 x 512: 350 us, against 605
+// us with 64 columns; 8 sequences of 2048 tokens, in one pass: 651 and 637 us). Below, 64: more
+// blocks a CU hide more of the waits between a chunk's phases (13 packed sequences of 32 heads of 64 x
+// 128, with one part of each score and state: 140 us, against 168 us with 128 columns).
 int columns(const LinArgs& a) { return a.dk > 128 && a.dv > 64 ? 128 : 64; }
 
 template <int DK, int CW, int VW, int DW, LinMode MODE>

@@ -2,7 +2,7 @@
 // coordinates is turned by p theta_j and scaled; the coordinates behind are copied.
 //
 // Bound by HBM (each value read and written once: 16384 tokens of 40 heads of 128, half of each
-// turned, bf16: 73 us, 4.6 TB/s; 2 x 2047 tokens of 32 heads of 256 float32: 59 us, 4.6 TB/s) as
+// turned, bf16: 76 us, 4.4 TB/s; 2 x 2047 tokens of 32 heads of 256 float32: 61 us, 4.4 TB/s) as
 // long as the sines stay cheap: an angle
 // takes a float64 product and reduction and a float32 sine and cosine, about as long as
 // moving forty values. So a block takes a few tokens, forms their cosines and sines once,
