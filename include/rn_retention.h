@@ -419,8 +419,8 @@ size_t rn_layernorm_backward_workspace_bytes(const rn_norm_desc* desc);
  *     dweight = sum over rows of dout xh,   dbias = sum over rows of dout.
  * dsum: the gradient reaching the residual sum by its other path, or NULL (0); dx is then the
  * gradient of both x and residual. dx: in_dtype, may equal x, dout or dsum where types and
- * strides agree, and overlaps nothing else. dweight, dbias: DEVICE float32 [d] or NULL, written (not added to); their
- * sums run in a fixed order (the same bits on every call). workspace: 256-byte aligned, at
+ * strides agree, and overlaps nothing else. dweight, dbias: DEVICE float32 [d] or NULL, written (not
+ * added to); their sums run in a fixed order (the same bits on every call). workspace: 256-byte aligned, at
  * least rn_layernorm_backward_workspace_bytes(desc); unused (may be NULL) when both dweight
  * and dbias are NULL.
  */

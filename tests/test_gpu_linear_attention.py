@@ -590,3 +590,24 @@ def test_step_in_several_whole_slices(kind, S, H, dk, dv):
     out = rn().rn_linear_attention_step(q, k, v, g, state, qk_scale=0.3)
     for s in (0, 1, S // 2, S - 1):
         check_sequence(out[s], state[s], q[s], k[s], v[s], g[s], 0.3, before[s])
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("dk,dv,N", [(64, 64, 200), (128, 64, 900), (256, 96, 200), (256, 512, 900)])
+def test_columns_beside_a_nonfinite_value_keep_their_precision(bad, dk, dv, N):
+    """Chunks whose values are not all finite are added up another way: the other columns' outputs are
+    rounded once there too, at every width of the state, in one pass and over segments."""
+    H = 2
+    q, k, v, g = inputs(1, H, H, H, H, N, dk, dv, "bf16", 31 + dk, True, fade=16.0)
+    rest = [c for c in range(dv) if c != 5]
+    v[0, 1, 100, 5] = bad
+    out, S = rn().rn_linear_attention_chunked(q, k, v, g, state_out=True, qk_scale=0.1)
+    o, So = K.linear_attention(q[0], k[0], v[0], g[0], 0.1)
+    assert np.array_equal(np.isfinite(np64(out[0])), np.isfinite(o)) and np.array_equal(np.isfinite(np64(S[0])), np.isfinite(So))
+    assert not np.isfinite(o[1, 100:, 5]).any() and np.isfinite(o[1, :100]).all()
+    o, So = o[..., rest], So[..., rest]
+    mo, mS = K.linear_attention(q[0].abs(), k[0].abs(), v[0][..., rest].abs(), g[0], 0.1)
+    c = (3 * reach(g[0]) + dk + 64) * U
+    off, tol = np.abs(np64(out[0])[..., rest] - o), (c + 2 * H16 * H16) * mo * (1 + 2 * H16) + H16 * np.abs(o) + 1e-30
+    assert (off <= tol).all(), f"{(off / tol).max()} of the tolerance at {np.unravel_index((off / tol).argmax(), off.shape)}"
+    assert (np.abs(np64(S[0])[..., rest] - So) <= c * mS + 1e-30).all()
