@@ -63,6 +63,8 @@ typedef int32_t rn_status;
 typedef int32_t rn_dtype;
 #define RN_F32  0   /* IEEE float32 */
 #define RN_BF16 1   /* bfloat16 (upper half of a float32) */
+#define RN_E4M3 2   /* 8-bit float, 4 exponent and 3 mantissa bits, largest 448, no infinities (rn_rmsnorm_forward's out) */
+#define RN_INT8 3   /* 8-bit integer (rn_rmsnorm_forward's out) */
 
 /* flags */
 #define RN_NORM_D_ROW (1u << 0) /* parallel only: D_nm / sqrt(sum_{i<=n} D_ni)  (hwhale notes, 2nd rescaling) */
@@ -430,6 +432,54 @@ rn_status rn_layernorm_backward(const rn_norm_desc* desc, const void* dout, cons
                                 void* stream);
 
 /*
+ * Root-mean-square norm of rows of d values, with the residual sum before it:
+ *     h = x + residual        (h = x where residual is NULL)
+ *     y = h / sqrt(mean(h^2) + eps) * weight
+ * formed in float32; out receives y in float32 or bf16, or in 8 bits with float32 scales, one for each
+ * row or for each `group` columns of it (the last group may be shorter):
+ *     scale = max(max|y| / most, 2^-126),    out = y * (1 / scale) rounded to nearest even,
+ * most = 448 (RN_E4M3) or 127 (RN_INT8); out * scale stands for y. Where a NaN or infinity is among the
+ * values of a scale, the scale is NaN (and out is NaN in RN_E4M3, 0 in RN_INT8). sum_out receives h
+ * rounded to in_dtype.
+ */
+typedef struct rn_rms_desc {
+    int64_t rows;          /* 1 .. 2^40 */
+    int32_t d;             /* 1 .. 16384 */
+    rn_dtype in_dtype;     /* RN_F32, RN_BF16: x, residual, sum_out; backward: x, dsum, dx */
+    rn_dtype out_dtype;    /* out: any; backward: dout, RN_F32 or RN_BF16 */
+    int32_t group;         /* columns a scale: 32, 64 or 128; 0 = the whole row, and where out is not of 8 bits */
+    float eps;             /* finite, >= 0 */
+    int64_t x_stride;      /* elements between rows: x */
+    int64_t res_stride;    /* residual; backward: dsum */
+    int64_t sum_stride;    /* sum_out; backward: dx */
+    int64_t out_stride;    /* out; backward: dout */
+    int64_t scale_stride;  /* scale */
+} rn_rms_desc;
+
+/*
+ * weight: DEVICE float32 [d] or NULL (1). residual, sum_out: NULL, or rows of in_dtype. scale: DEVICE
+ * float32, rows of 1 or ceil(d / group) values; required where out is of 8 bits, else not read. sum_out
+ * may equal x or residual with the same stride, out may equal x or residual where in_dtype == out_dtype
+ * and the strides agree (out and sum_out must differ); outputs overlap nothing else.
+ */
+rn_status rn_rmsnorm_forward(const rn_rms_desc* desc, const void* x, const void* residual,
+                             const float* weight, void* sum_out, void* out, float* scale,
+                             void* stream);
+
+/* Bytes of device workspace rn_rmsnorm_backward needs (0 for an invalid descriptor). */
+size_t rn_rmsnorm_backward_workspace_bytes(const rn_rms_desc* desc);
+
+/*
+ * Gradients of y with x the rows the forward call normalised (its sum_out where it had a residual):
+ *     g = dout * weight,  xh = x / sqrt(mean(x^2) + eps)
+ *     dx = (g - xh mean(g xh)) / sqrt(mean(x^2) + eps) + dsum,    dweight = sum over rows of dout xh.
+ * dsum, dx, dweight, workspace: as for rn_layernorm_backward (workspace unused where dweight is NULL).
+ */
+rn_status rn_rmsnorm_backward(const rn_rms_desc* desc, const void* dout, const void* x,
+                              const float* weight, const void* dsum, void* dx, float* dweight,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Rotary positions: coordinate pairs of the first `rot` of d coordinates of every head are
  * turned by the angle p * theta_j of their token's position p and scaled by `magnitude`:
  *     (a, b) -> magnitude * (a cos - b sin, a sin + b cos),
@@ -561,6 +611,123 @@ rn_status rn_linear_attention_chunked(const rn_linear_desc* desc, const int32_t*
 rn_status rn_linear_attention_step(const rn_linear_desc* desc, const int32_t* slots, const void* q,
                                    const void* k, const void* v, const float* log_decay,
                                    float* state, void* out, void* stream);
+
+/*
+ * ---- the short convolution and the selective scan ------------------------------------------
+ * Batches of sequences. Padded (T = 0): sequence s holds lengths[s] tokens (DEVICE int32 [S], clamped
+ * to [0, N]; NULL = N) at row s of tensors [S, N, D]. Packed (T > 0): cu_seqlens, DEVICE int32 [S+1],
+ * holds each sequence's first token row, 0 first, of tensors [1, T, D]; rows cu_seqlens[s] ..
+ * cu_seqlens[s+1]-1 are sequence s (clamped to [0, T] and to N tokens). Rows of no sequence are not
+ * read, and not written but with RN_SEQ_ZERO_REST. Strides are (sequence, token), the sequence's being
+ * ignored if packed; B and C, as heads, have (sequence, group, token).
+ * States are addressed as linear attention's: [S, ...], or [n_slots, ...] with slots (DEVICE int32
+ * [S]; one outside [0, n_slots) starts from zeros and keeps no state; two sequences must not share a
+ * slot); NULL = start from zeros / discard; state_in and state_out may be the same buffer. A sequence
+ * without tokens passes its state on. Outputs overlap no other operand.
+ */
+#define RN_SEQ_ZERO_REST (1u << 0)     /* rows of `out` (backward: of the token gradients) of no sequence
+                                          are set to zero */
+#define RN_CONV_SILU     (1u << 1)     /* out = u sigmoid(u) */
+#define RN_SCAN_SOFTPLUS (1u << 1)     /* the step is softplus(dt + bias) */
+
+/*
+ * Short causal convolution of every channel with its own K weights:
+ *     u_t = bias + sum_{j < K} weight_j x_{t-K+1+j},    out = u, or u sigmoid(u) with RN_CONV_SILU,
+ * in float32. The K - 1 inputs before a sequence's first token are its state: rows of K - 1 tokens,
+ * [K - 1, D] a sequence, in dtype (exact copies of x).
+ */
+typedef struct rn_conv_desc {
+    int32_t S;             /* sequences, 1 .. 65534 */
+    int32_t N;             /* most tokens of a sequence, 1 .. 2^30, S * N <= 2^31 - 1; the step form needs 1 */
+    int32_t D;             /* channels, 1 .. 65536 */
+    int32_t K;             /* 1 .. 8 */
+    rn_dtype dtype;        /* RN_F32, RN_BF16: x, out, states; backward: x, dout, dx, state_in */
+    uint32_t flags;        /* RN_SEQ_ZERO_REST, RN_CONV_SILU */
+    int64_t T;             /* packed batches: token rows of the tensors, 1 .. 2^31 - 1; else 0 */
+    int32_t n_slots;
+    int64_t x_stride[2];   /* elements between sequences and tokens */
+    int64_t out_stride[2]; /* out; backward: dout */
+    int64_t dx_stride[2];  /* backward: dx */
+} rn_conv_desc;
+
+/* weight: DEVICE float32 [D, K]; bias: DEVICE float32 [D] or NULL (0). */
+rn_status rn_short_conv(const rn_conv_desc* desc, const int32_t* cu_seqlens, const int32_t* lengths,
+                        const int32_t* slots, const void* x, const float* weight, const float* bias,
+                        const void* state_in, void* state_out, void* out, void* stream);
+
+/* One token for each of S sequences; `state` is updated in place (a sequence whose slot is outside
+ * [0, n_slots) is skipped and its output row set to zero). state may be NULL where K is 1. */
+rn_status rn_short_conv_step(const rn_conv_desc* desc, const int32_t* slots, const void* x,
+                             const float* weight, const float* bias, void* state, void* out,
+                             void* stream);
+
+/* Bytes of device workspace rn_short_conv_backward needs (0 for an invalid descriptor). */
+size_t rn_short_conv_backward_workspace_bytes(const rn_conv_desc* desc);
+
+/*
+ * Gradients of rn_short_conv (states per sequence, without slots), u being recomputed:
+ *     du = dout (the derivative of the output's form at u),   dx_t = sum_j weight_j du_{t+K-1-j},
+ *     dweight_j = sum_t du_t x_{t-K+1+j},   dbias = sum_t du_t.
+ * dstate_out: float32 [S, K - 1, D] or NULL (0): the gradient reaching the final state. dx: as out.
+ * dstate_in: float32 [S, K - 1, D] or NULL. dweight [D, K], dbias [D]: float32 or NULL, written; sums in a
+ * fixed order. workspace: 256-byte aligned; unused where dweight and dbias are NULL.
+ */
+rn_status rn_short_conv_backward(const rn_conv_desc* desc, const int32_t* cu_seqlens,
+                                 const int32_t* lengths, const void* dout, const void* x,
+                                 const float* weight, const float* bias, const void* state_in,
+                                 const float* dstate_out, void* dx, float* dweight, float* dbias,
+                                 float* dstate_in, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/*
+ * Selective scan: a diagonal linear recurrence whose step, input and output the tokens set, n states a
+ * channel:
+ *     D_t = softplus(dt_t + bias)    (dt_t + bias without RN_SCAN_SOFTPLUS)
+ *     h_t = exp(D_t A) h_{t-1} + D_t x_t B_t,     y_t = C_t h_t + skip x_t,
+ *     out_t = y_t, or y_t z_t sigmoid(z_t) where z is given.
+ * Channels come in G groups of D / G that share B and C. All arithmetic is float32. A NaN or infinity
+ * at a token reaches only outputs of that token and later ones of its sequence, and its final state.
+ */
+typedef struct rn_scan_desc {
+    int32_t S;             /* sequences, 1 .. 65534 */
+    int32_t N;             /* most tokens of a sequence, 1 .. 2^30, S * N <= 2^31 - 1; the step form needs 1 */
+    int32_t D;             /* channels, 1 .. 65536 */
+    int32_t n;             /* states a channel, 1 .. 64 */
+    int32_t G;             /* groups of channels: a divisor of D */
+    rn_dtype dtype;        /* RN_F32, RN_BF16: x, dt, B, C, z, out and their gradients */
+    uint32_t flags;        /* RN_SEQ_ZERO_REST, RN_SCAN_SOFTPLUS */
+    int32_t n_slots;
+    int64_t T;             /* packed batches: token rows of the tensors, 1 .. 2^31 - 1; else 0 */
+    int64_t x_stride[2];   /* elements between sequences and tokens */
+    int64_t dt_stride[2];
+    int64_t z_stride[2];
+    int64_t out_stride[2]; /* out; backward: dout */
+    int64_t b_stride[3];   /* elements between sequences, groups and tokens */
+    int64_t c_stride[3];
+} rn_scan_desc;
+
+/* Bytes of device workspace rn_selective_scan_chunked needs (0 when it needs none, or for an invalid
+ * descriptor). */
+size_t rn_selective_scan_workspace_bytes(const rn_scan_desc* desc);
+
+/*
+ * Prompts. x, dt, z (or NULL), out [.., D]; B, C [.., G, .., n]; A: DEVICE float32 [D, n]; skip, bias:
+ * DEVICE float32 [D] or NULL (0). States: float32 [D, n] a sequence, 16-byte aligned. workspace: 256-byte
+ * aligned.
+ */
+rn_status rn_selective_scan_chunked(const rn_scan_desc* desc, const int32_t* cu_seqlens,
+                                    const int32_t* lengths, const int32_t* slots, const void* x,
+                                    const void* dt, const float* A, const void* B, const void* C,
+                                    const float* skip, const float* bias, const void* z,
+                                    const float* state_in, float* state_out, void* out,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token for each of S sequences; `state` is updated in place (a sequence whose slot is outside
+ * [0, n_slots) is skipped and its output row set to zero). */
+rn_status rn_selective_scan_step(const rn_scan_desc* desc, const int32_t* slots, const void* x,
+                                 const void* dt, const float* A, const void* B, const void* C,
+                                 const float* skip, const float* bias, const void* z, float* state,
+                                 void* out, void* stream);
 
 /* Static name of a status code. */
 const char* rn_status_str(rn_status s);

@@ -1,7 +1,8 @@
 """Multi-scale retention (RetNet) forward pass on MI355X — Python binding.
 
 A thin ctypes layer over ``librn_retention.so`` (C ABI in include/rn_retention.h).
-(The operators around retention live in block_ops.py and are exported here.)
+(The operators around retention live in block_ops.py, the short convolution and the selective scan in
+scan_ops.py; both are exported here.)
 Functions carry the C names; they only marshal arguments: check tensors, allocate
 outputs with torch, pass device pointers and the current HIP stream. Every step of
 the computation runs in the library's HIP kernels. There is no CPU fallback: if the
@@ -23,7 +24,7 @@ import torch
 __all__ = [
     "RN_OK", "RN_ERR_INVALID_ARG", "RN_ERR_UNSUPPORTED", "RN_ERR_HIP", "RN_ERR_WORKSPACE",
     "RN_ERR_EXCHANGE", "RN_ERR_NONFINITE",
-    "RN_F32", "RN_BF16", "RN_NORM_D_ROW", "RN_NORM_R_ROW", "RN_EPI_GN", "RN_EPI_GATE",
+    "RN_F32", "RN_BF16", "RN_E4M3", "RN_INT8", "RN_NORM_D_ROW", "RN_NORM_R_ROW", "RN_EPI_GN", "RN_EPI_GATE",
     "RN_FORCE_GENERIC", "RN_CHUNK_PARALLEL", "RN_CHUNK_SEGMENTED", "RN_TEST_FORCE_TIMEOUT",
     "RnError", "RnDesc", "lib", "LIB_PATH", "EXPORTED_SYMBOLS", "rn_chunkwise_check",
     "rn_retention_parallel", "rn_retention_chunkwise", "rn_retention_recurrent_step",
@@ -36,6 +37,10 @@ __all__ = [
     "RnNormDesc", "RnRotaryDesc", "RnLinearDesc", "rn_layernorm", "rn_layernorm_backward",
     "rn_layernorm_backward_workspace_bytes", "rn_rotary", "rn_rotary_frequencies",
     "rn_linear_attention_chunked", "rn_linear_attention_step", "rn_linear_attention_workspace_bytes",
+    "RnRmsDesc", "rn_rmsnorm", "rn_rmsnorm_backward", "rn_rmsnorm_backward_workspace_bytes",
+    "RN_SEQ_ZERO_REST", "RN_CONV_SILU", "RN_SCAN_SOFTPLUS", "RnConvDesc", "RnScanDesc", "rn_short_conv",
+    "rn_short_conv_step", "rn_short_conv_backward", "rn_short_conv_backward_workspace_bytes",
+    "rn_selective_scan_chunked", "rn_selective_scan_step", "rn_selective_scan_workspace_bytes",
 ]
 
 # The in-tree build; RN_LIB_PATH names another build of the same sources (the host-side
@@ -44,7 +49,7 @@ LIB_PATH = Path(os.environ.get("RN_LIB_PATH") or Path(__file__).resolve().parent
 
 RN_OK, RN_ERR_INVALID_ARG, RN_ERR_UNSUPPORTED, RN_ERR_HIP, RN_ERR_WORKSPACE = 0, -1, -2, -3, -4
 RN_ERR_EXCHANGE, RN_ERR_NONFINITE = -5, -6
-RN_F32, RN_BF16 = 0, 1
+RN_F32, RN_BF16, RN_E4M3, RN_INT8 = 0, 1, 2, 3
 RN_NORM_D_ROW, RN_NORM_R_ROW, RN_EPI_GN, RN_EPI_GATE = 1, 2, 4, 8
 RN_FORCE_GENERIC = 1 << 8
 RN_CHUNK_PARALLEL = 1 << 9
@@ -61,6 +66,9 @@ EXPORTED_SYMBOLS = (
     "rn_layernorm_forward", "rn_layernorm_backward", "rn_layernorm_backward_workspace_bytes",
     "rn_rotary", "rn_rotary_frequencies", "rn_linear_attention_workspace_bytes",
     "rn_linear_attention_chunked", "rn_linear_attention_step",
+    "rn_rmsnorm_forward", "rn_rmsnorm_backward", "rn_rmsnorm_backward_workspace_bytes",
+    "rn_short_conv", "rn_short_conv_step", "rn_short_conv_backward", "rn_short_conv_backward_workspace_bytes",
+    "rn_selective_scan_chunked", "rn_selective_scan_step", "rn_selective_scan_workspace_bytes",
 )
 
 
@@ -588,6 +596,11 @@ def rn_chunkwise_check(q, v, gamma, theta, chunk, workspace, *, gn=False, gate=N
 
 from .block_ops import (  # noqa: E402  (needs the library and the names above)
     RN_LINEAR_GENERIC, RN_LINEAR_ZERO_REST, RN_ROPE_BASE, RN_ROPE_BY_PARTS, RN_ROPE_LINEAR, RN_ROPE_PLAIN,
-    RN_ROTARY_HALF, RN_ROTARY_INVERSE, RN_ROTARY_POS_TOKEN, RnLinearDesc, RnNormDesc, RnRotaryDesc,
+    RN_ROTARY_HALF, RN_ROTARY_INVERSE, RN_ROTARY_POS_TOKEN, RnLinearDesc, RnNormDesc, RnRmsDesc, RnRotaryDesc,
     rn_layernorm, rn_layernorm_backward, rn_layernorm_backward_workspace_bytes, rn_linear_attention_chunked,
-    rn_linear_attention_step, rn_linear_attention_workspace_bytes, rn_rotary, rn_rotary_frequencies)
+    rn_linear_attention_step, rn_linear_attention_workspace_bytes, rn_rmsnorm, rn_rmsnorm_backward,
+    rn_rmsnorm_backward_workspace_bytes, rn_rotary, rn_rotary_frequencies)
+from .scan_ops import (  # noqa: E402
+    RN_CONV_SILU, RN_SCAN_SOFTPLUS, RN_SEQ_ZERO_REST, RnConvDesc, RnScanDesc, rn_selective_scan_chunked,
+    rn_selective_scan_step, rn_selective_scan_workspace_bytes, rn_short_conv, rn_short_conv_backward,
+    rn_short_conv_backward_workspace_bytes, rn_short_conv_step)

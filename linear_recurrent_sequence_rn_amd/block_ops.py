@@ -1,5 +1,5 @@
-"""The operators around retention: layer norm (forward with the residual sum, backward),
-rotary positions, and linear attention with a decay per head and token.
+"""The operators around retention: layer norm and root-mean-square norm (forward with the residual
+sum, backward), rotary positions, and linear attention with a decay per head and token.
 
 As the retention calls: the functions carry the C names and only marshal arguments. Tensors
 may have any strides as long as their last axis is contiguous (a projection's output split
@@ -15,7 +15,7 @@ from typing import Optional
 import numpy as np
 import torch
 
-from . import RN_BF16, RN_F32, _check, lib
+from . import RN_BF16, RN_E4M3, RN_F32, RN_INT8, _check, lib
 
 RN_ROTARY_HALF, RN_ROTARY_INVERSE, RN_ROTARY_POS_TOKEN = 1, 2, 4
 RN_ROPE_PLAIN, RN_ROPE_LINEAR, RN_ROPE_BASE, RN_ROPE_BY_PARTS = 0, 1, 2, 3
@@ -28,6 +28,12 @@ _i32, _i64, _f32, _f64, _vp, _sz = (ctypes.c_int32, ctypes.c_int64, ctypes.c_flo
 class RnNormDesc(ctypes.Structure):
     _fields_ = [("rows", _i64), ("d", _i32), ("in_dtype", _i32), ("out_dtype", _i32), ("eps", _f32),
                 ("x_stride", _i64), ("res_stride", _i64), ("sum_stride", _i64), ("out_stride", _i64)]
+
+
+class RnRmsDesc(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("d", _i32), ("in_dtype", _i32), ("out_dtype", _i32), ("group", _i32), ("eps", _f32),
+                ("x_stride", _i64), ("res_stride", _i64), ("sum_stride", _i64), ("out_stride", _i64),
+                ("scale_stride", _i64)]
 
 
 class RnRotaryDesc(ctypes.Structure):
@@ -49,9 +55,11 @@ class RnLinearDesc(ctypes.Structure):
 # fields one by one: a call costs the host a few microseconds in all, which is what the
 # smallest ones take.
 _pack_norm = struct.Struct("@qiiifqqqq").pack
+_pack_rms = struct.Struct("@qiiiifqqqqq").pack
 _pack_rotary = struct.Struct("@iiiiiiiIqfP12q").pack
 _pack_linear = struct.Struct("@10iIfqi15q").pack
 assert struct.calcsize("@qiiifqqqq") == ctypes.sizeof(RnNormDesc)
+assert struct.calcsize("@qiiiifqqqqq") == ctypes.sizeof(RnRmsDesc)
 assert struct.calcsize("@iiiiiiiIqfP12q") == ctypes.sizeof(RnRotaryDesc)
 assert struct.calcsize("@10iIfqi15q") == ctypes.sizeof(RnLinearDesc)
 
@@ -62,6 +70,9 @@ def _bind(L):
             ("rn_layernorm_forward", [_vp] * 8, _i32),
             ("rn_layernorm_backward_workspace_bytes", [_vp], _sz),
             ("rn_layernorm_backward", [_vp] * 9 + [_sz, _vp], _i32),
+            ("rn_rmsnorm_forward", [_vp] * 8, _i32),
+            ("rn_rmsnorm_backward_workspace_bytes", [_vp], _sz),
+            ("rn_rmsnorm_backward", [_vp] * 8 + [_sz, _vp], _i32),
             ("rn_rotary", [_vp] * 7, _i32),
             ("rn_rotary_frequencies", [_i32, _f64, _i32, _f64, _f64, _f64, _f64, _vp, _vp], _i32),
             ("rn_linear_attention_workspace_bytes", [_vp], _sz),
@@ -234,6 +245,99 @@ def rn_layernorm_backward(dout, x, weight=None, eps=1e-5, *, dsum=None, dx=None,
         workspace = None
     _call(dev, lib.rn_layernorm_backward, desc, dout.data_ptr(), x.data_ptr(), _p(weight), _p(dsum), dx.data_ptr(),
           _p(got.get("dweight")), _p(got.get("dbias")), _p(workspace), 0 if workspace is None else workspace.numel())
+    return got
+
+
+# ---- root-mean-square norm ----------------------------------------------------------------
+
+_HELD8 = {torch.float8_e4m3fn: RN_E4M3, torch.int8: RN_INT8}
+
+
+def rn_rmsnorm(x, weight=None, eps=1e-5, *, residual=None, sum_out=None, out=None, out_dtype=None, group=0,
+               scale_out=None):
+    """Root-mean-square norm over the last axis of x [..., d], after adding ``residual`` (same shape
+    and type) where given: y = h / sqrt(mean(h^2) + eps) * weight. weight: float32 [d] or None.
+
+    ``out_dtype`` (default: x's type): float32, bfloat16, or torch.float8_e4m3fn / torch.int8 with a
+    float32 scale for each row ([...]) or, with ``group`` 32, 64 or 128, for each so many columns
+    ([..., ceil(d / group)]); out * scale stands for y. Returns out, and behind it the sum x + residual
+    in x's type where a residual or ``sum_out`` is given, and the scale where out is of 8 bits.
+    ``sum_out`` and ``out`` (of x's type) may be x or residual, not both the same one."""
+    dev = _device(x, residual, weight, sum_out, out, scale_out)
+    shape = x.shape
+    d = shape[-1] if shape else 0
+    n = x.numel()
+    if n == 0 or d == 0:
+        raise ValueError(f"x must be [..., d] with at least one row; got {tuple(shape)}")
+    _like(residual, x, "residual")
+    _whole(weight, torch.float32, (d,), "weight")
+    if out is None:
+        out = _new(x, x.dtype if out_dtype is None else out_dtype)
+    elif out.shape != shape or (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError(f"out must be {out_dtype or out.dtype} {tuple(shape)}; got {out.dtype} {tuple(out.shape)}")
+    code = _HELD8.get(out.dtype)
+    scale, step = None, 0
+    if code is None:
+        code = _code(out.dtype)
+        if scale_out is not None:
+            raise ValueError("scale_out goes with an output of 8 bits")
+    else:
+        step = -(-d // group) if group > 0 else 1
+        ss = (*shape[:-1], step) if group else shape[:-1]
+        if scale_out is None:
+            scale = torch.empty(ss, dtype=torch.float32, device=x.device)
+        else:
+            _whole(scale_out, torch.float32, ss, "scale_out")
+            scale = scale_out
+    if sum_out is None:
+        if residual is not None:
+            sum_out = _new(x, x.dtype)
+    else:
+        _like(sum_out, x, "sum_out")
+    desc = _pack_rms(n // d, d, _code(x.dtype), code, group, eps, _row_stride(x, "x"), _row_stride(residual, "residual"),
+                     _row_stride(sum_out, "sum_out"), _row_stride(out, "out"), step)
+    _call(dev, lib.rn_rmsnorm_forward, desc, x.data_ptr(), _p(residual), _p(weight), _p(sum_out), out.data_ptr(), _p(scale))
+    if sum_out is None and scale is None:
+        return out
+    return (out,) + (() if sum_out is None else (sum_out,)) + (() if scale is None else (scale,))
+
+
+def _rms_backward_desc(dout, x, eps, dsum, dx):
+    d = x.shape[-1]
+    return _pack_rms(x.numel() // d, d, _code(x.dtype), _code(dout.dtype), 0, eps, _row_stride(x, "x"),
+                     _row_stride(dsum, "dsum"), _row_stride(dx, "dx"), _row_stride(dout, "dout"), 0)
+
+
+def rn_rmsnorm_backward_workspace_bytes(dout, x) -> int:
+    return int(lib.rn_rmsnorm_backward_workspace_bytes(_rms_backward_desc(dout, x, 0.0, None, x)))
+
+
+def rn_rmsnorm_backward(dout, x, weight=None, eps=1e-5, *, dsum=None, dx=None, want_dweight=True, workspace=None):
+    """Gradients of ``rn_rmsnorm``'s y: x are the rows it normalised (its sum where it had a residual),
+    ``dsum`` the gradient that reaches this sum by its other path, in x's type. Returns a dict with dx
+    (the gradient of x and of the residual; in x's type) and, unless not wanted, dweight (float32 [d]).
+    ``dx`` may be x, dsum, or dout of x's type."""
+    dev = _device(x, dout, weight, dsum, dx, workspace)
+    if x.numel() == 0 or x.dim() == 0:
+        raise ValueError(f"x must be [..., d] with at least one row; got {tuple(x.shape)}")
+    d = x.shape[-1]
+    if dout.shape != x.shape:
+        raise ValueError(f"dout must have x's shape {tuple(x.shape)}; got {tuple(dout.shape)}")
+    _whole(weight, torch.float32, (d,), "weight")
+    _like(dsum, x, "dsum")
+    if dx is None:
+        dx = _new(x, x.dtype)
+    else:
+        _like(dx, x, "dx")
+    desc = _rms_backward_desc(dout, x, eps, dsum, dx)
+    got = {"dx": dx}
+    if want_dweight:
+        got["dweight"] = torch.empty(d, dtype=torch.float32, device=x.device)
+        workspace = _get_workspace(workspace, lib.rn_rmsnorm_backward_workspace_bytes(desc), x)
+    else:
+        workspace = None
+    _call(dev, lib.rn_rmsnorm_backward, desc, dout.data_ptr(), x.data_ptr(), _p(weight), _p(dsum), dx.data_ptr(),
+          _p(got.get("dweight")), _p(workspace), 0 if workspace is None else workspace.numel())
     return got
 
 

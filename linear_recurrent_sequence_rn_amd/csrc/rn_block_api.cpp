@@ -1,32 +1,19 @@
-// C ABI of the operators around retention (layer norm, rotary positions, linear attention):
+// C ABI of the operators around retention (norms, rotary positions, linear attention):
 // host-side validation and dispatch, before any HIP call.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
 #include <cstring>
-#include <utility>
 
+#include "api_checks.h"
 #include "rn_kernels.h"
 #include "rn_retention.h"
 
 namespace {
 
-using rn::fail;
-using rn::hip_status;
+using namespace rn;
 
-bool dtype_ok(rn_dtype d) { return d == RN_F32 || d == RN_BF16; }
-int64_t size_of(rn_dtype d) { return d == RN_F32 ? 4 : 2; }
-bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-constexpr int64_t kMaxStride = int64_t(1) << 40;
 constexpr int kMaxNorm = 16384;
-
-rn_status check_workspace(const void* ws, size_t have, size_t need) {
-  if (need == 0) return RN_OK;
-  if (!ws || have < need)
-    return fail(RN_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws ? have : size_t(0), need);
-  if (!aligned(ws, 256)) return fail(RN_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
-  return RN_OK;
-}
 
 // ---- layer norm ---------------------------------------------------------------------------
 
@@ -56,91 +43,52 @@ bool norm_vectors(const rn::NormCall& n) {
          ok(n.w, 0) && ok(n.b, 0);
 }
 
-rn_status check_rows_out(const rn::NormCall& n, int64_t stride, const char* what) {
-  if (n.rows > 1 && stride < n.d)
-    return fail(RN_ERR_INVALID_ARG, "%s: row stride %lld < d=%d (its rows would overlap)", what, (long long)stride, n.d);
+rn_status check_rows_out(int64_t rows, int d, int64_t stride, const char* what) {
+  if (rows > 1 && stride < d)
+    return fail(RN_ERR_INVALID_ARG, "%s: row stride %lld < d=%d (its rows would overlap)", what, (long long)stride, d);
+  return RN_OK;
+}
+Box row_box(const void* p, rn_dtype dt, int64_t stride, int64_t rows, int d) {
+  return Box{p, size_of(dt), {0, 0, stride}, {1, 1, rows}, d};
+}
+
+// ---- RMS norm -----------------------------------------------------------------------------
+
+bool held8(rn_dtype d) { return d == RN_E4M3 || d == RN_INT8; }
+
+rn_status check_rms(const rn_rms_desc* d, bool back, rn::RmsCall* n) {
+  if (!d) return fail(RN_ERR_INVALID_ARG, "desc is NULL");
+  if (d->rows < 1 || d->d < 1)
+    return fail(RN_ERR_INVALID_ARG, "sizes must be >= 1 (rows=%lld d=%d)", (long long)d->rows, d->d);
+  if (d->rows > (int64_t(1) << 40)) return fail(RN_ERR_UNSUPPORTED, "rows=%lld > 2^40", (long long)d->rows);
+  if (d->d > kMaxNorm) return fail(RN_ERR_UNSUPPORTED, "d=%d > %d", d->d, kMaxNorm);
+  if (!dtype_ok(d->in_dtype) || !(dtype_ok(d->out_dtype) || (!back && held8(d->out_dtype))))
+    return fail(RN_ERR_INVALID_ARG, "unknown dtype (in=%d out=%d)", d->in_dtype, d->out_dtype);
+  if (!(d->eps >= 0.f && std::isfinite(d->eps))) return fail(RN_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (d->group != 0 && !held8(d->out_dtype))
+    return fail(RN_ERR_INVALID_ARG, "group=%d goes with an output of 8 bits", d->group);
+  if (d->group != 0 && d->group != 32 && d->group != 64 && d->group != 128)
+    return fail(RN_ERR_UNSUPPORTED, "group=%d is not 0, 32, 64 or 128", d->group);
+  for (int64_t s : {d->x_stride, d->res_stride, d->sum_stride, d->out_stride, d->scale_stride})
+    if (s < 0 || s > kMaxStride) return fail(RN_ERR_INVALID_ARG, "row stride %lld outside [0, 2^40]", (long long)s);
+  std::memset(n, 0, sizeof(*n));
+  n->rows = d->rows; n->d = d->d; n->group = d->group; n->in_dt = d->in_dtype; n->out_dt = d->out_dtype; n->eps = d->eps;
+  n->xs = d->x_stride; n->rs = d->res_stride; n->ss = d->sum_stride; n->os = d->out_stride; n->cs = d->scale_stride;
+  n->backward = back;
   return RN_OK;
 }
 
-rn_status check_elements(const void* p, rn_dtype dt, const char* what) {
-  if (!aligned(p, size_of(dt)))
-    return fail(RN_ERR_INVALID_ARG, "%s must be %d-byte aligned", what, int(size_of(dt)));
-  return RN_OK;
+// Every row of every tensor starts and ends on a whole piece: 16 bytes of the input type.
+bool rms_vectors(const rn::RmsCall& n) {
+  const int v = n.in_dt == RN_BF16 ? 8 : 4;
+  auto ok = [&](const void* p, int64_t stride, size_t align) {
+    return !p || (aligned(p, align) && (n.rows == 1 || stride % v == 0));
+  };
+  return n.d % v == 0 && ok(n.x, n.xs, 16) && ok(n.r, n.rs, 16) && ok(n.sum, n.ss, 16) && ok(n.dout, n.os, 16) &&
+         ok(n.out, n.os, held8(n.out_dt) ? v : 16) && ok(n.w, 0, 16);
 }
 
 // ---- rotary -------------------------------------------------------------------------------
-
-rn_status check_strides(const int64_t* s, const char* what) {
-  for (int i = 0; i < 3; ++i)
-    if (s[i] < 0 || s[i] > kMaxStride)
-      return fail(RN_ERR_INVALID_ARG, "%s stride %lld outside [0, 2^40]", what, (long long)s[i]);
-  return RN_OK;
-}
-
-// An output's elements must be distinct: ordered by stride, each axis has to step over all
-// that the axes inside it cover.
-rn_status check_distinct(const int64_t* s, int64_t n0, int64_t n1, int64_t n2, int64_t d, const char* what) {
-  int64_t st[3] = {s[0], s[1], s[2]}, n[3] = {n0, n1, n2};
-  for (int i = 0; i < 3; ++i)
-    for (int j = i + 1; j < 3; ++j)
-      if (st[j] < st[i]) { std::swap(st[i], st[j]); std::swap(n[i], n[j]); }
-  __int128 span = d;   // stride * size may pass 64 bits
-  for (int i = 0; i < 3; ++i) {
-    if (n[i] <= 1) continue;
-    if (st[i] < span)
-      return fail(RN_ERR_INVALID_ARG, "%s: strides %lld, %lld, %lld make it overlap itself", what,
-                  (long long)s[0], (long long)s[1], (long long)s[2]);
-    span += static_cast<__int128>(st[i]) * (n[i] - 1);
-  }
-  return RN_OK;
-}
-
-// A tensor: three strided axes of elements of `es` bytes, and d contiguous ones.
-struct Box {
-  const void* p;
-  int64_t es, s[3], n[3], d;
-};
-
-// Whether elements at i . s + [0, a.d) and diff + j . s + [0, b.d) meet, i and j inside the boxes: the
-// steps k = i - j along the axes from `axis` on, ordered by falling stride, that bring diff near 0.
-bool meets(int64_t diff, const Box& a, const Box& b, const int64_t* s, const int* order, int axis) {
-  if (axis == 3) return diff < a.d * a.es && -diff < b.d * b.es;
-  const int x = order[axis];
-  const int64_t st = s[x] * a.es, up = a.n[x] - 1, down = b.n[x] - 1;
-  if (st == 0) return meets(diff, a, b, s, order, axis + 1);
-  const int64_t k0 = diff / st;           // (k st is at most st from diff, an address, away)
-  for (int64_t k = k0 - 1; k <= k0 + 1; ++k)
-    if (k <= up && -k <= down && meets(diff - k * st, a, b, s, order, axis + 1)) return true;
-  return false;
-}
-
-// Whether an output overlaps another operand, as far as two tensors of one type and the same strides
-// show it (of others nothing is said). The same tensor in both places is no overlap here.
-bool overlaps(const Box& out, const Box& in) {
-  if (!in.p || in.p == out.p || out.es != in.es) return false;
-  int64_t s[3];
-  int order[3] = {0, 1, 2};
-  for (int i = 0; i < 3; ++i) {
-    if (out.n[i] > 1 && in.n[i] > 1 && out.s[i] != in.s[i]) return false;
-    s[i] = out.n[i] > 1 ? out.s[i] : in.n[i] > 1 ? in.s[i] : 0;
-  }
-  for (int i = 0; i < 3; ++i)
-    for (int j = i + 1; j < 3; ++j)
-      if (s[order[j]] > s[order[i]]) std::swap(order[i], order[j]);
-  const int64_t diff = static_cast<int64_t>(reinterpret_cast<uintptr_t>(in.p) - reinterpret_cast<uintptr_t>(out.p));
-  return meets(diff, out, in, s, order, 0);
-}
-
-rn_status check_no_overlap(const Box& out, const Box& in, const char* what, const char* other) {
-  if (overlaps(out, in)) return fail(RN_ERR_INVALID_ARG, "%s overlaps %s", what, other);
-  return RN_OK;
-}
-Box box(const void* p, rn_dtype dt, const int64_t* s, int64_t n0, int64_t n1, int64_t n2, int64_t d) {
-  return Box{p, size_of(dt), {s[0], s[1], s[2]}, {n0, n1, n2}, d};
-}
-Box row_box(const void* p, rn_dtype dt, int64_t stride, const rn::NormCall& n) {
-  return Box{p, size_of(dt), {0, 0, stride}, {1, 1, n.rows}, n.d};
-}
 
 // ---- linear attention -----------------------------------------------------------------------
 
@@ -223,15 +171,15 @@ rn_status rn_layernorm_forward(const rn_norm_desc* desc, const void* x, const vo
   if ((s = check_elements(x, desc->in_dtype, "x")) || (s = check_elements(residual, desc->in_dtype, "residual")) ||
       (s = check_elements(sum_out, desc->in_dtype, "sum_out")) || (s = check_elements(out, desc->out_dtype, "out")) ||
       (s = check_elements(weight, RN_F32, "weight")) || (s = check_elements(bias, RN_F32, "bias")) ||
-      (s = check_rows_out(n, n.os, "out")) || (sum_out && (s = check_rows_out(n, n.ss, "sum_out"))))
+      (s = check_rows_out(n.rows, n.d, n.os, "out")) || (sum_out && (s = check_rows_out(n.rows, n.d, n.ss, "sum_out"))))
     return s;
   if (out == sum_out) return fail(RN_ERR_INVALID_ARG, "out and sum_out must differ");
   if ((out == x && (desc->in_dtype != desc->out_dtype || n.os != n.xs)) ||
       (out == residual && (desc->in_dtype != desc->out_dtype || n.os != n.rs)) ||
       (sum_out && ((sum_out == x && n.ss != n.xs) || (sum_out == residual && n.ss != n.rs))))
     return fail(RN_ERR_INVALID_ARG, "in place needs equal types and strides");
-  const Box bx = row_box(x, desc->in_dtype, n.xs, n), br = row_box(residual, desc->in_dtype, n.rs, n),
-            bs = row_box(sum_out, desc->in_dtype, n.ss, n), bo = row_box(out, desc->out_dtype, n.os, n);
+  const Box bx = row_box(x, desc->in_dtype, n.xs, n.rows, n.d), br = row_box(residual, desc->in_dtype, n.rs, n.rows, n.d),
+            bs = row_box(sum_out, desc->in_dtype, n.ss, n.rows, n.d), bo = row_box(out, desc->out_dtype, n.os, n.rows, n.d);
   if ((s = check_no_overlap(bo, bx, "out", "x")) || (s = check_no_overlap(bo, br, "out", "residual")) ||
       (s = check_no_overlap(bo, bs, "out", "sum_out")) ||
       (sum_out && ((s = check_no_overlap(bs, bx, "sum_out", "x")) || (s = check_no_overlap(bs, br, "sum_out", "residual")))))
@@ -258,15 +206,15 @@ rn_status rn_layernorm_backward(const rn_norm_desc* desc, const void* dout, cons
   if ((s = check_elements(x, desc->in_dtype, "x")) || (s = check_elements(dsum, desc->in_dtype, "dsum")) ||
       (s = check_elements(dx, desc->in_dtype, "dx")) || (s = check_elements(dout, desc->out_dtype, "dout")) ||
       (s = check_elements(weight, RN_F32, "weight")) || (s = check_elements(dweight, RN_F32, "dweight")) ||
-      (s = check_elements(dbias, RN_F32, "dbias")) || (s = check_rows_out(n, n.ss, "dx")))
+      (s = check_elements(dbias, RN_F32, "dbias")) || (s = check_rows_out(n.rows, n.d, n.ss, "dx")))
     return s;
   if ((dx == dout && (desc->in_dtype != desc->out_dtype || n.ss != n.os)) || (dx == x && n.ss != n.xs) ||
       (dx == dsum && n.ss != n.rs))
     return fail(RN_ERR_INVALID_ARG, "in place needs equal types and strides");
-  const Box bd = row_box(dx, desc->in_dtype, n.ss, n);
-  if ((s = check_no_overlap(bd, row_box(x, desc->in_dtype, n.xs, n), "dx", "x")) ||
-      (s = check_no_overlap(bd, row_box(dout, desc->out_dtype, n.os, n), "dx", "dout")) ||
-      (s = check_no_overlap(bd, row_box(dsum, desc->in_dtype, n.rs, n), "dx", "dsum")))
+  const Box bd = row_box(dx, desc->in_dtype, n.ss, n.rows, n.d);
+  if ((s = check_no_overlap(bd, row_box(x, desc->in_dtype, n.xs, n.rows, n.d), "dx", "x")) ||
+      (s = check_no_overlap(bd, row_box(dout, desc->out_dtype, n.os, n.rows, n.d), "dx", "dout")) ||
+      (s = check_no_overlap(bd, row_box(dsum, desc->in_dtype, n.rs, n.rows, n.d), "dx", "dsum")))
     return s;
   if (dweight || dbias) {
     const size_t need = (rn::norm_backward_ws_bytes(n) + 255) & ~size_t(255);
@@ -277,6 +225,73 @@ rn_status rn_layernorm_backward(const rn_norm_desc* desc, const void* dout, cons
   n.vec = norm_vectors(n);
   rn::clear_error();
   return hip_status(rn::launch_layernorm(n, static_cast<hipStream_t>(stream)), "layer norm backward launch");
+}
+
+rn_status rn_rmsnorm_forward(const rn_rms_desc* desc, const void* x, const void* residual, const float* weight,
+                             void* sum_out, void* out, float* scale, void* stream) {
+  rn::RmsCall n;
+  rn_status s = check_rms(desc, false, &n);
+  if (s != RN_OK) return s;
+  const bool small = held8(desc->out_dtype);
+  if (!x || !out || (small && !scale)) return fail(RN_ERR_INVALID_ARG, "x/out/scale pointer is NULL");
+  if ((s = check_elements(x, desc->in_dtype, "x")) || (s = check_elements(residual, desc->in_dtype, "residual")) ||
+      (s = check_elements(sum_out, desc->in_dtype, "sum_out")) || (s = check_elements(out, desc->out_dtype, "out")) ||
+      (s = check_elements(weight, RN_F32, "weight")) || (small && (s = check_elements(scale, RN_F32, "scale"))) ||
+      (s = check_rows_out(n.rows, n.d, n.os, "out")) || (sum_out && (s = check_rows_out(n.rows, n.d, n.ss, "sum_out"))))
+    return s;
+  const int scales = n.group ? (n.d + n.group - 1) / n.group : 1;
+  if (small && (s = check_rows_out(n.rows, scales, n.cs, "scale"))) return s;
+  if (out == sum_out) return fail(RN_ERR_INVALID_ARG, "out and sum_out must differ");
+  if ((out == x && (desc->in_dtype != desc->out_dtype || n.os != n.xs)) ||
+      (out == residual && (desc->in_dtype != desc->out_dtype || n.os != n.rs)) ||
+      (sum_out && ((sum_out == x && n.ss != n.xs) || (sum_out == residual && n.ss != n.rs))))
+    return fail(RN_ERR_INVALID_ARG, "in place needs equal types and strides");
+  if (small && (scale == x || scale == residual || scale == sum_out || scale == out || scale == weight))
+    return fail(RN_ERR_INVALID_ARG, "scale must be no other operand");
+  const Box bx = row_box(x, desc->in_dtype, n.xs, n.rows, n.d), br = row_box(residual, desc->in_dtype, n.rs, n.rows, n.d),
+            bs = row_box(sum_out, desc->in_dtype, n.ss, n.rows, n.d), bo = row_box(out, desc->out_dtype, n.os, n.rows, n.d);
+  if ((s = check_no_overlap(bo, bx, "out", "x")) || (s = check_no_overlap(bo, br, "out", "residual")) ||
+      (s = check_no_overlap(bo, bs, "out", "sum_out")) ||
+      (sum_out && ((s = check_no_overlap(bs, bx, "sum_out", "x")) || (s = check_no_overlap(bs, br, "sum_out", "residual")))))
+    return s;
+  n.x = x; n.r = residual; n.w = weight; n.sum = sum_out; n.out = out; n.scale = scale;
+  n.vec = rms_vectors(n);
+  rn::clear_error();
+  return hip_status(rn::launch_rmsnorm(n, static_cast<hipStream_t>(stream)), "RMS norm launch");
+}
+
+size_t rn_rmsnorm_backward_workspace_bytes(const rn_rms_desc* desc) {
+  rn::RmsCall n;
+  if (check_rms(desc, true, &n) != RN_OK) return 0;
+  return (rn::rms_backward_ws_bytes(n) + 255) & ~size_t(255);
+}
+
+rn_status rn_rmsnorm_backward(const rn_rms_desc* desc, const void* dout, const void* x, const float* weight,
+                              const void* dsum, void* dx, float* dweight, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  rn::RmsCall n;
+  rn_status s = check_rms(desc, true, &n);
+  if (s != RN_OK) return s;
+  if (!dout || !x || !dx) return fail(RN_ERR_INVALID_ARG, "dout/x/dx pointer is NULL");
+  if ((s = check_elements(x, desc->in_dtype, "x")) || (s = check_elements(dsum, desc->in_dtype, "dsum")) ||
+      (s = check_elements(dx, desc->in_dtype, "dx")) || (s = check_elements(dout, desc->out_dtype, "dout")) ||
+      (s = check_elements(weight, RN_F32, "weight")) || (s = check_elements(dweight, RN_F32, "dweight")) ||
+      (s = check_rows_out(n.rows, n.d, n.ss, "dx")))
+    return s;
+  if ((dx == dout && (desc->in_dtype != desc->out_dtype || n.ss != n.os)) || (dx == x && n.ss != n.xs) ||
+      (dx == dsum && n.ss != n.rs))
+    return fail(RN_ERR_INVALID_ARG, "in place needs equal types and strides");
+  const Box bd = row_box(dx, desc->in_dtype, n.ss, n.rows, n.d);
+  if ((s = check_no_overlap(bd, row_box(x, desc->in_dtype, n.xs, n.rows, n.d), "dx", "x")) ||
+      (s = check_no_overlap(bd, row_box(dout, desc->out_dtype, n.os, n.rows, n.d), "dx", "dout")) ||
+      (s = check_no_overlap(bd, row_box(dsum, desc->in_dtype, n.rs, n.rows, n.d), "dx", "dsum")))
+    return s;
+  if (dweight && (s = check_workspace(workspace, workspace_bytes, (rn::rms_backward_ws_bytes(n) + 255) & ~size_t(255))))
+    return s;
+  n.x = x; n.r = dsum; n.w = weight; n.sum = dx; n.dout = dout; n.dw = dweight; n.ws = workspace;
+  n.vec = rms_vectors(n);
+  rn::clear_error();
+  return hip_status(rn::launch_rmsnorm(n, static_cast<hipStream_t>(stream)), "RMS norm backward launch");
 }
 
 rn_status rn_rotary(const rn_rotary_desc* desc, const int64_t* pos, const void* q, const void* k, void* q_out,

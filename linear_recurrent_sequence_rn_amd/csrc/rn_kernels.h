@@ -105,6 +105,27 @@ struct NormCall {
 size_t norm_backward_ws_bytes(const NormCall& n);
 hipError_t launch_layernorm(const NormCall& n, hipStream_t st);
 
+struct RmsCall {
+  int64_t rows;
+  int32_t d, group;
+  int in_dt, out_dt;
+  float eps;
+  bool backward;
+  bool vec;                       // every row and pointer allows whole pieces
+  int64_t xs, rs, ss, os, cs;     // row strides: x, residual / dsum, sum_out / dx, out / dout, scale
+  const void* x;
+  const void* r;
+  const float* w;
+  void* sum;
+  void* out;
+  float* scale;
+  const void* dout;
+  float* dw;
+  void* ws;
+};
+size_t rms_backward_ws_bytes(const RmsCall& n);
+hipError_t launch_rmsnorm(const RmsCall& n, hipStream_t st);
+
 constexpr int kMaxRot = 256;
 struct RotaryCall {
   int32_t B, N, Hq, Hk, d, rot;
@@ -145,6 +166,60 @@ struct LinCall {
 size_t lin_ws_bytes(const LinCall& c);
 hipError_t launch_linear_step(const LinCall& c, hipStream_t st);
 hipError_t launch_linear_chunked(const LinCall& c, hipStream_t st);
+
+struct ConvCall {
+  int32_t S, N, D, K, n_slots;
+  int64_t T;
+  int dt;
+  bool silu, zero_rest, backward, step;
+  bool vec;                       // every row and pointer allows 16-byte accesses
+  const int64_t *xs, *os, *ds;    // host [2]: sequence and token strides of x, out / dout, dx
+  const int32_t* cu;
+  const int32_t* lens;
+  const int32_t* slots;
+  const void* x;
+  const float* w;
+  const float* b;
+  const void* state_in;
+  void* state_out;
+  void* out;
+  const void* dout;
+  void* dx;
+  const float* dstate_out;
+  float* dstate_in;
+  float* dw;
+  float* db;
+  void* ws;
+};
+size_t conv_backward_ws_bytes(const ConvCall& c);
+hipError_t launch_short_conv(const ConvCall& c, hipStream_t st);
+
+struct ScanCall {
+  int32_t S, N, D, n, G, n_slots;
+  int64_t T;
+  int type;
+  bool softplus, zero_rest;
+  const int64_t *xs, *dts, *zs, *os;   // host [2]: sequence and token strides
+  const int64_t *bs, *cs;              // host [3]: sequence, group and token strides
+  const int32_t* cu;
+  const int32_t* lens;
+  const int32_t* slots;
+  const void* x;
+  const void* dt;
+  const void* z;
+  const void* b;
+  const void* c;
+  const float* A;
+  const float* skip;
+  const float* bias;
+  const float* state_in;
+  float* state_out;
+  void* out;
+  void* ws;
+};
+size_t scan_ws_bytes(const ScanCall& c);
+hipError_t launch_selective_scan(const ScanCall& c, hipStream_t st);
+hipError_t launch_selective_step(const ScanCall& c, hipStream_t st);
 
 // Records the message of a failed call (rn_last_error) and returns its status.
 rn_status fail(rn_status s, const char* fmt, ...);

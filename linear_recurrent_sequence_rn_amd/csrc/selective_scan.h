@@ -1,0 +1,118 @@
+// Selective scan: what its kernels share.
+//     D_t = softplus(dt_t + bias),  h_t = exp(D_t A) h_{t-1} + D_t x_t B_t,
+//     y_t = C_t h_t + skip x_t,     out_t = y_t z_t sigmoid(z_t)
+// for every channel, with n states each; channels of a group share B and C.
+//
+// A block takes 64 channels of one group (a lane each) and a segment of a sequence; its four waves share
+// the n states, NS each, in registers. What belongs to a channel and a token (the softplus, the gate)
+// is worked out once, for a tile of kTile tokens at a time, and reaches the waves through LDS; B and C
+// are the same for all lanes and come through scalar registers.
+#pragma once
+#include <type_traits>
+
+#include "rn_kernels.h"
+#include "sequences.h"
+
+namespace rn {
+
+constexpr int kTile = 16;                // tokens a tile: each wave prepares four
+constexpr int kEach = kTile / 4;
+constexpr float kLog2e = 1.44269504088896341f;
+
+struct ScanArgs {
+  Seqs q;
+  int32_t D, n, G, n_slots;
+  int32_t tiles;                          // blocks along the channels of a group
+  bool softplus, zero_rest;
+  int64_t xs[2], dts[2], zs[2], os[2];    // sequence and token strides
+  int64_t bs[3], cs[3];                   // sequence, group and token strides
+  const int32_t* slots;
+  const void* x;
+  const void* dt;
+  const void* z;
+  const void* b;
+  const void* c;
+  const float* A;                         // [D][n]
+  const float* skip;                      // [D] or null
+  const float* bias;                      // [D] or null
+  const float* state_in;
+  float* state_out;
+  void* out;
+  float* seg_state;                       // [pieces][D][n]: what a segment adds, then its starting state
+  float* seg_step;                        // [pieces][D]: the sum of a segment's D_t
+};
+
+// softplus(v) to float32 accuracy at any v: max(v, 0) + log1p(e), e = exp(-|v|), with
+// log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3, by the series of atanh (its first dropped term is
+// 2 s^14 / 15 < 3e-8 of s).
+__device__ __forceinline__ float softplus(float v) {
+  const float m = -fabsf(v), t = m * kLog2e;
+  // (what rounding the exponent loses: |v| 2^-24 of e)
+  float e = __builtin_amdgcn_exp2f(t);
+  e = fmaf(e, fmaf(m, kLog2e, -t) * 0.6931472f, e);
+  const float d = 2.0f + e;
+  float r = __builtin_amdgcn_rcpf(d);
+  r = fmaf(fmaf(-d, r, 1.0f), r, r);
+  const float s = e * r, q = s * s;
+  float p = fmaf(q, 2.0f / 13.0f, 2.0f / 11.0f);
+  p = fmaf(p, q, 2.0f / 9.0f);
+  p = fmaf(p, q, 2.0f / 7.0f);
+  p = fmaf(p, q, 2.0f / 5.0f);
+  p = fmaf(p, q, 2.0f / 3.0f);
+  p = fmaf(p, q, 2.0f);
+  return fmaxf(v, 0.0f) + s * p;
+}
+__device__ __forceinline__ float sigmoidf(float v) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v * kLog2e));
+}
+
+// The wave's first lane's value, as a scalar.
+__device__ __forceinline__ int64_t uniform64(int64_t x) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(static_cast<uint64_t>(x) >> 32));
+  return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+// NS values of B or C, the same for the whole wave, from element i (also the same) of p. FAST: through
+// the scalar cache; all NS are there, bf16 in pairs that start on 4 bytes. Else every lane loads the
+// first `have` of them, the rest being zeros.
+template <int DT, int NS, bool FAST>
+struct Uniform;
+template <int DT, int NS>
+struct Uniform<DT, NS, true> {
+  static constexpr int kWords = DT == RN_F32 ? NS : NS / 2;
+  uint32_t u[kWords];
+  __device__ __forceinline__ void load(const void* p, int64_t i, int) {
+    typedef const __attribute__((address_space(4))) uint32_t* words;
+    const words w = (words)static_cast<uint64_t>(uniform64(reinterpret_cast<int64_t>(p) + i * (DT == RN_F32 ? 4 : 2)));
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) u[k] = w[k];
+  }
+  __device__ __forceinline__ float value(int k) const {
+    if constexpr (DT == RN_F32) return __uint_as_float(u[k]);
+    else return __uint_as_float(k % 2 ? u[k / 2] & 0xffff0000u : u[k / 2] << 16);
+  }
+};
+template <int DT, int NS>
+struct Uniform<DT, NS, false> {
+  float f[NS];
+  __device__ __forceinline__ void load(const void* p, int64_t i, int have) {
+#pragma unroll
+    for (int k = 0; k < NS; ++k) f[k] = k < have ? Elem<DT>::load(p, i + k) : 0.f;
+  }
+  __device__ __forceinline__ float value(int k) const { return f[k]; }
+};
+
+// States a wave holds: a quarter of them, at least two.
+inline int scan_states(int n) { return n <= 8 ? 2 : n <= 16 ? 4 : n <= 32 ? 8 : 16; }
+// Whether a call's B and C can come through the scalar cache.
+inline bool scan_fast(const ScanArgs& a, int dt) {
+  const int ns = scan_states(a.n);
+  if (a.n % ns) return false;
+  if (dt == RN_F32) return true;
+  for (int i = 0; i < 3; ++i)
+    if (a.bs[i] % 2 || a.cs[i] % 2) return false;
+  return reinterpret_cast<uintptr_t>(a.b) % 4 == 0 && reinterpret_cast<uintptr_t>(a.c) % 4 == 0;
+}
+
+}  // namespace rn

@@ -9,7 +9,9 @@ oracle, decomposition by coordinate pair, agreement of the forms) and
 tests/test_oracle_layer.py (the gated multi-scale layer: explicit loops, identity
 projections, head permutation) and tests/test_oracle_block.py (layer norm, rotary
 positions, linear attention: finite differences, closed forms, agreement with the
-retention oracle); no function here is left unpinned.
+retention oracle) and tests/test_oracle_scan.py (root-mean-square norm, short convolution,
+selective scan: finite differences, closed forms, agreement with linear attention); no function
+here is left unpinned.
 """
 from .retention import *  # noqa: F401,F403
 from .retention import __all__ as _fwd_all
@@ -19,6 +21,6 @@ from .vector_decay import __all__ as _vec_all
 from .layer import *  # noqa: F401,F403
 from .layer import __all__ as _layer_all
 
-from . import block  # noqa: F401
+from . import block, scan  # noqa: F401
 
-__all__ = list(_fwd_all) + ["backward", "block"] + list(_vec_all) + list(_layer_all)
+__all__ = list(_fwd_all) + ["backward", "block", "scan"] + list(_vec_all) + list(_layer_all)

@@ -1,0 +1,212 @@
+"""The short causal convolution on the GPU against the float64 oracle.
+
+Tolerances. u adds K products to the bias by fma: (K + 1) roundings of 2^-24 of the sum of their sizes M.
+u sigmoid(u): the sigmoid's exponential is off by |u| 2^-23 or so and its reciprocal and products by a
+few 2^-24, so (8 + 2 |u|) 2^-24 of the value; its slope is at most 1.1. Then half a step of the output."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import scan as O
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+U = 2.0 ** -24
+HALF = {torch.float32: U, torch.bfloat16: 2.0 ** -8}
+
+
+def rn():
+    import linear_recurrent_sequence_rn_amd as m
+    return m
+
+
+def f64(t):
+    return None if t is None else t.double().cpu().numpy()
+
+
+class Batch:
+    """Random sequences: padded with lengths, or packed with rows behind the last one."""
+
+    def __init__(self, seed, lens, D, K, kind, packed, pad=3, bias=True, start=True, view=False, dtype=torch.float32):
+        g = torch.Generator().manual_seed(seed)
+        self.lens, self.packed, self.K = lens, packed, K
+        rows = sum(lens) + pad if packed else max(max(lens), 1) + pad
+        B = 1 if packed else len(lens)
+        off = 1 if view else 0
+        rnd = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+        self.x = rnd(B, rows, D + 2 * off).to(kind).to(DEV)[..., off:D + off]
+        self.dy = rnd(B, rows, D + 3 * off).to(kind).to(DEV)[..., off:D + off]
+        self.w = (rnd(D, K) / K ** 0.5).to(DEV)
+        self.b = (rnd(D) * 0.3).to(DEV) if bias else None
+        self.state = rnd(len(lens), K - 1, D).to(kind).to(DEV) if start else None
+        self.dstate = rnd(len(lens), K - 1, D).to(DEV)
+        self.kw = {}
+        if packed:
+            self.kw["cu_seqlens"] = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device=DEV)
+        else:
+            self.kw["lengths"] = torch.tensor(lens, dtype=torch.int32, device=DEV)
+
+    def spans(self):
+        at = 0
+        for i, n in enumerate(self.lens):
+            yield i, (0, slice(at, at + n)) if self.packed else (i, slice(0, n)), n
+            at += n
+
+    def rest(self, t):
+        """The rows of no sequence."""
+        m = torch.ones(t.shape[:2], dtype=torch.bool, device=t.device)
+        for _, at, _ in self.spans():
+            m[at] = False
+        return t[m]
+
+
+def sizes(x, w, b, s):
+    """Sum of |w x| and |b| for each token."""
+    a = lambda t: None if t is None else np.abs(t)  # noqa: E731
+    return O.short_conv(a(x), a(w), a(b), False, a(s))[0]
+
+
+def allowed(b, x, silu, s):
+    u, _ = O.short_conv(x, f64(b.w), f64(b.b), False, s)
+    off = (b.K + 1) * U * sizes(x, f64(b.w), f64(b.b), s)
+    if silu:
+        off = 1.1 * off + (8 + 2 * np.abs(u)) * U * np.abs(u * O.sigmoid(u))
+    return off
+
+
+CASES = [([1], 1, 4), ([5], 3, 2), ([16], 8, 4), ([17, 0, 2], 64, 4), ([33, 1, 64], 65, 3), ([100], 130, 8), ([7, 7], 16, 1),
+         ([0, 0], 24, 4), ([1, 2, 3, 4, 5], 40, 5), ([65, 200, 3], 520, 4), ([70], 513, 6), ([1100], 8, 7), ([300, 0, 129], 1024, 4)]
+
+
+@pytest.mark.parametrize("lens,D,K", CASES)
+@pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("packed", [False, True])
+def test_prompts(lens, D, K, kind, packed):
+    for n, (silu, bias, start, view) in enumerate([(True, True, True, False), (False, False, False, False), (True, True, True, True)]):
+        b = Batch(D * 7 + K + n, lens, D, K, kind, packed, bias=bias, start=start, view=view)
+        out, state = rn().rn_short_conv(b.x, b.w, b.b, silu=silu, state_in=b.state, state_out=True, **b.kw)
+        assert (b.rest(out) == 0).all()
+        for i, at, m in b.spans():
+            s = f64(b.state[i]) if start else None
+            x = f64(b.x[at])
+            want, last = O.short_conv(x, f64(b.w), f64(b.b), silu, s)
+            assert (np.abs(f64(out[at]) - want) <= allowed(b, x, silu, s) + HALF[kind] * np.abs(want)).all()
+            assert np.array_equal(f64(state[i]), last)
+
+
+@pytest.mark.parametrize("lens,D,K", CASES)
+@pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("packed", [False, True])
+def test_gradients(lens, D, K, kind, packed):
+    """du is off by (|u| + 16) 2^-24 of its size and by the slope's change (at most 0.6) over u's own
+    error; dx adds K, dw and db a thread's 16 tokens and trees of them: (16 + 16 + 64) roundings."""
+    for n, (silu, bias, start, view) in enumerate([(True, True, True, False), (False, False, False, False), (True, True, True, True)]):
+        b = Batch(D * 5 + K + n, lens, D, K, kind, packed, bias=bias, start=start, view=view)
+        got = rn().rn_short_conv_backward(b.dy, b.x, b.w, b.b, silu=silu, state_in=b.state, dstate_out=b.dstate,
+                                          want_dstate_in=True, **b.kw)
+        assert ("dbias" in got) == bias
+        assert (b.rest(got["dx"]) == 0).all()
+        w = f64(b.w)
+        dw, db, bw, bb = np.zeros_like(w), np.zeros(D), np.zeros_like(w), np.zeros(D)
+        for i, at, m in b.spans():
+            s = f64(b.state[i]) if start else None
+            x, dy = f64(b.x[at]), f64(b.dy[at])
+            wx, ww, wb, ws = O.short_conv_backward(dy, x, w, f64(b.b), silu, s, f64(b.dstate[i]))
+            off = np.abs(dy)                # how far du may be off, and its size
+            size = np.abs(dy) * 1.1
+            if silu:
+                u, _ = O.short_conv(x, w, f64(b.b), False, s)
+                off = off * ((np.abs(u) * 2 + 16) * U + 0.6 * (K + 1) * U * sizes(x, w, f64(b.b), s))
+            else:
+                off = off * 0.0
+            per = off + (K + 2) * U * size
+            dxo, dwo, dbo, dso = O.short_conv_backward(per, np.abs(x), np.abs(w), None, False, None if s is None else np.abs(s), U * np.abs(f64(b.dstate[i])))
+            assert (np.abs(f64(got["dx"][at]) - wx) <= dxo + HALF[kind] * np.abs(wx) + 1e-37).all()
+            assert (np.abs(f64(got["dstate_in"][i]) - ws) <= dso + U * np.abs(ws) + 1e-37).all()
+            _, dws, dbs, _ = O.short_conv_backward(size, np.abs(x), np.abs(w), None, False, None if s is None else np.abs(s))
+            dw += ww
+            db += wb
+            bw += dwo + 96 * U * dws
+            bb += dbo + 96 * U * dbs
+        assert (np.abs(f64(got["dweight"]) - dw) <= bw + 1e-37).all()
+        if bias:
+            assert (np.abs(f64(got["dbias"]) - db) <= bb + 1e-37).all()
+
+
+@pytest.mark.parametrize("D,K", [(1, 4), (24, 1), (130, 2), (512, 4), (1000, 8), (4096, 3)])
+@pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
+def test_single_tokens_go_on_where_prompts_end(D, K, kind):
+    b = Batch(D + K, [9, 6], D, K, kind, False, pad=0)
+    whole, last = rn().rn_short_conv(b.x, b.w, b.b, silu=True, state_in=b.state, state_out=True)
+    _, state = rn().rn_short_conv(b.x[:, :3], b.w, b.b, silu=True, state_in=b.state, state_out=True)
+    for t in range(3, 9):
+        out = rn().rn_short_conv_step(b.x[:, t:t + 1], b.w, b.b, state, silu=True)
+        assert torch.equal(out, whole[:, t:t + 1])
+    assert torch.equal(state, last)
+
+
+def test_slots_in_place_and_skipped_sequences():
+    b = Batch(3, [5, 1, 0, 8], 40, 4, torch.bfloat16, True)
+    pool = torch.randn(7, 3, 40, generator=torch.Generator().manual_seed(1)).bfloat16().to(DEV)
+    before = pool.clone()
+    slots = torch.tensor([6, 2, -1, 9], dtype=torch.int32, device=DEV)
+    out, s = rn().rn_short_conv(b.x, b.w, b.b, state_in=pool, state_out=pool, slots=slots, **b.kw)
+    assert s is pool
+    for i, at, n in b.spans():
+        slot = int(slots[i])
+        first = before[slot][None] if 0 <= slot < 7 else torch.zeros_like(before[:1])
+        if n:
+            want, last = rn().rn_short_conv(b.x[at][None].contiguous(), b.w, b.b, state_in=first, state_out=True)
+            assert torch.equal(out[at], want[0])
+            if 0 <= slot < 7:
+                assert torch.equal(pool[slot], last[0])
+    for i in (0, 1, 3, 4, 5):
+        assert torch.equal(pool[i], before[i])
+    x = b.x[0, :4, None].contiguous()
+    y = rn().rn_short_conv_step(x, b.w, b.b, pool, slots=slots)
+    assert (y[2:] == 0).all() and (y[:2] != 0).any()
+    for i in (0, 1, 3, 4, 5):
+        assert torch.equal(pool[i], before[i])
+
+
+def test_rows_past_max_len_and_given_outputs():
+    """A given output keeps what it holds in rows of no sequence; longer sequences are cut."""
+    b = Batch(8, [20, 30], 48, 4, torch.float32, False)
+    out = torch.full_like(b.x, 7.0)
+    rn().rn_short_conv(b.x, b.w, b.b, out=out, max_len=25, **b.kw)
+    new, state = rn().rn_short_conv(b.x, b.w, b.b, max_len=25, state_out=True, **b.kw)
+    assert (out[0, 20:] == 7).all() and (out[1, 25:] == 7).all() and (new[0, 20:] == 0).all() and (new[1, 25:] == 0).all()
+    assert torch.equal(out[0, :20], new[0, :20]) and torch.equal(out[1, :25], new[1, :25])
+    assert torch.equal(state[1], b.x[1, 22:25])
+    p = Batch(9, [20, 30], 48, 4, torch.float32, True)
+    new, state = rn().rn_short_conv(p.x, p.w, p.b, max_len=25, state_out=True, **p.kw)
+    assert (new[0, 45:] == 0).all() and torch.equal(state[1], p.x[0, 42:45])
+    got = rn().rn_short_conv_backward(p.dy, p.x, p.w, p.b, max_len=25, dx=torch.full_like(p.x, 7.0), **p.kw)
+    assert (got["dx"][0, 45:] == 7).all() and (got["dx"][0, :45] != 7).any(-1).all()
+
+
+def test_values_that_are_not_finite_reach_the_next_tokens_only():
+    b = Batch(4, [40], 72, 4, torch.bfloat16, False, pad=0)
+    clean, _ = rn().rn_short_conv(b.x, b.w, b.b, silu=True)
+    x = b.x.clone()
+    x[0, 20, 5] = float("nan")
+    x[0, 30, 6] = float("inf")
+    out, _ = rn().rn_short_conv(x, b.w, b.b, silu=True)
+    bad = out.isnan()
+    assert bad[0, 20:24, 5].all() and not bad[0, :20].any() and not bad[0, 24:, 5].any()
+    keep = torch.ones_like(bad)
+    keep[0, 20:24, 5] = False
+    keep[0, 30:34, 6] = False
+    assert torch.equal(out[keep], clean[keep])
+
+
+def test_cu_seqlens_that_make_no_sense_stay_inside_the_tensors():
+    """Falling or far entries: nothing outside the tensors is touched (guard rows keep their values)."""
+    g = torch.Generator().manual_seed(2)
+    big = torch.randn(1, 300, 32, generator=g).to(DEV)
+    x = big[:, 100:200]
+    w = torch.randn(32, 4, generator=g).to(DEV)
+    for cu in ([0, 90, 20, 60], [0, 1 << 30, -5, 100], [-7, 50, 50, 1 << 30], [100, 100, 0, 0]):
+        out = torch.full((1, 300, 32), 7.0, device=DEV)
+        rn().rn_short_conv(x, w, cu_seqlens=torch.tensor(cu, dtype=torch.int32, device=DEV), out=out[:, 100:200])
+        assert (out[:, :100] == 7).all() and (out[:, 200:] == 7).all()
