@@ -729,6 +729,40 @@ rn_status rn_selective_scan_step(const rn_scan_desc* desc, const int32_t* slots,
                                  const float* skip, const float* bias, const void* z, float* state,
                                  void* out, void* stream);
 
+/* Strides of the gradients, as the inputs' own. */
+typedef struct rn_scan_grad_desc {
+    int64_t dx_stride[2];  /* elements between sequences and tokens */
+    int64_t ddt_stride[2];
+    int64_t dz_stride[2];
+    int64_t db_stride[3];  /* elements between sequences, groups and tokens */
+    int64_t dc_stride[3];
+} rn_scan_grad_desc;
+
+/* Bytes of device workspace rn_selective_scan_backward needs (0 for an invalid descriptor). */
+size_t rn_selective_scan_backward_workspace_bytes(const rn_scan_desc* desc);
+
+/*
+ * Gradients of rn_selective_scan_chunked (states per sequence, without slots) given those of its output and,
+ * optionally, of its final state (dstate_out: float32 [S, D, n] or NULL); the states are recomputed. With
+ * dy = dout z sigmoid(z) (dout without z), g_t = C_t dy_t + exp(D_{t+1} A) g_{t+1} and
+ * p_t = exp(D_t A) h_{t-1}:
+ *     dC_t = sum_d dy_t h_t,    dB_t = sum_d g_t D_t x_t    (d: the channels of a group)
+ *     dx_t = D_t sum_n g_t B_t + skip dy_t,    dz_t = dout_t y_t (z sigmoid(z))'
+ *     ddt_t = (x_t sum_n g_t B_t + sum_n g_t p_t A) times the derivative of the step
+ *     dA = sum_t g_t p_t D_t,    dskip = sum_t dy_t x_t,    dbias = sum_t ddt_t
+ * dx, ddt, dB, dC and dz (NULL without z) in dtype; dA float32 [D, n]; dskip, dbias float32 [D] or NULL
+ * (not wanted); dstate_in float32 [S, D, n] or NULL. All are written; sums run in a fixed order.
+ * workspace: 256-byte aligned.
+ */
+rn_status rn_selective_scan_backward(const rn_scan_desc* desc, const rn_scan_grad_desc* grads,
+                                     const int32_t* cu_seqlens, const int32_t* lengths,
+                                     const void* dout, const void* x, const void* dt, const float* A,
+                                     const void* B, const void* C, const float* skip,
+                                     const float* bias, const void* z, const float* state_in,
+                                     const float* dstate_out, void* dx, void* ddt, float* dA, void* dB,
+                                     void* dC, float* dskip, float* dbias, void* dz, float* dstate_in,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static name of a status code. */
 const char* rn_status_str(rn_status s);
 /* Message describing the last failure on the calling thread ("" if none). */

@@ -41,6 +41,7 @@ __all__ = [
     "RN_SEQ_ZERO_REST", "RN_CONV_SILU", "RN_SCAN_SOFTPLUS", "RnConvDesc", "RnScanDesc", "rn_short_conv",
     "rn_short_conv_step", "rn_short_conv_backward", "rn_short_conv_backward_workspace_bytes",
     "rn_selective_scan_chunked", "rn_selective_scan_step", "rn_selective_scan_workspace_bytes",
+    "RnScanGradDesc", "rn_selective_scan_backward", "rn_selective_scan_backward_workspace_bytes",
 ]
 
 # The in-tree build; RN_LIB_PATH names another build of the same sources (the host-side
@@ -69,6 +70,7 @@ EXPORTED_SYMBOLS = (
     "rn_rmsnorm_forward", "rn_rmsnorm_backward", "rn_rmsnorm_backward_workspace_bytes",
     "rn_short_conv", "rn_short_conv_step", "rn_short_conv_backward", "rn_short_conv_backward_workspace_bytes",
     "rn_selective_scan_chunked", "rn_selective_scan_step", "rn_selective_scan_workspace_bytes",
+    "rn_selective_scan_backward", "rn_selective_scan_backward_workspace_bytes",
 )
 
 
@@ -601,6 +603,7 @@ from .block_ops import (  # noqa: E402  (needs the library and the names above)
     rn_linear_attention_step, rn_linear_attention_workspace_bytes, rn_rmsnorm, rn_rmsnorm_backward,
     rn_rmsnorm_backward_workspace_bytes, rn_rotary, rn_rotary_frequencies)
 from .scan_ops import (  # noqa: E402
-    RN_CONV_SILU, RN_SCAN_SOFTPLUS, RN_SEQ_ZERO_REST, RnConvDesc, RnScanDesc, rn_selective_scan_chunked,
+    RN_CONV_SILU, RN_SCAN_SOFTPLUS, RN_SEQ_ZERO_REST, RnConvDesc, RnScanDesc, RnScanGradDesc,
+    rn_selective_scan_backward, rn_selective_scan_backward_workspace_bytes, rn_selective_scan_chunked,
     rn_selective_scan_step, rn_selective_scan_workspace_bytes, rn_short_conv, rn_short_conv_backward,
     rn_short_conv_backward_workspace_bytes, rn_short_conv_step)

@@ -221,6 +221,23 @@ size_t scan_ws_bytes(const ScanCall& c);
 hipError_t launch_selective_scan(const ScanCall& c, hipStream_t st);
 hipError_t launch_selective_step(const ScanCall& c, hipStream_t st);
 
+struct ScanGrads {                // the call's out strides are those of dout
+  const int64_t *dxs, *ddts, *dzs, *dbs, *dcs;   // host, as the inputs'
+  const void* dout;
+  const float* dstate_out;
+  void* dx;
+  void* ddt;
+  void* dz;
+  void* db;
+  void* dc;
+  float* dA;
+  float* dskip;
+  float* dbias;
+  float* dstate_in;
+};
+size_t scan_backward_ws_bytes(const ScanCall& c);
+hipError_t launch_selective_backward(const ScanCall& c, const ScanGrads& g, hipStream_t st);
+
 // Records the message of a failed call (rn_last_error) and returns its status.
 rn_status fail(rn_status s, const char* fmt, ...);
 rn_status hip_status(hipError_t e, const char* what);

@@ -260,4 +260,56 @@ rn_status rn_selective_scan_step(const rn_scan_desc* desc, const int32_t* slots,
   return hip_status(rn::launch_selective_step(c, static_cast<hipStream_t>(stream)), "selective scan step launch");
 }
 
+size_t rn_selective_scan_backward_workspace_bytes(const rn_scan_desc* desc) {
+  rn::ScanCall c;
+  if (check_scan(desc, false, &c) != RN_OK) return 0;
+  return (rn::scan_backward_ws_bytes(c) + 255) & ~size_t(255);
+}
+
+rn_status rn_selective_scan_backward(const rn_scan_desc* desc, const rn_scan_grad_desc* grads, const int32_t* cu_seqlens,
+                                     const int32_t* lengths, const void* dout, const void* x, const void* dt, const float* A,
+                                     const void* B, const void* C, const float* skip, const float* bias, const void* z,
+                                     const float* state_in, const float* dstate_out, void* dx, void* ddt, float* dA, void* dB,
+                                     void* dC, float* dskip, float* dbias, void* dz, float* dstate_in, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  rn::ScanCall c;
+  rn_status s = check_scan(desc, false, &c);
+  if (s != RN_OK) return s;
+  if (!grads) return fail(RN_ERR_INVALID_ARG, "grads is NULL");
+  if ((s = check_scan_ptrs(desc, x, dt, A, B, C, skip, bias, z, &c)) || (s = check_lists(desc->T, cu_seqlens, lengths, nullptr, 0)))
+    return s;
+  if (!dout || !dx || !ddt || !dA || !dB || !dC) return fail(RN_ERR_INVALID_ARG, "dout/dx/ddt/dA/dB/dC pointer is NULL");
+  if ((z != nullptr) != (dz != nullptr)) return fail(RN_ERR_INVALID_ARG, "dz goes with z");
+  const Box in = token_box(desc, dout, desc->out_stride);
+  struct { Box b; const int64_t* strides; const char* name; bool heads; } outs[5] = {
+      {token_box(desc, dx, grads->dx_stride), grads->dx_stride, "dx", false},
+      {token_box(desc, ddt, grads->ddt_stride), grads->ddt_stride, "ddt", false},
+      {group_box(desc, dB, grads->db_stride), grads->db_stride, "dB", true},
+      {group_box(desc, dC, grads->dc_stride), grads->dc_stride, "dC", true},
+      {token_box(desc, dz, grads->dz_stride), grads->dz_stride, "dz", false}};
+  if ((s = check_elements(dout, desc->dtype, "dout"))) return s;
+  for (int i = 0; i < (dz ? 5 : 4); ++i) {
+    const auto& o = outs[i];
+    if ((s = o.heads ? check_strides(o.strides, o.name) : check_pair(o.strides, o.name)) || (s = check_elements(o.b.p, desc->dtype, o.name)) ||
+        (s = check_distinct(o.b, o.name)) || (s = check_scan_apart(desc, c, o.b, o.name)) || (s = check_apart(o.b, in, o.name, "dout")))
+      return s;
+    for (int j = 0; j < i; ++j)
+      if ((s = check_apart(o.b, outs[j].b, o.name, outs[j].name))) return s;
+  }
+  for (const float* p : {static_cast<const float*>(dA), static_cast<const float*>(dskip), static_cast<const float*>(dbias)})
+    if ((s = check_elements(p, RN_F32, "dA/dskip/dbias"))) return s;
+  for (const float* p : {state_in, dstate_out, static_cast<const float*>(dstate_in)})
+    if (!aligned(p, 16)) return fail(RN_ERR_INVALID_ARG, "states and their gradients must be 16-byte aligned");
+  if (dstate_in && (dstate_in == dstate_out || dstate_in == state_in))
+    return fail(RN_ERR_INVALID_ARG, "dstate_in must be no other operand");
+  if ((s = check_workspace(workspace, workspace_bytes, rn_selective_scan_backward_workspace_bytes(desc)))) return s;
+  c.cu = cu_seqlens; c.lens = lengths; c.state_in = state_in; c.ws = workspace;
+  rn::ScanGrads g;
+  g.dxs = grads->dx_stride; g.ddts = grads->ddt_stride; g.dzs = grads->dz_stride; g.dbs = grads->db_stride; g.dcs = grads->dc_stride;
+  g.dout = dout; g.dstate_out = dstate_out; g.dx = dx; g.ddt = ddt; g.dz = dz; g.db = dB; g.dc = dC;
+  g.dA = dA; g.dskip = dskip; g.dbias = dbias; g.dstate_in = dstate_in;
+  rn::clear_error();
+  return hip_status(rn::launch_selective_backward(c, g, static_cast<hipStream_t>(stream)), "selective scan backward launch");
+}
+
 }  // extern "C"

@@ -88,6 +88,12 @@ struct Uniform<DT, NS, true> {
 #pragma unroll
     for (int k = 0; k < kWords; ++k) u[k] = w[k];
   }
+  // the same, or zeros (and nothing read) where `have` is 0
+  __device__ __forceinline__ void load_or_zero(const void* p, int64_t i, int have) {
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) u[k] = 0;
+    if (have) load(p, i, have);
+  }
   __device__ __forceinline__ float value(int k) const {
     if constexpr (DT == RN_F32) return __uint_as_float(u[k]);
     else return __uint_as_float(k % 2 ? u[k / 2] & 0xffff0000u : u[k / 2] << 16);
@@ -100,8 +106,23 @@ struct Uniform<DT, NS, false> {
 #pragma unroll
     for (int k = 0; k < NS; ++k) f[k] = k < have ? Elem<DT>::load(p, i + k) : 0.f;
   }
+  __device__ __forceinline__ void load_or_zero(const void* p, int64_t i, int have) { load(p, i, have); }
   __device__ __forceinline__ float value(int k) const { return f[k]; }
 };
+
+// The call's kernel arguments, with `len` tokens a piece.
+inline ScanArgs scan_args(const ScanCall& c, int len) {
+  ScanArgs a;
+  a.q = Seqs{c.S, c.N, c.T, 0, 0, c.cu, c.lens};
+  seq_cut(&a.q, len);
+  a.D = c.D; a.n = c.n; a.G = c.G; a.n_slots = c.n_slots; a.tiles = (c.D / c.G + 63) / 64;
+  a.softplus = c.softplus; a.zero_rest = c.zero_rest;
+  for (int i = 0; i < 2; ++i) { a.xs[i] = c.xs[i]; a.dts[i] = c.dts[i]; a.zs[i] = c.zs[i]; a.os[i] = c.os[i]; }
+  for (int i = 0; i < 3; ++i) { a.bs[i] = c.bs[i]; a.cs[i] = c.cs[i]; }
+  a.slots = c.slots; a.x = c.x; a.dt = c.dt; a.z = c.z; a.b = c.b; a.c = c.c; a.A = c.A; a.skip = c.skip; a.bias = c.bias;
+  a.state_in = c.state_in; a.state_out = c.state_out; a.out = c.out; a.seg_state = nullptr; a.seg_step = nullptr;
+  return a;
+}
 
 // States a wave holds: a quarter of them, at least two.
 inline int scan_states(int n) { return n <= 8 ? 2 : n <= 16 ? 4 : n <= 32 ? 8 : 16; }

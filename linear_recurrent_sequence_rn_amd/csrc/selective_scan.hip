@@ -275,19 +275,6 @@ int segment(const ScanCall& c) {
   return static_cast<int>(L);
 }
 
-ScanArgs scan_args(const ScanCall& c, int len) {
-  ScanArgs a;
-  a.q = Seqs{c.S, c.N, c.T, 0, 0, c.cu, c.lens};
-  seq_cut(&a.q, len);
-  a.D = c.D; a.n = c.n; a.G = c.G; a.n_slots = c.n_slots; a.tiles = (c.D / c.G + 63) / 64;
-  a.softplus = c.softplus; a.zero_rest = c.zero_rest;
-  for (int i = 0; i < 2; ++i) { a.xs[i] = c.xs[i]; a.dts[i] = c.dts[i]; a.zs[i] = c.zs[i]; a.os[i] = c.os[i]; }
-  for (int i = 0; i < 3; ++i) { a.bs[i] = c.bs[i]; a.cs[i] = c.cs[i]; }
-  a.slots = c.slots; a.x = c.x; a.dt = c.dt; a.z = c.z; a.b = c.b; a.c = c.c; a.A = c.A; a.skip = c.skip; a.bias = c.bias;
-  a.state_in = c.state_in; a.state_out = c.state_out; a.out = c.out; a.seg_state = nullptr; a.seg_step = nullptr;
-  return a;
-}
-
 }  // namespace
 
 size_t scan_ws_bytes(const ScanCall& c) {

@@ -1,0 +1,569 @@
+// Gradients of the selective scan (selective_scan.h). With dy = dout z sigmoid(z) (dout without z), and
+// g_t the gradient of h_t:
+//     g_t = C_t dy_t + a_{t+1} g_{t+1},    a_t = exp(D_t A),    p_t = a_t h_{t-1},   u_t = D_t x_t
+//     dC_t = sum_d dy_t h_t,   dB_t = sum_d g_t u_t,   du_t = sum_n g_t B_t
+//     dx_t = du_t D_t + skip dy_t,   dD_t = du_t x_t + sum_n g_t p_t A,   ddt_t = dD_t softplus'(dt_t + bias)
+//     dA = sum_t g_t p_t D_t,   dskip = sum_t dy_t x_t,   dbias = sum_t ddt_t
+//     dz_t = dout y_t (z sigmoid(z))'.
+//
+// Sequences are cut into pieces of 8 tiles. scan_edges gives, for each piece, the state it adds on its own
+// and the gradient it passes back on its own; scan_edges_carry joins them along the sequence; scan_main
+// takes every piece by itself: once forward for the state at each tile's start (kept in LDS), then tile by
+// tile from the last one, forward for a tile's decays and states (kept in registers) and back for the
+// gradients. Lanes are channels and waves share the states, so sums over states meet in LDS, and sums over
+// a block's 64 channels in a transposing tree across lanes: 64 sums of 64 lanes, one left in each lane,
+// in 141 instructions. Sums over all channels' blocks and over pieces are added in a fixed order by
+// scan_sum_tokens and scan_sum_pieces.
+#include <algorithm>
+
+#include "selective_scan.h"
+
+namespace rn {
+namespace {
+
+struct BackArgs {
+  ScanArgs s;                             // its out strides are dout's; its pieces of 8 tiles
+  int64_t dxs[2], ddts[2], dzs[2], dbs[3], dcs[3];
+  const void* dout;
+  const float* dstate_out;                // [S][D][n] or null
+  void* dx;
+  void* ddt;
+  void* dz;
+  void* db;
+  void* dc;
+  float* dA;
+  float* dskip;
+  float* dbias;
+  float* dstate_in;
+  float* seg_grad;                        // [pieces][D][n]: the gradient a piece passes back (on its own, then in all)
+  float* part_skip;                       // [pieces][D]
+  float* part_bias;                       // [pieces][D]
+  float* part_bc;                         // [token rows][blocks along channels][2][n]
+};
+
+constexpr int tile_of(int NS) { return 32 / NS; }
+constexpr int kTiles = 8;                 // tiles a piece
+
+// What a block of either kernel works on.
+template <int NS>
+struct Place {
+  Span p;
+  int64_t piece;
+  int first, nt, last;                    // first token, tokens, the sequence's last piece
+  int lane, wave, x, group, d, n0, have, waves;
+  bool mine;
+  __device__ __forceinline__ bool find(const ScanArgs& a) {
+    piece = blockIdx.y + static_cast<int64_t>(blockIdx.z) * gridDim.y;
+    x = blockIdx.x;
+    lane = threadIdx.x & 63;
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    group = x / a.tiles;
+    const int each = a.D / a.G, in_group = (x - group * a.tiles) * 64 + lane;
+    mine = in_group < each;
+    d = group * each + in_group;
+    n0 = wave * NS;
+    have = min(NS, a.n - n0);
+    waves = (a.n + NS - 1) / NS;
+    if (!seq_place(a.q, piece, &p)) return false;
+    p.piece = __builtin_amdgcn_readfirstlane(p.piece);
+    const int len = __builtin_amdgcn_readfirstlane(p.len);
+    first = p.piece * a.q.len;
+    last = len > 0 ? (len - 1) / a.q.len : 0;
+    nt = min(len - first, a.q.len);
+    return true;
+  }
+  __device__ __forceinline__ int64_t tokens(const ScanArgs& a, const int64_t* st) const {
+    return (a.q.T > 0 ? uniform64(p.row0) * st[1] : p.s * st[0]) + static_cast<int64_t>(first) * st[1] + d;
+  }
+  __device__ __forceinline__ int64_t groups(const ScanArgs& a, const int64_t* st) const {
+    return (a.q.T > 0 ? uniform64(p.row0) * st[2] : p.s * st[0]) + group * st[1] + static_cast<int64_t>(first) * st[2];
+  }
+  __device__ __forceinline__ int64_t states(const ScanArgs& a, int64_t row) const { return (row * a.D + d) * a.n + n0; }
+};
+
+// Values of a token and channel that the scan needs.
+struct Inputs {
+  float x, dt, z, dout;
+};
+template <int DT>
+__device__ __forceinline__ Inputs fetch_inputs(const BackArgs& a, bool there, int64_t x, int64_t dt, int64_t z, int64_t o) {
+  Inputs v = {0.f, 0.f, 0.f, 0.f};
+  if (there) {
+    v.x = Elem<DT>::load(a.s.x, x);
+    v.dt = Elem<DT>::load(a.s.dt, dt);
+    if (a.s.z) v.z = Elem<DT>::load(a.s.z, z);
+    v.dout = Elem<DT>::load(a.dout, o);
+  }
+  return v;
+}
+__device__ __forceinline__ float step_of(const ScanArgs& a, float v) { return a.softplus ? softplus(v) : v; }
+
+// ---- the edges of a piece -------------------------------------------------------------------
+// Forward over the piece: the state h it adds, and with P_t = a_1 .. a_t the gradient sum_t P_t C_t dy_t
+// that it passes back.
+template <int DT, int NS, bool FAST>
+__global__ void __launch_bounds__(256) scan_edges(BackArgs b) {
+  __shared__ float4 tile[kTile][64];      // D, u, dy
+  const ScanArgs& a = b.s;
+  Place<NS> w;
+  if (!w.find(a) || w.p.s >= a.q.S || w.last == 0 || w.p.piece > w.last) return;
+  const int nt = w.nt;
+  const int64_t xb = w.tokens(a, a.xs), dtb = w.tokens(a, a.dts), zb = w.tokens(a, a.zs), ob = w.tokens(a, a.os);
+  const int64_t bb = w.groups(a, a.bs) + w.n0, cb = w.groups(a, a.cs) + w.n0;
+  float A2[NS], h[NS], P[NS], e[NS];
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {
+    A2[i] = w.mine && i < w.have ? a.A[static_cast<int64_t>(w.d) * a.n + w.n0 + i] * kLog2e : 0.f;
+    h[i] = e[i] = 0.f;
+    P[i] = 1.f;
+  }
+  const float bias = w.mine && a.bias ? a.bias[w.d] : 0.f;
+  float total = 0.f;
+  Inputs in[kEach];
+  auto fetch = [&](int t0) {
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int t = t0 + w.wave * kEach + k;
+      in[k] = fetch_inputs<DT>(b, w.mine && t < nt, xb + t * a.xs[1], dtb + t * a.dts[1], zb + t * a.zs[1], ob + t * a.os[1]);
+    }
+  };
+  fetch(0);
+  for (int t0 = 0; t0 < nt; t0 += kTile) {
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int t = w.wave * kEach + k;
+      const float s = step_of(a, in[k].dt + bias);
+      tile[t][w.lane] = make_float4(s, s * in[k].x, a.z ? in[k].dout * in[k].z * sigmoidf(in[k].z) : in[k].dout, 0.f);
+    }
+    if (t0 + kTile < nt) fetch(t0 + kTile);
+    __syncthreads();
+    if (w.have > 0) {
+      const int n = min(kTile, nt - t0);
+#pragma unroll 4
+      for (int t = 0; t < n; ++t) {
+        Uniform<DT, NS, FAST> B, C;
+        B.load(a.b, bb + (t0 + t) * a.bs[2], w.have);
+        C.load(a.c, cb + (t0 + t) * a.cs[2], w.have);
+        const float4 v = tile[t][w.lane];
+        total += v.x;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+          const float d = __builtin_amdgcn_exp2f(v.x * A2[i]);
+          h[i] = fmaf(d, h[i], v.y * B.value(i));
+          P[i] *= d;
+          e[i] = fmaf(P[i], C.value(i) * v.z, e[i]);
+        }
+      }
+    }
+    __syncthreads();
+  }
+  if (!w.mine) return;
+#pragma unroll
+  for (int i = 0; i < NS; ++i)
+    if (i < w.have) {
+      a.seg_state[w.states(a, w.piece) + i] = h[i];
+      b.seg_grad[w.states(a, w.piece) + i] = e[i];
+    }
+  if (w.wave == 0) a.seg_step[w.piece * a.D + w.d] = total;
+}
+
+// Along the pieces of sequence blockIdx.y, a thread a state: forward (blockIdx.z = 0), seg_state becomes
+// the state a piece starts from; backward, seg_grad the gradient that reaches the token before a piece.
+__global__ void __launch_bounds__(256) scan_edges_carry(BackArgs b) {
+  const ScanArgs& a = b.s;
+  const int s = blockIdx.y;
+  Span p;
+  seq_span(a.q, s, &p);
+  const int pieces = p.len > 0 ? (p.len - 1) / a.q.len + 1 : 1;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, all = static_cast<int64_t>(a.D) * a.n;
+  if (pieces < 2 || i >= all) return;
+  const int64_t w0 = a.q.T > 0 ? p.row0 / a.q.len + s : static_cast<int64_t>(s) * a.q.n_seg;
+  const float A2 = a.A[i] * kLog2e;
+  const bool back = blockIdx.z;
+  const float* first = back ? b.dstate_out : a.state_in;
+  float h = first ? first[s * all + i] : 0.f;
+  float* to = (back ? b.seg_grad : a.seg_state) + w0 * all + i;
+  const float* step = a.seg_step + w0 * a.D + i / a.n;
+  constexpr int kAhead = 8;
+  for (int g0 = 0; g0 < pieces; g0 += kAhead) {
+    float own[kAhead], total[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const bool there = g0 + k < pieces;
+      const int g = back ? pieces - 1 - (g0 + k) : g0 + k;
+      own[k] = there ? to[g * all] : 0.f;
+      total[k] = there ? step[static_cast<int64_t>(g) * a.D] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int g = back ? pieces - 1 - (g0 + k) : g0 + k;
+      const float before = h;
+      h = fmaf(__builtin_amdgcn_exp2f(total[k] * A2), h, own[k]);
+      if (g0 + k < pieces) to[g * all] = back ? h : before;
+    }
+  }
+}
+
+// ---- a piece --------------------------------------------------------------------------------
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_move(float x) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CTRL, 0xf, 0xf, true));
+}
+// One level within 16 lanes: lanes whose bit is set keep the second of two values, and each pair of lanes
+// exchanges what the other keeps.
+template <int CTRL>
+__device__ __forceinline__ float fold(float a, float b, bool bit) {
+  return (bit ? b : a) + dpp_move<CTRL>(bit ? a : b);
+}
+// Sums of 64 values over the wave's 64 lanes: lane l receives that of v[l].
+__device__ __forceinline__ float sums64(float (&v)[64], int lane) {
+#pragma unroll
+  for (int k = 0; k < 32; ++k) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[k]), __float_as_uint(v[k + 32]), false, false);
+    v[k] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[k]), __float_as_uint(v[k + 16]), false, false);
+    v[k] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = fold<0x128>(v[k], v[k + 8], lane & 8);      // lane ^ 8
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = fold<0x141>(v[k], v[k + 4], lane & 4);      // lane ^ 7
+#pragma unroll
+  for (int k = 0; k < 2; ++k) v[k] = fold<0x4E>(v[k], v[k + 2], lane & 2);       // lane ^ 2
+  return fold<0xB1>(v[0], v[1], lane & 1);                                       // lane ^ 1
+}
+
+template <int DT, int NS, bool FAST>
+__global__ void __launch_bounds__(256) scan_main(BackArgs b) {
+  constexpr int TT = tile_of(NS);
+  constexpr int EACH = TT >= 4 ? TT / 4 : 1;
+  __shared__ float4 tile[TT][64];                  // D, u, dy
+  __shared__ float parts[3][4][TT][64];            // du, the sum of g p A, y: of a wave's states
+  __shared__ float starts[kTiles - 1][4][NS][64];  // the state at the start of tiles 1 and on
+  const ScanArgs& a = b.s;
+  Place<NS> w;
+  const bool found = w.find(a);
+  if (w.piece >= seq_pieces(a.q)) return;          // (the grid's last row may have more blocks than pieces)
+  const int nt = found ? max(w.nt, 0) : 0;
+  const int64_t sb = static_cast<int64_t>(w.p.s) * a.D * a.n + static_cast<int64_t>(w.d) * a.n + w.n0;
+  const bool real = found && w.p.s < a.q.S;
+  float A2[NS], h[NS], e[NS], dA[NS];
+#pragma unroll
+  for (int i = 0; i < NS; ++i) A2[i] = h[i] = e[i] = dA[i] = 0.f;
+  float dskip = 0.f, dbias = 0.f;
+  const bool ends = real && w.p.piece == w.last;   // the sequence's last piece, if it is empty too
+  if (w.mine && real && w.p.piece <= w.last) {
+    const float* from = w.p.piece > 0 ? a.seg_state + w.states(a, w.piece) : a.state_in ? a.state_in + sb : nullptr;
+    const float* grad = !ends ? b.seg_grad + w.states(a, w.piece + 1) : b.dstate_out ? b.dstate_out + sb : nullptr;
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+      if (i < w.have) {
+        A2[i] = a.A[static_cast<int64_t>(w.d) * a.n + w.n0 + i] * kLog2e;
+        if (from) h[i] = from[i];
+        if (grad) e[i] = grad[i];
+      }
+  }
+  if (nt > 0) {
+    const float skip = w.mine && a.skip ? a.skip[w.d] : 0.f, bias = w.mine && a.bias ? a.bias[w.d] : 0.f;
+    const int64_t xb = w.tokens(a, a.xs), dtb = w.tokens(a, a.dts), zb = w.tokens(a, a.zs), ob = w.tokens(a, a.os);
+    const int64_t bb = w.groups(a, a.bs) + w.n0, cb = w.groups(a, a.cs) + w.n0;
+    const int64_t dxb = w.tokens(a, b.dxs), ddtb = w.tokens(a, b.ddts), dzb = w.tokens(a, b.dzs);
+    const int64_t row = (a.q.T > 0 ? uniform64(w.p.row0) : static_cast<int64_t>(w.p.s) * a.q.N) + w.first;
+    const int tiles = (nt + TT - 1) / TT;
+    const bool stages = TT >= 4 || w.wave < TT;    // this wave prepares tokens wave * EACH and on of a tile
+    Inputs in[EACH];
+    auto fetch = [&](int t0) {
+#pragma unroll
+      for (int k = 0; k < EACH; ++k) {
+        const int t = t0 + w.wave * EACH + k;
+        in[k] = fetch_inputs<DT>(b, stages && w.mine && t < nt, xb + t * a.xs[1], dtb + t * a.dts[1], zb + t * a.zs[1], ob + t * a.os[1]);
+      }
+    };
+    // ---- forward: the states at the tiles' starts
+    fetch(0);
+    for (int q = 0; q < tiles - 1; ++q) {
+      if (stages) {
+#pragma unroll
+        for (int k = 0; k < EACH; ++k) {
+          const float s = step_of(a, in[k].dt + bias);
+          tile[w.wave * EACH + k][w.lane] = make_float4(s, s * in[k].x, 0.f, 0.f);
+        }
+      }
+      fetch((q + 1) * TT);
+      __syncthreads();
+      if (w.have > 0) {
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          Uniform<DT, NS, FAST> B;
+          B.load(a.b, bb + (q * TT + t) * a.bs[2], w.have);
+          const float4 v = tile[t][w.lane];
+#pragma unroll
+          for (int i = 0; i < NS; ++i) h[i] = fmaf(__builtin_amdgcn_exp2f(v.x * A2[i]), h[i], v.y * B.value(i));
+        }
+#pragma unroll
+        for (int i = 0; i < NS; ++i) starts[q][w.wave][i][w.lane] = h[i];
+      }
+      __syncthreads();
+    }
+    // ---- backward, tile by tile
+    for (int q = tiles - 1; q >= 0; --q) {
+      const int t0 = q * TT;
+      float s[EACH], sg[EACH];
+      Inputs v[EACH];
+#pragma unroll
+      for (int k = 0; k < EACH; ++k) {
+        const int t = w.wave * EACH + k;
+        v[k] = in[k];
+        s[k] = t0 + t < nt ? step_of(a, in[k].dt + bias) : 0.f;
+        sg[k] = a.z ? sigmoidf(in[k].z) : 0.f;
+        if (stages) tile[t][w.lane] = make_float4(s[k], s[k] * in[k].x, a.z ? in[k].dout * in[k].z * sg[k] : in[k].dout, 0.f);
+      }
+      if (q > 0) fetch(t0 - TT);
+      __syncthreads();
+      if (w.have > 0) {
+        if (q > 0) {
+#pragma unroll
+          for (int i = 0; i < NS; ++i) h[i] = starts[q - 1][w.wave][i][w.lane];
+        } else {
+#pragma unroll
+          for (int i = 0; i < NS; ++i) h[i] = 0.f;
+          const float* from = w.p.piece > 0 ? a.seg_state + w.states(a, w.piece) : a.state_in ? a.state_in + sb : nullptr;
+          if (w.mine && from) {
+#pragma unroll
+            for (int i = 0; i < NS; ++i)
+              if (i < w.have) h[i] = from[i];
+          }
+        }
+        float dec[TT][NS], p[TT][NS], sums[64];
+        Uniform<DT, NS, FAST> B[TT], C[TT];
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          const int have = t0 + t < nt ? w.have : 0;       // tokens behind the last one have zeros
+          B[t].load_or_zero(a.b, bb + (t0 + t) * a.bs[2], have);
+          C[t].load_or_zero(a.c, cb + (t0 + t) * a.cs[2], have);
+          const float4 u = tile[t][w.lane];
+          float y = 0.f;
+#pragma unroll
+          for (int i = 0; i < NS; ++i) {
+            dec[t][i] = __builtin_amdgcn_exp2f(u.x * A2[i]);
+            p[t][i] = dec[t][i] * h[i];
+            h[i] = fmaf(u.y, B[t].value(i), p[t][i]);
+            y = fmaf(C[t].value(i), h[i], y);
+            sums[32 + t * NS + i] = u.z * h[i];
+          }
+          parts[2][w.wave][t][w.lane] = y;
+        }
+#pragma unroll
+        for (int t = TT - 1; t >= 0; --t) {
+          const float4 u = tile[t][w.lane];
+          float du = 0.f, ws = 0.f;
+#pragma unroll
+          for (int i = 0; i < NS; ++i) {
+            const float g = fmaf(C[t].value(i), u.z, e[i]);
+            sums[t * NS + i] = g * u.y;
+            du = fmaf(g, B[t].value(i), du);
+            const float wp = g * p[t][i];
+            ws = fmaf(wp, A2[i], ws);
+            dA[i] = fmaf(wp, u.x, dA[i]);
+            e[i] = dec[t][i] * g;
+          }
+          parts[0][w.wave][t][w.lane] = du;
+          parts[1][w.wave][t][w.lane] = ws;
+        }
+        const float total = sums64(sums, w.lane);
+        const int r = w.lane & 31, t = r / NS, i = r % NS;
+        if (t0 + t < nt && i < w.have)
+          b.part_bc[((row + t0 + t) * (static_cast<int64_t>(a.tiles) * a.G) + w.x) * 2 * a.n + (w.lane >> 5) * a.n + w.n0 + i] = total;
+      }
+      __syncthreads();
+      if (stages && w.mine) {
+#pragma unroll
+        for (int k = 0; k < EACH; ++k) {
+          const int t = w.wave * EACH + k;
+          if (t0 + t < nt) {
+            float du = 0.f, ws = 0.f, y = skip * v[k].x;
+            for (int i = 0; i < w.waves; ++i) {
+              du += parts[0][i][t][w.lane];
+              ws += parts[1][i][t][w.lane];
+              y += parts[2][i][t][w.lane];
+            }
+            float dy = v[k].dout;
+            if (a.z) {
+              Elem<DT>::store(b.dz, dzb + (t0 + t) * b.dzs[1], dy * y * sg[k] * fmaf(v[k].z, 1.0f - sg[k], 1.0f));
+              dy *= v[k].z * sg[k];
+            }
+            float ddt = fmaf(du, v[k].x, ws * 0.69314718f);
+            if (a.softplus) ddt *= sigmoidf(v[k].dt + bias);
+            Elem<DT>::store(b.dx, dxb + (t0 + t) * b.dxs[1], fmaf(du, s[k], skip * dy));
+            Elem<DT>::store(b.ddt, ddtb + (t0 + t) * b.ddts[1], ddt);
+            dskip = fmaf(dy, v[k].x, dskip);
+            dbias += ddt;
+          }
+        }
+      }
+    }
+  }
+  if (w.mine) {
+    // the piece's own sums (zeros of a piece without tokens), where its starting state was
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+      if (i < w.have) {
+        a.seg_state[w.states(a, w.piece) + i] = dA[i];
+        if (real && w.p.piece == 0 && b.dstate_in) b.dstate_in[sb + i] = e[i];
+      }
+  }
+  __syncthreads();
+  parts[0][w.wave][0][w.lane] = dskip;
+  parts[1][w.wave][0][w.lane] = dbias;
+  __syncthreads();
+  if (w.wave == 0 && w.mine) {
+    dskip = dbias = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      dskip += parts[0][i][0][w.lane];
+      dbias += parts[1][i][0][w.lane];
+    }
+    b.part_skip[w.piece * a.D + w.d] = dskip;
+    b.part_bias[w.piece * a.D + w.d] = dbias;
+  }
+  if (a.zero_rest && found && w.mine) {
+    const int64_t rows = min(w.p.own - w.first, static_cast<int64_t>(a.q.len));
+    const int64_t dxb = w.tokens(a, b.dxs), ddtb = w.tokens(a, b.ddts), dzb = w.tokens(a, b.dzs);
+    for (int64_t t = nt + w.wave; t < rows; t += 4) {
+      Elem<DT>::store(b.dx, dxb + t * b.dxs[1], 0.f);
+      Elem<DT>::store(b.ddt, ddtb + t * b.ddts[1], 0.f);
+      if (a.z) Elem<DT>::store(b.dz, dzb + t * b.dzs[1], 0.f);
+    }
+  }
+}
+
+// ---- sums over blocks -----------------------------------------------------------------------
+
+// dB and dC of a piece's tokens: the blocks along the channels of a group, in their order.
+template <int DT>
+__global__ void __launch_bounds__(256) scan_sum_tokens(BackArgs b) {
+  const ScanArgs& a = b.s;
+  Span p;
+  if (!seq_place(a.q, blockIdx.y + static_cast<int64_t>(blockIdx.z) * gridDim.y, &p)) return;
+  const int64_t first = static_cast<int64_t>(p.piece) * a.q.len;
+  const int64_t rows = min(p.own - first, static_cast<int64_t>(a.q.len));
+  const int per = 2 * a.n * a.G;
+  const int64_t row = (a.q.T > 0 ? p.row0 : static_cast<int64_t>(p.s) * a.q.N) + first;
+  const int64_t bb = (a.q.T > 0 ? p.row0 * b.dbs[2] : p.s * b.dbs[0]) + first * b.dbs[2];
+  const int64_t cb = (a.q.T > 0 ? p.row0 * b.dcs[2] : p.s * b.dcs[0]) + first * b.dcs[2];
+  for (int64_t i = threadIdx.x; i < rows * per; i += 256) {
+    const int64_t t = i / per;
+    const int k = static_cast<int>(i - t * per), g = k / (2 * a.n), c = k - g * 2 * a.n;
+    float s = 0.f;
+    if (first + t < p.len) {
+      const float* from = b.part_bc + ((row + t) * a.G + g) * a.tiles * 2 * a.n + c;
+#pragma unroll 4
+      for (int x = 0; x < a.tiles; ++x) s += from[static_cast<int64_t>(x) * 2 * a.n];
+    } else if (!a.zero_rest) {
+      continue;
+    }
+    if (c < a.n) Elem<DT>::store(b.db, bb + t * b.dbs[2] + g * b.dbs[1] + c, s);
+    else Elem<DT>::store(b.dc, cb + t * b.dcs[2] + g * b.dcs[1] + c - a.n, s);
+  }
+}
+
+// dA, dskip and dbias: the pieces' sums in 32 interleaved ones a column, which are then added in turn.
+__global__ void __launch_bounds__(1024) scan_sum_pieces(BackArgs b, int64_t pieces) {
+  __shared__ float red[32][33];
+  const ScanArgs& a = b.s;
+  const int64_t all = static_cast<int64_t>(a.D) * a.n;
+  int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + (threadIdx.x & 31);
+  const float* from = nullptr;
+  float* to = nullptr;
+  int64_t step = a.D;
+  if (col < all) { from = a.seg_state; to = b.dA; step = all; }
+  else if ((col -= all) < a.D) { from = b.part_skip; to = b.dskip; }
+  else if ((col -= a.D) < a.D) { from = b.part_bias; to = b.dbias; }
+  const int grp = threadIdx.x >> 5;
+  float s = 0.f;
+  if (to) {
+#pragma unroll 4
+    for (int64_t i = grp; i < pieces; i += 32) s += from[i * step + col];
+  }
+  red[grp][threadIdx.x & 31] = s;
+  __syncthreads();
+  if (grp == 0 && to) {
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s += red[i][threadIdx.x];
+    to[col] = s;
+  }
+}
+
+template <int DT, int NS, bool FAST>
+hipError_t launch_back(const BackArgs& b, hipStream_t st) {
+  const ScanArgs& a = b.s;
+  const int64_t x = static_cast<int64_t>(a.tiles) * a.G, all = static_cast<int64_t>(a.D) * a.n;
+  const dim3 grid = seq_grid(a.q, x);
+  hipError_t e;
+  if (a.q.N > a.q.len) {
+    hipLaunchKernelGGL((scan_edges<DT, NS, FAST>), grid, dim3(256), 0, st, b);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    hipLaunchKernelGGL(scan_edges_carry, dim3(static_cast<unsigned>((all + 255) / 256), a.q.S, 2), dim3(256), 0, st, b);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((scan_main<DT, NS, FAST>), grid, dim3(256), 0, st, b);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  hipLaunchKernelGGL((scan_sum_tokens<DT>), seq_grid(a.q, 1), dim3(256), 0, st, b);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  hipLaunchKernelGGL(scan_sum_pieces, dim3(static_cast<unsigned>((all + 2 * a.D + 31) / 32)), dim3(1024), 0, st, b, seq_pieces(a.q));
+  return hipGetLastError();
+}
+template <int DT, bool FAST>
+hipError_t launch_n(const BackArgs& b, hipStream_t st) {
+  switch (scan_states(b.s.n)) {
+    case 2: return launch_back<DT, 2, FAST>(b, st);
+    case 4: return launch_back<DT, 4, FAST>(b, st);
+    case 8: return launch_back<DT, 8, FAST>(b, st);
+    default: return launch_back<DT, 16, FAST>(b, st);
+  }
+}
+
+// Floats of each part of the workspace.
+struct Parts {
+  size_t state, step, bc;
+  explicit Parts(const ScanArgs& a) {
+    const size_t rows = static_cast<size_t>(seq_pieces(a.q));
+    const size_t tokens = a.q.T > 0 ? static_cast<size_t>(a.q.T) : static_cast<size_t>(a.q.S) * a.q.N;
+    state = rows * a.D * a.n;
+    step = rows * a.D;
+    bc = tokens * a.tiles * a.G * 2 * a.n;
+  }
+  size_t all() const { return 2 * state + 3 * step + bc; }
+};
+ScanArgs pieces_of(const ScanCall& c) { return scan_args(c, kTiles * tile_of(scan_states(c.n))); }
+
+}  // namespace
+
+size_t scan_backward_ws_bytes(const ScanCall& c) { return Parts(pieces_of(c)).all() * sizeof(float); }
+
+hipError_t launch_selective_backward(const ScanCall& c, const ScanGrads& g, hipStream_t st) {
+  BackArgs b;
+  b.s = pieces_of(c);
+  for (int i = 0; i < 2; ++i) { b.dxs[i] = g.dxs[i]; b.ddts[i] = g.ddts[i]; b.dzs[i] = g.dzs[i]; }
+  for (int i = 0; i < 3; ++i) { b.dbs[i] = g.dbs[i]; b.dcs[i] = g.dcs[i]; }
+  b.dout = g.dout; b.dstate_out = g.dstate_out; b.dx = g.dx; b.ddt = g.ddt; b.dz = g.dz; b.db = g.db; b.dc = g.dc;
+  b.dA = g.dA; b.dskip = g.dskip; b.dbias = g.dbias; b.dstate_in = g.dstate_in;
+  const Parts parts(b.s);
+  float* ws = static_cast<float*>(c.ws);
+  b.s.seg_state = ws;
+  b.seg_grad = ws + parts.state;
+  b.s.seg_step = b.seg_grad + parts.state;
+  b.part_skip = b.s.seg_step + parts.step;
+  b.part_bias = b.part_skip + parts.step;
+  b.part_bc = b.part_bias + parts.step;
+  const bool fast = scan_fast(b.s, c.type);
+  if (c.type == RN_F32) return fast ? launch_n<RN_F32, true>(b, st) : launch_n<RN_F32, false>(b, st);
+  return fast ? launch_n<RN_BF16, true>(b, st) : launch_n<RN_BF16, false>(b, st);
+}
+
+}  // namespace rn

@@ -18,7 +18,7 @@ struct Seqs {
 // Pieces of all sequences. Packed, sequence s starting at row r has the pieces from r / len + s on up to
 // the next one's first: at least as many as its rows need, and one if it has none. Sequence S stands
 // for the rows behind the last one.
-inline int64_t seq_pieces(const Seqs& q) {
+__host__ __device__ inline int64_t seq_pieces(const Seqs& q) {
   return q.T > 0 ? q.T / q.len + q.S + 1 : static_cast<int64_t>(q.S) * q.n_seg;
 }
 inline void seq_cut(Seqs* q, int len) {

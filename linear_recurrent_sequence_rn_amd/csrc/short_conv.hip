@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(256) conv_backward(ConvArgs a) {
     for (int j = 0; j < K; ++j) w[v][j] = dw[j][v] = 0.f;
   }
   if (mine) conv_weights<K, V, FIT>(a, c, w, b);
-  const int64_t pieces = a.q.T > 0 ? a.q.T / a.q.len + a.q.S + 1 : static_cast<int64_t>(a.q.S) * a.q.n_seg;
+  const int64_t pieces = seq_pieces(a.q);
   for (int64_t piece = blockIdx.y; piece < pieces; piece += gridDim.y) {
     Span p;
     if (!seq_place(a.q, piece, &p) || !mine) continue;

@@ -35,10 +35,17 @@ class RnScanDesc(ctypes.Structure):
                 ("z_stride", _i64 * 2), ("out_stride", _i64 * 2), ("b_stride", _i64 * 3), ("c_stride", _i64 * 3)]
 
 
+class RnScanGradDesc(ctypes.Structure):
+    _fields_ = [("dx_stride", _i64 * 2), ("ddt_stride", _i64 * 2), ("dz_stride", _i64 * 2), ("db_stride", _i64 * 3),
+                ("dc_stride", _i64 * 3)]
+
+
 _pack_conv = struct.Struct("@iiiiiIqi6q").pack
 _pack_scan = struct.Struct("@iiiiiiIiq14q").pack
+_pack_grads = struct.Struct("@12q").pack
 assert struct.calcsize("@iiiiiIqi6q") == ctypes.sizeof(RnConvDesc)
 assert struct.calcsize("@iiiiiiIiq14q") == ctypes.sizeof(RnScanDesc)
+assert struct.calcsize("@12q") == ctypes.sizeof(RnScanGradDesc)
 
 
 def _bind(L):
@@ -49,7 +56,9 @@ def _bind(L):
             ("rn_short_conv_backward", [_vp] * 14 + [_sz, _vp], _i32),
             ("rn_selective_scan_workspace_bytes", [_vp], _sz),
             ("rn_selective_scan_chunked", [_vp] * 16 + [_sz, _vp], _i32),
-            ("rn_selective_scan_step", [_vp] * 13, _i32)):
+            ("rn_selective_scan_step", [_vp] * 13, _i32),
+            ("rn_selective_scan_backward_workspace_bytes", [_vp], _sz),
+            ("rn_selective_scan_backward", [_vp] * 25 + [_sz, _vp], _i32)):
         f = getattr(L, name)
         f.argtypes, f.restype = args, res
 
@@ -327,3 +336,65 @@ def rn_selective_scan_step(x, dt, A, B, C, state, D=None, *, dt_bias=None, softp
     _call(dev, lib.rn_selective_scan_step, desc, _p(slots), x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(),
           C.data_ptr(), _p(D), _p(dt_bias), _p(z), state.data_ptr(), out.data_ptr())
     return out
+
+
+def rn_selective_scan_backward_workspace_bytes(x, A, B, *, cu_seqlens=None, max_len=None) -> int:
+    """Bytes of workspace ``rn_selective_scan_backward`` needs for these tensors."""
+    S, N, T = _batch(x, None, cu_seqlens, max_len)
+    return int(lib.rn_selective_scan_backward_workspace_bytes(
+        _scan_desc(S, N, T, x, A.shape[1], B.shape[1], 0, 0, (0,) * 6, (0, 0), (0,) * 6)))
+
+
+def rn_selective_scan_backward(dout, x, dt, A, B, C, D=None, *, dt_bias=None, softplus=True, z=None, lengths=None,
+                               cu_seqlens=None, max_len=None, state_in=None, dstate_out=None, want_dstate_in=False,
+                               dx=None, ddt=None, dB=None, dC=None, dz=None, workspace=None):
+    """Gradients of ``rn_selective_scan_chunked`` (same arguments; states per sequence, without slots) given
+    those of its output and, optionally, of its final state (``dstate_out``, float32 [S, D, n]). Returns a
+    dict with dx, ddt, dB, dC (x's type; new, or those given, whose rows of no sequence are not written),
+    dA (float32) and, where there is a z, D or dt_bias, dz (x's type), dD and ddt_bias (float32); with
+    ``want_dstate_in`` dstate_in (float32 [S, D, n])."""
+    dev = _device(x, dout, dt, A, B, C, D, dt_bias, z, lengths, cu_seqlens, state_in, dstate_out, dx, ddt, dB, dC, dz,
+                  workspace)
+    S, N, T = _batch(x, lengths, cu_seqlens, max_len)
+    _same(dout, x, "dout")
+    n, G, tokens, groups = _scan_tensors(x, dt, A, B, C, D, dt_bias, z)
+    row = (x.shape[2], n)
+    _states(state_in, None, None, S, row, torch.float32, x)
+    _grad_state(dstate_out, S, row, "dstate_out")
+    if dz is not None and z is None:
+        raise ValueError("dz without z")
+    got, new = {}, []
+    for name, t, like in (("dx", dx, x), ("ddt", ddt, x), ("dB", dB, B), ("dC", dC, C), ("dz", dz, z)):
+        if like is None:
+            continue
+        if t is None:
+            t = torch.empty(like.shape, dtype=x.dtype, device=x.device)
+            new.append(t)
+        else:
+            _same(t, like, name)
+        got[name] = t
+    given = len(got) - len(new)
+    rest = _rest(new, x.shape[1], N, T, lengths)
+    if rest and given:                  # the call's zeros would reach the given ones too
+        for t in new:
+            t.zero_()
+        rest = 0
+    flags = rest | (RN_SCAN_SOFTPLUS if softplus else 0)
+    got["dA"] = torch.empty_like(A)
+    if D is not None:
+        got["dD"] = torch.empty_like(D)
+    if dt_bias is not None:
+        got["ddt_bias"] = torch.empty_like(dt_bias)
+    if want_dstate_in:
+        got["dstate_in"] = torch.empty((S, *row), dtype=torch.float32, device=x.device)
+    desc = _scan_desc(S, N, T, x, n, G, flags, 0, tokens, _tokens(dout, "dout"), groups)
+    grads = _pack_grads(*_tokens(got["dx"], "dx"), *_tokens(got["ddt"], "ddt"),
+                        *((0, 0) if z is None else _tokens(got["dz"], "dz")), *_groups(got["dB"], x, n, "dB"),
+                        *_groups(got["dC"], x, n, "dC"))
+    workspace = _get_workspace(workspace, lib.rn_selective_scan_backward_workspace_bytes(desc), x)
+    _call(dev, lib.rn_selective_scan_backward, desc, grads, _p(cu_seqlens), _p(lengths), dout.data_ptr(), x.data_ptr(),
+          dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _p(D), _p(dt_bias), _p(z), _p(state_in), _p(dstate_out),
+          got["dx"].data_ptr(), got["ddt"].data_ptr(), got["dA"].data_ptr(), got["dB"].data_ptr(), got["dC"].data_ptr(),
+          _p(got.get("dD")), _p(got.get("ddt_bias")), _p(got.get("dz")), _p(got.get("dstate_in")), _p(workspace),
+          0 if workspace is None else workspace.numel())
+    return got

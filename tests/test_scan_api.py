@@ -169,6 +169,41 @@ def test_scan_calls():
     assert need > 0 and run_scan(long, n=need - 1) == WS and run_scan(long, ws=None) == WS and run_scan(long, ws=FAKE + 16) == INV
 
 
+def grads(**kw):
+    s, h = (6400, 64), (1600, 1600, 16)
+    return fill(rn.RnScanGradDesc, dict(dx_stride=s, ddt_stride=s, dz_stride=s, db_stride=h, dc_stride=h), kw)
+
+
+Q = [FAKE * i for i in range(200, 212)]
+
+
+def scan_back(d, g=grads(), cu=None, lens=None, dout=P[5], x=P[0], z=None, s0=None, ds1=None, dx=Q[0], ddt=Q[1], dA=Q[2], dB=Q[3],
+              dC=Q[4], dskip=None, dbias=None, dz=None, ds0=None, ws=FAKE, n=1 << 40):
+    return L.rn_selective_scan_backward(ref(d), ref(g) if g else None, cu, lens, dout, x, P[1], P[2], P[3], P[4], None, None, z, s0,
+                                        ds1, dx, ddt, dA, dB, dC, dskip, dbias, dz, ds0, ws, n, None)
+
+
+@pytest.mark.parametrize("kw,code", SCAN)
+def test_scan_backward_descriptors(kw, code):
+    assert scan_back(scan(**kw)) == code
+    assert L.rn_selective_scan_backward_workspace_bytes(ref(scan(**kw))) == 0
+
+
+def test_scan_backward_calls():
+    d = scan()
+    for kw in (dict(g=None), dict(cu=FAKE), dict(lens=FAKE + 1), dict(dout=None), dict(x=None), dict(dx=None), dict(ddt=None),
+               dict(dA=None), dict(dB=None), dict(dC=None), dict(z=P[6]), dict(dz=Q[5]), dict(dx=Q[0] + 1), dict(dB=Q[3] + 1),
+               dict(dA=Q[2] + 2), dict(dskip=FAKE + 2), dict(dbias=FAKE + 1), dict(s0=FAKE + 8), dict(ds1=FAKE + 4),
+               dict(ds0=FAKE + 8), dict(ds0=FAKE, ds1=FAKE), dict(ds0=FAKE, s0=FAKE), dict(dx=P[0]), dict(ddt=P[1]), dict(dx=P[5]),
+               dict(dB=P[3]), dict(dC=P[4]), dict(dx=Q[1]), dict(dC=Q[3]), dict(dC=Q[3] + 16), dict(dx=P[0] + 256),
+               dict(z=P[6], dz=P[6]), dict(g=grads(dx_stride=(6400, 63))), dict(g=grads(ddt_stride=(-1, 64))),
+               dict(g=grads(db_stride=(0, 0, 16))), dict(g=grads(dc_stride=(1600, 1600, 15))), dict(g=grads(dz_stride=(0, 0)), z=P[6], dz=Q[5])):
+        assert scan_back(d, **kw) == INV, kw
+    need = L.rn_selective_scan_backward_workspace_bytes(ref(d))
+    assert need > 0 and scan_back(d, n=need - 1) == WS and scan_back(d, ws=None) == WS and scan_back(d, ws=FAKE + 16) == INV
+    assert L.rn_selective_scan_backward_workspace_bytes(None) == 0
+
+
 def test_workspace_sizes_pass_32_bits():
     d = scan(S=2048, N=1 << 20, D=64, x_stride=(1 << 40, 64), out_stride=(1 << 40, 64))
     d.S = 1
@@ -184,6 +219,7 @@ def test_binding_refuses_cpu_tensors():
     for f in (lambda: rn.rn_rmsnorm(x), lambda: rn.rn_rmsnorm_backward(x, x), lambda: rn.rn_short_conv(x, w),
               lambda: rn.rn_short_conv_step(x[:, :1], w, None, torch.zeros(2, 3, 64)), lambda: rn.rn_short_conv_backward(x, x, w),
               lambda: rn.rn_selective_scan_chunked(x, x, w, x[:, None, :, :4], x[:, None, :, :4]),
+              lambda: rn.rn_selective_scan_backward(x, x, x, w, x[:, None, :, :4], x[:, None, :, :4]),
               lambda: rn.rn_selective_scan_step(x[:, :1], x[:, :1], w, x[:, None, :1, :4], x[:, None, :1, :4], torch.zeros(2, 64, 4))):
         with pytest.raises(ValueError):
             f()
