@@ -2,11 +2,8 @@
 //     D_t = softplus(dt_t + bias),  h_t = exp(D_t A) h_{t-1} + D_t x_t B_t,
 //     y_t = C_t h_t + skip x_t,     out_t = y_t z_t sigmoid(z_t)
 // for every channel, with n states each; channels of a group share B and C.
-//
-// A block takes 64 channels of one group (a lane each) and a segment of a sequence; its four waves share
-// the n states, NS each, in registers. What belongs to a channel and a token (the softplus, the gate)
-// is worked out once, for a tile of kTile tokens at a time, and reaches the waves through LDS; B and C
-// are the same for all lanes and come through scalar registers.
+// Lanes are channels, so that B and C are the same for all lanes of a wave and come through scalar
+// registers.
 #pragma once
 #include <type_traits>
 
@@ -15,15 +12,14 @@
 
 namespace rn {
 
-constexpr int kTile = 16;                // tokens a tile: each wave prepares four
-constexpr int kEach = kTile / 4;
-constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kLog2e = 1.44269502f, kLog2eLow = 1.92596299e-8f;   // log2(e) in two parts
 
 struct ScanArgs {
   Seqs q;
   int32_t D, n, G, n_slots;
   int32_t tiles;                          // blocks along the channels of a group
   bool softplus, zero_rest;
+  bool a4;                                // A's rows are whole fours on 16 bytes (states' always are, if whole)
   int64_t xs[2], dts[2], zs[2], os[2];    // sequence and token strides
   int64_t bs[3], cs[3];                   // sequence, group and token strides
   const int32_t* slots;
@@ -42,25 +38,18 @@ struct ScanArgs {
   float* seg_step;                        // [pieces][D]: the sum of a segment's D_t
 };
 
-// softplus(v) to float32 accuracy at any v: max(v, 0) + log1p(e), e = exp(-|v|), with
-// log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3, by the series of atanh (its first dropped term is
-// 2 s^14 / 15 < 3e-8 of s).
+// x log2(e), rounded once (the constant in two parts).
+__device__ __forceinline__ float in_log2(float x) { return fmaf(x, kLog2eLow, x * kLog2e); }
+// softplus(v) to float32 accuracy at any v: max(v, 0) + log1p(e), e = exp(-|v|). What rounding the exponent
+// loses goes back into e (it is |v| 2^-24 of it), and with w = 1 + e, what rounding w loses into the
+// logarithm: log1p(e) = log(w) + (e - (w - 1)) / w, of which 1 / w is left out (the term is at most 2^-24 in
+// all, and where w is not near 1 the result is not small). The hardware's logarithm is relative near 1.
 __device__ __forceinline__ float softplus(float v) {
   const float m = -fabsf(v), t = m * kLog2e;
-  // (what rounding the exponent loses: |v| 2^-24 of e)
   float e = __builtin_amdgcn_exp2f(t);
-  e = fmaf(e, fmaf(m, kLog2e, -t) * 0.6931472f, e);
-  const float d = 2.0f + e;
-  float r = __builtin_amdgcn_rcpf(d);
-  r = fmaf(fmaf(-d, r, 1.0f), r, r);
-  const float s = e * r, q = s * s;
-  float p = fmaf(q, 2.0f / 13.0f, 2.0f / 11.0f);
-  p = fmaf(p, q, 2.0f / 9.0f);
-  p = fmaf(p, q, 2.0f / 7.0f);
-  p = fmaf(p, q, 2.0f / 5.0f);
-  p = fmaf(p, q, 2.0f / 3.0f);
-  p = fmaf(p, q, 2.0f);
-  return fmaxf(v, 0.0f) + s * p;
+  e = fmaf(e, fmaf(m, kLog2eLow, fmaf(m, kLog2e, -t)) * 0.6931472f, e);
+  const float w = 1.0f + e;
+  return fmaxf(v, 0.0f) + fmaf(__builtin_amdgcn_logf(w), 0.6931472f, e - (w - 1.0f));
 }
 __device__ __forceinline__ float sigmoidf(float v) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v * kLog2e));
@@ -73,26 +62,41 @@ __device__ __forceinline__ int64_t uniform64(int64_t x) {
   return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
 }
 
-// NS values of B or C, the same for the whole wave, from element i (also the same) of p. FAST: through
-// the scalar cache; all NS are there, bf16 in pairs that start on 4 bytes. Else every lane loads the
-// first `have` of them, the rest being zeros.
-template <int DT, int NS, bool FAST>
-struct Uniform;
-template <int DT, int NS>
-struct Uniform<DT, NS, true> {
+// How B and C reach the waves, for all lanes of which they are the same: through the scalar cache, in whole
+// sets of states (bf16: in pairs that start on 4 bytes), or in sets of which the last one is short; or
+// by loads of every lane.
+enum Reach : int { kScalar = 0, kScalarSome = 1, kVector = 2 };
+
+// NS values of B or C from element i of p (both the same for the whole wave), of which the first `have` are
+// there; the rest are zeros.
+template <int DT, int NS, Reach HOW>
+struct Uniform {
   static constexpr int kWords = DT == RN_F32 ? NS : NS / 2;
+  static constexpr int kPer = DT == RN_F32 ? 1 : 2;
   uint32_t u[kWords];
-  __device__ __forceinline__ void load(const void* p, int64_t i, int) {
+  __device__ __forceinline__ void load(const void* p, int64_t i, int have) {
     typedef const __attribute__((address_space(4))) uint32_t* words;
-    const words w = (words)static_cast<uint64_t>(uniform64(reinterpret_cast<int64_t>(p) + i * (DT == RN_F32 ? 4 : 2)));
+    const words w = (words)static_cast<uint64_t>(uniform64(reinterpret_cast<int64_t>(p) + i * (4 / kPer)));
+    if constexpr (HOW == kScalar) {
 #pragma unroll
-    for (int k = 0; k < kWords; ++k) u[k] = w[k];
+      for (int k = 0; k < kWords; ++k) u[k] = w[k];
+    } else {
+      // quarters of four: those that are not there read the last one that is, and count nothing
+      constexpr int kFour = 4 / kPer;
+      const int there = have < NS ? have : NS;
+#pragma unroll
+      for (int k = 0; k < kWords; ++k) {
+        const int q = k / kFour;
+        const uint32_t v = w[(q * 4 < there ? q : there / 4 - 1) * kFour + k % kFour];
+        u[k] = q * 4 < there ? v : 0;
+      }
+    }
   }
   // the same, or zeros (and nothing read) where `have` is 0
   __device__ __forceinline__ void load_or_zero(const void* p, int64_t i, int have) {
 #pragma unroll
     for (int k = 0; k < kWords; ++k) u[k] = 0;
-    if (have) load(p, i, have);
+    if (have > 0) load(p, i, have);
   }
   __device__ __forceinline__ float value(int k) const {
     if constexpr (DT == RN_F32) return __uint_as_float(u[k]);
@@ -100,7 +104,7 @@ struct Uniform<DT, NS, true> {
   }
 };
 template <int DT, int NS>
-struct Uniform<DT, NS, false> {
+struct Uniform<DT, NS, kVector> {
   float f[NS];
   __device__ __forceinline__ void load(const void* p, int64_t i, int have) {
 #pragma unroll
@@ -109,6 +113,18 @@ struct Uniform<DT, NS, false> {
   __device__ __forceinline__ void load_or_zero(const void* p, int64_t i, int have) { load(p, i, have); }
   __device__ __forceinline__ float value(int k) const { return f[k]; }
 };
+
+// `whole`: every set is of NS states.
+inline Reach scan_reach(const ScanArgs& a, int dt, bool whole) {
+  if (!whole && a.n % 4) return kVector;
+  if (dt == RN_BF16) {
+    if (a.n % 2) return kVector;
+    for (int i = 0; i < 3; ++i)
+      if (a.bs[i] % 2 || a.cs[i] % 2) return kVector;
+    if (reinterpret_cast<uintptr_t>(a.b) % 4 || reinterpret_cast<uintptr_t>(a.c) % 4) return kVector;
+  }
+  return whole ? kScalar : kScalarSome;
+}
 
 // The call's kernel arguments, with `len` tokens a piece.
 inline ScanArgs scan_args(const ScanCall& c, int len) {
@@ -119,21 +135,10 @@ inline ScanArgs scan_args(const ScanCall& c, int len) {
   a.softplus = c.softplus; a.zero_rest = c.zero_rest;
   for (int i = 0; i < 2; ++i) { a.xs[i] = c.xs[i]; a.dts[i] = c.dts[i]; a.zs[i] = c.zs[i]; a.os[i] = c.os[i]; }
   for (int i = 0; i < 3; ++i) { a.bs[i] = c.bs[i]; a.cs[i] = c.cs[i]; }
+  a.a4 = c.n % 4 == 0 && reinterpret_cast<uintptr_t>(c.A) % 16 == 0;
   a.slots = c.slots; a.x = c.x; a.dt = c.dt; a.z = c.z; a.b = c.b; a.c = c.c; a.A = c.A; a.skip = c.skip; a.bias = c.bias;
   a.state_in = c.state_in; a.state_out = c.state_out; a.out = c.out; a.seg_state = nullptr; a.seg_step = nullptr;
   return a;
-}
-
-// States a wave holds: a quarter of them, at least two.
-inline int scan_states(int n) { return n <= 8 ? 2 : n <= 16 ? 4 : n <= 32 ? 8 : 16; }
-// Whether a call's B and C can come through the scalar cache.
-inline bool scan_fast(const ScanArgs& a, int dt) {
-  const int ns = scan_states(a.n);
-  if (a.n % ns) return false;
-  if (dt == RN_F32) return true;
-  for (int i = 0; i < 3; ++i)
-    if (a.bs[i] % 2 || a.cs[i] % 2) return false;
-  return reinterpret_cast<uintptr_t>(a.b) % 4 == 0 && reinterpret_cast<uintptr_t>(a.c) % 4 == 0;
 }
 
 }  // namespace rn

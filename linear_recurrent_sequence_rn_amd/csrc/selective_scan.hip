@@ -17,141 +17,194 @@ namespace {
 // workspace; or the state a segment adds on its own.
 enum ScanMode : int { kScanOut = 0, kScanState = 1 };
 
-template <int DT, int NS, bool FAST, ScanMode MODE>
+template <int DT, class T>
+__device__ __forceinline__ float value_of(T x) {
+  if constexpr (DT == RN_F32) return x;
+  else return bf16_to_f32(x);
+}
+
+// A channel's n states (or decays), zeros behind them; by fours where they are whole fours on 16 bytes.
+template <int NS>
+__device__ __forceinline__ void load_states(const float* p, int n, bool fours, float* v) {
+  if (fours) {
+#pragma unroll
+    for (int i = 0; i < NS; i += 4) {
+      float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < n) q = *reinterpret_cast<const float4*>(p + i);
+      v[i] = q.x; v[i + 1] = q.y; v[i + 2] = q.z; v[i + 3] = q.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NS; ++i) v[i] = i < n ? p[i] : 0.f;
+  }
+}
+template <int NS>
+__device__ __forceinline__ void store_states(float* p, int n, const float* v) {
+  if (n % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < NS; i += 4)
+      if (i < n) *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+      if (i < n) p[i] = v[i];
+  }
+}
+
+// A wave takes 64 channels of a group, a lane each with all its states, and a piece of a sequence. Waves
+// meet nowhere. Tokens go in groups, the next group's values on their way.
+template <int DT, int NS, Reach HOW, ScanMode MODE>
 __global__ void __launch_bounds__(256) scan_rows(ScanArgs a) {
-  __shared__ float2 steps[kTile][64];     // D_t and D_t x_t
-  __shared__ float parts[MODE == kScanOut ? 4 : 1][kTile][64];
+  constexpr int CH = HOW == kVector ? 4 : NS < 16 ? NS : 16;   // states whose B and C are held at once
+  constexpr int kGroup = NS > 16 || HOW == kVector ? 2 : 4;
+  typedef typename std::conditional<DT == RN_F32, float, uint16_t>::type elem;
   Span p;
   const int64_t piece = blockIdx.y + static_cast<int64_t>(blockIdx.z) * gridDim.y;
-  if (!seq_place(a.q, piece, &p)) return;
-  const int len = __builtin_amdgcn_readfirstlane(p.len);
+  const int x = blockIdx.x * (blockDim.x >> 6) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (x >= a.tiles * a.G || !seq_place(a.q, piece, &p)) return;
   p.piece = __builtin_amdgcn_readfirstlane(p.piece);
+  const int len = __builtin_amdgcn_readfirstlane(p.len);
   const int first = p.piece * a.q.len;
   const int last = len > 0 ? (len - 1) / a.q.len : 0;      // the piece that ends the sequence
   if (MODE == kScanState && p.piece >= last) return;
   const int nt = min(len - first, a.q.len);                // tokens of the piece
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int group = blockIdx.x / a.tiles, each = a.D / a.G;
-  const int in_group = (blockIdx.x - group * a.tiles) * 64 + lane;
-  const bool mine = in_group < each;
-  const int d = group * each + in_group;
-  const int n0 = wave * NS, have = min(NS, a.n - n0);      // this wave's states (have <= 0: none)
-  const int waves = (a.n + NS - 1) / NS;
+  const int group = x / a.tiles, each = a.D / a.G, left = each - (x - group * a.tiles) * 64;
+  const int lane = threadIdx.x & 63;
+  const bool mine = lane < left;
+  const unsigned d = group * each + (each - left) + min(lane, left - 1);     // (lanes past the last channel repeat it)
+  const unsigned off = d * sizeof(elem);
   const int64_t row0 = uniform64(p.row0);
-  auto base = [&](const int64_t* st) {
-    return (a.q.T > 0 ? row0 * st[1] : p.s * st[0]) + static_cast<int64_t>(first) * st[1];
+  auto at = [&](const void* t, const int64_t* st) {        // the piece's first row
+    return static_cast<const elem*>(t) + ((a.q.T > 0 ? row0 : static_cast<int64_t>(first)) * st[1] +
+                                          (a.q.T > 0 ? first * st[1] : p.s * st[0]));
   };
-  const int64_t xb = base(a.xs) + d, dtb = base(a.dts) + d, zb = base(a.zs) + d, ob = base(a.os) + d;
-  auto base3 = [&](const int64_t* st) {
-    return (a.q.T > 0 ? row0 * st[2] : p.s * st[0]) + group * st[1] + static_cast<int64_t>(first) * st[2] + n0;
+  auto heads = [&](const int64_t* st) {
+    return (a.q.T > 0 ? row0 * st[2] : p.s * st[0]) + group * st[1] + static_cast<int64_t>(first) * st[2];
   };
-  const int64_t bb = base3(a.bs), cb = base3(a.cs);
+  const elem* px = at(a.x, a.xs);
+  const elem* pdt = at(a.dt, a.dts);
+  const elem* pz = MODE == kScanOut && a.z ? at(a.z, a.zs) : nullptr;
+  const elem* pb = static_cast<const elem*>(a.b) + heads(a.bs);
+  const elem* pc = static_cast<const elem*>(a.c) + heads(a.cs);
   float A2[NS], h[NS];
+  load_states<NS>(a.A + static_cast<int64_t>(d) * a.n, a.n, a.a4, A2);
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
-    A2[i] = mine && i < have ? a.A[static_cast<int64_t>(d) * a.n + n0 + i] * kLog2e : 0.f;
+    A2[i] = in_log2(A2[i]);
     h[i] = 0.f;
   }
-  const float skip = mine && a.skip ? a.skip[d] : 0.f, bias = mine && a.bias ? a.bias[d] : 0.f;
+  const float skip = a.skip ? a.skip[d] : 0.f, bias = a.bias ? a.bias[d] : 0.f;
   const int slot = p.s < a.q.S ? seq_slot(a.slots, a.n_slots, p.s) : -1;
-  const int64_t sb = (static_cast<int64_t>(slot) * a.D + d) * a.n + n0;
-  if (MODE == kScanOut && mine) {
-    const float* from = p.piece <= last && last > 0 ? a.seg_state + (piece * a.D + d) * a.n + n0
+  const int64_t sb = (static_cast<int64_t>(slot) * a.D + d) * a.n;
+  if (MODE == kScanOut) {
+    const float* from = p.piece <= last && last > 0 ? a.seg_state + (piece * a.D + d) * a.n
                         : slot >= 0 && a.state_in && p.piece == 0 ? a.state_in + sb : nullptr;
-    if (from) {
-#pragma unroll
-      for (int i = 0; i < NS; ++i)
-        if (i < have) h[i] = from[i];
-    }
+    if (from) load_states<NS>(from, a.n, a.n % 4 == 0, h);
   }
+  elem* out = MODE == kScanOut ? const_cast<elem*>(at(a.out, a.os)) : nullptr;
   float total = 0.f;                      // kScanState: the sum of D_t
-  float nx[kEach], ndt[kEach], nz[kEach];
-  auto fetch = [&](int t0) {
+  elem nx[kGroup], ndt[kGroup], nz[kGroup] = {};
+  auto take = [&](const elem*& p, int64_t step) {          // the lane's value of the row p stands at
+    const elem v = *reinterpret_cast<const elem*>(reinterpret_cast<const char*>(p) + off);
+    p += step;
+    return v;
+  };
+  auto fetch = [&]() {                    // the next group's values
 #pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-      const int t = t0 + wave * kEach + k;
-      const bool there = mine && t < nt;
-      nx[k] = there ? Elem<DT>::load(a.x, xb + t * a.xs[1]) : 0.f;
-      ndt[k] = there ? Elem<DT>::load(a.dt, dtb + t * a.dts[1]) : 0.f;
-      if (MODE == kScanOut) nz[k] = there && a.z ? Elem<DT>::load(a.z, zb + t * a.zs[1]) : 0.f;
+    for (int k = 0; k < kGroup; ++k) {
+      nx[k] = take(px, a.xs[1]);
+      ndt[k] = take(pdt, a.dts[1]);
+    }
+    if (MODE == kScanOut && pz) {
+#pragma unroll
+      for (int k = 0; k < kGroup; ++k) nz[k] = take(pz, a.zs[1]);
     }
   };
-  fetch(0);
-  for (int t0 = 0; t0 < nt; t0 += kTile) {
-    float x[kEach], z[kEach];
-#pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-      const int t = wave * kEach + k;
-      float s = ndt[k] + bias;
-      if (a.softplus) s = softplus(s);
-      if (t0 + t >= nt) s = 0.f;
-      steps[t][lane] = make_float2(s, s * nx[k]);
-      x[k] = nx[k];
-      z[k] = nz[k];
+  // Up to 16 states' B and C are on their way while the token before is worked on; of more, each set's when
+  // it is needed.
+  constexpr bool kAhead = NS == CH && HOW != kVector;
+  Uniform<DT, CH, HOW> nb, nc;
+  auto heads_of = [&](int c, Uniform<DT, CH, HOW>* B, Uniform<DT, CH, HOW>* C) {
+    B->load(pb, c, a.n - c);
+    if (MODE == kScanOut) C->load(pc, c, a.n - c);
+  };
+  auto token = [&](float xv, float s, int t) {
+    const float u = s * xv;
+    float y = skip * xv;
+    Uniform<DT, CH, HOW> B, C;
+    if (kAhead) {
+      B = nb;
+      C = nc;
+      if (t + 1 < nt) { pb += a.bs[2]; pc += a.cs[2]; }      // (behind the last token it is read again)
+      heads_of(0, &nb, &nc);
     }
-    if (t0 + kTile < nt) fetch(t0 + kTile);
-    __syncthreads();
-    if (have > 0) {
-      auto token = [&](int t, const Uniform<DT, NS, FAST>& b, const Uniform<DT, NS, FAST>& c) {
-        const float2 s = steps[t][lane];
-        float y = 0.f;
 #pragma unroll
-        for (int i = 0; i < NS; ++i) {
-          h[i] = fmaf(__builtin_amdgcn_exp2f(s.x * A2[i]), h[i], s.y * b.value(i));
-          if (MODE == kScanOut) y = fmaf(c.value(i), h[i], y);
-        }
-        if (MODE == kScanOut) parts[wave][t][lane] = y;
-        else total += s.x;
-      };
-      if (t0 + kTile <= nt) {
-#pragma unroll 4
-        for (int t = 0; t < kTile; ++t) {
-          Uniform<DT, NS, FAST> b, c;
-          b.load(a.b, bb + (t0 + t) * a.bs[2], have);
-          if (MODE == kScanOut) c.load(a.c, cb + (t0 + t) * a.cs[2], have);
-          token(t, b, c);
-        }
-      } else {
-        for (int t = 0; t < nt - t0; ++t) {
-          Uniform<DT, NS, FAST> b, c;
-          b.load(a.b, bb + (t0 + t) * a.bs[2], have);
-          if (MODE == kScanOut) c.load(a.c, cb + (t0 + t) * a.cs[2], have);
-          token(t, b, c);
-        }
+    for (int c = 0; c < NS; c += CH) {
+      if (!kAhead) heads_of(c, &B, &C);
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        h[c + i] = fmaf(__builtin_amdgcn_exp2f(s * A2[c + i]), h[c + i], u * B.value(i));
+        if (MODE == kScanOut) y = fmaf(C.value(i), h[c + i], y);
       }
     }
-    __syncthreads();
+    if (!kAhead) { pb += a.bs[2]; pc += a.cs[2]; }
+    if (MODE == kScanState) total += s;
+    return y;
+  };
+  const int groups = nt > 0 ? nt / kGroup : 0;
+  if (groups > 0) fetch();
+  if (kAhead && nt > 0) heads_of(0, &nb, &nc);
+  for (int g = 0; g < groups; ++g) {
+    float xv[kGroup], s[kGroup], y[kGroup], z[kGroup];
+#pragma unroll
+    for (int k = 0; k < kGroup; ++k) {
+      xv[k] = value_of<DT>(nx[k]);
+      s[k] = value_of<DT>(ndt[k]) + bias;
+      if (MODE == kScanOut) z[k] = value_of<DT>(nz[k]);
+    }
+    if (g + 1 < groups) fetch();
+    if (a.softplus) {
+#pragma unroll
+      for (int k = 0; k < kGroup; ++k) s[k] = softplus(s[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kGroup; ++k) y[k] = token(xv[k], s[k], g * kGroup + k);
     if (MODE == kScanOut) {
+      if (pz) {
 #pragma unroll
-      for (int k = 0; k < kEach; ++k) {
-        const int t = wave * kEach + k;
-        if (mine && t0 + t < nt) {
-          float y = skip * x[k];
-          for (int w = 0; w < waves; ++w) y += parts[w][t][lane];
-          if (a.z) y *= z[k] * sigmoidf(z[k]);
-          Elem<DT>::store(a.out, ob + (t0 + t) * a.os[1], y);
-        }
+        for (int k = 0; k < kGroup; ++k) y[k] *= z[k] * sigmoidf(z[k]);
       }
+      if (mine) {
+#pragma unroll
+        for (int k = 0; k < kGroup; ++k) Elem<DT>::store(reinterpret_cast<char*>(out + k * a.os[1]) + off, 0, y[k]);
+      }
+      out += kGroup * a.os[1];
     }
   }
-  if (MODE == kScanState) {
-    if (mine) {
-      float* to = a.seg_state + (piece * a.D + d) * a.n + n0;
-#pragma unroll
-      for (int i = 0; i < NS; ++i)
-        if (i < have) to[i] = h[i];
-      if (wave == 0) a.seg_step[piece * a.D + d] = total;
+  for (int t = groups * kGroup; t < nt; ++t) {     // fewer than a group
+    const float xv = value_of<DT>(take(px, a.xs[1]));
+    float s = value_of<DT>(take(pdt, a.dts[1])) + bias;
+    if (a.softplus) s = softplus(s);
+    float y = token(xv, s, t);
+    if (MODE == kScanOut) {
+      if (pz) {
+        const float z = value_of<DT>(take(pz, a.zs[1]));
+        y *= z * sigmoidf(z);
+      }
+      if (mine) Elem<DT>::store(reinterpret_cast<char*>(out) + off, 0, y);
+      out += a.os[1];
     }
+  }
+  if (!mine) return;
+  if (MODE == kScanState) {
+    store_states<NS>(a.seg_state + (piece * a.D + d) * a.n, a.n, h);
+    a.seg_step[piece * a.D + d] = total;
     return;
   }
-  if (mine && p.piece == last && slot >= 0 && a.state_out) {
-#pragma unroll
-    for (int i = 0; i < NS; ++i)
-      if (i < have) a.state_out[sb + i] = h[i];
-  }
-  if (a.zero_rest && mine) {
+  if (p.piece == last && slot >= 0 && a.state_out) store_states<NS>(a.state_out + sb, a.n, h);
+  if (a.zero_rest) {
     const int64_t rows = min(p.own - first, static_cast<int64_t>(a.q.len));
-    for (int64_t t = max(nt, 0) + wave; t < rows; t += 4) Elem<DT>::store(a.out, ob + t * a.os[1], 0.f);
+    for (int64_t t = max(nt, 0); t < rows; ++t, out += a.os[1]) Elem<DT>::store(out, d, 0.f);
   }
 }
 
@@ -167,7 +220,7 @@ __global__ void __launch_bounds__(256) scan_carry(ScanArgs a) {
   const int64_t w0 = a.q.T > 0 ? p.row0 / a.q.len + s : static_cast<int64_t>(s) * a.q.n_seg;
   const int slot = seq_slot(a.slots, a.n_slots, s);
   const int d = static_cast<int>(i / a.n);
-  const float A2 = a.A[i] * kLog2e;
+  const float A2 = in_log2(a.A[i]);
   float h = slot >= 0 && a.state_in ? a.state_in[slot * all + i] : 0.f;
   float* to = a.seg_state + w0 * all + i;
   const float* step = a.seg_step + w0 * a.D + d;
@@ -227,7 +280,7 @@ __global__ void __launch_bounds__(256) scan_step(ScanArgs a, int P) {
   vec to;
 #pragma unroll
   for (int i = 0; i < VEC; ++i) {
-    h[i] = fmaf(__builtin_amdgcn_exp2f(step * (A[i] * kLog2e)), h[i], step * x * b[i]);
+    h[i] = fmaf(__builtin_amdgcn_exp2f(step * (in_log2(A[i]))), h[i], step * x * b[i]);
     y = fmaf(c[i], h[i], y);
     to[i] = h[i];
   }
@@ -243,26 +296,33 @@ __global__ void __launch_bounds__(256) scan_step(ScanArgs a, int P) {
   }
 }
 
-template <int DT, int NS, bool FAST>
+template <int DT, int NS, Reach HOW>
 hipError_t launch_rows(const ScanArgs& a, bool state, hipStream_t st) {
-  const dim3 grid = seq_grid(a.q, static_cast<int64_t>(a.tiles) * a.G);
-  if (state) hipLaunchKernelGGL((scan_rows<DT, NS, FAST, kScanState>), grid, dim3(256), 0, st, a);
-  else hipLaunchKernelGGL((scan_rows<DT, NS, FAST, kScanOut>), grid, dim3(256), 0, st, a);
+  const int64_t x = static_cast<int64_t>(a.tiles) * a.G;
+  const int waves = static_cast<int>(std::min<int64_t>(x, 4));
+  const dim3 grid = seq_grid(a.q, (x + waves - 1) / waves), block(64 * waves);
+  if (state) hipLaunchKernelGGL((scan_rows<DT, NS, HOW, kScanState>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((scan_rows<DT, NS, HOW, kScanOut>), grid, block, 0, st, a);
   return hipGetLastError();
 }
-template <int DT, bool FAST>
-hipError_t launch_n(const ScanArgs& a, bool state, hipStream_t st) {
-  switch (scan_states(a.n)) {
-    case 2: return launch_rows<DT, 2, FAST>(a, state, st);
-    case 4: return launch_rows<DT, 4, FAST>(a, state, st);
-    case 8: return launch_rows<DT, 8, FAST>(a, state, st);
-    default: return launch_rows<DT, 16, FAST>(a, state, st);
+template <int DT, int NS>
+hipError_t launch_how(const ScanArgs& a, bool state, hipStream_t st) {
+  switch (scan_reach(a, DT, a.n == NS)) {
+    case kScalar: return launch_rows<DT, NS, kScalar>(a, state, st);
+    case kScalarSome: return launch_rows<DT, NS, kScalarSome>(a, state, st);
+    default: return launch_rows<DT, NS, kVector>(a, state, st);
   }
 }
+template <int DT>
+hipError_t launch_n(const ScanArgs& a, bool state, hipStream_t st) {
+  if (a.n <= 4) return launch_how<DT, 4>(a, state, st);
+  if (a.n <= 8) return launch_how<DT, 8>(a, state, st);
+  if (a.n <= 16) return launch_how<DT, 16>(a, state, st);
+  if (a.n <= 32) return launch_how<DT, 32>(a, state, st);
+  return launch_how<DT, 64>(a, state, st);
+}
 hipError_t launch_pass(const ScanArgs& a, int dt, bool state, hipStream_t st) {
-  const bool fast = scan_fast(a, dt);
-  if (dt == RN_F32) return fast ? launch_n<RN_F32, true>(a, state, st) : launch_n<RN_F32, false>(a, state, st);
-  return fast ? launch_n<RN_BF16, true>(a, state, st) : launch_n<RN_BF16, false>(a, state, st);
+  return dt == RN_F32 ? launch_n<RN_F32>(a, state, st) : launch_n<RN_BF16>(a, state, st);
 }
 
 // Tokens a segment: whole sequences where their channels fill the chip by themselves (three blocks of
@@ -270,7 +330,7 @@ hipError_t launch_pass(const ScanArgs& a, int dt, bool state, hipStream_t st) {
 int segment(const ScanCall& c) {
   const int64_t per = static_cast<int64_t>(c.G) * ((c.D / c.G + 63) / 64);
   const int64_t tokens = c.T > 0 ? std::min<int64_t>(c.T, static_cast<int64_t>(c.S) * c.N) : static_cast<int64_t>(c.S) * c.N;
-  int64_t L = std::max<int64_t>((tokens * per / 1024 + 15) / 16 * 16, 64);
+  int64_t L = std::max<int64_t>((tokens * per / 8192 + 15) / 16 * 16, 32);
   if (2 * L > c.N) L = c.N;
   return static_cast<int>(L);
 }

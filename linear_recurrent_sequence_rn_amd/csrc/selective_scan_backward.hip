@@ -41,6 +41,10 @@ struct BackArgs {
   float* part_bc;                         // [token rows][blocks along channels][2][n]
 };
 
+constexpr int kTile = 16;                 // tokens a tile of scan_edges: each wave prepares four
+constexpr int kEach = kTile / 4;
+// States a wave holds: a quarter of them, at least two.
+int scan_states(int n) { return n <= 8 ? 2 : n <= 16 ? 4 : n <= 32 ? 8 : 16; }
 constexpr int tile_of(int NS) { return 32 / NS; }
 constexpr int kTiles = 8;                 // tiles a piece
 
@@ -101,7 +105,7 @@ __device__ __forceinline__ float step_of(const ScanArgs& a, float v) { return a.
 // ---- the edges of a piece -------------------------------------------------------------------
 // Forward over the piece: the state h it adds, and with P_t = a_1 .. a_t the gradient sum_t P_t C_t dy_t
 // that it passes back.
-template <int DT, int NS, bool FAST>
+template <int DT, int NS, Reach HOW>
 __global__ void __launch_bounds__(256) scan_edges(BackArgs b) {
   __shared__ float4 tile[kTile][64];      // D, u, dy
   const ScanArgs& a = b.s;
@@ -113,7 +117,7 @@ __global__ void __launch_bounds__(256) scan_edges(BackArgs b) {
   float A2[NS], h[NS], P[NS], e[NS];
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
-    A2[i] = w.mine && i < w.have ? a.A[static_cast<int64_t>(w.d) * a.n + w.n0 + i] * kLog2e : 0.f;
+    A2[i] = w.mine && i < w.have ? in_log2(a.A[static_cast<int64_t>(w.d) * a.n + w.n0 + i]) : 0.f;
     h[i] = e[i] = 0.f;
     P[i] = 1.f;
   }
@@ -141,7 +145,7 @@ __global__ void __launch_bounds__(256) scan_edges(BackArgs b) {
       const int n = min(kTile, nt - t0);
 #pragma unroll 4
       for (int t = 0; t < n; ++t) {
-        Uniform<DT, NS, FAST> B, C;
+        Uniform<DT, NS, HOW> B, C;
         B.load(a.b, bb + (t0 + t) * a.bs[2], w.have);
         C.load(a.c, cb + (t0 + t) * a.cs[2], w.have);
         const float4 v = tile[t][w.lane];
@@ -178,7 +182,7 @@ __global__ void __launch_bounds__(256) scan_edges_carry(BackArgs b) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, all = static_cast<int64_t>(a.D) * a.n;
   if (pieces < 2 || i >= all) return;
   const int64_t w0 = a.q.T > 0 ? p.row0 / a.q.len + s : static_cast<int64_t>(s) * a.q.n_seg;
-  const float A2 = a.A[i] * kLog2e;
+  const float A2 = in_log2(a.A[i]);
   const bool back = blockIdx.z;
   const float* first = back ? b.dstate_out : a.state_in;
   float h = first ? first[s * all + i] : 0.f;
@@ -237,7 +241,7 @@ __device__ __forceinline__ float sums64(float (&v)[64], int lane) {
   return fold<0xB1>(v[0], v[1], lane & 1);                                       // lane ^ 1
 }
 
-template <int DT, int NS, bool FAST>
+template <int DT, int NS, Reach HOW>
 __global__ void __launch_bounds__(256) scan_main(BackArgs b) {
   constexpr int TT = tile_of(NS);
   constexpr int EACH = TT >= 4 ? TT / 4 : 1;
@@ -262,7 +266,7 @@ __global__ void __launch_bounds__(256) scan_main(BackArgs b) {
 #pragma unroll
     for (int i = 0; i < NS; ++i)
       if (i < w.have) {
-        A2[i] = a.A[static_cast<int64_t>(w.d) * a.n + w.n0 + i] * kLog2e;
+        A2[i] = in_log2(a.A[static_cast<int64_t>(w.d) * a.n + w.n0 + i]);
         if (from) h[i] = from[i];
         if (grad) e[i] = grad[i];
       }
@@ -298,7 +302,7 @@ __global__ void __launch_bounds__(256) scan_main(BackArgs b) {
       if (w.have > 0) {
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-          Uniform<DT, NS, FAST> B;
+          Uniform<DT, NS, HOW> B;
           B.load(a.b, bb + (q * TT + t) * a.bs[2], w.have);
           const float4 v = tile[t][w.lane];
 #pragma unroll
@@ -339,7 +343,7 @@ __global__ void __launch_bounds__(256) scan_main(BackArgs b) {
           }
         }
         float dec[TT][NS], p[TT][NS], sums[64];
-        Uniform<DT, NS, FAST> B[TT], C[TT];
+        Uniform<DT, NS, HOW> B[TT], C[TT];
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
           const int have = t0 + t < nt ? w.have : 0;       // tokens behind the last one have zeros
@@ -499,32 +503,41 @@ __global__ void __launch_bounds__(1024) scan_sum_pieces(BackArgs b, int64_t piec
   }
 }
 
-template <int DT, int NS, bool FAST>
+template <int DT, int NS, Reach HOW>
 hipError_t launch_back(const BackArgs& b, hipStream_t st) {
   const ScanArgs& a = b.s;
   const int64_t x = static_cast<int64_t>(a.tiles) * a.G, all = static_cast<int64_t>(a.D) * a.n;
   const dim3 grid = seq_grid(a.q, x);
   hipError_t e;
   if (a.q.N > a.q.len) {
-    hipLaunchKernelGGL((scan_edges<DT, NS, FAST>), grid, dim3(256), 0, st, b);
+    hipLaunchKernelGGL((scan_edges<DT, NS, HOW>), grid, dim3(256), 0, st, b);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     hipLaunchKernelGGL(scan_edges_carry, dim3(static_cast<unsigned>((all + 255) / 256), a.q.S, 2), dim3(256), 0, st, b);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((scan_main<DT, NS, FAST>), grid, dim3(256), 0, st, b);
+  hipLaunchKernelGGL((scan_main<DT, NS, HOW>), grid, dim3(256), 0, st, b);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   hipLaunchKernelGGL((scan_sum_tokens<DT>), seq_grid(a.q, 1), dim3(256), 0, st, b);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   hipLaunchKernelGGL(scan_sum_pieces, dim3(static_cast<unsigned>((all + 2 * a.D + 31) / 32)), dim3(1024), 0, st, b, seq_pieces(a.q));
   return hipGetLastError();
 }
-template <int DT, bool FAST>
+template <int DT, Reach HOW>
 hipError_t launch_n(const BackArgs& b, hipStream_t st) {
   switch (scan_states(b.s.n)) {
-    case 2: return launch_back<DT, 2, FAST>(b, st);
-    case 4: return launch_back<DT, 4, FAST>(b, st);
-    case 8: return launch_back<DT, 8, FAST>(b, st);
-    default: return launch_back<DT, 16, FAST>(b, st);
+    case 2: return launch_back<DT, 2, HOW>(b, st);
+    case 4: return launch_back<DT, 4, HOW>(b, st);
+    case 8: return launch_back<DT, 8, HOW>(b, st);
+    default: return launch_back<DT, 16, HOW>(b, st);
+  }
+}
+
+template <int DT>
+hipError_t launch_how(const BackArgs& b, Reach how, hipStream_t st) {
+  switch (how) {
+    case kScalar: return launch_n<DT, kScalar>(b, st);
+    case kScalarSome: return launch_n<DT, kScalarSome>(b, st);
+    default: return launch_n<DT, kVector>(b, st);
   }
 }
 
@@ -561,9 +574,9 @@ hipError_t launch_selective_backward(const ScanCall& c, const ScanGrads& g, hipS
   b.part_skip = b.s.seg_step + parts.step;
   b.part_bias = b.part_skip + parts.step;
   b.part_bc = b.part_bias + parts.step;
-  const bool fast = scan_fast(b.s, c.type);
-  if (c.type == RN_F32) return fast ? launch_n<RN_F32, true>(b, st) : launch_n<RN_F32, false>(b, st);
-  return fast ? launch_n<RN_BF16, true>(b, st) : launch_n<RN_BF16, false>(b, st);
+  const Reach how = scan_reach(b.s, c.type, c.n % scan_states(c.n) == 0);
+  if (c.type == RN_F32) return launch_how<RN_F32>(b, how, st);
+  return launch_how<RN_BF16>(b, how, st);
 }
 
 }  // namespace rn
