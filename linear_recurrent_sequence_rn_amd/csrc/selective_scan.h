@@ -62,35 +62,20 @@ __device__ __forceinline__ int64_t uniform64(int64_t x) {
   return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
 }
 
-// How B and C reach the waves, for all lanes of which they are the same: through the scalar cache, in whole
-// sets of states (bf16: in pairs that start on 4 bytes), or in sets of which the last one is short; or
-// by loads of every lane.
-enum Reach : int { kScalar = 0, kScalarSome = 1, kVector = 2 };
-
-// NS values of B or C from element i of p (both the same for the whole wave), of which the first `have` are
-// there; the rest are zeros.
-template <int DT, int NS, Reach HOW>
-struct Uniform {
+// NS values of B or C from element i of p (both the same for the whole wave). FAST: through the scalar
+// cache; all NS are there, bf16 in pairs that start on 4 bytes. Else every lane loads the first `have` of
+// them, the rest being zeros.
+template <int DT, int NS, bool FAST>
+struct Uniform;
+template <int DT, int NS>
+struct Uniform<DT, NS, true> {
   static constexpr int kWords = DT == RN_F32 ? NS : NS / 2;
-  static constexpr int kPer = DT == RN_F32 ? 1 : 2;
   uint32_t u[kWords];
-  __device__ __forceinline__ void load(const void* p, int64_t i, int have) {
+  __device__ __forceinline__ void load(const void* p, int64_t i, int) {
     typedef const __attribute__((address_space(4))) uint32_t* words;
-    const words w = (words)static_cast<uint64_t>(uniform64(reinterpret_cast<int64_t>(p) + i * (4 / kPer)));
-    if constexpr (HOW == kScalar) {
+    const words w = (words)static_cast<uint64_t>(uniform64(reinterpret_cast<int64_t>(p) + i * (DT == RN_F32 ? 4 : 2)));
 #pragma unroll
-      for (int k = 0; k < kWords; ++k) u[k] = w[k];
-    } else {
-      // quarters of four: those that are not there read the last one that is, and count nothing
-      constexpr int kFour = 4 / kPer;
-      const int there = have < NS ? have : NS;
-#pragma unroll
-      for (int k = 0; k < kWords; ++k) {
-        const int q = k / kFour;
-        const uint32_t v = w[(q * 4 < there ? q : there / 4 - 1) * kFour + k % kFour];
-        u[k] = q * 4 < there ? v : 0;
-      }
-    }
+    for (int k = 0; k < kWords; ++k) u[k] = w[k];
   }
   // the same, or zeros (and nothing read) where `have` is 0
   __device__ __forceinline__ void load_or_zero(const void* p, int64_t i, int have) {
@@ -104,7 +89,7 @@ struct Uniform {
   }
 };
 template <int DT, int NS>
-struct Uniform<DT, NS, kVector> {
+struct Uniform<DT, NS, false> {
   float f[NS];
   __device__ __forceinline__ void load(const void* p, int64_t i, int have) {
 #pragma unroll
@@ -114,16 +99,13 @@ struct Uniform<DT, NS, kVector> {
   __device__ __forceinline__ float value(int k) const { return f[k]; }
 };
 
-// `whole`: every set is of NS states.
-inline Reach scan_reach(const ScanArgs& a, int dt, bool whole) {
-  if (!whole && a.n % 4) return kVector;
-  if (dt == RN_BF16) {
-    if (a.n % 2) return kVector;
-    for (int i = 0; i < 3; ++i)
-      if (a.bs[i] % 2 || a.cs[i] % 2) return kVector;
-    if (reinterpret_cast<uintptr_t>(a.b) % 4 || reinterpret_cast<uintptr_t>(a.c) % 4) return kVector;
-  }
-  return whole ? kScalar : kScalarSome;
+// Whether B and C can come through the scalar cache, in sets of `set` states.
+inline bool scan_fast(const ScanArgs& a, int dt, int set) {
+  if (a.n % set) return false;
+  if (dt == RN_F32) return true;
+  for (int i = 0; i < 3; ++i)
+    if (a.bs[i] % 2 || a.cs[i] % 2) return false;
+  return reinterpret_cast<uintptr_t>(a.b) % 4 == 0 && reinterpret_cast<uintptr_t>(a.c) % 4 == 0;
 }
 
 // The call's kernel arguments, with `len` tokens a piece.

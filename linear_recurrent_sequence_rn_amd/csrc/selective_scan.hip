@@ -53,10 +53,10 @@ __device__ __forceinline__ void store_states(float* p, int n, const float* v) {
 
 // A wave takes 64 channels of a group, a lane each with all its states, and a piece of a sequence. Waves
 // meet nowhere. Tokens go in groups, the next group's values on their way.
-template <int DT, int NS, Reach HOW, ScanMode MODE>
+template <int DT, int NS, bool FAST, ScanMode MODE>
 __global__ void __launch_bounds__(256) scan_rows(ScanArgs a) {
-  constexpr int CH = HOW == kVector ? 4 : NS < 16 ? NS : 16;   // states whose B and C are held at once
-  constexpr int kGroup = NS > 16 || HOW == kVector ? 2 : 4;
+  constexpr int CH = !FAST ? 4 : NS <= 16 ? NS : NS % 16 ? 12 : 16;   // states whose B and C are held at once
+  constexpr int kGroup = NS > 16 || !FAST ? 2 : 4;
   typedef typename std::conditional<DT == RN_F32, float, uint16_t>::type elem;
   Span p;
   const int64_t piece = blockIdx.y + static_cast<int64_t>(blockIdx.z) * gridDim.y;
@@ -122,16 +122,16 @@ __global__ void __launch_bounds__(256) scan_rows(ScanArgs a) {
   };
   // Up to 16 states' B and C are on their way while the token before is worked on; of more, each set's when
   // it is needed.
-  constexpr bool kAhead = NS == CH && HOW != kVector;
-  Uniform<DT, CH, HOW> nb, nc;
-  auto heads_of = [&](int c, Uniform<DT, CH, HOW>* B, Uniform<DT, CH, HOW>* C) {
+  constexpr bool kAhead = NS == CH && FAST;
+  Uniform<DT, CH, FAST> nb, nc;
+  auto heads_of = [&](int c, Uniform<DT, CH, FAST>* B, Uniform<DT, CH, FAST>* C) {
     B->load(pb, c, a.n - c);
     if (MODE == kScanOut) C->load(pc, c, a.n - c);
   };
   auto token = [&](float xv, float s, int t) {
     const float u = s * xv;
     float y = skip * xv;
-    Uniform<DT, CH, HOW> B, C;
+    Uniform<DT, CH, FAST> B, C;
     if (kAhead) {
       B = nb;
       C = nc;
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(256) scan_carry(ScanArgs a) {
   float h = slot >= 0 && a.state_in ? a.state_in[slot * all + i] : 0.f;
   float* to = a.seg_state + w0 * all + i;
   const float* step = a.seg_step + w0 * a.D + d;
-  constexpr int kAhead = 8;
+  constexpr int kAhead = 16;
   for (int g0 = 0; g0 < pieces; g0 += kAhead) {
     float own[kAhead], total[kAhead];
 #pragma unroll
@@ -296,42 +296,46 @@ __global__ void __launch_bounds__(256) scan_step(ScanArgs a, int P) {
   }
 }
 
-template <int DT, int NS, Reach HOW>
+template <int DT, int NS, bool FAST>
 hipError_t launch_rows(const ScanArgs& a, bool state, hipStream_t st) {
   const int64_t x = static_cast<int64_t>(a.tiles) * a.G;
   const int waves = static_cast<int>(std::min<int64_t>(x, 4));
   const dim3 grid = seq_grid(a.q, (x + waves - 1) / waves), block(64 * waves);
-  if (state) hipLaunchKernelGGL((scan_rows<DT, NS, HOW, kScanState>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((scan_rows<DT, NS, HOW, kScanOut>), grid, block, 0, st, a);
+  if (state) hipLaunchKernelGGL((scan_rows<DT, NS, FAST, kScanState>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((scan_rows<DT, NS, FAST, kScanOut>), grid, block, 0, st, a);
   return hipGetLastError();
 }
 template <int DT, int NS>
 hipError_t launch_how(const ScanArgs& a, bool state, hipStream_t st) {
-  switch (scan_reach(a, DT, a.n == NS)) {
-    case kScalar: return launch_rows<DT, NS, kScalar>(a, state, st);
-    case kScalarSome: return launch_rows<DT, NS, kScalarSome>(a, state, st);
-    default: return launch_rows<DT, NS, kVector>(a, state, st);
-  }
+  return scan_fast(a, DT, NS) ? launch_rows<DT, NS, true>(a, state, st) : launch_rows<DT, NS, false>(a, state, st);
 }
 template <int DT>
 hipError_t launch_n(const ScanArgs& a, bool state, hipStream_t st) {
   if (a.n <= 4) return launch_how<DT, 4>(a, state, st);
   if (a.n <= 8) return launch_how<DT, 8>(a, state, st);
+  if (a.n <= 12) return launch_how<DT, 12>(a, state, st);
   if (a.n <= 16) return launch_how<DT, 16>(a, state, st);
+  if (a.n <= 24) return launch_how<DT, 24>(a, state, st);
   if (a.n <= 32) return launch_how<DT, 32>(a, state, st);
+  if (a.n <= 48) return launch_how<DT, 48>(a, state, st);
   return launch_how<DT, 64>(a, state, st);
 }
 hipError_t launch_pass(const ScanArgs& a, int dt, bool state, hipStream_t st) {
   return dt == RN_F32 ? launch_n<RN_F32>(a, state, st) : launch_n<RN_BF16>(a, state, st);
 }
 
-// Tokens a segment: whole sequences where their channels fill the chip by themselves (three blocks of
-// four waves a CU); else as many segments as do.
+// Tokens a segment. Whole sequences where their channels make a wave or more for each of the chip's 1024
+// SIMDs (bf16 with gate, 16 states, 4096 channels: 32 sequences of 512 tokens 295 us, cut 442; 24: 292 and
+// 343; 16: 231 and 227; 12 of 1024: 470 and 323), or where the sequences are short (8 of 32 tokens, 1000
+// channels, 12 states, float32: 20 and 28 us; of 64: 28 and 28); sequences of unknown lengths count as so many
+// of the longest's. Else 10 waves a SIMD in all: about 5 are there at once, and more take turns better than one
+// round of waves, half as many again being slower for the states that pass between them (8192 tokens of
+// 4096 channels: 232 us; 4 to 7 waves: 246 to 261, 12: 234).
 int segment(const ScanCall& c) {
   const int64_t per = static_cast<int64_t>(c.G) * ((c.D / c.G + 63) / 64);
   const int64_t tokens = c.T > 0 ? std::min<int64_t>(c.T, static_cast<int64_t>(c.S) * c.N) : static_cast<int64_t>(c.S) * c.N;
-  int64_t L = std::max<int64_t>((tokens * per / 8192 + 15) / 16 * 16, 32);
-  if (2 * L > c.N) L = c.N;
+  const int64_t L = std::max<int64_t>((tokens * per / 10240 + 15) / 16 * 16, 16);
+  if (c.N < 64 || 2 * L > c.N || tokens * per >= 1280 * static_cast<int64_t>(c.N)) return c.N;
   return static_cast<int>(L);
 }
 

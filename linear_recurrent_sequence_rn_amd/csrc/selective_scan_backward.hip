@@ -105,7 +105,7 @@ __device__ __forceinline__ float step_of(const ScanArgs& a, float v) { return a.
 // ---- the edges of a piece -------------------------------------------------------------------
 // Forward over the piece: the state h it adds, and with P_t = a_1 .. a_t the gradient sum_t P_t C_t dy_t
 // that it passes back.
-template <int DT, int NS, Reach HOW>
+template <int DT, int NS, bool FAST>
 __global__ void __launch_bounds__(256) scan_edges(BackArgs b) {
   __shared__ float4 tile[kTile][64];      // D, u, dy
   const ScanArgs& a = b.s;
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(256) scan_edges(BackArgs b) {
       const int n = min(kTile, nt - t0);
 #pragma unroll 4
       for (int t = 0; t < n; ++t) {
-        Uniform<DT, NS, HOW> B, C;
+        Uniform<DT, NS, FAST> B, C;
         B.load(a.b, bb + (t0 + t) * a.bs[2], w.have);
         C.load(a.c, cb + (t0 + t) * a.cs[2], w.have);
         const float4 v = tile[t][w.lane];
@@ -241,7 +241,7 @@ __device__ __forceinline__ float sums64(float (&v)[64], int lane) {
   return fold<0xB1>(v[0], v[1], lane & 1);                                       // lane ^ 1
 }
 
-template <int DT, int NS, Reach HOW>
+template <int DT, int NS, bool FAST>
 __global__ void __launch_bounds__(256) scan_main(BackArgs b) {
   constexpr int TT = tile_of(NS);
   constexpr int EACH = TT >= 4 ? TT / 4 : 1;
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(256) scan_main(BackArgs b) {
       if (w.have > 0) {
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-          Uniform<DT, NS, HOW> B;
+          Uniform<DT, NS, FAST> B;
           B.load(a.b, bb + (q * TT + t) * a.bs[2], w.have);
           const float4 v = tile[t][w.lane];
 #pragma unroll
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(256) scan_main(BackArgs b) {
           }
         }
         float dec[TT][NS], p[TT][NS], sums[64];
-        Uniform<DT, NS, HOW> B[TT], C[TT];
+        Uniform<DT, NS, FAST> B[TT], C[TT];
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
           const int have = t0 + t < nt ? w.have : 0;       // tokens behind the last one have zeros
@@ -503,41 +503,32 @@ __global__ void __launch_bounds__(1024) scan_sum_pieces(BackArgs b, int64_t piec
   }
 }
 
-template <int DT, int NS, Reach HOW>
+template <int DT, int NS, bool FAST>
 hipError_t launch_back(const BackArgs& b, hipStream_t st) {
   const ScanArgs& a = b.s;
   const int64_t x = static_cast<int64_t>(a.tiles) * a.G, all = static_cast<int64_t>(a.D) * a.n;
   const dim3 grid = seq_grid(a.q, x);
   hipError_t e;
   if (a.q.N > a.q.len) {
-    hipLaunchKernelGGL((scan_edges<DT, NS, HOW>), grid, dim3(256), 0, st, b);
+    hipLaunchKernelGGL((scan_edges<DT, NS, FAST>), grid, dim3(256), 0, st, b);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     hipLaunchKernelGGL(scan_edges_carry, dim3(static_cast<unsigned>((all + 255) / 256), a.q.S, 2), dim3(256), 0, st, b);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((scan_main<DT, NS, HOW>), grid, dim3(256), 0, st, b);
+  hipLaunchKernelGGL((scan_main<DT, NS, FAST>), grid, dim3(256), 0, st, b);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   hipLaunchKernelGGL((scan_sum_tokens<DT>), seq_grid(a.q, 1), dim3(256), 0, st, b);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   hipLaunchKernelGGL(scan_sum_pieces, dim3(static_cast<unsigned>((all + 2 * a.D + 31) / 32)), dim3(1024), 0, st, b, seq_pieces(a.q));
   return hipGetLastError();
 }
-template <int DT, Reach HOW>
+template <int DT, bool FAST>
 hipError_t launch_n(const BackArgs& b, hipStream_t st) {
   switch (scan_states(b.s.n)) {
-    case 2: return launch_back<DT, 2, HOW>(b, st);
-    case 4: return launch_back<DT, 4, HOW>(b, st);
-    case 8: return launch_back<DT, 8, HOW>(b, st);
-    default: return launch_back<DT, 16, HOW>(b, st);
-  }
-}
-
-template <int DT>
-hipError_t launch_how(const BackArgs& b, Reach how, hipStream_t st) {
-  switch (how) {
-    case kScalar: return launch_n<DT, kScalar>(b, st);
-    case kScalarSome: return launch_n<DT, kScalarSome>(b, st);
-    default: return launch_n<DT, kVector>(b, st);
+    case 2: return launch_back<DT, 2, FAST>(b, st);
+    case 4: return launch_back<DT, 4, FAST>(b, st);
+    case 8: return launch_back<DT, 8, FAST>(b, st);
+    default: return launch_back<DT, 16, FAST>(b, st);
   }
 }
 
@@ -574,9 +565,9 @@ hipError_t launch_selective_backward(const ScanCall& c, const ScanGrads& g, hipS
   b.part_skip = b.s.seg_step + parts.step;
   b.part_bias = b.part_skip + parts.step;
   b.part_bc = b.part_bias + parts.step;
-  const Reach how = scan_reach(b.s, c.type, c.n % scan_states(c.n) == 0);
-  if (c.type == RN_F32) return launch_how<RN_F32>(b, how, st);
-  return launch_how<RN_BF16>(b, how, st);
+  const bool fast = scan_fast(b.s, c.type, scan_states(c.n));
+  if (c.type == RN_F32) return fast ? launch_n<RN_F32, true>(b, st) : launch_n<RN_F32, false>(b, st);
+  return fast ? launch_n<RN_BF16, true>(b, st) : launch_n<RN_BF16, false>(b, st);
 }
 
 }  // namespace rn
