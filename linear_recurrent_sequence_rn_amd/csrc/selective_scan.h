@@ -55,6 +55,40 @@ __device__ __forceinline__ float sigmoidf(float v) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v * kLog2e));
 }
 
+template <int DT, class T>
+__device__ __forceinline__ float value_of(T x) {
+  if constexpr (DT == RN_F32) return x;
+  else return bf16_to_f32(x);
+}
+
+// A channel's n states (or decays), zeros behind them; by fours where they are whole fours on 16 bytes.
+template <int NS>
+__device__ __forceinline__ void load_states(const float* p, int n, bool fours, float* v) {
+  if (fours) {
+#pragma unroll
+    for (int i = 0; i < NS; i += 4) {
+      float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < n) q = *reinterpret_cast<const float4*>(p + i);
+      v[i] = q.x; v[i + 1] = q.y; v[i + 2] = q.z; v[i + 3] = q.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NS; ++i) v[i] = i < n ? p[i] : 0.f;
+  }
+}
+template <int NS>
+__device__ __forceinline__ void store_states(float* p, int n, bool fours, const float* v) {
+  if (fours) {
+#pragma unroll
+    for (int i = 0; i < NS; i += 4)
+      if (i < n) *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+      if (i < n) p[i] = v[i];
+  }
+}
+
 // The wave's first lane's value, as a scalar.
 __device__ __forceinline__ int64_t uniform64(int64_t x) {
   const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x));
@@ -83,6 +117,10 @@ struct Uniform<DT, NS, true> {
     for (int k = 0; k < kWords; ++k) u[k] = 0;
     if (have > 0) load(p, i, have);
   }
+  __device__ __forceinline__ void keep_if(bool yes) {
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) u[k] = yes ? u[k] : 0;
+  }
   __device__ __forceinline__ float value(int k) const {
     if constexpr (DT == RN_F32) return __uint_as_float(u[k]);
     else return __uint_as_float(k % 2 ? u[k / 2] & 0xffff0000u : u[k / 2] << 16);
@@ -96,6 +134,10 @@ struct Uniform<DT, NS, false> {
     for (int k = 0; k < NS; ++k) f[k] = k < have ? Elem<DT>::load(p, i + k) : 0.f;
   }
   __device__ __forceinline__ void load_or_zero(const void* p, int64_t i, int have) { load(p, i, have); }
+  __device__ __forceinline__ void keep_if(bool yes) {
+#pragma unroll
+    for (int k = 0; k < NS; ++k) f[k] = yes ? f[k] : 0.f;
+  }
   __device__ __forceinline__ float value(int k) const { return f[k]; }
 };
 

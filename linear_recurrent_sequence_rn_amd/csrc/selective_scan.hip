@@ -17,39 +17,6 @@ namespace {
 // workspace; or the state a segment adds on its own.
 enum ScanMode : int { kScanOut = 0, kScanState = 1 };
 
-template <int DT, class T>
-__device__ __forceinline__ float value_of(T x) {
-  if constexpr (DT == RN_F32) return x;
-  else return bf16_to_f32(x);
-}
-
-// A channel's n states (or decays), zeros behind them; by fours where they are whole fours on 16 bytes.
-template <int NS>
-__device__ __forceinline__ void load_states(const float* p, int n, bool fours, float* v) {
-  if (fours) {
-#pragma unroll
-    for (int i = 0; i < NS; i += 4) {
-      float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i < n) q = *reinterpret_cast<const float4*>(p + i);
-      v[i] = q.x; v[i + 1] = q.y; v[i + 2] = q.z; v[i + 3] = q.w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < NS; ++i) v[i] = i < n ? p[i] : 0.f;
-  }
-}
-template <int NS>
-__device__ __forceinline__ void store_states(float* p, int n, const float* v) {
-  if (n % 4 == 0) {
-#pragma unroll
-    for (int i = 0; i < NS; i += 4)
-      if (i < n) *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < NS; ++i)
-      if (i < n) p[i] = v[i];
-  }
-}
 
 // A wave takes 64 channels of a group, a lane each with all its states, and a piece of a sequence. Waves
 // meet nowhere. Tokens go in groups, the next group's values on their way.
@@ -197,11 +164,11 @@ __global__ void __launch_bounds__(256) scan_rows(ScanArgs a) {
   }
   if (!mine) return;
   if (MODE == kScanState) {
-    store_states<NS>(a.seg_state + (piece * a.D + d) * a.n, a.n, h);
+    store_states<NS>(a.seg_state + (piece * a.D + d) * a.n, a.n, a.n % 4 == 0, h);
     a.seg_step[piece * a.D + d] = total;
     return;
   }
-  if (p.piece == last && slot >= 0 && a.state_out) store_states<NS>(a.state_out + sb, a.n, h);
+  if (p.piece == last && slot >= 0 && a.state_out) store_states<NS>(a.state_out + sb, a.n, a.n % 4 == 0, h);
   if (a.zero_rest) {
     const int64_t rows = min(p.own - first, static_cast<int64_t>(a.q.len));
     for (int64_t t = max(nt, 0); t < rows; ++t, out += a.os[1]) Elem<DT>::store(out, d, 0.f);

@@ -41,10 +41,9 @@ struct BackArgs {
   float* part_bc;                         // [token rows][blocks along channels][2][n]
 };
 
-constexpr int kTile = 16;                 // tokens a tile of scan_edges: each wave prepares four
-constexpr int kEach = kTile / 4;
-// States a wave holds: a quarter of them, at least two.
-int scan_states(int n) { return n <= 8 ? 2 : n <= 16 ? 4 : n <= 32 ? 8 : 16; }
+constexpr int kPieceTile = 8, kPieceTiles = 4;   // scan_piece: tokens a tile, tiles a piece
+// States a wave of scan_main holds: a quarter of them.
+int scan_states(int n) { return n <= 32 ? 8 : 16; }
 constexpr int tile_of(int NS) { return 32 / NS; }
 constexpr int kTiles = 8;                 // tiles a piece
 
@@ -85,6 +84,57 @@ struct Place {
   __device__ __forceinline__ int64_t states(const ScanArgs& a, int64_t row) const { return (row * a.D + d) * a.n + n0; }
 };
 
+// What a wave works on that holds 64 channels, a lane each (lanes past the group's last channel repeat it).
+template <int DT>
+struct Lanes {
+  typedef typename std::conditional<DT == RN_F32, float, uint16_t>::type elem;
+  Span p;
+  int64_t piece, row0;
+  int first, nt, last, x, group;          // first token, tokens, the sequence's last piece
+  unsigned d;                             // channel
+  bool mine;
+  // A lane's values of a tensor, token after token.
+  struct Row {
+    const elem* p;
+    int64_t step;
+    unsigned off;
+    __device__ __forceinline__ elem at(int t) const {
+      return *reinterpret_cast<const elem*>(reinterpret_cast<const char*>(p + t * step) + off);
+    }
+    __device__ __forceinline__ elem take() {
+      const elem v = at(0);
+      p += step;
+      return v;
+    }
+    __device__ __forceinline__ void put(int t, float v) const {
+      Elem<DT>::store(reinterpret_cast<char*>(const_cast<elem*>(p + t * step)) + off, 0, v);
+    }
+  };
+  __device__ __forceinline__ bool find(const ScanArgs& a, int tile) {
+    piece = blockIdx.y + static_cast<int64_t>(blockIdx.z) * gridDim.y;
+    x = tile;
+    group = x / a.tiles;
+    const int each = a.D / a.G, left = each - (x - group * a.tiles) * 64, lane = threadIdx.x & 63;
+    mine = lane < left;
+    d = group * each + (each - left) + min(lane, left - 1);
+    if (!seq_place(a.q, piece, &p)) return false;
+    p.piece = __builtin_amdgcn_readfirstlane(p.piece);
+    row0 = uniform64(p.row0);
+    const int len = __builtin_amdgcn_readfirstlane(p.len);
+    first = p.piece * a.q.len;
+    last = len > 0 ? (len - 1) / a.q.len : 0;
+    nt = min(len - first, a.q.len);
+    return true;
+  }
+  __device__ __forceinline__ Row row(const ScanArgs& a, const void* t, const int64_t* st) const {
+    return Row{static_cast<const elem*>(t) + (a.q.T > 0 ? row0 * st[1] : p.s * st[0]) + static_cast<int64_t>(first) * st[1], st[1],
+               static_cast<unsigned>(d * sizeof(elem))};
+  }
+  __device__ __forceinline__ const elem* heads(const ScanArgs& a, const void* t, const int64_t* st) const {
+    return static_cast<const elem*>(t) + (a.q.T > 0 ? row0 * st[2] : p.s * st[0]) + group * st[1] + static_cast<int64_t>(first) * st[2];
+  }
+};
+
 // Values of a token and channel that the scan needs.
 struct Inputs {
   float x, dt, z, dout;
@@ -104,71 +154,97 @@ __device__ __forceinline__ float step_of(const ScanArgs& a, float v) { return a.
 
 // ---- the edges of a piece -------------------------------------------------------------------
 // Forward over the piece: the state h it adds, and with P_t = a_1 .. a_t the gradient sum_t P_t C_t dy_t
-// that it passes back.
+// that it passes back. A wave takes 64 channels, a lane each, and up to 16 of their states; waves meet
+// nowhere.
 template <int DT, int NS, bool FAST>
 __global__ void __launch_bounds__(256) scan_edges(BackArgs b) {
-  __shared__ float4 tile[kTile][64];      // D, u, dy
+  constexpr int kGroup = FAST ? 4 : 2;
   const ScanArgs& a = b.s;
-  Place<NS> w;
-  if (!w.find(a) || w.p.s >= a.q.S || w.last == 0 || w.p.piece > w.last) return;
-  const int nt = w.nt;
-  const int64_t xb = w.tokens(a, a.xs), dtb = w.tokens(a, a.dts), zb = w.tokens(a, a.zs), ob = w.tokens(a, a.os);
-  const int64_t bb = w.groups(a, a.bs) + w.n0, cb = w.groups(a, a.cs) + w.n0;
+  const int sets = (a.n + NS - 1) / NS;
+  const int wave = blockIdx.x * (blockDim.x >> 6) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  Lanes<DT> w;
+  if (wave >= a.tiles * a.G * sets || !w.find(a, wave / sets) || w.p.s >= a.q.S || w.last == 0 || w.p.piece > w.last) return;
+  const int n0 = (wave % sets) * NS, have = a.n - n0, nt = w.nt;
   float A2[NS], h[NS], P[NS], e[NS];
+  load_states<NS>(a.A + static_cast<int64_t>(w.d) * a.n + n0, have, a.a4, A2);
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
-    A2[i] = w.mine && i < w.have ? in_log2(a.A[static_cast<int64_t>(w.d) * a.n + w.n0 + i]) : 0.f;
+    A2[i] = in_log2(A2[i]);
     h[i] = e[i] = 0.f;
     P[i] = 1.f;
   }
-  const float bias = w.mine && a.bias ? a.bias[w.d] : 0.f;
+  const float bias = a.bias ? a.bias[w.d] : 0.f;
   float total = 0.f;
-  Inputs in[kEach];
-  auto fetch = [&](int t0) {
+  typename Lanes<DT>::Row x = w.row(a, a.x, a.xs), dt = w.row(a, a.dt, a.dts), dout = w.row(a, b.dout, a.os),
+                          z = w.row(a, a.z ? a.z : a.x, a.z ? a.zs : a.xs);
+  typename Lanes<DT>::elem nx[kGroup], ndt[kGroup], ndo[kGroup], nz[kGroup] = {};
+  auto fetch = [&]() {
 #pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-      const int t = t0 + w.wave * kEach + k;
-      in[k] = fetch_inputs<DT>(b, w.mine && t < nt, xb + t * a.xs[1], dtb + t * a.dts[1], zb + t * a.zs[1], ob + t * a.os[1]);
+    for (int k = 0; k < kGroup; ++k) {
+      nx[k] = x.take();
+      ndt[k] = dt.take();
+      ndo[k] = dout.take();
+    }
+    if (a.z) {
+#pragma unroll
+      for (int k = 0; k < kGroup; ++k) nz[k] = z.take();
     }
   };
-  fetch(0);
-  for (int t0 = 0; t0 < nt; t0 += kTile) {
+  const typename Lanes<DT>::elem* pb = w.heads(a, a.b, a.bs) + n0;
+  const typename Lanes<DT>::elem* pc = w.heads(a, a.c, a.cs) + n0;
+  Uniform<DT, NS, FAST> nb, nc;
+  nb.load(pb, 0, have);
+  nc.load(pc, 0, have);
+  auto token = [&](int t, float s, float u, float dy) {
+    const Uniform<DT, NS, FAST> B = nb, C = nc;
+    if (t + 1 < nt) { pb += a.bs[2]; pc += a.cs[2]; }      // (behind the last token it is read again)
+    nb.load(pb, 0, have);
+    nc.load(pc, 0, have);
+    total += s;
 #pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-      const int t = w.wave * kEach + k;
-      const float s = step_of(a, in[k].dt + bias);
-      tile[t][w.lane] = make_float4(s, s * in[k].x, a.z ? in[k].dout * in[k].z * sigmoidf(in[k].z) : in[k].dout, 0.f);
+    for (int i = 0; i < NS; ++i) {
+      const float d = __builtin_amdgcn_exp2f(s * A2[i]);
+      h[i] = fmaf(d, h[i], u * B.value(i));
+      P[i] *= d;
+      e[i] = fmaf(P[i], C.value(i) * dy, e[i]);
     }
-    if (t0 + kTile < nt) fetch(t0 + kTile);
-    __syncthreads();
-    if (w.have > 0) {
-      const int n = min(kTile, nt - t0);
-#pragma unroll 4
-      for (int t = 0; t < n; ++t) {
-        Uniform<DT, NS, FAST> B, C;
-        B.load(a.b, bb + (t0 + t) * a.bs[2], w.have);
-        C.load(a.c, cb + (t0 + t) * a.cs[2], w.have);
-        const float4 v = tile[t][w.lane];
-        total += v.x;
+  };
+  auto gate = [](float v) { return v * sigmoidf(v); };
+  const int groups = nt / kGroup;
+  if (groups > 0) fetch();
+  for (int g = 0; g < groups; ++g) {
+    float s[kGroup], u[kGroup], dy[kGroup], zv[kGroup];
 #pragma unroll
-        for (int i = 0; i < NS; ++i) {
-          const float d = __builtin_amdgcn_exp2f(v.x * A2[i]);
-          h[i] = fmaf(d, h[i], v.y * B.value(i));
-          P[i] *= d;
-          e[i] = fmaf(P[i], C.value(i) * v.z, e[i]);
-        }
-      }
+    for (int k = 0; k < kGroup; ++k) {
+      u[k] = value_of<DT>(nx[k]);
+      s[k] = value_of<DT>(ndt[k]) + bias;
+      dy[k] = value_of<DT>(ndo[k]);
+      zv[k] = value_of<DT>(nz[k]);
     }
-    __syncthreads();
+    if (g + 1 < groups) fetch();
+    if (a.softplus) {
+#pragma unroll
+      for (int k = 0; k < kGroup; ++k) s[k] = softplus(s[k]);
+    }
+    if (a.z) {
+#pragma unroll
+      for (int k = 0; k < kGroup; ++k) dy[k] *= gate(zv[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kGroup; ++k) token(g * kGroup + k, s[k], s[k] * u[k], dy[k]);
+  }
+  for (int t = groups * kGroup; t < nt; ++t) {     // fewer than a group
+    const float xv = value_of<DT>(x.take());
+    const float s = step_of(a, value_of<DT>(dt.take()) + bias);
+    float dy = value_of<DT>(dout.take());
+    if (a.z) dy *= gate(value_of<DT>(z.take()));
+    token(t, s, s * xv, dy);
   }
   if (!w.mine) return;
-#pragma unroll
-  for (int i = 0; i < NS; ++i)
-    if (i < w.have) {
-      a.seg_state[w.states(a, w.piece) + i] = h[i];
-      b.seg_grad[w.states(a, w.piece) + i] = e[i];
-    }
-  if (w.wave == 0) a.seg_step[w.piece * a.D + w.d] = total;
+  const int64_t to = (w.piece * a.D + w.d) * a.n + n0;
+  store_states<NS>(a.seg_state + to, have, a.n % 4 == 0, h);
+  store_states<NS>(b.seg_grad + to, have, a.n % 4 == 0, e);
+  if (n0 == 0) a.seg_step[w.piece * a.D + w.d] = total;
 }
 
 // Along the pieces of sequence blockIdx.y, a thread a state: forward (blockIdx.z = 0), seg_state becomes
@@ -445,6 +521,211 @@ __global__ void __launch_bounds__(256) scan_main(BackArgs b) {
   }
 }
 
+// Up to 16 states: a wave takes 64 channels, a lane each, and meets no other. A tile's states go four at a
+// time: their decays and states over the tile's 8 tokens are in registers, and a lane sums over all of
+// them what its channel needs.
+template <int DT, int SETS, bool FAST>
+__global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
+  constexpr int TT = kPieceTile, NS = 4 * SETS;
+  // The state at the start of tiles 1 and on; a tile's is read once, and then replaced by the gradient that
+  // reaches the tile before.
+  __shared__ float starts[kPieceTiles - 1][NS][64];
+  __shared__ float own[NS][64];                       // dA of the piece
+  const ScanArgs& a = b.s;
+  Lanes<DT> w;
+  const bool found = w.find(a, blockIdx.x);
+  if (w.piece >= seq_pieces(a.q)) return;          // (the grid's last row may have more blocks than pieces)
+  const int lane = threadIdx.x, n = a.n;
+  const bool real = found && w.p.s < a.q.S, fours = n % 4 == 0;
+  const int nt = real ? max(w.nt, 0) : 0;
+  const int64_t sb = (static_cast<int64_t>(w.p.s) * a.D + w.d) * n, wb = (w.piece * a.D + w.d) * n;
+  float dskip = 0.f, dbias = 0.f;
+#pragma unroll
+  for (int i = 0; i < NS; ++i) own[i][lane] = 0.f;
+  const float* from = nullptr;                     // the starting state
+  const float* grad = nullptr;                     // and the gradient that reaches the piece from behind
+  if (real && w.p.piece <= w.last) {
+    const bool ends = w.p.piece == w.last;         // the sequence's last piece, if it is empty too
+    grad = !ends ? b.seg_grad + wb + static_cast<int64_t>(a.D) * n : b.dstate_out ? b.dstate_out + sb : nullptr;
+    from = w.p.piece > 0 ? a.seg_state + wb : a.state_in ? a.state_in + sb : nullptr;
+  }
+  float* const passed = real && w.p.piece == 0 && w.mine && b.dstate_in ? b.dstate_in + sb : nullptr;
+  if (passed && nt == 0) {                         // a sequence without tokens
+    float e[NS];
+#pragma unroll
+    for (int i = 0; i < NS; ++i) e[i] = 0.f;
+    if (grad) load_states<NS>(grad, n, fours, e);
+    store_states<NS>(passed, n, fours, e);
+  }
+  if (nt > 0) {
+    const float skip = a.skip ? a.skip[w.d] : 0.f, bias = a.bias ? a.bias[w.d] : 0.f;
+    const typename Lanes<DT>::elem* pb = w.heads(a, a.b, a.bs);
+    const typename Lanes<DT>::elem* pc = w.heads(a, a.c, a.cs);
+    const auto x = w.row(a, a.x, a.xs), dt = w.row(a, a.dt, a.dts), dout = w.row(a, b.dout, a.os),
+               z = w.row(a, a.z ? a.z : a.x, a.z ? a.zs : a.xs);
+    const int tiles = (nt + TT - 1) / TT;
+    const float* const A = a.A + static_cast<int64_t>(w.d) * n;
+    // ---- forward: the states at the tiles' starts
+    if (tiles > 1) {
+      float A2[NS], h[NS];
+      load_states<NS>(A, n, a.a4, A2);
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        A2[i] = in_log2(A2[i]);
+        h[i] = 0.f;
+      }
+      if (from) load_states<NS>(from, n, fours, h);
+      for (int q = 0; q < tiles - 1; ++q) {
+        float s[TT], u[TT];
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          u[t] = value_of<DT>(x.at(q * TT + t));
+          s[t] = value_of<DT>(dt.at(q * TT + t)) + bias;
+        }
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          if (a.softplus) s[t] = softplus(s[t]);
+          u[t] *= s[t];
+        }
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          Uniform<DT, NS, FAST> B;
+          B.load(pb, (q * TT + t) * a.bs[2], n);
+#pragma unroll
+          for (int i = 0; i < NS; ++i) h[i] = fmaf(__builtin_amdgcn_exp2f(s[t] * A2[i]), h[i], u[t] * B.value(i));
+        }
+#pragma unroll
+        for (int i = 0; i < NS; ++i) starts[q][i][lane] = h[i];
+      }
+    }
+    // ---- backward, tile by tile
+    const auto dx = w.row(a, b.dx, b.dxs), ddt = w.row(a, b.ddt, b.ddts), dz = w.row(a, a.z ? b.dz : b.dx, a.z ? b.dzs : b.dxs);
+    const int64_t row = (a.q.T > 0 ? w.row0 : static_cast<int64_t>(w.p.s) * a.q.N) + w.first;
+    const int64_t bc_step = static_cast<int64_t>(a.tiles) * a.G * 2 * n;
+    for (int q = tiles - 1; q >= 0; --q) {
+      const int t0 = q * TT, count = min(nt - t0, TT);
+      float s[TT], u[TT], dy[TT], du[TT], ws[TT], y[TT];
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        const int at = t0 + min(t, count - 1);
+        u[t] = value_of<DT>(x.at(at));
+        s[t] = value_of<DT>(dt.at(at)) + bias;
+        dy[t] = value_of<DT>(dout.at(at));
+        y[t] = value_of<DT>(z.at(at));
+      }
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        const bool there = w.mine && t < count;    // tokens behind the last one, and lanes past the channels: zeros
+        if (a.softplus) s[t] = softplus(s[t]);
+        if (a.z) dy[t] *= y[t] * sigmoidf(y[t]);
+        u[t] = there ? s[t] * u[t] : 0.f;
+        s[t] = there ? s[t] : 0.f;
+        dy[t] = there ? dy[t] : 0.f;
+        du[t] = ws[t] = y[t] = 0.f;
+      }
+#pragma unroll 1
+      for (int c = 0; c < NS; c += 4) {
+        float A2[4], h[4], e[4], dec[TT][4], p[TT][4], sums[64];
+        Uniform<DT, 4, FAST> B[TT], C[TT];
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          const int64_t at = t0 + min(t, count - 1);
+          B[t].load(pb, at * a.bs[2] + c, n - c);
+          C[t].load(pc, at * a.cs[2] + c, n - c);
+          B[t].keep_if(t < count);
+          C[t].keep_if(t < count);
+        }
+        load_states<4>(A + c, n - c, a.a4, A2);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          A2[i] = in_log2(A2[i]);
+          h[i] = e[i] = 0.f;
+        }
+        if (q == tiles - 1) {
+          if (grad) load_states<4>(grad + c, n - c, fours, e);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) e[i] = starts[q][c + i][lane];
+        }
+        if (q == 0) {
+          if (from) load_states<4>(from + c, n - c, fours, h);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) h[i] = starts[q - 1][c + i][lane];
+        }
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            dec[t][i] = __builtin_amdgcn_exp2f(s[t] * A2[i]);
+            p[t][i] = dec[t][i] * h[i];
+            h[i] = fmaf(u[t], B[t].value(i), p[t][i]);
+            y[t] = fmaf(C[t].value(i), h[i], y[t]);
+            sums[32 + t * 4 + i] = dy[t] * h[i];
+          }
+        }
+        float dA[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int t = TT - 1; t >= 0; --t) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float g = fmaf(C[t].value(i), dy[t], e[i]);
+            sums[t * 4 + i] = g * u[t];
+            du[t] = fmaf(g, B[t].value(i), du[t]);
+            const float wp = g * p[t][i];
+            ws[t] = fmaf(wp, A2[i], ws[t]);
+            dA[i] = fmaf(wp, s[t], dA[i]);
+            e[i] = dec[t][i] * g;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          own[c + i][lane] += dA[i];
+          if (q > 0) starts[q - 1][c + i][lane] = e[i];
+        }
+        if (q == 0 && passed) store_states<4>(passed + c, n - c, fours, e);
+        const float total = sums64(sums, lane);
+        const int r = lane & 31, t = r / 4, i = c + r % 4;
+        if (t < count && i < n) b.part_bc[(row + t0 + t) * bc_step + w.x * 2 * n + (lane >> 5) * n + i] = total;
+      }
+      if (w.mine) {
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+          if (t < count) {
+            const float xv = value_of<DT>(x.at(t0 + t));
+            if (a.z) {
+              const float zv = value_of<DT>(z.at(t0 + t)), sg = sigmoidf(zv);
+              dz.put(t0 + t, value_of<DT>(dout.at(t0 + t)) * fmaf(skip, xv, y[t]) * sg * fmaf(zv, 1.0f - sg, 1.0f));
+            }
+            float g = fmaf(du[t], xv, ws[t] * 0.69314718f);
+            if (a.softplus) g *= sigmoidf(value_of<DT>(dt.at(t0 + t)) + bias);
+            dx.put(t0 + t, fmaf(du[t], s[t], skip * dy[t]));
+            ddt.put(t0 + t, g);
+            dskip = fmaf(dy[t], xv, dskip);
+            dbias += g;
+          }
+      }
+    }
+  }
+  if (!w.mine) return;
+  // the piece's own sums (zeros of a piece without tokens), where its starting state was
+  float dA[NS];
+#pragma unroll
+  for (int i = 0; i < NS; ++i) dA[i] = own[i][lane];
+  store_states<NS>(a.seg_state + wb, n, fours, dA);
+  b.part_skip[w.piece * a.D + w.d] = dskip;
+  b.part_bias[w.piece * a.D + w.d] = dbias;
+  if (a.zero_rest && found) {
+    const auto dx = w.row(a, b.dx, b.dxs), ddt = w.row(a, b.ddt, b.ddts), dz = w.row(a, a.z ? b.dz : b.dx, a.z ? b.dzs : b.dxs);
+    const int rows = static_cast<int>(min(w.p.own - w.first, static_cast<int64_t>(a.q.len)));
+    for (int t = nt; t < rows; ++t) {
+      dx.put(t, 0.f);
+      ddt.put(t, 0.f);
+      if (a.z) dz.put(t, 0.f);
+    }
+  }
+}
+
 // ---- sums over blocks -----------------------------------------------------------------------
 
 // dB and dC of a piece's tokens: the blocks along the channels of a group, in their order.
@@ -503,33 +784,53 @@ __global__ void __launch_bounds__(1024) scan_sum_pieces(BackArgs b, int64_t piec
   }
 }
 
-template <int DT, int NS, bool FAST>
+template <int DT, int NS>
+hipError_t launch_edges(const BackArgs& b, hipStream_t st) {
+  const ScanArgs& a = b.s;
+  const int64_t x = static_cast<int64_t>(a.tiles) * a.G * ((a.n + NS - 1) / NS);
+  const int waves = static_cast<int>(std::min<int64_t>(x, 4));
+  const dim3 grid = seq_grid(a.q, (x + waves - 1) / waves), block(64 * waves);
+  if (scan_fast(a, DT, NS)) hipLaunchKernelGGL((scan_edges<DT, NS, true>), grid, block, 0, st, b);
+  else hipLaunchKernelGGL((scan_edges<DT, NS, false>), grid, block, 0, st, b);
+  return hipGetLastError();
+}
+template <int DT, int SETS>
+hipError_t launch_piece(const BackArgs& b, hipStream_t st) {
+  const dim3 grid = seq_grid(b.s.q, static_cast<int64_t>(b.s.tiles) * b.s.G);
+  if (scan_fast(b.s, DT, 4 * SETS)) hipLaunchKernelGGL((scan_piece<DT, SETS, true>), grid, dim3(64), 0, st, b);
+  else hipLaunchKernelGGL((scan_piece<DT, SETS, false>), grid, dim3(64), 0, st, b);
+  return hipGetLastError();
+}
+template <int DT, int NS>
+hipError_t launch_main(const BackArgs& b, hipStream_t st) {
+  const dim3 grid = seq_grid(b.s.q, static_cast<int64_t>(b.s.tiles) * b.s.G);
+  if (scan_fast(b.s, DT, NS)) hipLaunchKernelGGL((scan_main<DT, NS, true>), grid, dim3(256), 0, st, b);
+  else hipLaunchKernelGGL((scan_main<DT, NS, false>), grid, dim3(256), 0, st, b);
+  return hipGetLastError();
+}
+template <int DT>
 hipError_t launch_back(const BackArgs& b, hipStream_t st) {
   const ScanArgs& a = b.s;
-  const int64_t x = static_cast<int64_t>(a.tiles) * a.G, all = static_cast<int64_t>(a.D) * a.n;
-  const dim3 grid = seq_grid(a.q, x);
+  const int64_t all = static_cast<int64_t>(a.D) * a.n;
   hipError_t e;
   if (a.q.N > a.q.len) {
-    hipLaunchKernelGGL((scan_edges<DT, NS, FAST>), grid, dim3(256), 0, st, b);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    e = a.n <= 4 ? launch_edges<DT, 4>(b, st) : a.n <= 8 ? launch_edges<DT, 8>(b, st) : a.n % 12 == 0 ? launch_edges<DT, 12>(b, st)
+                                                                                      : launch_edges<DT, 16>(b, st);
+    if (e != hipSuccess) return e;
     hipLaunchKernelGGL(scan_edges_carry, dim3(static_cast<unsigned>((all + 255) / 256), a.q.S, 2), dim3(256), 0, st, b);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((scan_main<DT, NS, FAST>), grid, dim3(256), 0, st, b);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
+  e = a.n <= 4    ? launch_piece<DT, 1>(b, st)
+      : a.n <= 8  ? launch_piece<DT, 2>(b, st)
+      : a.n <= 12 ? launch_piece<DT, 3>(b, st)
+      : a.n <= 16 ? launch_piece<DT, 4>(b, st)
+      : a.n <= 32 ? launch_main<DT, 8>(b, st)
+                  : launch_main<DT, 16>(b, st);
+  if (e != hipSuccess) return e;
   hipLaunchKernelGGL((scan_sum_tokens<DT>), seq_grid(a.q, 1), dim3(256), 0, st, b);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   hipLaunchKernelGGL(scan_sum_pieces, dim3(static_cast<unsigned>((all + 2 * a.D + 31) / 32)), dim3(1024), 0, st, b, seq_pieces(a.q));
   return hipGetLastError();
-}
-template <int DT, bool FAST>
-hipError_t launch_n(const BackArgs& b, hipStream_t st) {
-  switch (scan_states(b.s.n)) {
-    case 2: return launch_back<DT, 2, FAST>(b, st);
-    case 4: return launch_back<DT, 4, FAST>(b, st);
-    case 8: return launch_back<DT, 8, FAST>(b, st);
-    default: return launch_back<DT, 16, FAST>(b, st);
-  }
 }
 
 // Floats of each part of the workspace.
@@ -544,7 +845,9 @@ struct Parts {
   }
   size_t all() const { return 2 * state + 3 * step + bc; }
 };
-ScanArgs pieces_of(const ScanCall& c) { return scan_args(c, kTiles * tile_of(scan_states(c.n))); }
+ScanArgs pieces_of(const ScanCall& c) {
+  return scan_args(c, c.n <= 16 ? kPieceTile * kPieceTiles : kTiles * tile_of(scan_states(c.n)));
+}
 
 }  // namespace
 
@@ -565,9 +868,7 @@ hipError_t launch_selective_backward(const ScanCall& c, const ScanGrads& g, hipS
   b.part_skip = b.s.seg_step + parts.step;
   b.part_bias = b.part_skip + parts.step;
   b.part_bc = b.part_bias + parts.step;
-  const bool fast = scan_fast(b.s, c.type, scan_states(c.n));
-  if (c.type == RN_F32) return fast ? launch_n<RN_F32, true>(b, st) : launch_n<RN_F32, false>(b, st);
-  return fast ? launch_n<RN_BF16, true>(b, st) : launch_n<RN_BF16, false>(b, st);
+  return c.type == RN_F32 ? launch_back<RN_F32>(b, st) : launch_back<RN_BF16>(b, st);
 }
 
 }  // namespace rn
