@@ -91,7 +91,7 @@ struct Lanes {
   Span p;
   int64_t piece, row0;
   int first, nt, last, x, group;          // first token, tokens, the sequence's last piece
-  unsigned d;                             // channel
+  unsigned d, c0;                         // channel, the wave's first one
   bool mine;
   // A lane's values of a tensor, token after token.
   struct Row {
@@ -106,6 +106,31 @@ struct Lanes {
       p += step;
       return v;
     }
+    // N tokens from t0 on; those from `count` (>= 1) on repeat the last one, or are not stored
+    template <int N>
+    __device__ __forceinline__ void load(int t0, int count, float (&v)[N]) const {
+      const elem* r = p + t0 * step;
+      elem raw[N];
+#pragma unroll
+      for (int t = 0; t < N; ++t) {
+        raw[t] = *reinterpret_cast<const elem*>(reinterpret_cast<const char*>(r) + off);
+        if (t + 1 < count) r += step;
+      }
+#pragma unroll
+      for (int t = 0; t < N; ++t) v[t] = value_of<DT>(raw[t]);
+    }
+    template <int N>
+    __device__ __forceinline__ void store(int t0, int count, const float (&v)[N]) const {
+      elem* r = const_cast<elem*>(p + t0 * step);
+      if (count >= N) {
+#pragma unroll
+        for (int t = 0; t < N; ++t, r += step) Elem<DT>::store(reinterpret_cast<char*>(r) + off, 0, v[t]);
+      } else {
+#pragma unroll
+        for (int t = 0; t < N; ++t, r += step)
+          if (t < count) Elem<DT>::store(reinterpret_cast<char*>(r) + off, 0, v[t]);
+      }
+    }
     __device__ __forceinline__ void put(int t, float v) const {
       Elem<DT>::store(reinterpret_cast<char*>(const_cast<elem*>(p + t * step)) + off, 0, v);
     }
@@ -116,7 +141,8 @@ struct Lanes {
     group = x / a.tiles;
     const int each = a.D / a.G, left = each - (x - group * a.tiles) * 64, lane = threadIdx.x & 63;
     mine = lane < left;
-    d = group * each + (each - left) + min(lane, left - 1);
+    c0 = group * each + (each - left);
+    d = c0 + min(lane, left - 1);
     if (!seq_place(a.q, piece, &p)) return false;
     p.piece = __builtin_amdgcn_readfirstlane(p.piece);
     row0 = uniform64(p.row0);
@@ -315,6 +341,26 @@ __device__ __forceinline__ float sums64(float (&v)[64], int lane) {
 #pragma unroll
   for (int k = 0; k < 2; ++k) v[k] = fold<0x4E>(v[k], v[k + 2], lane & 2);       // lane ^ 2
   return fold<0xB1>(v[0], v[1], lane & 1);                                       // lane ^ 1
+}
+
+// Sums of 32 values over the wave's 64 lanes: lane l receives that of v[l / 2].
+__device__ __forceinline__ float sums32(float (&v)[32], int lane) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[k]), __float_as_uint(v[k + 16]), false, false);
+    v[k] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[k]), __float_as_uint(v[k + 8]), false, false);
+    v[k] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = fold<0x128>(v[k], v[k + 4], lane & 8);      // lane ^ 8
+#pragma unroll
+  for (int k = 0; k < 2; ++k) v[k] = fold<0x141>(v[k], v[k + 2], lane & 4);      // lane ^ 7
+  v[0] = fold<0x4E>(v[0], v[1], lane & 2);                                       // lane ^ 2
+  return v[0] + dpp_move<0xB1>(v[0]);                                            // lane ^ 1
 }
 
 template <int DT, int NS, bool FAST>
@@ -559,10 +605,19 @@ __global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
   }
   if (nt > 0) {
     const float skip = a.skip ? a.skip[w.d] : 0.f, bias = a.bias ? a.bias[w.d] : 0.f;
-    const typename Lanes<DT>::elem* pb = w.heads(a, a.b, a.bs);
-    const typename Lanes<DT>::elem* pc = w.heads(a, a.c, a.cs);
+    typedef typename Lanes<DT>::elem elem;
+    const elem* pb = w.heads(a, a.b, a.bs);
+    const elem* pc = w.heads(a, a.c, a.cs);
     const auto x = w.row(a, a.x, a.xs), dt = w.row(a, a.dt, a.dts), dout = w.row(a, b.dout, a.os),
                z = w.row(a, a.z ? a.z : a.x, a.z ? a.zs : a.xs);
+    // every row of the piece is asked for at once, a lane a row, so that the loads below find it in a cache
+    elem asked[2];
+    {
+      const int64_t t = min(lane & 31, nt - 1);
+      const unsigned half = lane >> 5;
+      asked[0] = half ? x.p[t * x.step + w.c0] : dt.p[t * dt.step + w.c0];
+      asked[1] = half ? dout.p[t * dout.step + w.c0] : z.p[t * z.step + w.c0];
+    }
     const int tiles = (nt + TT - 1) / TT;
     const float* const A = a.A + static_cast<int64_t>(w.d) * n;
     // ---- forward: the states at the tiles' starts
@@ -577,16 +632,16 @@ __global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
       if (from) load_states<NS>(from, n, fours, h);
       for (int q = 0; q < tiles - 1; ++q) {
         float s[TT], u[TT];
+        x.load(q * TT, TT, u);
+        dt.load(q * TT, TT, s);
 #pragma unroll
-        for (int t = 0; t < TT; ++t) {
-          u[t] = value_of<DT>(x.at(q * TT + t));
-          s[t] = value_of<DT>(dt.at(q * TT + t)) + bias;
+        for (int t = 0; t < TT; ++t) s[t] += bias;
+        if (a.softplus) {
+#pragma unroll
+          for (int t = 0; t < TT; ++t) s[t] = softplus(s[t]);
         }
 #pragma unroll
-        for (int t = 0; t < TT; ++t) {
-          if (a.softplus) s[t] = softplus(s[t]);
-          u[t] *= s[t];
-        }
+        for (int t = 0; t < TT; ++t) u[t] *= s[t];
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
           Uniform<DT, NS, FAST> B;
@@ -598,26 +653,32 @@ __global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
         for (int i = 0; i < NS; ++i) starts[q][i][lane] = h[i];
       }
     }
+    asm volatile("" ::"v"(asked[0]), "v"(asked[1]));
     // ---- backward, tile by tile
-    const auto dx = w.row(a, b.dx, b.dxs), ddt = w.row(a, b.ddt, b.ddts), dz = w.row(a, a.z ? b.dz : b.dx, a.z ? b.dzs : b.dxs);
-    const int64_t row = (a.q.T > 0 ? w.row0 : static_cast<int64_t>(w.p.s) * a.q.N) + w.first;
+    auto dx = w.row(a, b.dx, b.dxs), ddt = w.row(a, b.ddt, b.ddts), dz = w.row(a, a.z ? b.dz : b.dx, a.z ? b.dzs : b.dxs);
     const int64_t bc_step = static_cast<int64_t>(a.tiles) * a.G * 2 * n;
+    float* bc = b.part_bc + ((a.q.T > 0 ? w.row0 : static_cast<int64_t>(w.p.s) * a.q.N) + w.first) * bc_step +
+                w.x * 2 * n + (lane & 1) * n;
     for (int q = tiles - 1; q >= 0; --q) {
       const int t0 = q * TT, count = min(nt - t0, TT);
       float s[TT], u[TT], dy[TT], du[TT], ws[TT], y[TT];
+      x.load(t0, count, u);
+      dt.load(t0, count, s);
+      dout.load(t0, count, dy);
+      if (a.z) {
+        z.load(t0, count, y);
 #pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        const int at = t0 + min(t, count - 1);
-        u[t] = value_of<DT>(x.at(at));
-        s[t] = value_of<DT>(dt.at(at)) + bias;
-        dy[t] = value_of<DT>(dout.at(at));
-        y[t] = value_of<DT>(z.at(at));
+        for (int t = 0; t < TT; ++t) dy[t] *= y[t] * sigmoidf(y[t]);
+      }
+#pragma unroll
+      for (int t = 0; t < TT; ++t) s[t] += bias;
+      if (a.softplus) {
+#pragma unroll
+        for (int t = 0; t < TT; ++t) s[t] = softplus(s[t]);
       }
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
         const bool there = w.mine && t < count;    // tokens behind the last one, and lanes past the channels: zeros
-        if (a.softplus) s[t] = softplus(s[t]);
-        if (a.z) dy[t] *= y[t] * sigmoidf(y[t]);
         u[t] = there ? s[t] * u[t] : 0.f;
         s[t] = there ? s[t] : 0.f;
         dy[t] = there ? dy[t] : 0.f;
@@ -625,15 +686,17 @@ __global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
       }
 #pragma unroll 1
       for (int c = 0; c < NS; c += 4) {
-        float A2[4], h[4], e[4], dec[TT][4], p[TT][4], sums[64];
+        float A2[4], h[4], e[4], dec[TT][4], p[TT][4], sums[32];
         Uniform<DT, 4, FAST> B[TT], C[TT];
+        {
+          const elem* rb = pb + t0 * a.bs[2] + c;
+          const elem* rc = pc + t0 * a.cs[2] + c;
 #pragma unroll
-        for (int t = 0; t < TT; ++t) {
-          const int64_t at = t0 + min(t, count - 1);
-          B[t].load(pb, at * a.bs[2] + c, n - c);
-          C[t].load(pc, at * a.cs[2] + c, n - c);
-          B[t].keep_if(t < count);
-          C[t].keep_if(t < count);
+          for (int t = 0; t < TT; ++t) {
+            B[t].load(rb, 0, n - c);
+            C[t].load(rc, 0, n - c);
+            if (t + 1 < count) { rb += a.bs[2]; rc += a.cs[2]; }
+          }
         }
         load_states<4>(A + c, n - c, a.a4, A2);
 #pragma unroll
@@ -653,6 +716,13 @@ __global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) h[i] = starts[q - 1][c + i][lane];
         }
+        if (count < TT) {
+#pragma unroll
+          for (int t = 0; t < TT; ++t) {
+            B[t].keep_if(t < count);
+            C[t].keep_if(t < count);
+          }
+        }
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
 #pragma unroll
@@ -661,9 +731,10 @@ __global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
             p[t][i] = dec[t][i] * h[i];
             h[i] = fmaf(u[t], B[t].value(i), p[t][i]);
             y[t] = fmaf(C[t].value(i), h[i], y[t]);
-            sums[32 + t * 4 + i] = dy[t] * h[i];
+            sums[t * 4 + i] = dy[t] * h[i];
           }
         }
+        const float sum_c = sums32(sums, lane);
         float dA[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int t = TT - 1; t >= 0; --t) {
@@ -684,26 +755,36 @@ __global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
           if (q > 0) starts[q - 1][c + i][lane] = e[i];
         }
         if (q == 0 && passed) store_states<4>(passed + c, n - c, fours, e);
-        const float total = sums64(sums, lane);
-        const int r = lane & 31, t = r / 4, i = c + r % 4;
-        if (t < count && i < n) b.part_bc[(row + t0 + t) * bc_step + w.x * 2 * n + (lane >> 5) * n + i] = total;
+        const float sum_b = sums32(sums, lane);
+        const int t = lane >> 3, i = c + (lane >> 1 & 3);
+        if (t < count && i < n) bc[(t0 + t) * bc_step + i] = lane & 1 ? sum_c : sum_b;
+      }
+      // what belongs to a channel and token
+      float xv[TT], g[TT];
+      x.load(t0, count, xv);
+      dt.load(t0, count, g);
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        const float slope = a.softplus ? sigmoidf(g[t] + bias) : 1.f;
+        g[t] = fmaf(du[t], xv[t], ws[t] * 0.69314718f) * slope;
+        du[t] = fmaf(du[t], s[t], skip * dy[t]);
+        dskip = fmaf(dy[t], xv[t], dskip);
+        if (t < count) dbias += g[t];
+        y[t] = fmaf(skip, xv[t], y[t]);
       }
       if (w.mine) {
+        dx.store(t0, count, du);
+        ddt.store(t0, count, g);
+      }
+      if (a.z) {
+        dout.load(t0, count, g);
+        z.load(t0, count, xv);
 #pragma unroll
-        for (int t = 0; t < TT; ++t)
-          if (t < count) {
-            const float xv = value_of<DT>(x.at(t0 + t));
-            if (a.z) {
-              const float zv = value_of<DT>(z.at(t0 + t)), sg = sigmoidf(zv);
-              dz.put(t0 + t, value_of<DT>(dout.at(t0 + t)) * fmaf(skip, xv, y[t]) * sg * fmaf(zv, 1.0f - sg, 1.0f));
-            }
-            float g = fmaf(du[t], xv, ws[t] * 0.69314718f);
-            if (a.softplus) g *= sigmoidf(value_of<DT>(dt.at(t0 + t)) + bias);
-            dx.put(t0 + t, fmaf(du[t], s[t], skip * dy[t]));
-            ddt.put(t0 + t, g);
-            dskip = fmaf(dy[t], xv, dskip);
-            dbias += g;
-          }
+        for (int t = 0; t < TT; ++t) {
+          const float sg = sigmoidf(xv[t]);
+          y[t] *= g[t] * sg * fmaf(xv[t], 1.0f - sg, 1.0f);
+        }
+        if (w.mine) dz.store(t0, count, y);
       }
     }
   }
