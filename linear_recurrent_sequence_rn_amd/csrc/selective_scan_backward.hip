@@ -108,16 +108,13 @@ struct Lanes {
     }
     // N tokens from t0 on; those from `count` (>= 1) on repeat the last one, or are not stored
     template <int N>
-    __device__ __forceinline__ void load(int t0, int count, float (&v)[N]) const {
+    __device__ __forceinline__ void load(int t0, int count, elem (&v)[N]) const {
       const elem* r = p + t0 * step;
-      elem raw[N];
 #pragma unroll
       for (int t = 0; t < N; ++t) {
-        raw[t] = *reinterpret_cast<const elem*>(reinterpret_cast<const char*>(r) + off);
+        v[t] = *reinterpret_cast<const elem*>(reinterpret_cast<const char*>(r) + off);
         if (t + 1 < count) r += step;
       }
-#pragma unroll
-      for (int t = 0; t < N; ++t) v[t] = value_of<DT>(raw[t]);
     }
     template <int N>
     __device__ __forceinline__ void store(int t0, int count, const float (&v)[N]) const {
@@ -630,12 +627,20 @@ __global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
         h[i] = 0.f;
       }
       if (from) load_states<NS>(from, n, fours, h);
+      elem nx[TT], ndt[TT];
+      x.load(0, TT, nx);
+      dt.load(0, TT, ndt);
       for (int q = 0; q < tiles - 1; ++q) {
         float s[TT], u[TT];
-        x.load(q * TT, TT, u);
-        dt.load(q * TT, TT, s);
 #pragma unroll
-        for (int t = 0; t < TT; ++t) s[t] += bias;
+        for (int t = 0; t < TT; ++t) {
+          u[t] = value_of<DT>(nx[t]);
+          s[t] = value_of<DT>(ndt[t]) + bias;
+        }
+        if (q + 2 < tiles) {
+          x.load((q + 1) * TT, TT, nx);
+          dt.load((q + 1) * TT, TT, ndt);
+        }
         if (a.softplus) {
 #pragma unroll
           for (int t = 0; t < TT; ++t) s[t] = softplus(s[t]);
@@ -659,19 +664,29 @@ __global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
     const int64_t bc_step = static_cast<int64_t>(a.tiles) * a.G * 2 * n;
     float* bc = b.part_bc + ((a.q.T > 0 ? w.row0 : static_cast<int64_t>(w.p.s) * a.q.N) + w.first) * bc_step +
                 w.x * 2 * n + (lane & 1) * n;
+    struct Raw { elem x[TT], dt[TT], dout[TT], z[TT]; };
+    auto inputs = [&](int t0, int count, Raw& r) {
+      x.load(t0, count, r.x);
+      dt.load(t0, count, r.dt);
+      dout.load(t0, count, r.dout);
+      z.load(t0, count, r.z);
+    };
+    Raw next;
+    inputs((tiles - 1) * TT, nt - (tiles - 1) * TT, next);
     for (int q = tiles - 1; q >= 0; --q) {
       const int t0 = q * TT, count = min(nt - t0, TT);
       float s[TT], u[TT], dy[TT], du[TT], ws[TT], y[TT];
-      x.load(t0, count, u);
-      dt.load(t0, count, s);
-      dout.load(t0, count, dy);
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        u[t] = value_of<DT>(next.x[t]);
+        s[t] = value_of<DT>(next.dt[t]) + bias;
+        dy[t] = value_of<DT>(next.dout[t]);
+        y[t] = value_of<DT>(next.z[t]);
+      }
       if (a.z) {
-        z.load(t0, count, y);
 #pragma unroll
         for (int t = 0; t < TT; ++t) dy[t] *= y[t] * sigmoidf(y[t]);
       }
-#pragma unroll
-      for (int t = 0; t < TT; ++t) s[t] += bias;
       if (a.softplus) {
 #pragma unroll
         for (int t = 0; t < TT; ++t) s[t] = softplus(s[t]);
@@ -759,30 +774,29 @@ __global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
         const int t = lane >> 3, i = c + (lane >> 1 & 3);
         if (t < count && i < n) bc[(t0 + t) * bc_step + i] = lane & 1 ? sum_c : sum_b;
       }
-      // what belongs to a channel and token
-      float xv[TT], g[TT];
-      x.load(t0, count, xv);
-      dt.load(t0, count, g);
+      // what belongs to a channel and token, while the next tile's inputs are on their way
+      Raw r;
+      inputs(t0, count, r);
+      if (q > 0) inputs(t0 - TT, TT, next);
+      float g[TT];
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
-        const float slope = a.softplus ? sigmoidf(g[t] + bias) : 1.f;
-        g[t] = fmaf(du[t], xv[t], ws[t] * 0.69314718f) * slope;
+        const float xv = value_of<DT>(r.x[t]), slope = a.softplus ? sigmoidf(value_of<DT>(r.dt[t]) + bias) : 1.f;
+        g[t] = fmaf(du[t], xv, ws[t] * 0.69314718f) * slope;
         du[t] = fmaf(du[t], s[t], skip * dy[t]);
-        dskip = fmaf(dy[t], xv[t], dskip);
+        dskip = fmaf(dy[t], xv, dskip);
         if (t < count) dbias += g[t];
-        y[t] = fmaf(skip, xv[t], y[t]);
+        y[t] = fmaf(skip, xv, y[t]);
       }
       if (w.mine) {
         dx.store(t0, count, du);
         ddt.store(t0, count, g);
       }
       if (a.z) {
-        dout.load(t0, count, g);
-        z.load(t0, count, xv);
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-          const float sg = sigmoidf(xv[t]);
-          y[t] *= g[t] * sg * fmaf(xv[t], 1.0f - sg, 1.0f);
+          const float zv = value_of<DT>(r.z[t]), sg = sigmoidf(zv);
+          y[t] *= value_of<DT>(r.dout[t]) * sg * fmaf(zv, 1.0f - sg, 1.0f);
         }
         if (w.mine) dz.store(t0, count, y);
       }
