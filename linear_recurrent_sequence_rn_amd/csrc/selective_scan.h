@@ -96,6 +96,14 @@ __device__ __forceinline__ int64_t uniform64(int64_t x) {
   return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
 }
 
+// A lane's byte offset from uniform pointers for the accesses that follow, as the 32 bits that an access
+// takes beside the scalar registers of its pointer. (Widened ahead of a loop, it would be added to every
+// pointer by itself, in 64 bits.)
+__device__ __forceinline__ unsigned lane_offset(unsigned bytes) {
+  asm volatile("" : "+v"(bytes));
+  return bytes;
+}
+
 // NS values of B or C from element i of p (both the same for the whole wave). FAST: through the scalar
 // cache; all NS are there, bf16 in pairs that start on 4 bytes. Else every lane loads the first `have` of
 // them, the rest being zeros.

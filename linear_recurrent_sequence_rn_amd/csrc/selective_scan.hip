@@ -71,20 +71,21 @@ __global__ void __launch_bounds__(256) scan_rows(ScanArgs a) {
   elem* out = MODE == kScanOut ? const_cast<elem*>(at(a.out, a.os)) : nullptr;
   float total = 0.f;                      // kScanState: the sum of D_t
   elem nx[kGroup], ndt[kGroup], nz[kGroup] = {};
-  auto take = [&](const elem*& p, int64_t step) {          // the lane's value of the row p stands at
-    const elem v = *reinterpret_cast<const elem*>(reinterpret_cast<const char*>(p) + off);
+  auto take = [](const elem*& p, int64_t step, unsigned o) {   // the lane's value of the row p stands at
+    const elem v = *reinterpret_cast<const elem*>(reinterpret_cast<const char*>(p) + o);
     p += step;
     return v;
   };
   auto fetch = [&]() {                    // the next group's values
+    const unsigned o = lane_offset(off);
 #pragma unroll
     for (int k = 0; k < kGroup; ++k) {
-      nx[k] = take(px, a.xs[1]);
-      ndt[k] = take(pdt, a.dts[1]);
+      nx[k] = take(px, a.xs[1], o);
+      ndt[k] = take(pdt, a.dts[1], o);
     }
     if (MODE == kScanOut && pz) {
 #pragma unroll
-      for (int k = 0; k < kGroup; ++k) nz[k] = take(pz, a.zs[1]);
+      for (int k = 0; k < kGroup; ++k) nz[k] = take(pz, a.zs[1], o);
     }
   };
   // Up to 16 states' B and C are on their way while the token before is worked on; of more, each set's when
@@ -142,20 +143,21 @@ __global__ void __launch_bounds__(256) scan_rows(ScanArgs a) {
         for (int k = 0; k < kGroup; ++k) y[k] *= z[k] * sigmoidf(z[k]);
       }
       if (mine) {
+        const unsigned o = lane_offset(off);
 #pragma unroll
-        for (int k = 0; k < kGroup; ++k) Elem<DT>::store(reinterpret_cast<char*>(out + k * a.os[1]) + off, 0, y[k]);
+        for (int k = 0; k < kGroup; ++k) Elem<DT>::store(reinterpret_cast<char*>(out + k * a.os[1]) + o, 0, y[k]);
       }
       out += kGroup * a.os[1];
     }
   }
   for (int t = groups * kGroup; t < nt; ++t) {     // fewer than a group
-    const float xv = value_of<DT>(take(px, a.xs[1]));
-    float s = value_of<DT>(take(pdt, a.dts[1])) + bias;
+    const float xv = value_of<DT>(take(px, a.xs[1], off));
+    float s = value_of<DT>(take(pdt, a.dts[1], off)) + bias;
     if (a.softplus) s = softplus(s);
     float y = token(xv, s, t);
     if (MODE == kScanOut) {
       if (pz) {
-        const float z = value_of<DT>(take(pz, a.zs[1]));
+        const float z = value_of<DT>(take(pz, a.zs[1], off));
         y *= z * sigmoidf(z);
       }
       if (mine) Elem<DT>::store(reinterpret_cast<char*>(out) + off, 0, y);

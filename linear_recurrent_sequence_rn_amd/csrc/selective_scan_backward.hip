@@ -98,11 +98,8 @@ struct Lanes {
     const elem* p;
     int64_t step;
     unsigned off;
-    __device__ __forceinline__ elem at(int t) const {
-      return *reinterpret_cast<const elem*>(reinterpret_cast<const char*>(p + t * step) + off);
-    }
-    __device__ __forceinline__ elem take() {
-      const elem v = at(0);
+    __device__ __forceinline__ elem take(unsigned o) {
+      const elem v = *reinterpret_cast<const elem*>(reinterpret_cast<const char*>(p) + o);
       p += step;
       return v;
     }
@@ -110,22 +107,24 @@ struct Lanes {
     template <int N>
     __device__ __forceinline__ void load(int t0, int count, elem (&v)[N]) const {
       const elem* r = p + t0 * step;
+      const unsigned o = lane_offset(off);
 #pragma unroll
       for (int t = 0; t < N; ++t) {
-        v[t] = *reinterpret_cast<const elem*>(reinterpret_cast<const char*>(r) + off);
+        v[t] = *reinterpret_cast<const elem*>(reinterpret_cast<const char*>(r) + o);
         if (t + 1 < count) r += step;
       }
     }
     template <int N>
     __device__ __forceinline__ void store(int t0, int count, const float (&v)[N]) const {
       elem* r = const_cast<elem*>(p + t0 * step);
+      const unsigned o = lane_offset(off);
       if (count >= N) {
 #pragma unroll
-        for (int t = 0; t < N; ++t, r += step) Elem<DT>::store(reinterpret_cast<char*>(r) + off, 0, v[t]);
+        for (int t = 0; t < N; ++t, r += step) Elem<DT>::store(reinterpret_cast<char*>(r) + o, 0, v[t]);
       } else {
 #pragma unroll
         for (int t = 0; t < N; ++t, r += step)
-          if (t < count) Elem<DT>::store(reinterpret_cast<char*>(r) + off, 0, v[t]);
+          if (t < count) Elem<DT>::store(reinterpret_cast<char*>(r) + o, 0, v[t]);
       }
     }
     __device__ __forceinline__ void put(int t, float v) const {
@@ -149,9 +148,12 @@ struct Lanes {
     nt = min(len - first, a.q.len);
     return true;
   }
-  __device__ __forceinline__ Row row(const ScanArgs& a, const void* t, const int64_t* st) const {
-    return Row{static_cast<const elem*>(t) + (a.q.T > 0 ? row0 * st[1] : p.s * st[0]) + static_cast<int64_t>(first) * st[1], st[1],
+  __device__ __forceinline__ Row row(bool packed, const void* t, int64_t seq_step, int64_t step) const {
+    return Row{static_cast<const elem*>(t) + (packed ? row0 * step : p.s * seq_step) + first * step, step,
                static_cast<unsigned>(d * sizeof(elem))};
+  }
+  __device__ __forceinline__ Row row(const ScanArgs& a, const void* t, const int64_t* st) const {
+    return row(a.q.T > 0, t, st[0], st[1]);
   }
   __device__ __forceinline__ const elem* heads(const ScanArgs& a, const void* t, const int64_t* st) const {
     return static_cast<const elem*>(t) + (a.q.T > 0 ? row0 * st[2] : p.s * st[0]) + group * st[1] + static_cast<int64_t>(first) * st[2];
@@ -202,15 +204,16 @@ __global__ void __launch_bounds__(256) scan_edges(BackArgs b) {
                           z = w.row(a, a.z ? a.z : a.x, a.z ? a.zs : a.xs);
   typename Lanes<DT>::elem nx[kGroup], ndt[kGroup], ndo[kGroup], nz[kGroup] = {};
   auto fetch = [&]() {
+    const unsigned o = lane_offset(x.off);
 #pragma unroll
     for (int k = 0; k < kGroup; ++k) {
-      nx[k] = x.take();
-      ndt[k] = dt.take();
-      ndo[k] = dout.take();
+      nx[k] = x.take(o);
+      ndt[k] = dt.take(o);
+      ndo[k] = dout.take(o);
     }
     if (a.z) {
 #pragma unroll
-      for (int k = 0; k < kGroup; ++k) nz[k] = z.take();
+      for (int k = 0; k < kGroup; ++k) nz[k] = z.take(o);
     }
   };
   const typename Lanes<DT>::elem* pb = w.heads(a, a.b, a.bs) + n0;
@@ -257,10 +260,10 @@ __global__ void __launch_bounds__(256) scan_edges(BackArgs b) {
     for (int k = 0; k < kGroup; ++k) token(g * kGroup + k, s[k], s[k] * u[k], dy[k]);
   }
   for (int t = groups * kGroup; t < nt; ++t) {     // fewer than a group
-    const float xv = value_of<DT>(x.take());
-    const float s = step_of(a, value_of<DT>(dt.take()) + bias);
-    float dy = value_of<DT>(dout.take());
-    if (a.z) dy *= gate(value_of<DT>(z.take()));
+    const float xv = value_of<DT>(x.take(x.off));
+    const float s = step_of(a, value_of<DT>(dt.take(dt.off)) + bias);
+    float dy = value_of<DT>(dout.take(dout.off));
+    if (a.z) dy *= gate(value_of<DT>(z.take(z.off)));
     token(t, s, s * xv, dy);
   }
   if (!w.mine) return;
@@ -567,6 +570,16 @@ __global__ void __launch_bounds__(256) scan_main(BackArgs b) {
 // Up to 16 states: a wave takes 64 channels, a lane each, and meets no other. A tile's states go four at a
 // time: their decays and states over the tile's 8 tokens are in registers, and a lane sums over all of
 // them what its channel needs.
+// The kernel's arguments, read again from where the launch put them: what a tile needs of them before and
+// behind its states then holds no scalar register in between (held in all 250 of them are moved to lanes
+// of vector registers and back, 600 of a tile's 3700 instructions).
+typedef const __attribute__((address_space(4))) BackArgs* ArgsAgain;
+__device__ __forceinline__ ArgsAgain args_again() {
+  ArgsAgain p = (ArgsAgain)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return p;
+}
+
 template <int DT, int SETS, bool FAST>
 __global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
   constexpr int TT = kPieceTile, NS = 4 * SETS;
@@ -660,19 +673,19 @@ __global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
     }
     asm volatile("" ::"v"(asked[0]), "v"(asked[1]));
     // ---- backward, tile by tile
-    auto dx = w.row(a, b.dx, b.dxs), ddt = w.row(a, b.ddt, b.ddts), dz = w.row(a, a.z ? b.dz : b.dx, a.z ? b.dzs : b.dxs);
     const int64_t bc_step = static_cast<int64_t>(a.tiles) * a.G * 2 * n;
     float* bc = b.part_bc + ((a.q.T > 0 ? w.row0 : static_cast<int64_t>(w.p.s) * a.q.N) + w.first) * bc_step +
                 w.x * 2 * n + (lane & 1) * n;
     struct Raw { elem x[TT], dt[TT], dout[TT], z[TT]; };
-    auto inputs = [&](int t0, int count, Raw& r) {
-      x.load(t0, count, r.x);
-      dt.load(t0, count, r.dt);
-      dout.load(t0, count, r.dout);
-      z.load(t0, count, r.z);
+    auto inputs = [&](ArgsAgain k, int t0, int count, Raw& r) {
+      const bool packed = k->s.q.T > 0, gate = k->s.z;
+      w.row(packed, k->s.x, k->s.xs[0], k->s.xs[1]).load(t0, count, r.x);
+      w.row(packed, k->s.dt, k->s.dts[0], k->s.dts[1]).load(t0, count, r.dt);
+      w.row(packed, k->dout, k->s.os[0], k->s.os[1]).load(t0, count, r.dout);
+      w.row(packed, gate ? k->s.z : k->s.x, gate ? k->s.zs[0] : k->s.xs[0], gate ? k->s.zs[1] : k->s.xs[1]).load(t0, count, r.z);
     };
     Raw next;
-    inputs((tiles - 1) * TT, nt - (tiles - 1) * TT, next);
+    inputs(args_again(), (tiles - 1) * TT, nt - (tiles - 1) * TT, next);
     for (int q = tiles - 1; q >= 0; --q) {
       const int t0 = q * TT, count = min(nt - t0, TT);
       float s[TT], u[TT], dy[TT], du[TT], ws[TT], y[TT];
@@ -776,8 +789,10 @@ __global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
       }
       // what belongs to a channel and token, while the next tile's inputs are on their way
       Raw r;
-      inputs(t0, count, r);
-      if (q > 0) inputs(t0 - TT, TT, next);
+      const ArgsAgain k = args_again();
+      const bool packed = k->s.q.T > 0;
+      inputs(k, t0, count, r);
+      if (q > 0) inputs(k, t0 - TT, TT, next);
       float g[TT];
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
@@ -789,16 +804,16 @@ __global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
         y[t] = fmaf(skip, xv, y[t]);
       }
       if (w.mine) {
-        dx.store(t0, count, du);
-        ddt.store(t0, count, g);
+        w.row(packed, k->dx, k->dxs[0], k->dxs[1]).store(t0, count, du);
+        w.row(packed, k->ddt, k->ddts[0], k->ddts[1]).store(t0, count, g);
       }
-      if (a.z) {
+      if (k->s.z) {
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
           const float zv = value_of<DT>(r.z[t]), sg = sigmoidf(zv);
           y[t] *= value_of<DT>(r.dout[t]) * sg * fmaf(zv, 1.0f - sg, 1.0f);
         }
-        if (w.mine) dz.store(t0, count, y);
+        if (w.mine) w.row(packed, k->dz, k->dzs[0], k->dzs[1]).store(t0, count, y);
       }
     }
   }
@@ -940,8 +955,17 @@ struct Parts {
   }
   size_t all() const { return 2 * state + 3 * step + bc; }
 };
+// Tokens a piece: the most that leave waves for the chip to hold at once, two a SIMD (float32, 5 sequences of
+// 1501 tokens in all, 212 channels: 8 tokens 59 us, 32 110; bf16, 16 states, 4 x 512 tokens of 1024 channels: 8
+// tokens 102, 16 95, 32 135; 4 x 2048 of 2048: 663, 532 and 484). scan_main's blocks are four waves.
 ScanArgs pieces_of(const ScanCall& c) {
-  return scan_args(c, c.n <= 16 ? kPieceTile * kPieceTiles : kTiles * tile_of(scan_states(c.n)));
+  const bool small = c.n <= 16;
+  const int tile = small ? kPieceTile : tile_of(scan_states(c.n));
+  const int64_t per = static_cast<int64_t>(c.G) * ((c.D / c.G + 63) / 64);
+  const int64_t tokens = c.T > 0 ? c.T : static_cast<int64_t>(c.S) * c.N;
+  int len = tile * (small ? kPieceTiles : kTiles);
+  while (len > tile && tokens * per < (small ? 2048 : 512) * static_cast<int64_t>(len)) len /= 2;
+  return scan_args(c, len);
 }
 
 }  // namespace
