@@ -129,6 +129,13 @@ struct Uniform<DT, NS, true> {
 #pragma unroll
     for (int k = 0; k < kWords; ++k) u[k] = yes ? u[k] : 0;
   }
+  // What was unpacked so far is not kept: values are unpacked again when they are needed again.
+  __device__ __forceinline__ void fresh() {
+    if constexpr (DT != RN_F32) {
+#pragma unroll
+      for (int k = 0; k < kWords; ++k) asm volatile("" : "+s"(u[k]));
+    }
+  }
   __device__ __forceinline__ float value(int k) const {
     if constexpr (DT == RN_F32) return __uint_as_float(u[k]);
     else return __uint_as_float(k % 2 ? u[k / 2] & 0xffff0000u : u[k / 2] << 16);
@@ -146,6 +153,7 @@ struct Uniform<DT, NS, false> {
 #pragma unroll
     for (int k = 0; k < NS; ++k) f[k] = yes ? f[k] : 0.f;
   }
+  __device__ __forceinline__ void fresh() {}
   __device__ __forceinline__ float value(int k) const { return f[k]; }
 };
 

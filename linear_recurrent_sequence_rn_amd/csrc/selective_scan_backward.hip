@@ -108,10 +108,15 @@ struct Lanes {
     __device__ __forceinline__ void load(int t0, int count, elem (&v)[N]) const {
       const elem* r = p + t0 * step;
       const unsigned o = lane_offset(off);
+      if (count >= N) {
 #pragma unroll
-      for (int t = 0; t < N; ++t) {
-        v[t] = *reinterpret_cast<const elem*>(reinterpret_cast<const char*>(r) + o);
-        if (t + 1 < count) r += step;
+        for (int t = 0; t < N; ++t, r += step) v[t] = *reinterpret_cast<const elem*>(reinterpret_cast<const char*>(r) + o);
+      } else {
+#pragma unroll
+        for (int t = 0; t < N; ++t) {
+          v[t] = *reinterpret_cast<const elem*>(reinterpret_cast<const char*>(r) + o);
+          if (t + 1 < count) r += step;
+        }
       }
     }
     template <int N>
@@ -706,12 +711,16 @@ __global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
       }
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
-        const bool there = w.mine && t < count;    // tokens behind the last one, and lanes past the channels: zeros
-        u[t] = there ? s[t] * u[t] : 0.f;
-        s[t] = there ? s[t] : 0.f;
-        dy[t] = there ? dy[t] : 0.f;
+        if (!w.mine) s[t] = u[t] = dy[t] = 0.f;   // lanes past the channels, and tokens behind the last one: zeros
         du[t] = ws[t] = y[t] = 0.f;
       }
+      if (count < TT) {
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+          if (t >= count) s[t] = u[t] = dy[t] = 0.f;
+      }
+#pragma unroll
+      for (int t = 0; t < TT; ++t) u[t] *= s[t];
 #pragma unroll 1
       for (int c = 0; c < NS; c += 4) {
         float A2[4], h[4], e[4], dec[TT][4], p[TT][4], sums[32];
@@ -723,7 +732,8 @@ __global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
           for (int t = 0; t < TT; ++t) {
             B[t].load(rb, 0, n - c);
             C[t].load(rc, 0, n - c);
-            if (t + 1 < count) { rb += a.bs[2]; rc += a.cs[2]; }
+            rb += t + 1 < count ? a.bs[2] : 0;
+            rc += t + 1 < count ? a.cs[2] : 0;
           }
         }
         load_states<4>(A + c, n - c, a.a4, A2);
@@ -763,6 +773,11 @@ __global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
           }
         }
         const float sum_c = sums32(sums, lane);
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          B[t].fresh();
+          C[t].fresh();
+        }
         float dA[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int t = TT - 1; t >= 0; --t) {
@@ -793,6 +808,11 @@ __global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
       const bool packed = k->s.q.T > 0;
       inputs(k, t0, count, r);
       if (q > 0) inputs(k, t0 - TT, TT, next);
+      if (count < TT) {
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+          if (t >= count) ws[t] = 0.f;
+      }
       float g[TT];
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
@@ -800,7 +820,7 @@ __global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
         g[t] = fmaf(du[t], xv, ws[t] * 0.69314718f) * slope;
         du[t] = fmaf(du[t], s[t], skip * dy[t]);
         dskip = fmaf(dy[t], xv, dskip);
-        if (t < count) dbias += g[t];
+        dbias += g[t];
         y[t] = fmaf(skip, xv, y[t]);
       }
       if (w.mine) {
