@@ -572,6 +572,9 @@ __global__ void __launch_bounds__(256) scan_main(BackArgs b) {
   }
 }
 
+__device__ __forceinline__ void get4(const float4& from, float* v) { v[0] = from.x; v[1] = from.y; v[2] = from.z; v[3] = from.w; }
+__device__ __forceinline__ void put4(float4& to, const float* v) { to = make_float4(v[0], v[1], v[2], v[3]); }
+
 // Up to 16 states: a wave takes 64 channels, a lane each, and meets no other. A tile's states go four at a
 // time: their decays and states over the tile's 8 tokens are in registers, and a lane sums over all of
 // them what its channel needs.
@@ -590,8 +593,9 @@ __global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
   constexpr int TT = kPieceTile, NS = 4 * SETS;
   // The state at the start of tiles 1 and on; a tile's is read once, and then replaced by the gradient that
   // reaches the tile before.
-  __shared__ float starts[kPieceTiles - 1][NS][64];
-  __shared__ float own[NS][64];                       // dA of the piece
+  __shared__ float4 starts[kPieceTiles - 1][SETS][64];
+  __shared__ float4 own[SETS][64];                       // dA of the piece
+  __shared__ float4 decay[SETS][64];                     // A log2(e)
   const ScanArgs& a = b.s;
   Lanes<DT> w;
   const bool found = w.find(a, blockIdx.x);
@@ -602,7 +606,7 @@ __global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
   const int64_t sb = (static_cast<int64_t>(w.p.s) * a.D + w.d) * n, wb = (w.piece * a.D + w.d) * n;
   float dskip = 0.f, dbias = 0.f;
 #pragma unroll
-  for (int i = 0; i < NS; ++i) own[i][lane] = 0.f;
+  for (int i = 0; i < SETS; ++i) own[i][lane] = make_float4(0.f, 0.f, 0.f, 0.f);
   const float* from = nullptr;                     // the starting state
   const float* grad = nullptr;                     // and the gradient that reaches the piece from behind
   if (real && w.p.piece <= w.last) {
@@ -635,15 +639,17 @@ __global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
     }
     const int tiles = (nt + TT - 1) / TT;
     const float* const A = a.A + static_cast<int64_t>(w.d) * n;
+    float A2[NS];
+    load_states<NS>(A, n, a.a4, A2);
+#pragma unroll
+    for (int i = 0; i < NS; ++i) A2[i] = in_log2(A2[i]);
+#pragma unroll
+    for (int i = 0; i < SETS; ++i) put4(decay[i][lane], A2 + 4 * i);
     // ---- forward: the states at the tiles' starts
     if (tiles > 1) {
-      float A2[NS], h[NS];
-      load_states<NS>(A, n, a.a4, A2);
+      float h[NS];
 #pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        A2[i] = in_log2(A2[i]);
-        h[i] = 0.f;
-      }
+      for (int i = 0; i < NS; ++i) h[i] = 0.f;
       if (from) load_states<NS>(from, n, fours, h);
       elem nx[TT], ndt[TT];
       x.load(0, TT, nx);
@@ -673,7 +679,7 @@ __global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
           for (int i = 0; i < NS; ++i) h[i] = fmaf(__builtin_amdgcn_exp2f(s[t] * A2[i]), h[i], u[t] * B.value(i));
         }
 #pragma unroll
-        for (int i = 0; i < NS; ++i) starts[q][i][lane] = h[i];
+        for (int i = 0; i < SETS; ++i) put4(starts[q][i][lane], h + 4 * i);
       }
     }
     asm volatile("" ::"v"(asked[0]), "v"(asked[1]));
@@ -736,23 +742,18 @@ __global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
             rc += t + 1 < count ? a.cs[2] : 0;
           }
         }
-        load_states<4>(A + c, n - c, a.a4, A2);
+        get4(decay[c / 4][lane], A2);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          A2[i] = in_log2(A2[i]);
-          h[i] = e[i] = 0.f;
-        }
+        for (int i = 0; i < 4; ++i) h[i] = e[i] = 0.f;
         if (q == tiles - 1) {
           if (grad) load_states<4>(grad + c, n - c, fours, e);
         } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) e[i] = starts[q][c + i][lane];
+          get4(starts[q][c / 4][lane], e);
         }
         if (q == 0) {
           if (from) load_states<4>(from + c, n - c, fours, h);
         } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) h[i] = starts[q - 1][c + i][lane];
+          get4(starts[q - 1][c / 4][lane], h);
         }
         if (count < TT) {
 #pragma unroll
@@ -792,11 +793,12 @@ __global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
             e[i] = dec[t][i] * g;
           }
         }
+        float sum[4];
+        get4(own[c / 4][lane], sum);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          own[c + i][lane] += dA[i];
-          if (q > 0) starts[q - 1][c + i][lane] = e[i];
-        }
+        for (int i = 0; i < 4; ++i) sum[i] += dA[i];
+        put4(own[c / 4][lane], sum);
+        if (q > 0) put4(starts[q - 1][c / 4][lane], e);
         if (q == 0 && passed) store_states<4>(passed + c, n - c, fours, e);
         const float sum_b = sums32(sums, lane);
         const int t = lane >> 3, i = c + (lane >> 1 & 3);
@@ -841,7 +843,7 @@ __global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
   // the piece's own sums (zeros of a piece without tokens), where its starting state was
   float dA[NS];
 #pragma unroll
-  for (int i = 0; i < NS; ++i) dA[i] = own[i][lane];
+  for (int i = 0; i < SETS; ++i) get4(own[i][lane], dA + 4 * i);
   store_states<NS>(a.seg_state + wb, n, fours, dA);
   b.part_skip[w.piece * a.D + w.d] = dskip;
   b.part_bias[w.piece * a.D + w.d] = dbias;
