@@ -174,64 +174,72 @@ __global__ void __launch_bounds__(256) conv_backward(ConvArgs a) {
                   db0 = seq_base(a.q, p, a.ds[0], a.ds[1]) + c;
     const bool real = p.s < a.q.S;
     const int64_t sb = static_cast<int64_t>(p.s) * (K - 1) * a.D + c;     // of a state's row 0
-    // the last K inputs, and what du leaves for the last K tokens: dx[k] is token i - (K - 1) + k's
-    float x[K][V], dx[K][V];
+    // x[i]: token t0 - (K - 1) + i; g[i]: dout of token t0 + i. All at once, from rows inside the sequence, and
+    // zeros where the token is not.
+    Raw<DT, V, FIT> x[kRun + 2 * K - 2], g[kRun + K - 1];
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int i = 0; i < kRun + 2 * K - 2; ++i) x[i].clear();
 #pragma unroll
-      for (int v = 0; v < V; ++v) x[k][v] = dx[k][v] = 0.f;
+    for (int i = 0; i < kRun + K - 1; ++i) g[i].clear();
+    if (p.len > 0) {
+      auto row = [&](int64_t t) { return min(max(t, int64_t(0)), static_cast<int64_t>(p.len) - 1); };
 #pragma unroll
-    for (int k = 0; k < K - 1; ++k) {
-      const int64_t t = t0 - (K - 1) + k;
-      if (t >= 0 && t < p.len) load<DT, V, FIT>(a.x, xb + t * a.xs[1], left, x[k + 1]);
-      else if (t < 0 && real && a.state_in) load<DT, V, FIT>(a.state_in, sb + (t + K - 1) * a.D, left, x[k + 1]);
+      for (int i = 0; i < kRun + 2 * K - 2; ++i) x[i].load(a.x, xb + row(t0 - (K - 1) + i) * a.xs[1], left);
+#pragma unroll
+      for (int i = 0; i < kRun + K - 1; ++i) g[i].load(a.dout, ob + row(t0 + i) * a.os[1], left);
+      if (t0 < K - 1 || t0 + kRun + K - 1 > p.len) {
+#pragma unroll
+        for (int i = 0; i < kRun + 2 * K - 2; ++i)
+          if (t0 - (K - 1) + i < 0 || t0 - (K - 1) + i >= p.len) x[i].clear();
+      }
     }
+    if (head && real && a.state_in) {
+#pragma unroll
+      for (int i = 0; i < K - 1; ++i) x[i].load(a.state_in, sb + static_cast<int64_t>(i) * a.D, left);
+    }
+    float du[kRun + K - 1][V];
 #pragma unroll
     for (int i = 0; i < kRun + K - 1; ++i) {
-      const int64_t t = t0 + i;
-      const bool there = t < p.len;
-#pragma unroll
-      for (int k = 0; k < K - 1; ++k)
-#pragma unroll
-        for (int v = 0; v < V; ++v) { x[k][v] = x[k + 1][v]; dx[k][v] = dx[k + 1][v]; }
-      float du[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) x[K - 1][v] = dx[K - 1][v] = du[v] = 0.f;
-      if (there) {
-        load<DT, V, FIT>(a.x, xb + t * a.xs[1], left, x[K - 1]);
-        load<DT, V, FIT>(a.dout, ob + t * a.os[1], left, du);
-      }
+      const int64_t t = t0 + i, at = t - (K - 1);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
+        float d = g[i].value(v);
         if (a.silu) {
           float u = b[v];
 #pragma unroll
-          for (int j = 0; j < K; ++j) u = fmaf(w[v][j], x[j][v], u);
+          for (int j = 0; j < K; ++j) u = fmaf(w[v][j], x[i + j].value(v), u);
           const float sg = __builtin_amdgcn_rcpf(1.0f + __expf(-u));
-          if (there) du[v] *= sg * fmaf(u, 1.0f - sg, 1.0f);
+          d *= sg * fmaf(u, 1.0f - sg, 1.0f);
         }
-        if (i < kRun) db[v] += du[v];
+        du[i][v] = d = t < p.len ? d : 0.f;
+        if (i < kRun) {
+          db[v] += d;
 #pragma unroll
-        for (int j = 0; j < K; ++j) {
-          if (i < kRun && there) dw[j][v] = fmaf(du[v], x[j][v], dw[j][v]);
-          dx[j][v] = fmaf(w[v][j], du[v], dx[j][v]);
+          for (int j = 0; j < K; ++j) dw[j][v] = fmaf(d, x[i + j].value(v), dw[j][v]);
         }
       }
-      // dx[0] is whole now: of token t - (K - 1), a row of the state where it is before the first
+      // dx of token t - (K - 1), a row of the state where it is before the first
       if (i >= K - 1 || head) {
-        const int64_t at = t - (K - 1);
+        float dx[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          dx[v] = 0.f;
+#pragma unroll
+          for (int j = 0; j < K; ++j)
+            if (i - j >= 0) dx[v] = fmaf(w[v][j], du[i - j < 0 ? 0 : i - j][v], dx[v]);
+        }
         // the final state's gradient reaches the tokens that it holds
         const int64_t k = at - (static_cast<int64_t>(p.len) - (K - 1));
         if (real && a.dstate_out && k >= 0 && k < K - 1) {
           float more[V];
           load<RN_F32, V, FIT>(a.dstate_out, sb + k * a.D, left, more);
 #pragma unroll
-          for (int v = 0; v < V; ++v) dx[0][v] += more[v];
+          for (int v = 0; v < V; ++v) dx[v] += more[v];
         }
         if (at < 0) {
-          if (real && a.dstate_in) store<RN_F32, V, FIT>(a.dstate_in, sb + (at + K - 1) * a.D, left, dx[0]);
+          if (real && a.dstate_in) store<RN_F32, V, FIT>(a.dstate_in, sb + (at + K - 1) * a.D, left, dx);
         } else if (at < p.len) {
-          store<DT, V, FIT>(a.dx, db0 + at * a.ds[1], left, dx[0]);
+          store<DT, V, FIT>(a.dx, db0 + at * a.ds[1], left, dx);
         } else if (at < p.own && a.zero_rest) {
           Raw<DT, V, FIT> z;
           z.clear();
