@@ -166,7 +166,7 @@ def _new(x, dtype):
     """A new contiguous tensor of x's shape."""
     if x.dtype == dtype and x.is_contiguous():
         return torch.empty_like(x)
-    return torch.empty(x.shape, dtype=dtype, device=x.device)
+    return x.new_empty(x.shape, dtype=dtype)
 
 
 def _like(t, x, name):
@@ -285,7 +285,7 @@ def rn_rmsnorm(x, weight=None, eps=1e-5, *, residual=None, sum_out=None, out=Non
         step = -(-d // group) if group > 0 else 1
         ss = (*shape[:-1], step) if group else shape[:-1]
         if scale_out is None:
-            scale = torch.empty(ss, dtype=torch.float32, device=x.device)
+            scale = x.new_empty(ss, dtype=torch.float32)
         else:
             _whole(scale_out, torch.float32, ss, "scale_out")
             scale = scale_out

@@ -8,6 +8,7 @@
 // Single tokens. Bound by HBM: the float32 state is read and written once.
 #include <algorithm>
 
+#include "norm_rows.h"
 #include "selective_scan.h"
 
 namespace rn {
@@ -177,6 +178,20 @@ __global__ void __launch_bounds__(256) scan_rows(ScanArgs a) {
   }
 }
 
+// Four values, or one, of B or C: four in one load at any element's address.
+template <int DT, int VEC>
+struct Few {
+  Raw<DT, 4, kOdd> r;
+  __device__ __forceinline__ void load(const void* p, int64_t i) { r.load(p, i, 4); }
+  __device__ __forceinline__ float value(int i) const { return r.value(i); }
+};
+template <int DT>
+struct Few<DT, 1> {
+  float v;
+  __device__ __forceinline__ void load(const void* p, int64_t i) { v = Elem<DT>::load(p, i); }
+  __device__ __forceinline__ float value(int) const { return v; }
+};
+
 // The state at the start of each segment of sequence blockIdx.y, from what the segments before it add,
 // in place: a thread a state.
 __global__ void __launch_bounds__(256) scan_carry(ScanArgs a) {
@@ -210,58 +225,64 @@ __global__ void __launch_bounds__(256) scan_carry(ScanArgs a) {
   }
 }
 
-// One token a sequence: P lanes (a power of two) share a channel's states, VEC each.
-template <int DT, int VEC>
+// One token a sequence: P lanes (a power of two) share a channel's states, VEC each, and a thread takes
+// the same states of U sequences, whose loads it asks for at once.
+template <int DT, int VEC, int U>
 __global__ void __launch_bounds__(256) scan_step(ScanArgs a, int P) {
-  const int s = blockIdx.y;
   const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int64_t d = at / P;
   const int n0 = static_cast<int>(at - d * P) * VEC;
   if (d >= a.D) return;                             // (whole channels: P divides 64)
   const bool some = n0 < a.n;
-  const int slot = seq_slot(a.slots, a.n_slots, s);
-  const int64_t ob = s * a.os[0] + d;
-  if (slot < 0) {
-    if (n0 == 0) Elem<DT>::store(a.out, ob, 0.f);
-    return;
-  }
   typedef float vec __attribute__((ext_vector_type(VEC)));
-  float h[VEC], A[VEC], b[VEC], c[VEC];
-  const int64_t sb = (static_cast<int64_t>(slot) * a.D + d) * a.n + n0;
   const int64_t g = d / (a.D / a.G);
+  int slot[U];
+  vec h[U];
+  Few<DT, VEC> b[U], c[U];
+  float x[U], step[U], z[U];
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) h[i] = A[i] = b[i] = c[i] = 0.f;
-  if (some) {
-    const vec hv = __builtin_nontemporal_load(reinterpret_cast<const vec*>(a.state_in + sb));
-    const vec Av = *reinterpret_cast<const vec*>(a.A + d * a.n + n0);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      h[i] = hv[i];
-      A[i] = Av[i];
-      b[i] = Elem<DT>::load(a.b, s * a.bs[0] + g * a.bs[1] + n0 + i);
-      c[i] = Elem<DT>::load(a.c, s * a.cs[0] + g * a.cs[1] + n0 + i);
+  for (int u = 0; u < U; ++u) {
+    const int s = blockIdx.y * U + u;
+    slot[u] = s < a.q.S ? seq_slot(a.slots, a.n_slots, s) : -1;
+    if (slot[u] >= 0) {
+      if (some) {
+        h[u] = __builtin_nontemporal_load(reinterpret_cast<const vec*>(a.state_in + (static_cast<int64_t>(slot[u]) * a.D + d) * a.n + n0));
+        b[u].load(a.b, s * a.bs[0] + g * a.bs[1] + n0);
+        c[u].load(a.c, s * a.cs[0] + g * a.cs[1] + n0);
+      }
+      x[u] = Elem<DT>::load(a.x, s * a.xs[0] + d);
+      step[u] = Elem<DT>::load(a.dt, s * a.dts[0] + d);
+      z[u] = a.z ? Elem<DT>::load(a.z, s * a.zs[0] + d) : 0.f;
     }
   }
-  const float x = Elem<DT>::load(a.x, s * a.xs[0] + d);
-  float step = Elem<DT>::load(a.dt, s * a.dts[0] + d) + (a.bias ? a.bias[d] : 0.f);
-  if (a.softplus) step = softplus(step);
-  float y = 0.f;
-  vec to;
+  vec A = {};
+  if (some) A = *reinterpret_cast<const vec*>(a.A + d * a.n + n0);
+  const float bias = a.bias ? a.bias[d] : 0.f, skip = a.skip ? a.skip[d] : 0.f;
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    h[i] = fmaf(__builtin_amdgcn_exp2f(step * (in_log2(A[i]))), h[i], step * x * b[i]);
-    y = fmaf(c[i], h[i], y);
-    to[i] = h[i];
-  }
-  if (some) __builtin_nontemporal_store(to, reinterpret_cast<vec*>(a.state_out + sb));
-  for (int o = 1; o < P; o *= 2) y += __shfl_xor(y, o);
-  if (n0 == 0) {
-    if (a.skip) y = fmaf(a.skip[d], x, y);
-    if (a.z) {
-      const float z = Elem<DT>::load(a.z, s * a.zs[0] + d);
-      y *= z * sigmoidf(z);
+  for (int u = 0; u < U; ++u) {
+    const int s = blockIdx.y * U + u;
+    if (s >= a.q.S) return;
+    if (slot[u] < 0) {
+      if (n0 == 0) Elem<DT>::store(a.out, s * a.os[0] + d, 0.f);
+      continue;
     }
-    Elem<DT>::store(a.out, ob, y);
+    float D = step[u] + bias, y = 0.f;
+    if (a.softplus) D = softplus(D);
+    if (some) {
+      vec to;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        to[i] = fmaf(__builtin_amdgcn_exp2f(D * in_log2(A[i])), h[u][i], D * x[u] * b[u].value(i));
+        y = fmaf(c[u].value(i), to[i], y);
+      }
+      __builtin_nontemporal_store(to, reinterpret_cast<vec*>(a.state_out + (static_cast<int64_t>(slot[u]) * a.D + d) * a.n + n0));
+    }
+    for (int o = 1; o < P; o *= 2) y += __shfl_xor(y, o);
+    if (n0 == 0) {
+      y = fmaf(skip, x[u], y);
+      if (a.z) y *= z[u] * sigmoidf(z[u]);
+      Elem<DT>::store(a.out, s * a.os[0] + d, y);
+    }
   }
 }
 
@@ -291,6 +312,21 @@ hipError_t launch_n(const ScanArgs& a, bool state, hipStream_t st) {
 }
 hipError_t launch_pass(const ScanArgs& a, int dt, bool state, hipStream_t st) {
   return dt == RN_F32 ? launch_n<RN_F32>(a, state, st) : launch_n<RN_BF16>(a, state, st);
+}
+
+template <int DT, int VEC>
+hipError_t launch_step(const ScanArgs& a, int P, hipStream_t st) {
+  const int64_t x = (static_cast<int64_t>(a.D) * P + 255) / 256;
+  // Two sequences a thread where that leaves the chip eight blocks a CU and more: A is read once for them. (128
+  // sequences of 4096 channels x 16 states, bf16, 24 such pools in turn: 18.1 us, of which the states' 67 MB
+  // take 14 at a large copy's rate; four a thread 19.1; through the caches 20.9. Two pools in turn, which the
+  // last-level cache holds: 17.6 and through the caches 16.2.)
+  if (x * a.q.S >= 4096) {
+    hipLaunchKernelGGL((scan_step<DT, VEC, 2>), dim3(static_cast<unsigned>(x), (a.q.S + 1) / 2), dim3(256), 0, st, a, P);
+  } else {
+    hipLaunchKernelGGL((scan_step<DT, VEC, 1>), dim3(static_cast<unsigned>(x), a.q.S), dim3(256), 0, st, a, P);
+  }
+  return hipGetLastError();
 }
 
 // Tokens a segment. Whole sequences where their channels make a wave or more for each of the chip's 1024
@@ -335,15 +371,8 @@ hipError_t launch_selective_step(const ScanCall& c, hipStream_t st) {
   const int vec = c.n % 4 == 0 && reinterpret_cast<uintptr_t>(c.A) % 16 == 0 ? 4 : 1;
   int P = 1;
   while (P * vec < c.n) P *= 2;
-  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(c.D) * P + 255) / 256), c.S);
-  if (c.type == RN_F32) {
-    if (vec == 4) hipLaunchKernelGGL((scan_step<RN_F32, 4>), grid, dim3(256), 0, st, a, P);
-    else hipLaunchKernelGGL((scan_step<RN_F32, 1>), grid, dim3(256), 0, st, a, P);
-  } else {
-    if (vec == 4) hipLaunchKernelGGL((scan_step<RN_BF16, 4>), grid, dim3(256), 0, st, a, P);
-    else hipLaunchKernelGGL((scan_step<RN_BF16, 1>), grid, dim3(256), 0, st, a, P);
-  }
-  return hipGetLastError();
+  if (c.type == RN_F32) return vec == 4 ? launch_step<RN_F32, 4>(a, P, st) : launch_step<RN_F32, 1>(a, P, st);
+  return vec == 4 ? launch_step<RN_BF16, 4>(a, P, st) : launch_step<RN_BF16, 1>(a, P, st);
 }
 
 }  // namespace rn

@@ -120,7 +120,7 @@ def _states(state_in, state_out, slots, S, row, dtype, like):
     if slots is not None and state_out is True:
         raise ValueError("with slots, state_out must be a tensor")
     if state_out is True:
-        state_out = torch.empty((S, *row), dtype=dtype, device=like.device)
+        state_out = like.new_empty((S, *row), dtype=dtype)
     elif state_out is False:
         state_out = None
     n = None
@@ -165,7 +165,7 @@ def rn_short_conv(x, weight, bias=None, *, silu=False, lengths=None, cu_seqlens=
     state_out, n_slots = _states(state_in, state_out, slots, S, (K - 1, D), x.dtype, x)
     flags = RN_CONV_SILU if silu else 0
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = x.new_empty(x.shape)
         flags |= _rest((out,), x.shape[1], N, T, lengths)
     else:
         _same(out, x, "out")
@@ -186,7 +186,7 @@ def rn_short_conv_step(x, weight, bias, state, *, silu=False, slots=None, out=No
     K = _conv_weight(x, weight, bias)
     _, n_slots = _states(state, None, slots, S, (K - 1, D), x.dtype, x)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = x.new_empty(x.shape)
     else:
         _same(out, x, "out")
     desc = _pack_conv(S, 1, D, K, _code(x.dtype), RN_CONV_SILU if silu else 0, 0, n_slots, *_tokens(x, "x"),
@@ -226,7 +226,7 @@ def rn_short_conv_backward(dout, x, weight, bias=None, *, silu=False, lengths=No
     _grad_state(dstate_out, S, row, "dstate_out")
     flags = RN_CONV_SILU if silu else 0
     if dx is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dx = x.new_empty(x.shape)
         flags |= _rest((dx,), x.shape[1], N, T, lengths)
     else:
         _same(dx, x, "dx")
@@ -236,7 +236,7 @@ def rn_short_conv_backward(dout, x, weight, bias=None, *, silu=False, lengths=No
         if bias is not None:
             got["dbias"] = torch.empty_like(bias)
     if want_dstate_in:
-        got["dstate_in"] = torch.empty((S, *row), dtype=torch.float32, device=x.device)
+        got["dstate_in"] = x.new_empty((S, *row), dtype=torch.float32)
     desc = _pack_conv(S, N, D, K, _code(x.dtype), flags, T, 0, *_tokens(x, "x"), *_tokens(dout, "dout"), *_tokens(dx, "dx"))
     if want_dweight:
         workspace = _get_workspace(workspace, lib.rn_short_conv_backward_workspace_bytes(desc), x)
@@ -306,7 +306,7 @@ def rn_selective_scan_chunked(x, dt, A, B, C, D=None, *, dt_bias=None, softplus=
     state_out, n_slots = _states(state_in, state_out, slots, S, (x.shape[2], n), torch.float32, x)
     flags = RN_SCAN_SOFTPLUS if softplus else 0
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = x.new_empty(x.shape)
         flags |= _rest((out,), x.shape[1], N, T, lengths)
     else:
         _same(out, x, "out")
@@ -329,7 +329,7 @@ def rn_selective_scan_step(x, dt, A, B, C, state, D=None, *, dt_bias=None, softp
     n, G, tokens, groups = _scan_tensors(x, dt, A, B, C, D, dt_bias, z)
     _, n_slots = _states(state, None, slots, S, (x.shape[2], n), torch.float32, x)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = x.new_empty(x.shape)
     else:
         _same(out, x, "out")
     desc = _scan_desc(S, 1, 0, x, n, G, RN_SCAN_SOFTPLUS if softplus else 0, n_slots, tokens, _tokens(out, "out"), groups)
@@ -368,7 +368,7 @@ def rn_selective_scan_backward(dout, x, dt, A, B, C, D=None, *, dt_bias=None, so
         if like is None:
             continue
         if t is None:
-            t = torch.empty(like.shape, dtype=x.dtype, device=x.device)
+            t = x.new_empty(like.shape)
             new.append(t)
         else:
             _same(t, like, name)
@@ -386,7 +386,7 @@ def rn_selective_scan_backward(dout, x, dt, A, B, C, D=None, *, dt_bias=None, so
     if dt_bias is not None:
         got["ddt_bias"] = torch.empty_like(dt_bias)
     if want_dstate_in:
-        got["dstate_in"] = torch.empty((S, *row), dtype=torch.float32, device=x.device)
+        got["dstate_in"] = x.new_empty((S, *row), dtype=torch.float32)
     desc = _scan_desc(S, N, T, x, n, G, flags, 0, tokens, _tokens(dout, "dout"), groups)
     grads = _pack_grads(*_tokens(got["dx"], "dx"), *_tokens(got["ddt"], "ddt"),
                         *((0, 0) if z is None else _tokens(got["dz"], "dz")), *_groups(got["dB"], x, n, "dB"),
