@@ -40,16 +40,17 @@ struct ScanArgs {
 
 // x log2(e), rounded once (the constant in two parts).
 __device__ __forceinline__ float in_log2(float x) { return fmaf(x, kLog2eLow, x * kLog2e); }
-// softplus(v) to float32 accuracy at any v: max(v, 0) + log1p(e), e = exp(-|v|). What rounding the exponent
-// loses goes back into e (it is |v| 2^-24 of it), and with w = 1 + e, what rounding w loses into the
-// logarithm: log1p(e) = log(w) + (e - (w - 1)) / w, of which 1 / w is left out (the term is at most 2^-24 in
-// all, and where w is not near 1 the result is not small). The hardware's logarithm is relative near 1.
+// softplus(v) to float32 accuracy at any v, infinities too: max(v, 0) + log1p(e), e = exp(-|v|) (which is
+// nothing beside 1 from |v| = 126 on, and beside v long before). What rounding the exponent loses goes back
+// into e (it is |v| 2^-24 of it), and with w = 1 + e, what rounding w loses into the logarithm: log1p(e) =
+// log(w) + (e - (w - 1)) / w, of which 1 / w is left out (the term is at most 2^-24 in all, and where w is
+// not near 1 the result is not small). The hardware's logarithm is relative near 1.
 __device__ __forceinline__ float softplus(float v) {
-  const float m = -fabsf(v), t = m * kLog2e;
+  const float m = -fminf(fabsf(v), 126.0f), t = m * kLog2e;
   float e = __builtin_amdgcn_exp2f(t);
   e = fmaf(e, fmaf(m, kLog2eLow, fmaf(m, kLog2e, -t)) * 0.6931472f, e);
   const float w = 1.0f + e;
-  return fmaxf(v, 0.0f) + fmaf(__builtin_amdgcn_logf(w), 0.6931472f, e - (w - 1.0f));
+  return (v < 0.0f ? 0.0f : v) + fmaf(__builtin_amdgcn_logf(w), 0.6931472f, e - (w - 1.0f));
 }
 __device__ __forceinline__ float sigmoidf(float v) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v * kLog2e));

@@ -234,3 +234,27 @@ def test_cu_seqlens_that_make_no_sense_stay_inside_the_tensors():
         rn().rn_selective_scan_chunked(x, b.dt[:, 100:200], b.A, b.B[:, :, 100:200], b.C[:, :, 100:200],
                                        cu_seqlens=torch.tensor(cu, dtype=torch.int32, device=DEV), out=out[:, 100:200])
         assert (out[:, :100] == 7).all() and (out[:, 200:] == 7).all()
+
+
+def test_steps_at_the_ends_of_the_type():
+    """A token whose raw step is the type's lowest value or minus infinity changes no state (its step is
+    zero); one with infinities or NaN reaches later tokens of its channel only."""
+    low = torch.finfo(torch.bfloat16).min
+    for N in (40, 400):
+        b = Batch(14, [N], 72, 16, 1, torch.bfloat16, False, pad=0, gate=False, skip=False)
+        b.dt = b.dt.clone()
+        b.dt[0, 11] = low
+        b.dt[0, 12] = float("-inf")
+        out, state = b.run(state_out=True)
+        assert out.isfinite().all() and state.isfinite().all()
+        keep = [t for t in range(N) if t not in (11, 12)]
+        cut = lambda t: t[..., keep, :].contiguous()  # noqa: E731
+        rest, last = rn().rn_selective_scan_chunked(cut(b.x), cut(b.dt), b.A, cut(b.B), cut(b.C), dt_bias=b.bias, state_in=b.state,
+                                                    state_out=True)
+        assert np.abs(f64(state) - f64(last)).max() <= 1e-4 * np.abs(f64(last)).max()
+        assert (np.abs(f64(cut(out)) - f64(rest)) <= 2.0 ** -7 * np.abs(f64(rest)) + 1e-4).all()
+        b.dt[0, 20, 3], b.dt[0, 20, 4] = float("inf"), float("nan")
+        bad, _ = b.run(state_out=True)
+        assert torch.equal(bad[0, :20], out[0, :20]) and bad[0, 20:, 4].isnan().all()
+        other = [c for c in range(72) if c not in (3, 4)]
+        assert torch.equal(bad[0][:, other], out[0][:, other])
