@@ -6,9 +6,13 @@
 // nearest even (most: 448 for e4m3, 127 for int8). Backward, with g = dy w: dx = rstd g - x rstd^3
 // mean(g x) + dh, dw = sum_rows dy x rstd.
 //
-// Bound by HBM: every tensor is read or written once. Rows are held as in the layer norm: in the
-// registers of 16 lanes, of a wave or of a block, so that the passes over a row (squares, maximum,
-// result) cost no memory access; the backward needs one join of a row, for the sums of x x and g x.
+// Bound by HBM: every tensor is read or written once (16384 x 4096 bf16 with residual and an e4m3 output with a
+// scale for each 128 columns: 89 us, 5.3 TB/s; a large copy reaches 5.0 to 5.4). Smaller calls are bound by
+// latency (32 x 4096, e4m3: kernel 4 us, a call 10; backward of 3001 x 1537 float32 with the residual's
+// gradient: 19 us and 5 for the weights' sums). Rows are held as in the layer norm: in the registers of 16
+// lanes, of a wave or of a block, so that the passes over a row (squares, maximum, result) cost no memory
+// access; the backward needs one join of a row, for the sums of x x and g x. The largest value of a group of
+// 32 to 128 columns is found among the 4 to 32 lanes that hold them, without LDS.
 #include <algorithm>
 
 #include "norm_rows.h"

@@ -6,14 +6,20 @@
 //     dA = sum_t g_t p_t D_t,   dskip = sum_t dy_t x_t,   dbias = sum_t ddt_t
 //     dz_t = dout y_t (z sigmoid(z))'.
 //
-// Sequences are cut into pieces of 8 tiles. scan_edges gives, for each piece, the state it adds on its own
-// and the gradient it passes back on its own; scan_edges_carry joins them along the sequence; scan_main
-// takes every piece by itself: once forward for the state at each tile's start (kept in LDS), then tile by
-// tile from the last one, forward for a tile's decays and states (kept in registers) and back for the
-// gradients. Lanes are channels and waves share the states, so sums over states meet in LDS, and sums over
-// a block's 64 channels in a transposing tree across lanes: 64 sums of 64 lanes, one left in each lane,
-// in 141 instructions. Sums over all channels' blocks and over pieces are added in a fixed order by
-// scan_sum_tokens and scan_sum_pieces.
+// Sequences are cut into pieces. scan_edges gives, for each piece, the state it adds on its own and the
+// gradient it passes back on its own; scan_edges_carry joins them along the sequence. Then every piece is taken
+// by itself: once forward for the state at each tile's start (kept in LDS), then tile by tile from the last one,
+// forward for a tile's decays and states (kept in registers) and back for the gradients. Up to 16 states that
+// is scan_piece, whose waves take 64 channels, a lane each, and meet no other; for more, whose starting states
+// would not leave LDS for the waves, scan_main, where four waves share the states and join their sums in LDS.
+// Lanes are channels, so sums over the wave's 64 channels run across lanes, by a transposing tree: 32 sums of
+// 64 lanes, one left in two lanes each, in 71 instructions. Sums over all channels' blocks and over pieces are
+// added in a fixed order by scan_sum_tokens and scan_sum_pieces.
+//
+// Bound by the vector units: about 29 instructions a state and token in scan_piece and 10 in scan_edges, of
+// 13 that the gradients alone would take (4 x 2048 tokens of 2048 channels x 16 states, bf16 with gate: 340 and
+// 88 us of 464; busy 67 and 82 %; 250 registers a lane leave two waves a SIMD to hide the waits of each
+// other). All of them by four waves a block (scan_main): 640 us for scan_piece's part.
 #include <algorithm>
 
 #include "selective_scan.h"
@@ -22,7 +28,7 @@ namespace rn {
 namespace {
 
 struct BackArgs {
-  ScanArgs s;                             // its out strides are dout's; its pieces of 8 tiles
+  ScanArgs s;                             // its out strides are dout's
   int64_t dxs[2], ddts[2], dzs[2], dbs[3], dcs[3];
   const void* dout;
   const float* dstate_out;                // [S][D][n] or null
@@ -41,11 +47,11 @@ struct BackArgs {
   float* part_bc;                         // [token rows][blocks along channels][2][n]
 };
 
-constexpr int kPieceTile = 8, kPieceTiles = 4;   // scan_piece: tokens a tile, tiles a piece
+constexpr int kPieceTile = 8, kPieceTiles = 4;   // scan_piece: tokens a tile, tiles a piece at most
 // States a wave of scan_main holds: a quarter of them.
 int scan_states(int n) { return n <= 32 ? 8 : 16; }
 constexpr int tile_of(int NS) { return 32 / NS; }
-constexpr int kTiles = 8;                 // tiles a piece
+constexpr int kTiles = 8;                 // scan_main: tiles a piece, at most
 
 // What a block of either kernel works on.
 template <int NS>
@@ -575,12 +581,12 @@ __global__ void __launch_bounds__(256) scan_main(BackArgs b) {
 __device__ __forceinline__ void get4(const float4& from, float* v) { v[0] = from.x; v[1] = from.y; v[2] = from.z; v[3] = from.w; }
 __device__ __forceinline__ void put4(float4& to, const float* v) { to = make_float4(v[0], v[1], v[2], v[3]); }
 
-// Up to 16 states: a wave takes 64 channels, a lane each, and meets no other. A tile's states go four at a
-// time: their decays and states over the tile's 8 tokens are in registers, and a lane sums over all of
-// them what its channel needs.
+// Up to 16 states. A tile's states go four at a time: their decays and states over the tile's 8 tokens are in
+// registers, and a lane sums over all of them what its channel needs. What is asked for again at the tile's end
+// (its inputs) comes from a cache: held, it would take the registers of the states.
 // The kernel's arguments, read again from where the launch put them: what a tile needs of them before and
-// behind its states then holds no scalar register in between (held in all 250 of them are moved to lanes
-// of vector registers and back, 600 of a tile's 3700 instructions).
+// behind its states then holds no scalar register in between (held all the time, 250 of them are moved to
+// lanes of vector registers and back, 600 of a tile's 3700 instructions).
 typedef const __attribute__((address_space(4))) BackArgs* ArgsAgain;
 __device__ __forceinline__ ArgsAgain args_again() {
   ArgsAgain p = (ArgsAgain)__builtin_amdgcn_kernarg_segment_ptr();

