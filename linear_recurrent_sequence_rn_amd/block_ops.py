@@ -264,42 +264,47 @@ def rn_rmsnorm(x, weight=None, eps=1e-5, *, residual=None, sum_out=None, out=Non
     in x's type where a residual or ``sum_out`` is given, and the scale where out is of 8 bits.
     ``sum_out`` and ``out`` (of x's type) may be x or residual, not both the same one."""
     dev = _device(x, residual, weight, sum_out, out, scale_out)
-    shape = x.shape
+    shape, kind = x.shape, x.dtype
     d = shape[-1] if shape else 0
     n = x.numel()
     if n == 0 or d == 0:
         raise ValueError(f"x must be [..., d] with at least one row; got {tuple(shape)}")
-    _like(residual, x, "residual")
-    _whole(weight, torch.float32, (d,), "weight")
+    if weight is not None:
+        _whole(weight, torch.float32, (d,), "weight")
+    xs = _row_stride(x, "x")
+    rs = ss = os = d                      # new tensors are contiguous
+    if residual is not None:
+        _like(residual, x, "residual")
+        rs = _row_stride(residual, "residual")
     if out is None:
-        out = _new(x, x.dtype if out_dtype is None else out_dtype)
-    elif out.shape != shape or (out_dtype is not None and out.dtype != out_dtype):
-        raise ValueError(f"out must be {out_dtype or out.dtype} {tuple(shape)}; got {out.dtype} {tuple(out.shape)}")
-    code = _HELD8.get(out.dtype)
-    scale, step = None, 0
+        out = _new(x, kind if out_dtype is None else out_dtype)
+    else:
+        if out.shape != shape or (out_dtype is not None and out.dtype != out_dtype):
+            raise ValueError(f"out must be {out_dtype or out.dtype} {tuple(shape)}; got {out.dtype} {tuple(out.shape)}")
+        os = _row_stride(out, "out")
+    if sum_out is not None:
+        _like(sum_out, x, "sum_out")
+        ss = _row_stride(sum_out, "sum_out")
+    elif residual is not None:
+        sum_out = _new(x, kind)
+    code, scale, step = _HELD8.get(out.dtype), None, 0
     if code is None:
         code = _code(out.dtype)
         if scale_out is not None:
             raise ValueError("scale_out goes with an output of 8 bits")
     else:
         step = -(-d // group) if group > 0 else 1
-        ss = (*shape[:-1], step) if group else shape[:-1]
+        sizes = (*shape[:-1], step) if group else shape[:-1]
         if scale_out is None:
-            scale = x.new_empty(ss, dtype=torch.float32)
+            scale = x.new_empty(sizes, dtype=torch.float32)
         else:
-            _whole(scale_out, torch.float32, ss, "scale_out")
+            _whole(scale_out, torch.float32, sizes, "scale_out")
             scale = scale_out
-    if sum_out is None:
-        if residual is not None:
-            sum_out = _new(x, x.dtype)
-    else:
-        _like(sum_out, x, "sum_out")
-    desc = _pack_rms(n // d, d, _code(x.dtype), code, group, eps, _row_stride(x, "x"), _row_stride(residual, "residual"),
-                     _row_stride(sum_out, "sum_out"), _row_stride(out, "out"), step)
-    _call(dev, lib.rn_rmsnorm_forward, desc, x.data_ptr(), _p(residual), _p(weight), _p(sum_out), out.data_ptr(), _p(scale))
-    if sum_out is None and scale is None:
-        return out
-    return (out,) + (() if sum_out is None else (sum_out,)) + (() if scale is None else (scale,))
+    _call(dev, lib.rn_rmsnorm_forward, _pack_rms(n // d, d, _code(kind), code, group, eps, xs, rs, ss, os, step), x.data_ptr(),
+          _p(residual), _p(weight), _p(sum_out), out.data_ptr(), _p(scale))
+    if scale is None:
+        return out if sum_out is None else (out, sum_out)
+    return (out, scale) if sum_out is None else (out, sum_out, scale)
 
 
 def _rms_backward_desc(dout, x, eps, dsum, dx):

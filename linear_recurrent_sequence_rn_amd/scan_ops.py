@@ -139,12 +139,26 @@ def _states(state_in, state_out, slots, S, row, dtype, like):
 
 # ---- short convolution ----------------------------------------------------------------------
 
-def _conv_weight(x, weight, bias):
-    if weight.dim() != 2 or weight.shape[0] != x.shape[-1]:
-        raise ValueError(f"weight must be [{x.shape[-1]}, K]; got {tuple(weight.shape)}")
-    _whole(weight, torch.float32, weight.shape, "weight")
-    _whole(bias, torch.float32, (x.shape[-1],), "bias")
-    return weight.shape[1]
+def _conv_weight(D, weight, bias):
+    shape = weight.shape
+    if len(shape) != 2 or shape[0] != D:
+        raise ValueError(f"weight must be [{D}, K]; got {tuple(shape)}")
+    _whole(weight, torch.float32, shape, "weight")
+    if bias is not None:
+        _whole(bias, torch.float32, (D,), "bias")
+    return shape[1]
+
+
+def _state_pool(state, slots, S, row, dtype):
+    """The number of states in the buffer of a step."""
+    if slots is not None:
+        _int32(slots, S, "slots")
+    shape = state.shape
+    if state.dtype != dtype or len(shape) != 3 or shape[1:] != row or not state.is_contiguous() or shape[0] < 1 or \
+            (slots is None and shape[0] != S):
+        raise ValueError(f"state must be contiguous {dtype} {('slots' if slots is not None else S, *row)}; got {state.dtype} "
+                         f"{tuple(shape)}")
+    return shape[0]
 
 
 def rn_short_conv(x, weight, bias=None, *, silu=False, lengths=None, cu_seqlens=None, max_len=None, state_in=None,
@@ -160,8 +174,8 @@ def rn_short_conv(x, weight, bias=None, *, silu=False, lengths=None, cu_seqlens=
     dev = _device(x, weight, bias, lengths, cu_seqlens, slots, out, state_in,
                   state_out if isinstance(state_out, torch.Tensor) else None)
     S, N, T = _batch(x, lengths, cu_seqlens, max_len)
-    K = _conv_weight(x, weight, bias)
     D = x.shape[2]
+    K = _conv_weight(D, weight, bias)
     state_out, n_slots = _states(state_in, state_out, slots, S, (K - 1, D), x.dtype, x)
     flags = RN_CONV_SILU if silu else 0
     if out is None:
@@ -180,17 +194,18 @@ def rn_short_conv_step(x, weight, bias, state, *, silu=False, slots=None, out=No
     ``slots``) is updated in place. Returns out [S, 1, D]; a sequence with slot -1 is skipped, its row of
     out set to zero."""
     dev = _device(x, weight, bias, state, slots, out)
-    if x.dim() != 3 or x.shape[1] != 1 or x.numel() == 0:
-        raise ValueError(f"the step takes one token a sequence: x [S, 1, D]; got {tuple(x.shape)}")
-    S, _, D = x.shape
-    K = _conv_weight(x, weight, bias)
-    _, n_slots = _states(state, None, slots, S, (K - 1, D), x.dtype, x)
+    shape, kind = x.shape, x.dtype
+    if len(shape) != 3 or shape[1] != 1 or 0 in shape:
+        raise ValueError(f"the step takes one token a sequence: x [S, 1, D]; got {tuple(shape)}")
+    S, _, D = shape
+    K = _conv_weight(D, weight, bias)
+    n_slots = _state_pool(state, slots, S, (K - 1, D), kind)
     if out is None:
-        out = x.new_empty(x.shape)
+        out, os = x.new_empty(shape), (D, D)
     else:
         _same(out, x, "out")
-    desc = _pack_conv(S, 1, D, K, _code(x.dtype), RN_CONV_SILU if silu else 0, 0, n_slots, *_tokens(x, "x"),
-                      *_tokens(out, "out"), 0, 0)
+        os = _tokens(out, "out")
+    desc = _pack_conv(S, 1, D, K, _code(kind), RN_CONV_SILU if silu else 0, 0, n_slots, *_tokens(x, "x"), *os, 0, 0)
     _call(dev, lib.rn_short_conv_step, desc, _p(slots), x.data_ptr(), weight.data_ptr(), _p(bias), state.data_ptr(),
           out.data_ptr())
     return out
@@ -219,8 +234,8 @@ def rn_short_conv_backward(dout, x, weight, bias=None, *, silu=False, lengths=No
     dev = _device(x, dout, weight, bias, lengths, cu_seqlens, state_in, dstate_out, dx, workspace)
     S, N, T = _batch(x, lengths, cu_seqlens, max_len)
     _same(dout, x, "dout")
-    K = _conv_weight(x, weight, bias)
     D = x.shape[2]
+    K = _conv_weight(D, weight, bias)
     row = (K - 1, D)
     _states(state_in, None, None, S, row, x.dtype, x)
     _grad_state(dstate_out, S, row, "dstate_out")
@@ -323,11 +338,12 @@ def rn_selective_scan_step(x, dt, A, B, C, state, D=None, *, dt_bias=None, softp
     ``rn_selective_scan_chunked``; ``state`` (float32 [S, D, n], or a pool with ``slots``) is updated in
     place. Returns out [S, 1, D]; a sequence with slot -1 is skipped, its row of out set to zero."""
     dev = _device(x, dt, A, B, C, D, dt_bias, z, state, slots, out)
-    if x.dim() != 3 or x.shape[1] != 1 or x.numel() == 0:
-        raise ValueError(f"the step takes one token a sequence: x [S, 1, D]; got {tuple(x.shape)}")
-    S = x.shape[0]
+    shape = x.shape
+    if len(shape) != 3 or shape[1] != 1 or 0 in shape:
+        raise ValueError(f"the step takes one token a sequence: x [S, 1, D]; got {tuple(shape)}")
+    S = shape[0]
     n, G, tokens, groups = _scan_tensors(x, dt, A, B, C, D, dt_bias, z)
-    _, n_slots = _states(state, None, slots, S, (x.shape[2], n), torch.float32, x)
+    n_slots = _state_pool(state, slots, S, (shape[2], n), torch.float32)
     if out is None:
         out = x.new_empty(x.shape)
     else:
