@@ -217,10 +217,13 @@ __global__ void __launch_bounds__(256, DT == RN_BF16 && K <= 5 ? 3 : 2) conv_bac
           d *= sg * fmaf(u, 1.0f - sg, 1.0f);
         }
         du[i][v] = d = t < p.len ? d : 0.f;
-        if (i < kBackRun) {
-          db[v] += d;
+      }
+      if (i < kBackRun && t < p.len) {       // (no 0 x of a token behind the last one: x may be infinite)
 #pragma unroll
-          for (int j = 0; j < K; ++j) dw[j][v] = fmaf(d, x[i + j].value(v), dw[j][v]);
+        for (int v = 0; v < V; ++v) {
+          db[v] += du[i][v];
+#pragma unroll
+          for (int j = 0; j < K; ++j) dw[j][v] = fmaf(du[i][v], x[i + j].value(v), dw[j][v]);
         }
       }
       // dx of token t - (K - 1), a row of the state where it is before the first

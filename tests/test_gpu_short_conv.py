@@ -210,3 +210,17 @@ def test_cu_seqlens_that_make_no_sense_stay_inside_the_tensors():
         out = torch.full((1, 300, 32), 7.0, device=DEV)
         rn().rn_short_conv(x, w, cu_seqlens=torch.tensor(cu, dtype=torch.int32, device=DEV), out=out[:, 100:200])
         assert (out[:, :100] == 7).all() and (out[:, 200:] == 7).all()
+
+
+@pytest.mark.parametrize("n", [1, 3, 8, 10, 41])
+@pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("packed", [False, True])
+def test_an_infinite_last_input_reaches_the_last_weight_only(n, kind, packed):
+    """Only dw_{K-1} holds du_t x_t of a sequence's last token: the others keep their bits."""
+    b = Batch(n, [n, 13], 72, 4, kind, packed)
+    clean = rn().rn_short_conv_backward(b.dy, b.x, b.w, b.b, state_in=b.state, **b.kw)
+    x = b.x.clone()
+    x[0, n - 1, 5] = float("inf")
+    got = rn().rn_short_conv_backward(b.dy, x, b.w, b.b, state_in=b.state, **b.kw)
+    assert torch.equal(got["dx"], clean["dx"]) and torch.equal(got["dbias"], clean["dbias"])
+    assert torch.equal(got["dweight"][:, :3], clean["dweight"][:, :3]) and not got["dweight"][5, 3].isfinite()
