@@ -494,6 +494,13 @@ __global__ void __launch_bounds__(256) scan_main(BackArgs b) {
           }
           parts[2][w.wave][t][w.lane] = y;
         }
+        if (t0 + TT > nt) {                        // (no 0 p of a token behind the last one: h may be infinite)
+#pragma unroll
+          for (int t = 0; t < TT; ++t) {
+#pragma unroll
+            for (int i = 0; i < NS; ++i) p[t][i] = t0 + t < nt ? p[t][i] : 0.f;
+          }
+        }
 #pragma unroll
         for (int t = TT - 1; t >= 0; --t) {
           const float4 u = tile[t][w.lane];
@@ -777,6 +784,13 @@ __global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
             h[i] = fmaf(u[t], B[t].value(i), p[t][i]);
             y[t] = fmaf(C[t].value(i), h[i], y[t]);
             sums[t * 4 + i] = dy[t] * h[i];
+          }
+        }
+        if (count < TT) {                          // (no 0 p of a token behind the last one: h may be infinite)
+#pragma unroll
+          for (int t = 0; t < TT; ++t) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[t][i] = t < count ? p[t][i] : 0.f;
           }
         }
         const float sum_c = sums32(sums, lane);

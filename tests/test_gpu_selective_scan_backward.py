@@ -197,3 +197,17 @@ def test_cu_seqlens_that_make_no_sense_stay_inside_the_tensors():
                                         **{k: cut(t) for k, t in {**big, **heads}.items()})
         for t in (*big.values(), *heads.values()):
             assert (t[..., :100, :] == 7).all() and (t[..., 200:, :] == 7).all()
+
+
+@pytest.mark.parametrize("n", [12, 16, 32, 33])
+@pytest.mark.parametrize("last", [1, 8, 11, 90])
+@pytest.mark.parametrize("packed", [False, True])
+def test_an_infinite_last_input_leaves_the_decays_gradients(n, last, packed):
+    """dA holds g_t a_t h_{t-1} D_t, which the input of a sequence's last token is in nowhere."""
+    b = batch(n + last, [last, 13], 70, n, 1, torch.float32, packed)
+    clean = run(b)
+    b.x = b.x.clone()
+    b.x[0, last - 1, 5] = float("inf")
+    got = run(b)
+    assert torch.equal(got["dA"], clean["dA"]) and torch.equal(got["dx"], clean["dx"])
+    assert not got["ddt"][0, last - 1, 5].isfinite()
