@@ -16,9 +16,9 @@
 // 64 lanes, one left in two lanes each, in 71 instructions. Sums over all channels' blocks and over pieces are
 // added in a fixed order by scan_sum_tokens and scan_sum_pieces.
 //
-// Bound by the vector units: about 29 instructions a state and token in scan_piece and 10 in scan_edges, of
-// 13 that the gradients alone would take (4 x 2048 tokens of 2048 channels x 16 states, bf16 with gate: 340 and
-// 88 us of 464; busy 67 and 82 %; 250 registers a lane leave two waves a SIMD to hide the waits of each
+// Bound by the vector units: about 30 instructions a state and token in scan_piece and 10 in scan_edges, of
+// 13 that the gradients alone would take (4 x 2048 tokens of 2048 channels x 16 states, bf16 with gate: 352 and
+// 90 us of 474; busy 68 and 82 %; 250 registers a lane leave two waves a SIMD to hide the waits of each
 // other). All of them by four waves a block (scan_main): 640 us for scan_piece's part.
 #include <algorithm>
 

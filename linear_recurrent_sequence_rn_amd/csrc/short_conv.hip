@@ -5,7 +5,7 @@
 //     dx_t = sum_j w_j du_{t+K-1-j},   dw_j = sum_t du_t x_{t-K+1+j},   db = sum_t du_t.
 //
 // Bound by HBM: x is read once and out written once (14001 packed tokens of 4096 channels, bf16, K = 4 and
-// u sigmoid(u): 56 us, 4.1 TB/s; gradients of 2 x 4095: 64 us, 3.1 TB/s, and 5 for the weights' sums). A thread
+// u sigmoid(u): 56 us, 4.1 TB/s; gradients of 2 x 4095: 68 us, 3.0 TB/s, and 5 for the weights' sums). A thread
 // takes 16 bytes of channels (8 of bf16 backward, whose sums take registers) and a run of tokens, whose rows it
 // asks for at once; those before and behind it are its neighbours' and come from a cache.
 #include <algorithm>
@@ -19,7 +19,7 @@ namespace {
 
 // Tokens a thread takes, forward and backward, whose rows it asks for at once (14001 packed tokens of
 // 4096 channels bf16, K = 4, with runs of 8 tokens 56 us, of 16 59, of 4 75; gradients of 2 x 4095 tokens with
-// runs of 8 and three blocks a CU 65 us, of 16 in two 72).
+// runs of 8 and three blocks a CU 65 us, of 16 in two 72; now 66, sums leaving out tokens behind the last).
 constexpr int kRun = 8, kBackRun = 8;
 
 struct ConvArgs {
