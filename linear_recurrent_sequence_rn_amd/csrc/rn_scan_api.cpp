@@ -62,6 +62,17 @@ rn_status check_apart(const Box& out, const Box& in, const char* what, const cha
   return check_no_overlap(out, in, what, other);
 }
 
+// A sequence's state is read and replaced by the same threads: the one buffer in both places is fine, one
+// shifted against the other is not.
+template <class Desc>
+rn_status check_states(const Desc* d, bool slots, rn_dtype dt, int64_t row, const void* out, const void* in, const char* what,
+                       const char* other) {
+  if (!out || !in) return RN_OK;
+  const int64_t n = slots ? d->n_slots : d->S;
+  const Box a{out, size_of(dt), {row, 0, 0}, {n, 1, 1}, row}, b{in, size_of(dt), {row, 0, 0}, {n, 1, 1}, row};
+  return check_no_overlap(a, b, what, other);
+}
+
 // ---- short convolution ----------------------------------------------------------------------
 
 rn_status check_conv(const rn_conv_desc* d, bool step, bool back, rn::ConvCall* c) {
@@ -165,6 +176,7 @@ rn_status rn_short_conv(const rn_conv_desc* desc, const int32_t* cu_seqlens, con
   if (s != RN_OK) return s;
   if ((s = check_conv_ptrs(desc, weight, bias, x, out, "out")) || (s = check_lists(desc->T, cu_seqlens, lengths, slots, desc->n_slots)) ||
       (s = check_elements(state_in, desc->dtype, "state_in")) || (s = check_elements(state_out, desc->dtype, "state_out")) ||
+      (s = check_states(desc, slots, desc->dtype, int64_t(desc->K - 1) * desc->D, state_out, state_in, "state_out", "state_in")) ||
       (s = check_apart(token_box(desc, out, desc->out_stride), token_box(desc, x, desc->x_stride), "out", "x")))
     return s;
   c.cu = cu_seqlens; c.lens = lengths; c.slots = slots; c.x = x; c.w = weight; c.b = bias; c.out = out;
@@ -213,6 +225,7 @@ rn_status rn_short_conv_backward(const rn_conv_desc* desc, const int32_t* cu_seq
       (s = check_apart(bd, token_box(desc, dout, desc->out_stride), "dx", "dout")))
     return s;
   if (dstate_in && dstate_in == dstate_out) return fail(RN_ERR_INVALID_ARG, "dstate_in must not be dstate_out");
+  if ((s = check_states(desc, false, RN_F32, int64_t(desc->K - 1) * desc->D, dstate_in, dstate_out, "dstate_in", "dstate_out"))) return s;
   if ((dweight || dbias) && (s = check_workspace(workspace, workspace_bytes, rn_short_conv_backward_workspace_bytes(desc)))) return s;
   c.cu = cu_seqlens; c.lens = lengths; c.x = x; c.w = weight; c.b = bias; c.state_in = state_in; c.dout = dout; c.dx = dx;
   c.dstate_out = dstate_out; c.dstate_in = dstate_in; c.dw = dweight; c.db = dbias; c.ws = workspace;
@@ -238,6 +251,7 @@ rn_status rn_selective_scan_chunked(const rn_scan_desc* desc, const int32_t* cu_
       (s = check_lists(desc->T, cu_seqlens, lengths, slots, desc->n_slots)))
     return s;
   if (!aligned(state_in, 16) || !aligned(state_out, 16)) return fail(RN_ERR_INVALID_ARG, "states must be 16-byte aligned");
+  if ((s = check_states(desc, slots, RN_F32, int64_t(desc->D) * desc->n, state_out, state_in, "state_out", "state_in"))) return s;
   if ((s = check_workspace(workspace, workspace_bytes, rn_selective_scan_workspace_bytes(desc)))) return s;
   c.cu = cu_seqlens; c.lens = lengths; c.slots = slots; c.state_in = state_in; c.state_out = state_out; c.out = out; c.ws = workspace;
   rn::clear_error();
@@ -302,6 +316,8 @@ rn_status rn_selective_scan_backward(const rn_scan_desc* desc, const rn_scan_gra
     if (!aligned(p, 16)) return fail(RN_ERR_INVALID_ARG, "states and their gradients must be 16-byte aligned");
   if (dstate_in && (dstate_in == dstate_out || dstate_in == state_in))
     return fail(RN_ERR_INVALID_ARG, "dstate_in must be no other operand");
+  for (const float* p : {state_in, dstate_out})
+    if ((s = check_states(desc, false, RN_F32, int64_t(desc->D) * desc->n, dstate_in, p, "dstate_in", "a state"))) return s;
   if ((s = check_workspace(workspace, workspace_bytes, rn_selective_scan_backward_workspace_bytes(desc)))) return s;
   c.cu = cu_seqlens; c.lens = lengths; c.state_in = state_in; c.ws = workspace;
   rn::ScanGrads g;

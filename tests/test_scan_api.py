@@ -223,3 +223,20 @@ def test_binding_refuses_cpu_tensors():
               lambda: rn.rn_selective_scan_step(x[:, :1], x[:, :1], w, x[:, None, :1, :4], x[:, None, :1, :4], torch.zeros(2, 64, 4))):
         with pytest.raises(ValueError):
             f()
+
+
+def test_states_shifted_against_each_other_are_refused():
+    """A pool's first states as the start and its next ones as the result: one sequence would read what
+    another one writes."""
+    row = 3 * 64 * 2
+    for off in (row, -row, 2, 2 * row - 2):
+        assert run_conv(conv(), s0=FAKE, s1=FAKE + off) == INV and b"overlaps" in L.rn_last_error()
+    for off in (16, 32 * row - 16):
+        assert run_conv(conv(n_slots=32), slots=FAKE, s0=FAKE, s1=FAKE + off) == INV and b"overlaps" in L.rn_last_error()
+    assert conv_back(conv(), ds0=FAKE, ds1=FAKE + 3 * 64 * 4) == INV and b"overlaps" in L.rn_last_error()
+    row = 64 * 16 * 4
+    for off in (row, -row, 16, 2 * row - 16):
+        assert run_scan(scan(), s0=P[5], s1=P[5] + off) == INV and b"overlaps" in L.rn_last_error()
+    assert run_scan(scan(n_slots=9), slots=FAKE, s0=P[5], s1=P[5] + 8 * row) == INV and b"overlaps" in L.rn_last_error()
+    for kw in (dict(s0=P[5] + row), dict(ds1=P[5] + row), dict(ds1=P[5] - 16)):
+        assert scan_back(scan(), ds0=P[5], dout=P[6], **kw) == INV and b"overlaps" in L.rn_last_error()
