@@ -437,7 +437,7 @@ rn_status rn_layernorm_backward(const rn_norm_desc* desc, const void* dout, cons
  *     y = h / sqrt(mean(h^2) + eps) * weight
  * formed in float32; out receives y in float32 or bf16, or in 8 bits with float32 scales, one for each
  * row or for each `group` columns of it (the last group may be shorter):
- *     scale = max(max|y| / most, 2^-126),    out = y * (1 / scale) rounded to nearest even,
+ *     scale = max(max|y| / most, 2^-126),    out = y / scale rounded to nearest even,
  * most = 448 (RN_E4M3) or 127 (RN_INT8); out * scale stands for y. Where a NaN or infinity is among the
  * values of a scale, the scale is NaN (and out is NaN in RN_E4M3, 0 in RN_INT8). sum_out receives h
  * rounded to in_dtype. The sum of squares is float32: where it passes float32's range (values of 1e18

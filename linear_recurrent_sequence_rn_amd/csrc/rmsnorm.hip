@@ -2,7 +2,7 @@
 // bf16, or 8 bits with scales) and backward (with the weight's gradient).
 //
 // Forward, per row: h = x + r; rstd = 1 / sqrt(mean(h^2) + eps); y = h rstd w. In 8 bits, for the whole
-// row or each `group` columns of it: scale = max(max|y| / most, 2^-126), out = y (1 / scale) rounded to
+// row or each `group` columns of it: scale = max(max|y| / most, 2^-126), out = y / scale rounded to
 // nearest even (most: 448 for e4m3, 127 for int8). Backward, with g = dy w: dx = rstd g - x rstd^3
 // mean(g x) + dh, dw = sum_rows dy x rstd.
 //
@@ -60,21 +60,40 @@ __device__ __forceinline__ float scale_of(uint32_t m) {
   return fmaxf(__uint_as_float(m) / (OUT == RN_E4M3 ? 448.f : 127.f), 1.1754944e-38f);
 }
 
-// V consecutive values in 8 bits (V bytes), at any address; `left` as for Raw.
+// What a value is divided by its scale with. y (1 / scale) alone is off by up to two roundings, which moves about
+// one value in 3e6 that lies beside a border of e4m3 by a step; what it leaves of y, taken exactly, corrects it to
+// within 2^-46 before the one rounding. Small scales are raised with their values so that this rest is a
+// normal number. (16384 x 4096 bf16, residual, groups of 128: 95.3 us; by plain divisions 98.5, by
+// y (1 / scale) 95.3.)
+struct Scale {
+  float scale, inverse, raise;
+  __device__ __forceinline__ explicit Scale(float s) {
+    raise = s < 0x1p-90f ? 0x1p64f : 1.f;
+    scale = s * raise;
+    inverse = 1.f / scale;
+  }
+  __device__ __forceinline__ float of(float y) const {
+    y *= raise;
+    const float q = y * inverse;
+    return fmaf(fmaf(-q, scale, y), inverse, q);
+  }
+};
+
+// V consecutive values over their scale in 8 bits (V bytes), at any address; `left` as for Raw.
 template <int OUT, int V, Fit FIT>
-__device__ __forceinline__ void store8(void* p, int64_t i, int left, const float* y, float inv) {
+__device__ __forceinline__ void store8(void* p, int64_t i, int left, const float* y, const Scale& scale) {
   typedef uint32_t u32a __attribute__((aligned(1)));
   uint32_t u[V / 4];
 #pragma unroll
   for (int j = 0; j < V / 4; ++j) {
     if constexpr (OUT == RN_E4M3) {
-      u[j] = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * j] * inv, y[4 * j + 1] * inv, 0, false);
-      u[j] = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * j + 2] * inv, y[4 * j + 3] * inv, u[j], true);
+      u[j] = __builtin_amdgcn_cvt_pk_fp8_f32(scale.of(y[4 * j]), scale.of(y[4 * j + 1]), 0, false);
+      u[j] = __builtin_amdgcn_cvt_pk_fp8_f32(scale.of(y[4 * j + 2]), scale.of(y[4 * j + 3]), u[j], true);
     } else {
       u[j] = 0;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float t = y[4 * j + k] * inv;
+        const float t = scale.of(y[4 * j + k]);
         u[j] |= (static_cast<uint32_t>(static_cast<int>(t == t ? rintf(t) : 0.f)) & 0xffu) << (8 * k);
       }
     }
@@ -170,22 +189,24 @@ __global__ void __launch_bounds__(threads(W)) rms_rows(RmsArgs a) {
 #pragma unroll
           for (int i = 0; i < W; ++i) m[0] = max(m[0], top[turn][i]);
         }
-        const float sc = scale_of<OUT>(m[0]), inv = 1.0f / sc;
+        const float sc = scale_of<OUT>(m[0]);
+        const Scale by(sc);
         if (lane == 0) a.scale[row * a.cs] = sc;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           const int c = V * (lane + L * i);
-          if (FIT == kFull || c < a.d) store8<OUT, V, FIT>(a.out, row * a.os + c, a.d - c, h + i * V, inv);
+          if (FIT == kFull || c < a.d) store8<OUT, V, FIT>(a.out, row * a.os + c, a.d - c, h + i * V, by);
         }
       } else {
         const int n = a.group / V;        // lanes a group: a power of two
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           const int c = V * (lane + L * i);
-          const float sc = scale_of<OUT>(lanes_max(m[i], n)), inv = 1.0f / sc;
+          const float sc = scale_of<OUT>(lanes_max(m[i], n));
+          const Scale by(sc);
           if (FIT == kFull || c < a.d) {
             if (lane % n == 0) a.scale[row * a.cs + c / a.group] = sc;
-            store8<OUT, V, FIT>(a.out, row * a.os + c, a.d - c, h + i * V, inv);
+            store8<OUT, V, FIT>(a.out, row * a.os + c, a.d - c, h + i * V, by);
           }
         }
       }
