@@ -117,7 +117,8 @@ __global__ void __launch_bounds__(256) scan_rows(ScanArgs a) {
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
         h[c + i] = fmaf(__builtin_amdgcn_exp2f(s * A2[c + i]), h[c + i], u * B.value(i));
-        if (MODE == kScanOut) y = fmaf(C.value(i), h[c + i], y);
+        // (registers past the n states hold 0 times the token's values: NaN where those are infinite)
+        if (MODE == kScanOut) y = fmaf(C.value(i), FAST || c + i < a.n ? h[c + i] : 0.f, y);
       }
     }
     if (!kAhead) { pb += a.bs[2]; pc += a.cs[2]; }
