@@ -120,16 +120,6 @@ struct Uniform<DT, NS, true> {
 #pragma unroll
     for (int k = 0; k < kWords; ++k) u[k] = w[k];
   }
-  // the same, or zeros (and nothing read) where `have` is 0
-  __device__ __forceinline__ void load_or_zero(const void* p, int64_t i, int have) {
-#pragma unroll
-    for (int k = 0; k < kWords; ++k) u[k] = 0;
-    if (have > 0) load(p, i, have);
-  }
-  __device__ __forceinline__ void keep_if(bool yes) {
-#pragma unroll
-    for (int k = 0; k < kWords; ++k) u[k] = yes ? u[k] : 0;
-  }
   // What was unpacked so far is not kept: values are unpacked again when they are needed again.
   __device__ __forceinline__ void fresh() {
     if constexpr (DT != RN_F32) {
@@ -148,11 +138,6 @@ struct Uniform<DT, NS, false> {
   __device__ __forceinline__ void load(const void* p, int64_t i, int have) {
 #pragma unroll
     for (int k = 0; k < NS; ++k) f[k] = k < have ? Elem<DT>::load(p, i + k) : 0.f;
-  }
-  __device__ __forceinline__ void load_or_zero(const void* p, int64_t i, int have) { load(p, i, have); }
-  __device__ __forceinline__ void keep_if(bool yes) {
-#pragma unroll
-    for (int k = 0; k < NS; ++k) f[k] = yes ? f[k] : 0.f;
   }
   __device__ __forceinline__ void fresh() {}
   __device__ __forceinline__ float value(int k) const { return f[k]; }

@@ -374,8 +374,12 @@ __device__ __forceinline__ float sums32(float (&v)[32], int lane) {
   return v[0] + dpp_move<0xB1>(v[0]);                                            // lane ^ 1
 }
 
+// What a token leaves of a state, a gradient or a sum: nothing where it is behind the sequence's last one, whose
+// values it repeats. (Zeros in its place would not do: what reaches a tile may be infinite.)
+__device__ __forceinline__ float pick(bool there, float now, float before) { return there ? now : before; }
+
 template <int DT, int NS, bool FAST>
-__global__ void __launch_bounds__(256) scan_main(BackArgs b) {
+__global__ void __launch_bounds__(256, NS <= 8 ? 2 : 1) scan_main(BackArgs b) {
   constexpr int TT = tile_of(NS);
   constexpr int EACH = TT >= 4 ? TT / 4 : 1;
   __shared__ float4 tile[TT][64];                  // D, u, dy
@@ -455,7 +459,7 @@ __global__ void __launch_bounds__(256) scan_main(BackArgs b) {
       for (int k = 0; k < EACH; ++k) {
         const int t = w.wave * EACH + k;
         v[k] = in[k];
-        s[k] = t0 + t < nt ? step_of(a, in[k].dt + bias) : 0.f;
+        s[k] = step_of(a, in[k].dt + bias);
         sg[k] = a.z ? sigmoidf(in[k].z) : 0.f;
         if (stages) tile[t][w.lane] = make_float4(s[k], s[k] * in[k].x, a.z ? in[k].dout * in[k].z * sg[k] : in[k].dout, 0.f);
       }
@@ -475,49 +479,50 @@ __global__ void __launch_bounds__(256) scan_main(BackArgs b) {
               if (i < w.have) h[i] = from[i];
           }
         }
-        float dec[TT][NS], p[TT][NS], sums[64];
-        Uniform<DT, NS, FAST> B[TT], C[TT];
-#pragma unroll
-        for (int t = 0; t < TT; ++t) {
-          const int have = t0 + t < nt ? w.have : 0;       // tokens behind the last one have zeros
-          B[t].load_or_zero(a.b, bb + (t0 + t) * a.bs[2], have);
-          C[t].load_or_zero(a.c, cb + (t0 + t) * a.cs[2], have);
-          const float4 u = tile[t][w.lane];
-          float y = 0.f;
-#pragma unroll
-          for (int i = 0; i < NS; ++i) {
-            dec[t][i] = __builtin_amdgcn_exp2f(u.x * A2[i]);
-            p[t][i] = dec[t][i] * h[i];
-            h[i] = fmaf(u.y, B[t].value(i), p[t][i]);
-            y = fmaf(C[t].value(i), h[i], y);
-            sums[32 + t * NS + i] = u.z * h[i];
-          }
-          parts[2][w.wave][t][w.lane] = y;
-        }
-        if (t0 + TT > nt) {                        // (no 0 p of a token behind the last one: h may be infinite)
+        float sums[64];
+        auto tokens = [&](auto whole) {            // whole: every token is one of the sequence's
+          constexpr bool kWhole = decltype(whole)::value;
+          float dec[TT][NS], p[TT][NS];
+          Uniform<DT, NS, FAST> B[TT], C[TT];
 #pragma unroll
           for (int t = 0; t < TT; ++t) {
+            const bool there = kWhole || t0 + t < nt;
+            const int at = there ? t0 + t : nt - 1;
+            B[t].load(a.b, bb + at * a.bs[2], w.have);
+            C[t].load(a.c, cb + at * a.cs[2], w.have);
+            const float4 u = tile[t][w.lane];
+            float y = 0.f;
 #pragma unroll
-            for (int i = 0; i < NS; ++i) p[t][i] = t0 + t < nt ? p[t][i] : 0.f;
+            for (int i = 0; i < NS; ++i) {
+              dec[t][i] = __builtin_amdgcn_exp2f(u.x * A2[i]);
+              p[t][i] = dec[t][i] * h[i];
+              h[i] = pick(there, fmaf(u.y, B[t].value(i), p[t][i]), h[i]);
+              y = fmaf(C[t].value(i), h[i], y);
+              sums[32 + t * NS + i] = u.z * h[i];
+            }
+            parts[2][w.wave][t][w.lane] = y;
           }
-        }
 #pragma unroll
-        for (int t = TT - 1; t >= 0; --t) {
-          const float4 u = tile[t][w.lane];
-          float du = 0.f, ws = 0.f;
+          for (int t = TT - 1; t >= 0; --t) {
+            const bool there = kWhole || t0 + t < nt;
+            const float4 u = tile[t][w.lane];
+            float du = 0.f, ws = 0.f;
 #pragma unroll
-          for (int i = 0; i < NS; ++i) {
-            const float g = fmaf(C[t].value(i), u.z, e[i]);
-            sums[t * NS + i] = g * u.y;
-            du = fmaf(g, B[t].value(i), du);
-            const float wp = g * p[t][i];
-            ws = fmaf(wp, A2[i], ws);
-            dA[i] = fmaf(wp, u.x, dA[i]);
-            e[i] = dec[t][i] * g;
+            for (int i = 0; i < NS; ++i) {
+              const float g = fmaf(C[t].value(i), u.z, e[i]);
+              sums[t * NS + i] = g * u.y;
+              du = fmaf(g, B[t].value(i), du);
+              const float wp = g * p[t][i];
+              ws = fmaf(wp, A2[i], ws);
+              dA[i] = pick(there, fmaf(wp, u.x, dA[i]), dA[i]);
+              e[i] = pick(there, dec[t][i] * g, e[i]);
+            }
+            parts[0][w.wave][t][w.lane] = du;
+            parts[1][w.wave][t][w.lane] = ws;
           }
-          parts[0][w.wave][t][w.lane] = du;
-          parts[1][w.wave][t][w.lane] = ws;
-        }
+        };
+        if (!FAST || t0 + TT > nt) tokens(std::false_type());
+        else tokens(std::true_type());
         const float total = sums64(sums, w.lane);
         const int r = w.lane & 31, t = r / NS, i = r % NS;
         if (t0 + t < nt && i < w.have)
@@ -730,110 +735,103 @@ __global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
       }
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
-        if (!w.mine) s[t] = u[t] = dy[t] = 0.f;   // lanes past the channels, and tokens behind the last one: zeros
+        if (!w.mine) s[t] = u[t] = dy[t] = 0.f;   // lanes past the channels: zeros
         du[t] = ws[t] = y[t] = 0.f;
-      }
-      if (count < TT) {
-#pragma unroll
-        for (int t = 0; t < TT; ++t)
-          if (t >= count) s[t] = u[t] = dy[t] = 0.f;
       }
 #pragma unroll
       for (int t = 0; t < TT; ++t) u[t] *= s[t];
+      // whole: every token is one of the sequence's. (Where the lanes load B and C for themselves the other form
+      // serves both: two forms' registers spill more, 5 states, 4 x 2048 tokens of 1024 channels 481 us and 442.)
+      auto states = [&](auto whole) {
+        constexpr bool kWhole = decltype(whole)::value;
 #pragma unroll 1
-      for (int c = 0; c < NS; c += 4) {
-        float A2[4], h[4], e[4], dec[TT][4], p[TT][4], sums[32];
-        Uniform<DT, 4, FAST> B[TT], C[TT];
-        {
-          const elem* rb = pb + t0 * a.bs[2] + c;
-          const elem* rc = pc + t0 * a.cs[2] + c;
+        for (int c = 0; c < NS; c += 4) {
+          float A2[4], h[4], e[4], dec[TT][4], p[TT][4], sums[32];
+          Uniform<DT, 4, FAST> B[TT], C[TT];
+          {
+            const elem* rb = pb + t0 * a.bs[2] + c;
+            const elem* rc = pc + t0 * a.cs[2] + c;
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+              B[t].load(rb, 0, n - c);
+              C[t].load(rc, 0, n - c);
+              rb += t + 1 < count ? a.bs[2] : 0;
+              rc += t + 1 < count ? a.cs[2] : 0;
+            }
+          }
+          get4(decay[c / 4][lane], A2);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) h[i] = e[i] = 0.f;
+          if (q == tiles - 1) {
+            if (grad) load_states<4>(grad + c, n - c, fours, e);
+          } else {
+            get4(starts[q][c / 4][lane], e);
+          }
+          if (q == 0) {
+            if (from) load_states<4>(from + c, n - c, fours, h);
+          } else {
+            get4(starts[q - 1][c / 4][lane], h);
+          }
 #pragma unroll
           for (int t = 0; t < TT; ++t) {
-            B[t].load(rb, 0, n - c);
-            C[t].load(rc, 0, n - c);
-            rb += t + 1 < count ? a.bs[2] : 0;
-            rc += t + 1 < count ? a.cs[2] : 0;
-          }
-        }
-        get4(decay[c / 4][lane], A2);
+            const bool there = kWhole || t < count;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = e[i] = 0.f;
-        if (q == tiles - 1) {
-          if (grad) load_states<4>(grad + c, n - c, fours, e);
-        } else {
-          get4(starts[q][c / 4][lane], e);
-        }
-        if (q == 0) {
-          if (from) load_states<4>(from + c, n - c, fours, h);
-        } else {
-          get4(starts[q - 1][c / 4][lane], h);
-        }
-        if (count < TT) {
+            for (int i = 0; i < 4; ++i) {
+              dec[t][i] = __builtin_amdgcn_exp2f(s[t] * A2[i]);
+              p[t][i] = dec[t][i] * h[i];
+              h[i] = pick(there, fmaf(u[t], B[t].value(i), p[t][i]), h[i]);
+              y[t] = fmaf(C[t].value(i), h[i], y[t]);
+              sums[t * 4 + i] = dy[t] * h[i];
+            }
+          }
+          const float sum_c = sums32(sums, lane);
 #pragma unroll
           for (int t = 0; t < TT; ++t) {
-            B[t].keep_if(t < count);
-            C[t].keep_if(t < count);
+            B[t].fresh();
+            C[t].fresh();
           }
-        }
+          float dA[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int t = 0; t < TT; ++t) {
+          for (int t = TT - 1; t >= 0; --t) {
+            const bool there = kWhole || t < count;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            dec[t][i] = __builtin_amdgcn_exp2f(s[t] * A2[i]);
-            p[t][i] = dec[t][i] * h[i];
-            h[i] = fmaf(u[t], B[t].value(i), p[t][i]);
-            y[t] = fmaf(C[t].value(i), h[i], y[t]);
-            sums[t * 4 + i] = dy[t] * h[i];
+            for (int i = 0; i < 4; ++i) {
+              const float g = fmaf(C[t].value(i), dy[t], e[i]);
+              sums[t * 4 + i] = g * u[t];
+              du[t] = fmaf(g, B[t].value(i), du[t]);
+              const float wp = g * p[t][i];
+              ws[t] = fmaf(wp, A2[i], ws[t]);
+              dA[i] = pick(there, fmaf(wp, s[t], dA[i]), dA[i]);
+              e[i] = pick(there, dec[t][i] * g, e[i]);
+            }
           }
+          float sum[4];
+          get4(own[c / 4][lane], sum);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum[i] += dA[i];
+          put4(own[c / 4][lane], sum);
+          if (q > 0) put4(starts[q - 1][c / 4][lane], e);
+          if (q == 0 && passed) store_states<4>(passed + c, n - c, fours, e);
+          const float sum_b = sums32(sums, lane);
+          const int t = lane >> 3, i = c + (lane >> 1 & 3);
+          if (t < count && i < n) bc[(t0 + t) * bc_step + i] = lane & 1 ? sum_c : sum_b;
         }
-        if (count < TT) {                          // (no 0 p of a token behind the last one: h may be infinite)
-#pragma unroll
-          for (int t = 0; t < TT; ++t) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) p[t][i] = t < count ? p[t][i] : 0.f;
-          }
-        }
-        const float sum_c = sums32(sums, lane);
-#pragma unroll
-        for (int t = 0; t < TT; ++t) {
-          B[t].fresh();
-          C[t].fresh();
-        }
-        float dA[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int t = TT - 1; t >= 0; --t) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float g = fmaf(C[t].value(i), dy[t], e[i]);
-            sums[t * 4 + i] = g * u[t];
-            du[t] = fmaf(g, B[t].value(i), du[t]);
-            const float wp = g * p[t][i];
-            ws[t] = fmaf(wp, A2[i], ws[t]);
-            dA[i] = fmaf(wp, s[t], dA[i]);
-            e[i] = dec[t][i] * g;
-          }
-        }
-        float sum[4];
-        get4(own[c / 4][lane], sum);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sum[i] += dA[i];
-        put4(own[c / 4][lane], sum);
-        if (q > 0) put4(starts[q - 1][c / 4][lane], e);
-        if (q == 0 && passed) store_states<4>(passed + c, n - c, fours, e);
-        const float sum_b = sums32(sums, lane);
-        const int t = lane >> 3, i = c + (lane >> 1 & 3);
-        if (t < count && i < n) bc[(t0 + t) * bc_step + i] = lane & 1 ? sum_c : sum_b;
-      }
+      };
+      if (!FAST || count < TT) states(std::false_type());
+      else states(std::true_type());
       // what belongs to a channel and token, while the next tile's inputs are on their way
       Raw r;
       const ArgsAgain k = args_again();
       const bool packed = k->s.q.T > 0;
       inputs(k, t0, count, r);
       if (q > 0) inputs(k, t0 - TT, TT, next);
-      if (count < TT) {
+      if (count < TT) {                            // (no 0 x of a token behind the last one: x may be infinite)
 #pragma unroll
         for (int t = 0; t < TT; ++t)
-          if (t >= count) ws[t] = 0.f;
+          if (t >= count) {
+            s[t] = dy[t] = du[t] = ws[t] = 0.f;
+            r.x[t] = 0;
+          }
       }
       float g[TT];
 #pragma unroll

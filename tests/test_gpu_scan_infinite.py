@@ -64,3 +64,75 @@ def test_single_tokens_agree_with_prompts(n):
     steps = [rn().rn_selective_scan_step(one(b.x, t), one(b.dt, t), b.A, one(b.B, t), one(b.C, t), state, b.skip, dt_bias=b.bias)
              for t in range(12)]
     assert same_kinds(torch.cat(steps, 1), f64(out)) and same_kinds(state, f64(last))
+
+
+# ---- gradients ------------------------------------------------------------------------------
+
+def gradients(b, **kw):
+    return rn().rn_selective_scan_backward(b.dy, b.x, b.dt, b.A, b.B, b.C, b.skip, dt_bias=b.bias, z=b.z, state_in=b.state,
+                                           dstate_out=b.dstate, want_dstate_in=True, **{**b.kw, **kw})
+
+
+def oracle_gradients(b):
+    """The oracle's gradients in the calls' layouts, and zeros in rows of no sequence."""
+    got = {k: np.zeros(b.x.shape) for k in ("dx", "ddt")}
+    got.update({k: np.zeros(b.B.shape) for k in ("dB", "dC")})
+    got["dstate_in"] = np.zeros(b.state.shape)
+    with np.errstate(all="ignore"):
+        for i, (r, t), _ in b.spans():
+            w = O.selective_scan_backward(f64(b.dy[r, t]), dstate=f64(b.dstate[i]), **b.sequence(i, (r, t)))
+            for k in ("dx", "ddt"):
+                got[k][r, t] = w[k]
+            for k in ("dB", "dC"):
+                got[k][r][:, t] = w[k]
+            got["dstate_in"][i] = w["dstate_in"]
+            for k in ("dA", "dD", "ddt_bias"):
+                got[k] = got.get(k, 0) + w[k]
+    return got
+
+
+# Tokens, channels and groups: pieces of one tile, and (150 blocks along the channels) of several. Channel 4 is never
+# the one that lanes past its group repeat.
+GRADS = [(1, 70, 1), (11, 70, 1), (13, 70, 1), (90, 70, 1), (251, 300, 150)]
+
+
+@pytest.mark.parametrize("n", [5, 12, 16, 17, 32, 33])
+@pytest.mark.parametrize("last,D,G", GRADS)
+@pytest.mark.parametrize("packed", [False, True])
+def test_an_infinite_last_input_reaches_its_channels_sums_alone(n, last, D, G, packed):
+    """dD and the bias's gradient hold the last token's input: infinite there at any length, as they are elsewhere."""
+    b = positive(n + last, [last, 13], D, n, G, torch.float32, packed)
+    clean = gradients(b)
+    b.x = b.x.clone()
+    b.x[0, last - 1, 4] = INF
+    got = gradients(b)
+    others = [c for c in range(D) if c != 4]
+    for k in ("dD", "ddt_bias"):
+        assert torch.isposinf(got[k][4]) and torch.equal(got[k][others], clean[k][others]), k
+    assert torch.equal(got["dA"], clean["dA"]) and torch.equal(got["dx"], clean["dx"])
+
+
+@pytest.mark.parametrize("n", [4, 16, 24, 64])
+@pytest.mark.parametrize("last,D,G", GRADS)
+def test_an_infinite_gradient_of_the_last_state(n, last, D, G):
+    b = positive(n + last, [last, 13], D, n, G, torch.float32, True)
+    b.dstate[0, 4, n - 1] = INF
+    got, want = gradients(b), oracle_gradients(b)
+    for k, w in want.items():
+        assert same_kinds(got[k], w), k
+
+
+@pytest.mark.parametrize("n", [4, 16, 24, 64])
+@pytest.mark.parametrize("last,D,G", GRADS)
+def test_a_state_that_forgets_at_once(n, last, D, G):
+    """A of minus infinity: its decay is 0, and only the step's own gradient (0 times A) is NaN. The operands
+    being positive, the sums of sizes that rounding counts in are the gradients themselves, times at
+    most the tokens: 360 2^-24 of them for each."""
+    b = positive(n + last, [last, 13], D, n, G, torch.float32, True)
+    b.A[4, 1] = -INF
+    got, want = gradients(b), oracle_gradients(b)
+    for k, w in want.items():
+        if "ddt" in k:
+            assert same_kinds(got[k], w), k
+        else:
+            assert (np.abs(f64(got[k]) - w) <= 360 * 2.0 ** -24 * (last + 13) * np.abs(w)).all(), k
