@@ -375,7 +375,8 @@ __device__ __forceinline__ float sums32(float (&v)[32], int lane) {
 }
 
 // What a token leaves of a state, a gradient or a sum: nothing where it is behind the sequence's last one, whose
-// values it repeats. (Zeros in its place would not do: what reaches a tile may be infinite.)
+// values it repeats, nor in registers past the n states. (Zeros in their place would not do: what reaches a tile, or
+// the token's own values, may be infinite.)
 __device__ __forceinline__ float pick(bool there, float now, float before) { return there ? now : before; }
 
 template <int DT, int NS, bool FAST>
@@ -494,10 +495,11 @@ __global__ void __launch_bounds__(256, NS <= 8 ? 2 : 1) scan_main(BackArgs b) {
             float y = 0.f;
 #pragma unroll
             for (int i = 0; i < NS; ++i) {
+              const bool has = FAST || i == 0 || i < w.have;
               dec[t][i] = __builtin_amdgcn_exp2f(u.x * A2[i]);
               p[t][i] = dec[t][i] * h[i];
               h[i] = pick(there, fmaf(u.y, B[t].value(i), p[t][i]), h[i]);
-              y = fmaf(C[t].value(i), h[i], y);
+              y = pick(has, fmaf(C[t].value(i), h[i], y), y);
               sums[32 + t * NS + i] = u.z * h[i];
             }
             parts[2][w.wave][t][w.lane] = y;
@@ -509,11 +511,12 @@ __global__ void __launch_bounds__(256, NS <= 8 ? 2 : 1) scan_main(BackArgs b) {
             float du = 0.f, ws = 0.f;
 #pragma unroll
             for (int i = 0; i < NS; ++i) {
+              const bool has = FAST || i == 0 || i < w.have;
               const float g = fmaf(C[t].value(i), u.z, e[i]);
               sums[t * NS + i] = g * u.y;
-              du = fmaf(g, B[t].value(i), du);
+              du = pick(has, fmaf(g, B[t].value(i), du), du);
               const float wp = g * p[t][i];
-              ws = fmaf(wp, A2[i], ws);
+              ws = pick(has, fmaf(wp, A2[i], ws), ws);
               dA[i] = pick(there, fmaf(wp, u.x, dA[i]), dA[i]);
               e[i] = pick(there, dec[t][i] * g, e[i]);
             }
@@ -777,10 +780,11 @@ __global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
             const bool there = kWhole || t < count;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
+              const bool has = FAST || i == 0 || c + i < n;
               dec[t][i] = __builtin_amdgcn_exp2f(s[t] * A2[i]);
               p[t][i] = dec[t][i] * h[i];
               h[i] = pick(there, fmaf(u[t], B[t].value(i), p[t][i]), h[i]);
-              y[t] = fmaf(C[t].value(i), h[i], y[t]);
+              y[t] = pick(has, fmaf(C[t].value(i), h[i], y[t]), y[t]);
               sums[t * 4 + i] = dy[t] * h[i];
             }
           }
@@ -796,11 +800,12 @@ __global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
             const bool there = kWhole || t < count;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
+              const bool has = FAST || i == 0 || c + i < n;
               const float g = fmaf(C[t].value(i), dy[t], e[i]);
               sums[t * 4 + i] = g * u[t];
-              du[t] = fmaf(g, B[t].value(i), du[t]);
+              du[t] = pick(has, fmaf(g, B[t].value(i), du[t]), du[t]);
               const float wp = g * p[t][i];
-              ws[t] = fmaf(wp, A2[i], ws[t]);
+              ws[t] = pick(has, fmaf(wp, A2[i], ws[t]), ws[t]);
               dA[i] = pick(there, fmaf(wp, s[t], dA[i]), dA[i]);
               e[i] = pick(there, dec[t][i] * g, e[i]);
             }

@@ -136,3 +136,17 @@ def test_a_state_that_forgets_at_once(n, last, D, G):
             assert same_kinds(got[k], w), k
         else:
             assert (np.abs(f64(got[k]) - w) <= 360 * 2.0 ** -24 * (last + 13) * np.abs(w)).all(), k
+
+
+@pytest.mark.parametrize("n", [1, 3, 5, 11, 13, 16, 20, 33, 40])
+@pytest.mark.parametrize("last,D,G", GRADS[1:])
+@pytest.mark.parametrize("where", ["x", "dt", "dy"])
+def test_an_infinite_operand_of_one_channel(n, last, D, G, where):
+    """Whatever states the registers hold past the n: infinities of an input, a raw step or an output's gradient."""
+    b = positive(n + last, [last, 13], D, n, G, torch.float32, True)
+    t = getattr(b, where).clone()
+    t[0, last // 2, 4] = INF
+    setattr(b, where, t)
+    got, want = gradients(b), oracle_gradients(b)
+    for k, w in want.items():
+        assert same_kinds(got[k], w), k
