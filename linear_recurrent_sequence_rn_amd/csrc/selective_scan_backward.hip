@@ -60,7 +60,7 @@ struct Place {
   int64_t piece;
   int first, nt, last;                    // first token, tokens, the sequence's last piece
   int lane, wave, x, group, d, n0, have, waves;
-  bool mine;
+  bool mine, full;                        // this lane has a channel; every lane has
   __device__ __forceinline__ bool find(const ScanArgs& a) {
     piece = blockIdx.y + static_cast<int64_t>(blockIdx.z) * gridDim.y;
     x = blockIdx.x;
@@ -69,6 +69,7 @@ struct Place {
     group = x / a.tiles;
     const int each = a.D / a.G, in_group = (x - group * a.tiles) * 64 + lane;
     mine = in_group < each;
+    full = (x - group * a.tiles) * 64 + 64 <= each;
     d = group * each + in_group;
     n0 = wave * NS;
     have = min(NS, a.n - n0);
@@ -98,7 +99,7 @@ struct Lanes {
   int64_t piece, row0;
   int first, nt, last, x, group;          // first token, tokens, the sequence's last piece
   unsigned d, c0;                         // channel, the wave's first one
-  bool mine;
+  bool mine, full;                        // this lane has a channel of its own; every lane has
   // A lane's values of a tensor, token after token.
   struct Row {
     const elem* p;
@@ -148,6 +149,7 @@ struct Lanes {
     group = x / a.tiles;
     const int each = a.D / a.G, left = each - (x - group * a.tiles) * 64, lane = threadIdx.x & 63;
     mine = lane < left;
+    full = left >= 64;
     c0 = group * each + (each - left);
     d = c0 + min(lane, left - 1);
     if (!seq_place(a.q, piece, &p)) return false;
@@ -378,6 +380,12 @@ __device__ __forceinline__ float sums32(float (&v)[32], int lane) {
 // values it repeats, nor in registers past the n states. (Zeros in their place would not do: what reaches a tile, or
 // the token's own values, may be infinite.)
 __device__ __forceinline__ float pick(bool there, float now, float before) { return there ? now : before; }
+// Nor do lanes past the channels leave anything in sums over the lanes.
+template <int N>
+__device__ __forceinline__ void leave_out(float (&v)[N], bool mine) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = mine ? v[k] : 0.f;
+}
 
 template <int DT, int NS, bool FAST>
 __global__ void __launch_bounds__(256, NS <= 8 ? 2 : 1) scan_main(BackArgs b) {
@@ -526,6 +534,7 @@ __global__ void __launch_bounds__(256, NS <= 8 ? 2 : 1) scan_main(BackArgs b) {
         };
         if (!FAST || t0 + TT > nt) tokens(std::false_type());
         else tokens(std::true_type());
+        if (!w.full) leave_out(sums, w.mine);
         const float total = sums64(sums, w.lane);
         const int r = w.lane & 31, t = r / NS, i = r % NS;
         if (t0 + t < nt && i < w.have)
@@ -738,7 +747,6 @@ __global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
       }
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
-        if (!w.mine) s[t] = u[t] = dy[t] = 0.f;   // lanes past the channels: zeros
         du[t] = ws[t] = y[t] = 0.f;
       }
 #pragma unroll
@@ -788,6 +796,7 @@ __global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
               sums[t * 4 + i] = dy[t] * h[i];
             }
           }
+          if (!w.full) leave_out(sums, w.mine);
           const float sum_c = sums32(sums, lane);
 #pragma unroll
           for (int t = 0; t < TT; ++t) {
@@ -817,6 +826,7 @@ __global__ void __launch_bounds__(64, 2) scan_piece(BackArgs b) {
           put4(own[c / 4][lane], sum);
           if (q > 0) put4(starts[q - 1][c / 4][lane], e);
           if (q == 0 && passed) store_states<4>(passed + c, n - c, fours, e);
+          if (!w.full) leave_out(sums, w.mine);
           const float sum_b = sums32(sums, lane);
           const int t = lane >> 3, i = c + (lane >> 1 & 3);
           if (t < count && i < n) bc[(t0 + t) * bc_step + i] = lane & 1 ? sum_c : sum_b;

@@ -150,3 +150,20 @@ def test_an_infinite_operand_of_one_channel(n, last, D, G, where):
     got, want = gradients(b), oracle_gradients(b)
     for k, w in want.items():
         assert same_kinds(got[k], w), k
+
+
+@pytest.mark.parametrize("n", [4, 12, 16, 24, 48])
+@pytest.mark.parametrize("last,D,G", GRADS[1:])
+@pytest.mark.parametrize("where", ["B", "C", "state", "dstate"])
+def test_an_infinite_operand_of_all_channels_or_of_the_last(n, last, D, G, where):
+    """Lanes past a group's channels work on its last one, or on B and C, too: sums over channels leave them out."""
+    b = positive(n + last, [last, 13], D, n, G, torch.float32, True)
+    t = getattr(b, where).clone()
+    if where in "BC":
+        t[0, 0, last // 2, 1] = INF
+    else:
+        t[0, D - 1, 1] = INF
+    setattr(b, where, t)
+    got, want = gradients(b), oracle_gradients(b)
+    for k, w in want.items():
+        assert same_kinds(got[k], w), k
