@@ -440,8 +440,9 @@ rn_status rn_layernorm_backward(const rn_norm_desc* desc, const void* dout, cons
  *     scale = max(max|y| / most, 2^-126),    out = y / scale rounded to nearest even,
  * most = 448 (RN_E4M3) or 127 (RN_INT8); out * scale stands for y. Where a NaN or infinity is among the
  * values of a scale, the scale is NaN (and out is NaN in RN_E4M3, 0 in RN_INT8). sum_out receives h
- * rounded to in_dtype. The sum of squares is float32: where it passes float32's range (values of 1e18
- * and more), y is zero.
+ * rounded to in_dtype. The sum of squares is float32: where it passes float32's range (from values of
+ * 1.8e19 / sqrt(d) on: 1.4e17 at d = 16384), y is zero, and gradients hold zeros or NaN; beside an eps near 0,
+ * values below 1e-18 lose digits of it.
  */
 typedef struct rn_rms_desc {
     int64_t rows;          /* 1 .. 2^40 */
@@ -689,7 +690,8 @@ rn_status rn_short_conv_backward(const rn_conv_desc* desc, const int32_t* cu_seq
  * Channels come in G groups of D / G that share B and C. All arithmetic is float32. A NaN or infinity
  * at a token reaches only outputs of that token and later ones of its sequence, and its final state.
  * Decays are joined over many tokens: where D A is positive and exp of its sum over a sequence passes
- * float32's range, results may be infinite or NaN though the formula's are not.
+ * float32's range, results may be infinite or NaN though the formula's are not; where an infinite state (or
+ * gradient of one) meets joined decays below float32's range, results are NaN where the formula's are infinite.
  */
 typedef struct rn_scan_desc {
     int32_t S;             /* sequences, 1 .. 65534 */

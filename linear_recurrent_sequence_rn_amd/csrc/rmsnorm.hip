@@ -7,11 +7,11 @@
 // mean(g x) + dh, dw = sum_rows dy x rstd.
 //
 // Bound by HBM: every tensor is read or written once (16384 x 4096 bf16 with residual and an e4m3 output with a
-// scale for each 128 columns: 89 us, 5.3 TB/s; a large copy reaches 5.0 to 5.4). Smaller calls are bound by
-// latency (32 x 4096, e4m3: kernel 4 us, a call 10; backward of 3001 x 1537 float32 with the residual's
-// gradient: 19 us and 5 for the weights' sums). Rows are held as in the layer norm: in the registers of 16
-// lanes, of a wave or of a block, so that the passes over a row (squares, maximum, result) cost no memory
-// access; the backward needs one join of a row, for the sums of x x and g x. The largest value of a group of
+// scale for each 128 columns: 90 us, 5.2 TB/s; its gradients 102 us, 5.3 TB/s; a large copy reaches 5.0 to 5.4).
+// Smaller calls are bound by latency (32 x 4096, e4m3: kernel 4 us, a call 10; backward of 3001 x 1537 float32 with
+// the residual's gradient: a call 22 us, 5 of them the weights' sums). Rows are held as in the layer norm: in the
+// registers of 16 lanes, of a wave or of a block, so that the passes over a row (squares, maximum, result) cost no
+// memory access; the backward needs one join of a row, for the sums of x x and g x. The largest value of a group of
 // 32 to 128 columns is found among the 4 to 32 lanes that hold them, without LDS.
 #include <algorithm>
 
@@ -63,8 +63,8 @@ __device__ __forceinline__ float scale_of(uint32_t m) {
 // What a value is divided by its scale with. y (1 / scale) alone is off by up to two roundings, which moves about
 // one value in 3e6 that lies beside a border of e4m3 by a step; what it leaves of y, taken exactly, corrects it to
 // within 2^-46 before the one rounding. Small scales are raised with their values so that this rest is a
-// normal number. (16384 x 4096 bf16, residual, groups of 128: 95.3 us; by plain divisions 98.5, by
-// y (1 / scale) 95.3.)
+// normal number. (16384 x 4096 bf16, residual, groups of 128, in turn: 95.3 us, as by y (1 / scale);
+// by plain divisions 98.5.)
 struct Scale {
   float scale, inverse, raise;
   __device__ __forceinline__ explicit Scale(float s) {

@@ -1,14 +1,15 @@
 // Selective scan: prompts (selective_scan.h) and single tokens.
 //
 // Prompts. Bound by the vector units: a state takes 5 instructions a token (the exponent, its exponential, which
-// counts twice, the input's product, and the two sums), a channel about 35 more (softplus, gate, loads, the
-// output). A wave has 64 channels with all their states in its lanes' registers, B and C in its scalar ones, and
-// nothing to share with other waves: no LDS, no barrier (sharing a channel's states over four waves, joined in
-// LDS, took 547 us where this takes 228). A sequence whose channels do not fill the chip is cut into segments:
-// one pass gives the state that each adds on its own, scan_carry carries the states over the segments, a second
-// pass gives the outputs (8192 tokens of 4096 channels x 16 states, bf16 with gate: 90 to 104, 17 and 110 to 133
-// us; vector units 72 and 82 % busy, 2.3 GHz). 32 sequences of 512 tokens need no cut: 295 us for twice the
-// tokens.
+// counts twice, the input's product, and the two sums; 4 where only states are wanted), a channel 37 more (counted:
+// softplus 16, gate 8, loads, the skip and the output 13; 25 where only states are wanted). A wave has 64 channels
+// with all their states in its lanes' registers, B and C in its scalar ones, and nothing to share with other waves: no
+// LDS, no barrier (sharing a channel's states over four waves, joined in LDS, took 547 us where this takes 228). A
+// sequence whose channels do not fill the chip is cut into segments: one pass gives the state that each adds on its
+// own, scan_carry carries the states over the segments, a second pass gives the outputs (8192 tokens of 4096 channels
+// x 16 states, bf16 with gate: 106, 17 and 138 us under the profiler; vector units 91 and 93 % busy). 32 sequences of
+// 512 tokens need no cut: 295 us for twice the tokens. 32 states of 2048 channels take 241 us, 64 take 617: B and C of
+// more than 16 states are waited for, a set at a time.
 //
 // Single tokens. Bound by HBM: the float32 state is read and written once.
 #include <algorithm>

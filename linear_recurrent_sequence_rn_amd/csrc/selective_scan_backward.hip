@@ -16,10 +16,11 @@
 // 64 lanes, one left in two lanes each, in 71 instructions. Sums over all channels' blocks and over pieces are
 // added in a fixed order by scan_sum_tokens and scan_sum_pieces.
 //
-// Bound by the vector units: about 30 instructions a state and token in scan_piece and 10 in scan_edges, of
-// 13 that the gradients alone would take (4 x 2048 tokens of 2048 channels x 16 states, bf16 with gate: 352 and
-// 90 us of 474; busy 68 and 82 %; 250 registers a lane leave two waves a SIMD to hide the waits of each
-// other). All of them by four waves a block (scan_main): 640 us for scan_piece's part.
+// Bound by the vector units: 29 instructions a state and token in scan_piece and 10 in scan_edges, of 13 that
+// the gradients alone would take (4 x 2048 tokens of 2048 channels x 16 states, bf16 with gate: a call 460 us; under
+// the profiler 336 and 90 us, and 55 of joining and sums; busy 69 and 83 %; 250 registers a lane leave two waves a SIMD
+// to hide the waits of each other). All of them by four waves a block (scan_main): 640 us for scan_piece's part. Of
+// 1024 channels, 16 states 247 us, 32 (scan_main) 632, 64 2086.
 #include <algorithm>
 
 #include "selective_scan.h"
@@ -1012,7 +1013,8 @@ struct Parts {
 };
 // Tokens a piece: the most that leave waves for the chip to hold at once, two a SIMD (float32, 5 sequences of
 // 1501 tokens in all, 212 channels: 8 tokens 59 us, 32 110; bf16, 16 states, 4 x 512 tokens of 1024 channels: 8
-// tokens 102, 16 95, 32 135; 4 x 2048 of 2048: 663, 532 and 484). scan_main's blocks are four waves.
+// tokens 102, 16 95, 32 135; 4 x 2048 of 2048: 663, 532 and 484, which whole tiles in a form of their own made 460).
+// scan_main's blocks are four waves.
 ScanArgs pieces_of(const ScanCall& c) {
   const bool small = c.n <= 16;
   const int tile = small ? kPieceTile : tile_of(scan_states(c.n));

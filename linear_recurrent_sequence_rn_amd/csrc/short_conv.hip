@@ -5,7 +5,8 @@
 //     dx_t = sum_j w_j du_{t+K-1-j},   dw_j = sum_t du_t x_{t-K+1+j},   db = sum_t du_t.
 //
 // Bound by HBM: x is read once and out written once (14001 packed tokens of 4096 channels, bf16, K = 4 and
-// u sigmoid(u): 56 us, 4.1 TB/s; gradients of 2 x 4095: 68 us, 3.0 TB/s, and 5 for the weights' sums). A thread
+// u sigmoid(u): 56 us, 4.1 TB/s; gradients of 2 x 4095: a call 66 us, 5 of them the weights' sums, 3.3 TB/s in the
+// rest; in float32 96 us, 4.4 TB/s). A thread
 // takes 16 bytes of channels (8 of bf16 backward, whose sums take registers) and a run of tokens, whose rows it
 // asks for at once; those before and behind it are its neighbours' and come from a cache.
 #include <algorithm>
