@@ -717,8 +717,8 @@ size_t rn_selective_scan_workspace_bytes(const rn_scan_desc* desc);
 
 /*
  * Prompts. x, dt, z (or NULL), out [.., D]; B, C [.., G, .., n]; A: DEVICE float32 [D, n]; skip, bias:
- * DEVICE float32 [D] or NULL (0). States: float32 [D, n] a sequence, 16-byte aligned. workspace: 256-byte
- * aligned.
+ * DEVICE float32 [D] or NULL (0). States: float32 [D, n] a sequence, 16-byte aligned where n is a multiple
+ * of 4. workspace: 256-byte aligned.
  */
 rn_status rn_selective_scan_chunked(const rn_scan_desc* desc, const int32_t* cu_seqlens,
                                     const int32_t* lengths, const int32_t* slots, const void* x,

@@ -144,6 +144,14 @@ rn_status check_scan_ptrs(const rn_scan_desc* d, const void* x, const void* dt, 
   return RN_OK;
 }
 
+// States are moved by fours where a channel has whole fours of them, and one by one elsewhere: such states may be any
+// slice of a pool.
+rn_status check_state_address(const rn_scan_desc* d, const void* p, const char* what) {
+  const int n = d->n % 4 == 0 ? 16 : 4;
+  if (!aligned(p, n)) return fail(RN_ERR_INVALID_ARG, "%s must be %d-byte aligned", what, n);
+  return RN_OK;
+}
+
 // `out` (a token gradient) against every input that has rows of tokens.
 rn_status check_scan_apart(const rn_scan_desc* d, const rn::ScanCall& c, const Box& out, const char* what) {
   rn_status s;
@@ -250,7 +258,7 @@ rn_status rn_selective_scan_chunked(const rn_scan_desc* desc, const int32_t* cu_
   if ((s = check_scan_ptrs(desc, x, dt, A, B, C, skip, bias, z, &c)) || (s = check_scan_out(desc, c, out)) ||
       (s = check_lists(desc->T, cu_seqlens, lengths, slots, desc->n_slots)))
     return s;
-  if (!aligned(state_in, 16) || !aligned(state_out, 16)) return fail(RN_ERR_INVALID_ARG, "states must be 16-byte aligned");
+  if ((s = check_state_address(desc, state_in, "state_in")) || (s = check_state_address(desc, state_out, "state_out"))) return s;
   if ((s = check_states(desc, slots, RN_F32, int64_t(desc->D) * desc->n, state_out, state_in, "state_out", "state_in"))) return s;
   if ((s = check_workspace(workspace, workspace_bytes, rn_selective_scan_workspace_bytes(desc)))) return s;
   c.cu = cu_seqlens; c.lens = lengths; c.slots = slots; c.state_in = state_in; c.state_out = state_out; c.out = out; c.ws = workspace;
@@ -268,7 +276,7 @@ rn_status rn_selective_scan_step(const rn_scan_desc* desc, const int32_t* slots,
       (s = check_lists(0, nullptr, nullptr, slots, desc->n_slots)))
     return s;
   if (!state) return fail(RN_ERR_INVALID_ARG, "state pointer is NULL");
-  if (!aligned(state, 16)) return fail(RN_ERR_INVALID_ARG, "state must be 16-byte aligned");
+  if ((s = check_state_address(desc, state, "state"))) return s;
   c.slots = slots; c.state_in = state; c.state_out = state; c.out = out;
   rn::clear_error();
   return hip_status(rn::launch_selective_step(c, static_cast<hipStream_t>(stream)), "selective scan step launch");
@@ -313,7 +321,7 @@ rn_status rn_selective_scan_backward(const rn_scan_desc* desc, const rn_scan_gra
   for (const float* p : {static_cast<const float*>(dA), static_cast<const float*>(dskip), static_cast<const float*>(dbias)})
     if ((s = check_elements(p, RN_F32, "dA/dskip/dbias"))) return s;
   for (const float* p : {state_in, dstate_out, static_cast<const float*>(dstate_in)})
-    if (!aligned(p, 16)) return fail(RN_ERR_INVALID_ARG, "states and their gradients must be 16-byte aligned");
+    if ((s = check_state_address(desc, p, "a state or its gradient"))) return s;
   if (dstate_in && (dstate_in == dstate_out || dstate_in == state_in))
     return fail(RN_ERR_INVALID_ARG, "dstate_in must be no other operand");
   for (const float* p : {state_in, dstate_out})
